@@ -1,13 +1,18 @@
 /*
  * pkv.h -- C ABI of the paged KV-cache attention library (libpkv.so).
  *
- * Three operations, named and shaped after the calls that the vLLM and
+ * Its core operations are named and shaped after the calls that the vLLM and
  * Aphrodite attention backends make (sources cited per function, by page
  * title and section):
  *
  *   pkv_reshape_and_cache        -- "reshape_and_cache_flash"
  *   pkv_paged_attention_varlen   -- "flash_attn_varlen_func" with block_table
  *   pkv_merge_attn_states        -- "merge_attn_states"
+ *
+ * Beside them stand the steps between a model's QKV projection and the cache
+ * (pkv_qk_norm_rope, pkv_rope_reshape_and_cache) and a 4-bit cache
+ * (pkv_reshape_and_cache_fp4, pkv_paged_attention_varlen_fp4,
+ * pkv_dequantize_fp4_cache); the pages have no counterpart of these.
  *
  * Conventions shared by every entry point:
  *   - Every tensor pointer is a DEVICE pointer owned by the caller.  The
@@ -305,6 +310,199 @@ PKV_API pkv_status pkv_paged_attention_varlen_opts(
     const pkv_attention_options* opts);
 
 /*
+ * The 4-bit KV cache.  (No counterpart on the source pages, whose quantized
+ * cache is E4M3.)
+ *
+ * A row of head_size values is head_size / 2 bytes of E2M1 codes, two to a
+ * byte (the lower index in the lower four bits; the magnitudes 0, 0.5, 1,
+ * 1.5, 2, 3, 4, 6 and a sign bit), and head_size / 16 E4M3 ("fn") block
+ * scales, one byte for each 16 values.  A value reads back as
+ *   code * block_scale * tensor_scale.
+ *
+ * Codes: 4-D views [num_blocks, block_size, num_kv_heads, head_size / 2],
+ *   uint8, cache_strides in BYTES (cache_strides[3] = 1; the two matrices
+ *   share them); rows on 16-byte boundaries.
+ * Block scales: 4-D views [num_blocks, block_size, num_kv_heads, head_size /
+ *   16], one byte each, with the strides below in bytes (strides[3] = 1);
+ *   rows on boundaries of head_size / 64 bytes.  A layout that keeps each
+ *   (block, head) together, [num_blocks, num_kv_heads, block_size, ...], is
+ *   the one that reads fastest, for both.
+ * k_scale, v_scale: device float scalars, > 0.  About amax / (6 * 448) uses
+ *   the block scales' range best.
+ */
+typedef struct {
+  void* k_block_scale;
+  void* v_block_scale;
+  int64_t strides[4];
+  const float* k_scale;
+  const float* v_scale;
+} pkv_fp4_scales;
+
+/*
+ * pkv_reshape_and_cache_fp4 -- pkv_reshape_and_cache into a 4-bit cache.
+ *
+ * For each 16 values x of a row with largest magnitude a, in float32:
+ *   block_scale = e4m3(a * fl(1 / fl(6 * scale)))
+ *   code        = e2m1(x * fl(1 / fl(block_scale * scale)))
+ * each rounded to nearest, ties to even, and saturated (448 and 6); a group
+ * whose scale rounds to 0 has codes 0.  A NaN in a group makes its block
+ * scale NaN: the whole group reads back as NaN.  Slots, padding and
+ * num_tokens behave as in pkv_reshape_and_cache.
+ * key, value: 16-bit rows on 16-byte boundaries; head_size a multiple of 64
+ *   (PKV_ERR_UNSUPPORTED otherwise).
+ */
+PKV_API pkv_status pkv_reshape_and_cache_fp4(
+    const void* key, const void* value,
+    int64_t k_stride_tok, int64_t k_stride_head,
+    int64_t v_stride_tok, int64_t v_stride_head,
+    void* key_cache, void* value_cache, const int64_t cache_strides[4],
+    const pkv_fp4_scales* scales,
+    const int64_t* slot_mapping, int64_t num_tokens,
+    int num_kv_heads, int head_size, int block_size, int64_t num_blocks,
+    pkv_dtype dtype, pkv_stream_t stream);
+
+/*
+ * pkv_dequantize_fp4_cache -- blocks of one matrix of a 4-bit cache as
+ * 16-bit values.
+ *
+ * out[i] = block (block_ids ? block_ids[i] : i) of the cache, contiguous
+ *   [num_out, block_size, num_kv_heads, head_size], code * block_scale *
+ *   scale with the last product in float32, rounded to dtype; 16-byte
+ *   aligned.
+ * block_ids: int64 [num_out] device, or NULL (num_out <= num_blocks then);
+ *   ids outside [0, num_blocks) give zeros and are flagged.
+ */
+PKV_API pkv_status pkv_dequantize_fp4_cache(
+    const void* codes, const int64_t cache_strides[4],
+    const void* block_scale, const int64_t scale_strides[4],
+    const float* scale, const int64_t* block_ids, int64_t num_out,
+    int num_kv_heads, int head_size, int block_size, int64_t num_blocks,
+    void* out, pkv_dtype dtype, pkv_stream_t stream);
+
+/*
+ * pkv_paged_attention_varlen_fp4 -- pkv_paged_attention_varlen_opts over a
+ * 4-bit cache (q and out 16-bit, every mask, split and LSE option).
+ *
+ * cache_strides are in bytes; `scales` gives the block scales and the two
+ * tensor scales (opts->k_scale / v_scale are not read).  Decode-class
+ * requests read the codes directly (the decode kernel choice of
+ * pkv_set_decode_kernel does not apply); prefill-class requests read them
+ * through an exact 16-bit copy of their pages in the workspace.  An fp8 cache
+ * or query or non-paged keys in opts: PKV_ERR_UNSUPPORTED.
+ * workspace: pkv_paged_attention_workspace_size_fp4 bytes.
+ */
+PKV_API size_t pkv_paged_attention_workspace_size_fp4(
+    int batch, int total_q, int max_seqlen_q, int max_seqlen_k,
+    int num_heads, int num_kv_heads, int head_size, int block_size,
+    int causal, int window_left, int window_right, int num_splits,
+    int max_blocks_per_seq, const pkv_attention_options* opts);
+
+PKV_API pkv_status pkv_paged_attention_varlen_fp4(
+    const void* q, int64_t q_stride_tok, int64_t q_stride_head,
+    const void* key_cache, const void* value_cache,
+    const int64_t cache_strides[4], const pkv_fp4_scales* scales,
+    void* out, int64_t o_stride_tok, int64_t o_stride_head,
+    const int32_t* cu_seqlens_q, const int32_t* seqused_k, int batch,
+    int total_q, int max_seqlen_q, int max_seqlen_k,
+    const int32_t* block_table, int64_t block_table_stride,
+    int max_blocks_per_seq,
+    int num_heads, int num_kv_heads, int head_size, int block_size,
+    int64_t num_blocks,
+    float softmax_scale, int causal, int window_left, int window_right,
+    float softcap, const float* alibi_slopes,
+    int num_splits, float* softmax_lse,
+    void* workspace, size_t workspace_bytes,
+    pkv_dtype dtype, pkv_stream_t stream,
+    const pkv_attention_options* opts);
+
+/*
+ * Head norms and rotary positions.  (No counterpart on the source pages,
+ * whose backends take q and k after these steps.)
+ *
+ * For a row x of head_size values, one head of token t, in float32:
+ *   n = x * (1 / sqrt(mean(x^2) + eps)) * (weight + weight_offset)
+ *       with q_weight / k_weight (both or neither; n = x without), the sum
+ *       of squares taken pairwise, neighbours first;
+ *   for each pair i < rot_dim / 2, with c = cos_sin[pos, i] and
+ *   s = cos_sin[pos, rot_dim / 2 + i],
+ *   y_a = n_a c - n_b s,  y_b = n_b c + n_a s  (products rounded one by one)
+ *       where (a, b) = (i, i + rot_dim / 2) with is_neox, else
+ *       (2 i, 2 i + 1); dimensions from rot_dim on pass through;
+ *   and one rounding to the output's type.
+ * pos is the position of the pair's axis: positions[axis][t].  With
+ * num_axes > 1, sections[a] pairs belong to axis a (their sum is
+ * rot_dim / 2): in runs (axis 0's first), or, `interleaved_axes`, pair i to
+ * axis a = i % num_axes while i < num_axes * sections[a], else to axis 0.
+ *
+ * positions : int64 [num_axes][num_tokens] device, row stride
+ *             position_axis_stride.  A token with a negative position is
+ *             padding and is skipped (nothing of it is written); one with a
+ *             position >= max_position is skipped and flagged
+ *             (PKV_ERR_BAD_INDEX through pkv_check_device_errors).
+ * cos_sin   : [max_position, rot_dim], row stride cos_sin_stride elements,
+ *             float32 (cos_sin_f32) or the call's 16-bit type.
+ * q_weight,
+ * k_weight  : [head_size] in the call's type.
+ */
+typedef struct {
+  const int64_t* positions;
+  int64_t position_axis_stride;
+  int num_axes;                 /* 1 to 4 */
+  int interleaved_axes;
+  int sections[4];
+  const void* cos_sin;
+  int64_t cos_sin_stride;
+  int64_t max_position;
+  int cos_sin_f32;
+  int rot_dim;                  /* even, <= head_size */
+  int is_neox;
+  const void* q_weight;
+  const void* k_weight;
+  float eps;
+  float weight_offset;
+} pkv_rope_params;
+
+/*
+ * pkv_qk_norm_rope -- head norms and rotation of q and k in one pass.
+ *
+ * q [num_tokens, num_heads, head_size] and k [num_tokens, num_kv_heads,
+ * head_size] with element strides, to q_out and k_out, which may be q and k
+ * themselves (the same pointer and strides) and must not overlap them
+ * otherwise.  head_size: a multiple of 8, at most 512.  num_heads may be 0
+ * (keys alone).  num_tokens == 0 is a no-op.
+ */
+PKV_API pkv_status pkv_qk_norm_rope(
+    const void* q, int64_t q_stride_tok, int64_t q_stride_head,
+    const void* k, int64_t k_stride_tok, int64_t k_stride_head,
+    void* q_out, int64_t qo_stride_tok, int64_t qo_stride_head,
+    void* k_out, int64_t ko_stride_tok, int64_t ko_stride_head,
+    int64_t num_tokens, int num_heads, int num_kv_heads, int head_size,
+    const pkv_rope_params* rope, pkv_dtype dtype, pkv_stream_t stream);
+
+/*
+ * pkv_rope_reshape_and_cache -- the same on q and k, with the keys and the
+ * values v appended to the paged cache in the same pass.
+ *
+ * Every token's q rows go to q_out (also those whose slot is negative, a
+ * token whose keys are kept elsewhere); key and value rows of the tokens
+ * with a slot go to the cache as pkv_reshape_and_cache places them.  A key is
+ * rounded once, from float32 to the cache's type.  kv_cache_dtype: "auto",
+ * "fp8" / "fp8_e4m3" (k_scale, v_scale) or "fp4" (`fp4`, with cache_strides
+ * in bytes; head_size a multiple of 64 there).
+ */
+PKV_API pkv_status pkv_rope_reshape_and_cache(
+    const void* q, int64_t q_stride_tok, int64_t q_stride_head,
+    const void* k, int64_t k_stride_tok, int64_t k_stride_head,
+    const void* v, int64_t v_stride_tok, int64_t v_stride_head,
+    void* q_out, int64_t qo_stride_tok, int64_t qo_stride_head,
+    void* key_cache, void* value_cache, const int64_t cache_strides[4],
+    const int64_t* slot_mapping, int64_t num_tokens,
+    int num_heads, int num_kv_heads, int head_size, int block_size,
+    int64_t num_blocks, const pkv_rope_params* rope, pkv_dtype dtype,
+    const char* kv_cache_dtype, const float* k_scale, const float* v_scale,
+    const pkv_fp4_scales* fp4, pkv_stream_t stream);
+
+/*
  * pkv_cascade_attention -- shared-prefix ("cascade") attention in one call.
  *
  * Source: "vllm/v1/attention/backends/flash_attn.py", cascade_attention:
@@ -534,8 +732,9 @@ PKV_API int pkv_use_cascade_attention(
  *                      and returned without writing its outputs);
  *   PKV_ERR_BAD_INDEX  a kernel met an out-of-range block id or slot (the
  *                      access was skipped, never performed), a key range
- *                      past the table row, or a request with more queries
- *                      than the call's max_seqlen_q (not computed);
+ *                      past the table row, a request with more queries
+ *                      than the call's max_seqlen_q (not computed), or a
+ *                      position past the rotation table (token skipped);
  *   PKV_ERR_CUDA       an internal launch fault was caught (misaligned
  *                      shared memory);
  *   PKV_OK             nothing since the last check.

@@ -4,9 +4,10 @@ The compute lives in ``libpkv.so`` (C ABI, ``include/pkv.h``); this package is
 its thin binding.  The library is loaded on first use and a missing or
 unloadable library raises: there is no CPU fallback.
 """
-_API = ("PkvError", "cascade_attention", "flash_attn_varlen_func",
-        "merge_attn_states", "paged_attention_workspace_size",
-        "reshape_and_cache_flash")
+_API = ("PkvError", "cascade_attention", "dequantize_fp4_cache",
+        "flash_attn_varlen_func", "fp4_kv_cache", "merge_attn_states",
+        "paged_attention_workspace_size", "qk_norm_rope",
+        "reshape_and_cache_flash", "rope_reshape_and_cache")
 
 
 def __getattr__(name):

@@ -10,7 +10,10 @@ on the vLLM pages do.
 
 Names and argument orders follow those pages: ``reshape_and_cache_flash``,
 ``flash_attn_varlen_func``, ``merge_attn_states`` and ``cascade_attention``
-("vllm/v1/attention/backends/flash_attn.py").
+("vllm/v1/attention/backends/flash_attn.py").  ``qk_norm_rope``,
+``rope_reshape_and_cache`` and the 4-bit cache (``fp4_kv_cache``,
+``dequantize_fp4_cache``, the ``*_block_scale`` arguments) have no counterpart
+there.
 """
 from __future__ import annotations
 
@@ -49,6 +52,29 @@ class _Options(ctypes.Structure):
                 ("cu_seqlens_k", ctypes.c_void_p), ("total_k", ctypes.c_int),
                 ("fixed_split_size", ctypes.c_int), ("q_fp8", ctypes.c_int),
                 ("q_scale", ctypes.c_void_p), ("no_pdl", ctypes.c_int)]
+
+
+class _Fp4Scales(ctypes.Structure):
+    """pkv_fp4_scales (include/pkv.h)."""
+    _fields_ = [("k_block_scale", ctypes.c_void_p),
+                ("v_block_scale", ctypes.c_void_p),
+                ("strides", ctypes.c_int64 * 4),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p)]
+
+
+class _RopeParams(ctypes.Structure):
+    """pkv_rope_params (include/pkv.h)."""
+    _fields_ = [("positions", ctypes.c_void_p),
+                ("position_axis_stride", ctypes.c_int64),
+                ("num_axes", ctypes.c_int),
+                ("interleaved_axes", ctypes.c_int),
+                ("sections", ctypes.c_int * 4), ("cos_sin", ctypes.c_void_p),
+                ("cos_sin_stride", ctypes.c_int64),
+                ("max_position", ctypes.c_int64),
+                ("cos_sin_f32", ctypes.c_int), ("rot_dim", ctypes.c_int),
+                ("is_neox", ctypes.c_int), ("q_weight", ctypes.c_void_p),
+                ("k_weight", ctypes.c_void_p), ("eps", ctypes.c_float),
+                ("weight_offset", ctypes.c_float)]
 
 
 _FP8_CACHE = (torch.float8_e4m3fn, torch.uint8)
@@ -118,6 +144,27 @@ def load_library():
         lib.pkv_scaled_fp8_quant.restype = i32
         lib.pkv_scaled_fp8_quant.argtypes = [vp, i64, vp, i64, i64, i32, vp,
                                              i32, vp]
+        lib.pkv_reshape_and_cache_fp4.restype = i32
+        lib.pkv_reshape_and_cache_fp4.argtypes = [
+            vp, vp, i64, i64, i64, i64, vp, vp, c_i64p, vp, vp, i64, i32, i32,
+            i32, i64, i32, vp]
+        lib.pkv_dequantize_fp4_cache.restype = i32
+        lib.pkv_dequantize_fp4_cache.argtypes = [
+            vp, c_i64p, vp, c_i64p, vp, vp, i64, i32, i32, i32, i64, vp, i32,
+            vp]
+        lib.pkv_paged_attention_workspace_size_fp4.restype = sz
+        lib.pkv_paged_attention_workspace_size_fp4.argtypes = \
+            lib.pkv_paged_attention_workspace_size_opts.argtypes
+        lib.pkv_paged_attention_varlen_fp4.restype = i32
+        at = lib.pkv_paged_attention_varlen_opts.argtypes
+        lib.pkv_paged_attention_varlen_fp4.argtypes = at[:6] + [vp] + at[6:]
+        lib.pkv_qk_norm_rope.restype = i32
+        lib.pkv_qk_norm_rope.argtypes = [vp, i64, i64] * 4 + [
+            i64, i32, i32, i32, vp, i32, vp]
+        lib.pkv_rope_reshape_and_cache.restype = i32
+        lib.pkv_rope_reshape_and_cache.argtypes = [vp, i64, i64] * 4 + [
+            vp, vp, c_i64p, vp, i64, i32, i32, i32, i32, i64, vp, i32,
+            ctypes.c_char_p, vp, vp, vp, vp]
         lib.pkv_set_prefill_kernel.restype = i32
         lib.pkv_set_prefill_kernel.argtypes = [i32]
         lib.pkv_set_decode_kernel.restype = i32
@@ -151,6 +198,41 @@ def _ptr(t: Optional[torch.Tensor]):
     return ctypes.c_void_p(0 if t is None else t.data_ptr())
 
 
+def _on_device(*tensors) -> torch.device:
+    """The one CUDA device that every given tensor (None aside) is on."""
+    dev = None
+    for t in tensors:
+        if t is None:
+            continue
+        if dev is None:
+            dev = t.device
+            if dev.type != "cuda":
+                raise ValueError("tensors must be on a CUDA device")
+        elif t.device != dev:
+            raise ValueError("tensors must be on one device (%s and %s)" %
+                             (dev, t.device))
+    return dev
+
+
+def _call(dev, fn, *args):
+    """fn(*args, stream): on `dev` and its current stream; checks the
+    status."""
+    if dev.index == torch.cuda.current_device():
+        _check(fn(*args, torch.cuda.current_stream(dev).cuda_stream))
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(*args, torch.cuda.current_stream(dev).cuda_stream))
+
+
+def _call4(dev, fn, opts, *args):
+    """_call of a function that takes its options after the stream."""
+    _call(dev, lambda *a: fn(*a, ctypes.byref(opts)), *args)
+
+
+def _addr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
 def _dtype(t: torch.Tensor) -> int:
     try:
         return _DT[t.dtype]
@@ -167,6 +249,40 @@ def _cache_strides(key_cache, value_cache):
         raise ValueError("key_cache and value_cache must share shape and "
                          "strides")
     return (ctypes.c_int64 * 4)(*key_cache.stride())
+
+
+def _scalar(t, what):
+    if t is None or t.dtype != torch.float32 or t.numel() < 1:
+        raise ValueError("%s must be a float32 tensor" % what)
+
+
+def _fp4_scales(key_cache, value_cache, k_block_scale, v_block_scale,
+                k_scale, v_scale):
+    """Check a 4-bit cache's views; (pkv_fp4_scales, head_size)."""
+    NB, BS, H, half = key_cache.shape
+    if key_cache.dtype != torch.uint8 or value_cache.dtype != torch.uint8:
+        raise ValueError("a 4-bit cache holds its codes as uint8 "
+                         "[num_blocks, block_size, num_kv_heads, "
+                         "head_size / 2]")
+    if k_block_scale is None or v_block_scale is None:
+        raise ValueError("a 4-bit cache needs both block scales")
+    for t in (k_block_scale, v_block_scale):
+        if t.dtype not in _FP8_CACHE or \
+                tuple(t.shape) != (NB, BS, H, half // 8):
+            raise ValueError("block scales must be float8_e4m3fn (or uint8) "
+                             "[num_blocks, block_size, num_kv_heads, "
+                             "head_size / 16]")
+    if k_block_scale.stride() != v_block_scale.stride():
+        raise ValueError("both block scales must share their strides")
+    _scalar(k_scale, "k_scale")
+    _scalar(v_scale, "v_scale")
+    f = _Fp4Scales()
+    f.k_block_scale = k_block_scale.data_ptr()
+    f.v_block_scale = v_block_scale.data_ptr()
+    f.strides = (ctypes.c_int64 * 4)(*k_block_scale.stride())
+    f.k_scale = k_scale.data_ptr()
+    f.v_scale = v_scale.data_ptr()
+    return f, half * 2
 
 
 PREFILL_TCGEN05 = 0
@@ -218,14 +334,23 @@ def check_device_errors(device=None):
 
 def reshape_and_cache_flash(key, value, key_cache, value_cache, slot_mapping,
                             kv_cache_dtype: str = "auto", k_scale=None,
-                            v_scale=None):
+                            v_scale=None, k_block_scale=None,
+                            v_block_scale=None):
     """Scatter key/value [>= T, Hkv, D] into the paged cache at slot_mapping.
 
     T = len(slot_mapping); padded rows of key/value are ignored and slots < 0
     are skipped.  key_cache/value_cache are [num_blocks, block_size, Hkv, D]
     views (e.g. ``kv_cache.unbind(0)``), any strides with D contiguous.
+    With "fp4" they hold the codes of a 4-bit cache (see ``fp4_kv_cache``)
+    and k_block_scale / v_block_scale its block scales.
     """
     lib = load_library()
+    if kv_cache_dtype == "fp4":
+        return _reshape_and_cache_fp4(lib, key, value, key_cache, value_cache,
+                                      slot_mapping, k_scale, v_scale,
+                                      k_block_scale, v_block_scale)
+    if k_block_scale is not None or v_block_scale is not None:
+        raise ValueError("block scales need kv_cache_dtype 'fp4'")
     if slot_mapping.dtype != torch.int64:
         raise ValueError("slot_mapping must be int64")
     if key.stride(-1) != 1 or value.stride(-1) != 1:
@@ -247,6 +372,268 @@ def reshape_and_cache_flash(key, value, key_cache, value_cache, slot_mapping,
         _ptr(slot_mapping), slot_mapping.shape[0], H, D, BS, NB,
         _dtype(key), kv_cache_dtype.encode(), _ptr(k_scale), _ptr(v_scale),
         _stream(key)))
+
+
+def _check_rows(t, what, heads, head_size, tokens):
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != head_size or \
+            t.shape[0] < tokens:
+        raise ValueError("%s must be [>= %d, %d, %d], not %s" %
+                         (what, tokens, heads, head_size, tuple(t.shape)))
+    if t.stride(2) != 1:
+        raise ValueError("%s head_size dim must be contiguous" % what)
+
+
+def _check_slots(slot_mapping):
+    if slot_mapping.dtype != torch.int64 or slot_mapping.dim() != 1 or \
+            (slot_mapping.shape[0] > 1 and slot_mapping.stride(0) != 1):
+        raise ValueError("slot_mapping must be a contiguous int64 vector")
+
+
+def _reshape_and_cache_fp4(lib, key, value, key_cache, value_cache,
+                           slot_mapping, k_scale, v_scale, k_block_scale,
+                           v_block_scale):
+    _check_slots(slot_mapping)
+    cs = _cache_strides(key_cache, value_cache)
+    f, D = _fp4_scales(key_cache, value_cache, k_block_scale, v_block_scale,
+                       k_scale, v_scale)
+    NB, BS, H, _ = key_cache.shape
+    n = slot_mapping.shape[0]
+    _check_rows(key, "key", H, D, n)
+    _check_rows(value, "value", H, D, n)
+    if value.dtype != key.dtype:
+        raise ValueError("key and value must share a dtype")
+    dev = _on_device(key, value, key_cache, value_cache, slot_mapping,
+                     k_scale, v_scale, k_block_scale, v_block_scale)
+    _call(dev, lib.pkv_reshape_and_cache_fp4, key.data_ptr(),
+          value.data_ptr(), key.stride(0), key.stride(1), value.stride(0),
+          value.stride(1), key_cache.data_ptr(), value_cache.data_ptr(), cs,
+          ctypes.byref(f), slot_mapping.data_ptr(), n, H, D, BS, NB,
+          _dtype(key))
+
+
+def fp4_kv_cache(num_blocks, block_size, num_kv_heads, head_size,
+                 device="cuda"):
+    """An empty 4-bit cache: (kv_cache, block_scale).
+
+    kv_cache uint8 [2, num_blocks, block_size, num_kv_heads, head_size / 2]
+    (two E2M1 codes a byte, the lower index in the lower four bits) and
+    block_scale float8_e4m3fn [2, ..., head_size / 16]; index 0 is K, 1 is V.
+    Both are zero, laid out with each (block, head) contiguous.
+    """
+    if head_size % 64 != 0:
+        raise NotImplementedError("a 4-bit cache needs a head_size that is a "
+                                  "multiple of 64")
+    if block_size <= 0 or block_size % 16 != 0:
+        raise ValueError("block_size must be a multiple of 16")
+    shape = (2, num_blocks, num_kv_heads, block_size)
+    codes = torch.zeros(shape + (head_size // 2,), dtype=torch.uint8,
+                        device=device)
+    scale = torch.zeros(shape + (head_size // 16,), dtype=torch.uint8,
+                        device=device).view(torch.float8_e4m3fn)
+    return codes.transpose(2, 3), scale.transpose(2, 3)
+
+
+def dequantize_fp4_cache(codes, block_scale, scale, dtype=None, out=None,
+                         block_ids=None):
+    """Values of one matrix of a 4-bit cache, [num_blocks, block_size, Hkv,
+    D] in ``dtype`` (or into ``out``): code * block_scale * scale.
+
+    block_ids (int64 vector) picks the blocks, in its order; ids outside the
+    cache give zeros and are flagged (``check_device_errors``).
+    """
+    lib = load_library()
+    if codes.dim() != 4:
+        raise ValueError("codes must be [num_blocks, block_size, "
+                         "num_kv_heads, head_size / 2]")
+    f, D = _fp4_scales(codes, codes, block_scale, block_scale, scale, scale)
+    NB, BS, H, _ = codes.shape
+    if block_ids is not None:
+        if block_ids.dtype != torch.int64 or block_ids.dim() != 1 or \
+                (block_ids.shape[0] > 1 and block_ids.stride(0) != 1):
+            raise ValueError("block_ids must be a contiguous int64 vector")
+    n = NB if block_ids is None else block_ids.shape[0]
+    if out is None:
+        if dtype is None:
+            raise ValueError("dequantize_fp4_cache needs dtype or out")
+        out = torch.empty((n, BS, H, D), dtype=dtype, device=codes.device)
+    elif tuple(out.shape) != (n, BS, H, D) or not out.is_contiguous() or \
+            (dtype is not None and out.dtype != dtype):
+        raise ValueError("out must be contiguous %s of dtype" %
+                         ((n, BS, H, D),))
+    dt = _dtype(out)
+    dev = _on_device(codes, block_scale, scale, out, block_ids)
+    strides = (ctypes.c_int64 * 4)(*codes.stride())
+    _call(dev, lib.pkv_dequantize_fp4_cache, codes.data_ptr(), strides,
+          block_scale.data_ptr(), f.strides, scale.data_ptr(),
+          _addr(block_ids), n, H, D, BS, NB, out.data_ptr(), dt)
+    return out
+
+
+# ------------------------------------------------- head norms and rotation
+
+def _rope_params(q, positions, cos_sin_cache, q_weight, k_weight, eps,
+                 is_neox, mrope_section, mrope_interleaved, weight_offset,
+                 tokens, head_size):
+    if positions.dtype != torch.int64 or positions.dim() not in (1, 2) or \
+            (positions.shape[-1] > 1 and positions.stride(-1) != 1):
+        raise ValueError("positions must be int64 [tokens] or [axes, tokens] "
+                         "with contiguous rows")
+    if positions.shape[-1] < tokens:
+        raise ValueError("positions has %d tokens, %d are needed" %
+                         (positions.shape[-1], tokens))
+    if cos_sin_cache.dim() != 2 or (cos_sin_cache.shape[1] > 1 and
+                                    cos_sin_cache.stride(1) != 1):
+        raise ValueError("cos_sin_cache must be [max_position, rot_dim] with "
+                         "contiguous rows")
+    if cos_sin_cache.dtype not in (torch.float32, q.dtype):
+        raise ValueError("cos_sin_cache must be float32 or of q's dtype")
+    if (q_weight is None) != (k_weight is None):
+        raise ValueError("q_weight and k_weight go together (both or "
+                         "neither)")
+    r = _RopeParams()
+    axes = positions.shape[0] if positions.dim() == 2 else 1
+    if mrope_section is None:
+        if axes != 1:
+            raise ValueError("positions of several axes need mrope_section")
+    else:
+        if len(mrope_section) != axes or axes > 4:
+            raise ValueError("mrope_section must give one count for each of "
+                             "1 to 4 axes of positions")
+        for i, n in enumerate(mrope_section):
+            r.sections[i] = n
+    for w in (q_weight, k_weight):
+        if w is not None and (w.dtype != q.dtype or
+                              tuple(w.shape) != (head_size,) or
+                              w.stride(0) != 1):
+            raise ValueError("norm weights must be contiguous [head_size] of "
+                             "q's dtype")
+    r.positions = positions.data_ptr()
+    r.position_axis_stride = positions.stride(0) if axes > 1 else 0
+    r.num_axes = axes
+    r.interleaved_axes = 1 if mrope_interleaved and axes > 1 else 0
+    r.cos_sin = cos_sin_cache.data_ptr()
+    r.max_position = cos_sin_cache.shape[0]
+    r.cos_sin_stride = cos_sin_cache.stride(0) if r.max_position > 1 else \
+        cos_sin_cache.shape[1]
+    r.cos_sin_f32 = 1 if cos_sin_cache.dtype == torch.float32 else 0
+    r.rot_dim = cos_sin_cache.shape[1]
+    r.is_neox = 1 if is_neox else 0
+    r.q_weight = _addr(q_weight)
+    r.k_weight = _addr(k_weight)
+    r.eps = eps
+    r.weight_offset = weight_offset
+    return r
+
+
+def qk_norm_rope(q, k, positions, cos_sin_cache, q_weight=None,
+                 k_weight=None, eps=1e-6, is_neox=True, mrope_section=None,
+                 mrope_interleaved=False, weight_offset=0.0, q_out=None,
+                 k_out=None):
+    """RMS norm of every head of q and k (with q_weight and k_weight [D]),
+    then the rotary rotation, in one pass; returns (q_out, k_out).
+
+    q [T, Hq, D], k [T, Hkv, D], any token and head strides.  cos_sin_cache
+    [max_position, rot_dim] holds cos then sin of rot_dim / 2 pairs (float32
+    or q's dtype); the pairs are (i, i + rot_dim / 2), or neighbours without
+    ``is_neox``.  The norm weight is ``weight + weight_offset``.  positions
+    int64 [T], or [axes, T] with ``mrope_section``, the pairs that each axis
+    rotates (in runs, or interleaved).  Tokens with a negative position are
+    padding: their output rows stay as they were.  q_out and k_out may be q
+    and k themselves.
+    """
+    lib = load_library()
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError("q and k must be [tokens, heads, head_size]")
+    T, Hq, D = q.shape
+    Hkv = k.shape[1]
+    if q_out is None:
+        q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+    if k_out is None:
+        k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
+    _check_rows(q, "q", Hq, D, T)
+    _check_rows(k, "k", Hkv, D, T)
+    _check_rows(q_out, "q_out", Hq, D, T)
+    _check_rows(k_out, "k_out", Hkv, D, T)
+    if not (q.dtype == k.dtype == q_out.dtype == k_out.dtype):
+        raise ValueError("q, k, q_out and k_out must share a dtype")
+    dt = _dtype(q)
+    r = _rope_params(q, positions, cos_sin_cache, q_weight, k_weight, eps,
+                     is_neox, mrope_section, mrope_interleaved,
+                     weight_offset, T, D)
+    dev = _on_device(q, k, positions, cos_sin_cache, q_weight, k_weight,
+                     q_out, k_out)
+    _call(dev, lib.pkv_qk_norm_rope, q.data_ptr(), q.stride(0), q.stride(1),
+          k.data_ptr(), k.stride(0), k.stride(1), q_out.data_ptr(),
+          q_out.stride(0), q_out.stride(1), k_out.data_ptr(),
+          k_out.stride(0), k_out.stride(1), T, Hq, Hkv, D, ctypes.byref(r),
+          dt)
+    return q_out, k_out
+
+
+def rope_reshape_and_cache(q, k, v, key_cache, value_cache, slot_mapping,
+                           positions, cos_sin_cache, kv_cache_dtype="auto",
+                           k_scale=None, v_scale=None, k_block_scale=None,
+                           v_block_scale=None, q_weight=None, k_weight=None,
+                           eps=1e-6, is_neox=True, mrope_section=None,
+                           mrope_interleaved=False, weight_offset=0.0,
+                           q_out=None):
+    """``qk_norm_rope`` with the rotated keys and the values v appended to
+    the paged cache (``reshape_and_cache_flash``) in the same pass; returns
+    q_out.
+
+    T = len(slot_mapping) tokens; rows of q, k and v past it are ignored.
+    Every token's query is written, also where its slot is negative (its key
+    and value are then not stored).  kv_cache_dtype: "auto", "fp8" or "fp4".
+    """
+    lib = load_library()
+    _check_slots(slot_mapping)
+    T = slot_mapping.shape[0]
+    if q.dim() != 3:
+        raise ValueError("q must be [tokens, heads, head_size]")
+    Hq, D = q.shape[1], q.shape[2]
+    cs = _cache_strides(key_cache, value_cache)
+    NB, BS, H, Dc = key_cache.shape
+    fp4 = None
+    scales = (None, None)
+    if kv_cache_dtype == "fp4":
+        f, Dc = _fp4_scales(key_cache, value_cache, k_block_scale,
+                            v_block_scale, k_scale, v_scale)
+        fp4 = ctypes.byref(f)
+    elif k_block_scale is not None or v_block_scale is not None:
+        raise ValueError("block scales need kv_cache_dtype 'fp4'")
+    elif kv_cache_dtype.startswith("fp8"):
+        if key_cache.dtype not in _FP8_CACHE or \
+                value_cache.dtype not in _FP8_CACHE:
+            raise ValueError("an fp8 cache must be float8_e4m3fn or uint8")
+        _scalar(k_scale, "k_scale")
+        _scalar(v_scale, "v_scale")
+        scales = (k_scale.data_ptr(), v_scale.data_ptr())
+    elif key_cache.dtype != q.dtype or value_cache.dtype != q.dtype:
+        raise ValueError("cache dtype must match q's for 'auto'")
+    if Dc != D:
+        raise ValueError("q and cache head_size differ (%d and %d)" % (D, Dc))
+    if q_out is None:
+        q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+    _check_rows(q, "q", Hq, D, T)
+    _check_rows(k, "k", H, D, T)
+    _check_rows(v, "v", H, D, T)
+    _check_rows(q_out, "q_out", Hq, D, T)
+    if not (q.dtype == k.dtype == v.dtype == q_out.dtype):
+        raise ValueError("q, k, v and q_out must share a dtype")
+    dt = _dtype(q)
+    r = _rope_params(q, positions, cos_sin_cache, q_weight, k_weight, eps,
+                     is_neox, mrope_section, mrope_interleaved,
+                     weight_offset, T, D)
+    dev = _on_device(q, k, v, key_cache, value_cache, slot_mapping,
+                     positions, cos_sin_cache, k_scale, v_scale,
+                     k_block_scale, v_block_scale, q_weight, k_weight, q_out)
+    _call(dev, lib.pkv_rope_reshape_and_cache, q.data_ptr(), q.stride(0),
+          q.stride(1), k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(),
+          v.stride(0), v.stride(1), q_out.data_ptr(), q_out.stride(0),
+          q_out.stride(1), key_cache.data_ptr(), value_cache.data_ptr(), cs,
+          slot_mapping.data_ptr(), T, Hq, H, D, BS, NB, ctypes.byref(r), dt,
+          kv_cache_dtype.encode(), scales[0], scales[1], fp4)
+    return q_out
 
 
 def scaled_fp8_quant(input, scale, out=None):
@@ -303,7 +690,8 @@ def flash_attn_varlen_func(q, k, v, max_seqlen_q, cu_seqlens_q, max_seqlen_k,
                            cu_seqlens_k=None, workspace=None, s_aux=None,
                            k_descale=None, v_descale=None,
                            fixed_split_size=0, q_descale=None,
-                           enable_pdl=True):
+                           enable_pdl=True, k_block_scale=None,
+                           v_block_scale=None):
     """Varlen attention over a paged KV cache, or over plain K/V rows.
 
     q [T, Hq, D].  Paged: k, v are cache views [num_blocks, block_size, Hkv,
@@ -315,6 +703,8 @@ def flash_attn_varlen_func(q, k, v, max_seqlen_q, cu_seqlens_q, max_seqlen_k,
     scale as ``q_descale`` and ``out`` (which names the output type).
     ``enable_pdl=False`` launches every kernel in plain stream order
     (``no_pdl`` in pkv_attention_options).
+    With k_block_scale and v_block_scale, k and v are the codes of a 4-bit
+    cache (see ``fp4_kv_cache``) and k_descale / v_descale its tensor scales.
     Returns out (and lse [Hq, T] float32 when return_softmax_lse).
     """
     lib = load_library()
@@ -347,11 +737,24 @@ def flash_attn_varlen_func(q, k, v, max_seqlen_q, cu_seqlens_q, max_seqlen_k,
             raise ValueError("block_table rows must be contiguous")
         batch = seqused_k.shape[0]
         cs = _cache_strides(k, v)
-        max_blocks, bt_stride = block_table.shape[1], block_table.stride(0)
+        max_blocks = block_table.shape[1]
+        # (the row stride of a single request's table says nothing)
+        bt_stride = block_table.stride(0) if block_table.shape[0] > 1 else \
+            max_blocks
+    kv4 = k_block_scale is not None or v_block_scale is not None
+    q8 = q.dtype in _FP8_CACHE
+    if kv4:
+        if nonpaged or q8:
+            raise NotImplementedError("a 4-bit cache is paged, with a 16-bit "
+                                      "query")
+        fp4, Dk = _fp4_scales(k, v, k_block_scale, v_block_scale, k_descale,
+                              v_descale)
+        dev = _on_device(q, k, v, k_block_scale, v_block_scale, k_descale,
+                         v_descale, cu_seqlens_q, seqused_k, block_table,
+                         alibi_slopes, s_aux, out, workspace)
     if Dk != D:
         raise ValueError("q and k head_size differ")
-    kv8 = k.dtype in _FP8_CACHE
-    q8 = q.dtype in _FP8_CACHE
+    kv8 = not kv4 and k.dtype in _FP8_CACHE
     if q8:
         if not kv8:
             raise NotImplementedError("an fp8 query needs an fp8 cache")
@@ -366,7 +769,7 @@ def flash_attn_varlen_func(q, k, v, max_seqlen_q, cu_seqlens_q, max_seqlen_k,
         if v.dtype not in _FP8_CACHE or k_descale is None or \
                 v_descale is None:
             raise ValueError("an fp8 cache needs k_descale and v_descale")
-    elif k.dtype != q.dtype or v.dtype != q.dtype:
+    elif not kv4 and (k.dtype != q.dtype or v.dtype != q.dtype):
         raise NotImplementedError("q and cache dtypes must match")
     if cu_seqlens_q.dtype != torch.int32:
         raise ValueError("cu_seqlens_q must be int32")
@@ -399,7 +802,9 @@ def flash_attn_varlen_func(q, k, v, max_seqlen_q, cu_seqlens_q, max_seqlen_k,
         opts.total_k = k.shape[0]
     opts.fixed_split_size = int(fixed_split_size)
     opts.no_pdl = 0 if enable_pdl else 1
-    ws_need = lib.pkv_paged_attention_workspace_size_opts(
+    size = lib.pkv_paged_attention_workspace_size_fp4 if kv4 else \
+        lib.pkv_paged_attention_workspace_size_opts
+    ws_need = size(
         batch, T, max_seqlen_q, max_seqlen_k, Hq, Hkv, D, BS,
         int(bool(causal)), int(window_size[0]), int(window_size[1]),
         num_splits, max_blocks, ctypes.byref(opts))
@@ -411,6 +816,20 @@ def flash_attn_varlen_func(q, k, v, max_seqlen_q, cu_seqlens_q, max_seqlen_k,
         workspace.element_size()
     if alibi_slopes is not None and alibi_slopes.dtype != torch.float32:
         raise ValueError("alibi_slopes must be float32")
+    if kv4:
+        if out.shape != q.shape or out.stride(-1) != 1:
+            raise ValueError("out must have q's shape, D contiguous")
+        _call4(dev, lib.pkv_paged_attention_varlen_fp4, opts, q.data_ptr(),
+               q.stride(0), q.stride(1), k.data_ptr(), v.data_ptr(), cs,
+               ctypes.byref(fp4), out.data_ptr(), out.stride(0),
+               out.stride(1), cu_seqlens_q.data_ptr(), seqused_k.data_ptr(),
+               batch, T, int(max_seqlen_q), int(max_seqlen_k),
+               block_table.data_ptr(), bt_stride, max_blocks, Hq, Hkv, D, BS,
+               NB, float(softmax_scale), int(bool(causal)),
+               int(window_size[0]), int(window_size[1]),
+               float(softcap or 0.0), _addr(alibi_slopes), int(num_splits),
+               _addr(lse), _addr(workspace), ws_bytes, _dtype(out))
+        return (out, lse) if return_softmax_lse else out
     _check(lib.pkv_paged_attention_varlen_opts(
         _ptr(q), q.stride(0), q.stride(1), _ptr(k), _ptr(v), cs, _ptr(out),
         out.stride(0), out.stride(1), _ptr(cu_seqlens_q), _ptr(seqused_k),
@@ -533,6 +952,9 @@ def cascade_attention(output, query, key_cache, value_cache, cu_query_lens,
         raise ValueError("Cascade attention does not support sliding window.")
     T, Hq, D = query.shape
     NB, BS, Hkv, Dk = key_cache.shape
+    if Dk != D:
+        raise ValueError("query and cache head_size differ (a 4-bit cache "
+                         "has no cascade call)")
     if common_prefix_len % BS != 0:
         raise ValueError("common_prefix_len must be a multiple of block_size")
     if common_prefix_len <= 0:

@@ -1,0 +1,272 @@
+// 4-bit KV cache: the quantizing write and the read-back.
+//
+// A cache row of D values is D / 2 bytes of E2M1 codes (two to a byte, the
+// lower index in the lower four bits) and D / 16 E4M3 scales, one for each 16
+// values; one float32 scale covers the whole tensor.  A value reads back as
+// code * block scale * tensor scale.  The code (2 significant bits) times the
+// block scale (4) has at most 6, and its exponent fits both 16-bit types, so
+// that product is exact in bf16 and f16: the prefill kernels run on exact
+// 16-bit copies of the pages and fold the tensor scales into the logit scale
+// and the output, as they do for E4M3 caches.
+//
+// All three kernels stream: HBM bounds them (the write reads 2 D and writes
+// D / 2 + D / 16 bytes a row, the read-back the reverse).  A thread owns one
+// group of 16 values, so a group's maximum, its scale and its codes never
+// leave the thread.
+#include "pkv_common.cuh"
+
+namespace pkv {
+namespace {
+
+constexpr int kThreads = 256;
+
+// 16 consecutive 16-bit values at src (16-byte aligned) -> 8 bytes of codes
+// and the group's scale.
+template <typename T>
+__device__ __forceinline__ void quantize16(const T* src, float scale,
+                                           uint8_t* codes, uint8_t* sf) {
+  const uint4 r0 = *reinterpret_cast<const uint4*>(src);
+  const uint4 r1 = *reinterpret_cast<const uint4*>(src + 8);
+  float x[16];
+  widen8<T>(r0, x);
+  widen8<T>(r1, x + 8);
+  float top = 0.f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) top = max_nan(top, fabsf(x[i]));
+  const Fp4Scale s = fp4_scale(top, scale);
+  *reinterpret_cast<uint2*>(codes) =
+      make_uint2(fp4_codes8(x, s.inv), fp4_codes8(x + 8, s.inv));
+  *sf = static_cast<uint8_t>(s.code);
+}
+
+// One group of 16 codes and its scale -> 16 values; with `scaled`, times
+// `scale` before the rounding to T (else the exact product alone).
+template <typename T>
+__device__ __forceinline__ void dequantize16(uint2 codes, uint8_t sf,
+                                             bool scaled, float scale,
+                                             uint4* out) {
+  const uint32_t s2 = e4m3x2_to_f16(sf * 0x0101u);
+  uint32_t o[8];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t f[4];
+    e2m1x8_to_f16(h ? codes.y : codes.x, f[0], f[1], f[2], f[3]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t v = hmul2_u32(f[i], s2);
+      const __half2 hv = *reinterpret_cast<const __half2*>(&v);
+      float a = __low2float(hv), b = __high2float(hv);
+      if (scaled) {
+        a = __fmul_rn(a, scale);
+        b = __fmul_rn(b, scale);
+      }
+      o[4 * h + i] = pack2<T>(a, b);
+    }
+  }
+  out[0] = make_uint4(o[0], o[1], o[2], o[3]);
+  out[1] = make_uint4(o[4], o[5], o[6], o[7]);
+}
+
+// The block's threads cover whole tokens: thread i takes group i % per_token
+// of token i / per_token (a token with more groups than threads is looped
+// over), so the index math runs once per thread.
+template <typename T>
+__global__ void __launch_bounds__(kThreads)
+cache_write_fp4_kernel(const T* __restrict__ key, const T* __restrict__ value,
+                       int64_t k_st, int64_t k_sh, int64_t v_st, int64_t v_sh,
+                       uint8_t* __restrict__ kc, uint8_t* __restrict__ vc,
+                       int64_t c_sb, int64_t c_sr, int64_t c_sh,
+                       uint8_t* __restrict__ k_sf, uint8_t* __restrict__ v_sf,
+                       int64_t f_sb, int64_t f_sr, int64_t f_sh,
+                       const int64_t* __restrict__ slots, int64_t num_tokens,
+                       int groups, int per_token, int tokens_per_block,
+                       int BS, int64_t num_slots,
+                       const float* __restrict__ k_scale,
+                       const float* __restrict__ v_scale, unsigned* err) {
+  // an attention kernel queued next as a programmatic dependent may become
+  // resident now (it waits for this grid before reading the cache)
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int tl = threadIdx.x / per_token;
+  if (tl >= tokens_per_block) return;
+  const int r0 = threadIdx.x - tl * per_token;
+  const float ks = *k_scale, vs = *v_scale;
+  for (int64_t t = static_cast<int64_t>(blockIdx.x) * tokens_per_block + tl;
+       t < num_tokens; t += static_cast<int64_t>(gridDim.x) *
+                            tokens_per_block) {
+    const int64_t s = __ldg(slots + t);
+    if (s < 0) continue;                          // padding slot
+    if (s >= num_slots) {                         // outside the cache: skip
+      if (r0 == 0) atomicOr(err, kErrBadSlot);
+      continue;
+    }
+    const int64_t blk = s / BS;
+    const int64_t off = s - blk * BS;
+    for (int r = r0; r < per_token; r += kThreads) {
+      const int h = r / groups, g = r - h * groups;
+      const int64_t c = blk * c_sb + off * c_sr + h * c_sh + g * 8;
+      const int64_t f = blk * f_sb + off * f_sr + h * f_sh + g;
+      quantize16<T>(key + t * k_st + h * k_sh + g * 16, ks, kc + c, k_sf + f);
+      quantize16<T>(value + t * v_st + h * v_sh + g * 16, vs, vc + c,
+                    v_sf + f);
+    }
+  }
+}
+
+// One matrix of one block of rows: [BS, Hkv, D] values from its codes.
+template <typename T>
+__device__ __forceinline__ void dequantize_block(
+    const uint8_t* codes, const uint8_t* sf, int64_t c_sr, int64_t c_sh,
+    int64_t f_sr, int64_t f_sh, int BS, int Hkv, int groups, bool bad,
+    bool scaled, float scale, T* out) {
+  const int per_row = Hkv * groups;
+  for (int e = threadIdx.x; e < BS * per_row; e += blockDim.x) {
+    const int row = e / per_row;
+    const int rem = e - row * per_row;
+    const int h = rem / groups, g = rem - h * groups;
+    uint4 v[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+    if (!bad)
+      dequantize16<T>(
+          *reinterpret_cast<const uint2*>(
+              codes + static_cast<int64_t>(row) * c_sr +
+              static_cast<int64_t>(h) * c_sh + g * 8),
+          sf[static_cast<int64_t>(row) * f_sr +
+             static_cast<int64_t>(h) * f_sh + g],
+          scaled, scale, v);
+    uint4* dst = reinterpret_cast<uint4*>(out + static_cast<int64_t>(e) * 16);
+    dst[0] = v[0];
+    dst[1] = v[1];
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads)
+fp4_dequant_blocks_kernel(const uint8_t* __restrict__ codes, int64_t c_sb,
+                          int64_t c_sr, int64_t c_sh,
+                          const uint8_t* __restrict__ sf, int64_t f_sb,
+                          int64_t f_sr, int64_t f_sh,
+                          const float* __restrict__ scale,
+                          const int64_t* __restrict__ ids, int64_t n,
+                          int64_t num_blocks, int Hkv, int groups, int BS,
+                          T* __restrict__ out, unsigned* err) {
+  const float sc = *scale;
+  for (int64_t i = blockIdx.x; i < n; i += gridDim.x) {
+    const int64_t blk = ids ? __ldg(ids + i) : i;
+    const bool bad = blk < 0 || blk >= num_blocks;
+    if (bad && threadIdx.x == 0) atomicOr(err, kErrBadBlock);
+    dequantize_block<T>(codes + (bad ? 0 : blk * c_sb),
+                        sf + (bad ? 0 : blk * f_sb), c_sr, c_sh, f_sr, f_sh,
+                        BS, Hkv, groups, bad, true, sc,
+                        out + i * BS * Hkv * groups * 16);
+  }
+}
+
+// The pages of prefill-class requests as exact 16-bit copies: page j of
+// request b is block b * max_blocks + j of the copies (the contract of
+// launch_fp8_dequant_pages).
+template <typename T>
+__global__ void __launch_bounds__(kThreads)
+fp4_dequant_pages_kernel(const AttnParams p, T* __restrict__ mock_k,
+                         T* __restrict__ mock_v, int32_t* __restrict__ table,
+                         int groups) {
+  const int64_t pages = static_cast<int64_t>(p.batch) * p.max_blocks;
+  const int64_t elems = static_cast<int64_t>(p.BS) * p.Hkv * groups * 16;
+  for (int64_t m = blockIdx.x; m < pages; m += gridDim.x) {
+    const int b = static_cast<int>(m / p.max_blocks);
+    const int j = static_cast<int>(m - static_cast<int64_t>(b) *
+                                           p.max_blocks);
+    if (threadIdx.x == 0) table[m] = static_cast<int32_t>(m);
+    const int q0 = p.cu_q[b];
+    const int q_len = min(p.cu_q[b + 1] - q0, p.total_q - q0);
+    if (q0 < 0 || q_len <= 0 || q_len * p.G < p.min_rows) continue;
+    const int64_t L_tab =
+        min(static_cast<int64_t>(p.seqused_k[b]),
+            static_cast<int64_t>(p.max_blocks) * p.BS);
+    if (static_cast<int64_t>(j) * p.BS >= L_tab) continue;
+    const int blk = p.block_table[static_cast<int64_t>(b) * p.bt_stride + j];
+    const bool bad = blk < 0 || blk >= p.num_blocks;
+    if (bad && threadIdx.x == 0) atomicOr(p.err, kErrBadBlock);
+    const int64_t c = bad ? 0 : blk * p.c_sb, f = bad ? 0 : blk * p.f_sb;
+    dequantize_block<T>(static_cast<const uint8_t*>(p.kc) + c, p.k_sf + f,
+                        p.c_sr, p.c_sh, p.f_sr, p.f_sh, p.BS, p.Hkv, groups,
+                        bad, false, 1.f, mock_k + m * elems);
+    dequantize_block<T>(static_cast<const uint8_t*>(p.vc) + c, p.v_sf + f,
+                        p.c_sr, p.c_sh, p.f_sr, p.f_sh, p.BS, p.Hkv, groups,
+                        bad, false, 1.f, mock_v + m * elems);
+  }
+}
+
+unsigned capped_grid(int64_t blocks, int per_sm) {
+  const int64_t cap = static_cast<int64_t>(current_sm_count()) * per_sm;
+  return static_cast<unsigned>(blocks < 1 ? 1 : blocks < cap ? blocks : cap);
+}
+
+}  // namespace
+
+cudaError_t launch_cache_write_fp4(
+    const void* key, const void* value, int64_t k_st, int64_t k_sh,
+    int64_t v_st, int64_t v_sh, void* kc, void* vc, const int64_t* cs,
+    uint8_t* k_sf, uint8_t* v_sf, const int64_t* fs, const int64_t* slots,
+    int64_t num_tokens, int Hkv, int D, int BS, int64_t num_blocks, bool bf16,
+    const float* k_scale, const float* v_scale, unsigned* err,
+    cudaStream_t stream) {
+  const int groups = D / 16, per_token = Hkv * groups;
+  const int tpb = per_token >= kThreads ? 1 : kThreads / per_token;
+  const unsigned grid = capped_grid((num_tokens + tpb - 1) / tpb, 32);
+  note_launch();
+  auto go = [&](auto kern, const auto* k, const auto* v) {
+    kern<<<grid, kThreads, 0, stream>>>(
+        k, v, k_st, k_sh, v_st, v_sh, static_cast<uint8_t*>(kc),
+        static_cast<uint8_t*>(vc), cs[0], cs[1], cs[2], k_sf, v_sf, fs[0],
+        fs[1], fs[2], slots, num_tokens, groups, per_token, tpb, BS,
+        num_blocks * BS, k_scale, v_scale, err);
+  };
+  if (bf16)
+    go(cache_write_fp4_kernel<__nv_bfloat16>,
+       static_cast<const __nv_bfloat16*>(key),
+       static_cast<const __nv_bfloat16*>(value));
+  else
+    go(cache_write_fp4_kernel<__half>, static_cast<const __half*>(key),
+       static_cast<const __half*>(value));
+  return cudaGetLastError();
+}
+
+cudaError_t launch_fp4_dequant_blocks(const void* codes, const int64_t* cs,
+                                      const uint8_t* sf, const int64_t* fs,
+                                      const float* scale, const int64_t* ids,
+                                      int64_t n, int64_t num_blocks, int Hkv,
+                                      int D, int BS, void* out, bool bf16,
+                                      unsigned* err, cudaStream_t stream) {
+  const unsigned grid = capped_grid(n, 16);
+  note_launch();
+  if (bf16)
+    fp4_dequant_blocks_kernel<__nv_bfloat16><<<grid, kThreads, 0, stream>>>(
+        static_cast<const uint8_t*>(codes), cs[0], cs[1], cs[2], sf, fs[0],
+        fs[1], fs[2], scale, ids, n, num_blocks, Hkv, D / 16, BS,
+        static_cast<__nv_bfloat16*>(out), err);
+  else
+    fp4_dequant_blocks_kernel<__half><<<grid, kThreads, 0, stream>>>(
+        static_cast<const uint8_t*>(codes), cs[0], cs[1], cs[2], sf, fs[0],
+        fs[1], fs[2], scale, ids, n, num_blocks, Hkv, D / 16, BS,
+        static_cast<__half*>(out), err);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_fp4_dequant_pages(const AttnParams& p, int D, bool bf16,
+                                     void* mock_k, void* mock_v,
+                                     int32_t* mock_table,
+                                     cudaStream_t stream) {
+  const unsigned grid =
+      capped_grid(static_cast<int64_t>(p.batch) * p.max_blocks, 16);
+  note_launch();
+  if (bf16)
+    fp4_dequant_pages_kernel<__nv_bfloat16><<<grid, kThreads, 0, stream>>>(
+        p, static_cast<__nv_bfloat16*>(mock_k),
+        static_cast<__nv_bfloat16*>(mock_v), mock_table, D / 16);
+  else
+    fp4_dequant_pages_kernel<__half><<<grid, kThreads, 0, stream>>>(
+        p, static_cast<__half*>(mock_k), static_cast<__half*>(mock_v),
+        mock_table, D / 16);
+  return cudaGetLastError();
+}
+
+}  // namespace pkv

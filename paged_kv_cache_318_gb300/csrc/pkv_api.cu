@@ -112,9 +112,26 @@ struct Plan {
 
 size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
+// Pieces of a request's key range for the 4-bit decode kernel.
+int fp4_splits(int batch, int max_q, int G, int Hkv, int D, int64_t range,
+               int sms) {
+  const int64_t rows = static_cast<int64_t>(max_q) * G;
+  const int64_t units = static_cast<int64_t>(batch) * Hkv;
+  const int64_t slots =
+      static_cast<int64_t>(sms) *
+      decode_fp4_ctas_per_sm(D, rows < kDecodeRows ? static_cast<int>(rows)
+                                                   : kDecodeRows);
+  int64_t s = (4 * slots + units - 1) / units;
+  const int64_t most = (range + 255) / 256, least = (range + 2047) / 2048;
+  if (s > most) s = most;
+  if (s < least) s = least;
+  if (s > 512) s = 512;
+  return s < 1 ? 1 : static_cast<int>(s);
+}
+
 Plan make_plan(int batch, int total_q, int max_q, int max_k, int Hq, int Hkv,
                int D, int causal, int wl, int wr, int num_splits, int sms,
-               int fixed_split = 0) {
+               int fixed_split = 0, bool kv4 = false) {
   Plan pl;
   const int G = Hq / Hkv;
   if (batch == 0 || max_q == 0) return pl;
@@ -161,6 +178,8 @@ Plan make_plan(int batch, int total_q, int max_q, int max_k, int Hq, int Hkv,
     // plan made above
   } else if (num_splits > 1) {
     splits = num_splits;
+  } else if (num_splits == 0 && range > 0 && kv4) {
+    splits = fp4_splits(batch, max_q, G, Hkv, D, range, sms);
   } else if (num_splits == 0 && range > 0) {
     // Split only to fill the GPU: with at least one (request, KV head) per
     // resident CTA slot the requests' own length spread balances the SMs,
@@ -323,6 +342,29 @@ pkv_status check_attn_shape(int batch, int total_q, int max_q, int max_k,
   return PKV_OK;
 }
 
+// The 4-bit cache's scales (see pkv_fp4_scales).
+pkv_status check_fp4(const pkv_fp4_scales* f, int head_size) {
+  if (!f) return fail(PKV_ERR_INVALID_ARG, "a 4-bit cache needs its scales");
+  if (head_size % 64 != 0)
+    return fail(PKV_ERR_UNSUPPORTED,
+                "a 4-bit cache needs a head_size that is a multiple of 64");
+  if (!f->k_block_scale || !f->v_block_scale || !f->k_scale || !f->v_scale)
+    return fail(PKV_ERR_INVALID_ARG,
+                "a 4-bit cache needs block scales, k_scale and v_scale");
+  if (f->strides[3] != 1)
+    return fail(PKV_ERR_INVALID_ARG, "block scale rows must be contiguous");
+  const int a = head_size / 64;         // 1, 2 or 4 bytes a quarter row
+  const int unit = a % 4 == 0 ? 4 : a % 2 == 0 ? 2 : 1;
+  auto on = [&](const void* q) {
+    return reinterpret_cast<uintptr_t>(q) % unit == 0;
+  };
+  if (!on(f->k_block_scale) || !on(f->v_block_scale) ||
+      f->strides[0] % unit || f->strides[1] % unit || f->strides[2] % unit)
+    return fail(PKV_ERR_UNSUPPORTED,
+                "block scale rows must start on %d-byte boundaries", unit);
+  return PKV_OK;
+}
+
 }  // namespace
 
 // The workspace a call cannot do without (no prefill counter or split
@@ -436,17 +478,21 @@ pkv_status pkv_check_device_errors(pkv_stream_t stream) {
       (host & kErrQueryLen) ? " a request with more queries than "
                               "max_seqlen_q (not computed);"
                             : "",
+      (host & kErrBadPosition) ? " position past the rotation table (token "
+                                 "skipped);"
+                               : "",
       (host & kErrSmemAlign) ? " shared memory not 1024-byte aligned (the "
                                "kernel did nothing);"
                              : ""};
   const pkv_status code =
       (host & kErrTimeout)
           ? PKV_ERR_TIMEOUT
-          : (host & (kErrBadBlock | kErrBadSlot | kErrBadTable | kErrQueryLen))
+          : (host & (kErrBadBlock | kErrBadSlot | kErrBadTable |
+                     kErrQueryLen | kErrBadPosition))
                 ? PKV_ERR_BAD_INDEX
                 : PKV_ERR_CUDA;
-  return fail(code, "device error word 0x%x:%s%s%s%s%s%s", host, what[0],
-              what[1], what[2], what[3], what[4], what[5]);
+  return fail(code, "device error word 0x%x:%s%s%s%s%s%s%s", host, what[0],
+              what[1], what[2], what[3], what[4], what[5], what[6]);
 }
 
 pkv_status pkv_reshape_and_cache(
@@ -530,7 +576,7 @@ size_t workspace_bytes_impl(int batch, int total_q, int max_seqlen_q,
                             int window_left, int window_right, int num_splits,
                             int max_blocks_per_seq,
                             const pkv_attention_options* opts,
-                            int pre_splits) {
+                            int pre_splits, bool kv4 = false) {
   const int bs = non_paged(opts) ? 16 : block_size;
   if (check_attn_shape(batch, total_q, max_seqlen_q, max_seqlen_k, num_heads,
                        num_kv_heads, head_size, bs, num_splits) != PKV_OK)
@@ -544,7 +590,7 @@ size_t workspace_bytes_impl(int batch, int total_q, int max_seqlen_q,
                 num_kv_heads, head_size, causal,
                 window_left < 0 ? -1 : window_left,
                 window_right < 0 ? -1 : window_right, num_splits, sms,
-                fixed_split_of(opts));
+                fixed_split_of(opts), kv4);
   const bool fp8 = opts && opts->kv_cache_fp8;
   const size_t split_bytes = prefill_split_bytes(
       !pl.prefill ? 1
@@ -556,12 +602,12 @@ size_t workspace_bytes_impl(int batch, int total_q, int max_seqlen_q,
       total_q, num_heads, head_size);
   const bool q8 = fp8 && q_fp8_of(opts);
   const size_t skb =
-      sk_candidate(num_splits, fixed_split_of(opts), head_size, fp8)
+      !kv4 && sk_candidate(num_splits, fixed_split_of(opts), head_size, fp8)
           ? sk_scratch_bytes(head_size, fp8, q8, sms,
                              sk_rows(num_heads / num_kv_heads, max_seqlen_q))
           : 0;
   size_t need = pl.workspace;
-  if (fp8 && pl.prefill) {
+  if ((fp8 || kv4) && pl.prefill) {
     if (max_blocks_per_seq <= 0) return static_cast<size_t>(-1);
     need = align256(pl.workspace) +
            fp8_mock_bytes(batch, max_blocks_per_seq, block_size, num_kv_heads,
@@ -672,7 +718,8 @@ pkv_status attention_impl(
     int window_left, int window_right, float softcap,
     const float* alibi_slopes, int num_splits, float* softmax_lse,
     void* workspace, size_t workspace_bytes, pkv_dtype dtype,
-    pkv_stream_t stream, const pkv_attention_options* opts, Internal* in) {
+    pkv_stream_t stream, const pkv_attention_options* opts, Internal* in,
+    const pkv_fp4_scales* fp4 = nullptr) {
   int* pdl_done = in ? in->pdl_done : nullptr;
   const bool nonpaged = non_paged(opts);
   pkv_status st = check_attn_shape(batch, total_q, max_seqlen_q, max_seqlen_k,
@@ -720,7 +767,16 @@ pkv_status attention_impl(
     return fail(PKV_ERR_UNSUPPORTED, "an fp8 query needs an fp8 cache");
   if (q8 && !opts->q_scale)
     return fail(PKV_ERR_INVALID_ARG, "an fp8 query needs q_scale");
-  const int eb = 2, cb = kv8 ? 1 : 2, qb = q8 ? 1 : 2;
+  const bool kv4 = fp4 != nullptr;
+  if (kv4 && (kv8 || q8 || nonpaged))
+    return fail(PKV_ERR_UNSUPPORTED,
+                "a 4-bit cache excludes an fp8 cache or query and non-paged "
+                "keys");
+  if (kv4) {
+    st = check_fp4(fp4, head_size);
+    if (st != PKV_OK) return st;
+  }
+  const int eb = 2, cb = kv8 || kv4 ? 1 : 2, qb = q8 ? 1 : 2;
   if (!aligned16(q) || !aligned16(key_cache) || !aligned16(value_cache) ||
       !aligned16(out) || !stride16(q_stride_tok, qb) ||
       !stride16(q_stride_head, qb) || !stride16(o_stride_tok, eb) ||
@@ -738,10 +794,10 @@ pkv_status attention_impl(
   if (st != PKV_OK) return st;
   const Plan pl = make_plan(batch, total_q, max_seqlen_q, max_seqlen_k,
                             num_heads, num_kv_heads, head_size, causal, wl, wr,
-                            num_splits, sms, fixed_split);
+                            num_splits, sms, fixed_split, kv4);
   size_t need = pl.workspace;
   size_t mock_off = 0, q16_off = 0;
-  if (kv8 && pl.prefill) {
+  if ((kv8 || kv4) && pl.prefill) {
     mock_off = align256(pl.workspace);
     need = mock_off + fp8_mock_bytes(batch, max_blocks_per_seq, block_size,
                                      num_kv_heads, head_size);
@@ -783,13 +839,14 @@ pkv_status attention_impl(
           2 * static_cast<int64_t>(sms) * kDecodeCtasPerSm &&
       pl.range >= kLongUnitKeys;
   const bool sk_ok =
-      sk_candidate(num_splits, fixed_split, head_size, kv8) &&
+      !kv4 && sk_candidate(num_splits, fixed_split, head_size, kv8) &&
       (dsel == PKV_DECODE_PERSISTENT ||
        (dsel == PKV_DECODE_AUTO && (kv8 || many_units)));
   const int skr = sk_rows(num_heads / num_kv_heads, max_seqlen_q);
-  const size_t skb = sk_candidate(num_splits, fixed_split, head_size, kv8)
-                         ? sk_scratch_bytes(head_size, kv8, q8, sms, skr)
-                         : 0;
+  const size_t skb =
+      !kv4 && sk_candidate(num_splits, fixed_split, head_size, kv8)
+          ? sk_scratch_bytes(head_size, kv8, q8, sms, skr)
+          : 0;
   const Layout lay = make_layout(need, pl.prefill, skb, sb);
   const bool ws_ok = workspace &&
                      reinterpret_cast<uintptr_t>(workspace) % 256 == 0;
@@ -859,6 +916,16 @@ pkv_status attention_impl(
   p.kv_fp8 = kv8 ? 1 : 0;
   p.k_scale = kv8 ? opts->k_scale : nullptr;
   p.v_scale = kv8 ? opts->v_scale : nullptr;
+  if (kv4) {
+    p.kv_fp4 = 1;
+    p.k_scale = fp4->k_scale;
+    p.v_scale = fp4->v_scale;
+    p.k_sf = static_cast<const uint8_t*>(fp4->k_block_scale);
+    p.v_sf = static_cast<const uint8_t*>(fp4->v_block_scale);
+    p.f_sb = fp4->strides[0];
+    p.f_sr = fp4->strides[1];
+    p.f_sh = fp4->strides[2];
+  }
   if (nonpaged) {
     // one "block" holding all total_k rows; kernels index rows by cu_k
     const int rows = opts->total_k > 0 ? opts->total_k : 1;
@@ -917,6 +984,7 @@ pkv_status attention_impl(
   const bool pdl_ok = !(opts && opts->no_pdl);
   const bool prefill_first = pdl_ok && pl.prefill && pl.decode && sched &&
                              tc_prefill && sk_scratch == nullptr && !kv8 &&
+                             !kv4 &&
                              dsel != PKV_DECODE_CP_ASYNC &&
                              pdl_done == nullptr;
   // the prefill kernel's item counter (and the counter above) is zeroed
@@ -947,7 +1015,10 @@ pkv_status attention_impl(
     }
     cudaError_t e;
     const bool persistent = sk_scratch != nullptr;
-    if (persistent) {
+    if (kv4) {
+      d.sk_rows = skr;
+      e = launch_decode_attn_fp4(d, head_size, bf16, pl.splits, s);
+    } else if (persistent) {
       d.chunk = 0;
       e = launch_decode_attn_sk(d, head_size, bf16, sk_ctas, skr, sk_scratch,
                                 pdl_ok, s);
@@ -985,7 +1056,8 @@ pkv_status attention_impl(
       c.min_rows = 1;
       c.max_rows = kDecodeRows;
       // a dependent of the decode grid when that is one itself
-      e = launch_split_combine(c, bf16, s, done != nullptr);
+      e = kv4 ? launch_fp4_combine(c, bf16, pdl_ok, s)
+              : launch_split_combine(c, bf16, s, done != nullptr);
       if (e != cudaSuccess) return cuda_fail(e, "split combine launch");
     }
     return PKV_OK;
@@ -1004,7 +1076,7 @@ pkv_status attention_impl(
     f.max_ctas = in ? in->pre_ctas : 0;
     const int64_t prow = static_cast<int64_t>(max_seqlen_q) * p.G;
     cudaError_t e;
-    if (kv8) {
+    if (kv8 || kv4) {
       // 16-bit copies of the pages prefill-class requests read
       const size_t pages = static_cast<size_t>(batch) * max_blocks_per_seq;
       const size_t page_bytes =
@@ -1014,8 +1086,9 @@ pkv_status attention_impl(
       void* mv = base_ptr + align256(pages * page_bytes);
       int32_t* mt = reinterpret_cast<int32_t*>(
           base_ptr + 2 * align256(pages * page_bytes));
-      e = launch_fp8_dequant_pages(f, head_size, bf16, mk, mv, mt, s);
-      if (e != cudaSuccess) return cuda_fail(e, "fp8 page dequant launch");
+      e = kv4 ? launch_fp4_dequant_pages(f, head_size, bf16, mk, mv, mt, s)
+              : launch_fp8_dequant_pages(f, head_size, bf16, mk, mv, mt, s);
+      if (e != cudaSuccess) return cuda_fail(e, "page dequant launch");
       f.kc = mk;
       f.vc = mv;
       f.c_sb = static_cast<int64_t>(block_size) * num_kv_heads * head_size;
@@ -1029,14 +1102,14 @@ pkv_status attention_impl(
     int used = 1;
     if (tc_prefill)
       // as a programmatic dependent of the decode kernels just launched
-      // (none of their output is read here); not after an fp8 page copy,
-      // which this launch reads
+      // (none of their output is read here); not after a page copy, which
+      // this launch reads
       e = launch_prefill_attn_tc(f, head_size, bf16,
                                  static_cast<int>((prow + 127) / 128),
                                  which == PKV_PREFILL_TCGEN05, &used, s,
                                  pdl_ok && PKV_PREFILL_AFTER_DECODE_PDL &&
-                                     pl.decode &&
-                                     !kv8 && !prefill_first);
+                                     pl.decode && !kv8 && !kv4 &&
+                                     !prefill_first);
     else
       e = launch_prefill_attn_mma(f, head_size, bf16,
                                   static_cast<int>((prow + 63) / 64), s);
@@ -1351,6 +1424,352 @@ pkv_status pkv_merge_attn_states(void* output, const void* prefix_output,
                                num_tokens, num_heads, head_size, out_dtype,
                                in_dtype, reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "merge launch");
+  return PKV_OK;
+}
+
+}  // extern "C"
+
+namespace {
+
+// What the cache-writing calls share.
+pkv_status check_cache_write(int64_t num_tokens, int64_t num_blocks,
+                             int num_kv_heads, int head_size, int block_size,
+                             const int64_t* cache_strides, pkv_dtype dtype) {
+  if (dtype != PKV_F16 && dtype != PKV_BF16)
+    return fail(PKV_ERR_UNSUPPORTED, "dtype must be fp16 or bf16");
+  if (num_tokens < 0 || num_blocks < 0)
+    return fail(PKV_ERR_INVALID_ARG, "negative size argument");
+  if (num_kv_heads <= 0 || head_size <= 0)
+    return fail(PKV_ERR_INVALID_ARG, "num_kv_heads / head_size must be > 0");
+  if (block_size <= 0 || block_size % 16 != 0)
+    return fail(PKV_ERR_INVALID_ARG, "block_size must be a multiple of 16");
+  if (head_size % 8 != 0)
+    return fail(PKV_ERR_UNSUPPORTED, "head_size must be a multiple of 8");
+  if (!cache_strides)
+    return fail(PKV_ERR_INVALID_ARG, "cache_strides is NULL");
+  if (cache_strides[3] != 1)
+    return fail(PKV_ERR_INVALID_ARG, "the head_size dim must be contiguous");
+  return PKV_OK;
+}
+
+// Code rows of a 4-bit cache: 16-byte boundaries.
+pkv_status check_fp4_rows(const void* kc, const void* vc, const int64_t* cs) {
+  if (!aligned16(kc) || !aligned16(vc) || cs[0] % 16 || cs[1] % 16 ||
+      cs[2] % 16)
+    return fail(PKV_ERR_UNSUPPORTED,
+                "4-bit cache rows must start on 16-byte boundaries");
+  return PKV_OK;
+}
+
+pkv_status check_rope(const pkv_rope_params* r, int64_t num_tokens, int Hq,
+                      int Hkv, int D, pkv_dtype dtype) {
+  if (!r) return fail(PKV_ERR_INVALID_ARG, "rope is NULL");
+  if (dtype != PKV_F16 && dtype != PKV_BF16)
+    return fail(PKV_ERR_UNSUPPORTED, "dtype must be fp16 or bf16");
+  if (num_tokens < 0)
+    return fail(PKV_ERR_INVALID_ARG, "negative size argument");
+  if (Hq < 0 || Hkv <= 0 || D <= 0)
+    return fail(PKV_ERR_INVALID_ARG,
+                "num_heads must be >= 0, num_kv_heads and head_size > 0");
+  if (D % 8 != 0 || D > 512)
+    return fail(PKV_ERR_UNSUPPORTED,
+                "head_size must be a multiple of 8 and at most 512");
+  if (r->rot_dim <= 0 || r->rot_dim % 2 || r->rot_dim > D)
+    return fail(PKV_ERR_INVALID_ARG,
+                "rot_dim must be even, > 0 and at most head_size");
+  if (r->num_axes < 1 || r->num_axes > 4)
+    return fail(PKV_ERR_INVALID_ARG, "num_axes must be 1 to 4");
+  if (r->num_axes > 1) {
+    int sum = 0;
+    for (int a = 0; a < r->num_axes; ++a) {
+      const int n = r->sections[a];
+      if (n < 0 || n > r->rot_dim / 2)
+        return fail(PKV_ERR_INVALID_ARG, "a section is out of range");
+      sum += n;
+    }
+    if (sum != r->rot_dim / 2)
+      return fail(PKV_ERR_INVALID_ARG,
+                  "the sections must sum to rot_dim / 2 (%d), not %d",
+                  r->rot_dim / 2, sum);
+  }
+  if (r->max_position <= 0 || r->cos_sin_stride < r->rot_dim)
+    return fail(PKV_ERR_INVALID_ARG,
+                "cos_sin needs max_position >= 1 rows of at least rot_dim");
+  if (!r->q_weight != !r->k_weight)
+    return fail(PKV_ERR_INVALID_ARG,
+                "q_weight and k_weight go together (both or neither)");
+  if (r->q_weight && !(r->eps >= 0.f))
+    return fail(PKV_ERR_INVALID_ARG, "eps must be >= 0");
+  if (r->weight_offset != r->weight_offset || isinf(r->weight_offset))
+    return fail(PKV_ERR_INVALID_ARG, "weight_offset must be finite");
+  if (num_tokens > 0 && (!r->positions || !r->cos_sin))
+    return fail(PKV_ERR_INVALID_ARG, "NULL positions or cos_sin");
+  return PKV_OK;
+}
+
+void fill_rope(RopeLaunch* p, const pkv_rope_params* r, int64_t num_tokens,
+               int Hq, int Hkv, int D) {
+  p->num_tokens = num_tokens;
+  p->Hq = Hq;
+  p->Hkv = Hkv;
+  p->D = D;
+  p->rot = r->rot_dim;
+  p->neox = r->is_neox ? 1 : 0;
+  p->positions = r->positions;
+  p->pos_st = r->position_axis_stride;
+  p->axes = r->num_axes;
+  p->woven = r->interleaved_axes ? 1 : 0;
+  for (int a = 0; a < 4; ++a)
+    p->sections[a] = a < r->num_axes ? r->sections[a] : 0;
+  p->table = r->cos_sin;
+  p->table_st = r->cos_sin_stride;
+  p->max_position = r->max_position;
+  p->table_f32 = r->cos_sin_f32 ? 1 : 0;
+  p->q_weight = r->q_weight;
+  p->k_weight = r->k_weight;
+  p->norm = r->q_weight ? 1 : 0;
+  p->eps = r->eps;
+  p->weight_offset = r->weight_offset;
+}
+
+}  // namespace
+
+extern "C" {
+
+pkv_status pkv_reshape_and_cache_fp4(
+    const void* key, const void* value, int64_t k_stride_tok,
+    int64_t k_stride_head, int64_t v_stride_tok, int64_t v_stride_head,
+    void* key_cache, void* value_cache, const int64_t cache_strides[4],
+    const pkv_fp4_scales* scales, const int64_t* slot_mapping,
+    int64_t num_tokens, int num_kv_heads, int head_size, int block_size,
+    int64_t num_blocks, pkv_dtype dtype, pkv_stream_t stream) {
+  pkv_status st = check_cache_write(num_tokens, num_blocks, num_kv_heads,
+                                    head_size, block_size, cache_strides,
+                                    dtype);
+  if (st != PKV_OK) return st;
+  st = check_fp4(scales, head_size);
+  if (st != PKV_OK) return st;
+  if (num_tokens == 0) return PKV_OK;
+  if (!key || !value || !key_cache || !value_cache || !slot_mapping)
+    return fail(PKV_ERR_INVALID_ARG, "NULL tensor pointer");
+  if (!aligned16(key) || !aligned16(value) || !stride16(k_stride_tok, 2) ||
+      !stride16(k_stride_head, 2) || !stride16(v_stride_tok, 2) ||
+      !stride16(v_stride_head, 2))
+    return fail(PKV_ERR_UNSUPPORTED,
+                "key and value rows must start on 16-byte boundaries");
+  st = check_fp4_rows(key_cache, value_cache, cache_strides);
+  if (st != PKV_OK) return st;
+  unsigned* err = nullptr;
+  st = device_info(&err, nullptr);
+  if (st != PKV_OK) return st;
+  const cudaError_t e = launch_cache_write_fp4(
+      key, value, k_stride_tok, k_stride_head, v_stride_tok, v_stride_head,
+      key_cache, value_cache, cache_strides,
+      static_cast<uint8_t*>(scales->k_block_scale),
+      static_cast<uint8_t*>(scales->v_block_scale), scales->strides,
+      slot_mapping, num_tokens, num_kv_heads, head_size, block_size,
+      num_blocks, dtype == PKV_BF16, scales->k_scale, scales->v_scale, err,
+      reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "reshape_and_cache_fp4 launch");
+  return PKV_OK;
+}
+
+pkv_status pkv_dequantize_fp4_cache(
+    const void* codes, const int64_t cache_strides[4],
+    const void* block_scale, const int64_t scale_strides[4],
+    const float* scale, const int64_t* block_ids, int64_t num_out,
+    int num_kv_heads, int head_size, int block_size, int64_t num_blocks,
+    void* out, pkv_dtype dtype, pkv_stream_t stream) {
+  pkv_status st = check_cache_write(num_out, num_blocks, num_kv_heads,
+                                    head_size, block_size, cache_strides,
+                                    dtype);
+  if (st != PKV_OK) return st;
+  if (!scale_strides)
+    return fail(PKV_ERR_INVALID_ARG, "scale_strides is NULL");
+  // (one matrix: the check wants two)
+  pkv_fp4_scales both{};
+  both.k_block_scale = both.v_block_scale = const_cast<void*>(block_scale);
+  both.k_scale = both.v_scale = scale;
+  for (int i = 0; i < 4; ++i) both.strides[i] = scale_strides[i];
+  st = check_fp4(&both, head_size);
+  if (st != PKV_OK) return st;
+  if (!block_ids && num_out > num_blocks)
+    return fail(PKV_ERR_INVALID_ARG,
+                "num_out is larger than num_blocks (no block_ids)");
+  if (num_out == 0) return PKV_OK;
+  if (!codes || !out) return fail(PKV_ERR_INVALID_ARG, "NULL tensor pointer");
+  st = check_fp4_rows(codes, codes, cache_strides);
+  if (st != PKV_OK) return st;
+  if (!aligned16(out))
+    return fail(PKV_ERR_UNSUPPORTED, "out must be 16-byte aligned");
+  unsigned* err = nullptr;
+  st = device_info(&err, nullptr);
+  if (st != PKV_OK) return st;
+  const cudaError_t e = launch_fp4_dequant_blocks(
+      codes, cache_strides, static_cast<const uint8_t*>(block_scale),
+      scale_strides, scale, block_ids, num_out, num_blocks, num_kv_heads,
+      head_size, block_size, out, dtype == PKV_BF16, err,
+      reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "dequantize_fp4_cache launch");
+  return PKV_OK;
+}
+
+size_t pkv_paged_attention_workspace_size_fp4(
+    int batch, int total_q, int max_seqlen_q, int max_seqlen_k, int num_heads,
+    int num_kv_heads, int head_size, int block_size, int causal,
+    int window_left, int window_right, int num_splits,
+    int max_blocks_per_seq, const pkv_attention_options* opts) {
+  if (opts && (opts->kv_cache_fp8 || opts->q_fp8 || opts->cu_seqlens_k)) {
+    fail(PKV_ERR_UNSUPPORTED,
+         "a 4-bit cache excludes an fp8 cache or query and non-paged keys");
+    return static_cast<size_t>(-1);
+  }
+  return workspace_bytes_impl(batch, total_q, max_seqlen_q, max_seqlen_k,
+                              num_heads, num_kv_heads, head_size, block_size,
+                              causal, window_left, window_right, num_splits,
+                              max_blocks_per_seq, opts, 0, true);
+}
+
+pkv_status pkv_paged_attention_varlen_fp4(
+    const void* q, int64_t q_stride_tok, int64_t q_stride_head,
+    const void* key_cache, const void* value_cache,
+    const int64_t cache_strides[4], const pkv_fp4_scales* scales, void* out,
+    int64_t o_stride_tok, int64_t o_stride_head, const int32_t* cu_seqlens_q,
+    const int32_t* seqused_k, int batch, int total_q, int max_seqlen_q,
+    int max_seqlen_k, const int32_t* block_table, int64_t block_table_stride,
+    int max_blocks_per_seq, int num_heads, int num_kv_heads, int head_size,
+    int block_size, int64_t num_blocks, float softmax_scale, int causal,
+    int window_left, int window_right, float softcap,
+    const float* alibi_slopes, int num_splits, float* softmax_lse,
+    void* workspace, size_t workspace_bytes, pkv_dtype dtype,
+    pkv_stream_t stream, const pkv_attention_options* opts) {
+  if (!scales)
+    return fail(PKV_ERR_INVALID_ARG, "a 4-bit cache needs its scales");
+  return attention_impl(
+      q, q_stride_tok, q_stride_head, key_cache, value_cache, cache_strides,
+      out, o_stride_tok, o_stride_head, cu_seqlens_q, seqused_k, batch,
+      total_q, max_seqlen_q, max_seqlen_k, block_table, block_table_stride,
+      max_blocks_per_seq, num_heads, num_kv_heads, head_size, block_size,
+      num_blocks, softmax_scale, causal, window_left, window_right, softcap,
+      alibi_slopes, num_splits, softmax_lse, workspace, workspace_bytes,
+      dtype, stream, opts, nullptr, scales);
+}
+
+pkv_status pkv_qk_norm_rope(
+    const void* q, int64_t q_stride_tok, int64_t q_stride_head, const void* k,
+    int64_t k_stride_tok, int64_t k_stride_head, void* q_out,
+    int64_t qo_stride_tok, int64_t qo_stride_head, void* k_out,
+    int64_t ko_stride_tok, int64_t ko_stride_head, int64_t num_tokens,
+    int num_heads, int num_kv_heads, int head_size,
+    const pkv_rope_params* rope, pkv_dtype dtype, pkv_stream_t stream) {
+  pkv_status st = check_rope(rope, num_tokens, num_heads, num_kv_heads,
+                             head_size, dtype);
+  if (st != PKV_OK) return st;
+  if (num_tokens == 0) return PKV_OK;
+  if ((num_heads && (!q || !q_out)) || !k || !k_out)
+    return fail(PKV_ERR_INVALID_ARG, "NULL tensor pointer");
+  RopeLaunch p{};
+  fill_rope(&p, rope, num_tokens, num_heads, num_kv_heads, head_size);
+  p.q = q;
+  p.q_st = q_stride_tok;
+  p.q_sh = q_stride_head;
+  p.k = k;
+  p.k_st = k_stride_tok;
+  p.k_sh = k_stride_head;
+  p.q_out = q_out;
+  p.qo_st = qo_stride_tok;
+  p.qo_sh = qo_stride_head;
+  p.k_out = k_out;
+  p.ko_st = ko_stride_tok;
+  p.ko_sh = ko_stride_head;
+  st = device_info(&p.err, nullptr);
+  if (st != PKV_OK) return st;
+  const cudaError_t e = launch_rope(p, kRopeRows, dtype == PKV_BF16,
+                                    reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "qk_norm_rope launch");
+  return PKV_OK;
+}
+
+pkv_status pkv_rope_reshape_and_cache(
+    const void* q, int64_t q_stride_tok, int64_t q_stride_head, const void* k,
+    int64_t k_stride_tok, int64_t k_stride_head, const void* v,
+    int64_t v_stride_tok, int64_t v_stride_head, void* q_out,
+    int64_t qo_stride_tok, int64_t qo_stride_head, void* key_cache,
+    void* value_cache, const int64_t cache_strides[4],
+    const int64_t* slot_mapping, int64_t num_tokens, int num_heads,
+    int num_kv_heads, int head_size, int block_size, int64_t num_blocks,
+    const pkv_rope_params* rope, pkv_dtype dtype, const char* kv_cache_dtype,
+    const float* k_scale, const float* v_scale, const pkv_fp4_scales* fp4,
+    pkv_stream_t stream) {
+  RopeStore store = kRopeCache16;
+  if (kv_cache_dtype && strcmp(kv_cache_dtype, "auto") != 0) {
+    if (strcmp(kv_cache_dtype, "fp8") == 0 ||
+        strcmp(kv_cache_dtype, "fp8_e4m3") == 0)
+      store = kRopeCacheFp8;
+    else if (strcmp(kv_cache_dtype, "fp4") == 0)
+      store = kRopeCacheFp4;
+    else
+      return fail(PKV_ERR_UNSUPPORTED, "kv_cache_dtype '%s' is not supported",
+                  kv_cache_dtype);
+  }
+  pkv_status st = check_rope(rope, num_tokens, num_heads, num_kv_heads,
+                             head_size, dtype);
+  if (st != PKV_OK) return st;
+  st = check_cache_write(num_tokens, num_blocks, num_kv_heads, head_size,
+                         block_size, cache_strides, dtype);
+  if (st != PKV_OK) return st;
+  if (store == kRopeCacheFp8 && (!k_scale || !v_scale))
+    return fail(PKV_ERR_INVALID_ARG, "fp8 cache needs k_scale and v_scale");
+  if (store == kRopeCacheFp4) {
+    st = check_fp4(fp4, head_size);
+    if (st != PKV_OK) return st;
+  }
+  if (num_tokens == 0) return PKV_OK;
+  if ((num_heads && (!q || !q_out)) || !k || !v || !key_cache ||
+      !value_cache || !slot_mapping)
+    return fail(PKV_ERR_INVALID_ARG, "NULL tensor pointer");
+  if (store == kRopeCacheFp4) {
+    st = check_fp4_rows(key_cache, value_cache, cache_strides);
+    if (st != PKV_OK) return st;
+  }
+  RopeLaunch p{};
+  fill_rope(&p, rope, num_tokens, num_heads, num_kv_heads, head_size);
+  p.q = q;
+  p.q_st = q_stride_tok;
+  p.q_sh = q_stride_head;
+  p.k = k;
+  p.k_st = k_stride_tok;
+  p.k_sh = k_stride_head;
+  p.v = v;
+  p.v_st = v_stride_tok;
+  p.v_sh = v_stride_head;
+  p.q_out = q_out;
+  p.qo_st = qo_stride_tok;
+  p.qo_sh = qo_stride_head;
+  p.kc = key_cache;
+  p.vc = value_cache;
+  p.c_sb = cache_strides[0];
+  p.c_sr = cache_strides[1];
+  p.c_sh = cache_strides[2];
+  p.slots = slot_mapping;
+  p.num_slots = num_blocks * block_size;
+  p.BS = block_size;
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  if (store == kRopeCacheFp4) {
+    p.k_scale = fp4->k_scale;
+    p.v_scale = fp4->v_scale;
+    p.k_sf = static_cast<uint8_t*>(fp4->k_block_scale);
+    p.v_sf = static_cast<uint8_t*>(fp4->v_block_scale);
+    p.f_sb = fp4->strides[0];
+    p.f_sr = fp4->strides[1];
+    p.f_sh = fp4->strides[2];
+  }
+  st = device_info(&p.err, nullptr);
+  if (st != PKV_OK) return st;
+  const cudaError_t e = launch_rope(p, store, dtype == PKV_BF16,
+                                    reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "rope_reshape_and_cache launch");
   return PKV_OK;
 }
 

@@ -18,6 +18,7 @@ constexpr unsigned kErrTimeout = 8u;    // a bounded wait gave up
 constexpr unsigned kErrSmemAlign = 16u; // shared memory not 1024-byte aligned
 constexpr unsigned kErrQueryLen = 32u;  // a request's query count is above
                                         // the max_seqlen_q the call gave
+constexpr unsigned kErrBadPosition = 64u;   // position past the rotation table
 
 // ---------------------------------------------------------------- PTX helpers
 
@@ -223,6 +224,13 @@ struct AttnParams {
   int kv_fp8;                 // cache holds E4M3 codes (1 byte / element)
   const float* k_scale;       // fp8: device scalar, value = code * scale
   const float* v_scale;
+  // 4-bit cache: kc / vc hold two E2M1 codes a byte (c_sb, c_sr, c_sh in
+  // bytes), and these the E4M3 scales of each 16 values of a row (strides
+  // in bytes); value = code * block scale * (*k_scale)
+  int kv_fp4;
+  const uint8_t* k_sf;
+  const uint8_t* v_sf;
+  int64_t f_sb, f_sr, f_sh;
   // E4M3 query codes (1 byte / element, q_st / q_sh in bytes), value =
   // code * (*q_scale); only the persistent decode kernel reads them (the
   // other kernels get a 16-bit copy and k_scale * q_scale as k_scale)
@@ -356,6 +364,73 @@ cudaError_t launch_cache_write_fp8(const void* key, const void* value,
 cudaError_t launch_fp8_dequant_pages(const AttnParams& p, int D, bool bf16,
                                      void* mock_k, void* mock_v,
                                      int32_t* mock_table, cudaStream_t stream);
+// 4-bit caches (fp4_cache.cu): the quantizing write; the exact 16-bit copies
+// of the pages that prefill-class requests read (as launch_fp8_dequant_pages,
+// without the tensor scales); the values of listed blocks (all when `ids` is
+// null), tensor scale included, as contiguous [n, BS, Hkv, D].
+cudaError_t launch_cache_write_fp4(
+    const void* key, const void* value, int64_t k_st, int64_t k_sh,
+    int64_t v_st, int64_t v_sh, void* kc, void* vc, const int64_t* cs,
+    uint8_t* k_sf, uint8_t* v_sf, const int64_t* fs, const int64_t* slots,
+    int64_t num_tokens, int Hkv, int D, int BS, int64_t num_blocks, bool bf16,
+    const float* k_scale, const float* v_scale, unsigned* err,
+    cudaStream_t stream);
+cudaError_t launch_fp4_dequant_pages(const AttnParams& p, int D, bool bf16,
+                                     void* mock_k, void* mock_v,
+                                     int32_t* mock_table, cudaStream_t stream);
+cudaError_t launch_fp4_dequant_blocks(const void* codes, const int64_t* cs,
+                                      const uint8_t* sf, const int64_t* fs,
+                                      const float* scale, const int64_t* ids,
+                                      int64_t n, int64_t num_blocks, int Hkv,
+                                      int D, int BS, void* out, bool bf16,
+                                      unsigned* err, cudaStream_t stream);
+// Decode attention over a 4-bit cache (decode_fp4.cu): grid of (request,
+// split, KV head), `splits` pieces of p.chunk keys (0 = one piece, written
+// straight to the output); then the fold of the pieces.
+cudaError_t launch_decode_attn_fp4(const AttnParams& p, int D, bool bf16,
+                                   int splits, cudaStream_t stream);
+cudaError_t launch_fp4_combine(const CombineParams& p, bool bf16, bool pdl,
+                               cudaStream_t stream);
+// Resident CTAs of that kernel per SM for `rows` packed query rows.
+int decode_fp4_ctas_per_sm(int D, int rows);
+
+// Head norms, rotation and cache append (rope_cache.cu).
+enum RopeStore : int {
+  kRopeRows = 0,     // rotated keys to k_out; values not touched
+  kRopeCache16 = 1,  // rotated keys and values to a 16-bit cache
+  kRopeCacheFp8 = 2, // ... as E4M3 codes
+  kRopeCacheFp4 = 3  // ... as E2M1 codes with block scales
+};
+struct RopeLaunch {
+  const void *q, *k, *v;
+  int64_t q_st, q_sh, k_st, k_sh, v_st, v_sh;
+  void *q_out, *k_out;
+  int64_t qo_st, qo_sh, ko_st, ko_sh;
+  void *kc, *vc;                    // cache and its strides (elements; bytes
+  int64_t c_sb, c_sr, c_sh;         // for the one-byte and 4-bit caches)
+  uint8_t *k_sf, *v_sf;
+  int64_t f_sb, f_sr, f_sh;
+  const int64_t* slots;
+  int64_t num_slots;
+  int BS;
+  const float *k_scale, *v_scale;
+  int64_t num_tokens;
+  int Hq, Hkv, D, rot, neox;
+  const int64_t* positions;         // [axes][num_tokens], row stride pos_st
+  int64_t pos_st;
+  int axes, woven;
+  int sections[4];                  // pairs per axis (axes > 1)
+  const void* table;                // rows cos[rot / 2] | sin[rot / 2]
+  int64_t table_st, max_position;
+  int table_f32;
+  const void *q_weight, *k_weight;  // [D], used when `norm` is set
+  int norm;
+  float eps, weight_offset;
+  unsigned* err;
+};
+cudaError_t launch_rope(const RopeLaunch& p, RopeStore store, bool bf16,
+                        cudaStream_t stream);
+
 // E4M3 queries (q_fp8.cu): the per-tensor quantization, and the exact
 // 16-bit copy of the codes plus kq = k_scale * q_scale.
 cudaError_t launch_scaled_fp8_quant(const void* in, int64_t in_st, void* out,
@@ -464,6 +539,94 @@ template <>
 __device__ __forceinline__ float elem_f32<__half>(uint32_t w, int hi) {
   return __half2float(__ushort_as_half(
       static_cast<unsigned short>(hi ? (w >> 16) : (w & 0xffffu))));
+}
+
+// ---- 4-bit caches: E2M1 codes and E4M3 block scales
+
+// Eight E2M1 codes (lowest nibble first) -> four f16x2 (exact).
+__device__ __forceinline__ void e2m1x8_to_f16(uint32_t w, uint32_t& r0,
+                                              uint32_t& r1, uint32_t& r2,
+                                              uint32_t& r3) {
+  asm("{\n.reg .b8 a, b, c, d;\n"
+      "mov.b32 {a, b, c, d}, %4;\n"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n"
+      "cvt.rn.f16x2.e2m1x2 %1, b;\n"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n"
+      "cvt.rn.f16x2.e2m1x2 %3, d;\n}\n"
+      : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
+      : "r"(w));
+}
+
+// Two E4M3 codes (low byte first) -> f16x2 (exact).
+__device__ __forceinline__ uint32_t e4m3x2_to_f16(uint32_t w) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;"
+      : "=r"(r)
+      : "h"(static_cast<unsigned short>(w)));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t hmul2_u32(uint32_t a, uint32_t b) {
+  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a),
+                            *reinterpret_cast<const __half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// The 4-bit quantization of 16 values that share a block scale, given the
+// largest magnitude `top` (NaN if any value is) and the tensor scale:
+//   sf   = e4m3(top * fl(1 / fl(6 scale)))
+//   code = e2m1(x * fl(1 / fl(sf scale))), 0 where sf is 0
+// both rounded to nearest (ties to even) and saturated (448 and 6).  A NaN
+// in `top` gives a NaN scale, so the whole group reads back as NaN.
+struct Fp4Scale {
+  uint32_t code;    // the E4M3 code
+  float inv;
+};
+__device__ __forceinline__ Fp4Scale fp4_scale(float top, float scale) {
+  const float t = __fmul_rn(top, __frcp_rn(__fmul_rn(scale, 6.f)));
+  uint16_t c;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c) : "f"(0.f), "f"(t));
+  const uint32_t h = e4m3x2_to_f16(c);
+  const float step = __fmul_rn(
+      __low2float(*reinterpret_cast<const __half2*>(&h)), scale);
+  Fp4Scale r;
+  r.code = c & 0xffu;
+  r.inv = step > 0.f ? __frcp_rn(step) : 0.f;
+  return r;
+}
+// |x| maximum that keeps a NaN.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+// Eight values -> eight codes (lowest nibble first).
+__device__ __forceinline__ uint32_t fp4_codes8(const float* x, float inv) {
+  float y[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) y[i] = __fmul_rn(x[i], inv);
+  uint32_t r;
+  asm("{\n.reg .b8 a, b, c, d;\n"
+      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n"
+      "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n"
+      "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n"
+      "mov.b32 %0, {a, b, c, d};\n}\n"
+      : "=r"(r)
+      : "f"(y[0]), "f"(y[1]), "f"(y[2]), "f"(y[3]), "f"(y[4]), "f"(y[5]),
+        "f"(y[6]), "f"(y[7]));
+  return r;
+}
+
+// Eight 16-bit values of a 16-byte load, widened.
+template <typename T>
+__device__ __forceinline__ void widen8(const uint4& raw, float* x) {
+  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = elem_f32<T>(w[i], 0);
+    x[2 * i + 1] = elem_f32<T>(w[i], 1);
+  }
 }
 
 }  // namespace pkv

@@ -1,0 +1,582 @@
+// Head norms and rotary positions of q and k in one pass, with the rotated
+// keys and the values appended to a paged cache on the way.
+//
+// For a row x of D values (one head of one token), with the head norm
+//   n = x * (1 / sqrt(mean(x^2) + eps)) * (w + offset)       (or n = x)
+// and, for pair i < rot / 2 with c, s the table's entries at the position of
+// the pair's axis,
+//   y_a = n_a c - n_b s,   y_b = n_b c + n_a s
+// where (a, b) = (i, i + rot / 2) ("neox") or (2 i, 2 i + 1); dimensions from
+// rot on pass through.  All of it is float32 with one rounding at the end.
+// The sum of squares is taken pairwise (neighbours first, error at most
+// log2(D) half ulps), and the products of a rotation are rounded one by one,
+// so a row's bits depend neither on the kernel that takes it nor on the rows
+// beside it: a row that is quantized next has the same codes everywhere.
+//
+// HBM bounds it: a row is read once and written once (2 D + 2 D bytes for 16
+// bits), and the table row of a token is read once per warp that works on
+// the token.
+//
+// rope_kernel: a lane owns the 8-value chunks A and B of a row, rot / 2 apart,
+// so that a rotation never leaves the lane and every load and store of a row
+// is a run of whole 16-byte chunks; D / 16 lanes share a row and 512 / D rows
+// make one pass of a warp.  A warp works through the passes of one token (all
+// of them when there are many tokens, one when there are few) and keeps the
+// token's cos and sin in registers.  It takes D = 64, 128, 256, rows on
+// 16-byte boundaries, and rot = D / 2^n >= 32 (neox) or any multiple of 8
+// (adjacent pairs).  rope_any_kernel takes everything else: one warp a row,
+// through shared memory.
+#include "pkv_common.cuh"
+
+namespace pkv {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMaxD = 512;
+
+// Axis whose position rotates pair i.
+__device__ __forceinline__ int pair_axis(const RopeLaunch& p, int i) {
+  if (p.axes == 1) return 0;
+  if (p.woven) {
+    const int a = i % p.axes;
+    return i < p.axes * p.sections[a] ? a : 0;
+  }
+  int a = 0, end = p.sections[0];
+  while (a + 1 < p.axes && i >= end) end += p.sections[++a];
+  return a;
+}
+
+// The token's positions; false if the token is to be skipped: a negative
+// position is padding, one past the table is flagged.
+__device__ __forceinline__ bool read_positions(const RopeLaunch& p, int64_t t,
+                                               bool flag, int64_t* pos) {
+  bool ok = true, bad = false;
+#pragma unroll
+  for (int a = 0; a < 4; ++a) {
+    if (a >= p.axes) break;
+    pos[a] = __ldg(p.positions + a * p.pos_st + t);
+    ok = ok && pos[a] >= 0;
+    bad = bad || pos[a] >= p.max_position;
+  }
+  if (ok && bad && flag) atomicOr(p.err, kErrBadPosition);
+  return ok && !bad;
+}
+
+// The token's cache row: -1 = none (padding, or flagged as outside).
+__device__ __forceinline__ int64_t read_slot(const RopeLaunch& p, int64_t t,
+                                             bool flag) {
+  const int64_t s = __ldg(p.slots + t);
+  if (s < 0) return -1;
+  if (s >= p.num_slots) {
+    if (flag) atomicOr(p.err, kErrBadSlot);
+    return -1;
+  }
+  return s;
+}
+
+template <typename T>
+__device__ __forceinline__ float table_at(const RopeLaunch& p, int64_t pos,
+                                          int i) {
+  const int64_t at = pos * p.table_st + i;
+  return p.table_f32 ? __ldg(static_cast<const float*>(p.table) + at)
+                     : to_f32<T>(static_cast<const T*>(p.table)[at]);
+}
+
+// N consecutive table entries of one row (16-byte aligned).
+template <typename T, int N>
+__device__ __forceinline__ void table_run(const RopeLaunch& p, int64_t pos,
+                                          int i, float* out) {
+  const int64_t at = pos * p.table_st + i;
+  if (p.table_f32) {
+    const float* src = static_cast<const float*>(p.table) + at;
+#pragma unroll
+    for (int j = 0; j < N; j += 4) {
+      const float4 v = __ldg(reinterpret_cast<const float4*>(src + j));
+      out[j] = v.x;
+      out[j + 1] = v.y;
+      out[j + 2] = v.z;
+      out[j + 3] = v.w;
+    }
+  } else {
+    const T* src = static_cast<const T*>(p.table) + at;
+    if constexpr (N == 8) {
+      widen8<T>(__ldg(reinterpret_cast<const uint4*>(src)), out);
+    } else {
+      const uint2 v = __ldg(reinterpret_cast<const uint2*>(src));
+      out[0] = elem_f32<T>(v.x, 0);
+      out[1] = elem_f32<T>(v.x, 1);
+      out[2] = elem_f32<T>(v.y, 0);
+      out[3] = elem_f32<T>(v.y, 1);
+    }
+  }
+}
+
+__device__ __forceinline__ float sum8_pairwise(const float* x) {
+  float s[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) s[i] = __fmul_rn(x[i], x[i]);
+#pragma unroll
+  for (int n = 1; n < 8; n *= 2)
+#pragma unroll
+    for (int i = 0; i < 8; i += 2 * n) s[i] = __fadd_rn(s[i], s[i + n]);
+  return s[0];
+}
+
+__device__ __forceinline__ float inv_rms(float sum, int D, float eps) {
+  return __frcp_rn(__fsqrt_rn(
+      __fadd_rn(__fdiv_rn(sum, static_cast<float>(D)), eps)));
+}
+
+// y_a, y_b of one pair.
+__device__ __forceinline__ void rotate(float& a, float& b, float c, float s) {
+  const float ya = __fsub_rn(__fmul_rn(a, c), __fmul_rn(b, s));
+  const float yb = __fadd_rn(__fmul_rn(b, c), __fmul_rn(a, s));
+  a = ya;
+  b = yb;
+}
+
+template <typename T>
+__device__ __forceinline__ uint4 pack8(const float* x) {
+  return make_uint4(pack2<T>(x[0], x[1]), pack2<T>(x[2], x[3]),
+                    pack2<T>(x[4], x[5]), pack2<T>(x[6], x[7]));
+}
+
+__device__ __forceinline__ uint32_t e4m3_codes4(const float* x, float scale) {
+  uint16_t lo, hi;
+  // cvt puts its first operand in the upper byte
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo)
+      : "f"(__fdiv_rn(x[1], scale)), "f"(__fdiv_rn(x[0], scale)));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi)
+      : "f"(__fdiv_rn(x[3], scale)), "f"(__fdiv_rn(x[2], scale)));
+  return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
+}
+
+// One row's chunks A and B (chunk numbers ca, cb) to the cache row.  For
+// the 4-bit cache, chunks 2 m and 2 m + 1 share a block scale: they are a
+// lane's and its neighbour's (lane ^ 1) chunks.  `on`: this lane stores (all
+// lanes take part in the exchange).
+template <typename T, int STORE>
+__device__ __forceinline__ void store_cache(const RopeLaunch& p, bool value,
+                                            int64_t blk, int64_t off, int h,
+                                            int ca, int cb, const float* x,
+                                            const uint4* raw, bool on,
+                                            float scale) {
+  const int64_t row = blk * p.c_sb + off * p.c_sr + h * p.c_sh;
+  void* base = value ? p.vc : p.kc;
+  if constexpr (STORE == kRopeCache16) {
+    if (!on) return;
+    T* dst = static_cast<T*>(base) + row;
+    *reinterpret_cast<uint4*>(dst + 8 * ca) = value ? raw[0] : pack8<T>(x);
+    *reinterpret_cast<uint4*>(dst + 8 * cb) = value ? raw[1] : pack8<T>(x + 8);
+  } else if constexpr (STORE == kRopeCacheFp8) {
+    if (!on) return;
+    uint8_t* dst = static_cast<uint8_t*>(base) + row;
+    *reinterpret_cast<uint2*>(dst + 8 * ca) =
+        make_uint2(e4m3_codes4(x, scale), e4m3_codes4(x + 4, scale));
+    *reinterpret_cast<uint2*>(dst + 8 * cb) =
+        make_uint2(e4m3_codes4(x + 8, scale), e4m3_codes4(x + 12, scale));
+  } else {
+    float top[2];
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      float m = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) m = max_nan(m, fabsf(x[8 * c + i]));
+      top[c] = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    }
+    if (!on) return;
+    uint8_t* dst = static_cast<uint8_t*>(base) + row;
+    uint8_t* sf = (value ? p.v_sf : p.k_sf) + blk * p.f_sb + off * p.f_sr +
+                  h * p.f_sh;
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int ch = c ? cb : ca;
+      const Fp4Scale s = fp4_scale(top[c], scale);
+      *reinterpret_cast<uint32_t*>(dst + 4 * ch) =
+          fp4_codes8(x + 8 * c, s.inv);
+      if (!(ch & 1)) sf[ch >> 1] = static_cast<uint8_t>(s.code);
+    }
+  }
+}
+
+template <typename T, int D, int STORE, bool NEOX>
+__global__ void __launch_bounds__(kThreads)
+rope_kernel(const RopeLaunch p, int parts) {
+  // an attention kernel queued next as a programmatic dependent may become
+  // resident now (it waits for this grid before reading what this writes)
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  constexpr int LPR = D / 16;             // lanes of a row
+  constexpr int RPW = 32 / LPR;           // rows of a pass
+  const int lane = threadIdx.x & 31;
+  const int j = lane % LPR, sub = lane / LPR;
+  // chunk numbers: inside each block of `span` values, A is in the first
+  // half and B at the same place of the second
+  const int span = NEOX ? p.rot : D;
+  const int nb = span / 16;               // lanes of a span
+  const int blk0 = j / nb;
+  const int ca = blk0 * (span / 8) + (j - blk0 * nb), cb = ca + nb;
+  const bool rot_a = 8 * ca < p.rot, rot_b = 8 * cb < p.rot;
+  const int half = p.rot / 2;
+  const int pq = (p.Hq + RPW - 1) / RPW, pk = (p.Hkv + RPW - 1) / RPW;
+  const int passes = pq + (STORE == kRopeRows ? pk : 2 * pk);
+  const float ks = STORE >= kRopeCacheFp8 ? *p.k_scale : 1.f;
+  const float vs = STORE >= kRopeCacheFp8 ? *p.v_scale : 1.f;
+  const int64_t work = p.num_tokens * parts;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * (kThreads / 32);
+  for (int64_t w = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) +
+                   (threadIdx.x >> 5);
+       w < work; w += step) {
+    const int64_t t = w / parts;
+    const int part = static_cast<int>(w - t * parts);
+    int64_t pos[4] = {0, 0, 0, 0};
+    if (!read_positions(p, t, part == 0 && lane == 0, pos)) continue;
+    int64_t slot = -1, blk = 0, off = 0;
+    if constexpr (STORE != kRopeRows) {
+      slot = read_slot(p, t, part == 0 && lane == 0);
+      if (slot >= 0) {
+        blk = slot / p.BS;
+        off = slot - blk * p.BS;
+      }
+    }
+    // cos and sin of this lane's pairs: pairs 8 ca .. (neox, A with B), or
+    // 4 ca .. and 4 cb .. (adjacent pairs)
+    float c[8], s[8];
+    if (NEOX ? rot_a : (rot_a || rot_b)) {
+      if (p.axes == 1) {
+        if constexpr (NEOX) {
+          table_run<T, 8>(p, pos[0], 8 * ca, c);
+          table_run<T, 8>(p, pos[0], half + 8 * ca, s);
+        } else {
+          if (rot_a) {
+            table_run<T, 4>(p, pos[0], 4 * ca, c);
+            table_run<T, 4>(p, pos[0], half + 4 * ca, s);
+          }
+          if (rot_b) {
+            table_run<T, 4>(p, pos[0], 4 * cb, c + 4);
+            table_run<T, 4>(p, pos[0], half + 4 * cb, s + 4);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int i = NEOX ? 8 * ca + e
+                             : (e < 4 ? 4 * ca + e : 4 * cb + e - 4);
+          if (i >= half) continue;
+          const int a = pair_axis(p, i);
+          const int64_t at = a == 0 ? pos[0]
+                             : a == 1 ? pos[1] : a == 2 ? pos[2] : pos[3];
+          c[e] = table_at<T>(p, at, i);
+          s[e] = table_at<T>(p, at, half + i);
+        }
+      }
+    }
+    for (int i = part; i < passes; i += parts) {
+      const int kind = i < pq ? 0 : i < pq + pk ? 1 : 2;      // q, k or v
+      const int h0 = (kind == 0 ? i : kind == 1 ? i - pq : i - pq - pk) * RPW;
+      const int h = h0 + sub;
+      const bool on = h < (kind == 0 ? p.Hq : p.Hkv);
+      if (STORE != kRopeRows && kind > 0 && slot < 0) continue;
+      const T* src = static_cast<const T*>(kind == 0   ? p.q
+                                           : kind == 1 ? p.k
+                                                       : p.v) +
+                     t * (kind == 0 ? p.q_st : kind == 1 ? p.k_st : p.v_st) +
+                     h * (kind == 0   ? p.q_sh
+                          : kind == 1 ? p.k_sh
+                                      : p.v_sh);
+      uint4 raw[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+      if (on) {
+        raw[0] = *reinterpret_cast<const uint4*>(src + 8 * ca);
+        raw[1] = *reinterpret_cast<const uint4*>(src + 8 * cb);
+      }
+      float x[16];
+      widen8<T>(raw[0], x);
+      widen8<T>(raw[1], x + 8);
+      if (kind < 2) {
+        if (p.norm) {
+          float sa = sum8_pairwise(x), sb = sum8_pairwise(x + 8);
+          // neighbours first: lanes of the span, then A with B, then spans
+          for (int o = 1; o < nb; o *= 2) {
+            sa = __fadd_rn(sa, __shfl_xor_sync(0xffffffffu, sa, o));
+            sb = __fadd_rn(sb, __shfl_xor_sync(0xffffffffu, sb, o));
+          }
+          sa = __fadd_rn(sa, sb);
+          for (int o = nb; o < LPR; o *= 2)
+            sa = __fadd_rn(sa, __shfl_xor_sync(0xffffffffu, sa, o));
+          const float r = inv_rms(sa, D, p.eps);
+          const T* wt = static_cast<const T*>(kind == 0 ? p.q_weight
+                                                        : p.k_weight);
+          float wv[16];
+          widen8<T>(__ldg(reinterpret_cast<const uint4*>(wt + 8 * ca)), wv);
+          widen8<T>(__ldg(reinterpret_cast<const uint4*>(wt + 8 * cb)),
+                    wv + 8);
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            x[e] = __fmul_rn(__fmul_rn(x[e], r),
+                             __fadd_rn(wv[e], p.weight_offset));
+        }
+        if constexpr (NEOX) {
+          if (rot_a) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) rotate(x[e], x[8 + e], c[e], s[e]);
+          }
+        } else {
+          if (rot_a) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              rotate(x[2 * e], x[2 * e + 1], c[e], s[e]);
+          }
+          if (rot_b) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              rotate(x[8 + 2 * e], x[9 + 2 * e], c[4 + e], s[4 + e]);
+          }
+        }
+      }
+      if (kind == 0 || STORE == kRopeRows) {
+        if (on) {
+          T* dst = static_cast<T*>(kind == 0 ? p.q_out : p.k_out) +
+                   t * (kind == 0 ? p.qo_st : p.ko_st) +
+                   h * (kind == 0 ? p.qo_sh : p.ko_sh);
+          *reinterpret_cast<uint4*>(dst + 8 * ca) = pack8<T>(x);
+          *reinterpret_cast<uint4*>(dst + 8 * cb) = pack8<T>(x + 8);
+        }
+      } else if constexpr (STORE != kRopeRows) {
+        store_cache<T, STORE>(p, kind == 2, blk, off, h, ca, cb, x, raw, on,
+                              kind == 2 ? vs : ks);
+      }
+    }
+  }
+}
+
+// Any head size (a multiple of 8 up to 512), rotation width, stride and
+// alignment: one warp a row.
+template <typename T, int STORE>
+__global__ void __launch_bounds__(kThreads)
+rope_any_kernel(const RopeLaunch p) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  __shared__ float rows[kThreads / 32][2][kMaxD];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  float* xs = rows[warp][0];
+  float* ys = rows[warp][1];
+  const int D = p.D, half = p.rot / 2;
+  int dp = 32;                            // D up to a power of two
+  while (dp < D) dp *= 2;
+  const int per = dp / 32;
+  const int heads = p.Hq + (STORE == kRopeRows ? p.Hkv : 2 * p.Hkv);
+  const int64_t work = p.num_tokens * heads;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * (kThreads / 32);
+  for (int64_t w = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + warp;
+       w < work; w += step) {
+    const int64_t t = w / heads;
+    const int r = static_cast<int>(w - t * heads);
+    const int kind = r < p.Hq ? 0 : r < p.Hq + p.Hkv ? 1 : 2;
+    const int h = kind == 0 ? r : kind == 1 ? r - p.Hq : r - p.Hq - p.Hkv;
+    int64_t pos[4] = {0, 0, 0, 0};
+    if (!read_positions(p, t, r == 0 && lane == 0, pos)) continue;
+    int64_t slot = -1, blk = 0, off = 0;
+    if constexpr (STORE != kRopeRows) {
+      slot = read_slot(p, t, r == 0 && lane == 0);
+      if (kind > 0 && slot < 0) continue;
+      if (slot >= 0) {
+        blk = slot / p.BS;
+        off = slot - blk * p.BS;
+      }
+    }
+    const T* src = static_cast<const T*>(kind == 0   ? p.q
+                                         : kind == 1 ? p.k
+                                                     : p.v) +
+                   t * (kind == 0 ? p.q_st : kind == 1 ? p.k_st : p.v_st) +
+                   h * (kind == 0 ? p.q_sh : kind == 1 ? p.k_sh : p.v_sh);
+    __syncwarp();                         // the row before is done
+    for (int d = lane; d < D; d += 32) xs[d] = to_f32<T>(src[d]);
+    __syncwarp();
+    float* ready = xs;
+    if (kind < 2) {
+      if (p.norm) {
+        float sq[kMaxD / 32];
+#pragma unroll
+        for (int e = 0; e < kMaxD / 32; ++e) {
+          const int d = lane * per + e;
+          sq[e] = e < per && d < D ? __fmul_rn(xs[d], xs[d]) : 0.f;
+        }
+#pragma unroll
+        for (int n = 1; n < kMaxD / 32; n *= 2)
+#pragma unroll
+          for (int e = 0; e + n < kMaxD / 32; e += 2 * n)
+            if (n < per) sq[e] = __fadd_rn(sq[e], sq[e + n]);
+        float sum = sq[0];
+#pragma unroll
+        for (int o = 1; o < 32; o *= 2)
+          sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, o));
+        const float rms = inv_rms(sum, D, p.eps);
+        const T* wt = static_cast<const T*>(kind == 0 ? p.q_weight
+                                                      : p.k_weight);
+        __syncwarp();
+        for (int d = lane; d < D; d += 32)
+          xs[d] = __fmul_rn(__fmul_rn(xs[d], rms),
+                            __fadd_rn(to_f32<T>(wt[d]), p.weight_offset));
+        __syncwarp();
+      }
+      for (int d = lane; d < D; d += 32) {
+        float v = xs[d];
+        if (d < p.rot) {
+          const int i = p.neox ? (d < half ? d : d - half) : d >> 1;
+          const bool second = p.neox ? d >= half : (d & 1);
+          const int other = p.neox ? (second ? d - half : d + half) : d ^ 1;
+          const int a = pair_axis(p, i);
+          const int64_t at = a == 0 ? pos[0]
+                             : a == 1 ? pos[1] : a == 2 ? pos[2] : pos[3];
+          float lo = second ? xs[other] : v, hi = second ? v : xs[other];
+          rotate(lo, hi, table_at<T>(p, at, i), table_at<T>(p, at, half + i));
+          v = second ? hi : lo;
+        }
+        ys[d] = v;
+      }
+      ready = ys;
+      __syncwarp();
+    }
+    if (kind == 0 || STORE == kRopeRows) {
+      T* dst = static_cast<T*>(kind == 0 ? p.q_out : p.k_out) +
+               t * (kind == 0 ? p.qo_st : p.ko_st) +
+               h * (kind == 0 ? p.qo_sh : p.ko_sh);
+      for (int d = lane; d < D; d += 32) dst[d] = from_f32<T>(ready[d]);
+      continue;
+    }
+    const int64_t row = blk * p.c_sb + off * p.c_sr + h * p.c_sh;
+    void* base = kind == 2 ? p.vc : p.kc;
+    const float scale = STORE < kRopeCacheFp8 ? 1.f
+                        : kind == 2           ? *p.v_scale
+                                              : *p.k_scale;
+    if constexpr (STORE == kRopeCache16) {
+      T* dst = static_cast<T*>(base) + row;
+      // a value row is copied bit for bit, NaN payloads included
+      for (int d = lane; d < D; d += 32)
+        dst[d] = kind == 2 ? src[d] : from_f32<T>(ready[d]);
+    } else if constexpr (STORE == kRopeCacheFp8) {
+      uint8_t* dst = static_cast<uint8_t*>(base) + row;
+      for (int d = lane * 4; d < D; d += 128) {
+        const uint32_t codes = e4m3_codes4(ready + d, scale);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          dst[d + e] = static_cast<uint8_t>(codes >> (8 * e));
+      }
+    } else if constexpr (STORE == kRopeCacheFp4) {
+      uint8_t* dst = static_cast<uint8_t*>(base) + row;
+      uint8_t* sf = (kind == 2 ? p.v_sf : p.k_sf) + blk * p.f_sb +
+                    off * p.f_sr + h * p.f_sh;
+      for (int g = lane; g < D / 16; g += 32) {
+        float top = 0.f;
+        for (int e = 0; e < 16; ++e)
+          top = max_nan(top, fabsf(ready[16 * g + e]));
+        const Fp4Scale s = fp4_scale(top, scale);
+        for (int e = 0; e < 2; ++e) {
+          const uint32_t codes = fp4_codes8(ready + 16 * g + 8 * e, s.inv);
+          for (int b = 0; b < 4; ++b)
+            dst[8 * g + 4 * e + b] = static_cast<uint8_t>(codes >> (8 * b));
+        }
+        sf[g] = static_cast<uint8_t>(s.code);
+      }
+    }
+  }
+}
+
+bool on16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+
+// rope_kernel's conditions (see the head of this file).
+bool whole_chunks(const RopeLaunch& p, RopeStore store) {
+  if (p.D != 64 && p.D != 128 && p.D != 256) return false;
+  if (p.neox) {
+    if (p.rot < 32 || p.D % p.rot || (p.rot & (p.rot - 1))) return false;
+  } else if (p.rot % 8) {
+    return false;
+  }
+  const int tb = p.table_f32 ? 4 : 2;
+  // a lane reads 8 (neox) or 4 (adjacent pairs) entries from each half row
+  const int run = (p.neox ? 8 : 4) * tb < 16 ? (p.neox ? 8 : 4) * tb : 16;
+  if (p.axes == 1 &&
+      (reinterpret_cast<uintptr_t>(p.table) % run || p.table_st * tb % run ||
+       p.rot / 2 * tb % run))
+    return false;
+  auto rows16 = [](const void* b, int64_t st, int64_t sh) {
+    return on16(b) && st % 8 == 0 && sh % 8 == 0;
+  };
+  if (p.Hq && (!rows16(p.q, p.q_st, p.q_sh) ||
+               !rows16(p.q_out, p.qo_st, p.qo_sh)))
+    return false;
+  if (!rows16(p.k, p.k_st, p.k_sh)) return false;
+  if (!on16(p.q_weight) || !on16(p.k_weight)) return false;
+  if (store == kRopeRows) return rows16(p.k_out, p.ko_st, p.ko_sh);
+  if (!rows16(p.v, p.v_st, p.v_sh)) return false;
+  // a lane's store: 16 bytes (16-bit), 8 (E4M3) or 4 (4-bit)
+  const int unit = store == kRopeCache16 ? 8 : store == kRopeCacheFp8 ? 8 : 4;
+  const int bytes = store == kRopeCache16 ? 16 : unit;
+  return reinterpret_cast<uintptr_t>(p.kc) % bytes == 0 &&
+         reinterpret_cast<uintptr_t>(p.vc) % bytes == 0 &&
+         p.c_sb % unit == 0 && p.c_sr % unit == 0 && p.c_sh % unit == 0;
+}
+
+template <typename T, int D, int STORE>
+cudaError_t launch_chunks(const RopeLaunch& p, cudaStream_t stream) {
+  constexpr int rpw = 512 / D;
+  const int pk = (p.Hkv + rpw - 1) / rpw;
+  const int passes = (p.Hq + rpw - 1) / rpw + (STORE ? 2 : 1) * pk;
+  // one warp works through a token, or through a part of one while the
+  // warps would not fill the GPU
+  const int64_t fill = static_cast<int64_t>(current_sm_count()) * 32;
+  int64_t parts = (fill + p.num_tokens - 1) / p.num_tokens;
+  if (parts > passes) parts = passes;
+  const int64_t blocks = (p.num_tokens * parts + kThreads / 32 - 1) /
+                         (kThreads / 32);
+  const int64_t cap = static_cast<int64_t>(current_sm_count()) * 64;
+  const unsigned grid = static_cast<unsigned>(blocks < cap ? blocks : cap);
+  note_launch();
+  if (p.neox)
+    rope_kernel<T, D, STORE, true><<<grid, kThreads, 0, stream>>>(
+        p, static_cast<int>(parts));
+  else
+    rope_kernel<T, D, STORE, false><<<grid, kThreads, 0, stream>>>(
+        p, static_cast<int>(parts));
+  return cudaGetLastError();
+}
+
+template <typename T, int STORE>
+cudaError_t launch_store(const RopeLaunch& p, cudaStream_t stream) {
+  if (whole_chunks(p, static_cast<RopeStore>(STORE))) {
+    switch (p.D) {
+      case 64: return launch_chunks<T, 64, STORE>(p, stream);
+      case 128: return launch_chunks<T, 128, STORE>(p, stream);
+      default: return launch_chunks<T, 256, STORE>(p, stream);
+    }
+  }
+  const int64_t rows = p.num_tokens *
+                       (p.Hq + (STORE == kRopeRows ? 1 : 2) * p.Hkv);
+  const int64_t blocks = (rows + kThreads / 32 - 1) / (kThreads / 32);
+  const int64_t cap = static_cast<int64_t>(current_sm_count()) * 16;
+  note_launch();
+  rope_any_kernel<T, STORE>
+      <<<static_cast<unsigned>(blocks < cap ? blocks : cap), kThreads, 0,
+         stream>>>(p);
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_type(const RopeLaunch& p, RopeStore store,
+                        cudaStream_t stream) {
+  switch (store) {
+    case kRopeRows: return launch_store<T, kRopeRows>(p, stream);
+    case kRopeCache16: return launch_store<T, kRopeCache16>(p, stream);
+    case kRopeCacheFp8: return launch_store<T, kRopeCacheFp8>(p, stream);
+    default: return launch_store<T, kRopeCacheFp4>(p, stream);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_rope(const RopeLaunch& p, RopeStore store, bool bf16,
+                        cudaStream_t stream) {
+  if (p.num_tokens == 0) return cudaSuccess;
+  return bf16 ? launch_type<__nv_bfloat16>(p, store, stream)
+              : launch_type<__half>(p, store, stream);
+}
+
+}  // namespace pkv
