@@ -123,20 +123,20 @@ __device__ __forceinline__ void finish(float m, float l, const float* sinks,
   *lse = (M + lg2(den)) * kLn2;
 }
 
-// softcap * tanh(x / softcap): 1 - 2 / (1 + e^2x) keeps the absolute error
-// near one ulp of the cap (tanh.approx loses 2^-11 of the logit).
-__device__ __forceinline__ float soft_cap(float x, float cap, float inv_cap) {
-  const float e = ex2(x * inv_cap * (2.f * kLog2e));
-  return cap * (1.f - __fdividef(2.f, 1.f + e));
+// log2(e) softcap tanh(x / softcap) of a logit given in base 2, as t =
+// log2(e) softcap and u = 2 / softcap: t (1 - 2 / (1 + 2^(x u))) keeps the
+// absolute error near one ulp of the cap (tanh.approx loses 2^-11 of the
+// logit).
+__device__ __forceinline__ float soft_cap(float x, float t, float u) {
+  return t - __fdividef(2.f * t, 1.f + ex2(x * u));
 }
 
-template <typename T, int D, int NR>
+template <int D, int NR>
 struct Smem {
-  // query fragments (two n tiles or D = 256 keep them here) and the warps'
-  // states at the end
-  static constexpr bool QS = NR > 1 || D > 128;
+  // query fragments (one 16-byte load serves two k steps of every subtile)
+  // and the warps' states at the end
   static constexpr int ROWS = 8 * NR;
-  static constexpr int QBYTES = QS ? (D / 16) * NR * 32 * 8 : 0;
+  static constexpr int QBYTES = (D / 32) * NR * 32 * 16;
   static constexpr int OSTRIDE = ROWS * D + 4 * (ROWS / 2);   // floats a warp
   static constexpr int OBYTES = kWarps * OSTRIDE * 4;
   static constexpr int MLBYTES = kWarps * ROWS * 8;
@@ -148,13 +148,13 @@ constexpr int min_ctas() {
   return NR == 1 ? (D == 256 ? 3 : 4) : (D == 256 ? 2 : 3);
 }
 
-template <typename T, int D, int NR>
+template <typename T, int D, int NR, bool PACKED>
 __global__ void __launch_bounds__(kWarps * 32, min_ctas<D, NR>())
 decode_fp4_kernel(const AttnParams p, int splits) {
   // the fold of the pieces may become resident once every CTA has started
   // (it waits for this grid before reading them)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  using SM = Smem<T, D, NR>;
+  using SM = Smem<D, NR>;
   constexpr int MT = Geo<D>::MT;
   constexpr int KT = 16 * MT;            // keys of a warp's tile
   constexpr int KS = D / 16;             // k steps of S, and m tiles of O
@@ -201,12 +201,11 @@ decode_fp4_kernel(const AttnParams p, int splits) {
   // its K run.  A bf16 row is scaled by the power of two that puts its
   // largest magnitude in [2^14, 2^15): exact in f16; the factor joins the
   // row's logit scale.
-  uint32_t qf[SM::QS ? 1 : KS][SM::QS ? 1 : NR][2];
-  float row_scale[NR][2];        // logit scale (base 2) of rows 2 c4, 2 c4 + 1
+  float row_scale[NR][2];   // logit scale (base 2) of rows 2 c4, 2 c4 + 1
   {
     const T* Q = static_cast<const T*>(p.q);
-    const float base_scale = p.scale * *p.k_scale;
-    uint2* qs = reinterpret_cast<uint2*>(smem);
+    const float base_scale = p.scale * *p.k_scale * kLog2e;
+    uint4* qs = reinterpret_cast<uint4*>(smem);
 #pragma unroll
     for (int n = 0; n < NR; ++n) {
       const int r = g8 + 8 * n;
@@ -258,25 +257,17 @@ decode_fp4_kernel(const AttnParams p, int splits) {
                      ? w[e]
                      : pack2<__half>(elem_f32<T>(w[e], 0) * qmul,
                                      elem_f32<T>(w[e], 1) * qmul);
-        // 8 dimensions: k steps 2 i and 2 i + 1
-        if constexpr (SM::QS) {
-          if ((i & (kWarps - 1)) == warp || KW < kWarps) {
-            qs[((2 * i) * NR + n) * 32 + lane] = make_uint2(f[0], f[1]);
-            qs[((2 * i + 1) * NR + n) * 32 + lane] = make_uint2(f[2], f[3]);
-          }
-        } else {
-          qf[2 * i][n][0] = f[0];
-          qf[2 * i][n][1] = f[1];
-          qf[2 * i + 1][n][0] = f[2];
-          qf[2 * i + 1][n][1] = f[3];
-        }
+        // 8 dimensions: the B operands of k steps 2 i and 2 i + 1
+        if (KW < kWarps || (i & (kWarps - 1)) == warp)
+          qs[(i * NR + n) * 32 + lane] = make_uint4(f[0], f[1], f[2], f[3]);
       }
     }
   }
-  if constexpr (SM::QS) __syncthreads();
+  __syncthreads();
 
   const bool plain = p.softcap <= 0.f && p.alibi == nullptr;
-  const float inv_cap = p.softcap > 0.f ? 1.f / p.softcap : 0.f;
+  const float cap_t = p.softcap * kLog2e;
+  const float cap_u = p.softcap > 0.f ? 2.f / p.softcap : 0.f;
   const int ctx = L - q_len;
   int pos[NR][2];
   float slope[NR][2];
@@ -288,7 +279,8 @@ decode_fp4_kernel(const AttnParams p, int splits) {
       const int r = 8 * n + 2 * c4 + e;
       live[n][e] = r < rows;
       pos[n][e] = ctx + r / G;
-      slope[n][e] = p.alibi && r < rows ? p.alibi[h * G + r % G] : 0.f;
+      slope[n][e] =
+          p.alibi && r < rows ? p.alibi[h * G + r % G] * kLog2e : 0.f;
     }
   // keys in [full_lo, full_hi) are seen by every row
   int full_lo = lo, full_hi = hi;
@@ -321,107 +313,119 @@ decode_fp4_kernel(const AttnParams p, int splits) {
   auto sub_key = [&](int s) {            // first key of my subtile s
     return kt0 + (warp + (s / MT) * kWarps) * KT + (s % MT) * 16;
   };
-  auto fetch_ids = [&](int s0) -> int {  // page of subtile s0 + lane
+  // page and first row in it of subtile s0 + lane; subtiles past the range
+  // and pages outside the cache take page 0 (a bad page: with the sign bit)
+  auto fetch = [&](int s0, int& id, int& row) {
     const int s = s0 + lane;
     const int k0 = s < subs ? sub_key(s) : hi;
-    if (k0 >= hi) return -1;
-    const int id = __ldg(bt + k0 / p.BS);
+    id = row = 0;
+    if (k0 >= hi) return;
+    const int j = p.bs_shift >= 0 ? k0 >> p.bs_shift : k0 / p.BS;
+    row = k0 - j * p.BS;
+    id = __ldg(bt + j);
     if (id < 0 || id >= p.num_blocks) {
       atomicOr(p.err, kErrBadBlock);
-      return -1;
+      id = static_cast<int>(0x80000000u);
+      row = 0;
     }
-    return id;
   };
-  int ids = fetch_ids(0), ids_next = fetch_ids(32);
+  int ids, rows0, ids_next, rows0_next;
+  fetch(0, ids, rows0);
+  fetch(32, ids_next, rows0_next);
   const int kap = 4 * (g8 >> 1) + (g8 & 1);
-  const uint8_t* KC = static_cast<const uint8_t*>(p.kc) +
-                      static_cast<int64_t>(h) * p.c_sh;
-  const uint8_t* VC = static_cast<const uint8_t*>(p.vc) +
-                      static_cast<int64_t>(h) * p.c_sh;
-  const uint8_t* KF = p.k_sf + static_cast<int64_t>(h) * p.f_sh;
-  const uint8_t* VF = p.v_sf + static_cast<int64_t>(h) * p.f_sh;
-  // offset of subtile s of its page in the codes and the scales; false: no
-  // page (its keys read as zero)
-  auto locate = [&](int s, int64_t* c, int64_t* f) -> bool {
-    const int id = __shfl_sync(0xffffffffu, ids, s & 31);
-    const int k0 = sub_key(s);
-    const int row = p.bs_shift >= 0 ? (k0 & (p.BS - 1)) : k0 % p.BS;
-    *c = static_cast<int64_t>(id) * p.c_sb + static_cast<int64_t>(row) * p.c_sr;
-    *f = static_cast<int64_t>(id) * p.f_sb + static_cast<int64_t>(row) * p.f_sr;
-    return id >= 0;
-  };
+  const uint32_t c_sb = static_cast<uint32_t>(p.c_sb);
+  const uint32_t f_sb = static_cast<uint32_t>(p.f_sb);
+  const uint32_t c_sr = PACKED ? D / 2 : static_cast<uint32_t>(p.c_sr);
+  const uint32_t f_sr = PACKED ? D / 16 : static_cast<uint32_t>(p.f_sr);
+  // this lane's part of the page rows
+  const uint8_t* const KC = static_cast<const uint8_t*>(p.kc) +
+                            static_cast<int64_t>(h) * p.c_sh + kap * c_sr +
+                            (D == 64 ? 8 : 16) * c4;
+  const uint8_t* const VC = static_cast<const uint8_t*>(p.vc) +
+                            static_cast<int64_t>(h) * p.c_sh +
+                            4 * c4 * c_sr + (D / 16) * g8;
+  const uint8_t* const KF = p.k_sf + static_cast<int64_t>(h) * p.f_sh +
+                            kap * f_sr + (D == 64 ? 1 : 2) * c4;
+  const uint8_t* const VF = p.v_sf + static_cast<int64_t>(h) * p.f_sh +
+                            4 * c4 * f_sr +
+                            (D == 64 ? g8 >> 1 : (D / 128) * g8);
 
   uint32_t kw[MT][2][KW], vw[MT][4][VW];
   uint32_t kf[MT][2], vf[MT][4];         // scale bytes of the lane's groups
-  bool vgood[MT];
-  int64_t v_c[MT], v_f[MT];
+  int id_of[MT], row_of[MT];             // pages of the keys being loaded
   auto load_k = [&](int s0) {
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
-      const bool good = locate(s0 + i, &v_c[i], &v_f[i]);
-      vgood[i] = good;
+      id_of[i] = __shfl_sync(0xffffffffu, ids, (s0 + i) & 31);
+      row_of[i] = __shfl_sync(0xffffffffu, rows0, (s0 + i) & 31);
+      const uint32_t id = id_of[i] & 0x7fffffff;
+      const uint8_t* src = KC + static_cast<uint64_t>(id) * c_sb +
+                           static_cast<uint32_t>(row_of[i]) * c_sr;
+      const uint8_t* fs = KF + static_cast<uint64_t>(id) * f_sb +
+                          static_cast<uint32_t>(row_of[i]) * f_sr;
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const int64_t r = kap + 2 * e;
-        const uint8_t* src = KC + v_c[i] + r * p.c_sr;
-        const uint8_t* fs = KF + v_f[i] + r * p.f_sr;
+        if constexpr (D == 64) {
+          const uint2 v = ldg64(src + 2 * e * c_sr);
+          kw[i][e][0] = v.x;
+          kw[i][e][1] = v.y;
+          kf[i][e] = __ldg(fs + 2 * e * f_sr);
+        } else {
+          kf[i][e] = 0;
 #pragma unroll
-        for (int w = 0; w < KW; ++w) kw[i][e][w] = 0;
-        kf[i][e] = 0;
-        if (good) {
-          if constexpr (D == 64) {
-            const uint2 v = ldg64(src + 8 * c4);
-            kw[i][e][0] = v.x;
-            kw[i][e][1] = v.y;
-            kf[i][e] = __ldg(fs + c4);
-          } else {
-#pragma unroll
-            for (int q = 0; q < D / 128; ++q) {
-              const uint4 v = ldg128(src + 64 * q + 16 * c4);
-              kw[i][e][4 * q] = v.x;
-              kw[i][e][4 * q + 1] = v.y;
-              kw[i][e][4 * q + 2] = v.z;
-              kw[i][e][4 * q + 3] = v.w;
-              kf[i][e] |= static_cast<uint32_t>(
-                              __ldg(reinterpret_cast<const uint16_t*>(
-                                  fs + 8 * q + 2 * c4)))
-                          << (16 * q);
-            }
+          for (int q = 0; q < D / 128; ++q) {
+            const uint4 v = ldg128(src + 2 * e * c_sr + 64 * q);
+            kw[i][e][4 * q] = v.x;
+            kw[i][e][4 * q + 1] = v.y;
+            kw[i][e][4 * q + 2] = v.z;
+            kw[i][e][4 * q + 3] = v.w;
+            kf[i][e] |= static_cast<uint32_t>(
+                            __ldg(reinterpret_cast<const uint16_t*>(
+                                fs + 2 * e * f_sr + 8 * q)))
+                        << (16 * q);
           }
+        }
+      }
+      if (id_of[i] < 0) {                // a bad page: keys of zero
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          kf[i][e] = 0;
+#pragma unroll
+          for (int w = 0; w < KW; ++w) kw[i][e][w] = 0;
         }
       }
     }
   };
   auto load_v = [&]() {
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
+    for (int i = 0; i < MT; ++i) {
+      const uint32_t id = id_of[i] & 0x7fffffff;
+      const uint8_t* src = VC + static_cast<uint64_t>(id) * c_sb +
+                           static_cast<uint32_t>(row_of[i]) * c_sr;
+      const uint8_t* fs = VF + static_cast<uint64_t>(id) * f_sb +
+                          static_cast<uint32_t>(row_of[i]) * f_sr;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int64_t r = 4 * c4 + e;
-        const uint8_t* src = VC + v_c[i] + r * p.c_sr;
-        const uint8_t* fs = VF + v_f[i] + r * p.f_sr;
-#pragma unroll
-        for (int w = 0; w < VW; ++w) vw[i][e][w] = 0;
-        vf[i][e] = 0;
-        if (vgood[i]) {
-          if constexpr (D == 64) {
-            vw[i][e][0] = ldg32(src + 4 * g8);
-            vf[i][e] = __ldg(fs + (g8 >> 1));
-          } else if constexpr (D == 128) {
-            const uint2 v = ldg64(src + 8 * g8);
-            vw[i][e][0] = v.x;
-            vw[i][e][1] = v.y;
-            vf[i][e] = __ldg(fs + g8);
-          } else {
-            const uint4 v = ldg128(src + 16 * g8);
-            vw[i][e][0] = v.x;
-            vw[i][e][1] = v.y;
-            vw[i][e][2] = v.z;
-            vw[i][e][3] = v.w;
-            vf[i][e] = __ldg(reinterpret_cast<const uint16_t*>(fs + 2 * g8));
-          }
+        if constexpr (D == 64) {
+          vw[i][e][0] = ldg32(src + e * c_sr);
+        } else if constexpr (D == 128) {
+          const uint2 v = ldg64(src + e * c_sr);
+          vw[i][e][0] = v.x;
+          vw[i][e][1] = v.y;
+        } else {
+          const uint4 v = ldg128(src + e * c_sr);
+          vw[i][e][0] = v.x;
+          vw[i][e][1] = v.y;
+          vw[i][e][2] = v.z;
+          vw[i][e][3] = v.w;
         }
+        if constexpr (D == 256)
+          vf[i][e] = __ldg(reinterpret_cast<const uint16_t*>(fs + e * f_sr));
+        else
+          vf[i][e] = __ldg(fs + e * f_sr);
       }
+      if (id_of[i] < 0) vf[i][0] = vf[i][1] = vf[i][2] = vf[i][3] = 0;
+    }
   };
 
   if (mine > 0) {
@@ -439,34 +443,41 @@ decode_fp4_kernel(const AttnParams p, int splits) {
 #pragma unroll
       for (int n = 0; n < NR; ++n)
         sc[i][n][0] = sc[i][n][1] = sc[i][n][2] = sc[i][n][3] = 0.f;
+    // block scales of the lane's keys, two groups (D = 64: two keys) a word
+    constexpr int FW = D == 256 ? 2 : 1;
+    uint32_t fk[MT][2][FW];
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
-      // block scales of the two keys: (low, high) group of each 32-value run
-      uint32_t f0[KW <= 4 ? 1 : 2], f1[KW <= 4 ? 1 : 2];
       if constexpr (D == 64) {
-        const uint32_t f = e4m3x2_to_f16(kf[i][0] | (kf[i][1] << 8));
-        f0[0] = __byte_perm(f, 0, 0x1010);
-        f1[0] = __byte_perm(f, 0, 0x3232);
+        fk[i][0][0] = e4m3x2_to_f16(__byte_perm(kf[i][0], kf[i][1], 0x40));
+        fk[i][1][0] = 0;
       } else {
 #pragma unroll
-        for (int q = 0; q < D / 128; ++q) {
-          f0[q] = e4m3x2_to_f16(kf[i][0] >> (16 * q));
-          f1[q] = e4m3x2_to_f16(kf[i][1] >> (16 * q));
-        }
-      }
+        for (int e = 0; e < 2; ++e)
 #pragma unroll
-      for (int w = 0; w < KW; ++w) {
+          for (int q = 0; q < FW; ++q)
+            fk[i][e][q] = e4m3x2_to_f16(kf[i][e] >> (16 * q));
+      }
+    }
+#pragma unroll
+    for (int w = 0; w < KW; ++w) {
+      uint4 qb[NR];
+#pragma unroll
+      for (int n = 0; n < NR; ++n)
+        qb[n] = reinterpret_cast<const uint4*>(smem)[(w * NR + n) * 32 + lane];
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
         uint32_t a[4], c[4];
         e2m1x8_to_f16(kw[i][0][w], a[0], a[1], a[2], a[3]);
         e2m1x8_to_f16(kw[i][1][w], c[0], c[1], c[2], c[3]);
         uint32_t fa, fc;
         if constexpr (D == 64) {
-          fa = f0[0];
-          fc = f1[0];
+          fa = __byte_perm(fk[i][0][0], 0, 0x1010);
+          fc = __byte_perm(fk[i][0][0], 0, 0x3232);
         } else {
           const uint32_t sel = (w & 2) ? 0x3232u : 0x1010u;
-          fa = __byte_perm(f0[w >> 2], 0, sel);
-          fc = __byte_perm(f1[w >> 2], 0, sel);
+          fa = __byte_perm(fk[i][0][w >> 2], 0, sel);
+          fc = __byte_perm(fk[i][1][w >> 2], 0, sel);
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -475,23 +486,8 @@ decode_fp4_kernel(const AttnParams p, int splits) {
         }
 #pragma unroll
         for (int n = 0; n < NR; ++n) {
-          uint32_t b0, b1, b2, b3;
-          if constexpr (SM::QS) {
-            const uint2* qs = reinterpret_cast<const uint2*>(smem);
-            const uint2 u = qs[((2 * w) * NR + n) * 32 + lane];
-            const uint2 v = qs[((2 * w + 1) * NR + n) * 32 + lane];
-            b0 = u.x;
-            b1 = u.y;
-            b2 = v.x;
-            b3 = v.y;
-          } else {
-            b0 = qf[2 * w][n][0];
-            b1 = qf[2 * w][n][1];
-            b2 = qf[2 * w + 1][n][0];
-            b3 = qf[2 * w + 1][n][1];
-          }
-          mma(sc[i][n], a[0], c[0], a[1], c[1], b0, b1);
-          mma(sc[i][n], a[2], c[2], a[3], c[3], b2, b3);
+          mma(sc[i][n], a[0], c[0], a[1], c[1], qb[n].x, qb[n].y);
+          mma(sc[i][n], a[2], c[2], a[3], c[3], qb[n].z, qb[n].w);
         }
       }
     }
@@ -499,7 +495,8 @@ decode_fp4_kernel(const AttnParams p, int splits) {
     if (more) {
       if ((s_next & 31) == 0) {
         ids = ids_next;
-        ids_next = fetch_ids(s_next + 32);
+        rows0 = rows0_next;
+        fetch(s_next + 32, ids_next, rows0_next);
       }
       load_k(s_next);
     }
@@ -510,31 +507,31 @@ decode_fp4_kernel(const AttnParams p, int splits) {
     for (int n = 0; n < NR; ++n) mx[n][0] = mx[n][1] = -INFINITY;
     if (plain && interior) {
 #pragma unroll
-      for (int i = 0; i < MT; ++i)
+      for (int n = 0; n < NR; ++n)
 #pragma unroll
-        for (int n = 0; n < NR; ++n)
+        for (int i = 0; i < MT; ++i)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float x = sc[i][n][e] * (row_scale[n][e & 1] * kLog2e);
-            sc[i][n][e] = x;
-            mx[n][e & 1] = fmaxf(mx[n][e & 1], x);
+            // (the product is rounded once, here: a fused multiply-add with
+            // the maximum would differ from it by half an ulp of the logit,
+            // which may be far above 1)
+            sc[i][n][e] *= row_scale[n][e & 1];
+            mx[n][e & 1] = fmaxf(mx[n][e & 1], sc[i][n][e]);
           }
     } else {
 #pragma unroll
-      for (int i = 0; i < MT; ++i)
+      for (int n = 0; n < NR; ++n) {
 #pragma unroll
-        for (int n = 0; n < NR; ++n)
+        for (int i = 0; i < MT; ++i)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
+            float x = sc[i][n][e] * row_scale[n][e & 1];   // (base 2)
+            if (p.softcap > 0.f) x = soft_cap(x, cap_t, cap_u);
             const int key = kt + 16 * i + kap + (e & 2);
-            float x = sc[i][n][e] * row_scale[n][e & 1];
-            if (p.softcap > 0.f) x = soft_cap(x, p.softcap, inv_cap);
+            const int at = pos[n][e & 1];
             if (p.alibi)
-              x -= slope[n][e & 1] *
-                   fabsf(static_cast<float>(pos[n][e & 1] - key));
-            x *= kLog2e;
+              x -= slope[n][e & 1] * fabsf(static_cast<float>(at - key));
             if (!interior) {
-              const int at = pos[n][e & 1];
               bool ok = live[n][e & 1] && key >= lo && key < hi;
               if (p.causal) ok = ok && key <= at;
               if (p.wl >= 0) ok = ok && key >= at - p.wl;
@@ -544,6 +541,7 @@ decode_fp4_kernel(const AttnParams p, int splits) {
             sc[i][n][e] = x;
             mx[n][e & 1] = fmaxf(mx[n][e & 1], x);
           }
+      }
     }
     bool raise = false;
 #pragma unroll
@@ -828,10 +826,10 @@ __global__ void __launch_bounds__(128) combine_kernel(const CombineParams p) {
   }
 }
 
-template <typename T, int D, int NR>
+template <typename T, int D, int NR, bool PACKED>
 cudaError_t launch(const AttnParams& p, int splits, cudaStream_t stream) {
-  using SM = Smem<T, D, NR>;
-  auto kern = decode_fp4_kernel<T, D, NR>;
+  using SM = Smem<D, NR>;
+  auto kern = decode_fp4_kernel<T, D, NR, PACKED>;
   cudaError_t e = smem_opt_in(reinterpret_cast<const void*>(kern), SM::BYTES);
   if (e != cudaSuccess) return e;
   const int64_t ctas = static_cast<int64_t>(p.batch) * splits * p.Hkv;
@@ -842,17 +840,25 @@ cudaError_t launch(const AttnParams& p, int splits, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
+template <typename T, int D>
+cudaError_t dispatch_rows(const AttnParams& p, int splits,
+                          cudaStream_t stream) {
+  const bool one = p.sk_rows <= 8;       // packed query rows of a request
+  const bool packed = p.c_sr == D / 2 && p.f_sr == D / 16;
+  if (packed)
+    return one ? launch<T, D, 1, true>(p, splits, stream)
+               : launch<T, D, 2, true>(p, splits, stream);
+  return one ? launch<T, D, 1, false>(p, splits, stream)
+             : launch<T, D, 2, false>(p, splits, stream);
+}
+
 template <typename T>
 cudaError_t dispatch(const AttnParams& p, int D, int splits,
                      cudaStream_t stream) {
-  const bool one = p.sk_rows <= 8;       // packed query rows of a request
   switch (D) {
-    case 64: return one ? launch<T, 64, 1>(p, splits, stream)
-                        : launch<T, 64, 2>(p, splits, stream);
-    case 128: return one ? launch<T, 128, 1>(p, splits, stream)
-                         : launch<T, 128, 2>(p, splits, stream);
-    case 256: return one ? launch<T, 256, 1>(p, splits, stream)
-                         : launch<T, 256, 2>(p, splits, stream);
+    case 64: return dispatch_rows<T, 64>(p, splits, stream);
+    case 128: return dispatch_rows<T, 128>(p, splits, stream);
+    case 256: return dispatch_rows<T, 256>(p, splits, stream);
     default: return cudaErrorInvalidValue;
   }
 }

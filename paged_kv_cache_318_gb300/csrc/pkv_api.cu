@@ -775,6 +775,16 @@ pkv_status attention_impl(
   if (kv4) {
     st = check_fp4(fp4, head_size);
     if (st != PKV_OK) return st;
+    // (the decode kernel's offsets inside a block are 32-bit)
+    auto in_block = [&](const int64_t* s) {
+      return s[0] >= 0 && s[0] <= INT32_MAX && s[1] >= 0 &&
+             s[1] * block_size <= INT32_MAX;
+    };
+    if (!in_block(cache_strides) || !in_block(fp4->strides))
+      return fail(PKV_ERR_UNSUPPORTED,
+                  "a block of a 4-bit cache may span at most 2 GB");
+    if (num_blocks < 1)
+      return fail(PKV_ERR_INVALID_ARG, "the cache has no blocks");
   }
   const int eb = 2, cb = kv8 || kv4 ? 1 : 2, qb = q8 ? 1 : 2;
   if (!aligned16(q) || !aligned16(key_cache) || !aligned16(value_cache) ||

@@ -132,6 +132,9 @@ def attend(lib, **kw):
     (dict(softcap=-1.0), 1, b"softcap"),
     (dict(su=None), 1, b"NULL"),
     (dict(maxb=0), 1, b"block_table"),
+    (dict(NB=0), 1, b"no blocks"),
+    (dict(cs=strides(1 << 31, 64, 1024, 1)), 2, b"2 GB"),
+    (dict(cs=strides(4096, 1 << 28, 1024, 1)), 2, b"2 GB"),
 ])
 def test_attention_refuses(lib, kw, status, text):
     assert attend(lib, **kw) == status
