@@ -324,7 +324,8 @@ PKV_API pkv_status pkv_paged_attention_varlen_opts(
  *   share them); rows on 16-byte boundaries.
  * Block scales: 4-D views [num_blocks, block_size, num_kv_heads, head_size /
  *   16], one byte each, with the strides below in bytes (strides[3] = 1);
- *   rows on boundaries of head_size / 64 bytes.  A layout that keeps each
+ *   rows on boundaries of 4 bytes (8 and 16 where head_size is a multiple of
+ *   128 and of 256).  A layout that keeps each
  *   (block, head) together, [num_blocks, num_kv_heads, block_size, ...], is
  *   the one that reads fastest, for both.
  * k_scale, v_scale: device float scalars, > 0.  About amax / (6 * 448) uses

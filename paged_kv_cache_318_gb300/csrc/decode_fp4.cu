@@ -5,16 +5,17 @@
 // route from the cache to the tensor cores.  A key and a value of one head
 // are D / 2 bytes of codes and D / 16 of scales each, so at head size 128 a
 // page of 16 keys is 1 KB of codes a matrix: far below the size at which TMA
-// boxes reach the HBM rate (a box costs its SM about 200 cycles).  Here
-// nothing goes through shared memory: every lane loads exactly the codes of
-// its own MMA fragments into registers, converts them (cvt e2m1x2 -> f16x2,
-// times the block scale: both exact in f16) and feeds them to mma.sync.
+// boxes reach the HBM rate (a box costs its SM about 200 cycles).  Here each
+// warp copies its own key tiles with 16-byte cp.async into its own two-stage
+// ring (no barrier across warps), and its lanes read exactly the codes of
+// their own MMA fragments from there, convert them (cvt e2m1x2 -> f16x2,
+// times the block scale: both exact in f16) and feed them to mma.sync.
 //
 //  S^T = K Q^T   The keys are the MMA's 16 rows (A), the packed query rows its
 //    8 columns (B).  Lane (g8 = lane / 4, c4 = lane % 4) holds, for its two
 //    keys of a 16-key subtile, the c4-th run of the row; the order of the
 //    head dimension in the MMA's k steps is free (Q is laid out the same
-//    way), so a run is one 16-byte load (D = 128) whose codes feed eight k
+//    way), so a run is one 16-byte read (D = 128) whose codes feed eight k
 //    steps.
 //  O^T = V^T P^T  The head dimensions are the rows (A), the query rows the
 //    columns (B).  Lane (g8, c4) holds the g8-th run of four keys' rows:
@@ -30,12 +31,11 @@
 // is padding beyond 8, half of what 16-row query tiles would issue; 9 to 16
 // rows take two n tiles over the same converted operands.
 //
-// Each warp walks its own key tiles of a CTA's range, loading the next tile's
-// keys as soon as this one's are in the MMAs (and the next values likewise),
-// so a load has the rest of the tile to arrive; the warps meet once, at the
-// end.  The running maximum is raised (and O rescaled) only when a logit
-// passes it by 2^6: P stays below 64, which f16 holds with the same relative
-// error, and the common tile needs no reduction across lanes.
+// Each warp walks its own key tiles of a CTA's range, one tile ahead of its
+// reads; the warps meet once, at the end.  The running maximum is raised (and
+// O rescaled) only when a logit passes it by 2^6: P stays below 64, which f16
+// holds with the same relative error, and the common tile needs no reduction
+// across lanes.
 //
 // Keys outside [lo, hi) of the request are never seen: their logits are
 // -inf and their V scales 0 (a code is always finite, only a scale can be
@@ -53,20 +53,37 @@ namespace dfp4 {
 constexpr int kWarps = 4;
 constexpr float kRaise = 6.f;      // log2 slack of the running maximum
 
-// 16-key subtiles per tile of a warp, by head size.
+// One stage of a warp's ring: MT subtiles of 16 keys, K codes, V codes, then
+// 16 rows of 16 bytes of K scales and as many of V scales (row r: the scales
+// of key r of each subtile, side by side).
+//
+// Swizzles (of the 16-byte chunks of a subtile's rows), so that the lanes of
+// one read phase touch different banks: K is read as rows kappa(g8), chunk
+// c4; V as rows 4 c4 + e, eight (D = 64: four) bytes at g8.
 template <int D>
-struct Geo;
-template <>
-struct Geo<64> {
-  static constexpr int MT = 2;
-};
-template <>
-struct Geo<128> {
-  static constexpr int MT = 2;
-};
-template <>
-struct Geo<256> {
-  static constexpr int MT = 1;
+struct Geo {
+  static constexpr int MT = D == 256 ? 1 : 2;
+  static constexpr int RB = D / 2;                 // bytes of a row's codes
+  static constexpr int SUB = 16 * RB;              // ... of a subtile
+  static constexpr int CPR = RB / 16;              // chunks of a row
+  static constexpr int OFF_V = MT * SUB;
+  static constexpr int OFF_KF = 2 * MT * SUB;
+  static constexpr int OFF_VF = OFF_KF + 256;
+  static constexpr int STAGE = OFF_VF + 256;
+  static constexpr int STAGES = 2;
+
+  static __device__ __forceinline__ uint32_t k_off(int r, int ch) {
+    if (D == 64) return (r ^ (2 * ((r >> 2) & 1))) * RB + ch * 16;
+    if (D == 128) return r * RB + ch * 16;
+    return r * RB + (ch ^ (4 * (r & 1))) * 16;
+  }
+  static __device__ __forceinline__ uint32_t v_off(int r, int ch) {
+    if (D == 64)
+      return ((r & ~3) | ((r & 3) ^ ((r >> 2) & 3))) * RB + ch * 16;
+    if (D == 128)
+      return (r ^ ((r >> 3) & 1)) * RB + (ch ^ (2 * ((r >> 2) & 1))) * 16;
+    return r * RB + (ch ^ (2 * ((r >> 2) & 3))) * 16;
+  }
 };
 
 __device__ __forceinline__ uint32_t movmatrix(uint32_t a) {
@@ -75,27 +92,40 @@ __device__ __forceinline__ uint32_t movmatrix(uint32_t a) {
   return d;
 }
 
-__device__ __forceinline__ uint4 ldg128(const uint8_t* p) {
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
   uint4 v;
-  asm volatile(
-      "ld.global.nc.L1::no_allocate.L2::128B.v4.u32 {%0,%1,%2,%3}, [%4];"
-      : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-      : "l"(p));
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a));
   return v;
 }
-__device__ __forceinline__ uint2 ldg64(const uint8_t* p) {
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
   uint2 v;
-  asm volatile("ld.global.nc.L1::no_allocate.L2::128B.v2.u32 {%0,%1}, [%2];"
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];"
                : "=r"(v.x), "=r"(v.y)
-               : "l"(p));
+               : "r"(a));
   return v;
 }
-__device__ __forceinline__ uint32_t ldg32(const uint8_t* p) {
-  uint32_t v;
-  asm volatile("ld.global.nc.L1::no_allocate.L2::128B.u32 %0, [%1];"
-               : "=r"(v)
-               : "l"(p));
+__device__ __forceinline__ uint32_t lds16(uint32_t a) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
   return v;
+}
+__device__ __forceinline__ uint32_t lds8(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
+
+// N-byte global -> shared copy (4, 8: through L1); src_bytes 0 writes zeros.
+template <int N>
+__device__ __forceinline__ void cp_async_n(uint32_t dst, const void* src,
+                                           int src_bytes) {
+  if constexpr (N == 16)
+    cp_async_16(dst, src, src_bytes);
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;\n" ::"r"(dst),
+                 "l"(src), "r"(src_bytes), "n"(N));
 }
 
 // D(16 x 8) += A(16 x 16) B(16 x 8), f16 in, fp32 accumulate.
@@ -140,7 +170,10 @@ struct Smem {
   static constexpr int OSTRIDE = ROWS * D + 4 * (ROWS / 2);   // floats a warp
   static constexpr int OBYTES = kWarps * OSTRIDE * 4;
   static constexpr int MLBYTES = kWarps * ROWS * 8;
-  static constexpr int BYTES = QBYTES + OBYTES + MLBYTES;
+  // (the states take the rings' place)
+  static constexpr int RBYTES = kWarps * Geo<D>::STAGES * Geo<D>::STAGE;
+  static constexpr int BYTES =
+      QBYTES + (RBYTES > OBYTES + MLBYTES ? RBYTES : OBYTES + MLBYTES);
 };
 
 template <int D, int NR>
@@ -148,14 +181,15 @@ constexpr int min_ctas() {
   return NR == 1 ? (D == 256 ? 3 : 4) : (D == 256 ? 2 : 3);
 }
 
-template <typename T, int D, int NR, bool PACKED>
+template <typename T, int D, int NR>
 __global__ void __launch_bounds__(kWarps * 32, min_ctas<D, NR>())
 decode_fp4_kernel(const AttnParams p, int splits) {
   // the fold of the pieces may become resident once every CTA has started
   // (it waits for this grid before reading them)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   using SM = Smem<D, NR>;
-  constexpr int MT = Geo<D>::MT;
+  using GE = Geo<D>;
+  constexpr int MT = GE::MT;
   constexpr int KT = 16 * MT;            // keys of a warp's tile
   constexpr int KS = D / 16;             // k steps of S, and m tiles of O
   constexpr int KW = D / 32;             // words of a lane's K codes per key
@@ -313,20 +347,20 @@ decode_fp4_kernel(const AttnParams p, int splits) {
   auto sub_key = [&](int s) {            // first key of my subtile s
     return kt0 + (warp + (s / MT) * kWarps) * KT + (s % MT) * 16;
   };
-  // page and first row in it of subtile s0 + lane; subtiles past the range
-  // and pages outside the cache take page 0 (a bad page: with the sign bit)
+  // page and first row in it of subtile s0 + lane (-1: past the range, or a
+  // page outside the cache, whose keys read as zero)
   auto fetch = [&](int s0, int& id, int& row) {
     const int s = s0 + lane;
     const int k0 = s < subs ? sub_key(s) : hi;
-    id = row = 0;
+    id = -1;
+    row = 0;
     if (k0 >= hi) return;
     const int j = p.bs_shift >= 0 ? k0 >> p.bs_shift : k0 / p.BS;
     row = k0 - j * p.BS;
     id = __ldg(bt + j);
     if (id < 0 || id >= p.num_blocks) {
       atomicOr(p.err, kErrBadBlock);
-      id = static_cast<int>(0x80000000u);
-      row = 0;
+      id = -1;
     }
   };
   int ids, rows0, ids_next, rows0_next;
@@ -335,107 +369,62 @@ decode_fp4_kernel(const AttnParams p, int splits) {
   const int kap = 4 * (g8 >> 1) + (g8 & 1);
   const uint32_t c_sb = static_cast<uint32_t>(p.c_sb);
   const uint32_t f_sb = static_cast<uint32_t>(p.f_sb);
-  const uint32_t c_sr = PACKED ? D / 2 : static_cast<uint32_t>(p.c_sr);
-  const uint32_t f_sr = PACKED ? D / 16 : static_cast<uint32_t>(p.f_sr);
-  // this lane's part of the page rows
+  const uint32_t c_sr = static_cast<uint32_t>(p.c_sr);
+  const uint32_t f_sr = static_cast<uint32_t>(p.f_sr);
+  // this lane's copies: chunk lane + 32 i of a subtile's codes, and the
+  // scales of one row (lanes 0 .. 15 of K, 16 .. 31 of V)
+  constexpr int NC = GE::SUB / 16 / 32;  // chunks of a lane
+  constexpr int RI = 32 / GE::CPR;       // rows from one to the next
+  const int cp_r = lane / GE::CPR, cp_c = lane % GE::CPR;
   const uint8_t* const KC = static_cast<const uint8_t*>(p.kc) +
-                            static_cast<int64_t>(h) * p.c_sh + kap * c_sr +
-                            (D == 64 ? 8 : 16) * c4;
-  const uint8_t* const VC = static_cast<const uint8_t*>(p.vc) +
-                            static_cast<int64_t>(h) * p.c_sh +
-                            4 * c4 * c_sr + (D / 16) * g8;
-  const uint8_t* const KF = p.k_sf + static_cast<int64_t>(h) * p.f_sh +
-                            kap * f_sr + (D == 64 ? 1 : 2) * c4;
-  const uint8_t* const VF = p.v_sf + static_cast<int64_t>(h) * p.f_sh +
-                            4 * c4 * f_sr +
-                            (D == 64 ? g8 >> 1 : (D / 128) * g8);
-
-  uint32_t kw[MT][2][KW], vw[MT][4][VW];
-  uint32_t kf[MT][2], vf[MT][4];         // scale bytes of the lane's groups
-  int id_of[MT], row_of[MT];             // pages of the keys being loaded
-  auto load_k = [&](int s0) {
+                            static_cast<int64_t>(h) * p.c_sh + cp_r * c_sr +
+                            16 * cp_c;
+  const int64_t k_to_v = static_cast<const uint8_t*>(p.vc) -
+                         static_cast<const uint8_t*>(p.kc);
+  const uint8_t* const SF = (lane < 16 ? p.k_sf : p.v_sf) +
+                            static_cast<int64_t>(h) * p.f_sh +
+                            (lane & 15) * f_sr;
+  const uint32_t ring = smem_u32(smem) + SM::QBYTES +
+                        warp * (GE::STAGES * GE::STAGE);
+  uint32_t k_dst[NC], v_dst[NC];
 #pragma unroll
-    for (int i = 0; i < MT; ++i) {
-      id_of[i] = __shfl_sync(0xffffffffu, ids, (s0 + i) & 31);
-      row_of[i] = __shfl_sync(0xffffffffu, rows0, (s0 + i) & 31);
-      const uint32_t id = id_of[i] & 0x7fffffff;
-      const uint8_t* src = KC + static_cast<uint64_t>(id) * c_sb +
-                           static_cast<uint32_t>(row_of[i]) * c_sr;
-      const uint8_t* fs = KF + static_cast<uint64_t>(id) * f_sb +
-                          static_cast<uint32_t>(row_of[i]) * f_sr;
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        if constexpr (D == 64) {
-          const uint2 v = ldg64(src + 2 * e * c_sr);
-          kw[i][e][0] = v.x;
-          kw[i][e][1] = v.y;
-          kf[i][e] = __ldg(fs + 2 * e * f_sr);
-        } else {
-          kf[i][e] = 0;
-#pragma unroll
-          for (int q = 0; q < D / 128; ++q) {
-            const uint4 v = ldg128(src + 2 * e * c_sr + 64 * q);
-            kw[i][e][4 * q] = v.x;
-            kw[i][e][4 * q + 1] = v.y;
-            kw[i][e][4 * q + 2] = v.z;
-            kw[i][e][4 * q + 3] = v.w;
-            kf[i][e] |= static_cast<uint32_t>(
-                            __ldg(reinterpret_cast<const uint16_t*>(
-                                fs + 2 * e * f_sr + 8 * q)))
-                        << (16 * q);
-          }
-        }
-      }
-      if (id_of[i] < 0) {                // a bad page: keys of zero
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          kf[i][e] = 0;
-#pragma unroll
-          for (int w = 0; w < KW; ++w) kw[i][e][w] = 0;
-        }
-      }
-    }
-  };
-  auto load_v = [&]() {
-#pragma unroll
-    for (int i = 0; i < MT; ++i) {
-      const uint32_t id = id_of[i] & 0x7fffffff;
-      const uint8_t* src = VC + static_cast<uint64_t>(id) * c_sb +
-                           static_cast<uint32_t>(row_of[i]) * c_sr;
-      const uint8_t* fs = VF + static_cast<uint64_t>(id) * f_sb +
-                          static_cast<uint32_t>(row_of[i]) * f_sr;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if constexpr (D == 64) {
-          vw[i][e][0] = ldg32(src + e * c_sr);
-        } else if constexpr (D == 128) {
-          const uint2 v = ldg64(src + e * c_sr);
-          vw[i][e][0] = v.x;
-          vw[i][e][1] = v.y;
-        } else {
-          const uint4 v = ldg128(src + e * c_sr);
-          vw[i][e][0] = v.x;
-          vw[i][e][1] = v.y;
-          vw[i][e][2] = v.z;
-          vw[i][e][3] = v.w;
-        }
-        if constexpr (D == 256)
-          vf[i][e] = __ldg(reinterpret_cast<const uint16_t*>(fs + e * f_sr));
-        else
-          vf[i][e] = __ldg(fs + e * f_sr);
-      }
-      if (id_of[i] < 0) vf[i][0] = vf[i][1] = vf[i][2] = vf[i][3] = 0;
-    }
-  };
-
-  if (mine > 0) {
-    load_k(0);
-    load_v();
+  for (int i = 0; i < NC; ++i) {
+    k_dst[i] = ring + GE::k_off(cp_r + RI * i, cp_c);
+    v_dst[i] = ring + GE::OFF_V + GE::v_off(cp_r + RI * i, cp_c);
   }
+  const uint32_t f_dst = ring + GE::OFF_KF + (lane >> 4) * 256 +
+                         (lane & 15) * 16;
+  auto issue = [&](int s0, uint32_t stage) {
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+      const int id = __shfl_sync(0xffffffffu, ids, (s0 + i) & 31);
+      const uint32_t row = __shfl_sync(0xffffffffu, rows0, (s0 + i) & 31);
+      const int n = id < 0 ? 0 : 16;
+      const uint32_t page = id < 0 ? 0 : id;
+      const uint8_t* src = KC + static_cast<uint64_t>(page) * c_sb +
+                           row * c_sr;
+#pragma unroll
+      for (int j = 0; j < NC; ++j) {
+        const uint8_t* ks = src + j * RI * c_sr;
+        cp_async_16(stage + k_dst[j] + i * GE::SUB, ks, n);
+        cp_async_16(stage + v_dst[j] + i * GE::SUB, ks + k_to_v, n);
+      }
+      cp_async_n<D / 16>(stage + f_dst + i * (D / 16),
+                         SF + static_cast<uint64_t>(page) * f_sb + row * f_sr,
+                         id < 0 ? 0 : D / 16);
+    }
+  };
+
+  if (mine > 0) issue(0, 0);
+  cp_async_commit();
+  if (mine > 1) issue(MT, GE::STAGE);
+  cp_async_commit();
   for (int it = 0; it < mine; ++it) {
     const int kt = kt0 + (warp + it * kWarps) * KT;
-    const int s_next = (it + 1) * MT;
-    const bool more = it + 1 < mine;
+    const uint32_t stage = (it & 1) * GE::STAGE;
+    const uint32_t st = ring + stage;
+    cp_async_wait<1>();
+    __syncwarp();
     // ---- S^T
     float sc[MT][NR][4];
 #pragma unroll
@@ -443,6 +432,32 @@ decode_fp4_kernel(const AttnParams p, int splits) {
 #pragma unroll
       for (int n = 0; n < NR; ++n)
         sc[i][n][0] = sc[i][n][1] = sc[i][n][2] = sc[i][n][3] = 0.f;
+    uint32_t kw[MT][2][KW], kf[MT][2];
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = kap + 2 * e;
+        const uint32_t src = st + i * GE::SUB;
+        const uint32_t fs = st + GE::OFF_KF + r * 16 + i * (D / 16);
+        if constexpr (D == 64) {
+          const uint2 v = lds64(src + GE::k_off(r, c4 >> 1) + 8 * (c4 & 1));
+          kw[i][e][0] = v.x;
+          kw[i][e][1] = v.y;
+          kf[i][e] = lds8(fs + c4);
+        } else {
+          kf[i][e] = 0;
+#pragma unroll
+          for (int q = 0; q < D / 128; ++q) {
+            const uint4 v = lds128(src + GE::k_off(r, 4 * q + c4));
+            kw[i][e][4 * q] = v.x;
+            kw[i][e][4 * q + 1] = v.y;
+            kw[i][e][4 * q + 2] = v.z;
+            kw[i][e][4 * q + 3] = v.w;
+            kf[i][e] |= lds16(fs + 8 * q + 2 * c4) << (16 * q);
+          }
+        }
+      }
     // block scales of the lane's keys, two groups (D = 64: two keys) a word
     constexpr int FW = D == 256 ? 2 : 1;
     uint32_t fk[MT][2][FW];
@@ -490,15 +505,6 @@ decode_fp4_kernel(const AttnParams p, int splits) {
           mma(sc[i][n], a[2], c[2], a[3], c[3], qb[n].z, qb[n].w);
         }
       }
-    }
-    // the next tile's keys
-    if (more) {
-      if ((s_next & 31) == 0) {
-        ids = ids_next;
-        rows0 = rows0_next;
-        fetch(s_next + 32, ids_next, rows0_next);
-      }
-      load_k(s_next);
     }
     // ---- logits (base 2) and masks
     const bool interior = kt >= full_lo && kt + KT <= full_hi;
@@ -590,15 +596,37 @@ decode_fp4_kernel(const AttnParams p, int splits) {
       }
     }
     // ---- O^T += V^T P^T
+    constexpr int VG = D == 256 ? 2 : 1;     // block scales of a lane
+    // scales of the lane's four keys, a byte each, per subtile and group
+    uint32_t vf[MT][VG];
+    if constexpr (D == 64) {
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        uint32_t f[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          f[e] = lds8(st + GE::OFF_VF + (4 * c4 + e) * 16 + i * 4 +
+                      (g8 >> 1));
+        vf[i][0] = __byte_perm(__byte_perm(f[0], f[1], 0x40),
+                               __byte_perm(f[2], f[3], 0x40), 0x5410);
+      }
+    } else {
+      // rows are keys, columns groups (of two subtiles at D = 128)
+      uint32_t d0, d1;
+      ldmatrix_b8_trans(st + GE::OFF_VF + (lane & 15) * 16, d0, d1);
+      vf[0][0] = d0;
+      vf[MT - 1][VG - 1] = d1;
+    }
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
-      constexpr int VG = D == 256 ? 2 : 1;   // block scales of a lane's run
       if (!interior) {
         // keys outside [lo, hi): a scale of 0
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int key = kt + 16 * i + 4 * c4 + e;
-          if (key < lo || key >= hi) vf[i][e] = 0;
+          if (key < lo || key >= hi)
+#pragma unroll
+            for (int v = 0; v < VG; ++v) vf[i][v] &= ~(0xffu << (8 * e));
         }
         // NaN scales: set aside, and added to the rows that see the key
         uint32_t nan_bits[VG];
@@ -608,7 +636,7 @@ decode_fp4_kernel(const AttnParams p, int splits) {
           nan_bits[v] = 0;
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            if (((vf[i][e] >> (8 * v)) & 0x7fu) == 0x7fu)
+            if (((vf[i][v] >> (8 * e)) & 0x7fu) == 0x7fu)
               nan_bits[v] |= 1u << (4 * c4 + e);
           any = any || nan_bits[v] != 0;
         }
@@ -618,7 +646,7 @@ decode_fp4_kernel(const AttnParams p, int splits) {
 #pragma unroll
             for (int e = 0; e < 4; ++e)
               if ((nan_bits[v] >> (4 * c4 + e)) & 1u)
-                vf[i][e] &= ~(0xffu << (8 * v));
+                vf[i][v] &= ~(0xffu << (8 * e));
             nan_bits[v] |= __shfl_xor_sync(0xffffffffu, nan_bits[v], 1);
             nan_bits[v] |= __shfl_xor_sync(0xffffffffu, nan_bits[v], 2);
 #pragma unroll
@@ -646,42 +674,69 @@ decode_fp4_kernel(const AttnParams p, int splits) {
           }
         }
       }
-      uint32_t s01[VG], s23[VG];
 #pragma unroll
       for (int v = 0; v < VG; ++v) {
-        const uint32_t sel = v ? 0x51u : 0x40u;   // byte v of each
-        s01[v] = e4m3x2_to_f16(__byte_perm(vf[i][0], vf[i][1], sel));
-        s23[v] = e4m3x2_to_f16(__byte_perm(vf[i][2], vf[i][3], sel));
-      }
-#pragma unroll
-      for (int w = 0; w < VW; ++w) {
-        const uint32_t w0 = vw[i][0][w], w1 = vw[i][1][w];
-        const uint32_t w2 = vw[i][2][w], w3 = vw[i][3][w];
-        // bytes (key, next key) of the even and of the odd dimensions
-        const uint32_t e01 = (w0 & 0x0f0f0f0fu) | ((w1 << 4) & 0xf0f0f0f0u);
-        const uint32_t o01 = ((w0 >> 4) & 0x0f0f0f0fu) | (w1 & 0xf0f0f0f0u);
-        const uint32_t e23 = (w2 & 0x0f0f0f0fu) | ((w3 << 4) & 0xf0f0f0f0u);
-        const uint32_t o23 = ((w2 >> 4) & 0x0f0f0f0fu) | (w3 & 0xf0f0f0f0u);
-        uint32_t a0[4], a1[4], a2[4], a3[4];
-        e2m1x8_to_f16(e01, a0[0], a0[1], a0[2], a0[3]);
-        e2m1x8_to_f16(o01, a1[0], a1[1], a1[2], a1[3]);
-        e2m1x8_to_f16(e23, a2[0], a2[1], a2[2], a2[3]);
-        e2m1x8_to_f16(o23, a3[0], a3[1], a3[2], a3[3]);
-        const int v = D == 256 ? w >> 1 : 0;
+        const uint32_t s01 = e4m3x2_to_f16(vf[i][v]);
+        const uint32_t s23 = e4m3x2_to_f16(vf[i][v] >> 16);
+        // the lane's run of the four keys' rows: 16 dimensions (D = 64: 8)
+        constexpr int RW = D == 64 ? 1 : 2;
+        uint32_t vw[4][RW];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const uint32_t x0 = hmul2_u32(a0[e], s01[v]);
-          const uint32_t x1 = hmul2_u32(a1[e], s01[v]);
-          const uint32_t x2 = hmul2_u32(a2[e], s23[v]);
-          const uint32_t x3 = hmul2_u32(a3[e], s23[v]);
+          const int r = 4 * c4 + e;
+          const uint32_t src = st + GE::OFF_V + i * GE::SUB;
+          if constexpr (D == 64) {
+            vw[e][0] = lds32(src + GE::v_off(r, g8 >> 2) + 4 * (g8 & 3));
+          } else {
+            const uint2 x = lds64(src + GE::v_off(r, 4 * v + (g8 >> 1)) +
+                                  8 * (g8 & 1));
+            vw[e][0] = x.x;
+            vw[e][1] = x.y;
+          }
+        }
 #pragma unroll
-          for (int n = 0; n < NR; ++n)
-            mma(o[4 * w + e][n], x0, x1, x2, x3, pb[i][n][0], pb[i][n][1]);
+        for (int w = 0; w < RW; ++w) {
+          const uint32_t w0 = vw[0][w], w1 = vw[1][w];
+          const uint32_t w2 = vw[2][w], w3 = vw[3][w];
+          // bytes (key, next key) of the even and of the odd dimensions
+          const uint32_t e01 = (w0 & 0x0f0f0f0fu) | ((w1 << 4) & 0xf0f0f0f0u);
+          const uint32_t o01 = ((w0 >> 4) & 0x0f0f0f0fu) | (w1 & 0xf0f0f0f0u);
+          const uint32_t e23 = (w2 & 0x0f0f0f0fu) | ((w3 << 4) & 0xf0f0f0f0u);
+          const uint32_t o23 = ((w2 >> 4) & 0x0f0f0f0fu) | (w3 & 0xf0f0f0f0u);
+          uint32_t a0[4], a1[4], a2[4], a3[4];
+          e2m1x8_to_f16(e01, a0[0], a0[1], a0[2], a0[3]);
+          e2m1x8_to_f16(o01, a1[0], a1[1], a1[2], a1[3]);
+          e2m1x8_to_f16(e23, a2[0], a2[1], a2[2], a2[3]);
+          e2m1x8_to_f16(o23, a3[0], a3[1], a3[2], a3[3]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t x0 = hmul2_u32(a0[e], s01);
+            const uint32_t x1 = hmul2_u32(a1[e], s01);
+            const uint32_t x2 = hmul2_u32(a2[e], s23);
+            const uint32_t x3 = hmul2_u32(a3[e], s23);
+#pragma unroll
+            for (int n = 0; n < NR; ++n)
+              mma(o[(v * RW + w) * 4 + e][n], x0, x1, x2, x3, pb[i][n][0],
+                  pb[i][n][1]);
+          }
         }
       }
     }
-    if (more) load_v();
+    // this stage is read: the tile after the next one into it
+    __syncwarp();
+    const int s_new = (it + 2) * MT;
+    if (it + 2 < mine) {
+      if ((s_new & 31) == 0) {
+        ids = ids_next;
+        rows0 = rows0_next;
+        fetch(s_new + 32, ids_next, rows0_next);
+      }
+      issue(s_new, stage);
+    }
+    cp_async_commit();
   }
+  cp_async_wait<0>();
+  __syncthreads();       // (the states take the rings' place)
 
   // ---- the warps' states meet: row r of warp w at r D + 4 (r / 2) floats
   // (conflict-free float4 stores)
@@ -698,11 +753,12 @@ decode_fp4_kernel(const AttnParams p, int splits) {
       t += __shfl_xor_sync(0xffffffffu, t, 16);
       const int r = 8 * n + 2 * c4 + e;
       if (g8 == 0) ml[warp * SM::ROWS + r] = make_float2(m[n][e], t);
-      // dimensions 16 (D / 128) g8 .. of the row, two m tiles a store
-      float* dst = mine_o + r * D + 4 * (r >> 1) + (D / 8) * g8;
+      // o[i]: dimensions 2 (i % 8) and the next one of the lane's run
+      // i / 8 (16 g8 of each 128; D = 64: 8 g8), two m tiles a store
+      float* dst = mine_o + r * D + 4 * (r >> 1) + (D == 64 ? 8 : 16) * g8;
 #pragma unroll
       for (int i = 0; i < KS; i += 2)
-        *reinterpret_cast<float4*>(dst + 2 * i) =
+        *reinterpret_cast<float4*>(dst + 128 * (i >> 3) + 2 * (i & 7)) =
             make_float4(o[i][n][e], o[i][n][e + 2], o[i + 1][n][e],
                         o[i + 1][n][e + 2]);
     }
@@ -826,10 +882,10 @@ __global__ void __launch_bounds__(128) combine_kernel(const CombineParams p) {
   }
 }
 
-template <typename T, int D, int NR, bool PACKED>
+template <typename T, int D, int NR>
 cudaError_t launch(const AttnParams& p, int splits, cudaStream_t stream) {
   using SM = Smem<D, NR>;
-  auto kern = decode_fp4_kernel<T, D, NR, PACKED>;
+  auto kern = decode_fp4_kernel<T, D, NR>;
   cudaError_t e = smem_opt_in(reinterpret_cast<const void*>(kern), SM::BYTES);
   if (e != cudaSuccess) return e;
   const int64_t ctas = static_cast<int64_t>(p.batch) * splits * p.Hkv;
@@ -844,12 +900,8 @@ template <typename T, int D>
 cudaError_t dispatch_rows(const AttnParams& p, int splits,
                           cudaStream_t stream) {
   const bool one = p.sk_rows <= 8;       // packed query rows of a request
-  const bool packed = p.c_sr == D / 2 && p.f_sr == D / 16;
-  if (packed)
-    return one ? launch<T, D, 1, true>(p, splits, stream)
-               : launch<T, D, 2, true>(p, splits, stream);
-  return one ? launch<T, D, 1, false>(p, splits, stream)
-             : launch<T, D, 2, false>(p, splits, stream);
+  return one ? launch<T, D, 1>(p, splits, stream)
+             : launch<T, D, 2>(p, splits, stream);
 }
 
 template <typename T>

@@ -353,8 +353,9 @@ pkv_status check_fp4(const pkv_fp4_scales* f, int head_size) {
                 "a 4-bit cache needs block scales, k_scale and v_scale");
   if (f->strides[3] != 1)
     return fail(PKV_ERR_INVALID_ARG, "block scale rows must be contiguous");
-  const int a = head_size / 64;         // 1, 2 or 4 bytes a quarter row
-  const int unit = a % 4 == 0 ? 4 : a % 2 == 0 ? 2 : 1;
+  // (a row of 4, 8 or 16 scales is one copy of the decode kernel)
+  const int a = head_size / 16;
+  const int unit = a % 16 == 0 ? 16 : a % 8 == 0 ? 8 : 4;
   auto on = [&](const void* q) {
     return reinterpret_cast<uintptr_t>(q) % unit == 0;
   };

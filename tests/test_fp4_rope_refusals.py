@@ -70,11 +70,11 @@ def write(lib, **kw):
     (dict(slots=None), 1, b"NULL"),
     (dict(sc=ctypes.byref(Scales(v_block_scale=None))), 1, b"block scales"),
     (dict(sc=ctypes.byref(Scales(k_scale=None))), 1, b"k_scale"),
-    (dict(sc=ctypes.byref(Scales(k_block_scale=P + 1))), 2, b"2-byte"),
+    (dict(sc=ctypes.byref(Scales(k_block_scale=P + 1))), 2, b"8-byte"),
     (dict(sc=ctypes.byref(Scales(strides=strides(512, 8, 128, 2)))), 1,
      b"contiguous"),
     (dict(sc=ctypes.byref(Scales(strides=strides(512, 9, 128, 1)))), 2,
-     b"2-byte"),
+     b"8-byte"),
 ])
 def test_write_refuses(lib, kw, status, text):
     assert write(lib, **kw) == status
