@@ -52,6 +52,11 @@ namespace dfp4 {
 
 constexpr int kWarps = 4;
 constexpr float kRaise = 6.f;      // log2 slack of the running maximum
+// Tiles of a CTA's share at least, so that each warp has some.
+constexpr int kMinTiles = 2 * kWarps;
+constexpr int kFoldThreads = 256;
+
+inline size_t up256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 // One stage of a warp's ring: MT subtiles of 16 keys, K codes, V codes, then
 // 16 rows of 16 bytes of K scales and as many of V scales (row r: the scales
@@ -128,6 +133,26 @@ __device__ __forceinline__ void cp_async_n(uint32_t dst, const void* src,
                  "l"(src), "r"(src_bytes), "n"(N));
 }
 
+// Two float32 values as one operand of the packed instructions.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
 // D(16 x 8) += A(16 x 16) B(16 x 8), f16 in, fp32 accumulate.
 __device__ __forceinline__ void mma(float* d, uint32_t a0, uint32_t a1,
                                     uint32_t a2, uint32_t a3, uint32_t b0,
@@ -163,23 +188,61 @@ __device__ __forceinline__ float soft_cap(float x, float t, float u) {
 
 template <int D, int NR>
 struct Smem {
-  // query fragments (one 16-byte load serves two k steps of every subtile)
-  // and the warps' states at the end
+  // query fragments (one 16-byte load serves two k steps of every subtile),
+  // the warps' rings, and their states at the end of a unit
   static constexpr int ROWS = 8 * NR;
   static constexpr int QBYTES = (D / 32) * NR * 32 * 16;
   static constexpr int OSTRIDE = ROWS * D + 4 * (ROWS / 2);   // floats a warp
-  static constexpr int OBYTES = kWarps * OSTRIDE * 4;
-  static constexpr int MLBYTES = kWarps * ROWS * 8;
-  // (the states take the rings' place)
-  static constexpr int RBYTES = kWarps * Geo<D>::STAGES * Geo<D>::STAGE;
-  static constexpr int BYTES =
-      QBYTES + (RBYTES > OBYTES + MLBYTES ? RBYTES : OBYTES + MLBYTES);
+  static constexpr int OFF_RING = QBYTES;
+  static constexpr int OFF_O =
+      OFF_RING + kWarps * Geo<D>::STAGES * Geo<D>::STAGE;
+  static constexpr int OFF_ML = OFF_O + kWarps * OSTRIDE * 4;
+  static constexpr int BYTES = OFF_ML + kWarps * ROWS * 8;
 };
 
 template <int D, int NR>
 constexpr int min_ctas() {
-  return NR == 1 ? (D == 256 ? 3 : 4) : (D == 256 ? 2 : 3);
+  return NR == 1 ? 3 : (D == 256 ? 2 : 3);
 }
+
+// What a request's rows see of its keys.
+struct Req {
+  int q0, q_len, rows, L, lo, hi;      // rows 0: not of this launch
+};
+__device__ __forceinline__ Req request(const AttnParams& p, int b,
+                                       int max_rows, bool flag) {
+  Req r{};
+  const int L = p.seqused_k[b];          // (three loads in flight at once)
+  r.q0 = p.cu_q[b];
+  r.q_len = min(p.cu_q[b + 1] - r.q0, p.total_q - r.q0);
+  if (r.q0 < 0 || r.q_len <= 0) return r;
+  const int rows = r.q_len * p.G;
+  if (rows < p.min_rows || rows > p.max_rows) return r;
+  if (rows > max_rows) {
+    // more query rows than the call's max_seqlen_q allows: not computed
+    if (flag) atomicOr(p.err, kErrQueryLen);
+    return r;
+  }
+  r.rows = rows;
+  r.L = L;
+  const int64_t tab = static_cast<int64_t>(p.max_blocks) * p.BS;
+  const int L_tab = r.L < tab ? r.L : static_cast<int>(tab);
+  if (flag && L_tab < r.L) atomicOr(p.err, kErrBadTable);
+  int kmin, kmax;
+  key_range(r.L, r.q_len, 0, r.q_len - 1, p.causal, p.wl, p.wr, kmin, kmax);
+  r.lo = kmin;
+  r.hi = max(kmin, min(kmax, L_tab));
+  return r;
+}
+
+// A run of tiles of one (request, KV head), as a CTA works through it.
+struct Piece {
+  int b, h;
+  Req r;
+  int kt0;              // first key of tile 0 of the unit (or of the split)
+  int t0, t1;           // tiles
+  int slot;             // partial slot, or -1
+};
 
 template <typename T, int D, int NR>
 __global__ void __launch_bounds__(kWarps * 32, min_ctas<D, NR>())
@@ -187,204 +250,173 @@ decode_fp4_kernel(const AttnParams p, int splits) {
   // the fold of the pieces may become resident once every CTA has started
   // (it waits for this grid before reading them)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  // launched as a programmatic dependent of the kernel before it: nothing is
+  // read before that one is complete (a no-op for a plain launch)
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   using SM = Smem<D, NR>;
   using GE = Geo<D>;
   constexpr int MT = GE::MT;
   constexpr int KT = 16 * MT;            // keys of a warp's tile
   constexpr int KS = D / 16;             // k steps of S, and m tiles of O
   constexpr int KW = D / 32;             // words of a lane's K codes per key
-  constexpr int VW = D / 64;             // words of a lane's V codes per key
-  extern __shared__ __align__(16) unsigned char smem[];
+  constexpr int NT = kWarps * 32;
+  // (a cp.async chunk pair that straddles 32 bytes of shared memory costs two
+  // L2 sectors: 0.226 against 0.205 ms on 8 x 131072 keys)
+  extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ long long scan[kWarps];
+  // what the inner loop seldom needs: the piece, and by packed row the token
+  // of its request and its ALiBi slope (base 2)
+  __shared__ Piece cur;
+  __shared__ int row_tok[16];
+  __shared__ float row_slope[16];
 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g8 = lane >> 2, c4 = lane & 3;
   const int G = p.G;
-  // CTAs in the order (request, piece, KV head): neighbours read the same
-  // pages
-  const int h = blockIdx.x % p.Hkv;
-  const unsigned rest = blockIdx.x / p.Hkv;
-  const int sp = rest % splits;
-  const int b = rest / splits;
+  const bool sequence = p.sk_chunks > 0;
+  const float base_scale = p.scale * *p.k_scale * kLog2e;
+  const float vscale = *p.v_scale;
 
-  const int q0 = p.cu_q[b];
-  const int q_len = min(p.cu_q[b + 1] - q0, p.total_q - q0);
-  if (q0 < 0 || q_len <= 0) return;
-  const int rows = q_len * G;
-  if (rows < p.min_rows || rows > p.max_rows) return;
-  if (rows > 8 * NR) {
-    // more query rows than the call's max_seqlen_q allows: not computed
-    if (sp == 0 && h == 0 && threadIdx.x == 0) atomicOr(p.err, kErrQueryLen);
-    return;
-  }
-  const int L = p.seqused_k[b];
-  const int64_t tab = static_cast<int64_t>(p.max_blocks) * p.BS;
-  const int L_tab = L < tab ? L : static_cast<int>(tab);
-  if (L_tab < L && sp == 0 && h == 0 && threadIdx.x == 0)
-    atomicOr(p.err, kErrBadTable);
-  int kmin, kmax;
-  key_range(L, q_len, 0, q_len - 1, p.causal, p.wl, p.wr, kmin, kmax);
-  int lo = kmin, hi = kmax;
-  if (p.chunk > 0) {
-    const int ns = split_count(kmin, kmax, p.chunk, splits);
-    if (sp >= ns) return;
-    split_bounds(kmin, kmax, p.chunk, ns, sp, lo, hi);
-  }
-  hi = max(lo, min(hi, L_tab));
-
-  // ---- queries: lane (g8, c4) takes row g8 (and g8 + 8), the dimensions of
-  // its K run.  A bf16 row is scaled by the power of two that puts its
-  // largest magnitude in [2^14, 2^15): exact in f16; the factor joins the
-  // row's logit scale.
-  float row_scale[NR][2];   // logit scale (base 2) of rows 2 c4, 2 c4 + 1
-  {
-    const T* Q = static_cast<const T*>(p.q);
-    const float base_scale = p.scale * *p.k_scale * kLog2e;
-    uint4* qs = reinterpret_cast<uint4*>(smem);
-#pragma unroll
-    for (int n = 0; n < NR; ++n) {
-      const int r = g8 + 8 * n;
-      uint4 raw[KW];
-      float mx = 0.f;
-#pragma unroll
-      for (int i = 0; i < KW; ++i) raw[i] = make_uint4(0, 0, 0, 0);
-      if (r < rows) {
-        const T* src = Q + static_cast<int64_t>(q0 + r / G) * p.q_st +
-                       static_cast<int64_t>(h * G + r % G) * p.q_sh;
-#pragma unroll
-        for (int i = 0; i < KW; ++i) {
-          // word i of the run: 8 dimensions (D = 256: two runs of 4 words)
-          const int d = D == 256 ? 128 * (i >> 2) + 32 * c4 + 8 * (i & 3)
-                                 : 8 * KW * c4 + 8 * i;
-          raw[i] = *reinterpret_cast<const uint4*>(src + d);
-        }
-      }
-      float qmul = 1.f, back = 1.f;
-      if constexpr (!std::is_same<T, __half>::value) {
-#pragma unroll
-        for (int i = 0; i < KW; ++i) {
-          float x[8];
-          widen8<T>(raw[i], x);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) mx = fmaxf(mx, fabsf(x[e]));
-        }
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        int shift = 0;
-        if (mx > 0.f) {
-          shift = static_cast<int>((__float_as_uint(mx) >> 23) & 0xff) - 141;
-          shift = max(-100, min(100, shift));
-        }
-        qmul = __uint_as_float(static_cast<uint32_t>(127 - shift) << 23);
-        back = __uint_as_float(static_cast<uint32_t>(127 + shift) << 23);
-      }
-#pragma unroll
-      for (int e = 0; e < 2; ++e)
-        row_scale[n][e] =
-            __shfl_sync(0xffffffffu, back, (2 * c4 + e) * 4) * base_scale;
-#pragma unroll
-      for (int i = 0; i < KW; ++i) {
-        const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-        uint32_t f[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          f[e] = std::is_same<T, __half>::value
-                     ? w[e]
-                     : pack2<__half>(elem_f32<T>(w[e], 0) * qmul,
-                                     elem_f32<T>(w[e], 1) * qmul);
-        // 8 dimensions: the B operands of k steps 2 i and 2 i + 1
-        if (KW < kWarps || (i & (kWarps - 1)) == warp)
-          qs[(i * NR + n) * 32 + lane] = make_uint4(f[0], f[1], f[2], f[3]);
-      }
-    }
-  }
-  __syncthreads();
-
-  const bool plain = p.softcap <= 0.f && p.alibi == nullptr;
-  const float cap_t = p.softcap * kLog2e;
-  const float cap_u = p.softcap > 0.f ? 2.f / p.softcap : 0.f;
-  const int ctx = L - q_len;
-  int pos[NR][2];
-  float slope[NR][2];
-  bool live[NR][2];
-#pragma unroll
-  for (int n = 0; n < NR; ++n)
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int r = 8 * n + 2 * c4 + e;
-      live[n][e] = r < rows;
-      pos[n][e] = ctx + r / G;
-      slope[n][e] =
-          p.alibi && r < rows ? p.alibi[h * G + r % G] * kLog2e : 0.f;
-    }
-  // keys in [full_lo, full_hi) are seen by every row
-  int full_lo = lo, full_hi = hi;
-  {
-    const int p_lo = ctx, p_hi = ctx + q_len - 1;
-    if (p.wl >= 0) full_lo = max(full_lo, p_hi - p.wl);
-    if (p.causal) full_hi = min(full_hi, p_lo + 1);
-    if (p.wr >= 0) full_hi = min(full_hi, p_lo + p.wr + 1);
-  }
-
-  float o[KS][NR][4];
-#pragma unroll
-  for (int i = 0; i < KS; ++i)
-#pragma unroll
-    for (int n = 0; n < NR; ++n)
-      o[i][n][0] = o[i][n][1] = o[i][n][2] = o[i][n][3] = 0.f;
-  float m[NR][2], l[NR][2];
-#pragma unroll
-  for (int n = 0; n < NR; ++n) {
-    m[n][0] = m[n][1] = -INFINITY;
-    l[n][0] = l[n][1] = 0.f;
-  }
-
-  // ---- the warp's tiles: kt0 + (warp + i kWarps) KT
-  const int kt0 = lo & ~15;
-  const int tiles = hi > lo ? (hi - kt0 + KT - 1) / KT : 0;
-  const int32_t* bt = p.block_table + static_cast<int64_t>(b) * p.bt_stride;
-  const int mine = tiles > warp ? (tiles - warp + kWarps - 1) / kWarps : 0;
-  const int subs = mine * MT;
-  auto sub_key = [&](int s) {            // first key of my subtile s
-    return kt0 + (warp + (s / MT) * kWarps) * KT + (s % MT) * 16;
+  // ---- this CTA's first piece
+  Piece pc;
+  int left = 0;          // tiles of the CTA's share past this piece
+  auto tiles_of = [&](const Req& r) {
+    const int k0 = r.lo & ~15;
+    return r.rows == 0 ? 0 : max(1, (r.hi - k0 + KT - 1) / KT);
   };
-  // page and first row in it of subtile s0 + lane (-1: past the range, or a
-  // page outside the cache, whose keys read as zero)
-  auto fetch = [&](int s0, int& id, int& row) {
-    const int s = s0 + lane;
-    const int k0 = s < subs ? sub_key(s) : hi;
-    id = -1;
-    row = 0;
-    if (k0 >= hi) return;
-    const int j = p.bs_shift >= 0 ? k0 >> p.bs_shift : k0 / p.BS;
-    row = k0 - j * p.BS;
-    id = __ldg(bt + j);
-    if (id < 0 || id >= p.num_blocks) {
-      atomicOr(p.err, kErrBadBlock);
-      id = -1;
+  if (!sequence) {
+    // one (request, piece, KV head) each; neighbours read the same pages
+    pc.h = blockIdx.x % p.Hkv;
+    const unsigned rest = blockIdx.x / p.Hkv;
+    const int sp = rest % splits;
+    pc.b = rest / splits;
+    pc.r = request(p, pc.b, 8 * NR, sp == 0 && pc.h == 0 && threadIdx.x == 0);
+    if (pc.r.rows == 0) return;
+    pc.slot = -1;
+    if (p.chunk > 0) {
+      // (the pieces are cut before the table's end clips the range)
+      int kmin, kmax;
+      key_range(pc.r.L, pc.r.q_len, 0, pc.r.q_len - 1, p.causal, p.wl, p.wr,
+                kmin, kmax);
+      const int ns = split_count(kmin, kmax, p.chunk, splits);
+      if (sp >= ns) return;
+      int lo, hi;
+      split_bounds(kmin, kmax, p.chunk, ns, sp, lo, hi);
+      pc.r.lo = lo;
+      pc.r.hi = max(lo, min(hi, pc.r.hi));
+      pc.slot = sp;
     }
+    pc.kt0 = pc.r.lo & ~15;
+    pc.t0 = 0;
+    pc.t1 = tiles_of(pc.r);
+  } else {
+    // The units (request, KV head) in order form a sequence of N tiles, of
+    // which every CTA takes an equal run.  Thread t counts the tiles of a
+    // run of requests; the one whose run holds the CTA's first tile finds it.
+    const int per = (p.batch + NT - 1) / NT;
+    const int b_lo = min(p.batch, static_cast<int>(threadIdx.x) * per);
+    const int b_hi = min(p.batch, b_lo + per);
+    long long sum = 0;
+    Req mine_req{};
+    for (int b = b_lo; b < b_hi; ++b) {
+      mine_req = request(p, b, p.sk_rows, blockIdx.x == 0);
+      sum += static_cast<long long>(tiles_of(mine_req)) * p.Hkv;
+    }
+    long long incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+      const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    if (lane == 31) scan[warp] = incl;
+    __syncthreads();
+    long long N = 0, excl = incl - sum;
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) excl += scan[w];
+      N += scan[w];
+    }
+    // at least kMinTiles tiles a CTA
+    const long long Cs =
+        max(1LL, min(static_cast<long long>(p.sk_chunks), N / kMinTiles));
+    const int c = blockIdx.x;
+    if (c >= Cs || N == 0) {
+      if (threadIdx.x == 0) p.sk_marks[c] = make_int2(-1, -1);
+      return;
+    }
+    auto bound = [&](long long k) -> long long {     // (32-bit where it can)
+      return N < (1 << 16) ? static_cast<unsigned>(k * N) /
+                                 static_cast<unsigned>(Cs)
+                           : k * N / Cs;
+    };
+    const long long T0 = bound(c), T1 = bound(c + 1);
+    if (sum > 0 && T0 >= excl && T0 < excl + sum) {
+      long long at = excl;
+      for (int b = b_lo; b < b_hi; ++b) {
+        const Req r = per == 1 ? mine_req : request(p, b, p.sk_rows, false);
+        const int n = tiles_of(r);
+        const long long all = static_cast<long long>(n) * p.Hkv;
+        if (T0 < at + all) {
+          const unsigned off = static_cast<unsigned>(T0 - at);
+          cur.b = b;
+          cur.h = off / n;
+          cur.t0 = off % n;
+          cur.r = r;
+          break;
+        }
+        at += all;
+      }
+    }
+    __syncthreads();
+    pc = cur;
+    pc.kt0 = pc.r.lo & ~15;
+    const int n = tiles_of(pc.r), want = static_cast<int>(T1 - T0);
+    pc.t1 = min(n, pc.t0 + want);
+    left = want - (pc.t1 - pc.t0);
+    __syncthreads();                     // (`cur` is written again)
+    // a unit cut by the share's ends leaves its part in slot 2 c (begun
+    // before) or 2 c + 1 (ending after)
+    pc.slot = pc.t0 > 0 ? 2 * c : pc.t1 < n ? 2 * c + 1 : -1;
+    if (threadIdx.x == 0) {
+      p.sk_marks[c].x = pc.t0 > 0 ? pc.b * p.Hkv + pc.h : -1;
+      if (left == 0)
+        p.sk_marks[c].y =
+            pc.t0 == 0 && pc.t1 < n ? pc.b * p.Hkv + pc.h : -1;
+    }
+  }
+  // the piece after `a` in the CTA's share (left > 0)
+  auto next_piece = [&](const Piece& a) {
+    Piece x = a;
+    if (++x.h == p.Hkv) {
+      x.h = 0;
+      do {
+        ++x.b;
+        x.r = request(p, x.b, p.sk_rows, false);
+      } while (x.r.rows == 0 && x.b + 1 < p.batch);
+      x.kt0 = x.r.lo & ~15;
+    }
+    const int n = tiles_of(x.r);
+    x.t0 = 0;
+    x.t1 = min(n, left);
+    left -= x.t1;
+    x.slot = x.t1 < n ? 2 * static_cast<int>(blockIdx.x) + 1 : -1;
+    if (left == 0 && threadIdx.x == 0)
+      p.sk_marks[blockIdx.x].y = x.t1 < n ? x.b * p.Hkv + x.h : -1;
+    return x;
   };
-  int ids, rows0, ids_next, rows0_next;
-  fetch(0, ids, rows0);
-  fetch(32, ids_next, rows0_next);
+
+  // ---- copies: chunk lane + 32 i of a subtile's codes, and the scales of
+  // one row (lanes 0 .. 15 of K, 16 .. 31 of V)
   const int kap = 4 * (g8 >> 1) + (g8 & 1);
   const uint32_t c_sb = static_cast<uint32_t>(p.c_sb);
   const uint32_t f_sb = static_cast<uint32_t>(p.f_sb);
   const uint32_t c_sr = static_cast<uint32_t>(p.c_sr);
   const uint32_t f_sr = static_cast<uint32_t>(p.f_sr);
-  // this lane's copies: chunk lane + 32 i of a subtile's codes, and the
-  // scales of one row (lanes 0 .. 15 of K, 16 .. 31 of V)
   constexpr int NC = GE::SUB / 16 / 32;  // chunks of a lane
   constexpr int RI = 32 / GE::CPR;       // rows from one to the next
   const int cp_r = lane / GE::CPR, cp_c = lane % GE::CPR;
-  const uint8_t* const KC = static_cast<const uint8_t*>(p.kc) +
-                            static_cast<int64_t>(h) * p.c_sh + cp_r * c_sr +
-                            16 * cp_c;
   const int64_t k_to_v = static_cast<const uint8_t*>(p.vc) -
                          static_cast<const uint8_t*>(p.kc);
-  const uint8_t* const SF = (lane < 16 ? p.k_sf : p.v_sf) +
-                            static_cast<int64_t>(h) * p.f_sh +
-                            (lane & 15) * f_sr;
-  const uint32_t ring = smem_u32(smem) + SM::QBYTES +
+  const uint32_t ring = smem_u32(smem) + SM::OFF_RING +
                         warp * (GE::STAGES * GE::STAGE);
   uint32_t k_dst[NC], v_dst[NC];
 #pragma unroll
@@ -394,6 +426,29 @@ decode_fp4_kernel(const AttnParams p, int splits) {
   }
   const uint32_t f_dst = ring + GE::OFF_KF + (lane >> 4) * 256 +
                          (lane & 15) * 16;
+
+  // state of the copies: the piece's tiles warp, warp + kWarps, ..., as
+  // subtiles s = 0 .. subs - 1; lane i holds subtile i of the current batch
+  // of 32: its page and first row in it (-1: past the range, or a page
+  // outside the cache, whose keys read as zero)
+  int ids, rows0, ids_next, rows0_next;
+  const uint8_t* KC;
+  const uint8_t* SF;
+  int mine, key0;
+  auto fetch = [&](int s0, int b, int hi, int& id, int& row) {
+    const int s = s0 + lane;
+    const int k0 = key0 + (s / MT) * (kWarps * KT) + (s % MT) * 16;
+    id = -1;
+    row = 0;
+    if (s >= mine * MT || k0 >= hi) return;
+    const int j = p.bs_shift >= 0 ? k0 >> p.bs_shift : k0 / p.BS;
+    row = k0 - j * p.BS;
+    id = __ldg(p.block_table + static_cast<int64_t>(b) * p.bt_stride + j);
+    if (id < 0 || id >= p.num_blocks) {
+      atomicOr(p.err, kErrBadBlock);
+      id = -1;
+    }
+  };
   auto issue = [&](int s0, uint32_t stage) {
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
@@ -414,403 +469,613 @@ decode_fp4_kernel(const AttnParams p, int splits) {
                          id < 0 ? 0 : D / 16);
     }
   };
+  // a piece's pages, then its first two tiles
+  auto begin_pages = [&](const Piece& x) {
+    const int n = x.t1 - x.t0;
+    mine = n > warp ? (n - warp + kWarps - 1) / kWarps : 0;
+    key0 = x.kt0 + (x.t0 + warp) * KT;
+    KC = static_cast<const uint8_t*>(p.kc) +
+         static_cast<int64_t>(x.h) * p.c_sh + cp_r * c_sr + 16 * cp_c;
+    SF = (lane < 16 ? p.k_sf : p.v_sf) + static_cast<int64_t>(x.h) * p.f_sh +
+         (lane & 15) * f_sr;
+    fetch(0, x.b, x.r.hi, ids, rows0);
+    fetch(32, x.b, x.r.hi, ids_next, rows0_next);
+  };
+  auto begin_copies = [&]() {
+    if (mine > 0) issue(0, 0);
+    cp_async_commit();
+    if (mine > 1) issue(MT, GE::STAGE);
+    cp_async_commit();
+  };
 
-  if (mine > 0) issue(0, 0);
-  cp_async_commit();
-  if (mine > 1) issue(MT, GE::STAGE);
-  cp_async_commit();
-  for (int it = 0; it < mine; ++it) {
-    const int kt = kt0 + (warp + it * kWarps) * KT;
-    const uint32_t stage = (it & 1) * GE::STAGE;
-    const uint32_t st = ring + stage;
-    cp_async_wait<1>();
-    __syncwarp();
-    // ---- S^T
-    float sc[MT][NR][4];
+  // the lane's reads of a stage: the swizzles make them constants apart but
+  // for one bit (rows kap + 2 e of K, rows 4 c4 + e of V)
+  const uint32_t k_rd = ring + GE::k_off(kap, D == 64 ? c4 >> 1 : c4) +
+                        (D == 64 ? 8 * (c4 & 1) : 0);
+  const uint32_t k_rd1 =
+      ring + (D == 64    ? GE::k_off(kap + 2, c4 >> 1) + 8 * (c4 & 1)
+              : D == 128 ? GE::k_off(kap + 2, c4)
+                         : GE::k_off(kap, 4 + c4));
+  const uint32_t v_rd =
+      ring + GE::OFF_V +
+      (D == 64 ? GE::v_off(4 * c4, g8 >> 2) + 4 * (g8 & 3)
+               : GE::v_off(4 * c4, g8 >> 1) + 8 * (g8 & 1));
+  const uint32_t v_rd1 =
+      ring + GE::OFF_V +
+      (D == 64    ? GE::v_off(4 * c4 + 1, g8 >> 2) + 4 * (g8 & 3)
+       : D == 128 ? GE::v_off(4 * c4 + 1, g8 >> 1) + 8 * (g8 & 1)
+                  : GE::v_off(4 * c4, 4 + (g8 >> 1)) + 8 * (g8 & 1));
+  const uint32_t f_rd = ring + GE::OFF_KF + kap * 16 +
+                        (D == 64 ? c4 : 2 * c4);
+  const uint32_t vf_rd = ring + GE::OFF_VF +
+                         (D == 64 ? 64 * c4 + (g8 >> 1) : (lane & 15) * 16);
+  auto k_at = [&](uint32_t stage, int e, int q) -> uint32_t {
+    if (D == 256) return (q ? k_rd1 : k_rd) + stage + e * (2 * GE::RB);
+    return (e ? k_rd1 : k_rd) + stage;
+  };
+  auto v_at = [&](uint32_t stage, int e, int v) -> uint32_t {
+    if (D == 256) return (v ? v_rd1 : v_rd) + stage + e * GE::RB;
+    if (D == 128)
+      return ((e & 1) ? v_rd1 : v_rd) + stage + (e >> 1) * (2 * GE::RB);
+    // (rows e ^ c4 of the four)
+    return v_rd + stage + (static_cast<int>((e ^ c4) - c4) * GE::RB);
+  };
+
+  if (threadIdx.x < 16) row_tok[threadIdx.x] = threadIdx.x / G;
+  const bool plain = p.softcap <= 0.f && p.alibi == nullptr;
+  const float cap_t = p.softcap * kLog2e;
+  const float cap_u = p.softcap > 0.f ? 2.f / p.softcap : 0.f;
+
+  // ---- queries: lane (g8, c4) takes row g8 (and g8 + 8), the dimensions of
+  // its K run.  A bf16 row is scaled by the power of two that puts its
+  // largest magnitude in [2^14, 2^15): exact in f16; the factor joins the
+  // row's logit scale.
+  uint4 raw[NR][KW];
+  auto load_queries = [&](const Piece& x, int rows) {
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
+    for (int n = 0; n < NR; ++n) {
+      const int r = g8 + 8 * n;
 #pragma unroll
-      for (int n = 0; n < NR; ++n)
-        sc[i][n][0] = sc[i][n][1] = sc[i][n][2] = sc[i][n][3] = 0.f;
-    uint32_t kw[MT][2][KW], kf[MT][2];
+      for (int i = 0; i < KW; ++i) raw[n][i] = make_uint4(0, 0, 0, 0);
+      if (r < rows) {
+        const int t = r / G;
+        const T* src = static_cast<const T*>(p.q) +
+                       static_cast<int64_t>(x.r.q0 + t) * p.q_st +
+                       static_cast<int64_t>(x.h * G + r - t * G) * p.q_sh;
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int r = kap + 2 * e;
-        const uint32_t src = st + i * GE::SUB;
-        const uint32_t fs = st + GE::OFF_KF + r * 16 + i * (D / 16);
-        if constexpr (D == 64) {
-          const uint2 v = lds64(src + GE::k_off(r, c4 >> 1) + 8 * (c4 & 1));
-          kw[i][e][0] = v.x;
-          kw[i][e][1] = v.y;
-          kf[i][e] = lds8(fs + c4);
-        } else {
-          kf[i][e] = 0;
-#pragma unroll
-          for (int q = 0; q < D / 128; ++q) {
-            const uint4 v = lds128(src + GE::k_off(r, 4 * q + c4));
-            kw[i][e][4 * q] = v.x;
-            kw[i][e][4 * q + 1] = v.y;
-            kw[i][e][4 * q + 2] = v.z;
-            kw[i][e][4 * q + 3] = v.w;
-            kf[i][e] |= lds16(fs + 8 * q + 2 * c4) << (16 * q);
-          }
+        for (int i = 0; i < KW; ++i) {
+          // word i of the run: 8 dimensions (D = 256: two runs of 4 words)
+          const int d = D == 256 ? 128 * (i >> 2) + 32 * c4 + 8 * (i & 3)
+                                 : 8 * KW * c4 + 8 * i;
+          raw[n][i] = *reinterpret_cast<const uint4*>(src + d);
         }
       }
-    // block scales of the lane's keys, two groups (D = 64: two keys) a word
-    constexpr int FW = D == 256 ? 2 : 1;
-    uint32_t fk[MT][2][FW];
+    }
+  };
+
+  begin_pages(pc);
+  load_queries(pc, pc.r.rows);
+  begin_copies();
+  for (;;) {
+    if (threadIdx.x == 0) cur = pc;
+    if (p.alibi && threadIdx.x < 16)
+      row_slope[threadIdx.x] =
+          threadIdx.x < pc.r.rows
+              ? p.alibi[pc.h * G + threadIdx.x % G] * kLog2e
+              : 0.f;
+    uint64_t row_scale[NR];   // logit scales (base 2), rows 2 c4, 2 c4 + 1
 #pragma unroll
-    for (int i = 0; i < MT; ++i) {
-      if constexpr (D == 64) {
-        fk[i][0][0] = e4m3x2_to_f16(__byte_perm(kf[i][0], kf[i][1], 0x40));
-        fk[i][1][0] = 0;
-      } else {
+    for (int n = 0; n < NR; ++n) {
+      float qmul = 1.f, back = 1.f;
+      if constexpr (!std::is_same<T, __half>::value) {
+        float mx = 0.f;
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
+        for (int i = 0; i < KW; ++i) {
+          float x[8];
+          widen8<T>(raw[n][i], x);
 #pragma unroll
-          for (int q = 0; q < FW; ++q)
-            fk[i][e][q] = e4m3x2_to_f16(kf[i][e] >> (16 * q));
+          for (int e = 0; e < 8; ++e) mx = fmaxf(mx, fabsf(x[e]));
+        }
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        int shift = 0;
+        if (mx > 0.f) {
+          shift = static_cast<int>((__float_as_uint(mx) >> 23) & 0xff) - 141;
+          shift = max(-100, min(113, shift));
+        }
+        qmul = __uint_as_float(static_cast<uint32_t>(127 - shift) << 23);
+        back = __uint_as_float(static_cast<uint32_t>(127 + shift) << 23);
+      }
+      row_scale[n] =
+          pair(__shfl_sync(0xffffffffu, back, 8 * c4) * base_scale,
+               __shfl_sync(0xffffffffu, back, 8 * c4 + 4) * base_scale);
+#pragma unroll
+      for (int i = 0; i < KW; ++i) {
+        const uint32_t w[4] = {raw[n][i].x, raw[n][i].y, raw[n][i].z,
+                               raw[n][i].w};
+        uint32_t f[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          f[e] = std::is_same<T, __half>::value
+                     ? w[e]
+                     : pack2<__half>(elem_f32<T>(w[e], 0) * qmul,
+                                     elem_f32<T>(w[e], 1) * qmul);
+        // 8 dimensions: the B operands of k steps 2 i and 2 i + 1
+        if (KW < kWarps || (i & (kWarps - 1)) == warp)
+          reinterpret_cast<uint4*>(smem)[(i * NR + n) * 32 + lane] =
+              make_uint4(f[0], f[1], f[2], f[3]);
       }
     }
+    __syncthreads();
+
+    // my tiles i0 <= it < i1 are seen whole by every row
+    int i0, i1;
+    {
+      int full_lo = pc.r.lo, full_hi = pc.r.hi;
+      const int p_lo = pc.r.L - pc.r.q_len, p_hi = pc.r.L - 1;
+      if (p.wl >= 0) full_lo = max(full_lo, p_hi - p.wl);
+      if (p.causal) full_hi = min(full_hi, p_lo + 1);
+      if (p.wr >= 0) full_hi = min(full_hi, p_lo + p.wr + 1);
+      constexpr int STEP = kWarps * KT;
+      i0 = max(0, (full_lo - key0 + STEP - 1) / STEP);
+      i1 = full_hi - key0 >= KT ? (full_hi - key0 - KT) / STEP + 1 : 0;
+    }
+    const volatile Piece* cold = &cur;
+
+    float o[KS][NR][4];
 #pragma unroll
-    for (int w = 0; w < KW; ++w) {
-      uint4 qb[NR];
+    for (int i = 0; i < KS; ++i)
 #pragma unroll
       for (int n = 0; n < NR; ++n)
-        qb[n] = reinterpret_cast<const uint4*>(smem)[(w * NR + n) * 32 + lane];
+        o[i][n][0] = o[i][n][1] = o[i][n][2] = o[i][n][3] = 0.f;
+    float m[NR][2];
+    uint64_t l[NR];
+#pragma unroll
+    for (int n = 0; n < NR; ++n) {
+      m[n][0] = m[n][1] = -INFINITY;
+      l[n] = pair(0.f, 0.f);
+    }
+
+    for (int it = 0; it < mine; ++it) {
+      const uint32_t stage = (it & 1) * GE::STAGE;
+      cp_async_wait<1>();
+      __syncwarp();
+      // ---- S^T
+      float sc[MT][NR][4];
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int n = 0; n < NR; ++n)
+          sc[i][n][0] = sc[i][n][1] = sc[i][n][2] = sc[i][n][3] = 0.f;
+      uint32_t kw[MT][2][KW], kf[MT][2];
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const uint32_t fs = f_rd + stage + e * 32 + i * (D / 16);
+          if constexpr (D == 64) {
+            const uint2 v = lds64(k_at(stage, e, 0) + i * GE::SUB);
+            kw[i][e][0] = v.x;
+            kw[i][e][1] = v.y;
+            kf[i][e] = lds8(fs);
+          } else {
+            kf[i][e] = 0;
+#pragma unroll
+            for (int q = 0; q < D / 128; ++q) {
+              const uint4 v = lds128(k_at(stage, e, q) + i * GE::SUB);
+              kw[i][e][4 * q] = v.x;
+              kw[i][e][4 * q + 1] = v.y;
+              kw[i][e][4 * q + 2] = v.z;
+              kw[i][e][4 * q + 3] = v.w;
+              kf[i][e] |= lds16(fs + 8 * q) << (16 * q);
+            }
+          }
+        }
+      // block scales of the lane's keys, two groups (D = 64: two keys) a word
+      constexpr int FW = D == 256 ? 2 : 1;
+      uint32_t fk[MT][2][FW];
 #pragma unroll
       for (int i = 0; i < MT; ++i) {
-        uint32_t a[4], c[4];
-        e2m1x8_to_f16(kw[i][0][w], a[0], a[1], a[2], a[3]);
-        e2m1x8_to_f16(kw[i][1][w], c[0], c[1], c[2], c[3]);
-        uint32_t fa, fc;
         if constexpr (D == 64) {
-          fa = __byte_perm(fk[i][0][0], 0, 0x1010);
-          fc = __byte_perm(fk[i][0][0], 0, 0x3232);
+          fk[i][0][0] = e4m3x2_to_f16(__byte_perm(kf[i][0], kf[i][1], 0x40));
+          fk[i][1][0] = 0;
         } else {
-          const uint32_t sel = (w & 2) ? 0x3232u : 0x1010u;
-          fa = __byte_perm(fk[i][0][w >> 2], 0, sel);
-          fc = __byte_perm(fk[i][1][w >> 2], 0, sel);
-        }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          a[e] = hmul2_u32(a[e], fa);
-          c[e] = hmul2_u32(c[e], fc);
-        }
+          for (int e = 0; e < 2; ++e)
 #pragma unroll
-        for (int n = 0; n < NR; ++n) {
-          mma(sc[i][n], a[0], c[0], a[1], c[1], qb[n].x, qb[n].y);
-          mma(sc[i][n], a[2], c[2], a[3], c[3], qb[n].z, qb[n].w);
+            for (int q = 0; q < FW; ++q)
+              fk[i][e][q] = e4m3x2_to_f16(kf[i][e] >> (16 * q));
         }
       }
-    }
-    // ---- logits (base 2) and masks
-    const bool interior = kt >= full_lo && kt + KT <= full_hi;
-    float mx[NR][2];
 #pragma unroll
-    for (int n = 0; n < NR; ++n) mx[n][0] = mx[n][1] = -INFINITY;
-    if (plain && interior) {
+      for (int w = 0; w < KW; ++w) {
+        uint4 qb[NR];
+#pragma unroll
+        for (int n = 0; n < NR; ++n)
+          qb[n] = reinterpret_cast<const uint4*>(smem)[(w * NR + n) * 32 + lane];
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+          uint32_t a[4], c[4];
+          e2m1x8_to_f16(kw[i][0][w], a[0], a[1], a[2], a[3]);
+          e2m1x8_to_f16(kw[i][1][w], c[0], c[1], c[2], c[3]);
+          uint32_t fa, fc;
+          if constexpr (D == 64) {
+            fa = __byte_perm(fk[i][0][0], 0, 0x1010);
+            fc = __byte_perm(fk[i][0][0], 0, 0x3232);
+          } else {
+            const uint32_t sel = (w & 2) ? 0x3232u : 0x1010u;
+            fa = __byte_perm(fk[i][0][w >> 2], 0, sel);
+            fc = __byte_perm(fk[i][1][w >> 2], 0, sel);
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            a[e] = hmul2_u32(a[e], fa);
+            c[e] = hmul2_u32(c[e], fc);
+          }
+#pragma unroll
+          for (int n = 0; n < NR; ++n) {
+            mma(sc[i][n], a[0], c[0], a[1], c[1], qb[n].x, qb[n].y);
+            mma(sc[i][n], a[2], c[2], a[3], c[3], qb[n].z, qb[n].w);
+          }
+        }
+      }
+      // ---- logits (base 2) and masks
+      const bool interior = it >= i0 && it < i1;
+      float mx[NR][2];
+      // (the products are rounded here, once: a fused multiply-add with the
+      // maximum would differ from it by half an ulp of the logit, which may
+      // be far above 1)
 #pragma unroll
       for (int n = 0; n < NR; ++n)
 #pragma unroll
-        for (int i = 0; i < MT; ++i)
+        for (int i = 0; i < MT; ++i) {
+          float* x = sc[i][n];
+          unpair(mul2(pair(x[0], x[1]), row_scale[n]), x[0], x[1]);
+          unpair(mul2(pair(x[2], x[3]), row_scale[n]), x[2], x[3]);
+        }
+      if (!plain) {
+        if (p.softcap > 0.f) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            // (the product is rounded once, here: a fused multiply-add with
-            // the maximum would differ from it by half an ulp of the logit,
-            // which may be far above 1)
-            sc[i][n][e] *= row_scale[n][e & 1];
-            mx[n][e & 1] = fmaxf(mx[n][e & 1], sc[i][n][e]);
-          }
-    } else {
+          for (int n = 0; n < NR; ++n)
 #pragma unroll
-      for (int n = 0; n < NR; ++n) {
+            for (int i = 0; i < MT; ++i)
 #pragma unroll
-        for (int i = 0; i < MT; ++i)
+              for (int e = 0; e < 4; ++e)
+                sc[i][n][e] = soft_cap(sc[i][n][e], cap_t, cap_u);
+        }
+        if (p.alibi) {
+          const int at0 = cold->r.L - cold->r.q_len -
+                          (key0 + it * (kWarps * KT) + kap);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float x = sc[i][n][e] * row_scale[n][e & 1];   // (base 2)
-            if (p.softcap > 0.f) x = soft_cap(x, cap_t, cap_u);
-            const int key = kt + 16 * i + kap + (e & 2);
-            const int at = pos[n][e & 1];
-            if (p.alibi)
-              x -= slope[n][e & 1] * fabsf(static_cast<float>(at - key));
-            if (!interior) {
-              bool ok = live[n][e & 1] && key >= lo && key < hi;
-              if (p.causal) ok = ok && key <= at;
-              if (p.wl >= 0) ok = ok && key >= at - p.wl;
-              if (p.wr >= 0) ok = ok && key <= at + p.wr;
-              x = ok ? x : -INFINITY;
+          for (int n = 0; n < NR; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int r = 8 * n + 2 * c4 + e;
+              const float sl = row_slope[r];
+              const int at = at0 + row_tok[r];
+#pragma unroll
+              for (int i = 0; i < MT; ++i) {
+                sc[i][n][e] -= sl * fabsf(static_cast<float>(at - 16 * i));
+                sc[i][n][e + 2] -=
+                    sl * fabsf(static_cast<float>(at - 16 * i - 2));
+              }
             }
-            sc[i][n][e] = x;
-            mx[n][e & 1] = fmaxf(mx[n][e & 1], x);
+        }
+      }
+      if (!interior) {
+        const int k0 = key0 + it * (kWarps * KT) + kap;
+        const int ctx = cold->r.L - cold->r.q_len;
+        const int rows = cold->r.rows;
+#pragma unroll
+        for (int n = 0; n < NR; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            // keys [from, to) that this row sees
+            const int r = 8 * n + 2 * c4 + e;
+            const int at = ctx + row_tok[r];
+            int from = cold->r.lo, to = cold->r.hi;
+            if (p.causal) to = min(to, at + 1);
+            if (p.wr >= 0) to = min(to, at + p.wr + 1);
+            if (p.wl >= 0) from = max(from, at - p.wl);
+            if (r >= rows) to = from;
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+              for (int f = 0; f < 4; f += 2) {
+                const int key = k0 + 16 * i + f;
+                if (key < from || key >= to) sc[i][n][e + f] = -INFINITY;
+              }
           }
       }
-    }
-    bool raise = false;
-#pragma unroll
-    for (int n = 0; n < NR; ++n)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) raise = raise || mx[n][e] > m[n][e] + kRaise;
-    if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
       for (int n = 0; n < NR; ++n)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float t = mx[n][e];
-          t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 4));
-          t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
-          t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16));
-          t = fmaxf(t, m[n][e]);
-          const float al = t == m[n][e] ? 1.f : ex2(m[n][e] - t);
-          m[n][e] = t;
-          l[n][e] *= al;
+          mx[n][e] = fmaxf(sc[0][n][e], sc[0][n][e + 2]);
 #pragma unroll
-          for (int i = 0; i < KS; ++i) {
-            o[i][n][e] *= al;
-            o[i][n][e + 2] *= al;
+          for (int i = 1; i < MT; ++i)
+            mx[n][e] = fmaxf(mx[n][e], fmaxf(sc[i][n][e], sc[i][n][e + 2]));
+        }
+      bool raise = false;
+#pragma unroll
+      for (int n = 0; n < NR; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) raise = raise || mx[n][e] > m[n][e] + kRaise;
+      if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+        for (int n = 0; n < NR; ++n) {
+          float al[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float t = mx[n][e];
+            t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 4));
+            t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
+            t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16));
+            t = fmaxf(t, m[n][e]);
+            al[e] = t == m[n][e] ? 1.f : ex2(m[n][e] - t);
+            m[n][e] = t;
+#pragma unroll
+            for (int i = 0; i < KS; ++i) {
+              o[i][n][e] *= al[e];
+              o[i][n][e + 2] *= al[e];
+            }
           }
+          l[n] = mul2(l[n], pair(al[0], al[1]));
         }
-    }
-    // P and its sums, and P^T as the B operand of each subtile
-    uint32_t pb[MT][NR][2];
-#pragma unroll
-    for (int n = 0; n < NR; ++n) {
-      const float base0 = m[n][0] == -INFINITY ? 0.f : m[n][0];
-      const float base1 = m[n][1] == -INFINITY ? 0.f : m[n][1];
-#pragma unroll
-      for (int i = 0; i < MT; ++i) {
-        float* x = sc[i][n];
-        x[0] = ex2(x[0] - base0);
-        x[1] = ex2(x[1] - base1);
-        x[2] = ex2(x[2] - base0);
-        x[3] = ex2(x[3] - base1);
-        l[n][0] += x[0] + x[2];
-        l[n][1] += x[1] + x[3];
-        // P rounds to f16 (half a step of 2^-11 relative) for the MMA; the
-        // sums keep the float32 values
-        pb[i][n][0] = movmatrix(pack2<__half>(x[0], x[1]));
-        pb[i][n][1] = movmatrix(pack2<__half>(x[2], x[3]));
       }
-    }
-    // ---- O^T += V^T P^T
-    constexpr int VG = D == 256 ? 2 : 1;     // block scales of a lane
-    // scales of the lane's four keys, a byte each, per subtile and group
-    uint32_t vf[MT][VG];
-    if constexpr (D == 64) {
+      // P and its sums, and P^T as the B operand of each subtile
+      uint32_t pb[MT][NR][2];
 #pragma unroll
-      for (int i = 0; i < MT; ++i) {
-        uint32_t f[4];
+      for (int n = 0; n < NR; ++n) {
+        const uint64_t base = pair(m[n][0] == -INFINITY ? 0.f : -m[n][0],
+                                   m[n][1] == -INFINITY ? 0.f : -m[n][1]);
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          f[e] = lds8(st + GE::OFF_VF + (4 * c4 + e) * 16 + i * 4 +
-                      (g8 >> 1));
-        vf[i][0] = __byte_perm(__byte_perm(f[0], f[1], 0x40),
-                               __byte_perm(f[2], f[3], 0x40), 0x5410);
-      }
-    } else {
-      // rows are keys, columns groups (of two subtiles at D = 128)
-      uint32_t d0, d1;
-      ldmatrix_b8_trans(st + GE::OFF_VF + (lane & 15) * 16, d0, d1);
-      vf[0][0] = d0;
-      vf[MT - 1][VG - 1] = d1;
-    }
+        for (int i = 0; i < MT; ++i) {
+          float* x = sc[i][n];
+          unpair(add2(pair(x[0], x[1]), base), x[0], x[1]);
+          unpair(add2(pair(x[2], x[3]), base), x[2], x[3]);
 #pragma unroll
-    for (int i = 0; i < MT; ++i) {
-      if (!interior) {
-        // keys outside [lo, hi): a scale of 0
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int key = kt + 16 * i + 4 * c4 + e;
-          if (key < lo || key >= hi)
-#pragma unroll
-            for (int v = 0; v < VG; ++v) vf[i][v] &= ~(0xffu << (8 * e));
+          for (int e = 0; e < 4; ++e) x[e] = ex2(x[e]);
+          l[n] = add2(l[n], add2(pair(x[0], x[1]), pair(x[2], x[3])));
+          // P rounds to f16 (half a step of 2^-11 relative) for the MMA; the
+          // sums keep the float32 values
+          pb[i][n][0] = movmatrix(pack2<__half>(x[0], x[1]));
+          pb[i][n][1] = movmatrix(pack2<__half>(x[2], x[3]));
         }
-        // NaN scales: set aside, and added to the rows that see the key
-        uint32_t nan_bits[VG];
-        bool any = false;
+      }
+      // ---- O^T += V^T P^T
+      constexpr int VG = D == 256 ? 2 : 1;     // block scales of a lane
+      // scales of the lane's four keys, a byte each, per subtile and group
+      uint32_t vf[MT][VG];
+      if constexpr (D == 64) {
 #pragma unroll
-        for (int v = 0; v < VG; ++v) {
-          nan_bits[v] = 0;
+        for (int i = 0; i < MT; ++i) {
+          uint32_t f[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            if (((vf[i][v] >> (8 * e)) & 0x7fu) == 0x7fu)
-              nan_bits[v] |= 1u << (4 * c4 + e);
-          any = any || nan_bits[v] != 0;
+            f[e] = lds8(vf_rd + stage + e * 16 + i * 4);
+          vf[i][0] = __byte_perm(__byte_perm(f[0], f[1], 0x40),
+                                 __byte_perm(f[2], f[3], 0x40), 0x5410);
         }
-        if (__any_sync(0xffffffffu, any)) {
-#pragma unroll
-          for (int v = 0; v < VG; ++v) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if ((nan_bits[v] >> (4 * c4 + e)) & 1u)
-                vf[i][v] &= ~(0xffu << (8 * e));
-            nan_bits[v] |= __shfl_xor_sync(0xffffffffu, nan_bits[v], 1);
-            nan_bits[v] |= __shfl_xor_sync(0xffffffffu, nan_bits[v], 2);
-#pragma unroll
-            for (int n = 0; n < NR; ++n)
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const int at = pos[n][e];
-                bool hit = false;
-                for (int j = 0; j < 16; ++j) {
-                  const int key = kt + 16 * i + j;
-                  bool ok = (nan_bits[v] >> j) & 1u;
-                  if (p.causal) ok = ok && key <= at;
-                  if (p.wl >= 0) ok = ok && key >= at - p.wl;
-                  if (p.wr >= 0) ok = ok && key <= at + p.wr;
-                  hit = hit || ok;
-                }
-                if (hit) {
-#pragma unroll
-                  for (int w = 0; w < KS / VG; ++w) {
-                    o[v * (KS / VG) + w][n][e] = NAN;
-                    o[v * (KS / VG) + w][n][e + 2] = NAN;
-                  }
-                }
-              }
-          }
-        }
+      } else {
+        // rows are keys, columns groups (of two subtiles at D = 128)
+        uint32_t d0, d1;
+        ldmatrix_b8_trans(vf_rd + stage, d0, d1);
+        vf[0][0] = d0;
+        vf[MT - 1][VG - 1] = d1;
       }
 #pragma unroll
-      for (int v = 0; v < VG; ++v) {
-        const uint32_t s01 = e4m3x2_to_f16(vf[i][v]);
-        const uint32_t s23 = e4m3x2_to_f16(vf[i][v] >> 16);
-        // the lane's run of the four keys' rows: 16 dimensions (D = 64: 8)
-        constexpr int RW = D == 64 ? 1 : 2;
-        uint32_t vw[4][RW];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int r = 4 * c4 + e;
-          const uint32_t src = st + GE::OFF_V + i * GE::SUB;
-          if constexpr (D == 64) {
-            vw[e][0] = lds32(src + GE::v_off(r, g8 >> 2) + 4 * (g8 & 3));
-          } else {
-            const uint2 x = lds64(src + GE::v_off(r, 4 * v + (g8 >> 1)) +
-                                  8 * (g8 & 1));
-            vw[e][0] = x.x;
-            vw[e][1] = x.y;
-          }
-        }
-#pragma unroll
-        for (int w = 0; w < RW; ++w) {
-          const uint32_t w0 = vw[0][w], w1 = vw[1][w];
-          const uint32_t w2 = vw[2][w], w3 = vw[3][w];
-          // bytes (key, next key) of the even and of the odd dimensions
-          const uint32_t e01 = (w0 & 0x0f0f0f0fu) | ((w1 << 4) & 0xf0f0f0f0u);
-          const uint32_t o01 = ((w0 >> 4) & 0x0f0f0f0fu) | (w1 & 0xf0f0f0f0u);
-          const uint32_t e23 = (w2 & 0x0f0f0f0fu) | ((w3 << 4) & 0xf0f0f0f0u);
-          const uint32_t o23 = ((w2 >> 4) & 0x0f0f0f0fu) | (w3 & 0xf0f0f0f0u);
-          uint32_t a0[4], a1[4], a2[4], a3[4];
-          e2m1x8_to_f16(e01, a0[0], a0[1], a0[2], a0[3]);
-          e2m1x8_to_f16(o01, a1[0], a1[1], a1[2], a1[3]);
-          e2m1x8_to_f16(e23, a2[0], a2[1], a2[2], a2[3]);
-          e2m1x8_to_f16(o23, a3[0], a3[1], a3[2], a3[3]);
+      for (int i = 0; i < MT; ++i) {
+        if (!interior) {
+          // keys outside [lo, hi): a scale of 0
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const uint32_t x0 = hmul2_u32(a0[e], s01);
-            const uint32_t x1 = hmul2_u32(a1[e], s01);
-            const uint32_t x2 = hmul2_u32(a2[e], s23);
-            const uint32_t x3 = hmul2_u32(a3[e], s23);
+            const int key = key0 + it * (kWarps * KT) + 16 * i + 4 * c4 + e;
+            if (key < cold->r.lo || key >= cold->r.hi)
 #pragma unroll
-            for (int n = 0; n < NR; ++n)
-              mma(o[(v * RW + w) * 4 + e][n], x0, x1, x2, x3, pb[i][n][0],
-                  pb[i][n][1]);
+              for (int v = 0; v < VG; ++v) vf[i][v] &= ~(0xffu << (8 * e));
+          }
+          // NaN scales: set aside, and added to the rows that see the key
+          uint32_t nan_bits[VG];
+          bool any = false;
+#pragma unroll
+          for (int v = 0; v < VG; ++v) {
+            nan_bits[v] = 0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (((vf[i][v] >> (8 * e)) & 0x7fu) == 0x7fu)
+                nan_bits[v] |= 1u << (4 * c4 + e);
+            any = any || nan_bits[v] != 0;
+          }
+          if (__any_sync(0xffffffffu, any)) {
+#pragma unroll
+            for (int v = 0; v < VG; ++v) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if ((nan_bits[v] >> (4 * c4 + e)) & 1u)
+                  vf[i][v] &= ~(0xffu << (8 * e));
+              nan_bits[v] |= __shfl_xor_sync(0xffffffffu, nan_bits[v], 1);
+              nan_bits[v] |= __shfl_xor_sync(0xffffffffu, nan_bits[v], 2);
+#pragma unroll
+              for (int n = 0; n < NR; ++n)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  const int at = cold->r.L - cold->r.q_len +
+                                 row_tok[8 * n + 2 * c4 + e];
+                  bool hit = false;
+                  for (int j = 0; j < 16; ++j) {
+                    const int key = key0 + it * (kWarps * KT) + 16 * i + j;
+                    bool ok = (nan_bits[v] >> j) & 1u;
+                    if (p.causal) ok = ok && key <= at;
+                    if (p.wl >= 0) ok = ok && key >= at - p.wl;
+                    if (p.wr >= 0) ok = ok && key <= at + p.wr;
+                    hit = hit || ok;
+                  }
+                  if (hit) {
+#pragma unroll
+                    for (int w = 0; w < KS / VG; ++w) {
+                      o[v * (KS / VG) + w][n][e] = NAN;
+                      o[v * (KS / VG) + w][n][e + 2] = NAN;
+                    }
+                  }
+                }
+            }
+          }
+        }
+#pragma unroll
+        for (int v = 0; v < VG; ++v) {
+          const uint32_t s01 = e4m3x2_to_f16(vf[i][v]);
+          const uint32_t s23 = e4m3x2_to_f16(vf[i][v] >> 16);
+          // the lane's run of the four keys' rows: 16 dimensions (D = 64: 8)
+          constexpr int RW = D == 64 ? 1 : 2;
+          uint32_t vw[4][RW];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            if constexpr (D == 64) {
+              vw[e][0] = lds32(v_at(stage, e, 0) + i * GE::SUB);
+            } else {
+              const uint2 x = lds64(v_at(stage, e, v) + i * GE::SUB);
+              vw[e][0] = x.x;
+              vw[e][1] = x.y;
+            }
+          }
+#pragma unroll
+          for (int w = 0; w < RW; ++w) {
+            const uint32_t w0 = vw[0][w], w1 = vw[1][w];
+            const uint32_t w2 = vw[2][w], w3 = vw[3][w];
+            // bytes (key, next key) of the even and of the odd dimensions
+            const uint32_t e01 = (w0 & 0x0f0f0f0fu) | ((w1 << 4) & 0xf0f0f0f0u);
+            const uint32_t o01 = ((w0 >> 4) & 0x0f0f0f0fu) | (w1 & 0xf0f0f0f0u);
+            const uint32_t e23 = (w2 & 0x0f0f0f0fu) | ((w3 << 4) & 0xf0f0f0f0u);
+            const uint32_t o23 = ((w2 >> 4) & 0x0f0f0f0fu) | (w3 & 0xf0f0f0f0u);
+            uint32_t a0[4], a1[4], a2[4], a3[4];
+            e2m1x8_to_f16(e01, a0[0], a0[1], a0[2], a0[3]);
+            e2m1x8_to_f16(o01, a1[0], a1[1], a1[2], a1[3]);
+            e2m1x8_to_f16(e23, a2[0], a2[1], a2[2], a2[3]);
+            e2m1x8_to_f16(o23, a3[0], a3[1], a3[2], a3[3]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const uint32_t x0 = hmul2_u32(a0[e], s01);
+              const uint32_t x1 = hmul2_u32(a1[e], s01);
+              const uint32_t x2 = hmul2_u32(a2[e], s23);
+              const uint32_t x3 = hmul2_u32(a3[e], s23);
+#pragma unroll
+              for (int n = 0; n < NR; ++n)
+                mma(o[(v * RW + w) * 4 + e][n], x0, x1, x2, x3, pb[i][n][0],
+                    pb[i][n][1]);
+            }
           }
         }
       }
-    }
-    // this stage is read: the tile after the next one into it
-    __syncwarp();
-    const int s_new = (it + 2) * MT;
-    if (it + 2 < mine) {
-      if ((s_new & 31) == 0) {
-        ids = ids_next;
-        rows0 = rows0_next;
-        fetch(s_new + 32, ids_next, rows0_next);
+      // this stage is read: the tile after the next one into it
+      __syncwarp();
+      const int s_new = (it + 2) * MT;
+      if (it + 2 < mine) {
+        if ((s_new & 31) == 0) {
+          ids = ids_next;
+          rows0 = rows0_next;
+          fetch(s_new + 32, cold->b, cold->r.hi, ids_next, rows0_next);
+        }
+        issue(s_new, stage);
       }
-      issue(s_new, stage);
+      cp_async_commit();
     }
-    cp_async_commit();
+
+    // ---- the next piece's first copies, then the end of this one: the
+    // warps' states meet, row r of warp w at r D + 4 (r / 2) floats
+    // (conflict-free float4 stores)
+    const Piece done = cur;
+    const int h = done.h, q0 = done.r.q0, rows = done.r.rows;
+    const bool more_pieces = left > 0;
+    if (more_pieces) {
+      pc = next_piece(done);
+      begin_pages(pc);
+    }
+    float* ow = reinterpret_cast<float*>(smem + SM::OFF_O);
+    float2* ml = reinterpret_cast<float2*>(smem + SM::OFF_ML);
+#pragma unroll
+    for (int n = 0; n < NR; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float t, t1;
+        unpair(l[n], t, t1);
+        if (e) t = t1;
+        t += __shfl_xor_sync(0xffffffffu, t, 4);
+        t += __shfl_xor_sync(0xffffffffu, t, 8);
+        t += __shfl_xor_sync(0xffffffffu, t, 16);
+        const int r = 8 * n + 2 * c4 + e;
+        if (g8 == 0) ml[warp * SM::ROWS + r] = make_float2(m[n][e], t);
+        if (r >= rows) continue;
+        // o[i]: dimensions 2 (i % 8) and the next one of the lane's run
+        // i / 8 (16 g8 of each 128; D = 64: 8 g8), two m tiles a store
+        float* dst = ow + warp * SM::OSTRIDE + r * D + 4 * (r >> 1) +
+                     (D == 64 ? 8 : 16) * g8;
+#pragma unroll
+        for (int i = 0; i < KS; i += 2)
+          *reinterpret_cast<float4*>(dst + 128 * (i >> 3) + 2 * (i & 7)) =
+              make_float4(o[i][n][e], o[i][n][e + 2], o[i + 1][n][e],
+                          o[i + 1][n][e + 2]);
+      }
+    if (more_pieces) begin_copies();
+    load_queries(pc, more_pieces ? pc.r.rows : 0);
+    __syncthreads();
+    for (int i = threadIdx.x; i < rows * (D / 4); i += NT) {
+      const int r = i / (D / 4), col = (i - r * (D / 4)) * 4;
+      float M = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, ml[w * SM::ROWS + r].x);
+      const float base = M == -INFINITY ? 0.f : M;
+      float sum = 0.f;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float2 s = ml[w * SM::ROWS + r];
+        // a warp that saw nothing but NaN keeps its NaN sum
+        const float f = s.x == -INFINITY ? (s.y == 0.f ? 0.f : 1.f)
+                                         : ex2(s.x - base);
+        if (f == 0.f) continue;
+        const float4 v = *reinterpret_cast<const float4*>(
+            ow + w * SM::OSTRIDE + r * D + 4 * (r >> 1) + col);
+        sum += f * s.y;
+        acc.x += f * v.x;
+        acc.y += f * v.y;
+        acc.z += f * v.z;
+        acc.w += f * v.w;
+      }
+      const int tok = q0 + row_tok[r], hq = h * G + r - row_tok[r] * G;
+      float inv, lse;
+      finish(M, sum, done.slot >= 0 ? nullptr : p.sinks, hq, &inv, &lse);
+      inv *= vscale;
+      if (done.slot >= 0) {
+        // partial rows: [slot][row] of the sequence, or of the split
+        const int64_t row =
+            sequence ? static_cast<int64_t>(done.slot) * p.sk_rows + r
+                     : (static_cast<int64_t>(done.slot) * p.part_rows +
+                        part_row(p.part_tpr, done.b, q0, tok)) *
+                               p.Hq +
+                           hq;
+        *reinterpret_cast<float4*>(p.part_o + row * D + col) =
+            make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+        if (col == 0)
+          p.part_lse[sequence ? row
+                              : (static_cast<int64_t>(done.slot) * p.Hq +
+                                 hq) * p.part_rows +
+                                    part_row(p.part_tpr, done.b, q0, tok)] =
+              lse;
+      } else {
+        T* dst = static_cast<T*>(p.out) + static_cast<int64_t>(tok) * p.o_st +
+                 static_cast<int64_t>(hq) * p.o_sh + col;
+        *reinterpret_cast<uint2*>(dst) =
+            make_uint2(pack2<T>(acc.x * inv, acc.y * inv),
+                       pack2<T>(acc.z * inv, acc.w * inv));
+        if (p.lse && col == 0)
+          p.lse[static_cast<int64_t>(hq) * p.total_q + tok] = lse;
+      }
+    }
+    if (!more_pieces) break;
+    __syncthreads();       // the states and the queries are read
   }
   cp_async_wait<0>();
-  __syncthreads();       // (the states take the rings' place)
-
-  // ---- the warps' states meet: row r of warp w at r D + 4 (r / 2) floats
-  // (conflict-free float4 stores)
-  float* ow = reinterpret_cast<float*>(smem + SM::QBYTES);
-  float2* ml = reinterpret_cast<float2*>(smem + SM::QBYTES + SM::OBYTES);
-  float* mine_o = ow + warp * SM::OSTRIDE;
-#pragma unroll
-  for (int n = 0; n < NR; ++n)
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      float t = l[n][e];
-      t += __shfl_xor_sync(0xffffffffu, t, 4);
-      t += __shfl_xor_sync(0xffffffffu, t, 8);
-      t += __shfl_xor_sync(0xffffffffu, t, 16);
-      const int r = 8 * n + 2 * c4 + e;
-      if (g8 == 0) ml[warp * SM::ROWS + r] = make_float2(m[n][e], t);
-      // o[i]: dimensions 2 (i % 8) and the next one of the lane's run
-      // i / 8 (16 g8 of each 128; D = 64: 8 g8), two m tiles a store
-      float* dst = mine_o + r * D + 4 * (r >> 1) + (D == 64 ? 8 : 16) * g8;
-#pragma unroll
-      for (int i = 0; i < KS; i += 2)
-        *reinterpret_cast<float4*>(dst + 128 * (i >> 3) + 2 * (i & 7)) =
-            make_float4(o[i][n][e], o[i][n][e + 2], o[i + 1][n][e],
-                        o[i + 1][n][e + 2]);
-    }
-  __syncthreads();
-  const float vscale = *p.v_scale;
-  for (int i = threadIdx.x; i < rows * (D / 4); i += kWarps * 32) {
-    const int r = i / (D / 4), col = (i - r * (D / 4)) * 4;
-    float M = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, ml[w * SM::ROWS + r].x);
-    const float base = M == -INFINITY ? 0.f : M;
-    float sum = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const float2 s = ml[w * SM::ROWS + r];
-      // a warp that saw nothing but NaN keeps its NaN sum
-      const float f = s.x == -INFINITY ? (s.y == 0.f ? 0.f : 1.f)
-                                       : ex2(s.x - base);
-      if (f == 0.f) continue;
-      const float4 v = *reinterpret_cast<const float4*>(
-          ow + w * SM::OSTRIDE + r * D + 4 * (r >> 1) + col);
-      sum += f * s.y;
-      acc.x += f * v.x;
-      acc.y += f * v.y;
-      acc.z += f * v.z;
-      acc.w += f * v.w;
-    }
-    const int tok = q0 + r / G, hq = h * G + r % G;
-    float inv, lse;
-    finish(M, sum, p.chunk > 0 ? nullptr : p.sinks, hq, &inv, &lse);
-    inv *= vscale;
-    if (p.chunk > 0) {
-      const int64_t row = part_row(p.part_tpr, b, q0, tok);
-      *reinterpret_cast<float4*>(
-          p.part_o +
-          ((static_cast<int64_t>(sp) * p.part_rows + row) * p.Hq + hq) * D +
-          col) = make_float4(acc.x * inv, acc.y * inv, acc.z * inv,
-                             acc.w * inv);
-      if (col == 0)
-        p.part_lse[(static_cast<int64_t>(sp) * p.Hq + hq) * p.part_rows +
-                   row] = lse;
-    } else {
-      T* dst = static_cast<T*>(p.out) + static_cast<int64_t>(tok) * p.o_st +
-               static_cast<int64_t>(hq) * p.o_sh + col;
-      *reinterpret_cast<uint2*>(dst) =
-          make_uint2(pack2<T>(acc.x * inv, acc.y * inv),
-                     pack2<T>(acc.z * inv, acc.w * inv));
-      if (p.lse && col == 0)
-        p.lse[static_cast<int64_t>(hq) * p.total_q + tok] = lse;
-    }
-  }
 }
 
 // Fold the pieces of each (token, head) by their LSEs: one warp each, lanes
@@ -882,35 +1147,175 @@ __global__ void __launch_bounds__(128) combine_kernel(const CombineParams p) {
   }
 }
 
+// Join the parts of the units that the ends of the CTAs' shares cut.  A unit
+// in np parts has its first in slot 2 (s - 1) + 1 of share s - 1 (where it
+// begins) and the others in slots 2 s, 2 (s + 1), ... of the shares that mark
+// it as begun before.  Block c stands at the start of share c: the np - 1
+// blocks inside a unit divide its (row, 4 columns) items, and where a block
+// has threads over, groups of them take every kg-th part.
+template <typename T, int D>
+__global__ void __launch_bounds__(kFoldThreads)
+fold_kernel(const AttnParams p) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  constexpr int HALF = kFoldThreads / 2;
+  __shared__ int reach[2];
+  __shared__ float row_base[16], row_inv[16], row_lse[16];
+  __shared__ float4 part[kFoldThreads];
+  const int c = blockIdx.x + 1;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int u = p.sk_marks[c].x;
+  if (u < 0) return;
+  // the run of shares around c that mark u: the lower half of the threads
+  // looks back, the upper half on
+  int first = c, last = c;
+  {
+    const int dir = tid < HALF ? -1 : 1, i = tid < HALF ? tid : tid - HALF;
+    bool open[2] = {true, true};
+    for (int step = 1; open[0] || open[1]; step += HALF) {
+      if (tid < 2) reach[tid] = HALF;
+      __syncthreads();
+      const int at = c + dir * (step + i);
+      if (at < 0 || at >= p.sk_chunks || p.sk_marks[at].x != u)
+        atomicMin(&reach[tid < HALF ? 0 : 1], i);
+      __syncthreads();
+      const int back = reach[0], on = reach[1];
+      if (open[0]) first -= back;
+      if (open[1]) last += on;
+      open[0] = open[0] && back == HALF;
+      open[1] = open[1] && on == HALF;
+      __syncthreads();
+    }
+  }
+  const int np = last - first + 2;       // parts, shares first - 1 .. last
+  const int b = u / p.Hkv, h = u - b * p.Hkv;
+  const int q0 = p.cu_q[b];
+  const int q_len = min(p.cu_q[b + 1] - q0, p.total_q - q0);
+  const int rows = min(q_len * p.G, p.sk_rows);
+  auto row_of = [&](int k, int r) {
+    const int slot = k == 0 ? 2 * (first - 1) + 1 : 2 * (first + k - 1);
+    return static_cast<int64_t>(slot) * p.sk_rows + r;
+  };
+  // this block's items
+  const int all = rows * (D / 4);
+  const int per = (all + np - 2) / (np - 1);
+  const int i0 = (c - first) * per, i1 = min(all, i0 + per);
+  if (i0 >= i1) return;
+  const int r0 = i0 / (D / 4), r1 = (i1 - 1) / (D / 4);
+  for (int r = r0 + warp; r <= r1; r += kFoldThreads / 32) {
+    float M = -INFINITY;
+    for (int k = lane; k < np; k += 32) M = fmaxf(M, p.part_lse[row_of(k, r)]);
+#pragma unroll
+    for (int o = 16; o; o >>= 1)
+      M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    const float base = M == -INFINITY ? 0.f : M * kLog2e;
+    float sum = 0.f;
+    for (int k = lane; k < np; k += 32)
+      sum += ex2(p.part_lse[row_of(k, r)] * kLog2e - base);
+#pragma unroll
+    for (int o = 16; o; o >>= 1)
+      sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0) {
+      float inv, lse;
+      finish(M == -INFINITY ? M : base, sum, p.sinks, h * p.G + r % p.G, &inv,
+             &lse);
+      row_base[r] = base;
+      row_inv[r] = inv;
+      row_lse[r] = lse;
+    }
+  }
+  __syncthreads();
+  const int width = min(i1 - i0, kFoldThreads);
+  const int kg = kFoldThreads / width;
+  const int grp = tid / width, in = tid - grp * width;
+  for (int ib = i0; ib < i1; ib += width) {
+    const int i = ib + in;
+    const bool on = i < i1 && grp < kg;
+    const int r = i / (D / 4), col = (i - r * (D / 4)) * 4;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (on) {
+      const float base = row_base[r];
+#pragma unroll 4
+      for (int k = grp; k < np; k += kg) {
+        const int64_t at = row_of(k, r);
+        const float4 v =
+            *reinterpret_cast<const float4*>(p.part_o + at * D + col);
+        const float w = ex2(p.part_lse[at] * kLog2e - base);  // -inf -> 0
+        if (w == 0.f) continue;
+        acc.x += w * v.x;
+        acc.y += w * v.y;
+        acc.z += w * v.z;
+        acc.w += w * v.w;
+      }
+    }
+    if (kg > 1) {
+      __syncthreads();
+      part[tid] = acc;
+      __syncthreads();
+      if (grp == 0)
+        for (int g = 1; g < kg; ++g) {
+          const float4 v = part[g * width + in];
+          acc.x += v.x;
+          acc.y += v.y;
+          acc.z += v.z;
+          acc.w += v.w;
+        }
+    }
+    if (on && grp == 0) {
+      const float inv = row_inv[r];
+      const int t = q0 + r / p.G, hq = h * p.G + r % p.G;
+      T* dst = static_cast<T*>(p.out) + static_cast<int64_t>(t) * p.o_st +
+               static_cast<int64_t>(hq) * p.o_sh + col;
+      *reinterpret_cast<uint2*>(dst) =
+          make_uint2(pack2<T>(acc.x * inv, acc.y * inv),
+                     pack2<T>(acc.z * inv, acc.w * inv));
+      if (p.lse && col == 0)
+        p.lse[static_cast<int64_t>(hq) * p.total_q + t] = row_lse[r];
+    }
+  }
+}
+
 template <typename T, int D, int NR>
-cudaError_t launch(const AttnParams& p, int splits, cudaStream_t stream) {
+cudaError_t launch(const AttnParams& p, int splits, bool pdl,
+                   cudaStream_t stream) {
   using SM = Smem<D, NR>;
   auto kern = decode_fp4_kernel<T, D, NR>;
   cudaError_t e = smem_opt_in(reinterpret_cast<const void*>(kern), SM::BYTES);
   if (e != cudaSuccess) return e;
-  const int64_t ctas = static_cast<int64_t>(p.batch) * splits * p.Hkv;
+  const int64_t ctas =
+      p.sk_chunks > 0 ? p.sk_chunks
+                      : static_cast<int64_t>(p.batch) * splits * p.Hkv;
   if (ctas > 0x7fffffff) return cudaErrorInvalidConfiguration;
   note_launch();
-  kern<<<static_cast<unsigned>(ctas), kWarps * 32, SM::BYTES, stream>>>(
-      p, splits);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+  cfg.blockDim = dim3(kWarps * 32);
+  cfg.dynamicSmemBytes = SM::BYTES;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = pdl ? attr : nullptr;
+  cfg.numAttrs = pdl ? 1 : 0;
+  e = cudaLaunchKernelEx(&cfg, kern, p, splits);
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 template <typename T, int D>
-cudaError_t dispatch_rows(const AttnParams& p, int splits,
+cudaError_t dispatch_rows(const AttnParams& p, int splits, bool pdl,
                           cudaStream_t stream) {
   const bool one = p.sk_rows <= 8;       // packed query rows of a request
-  return one ? launch<T, D, 1>(p, splits, stream)
-             : launch<T, D, 2>(p, splits, stream);
+  return one ? launch<T, D, 1>(p, splits, pdl, stream)
+             : launch<T, D, 2>(p, splits, pdl, stream);
 }
 
 template <typename T>
-cudaError_t dispatch(const AttnParams& p, int D, int splits,
+cudaError_t dispatch(const AttnParams& p, int D, int splits, bool pdl,
                      cudaStream_t stream) {
   switch (D) {
-    case 64: return dispatch_rows<T, 64>(p, splits, stream);
-    case 128: return dispatch_rows<T, 128>(p, splits, stream);
-    case 256: return dispatch_rows<T, 256>(p, splits, stream);
+    case 64: return dispatch_rows<T, 64>(p, splits, pdl, stream);
+    case 128: return dispatch_rows<T, 128>(p, splits, pdl, stream);
+    case 256: return dispatch_rows<T, 256>(p, splits, pdl, stream);
     default: return cudaErrorInvalidValue;
   }
 }
@@ -918,13 +1323,67 @@ cudaError_t dispatch(const AttnParams& p, int D, int splits,
 }  // namespace dfp4
 
 int decode_fp4_ctas_per_sm(int D, int rows) {
-  return rows <= 8 ? (D == 256 ? 3 : 4) : (D == 256 ? 2 : 3);
+  return rows <= 8 ? 3 : (D == 256 ? 2 : 3);
 }
 
 cudaError_t launch_decode_attn_fp4(const AttnParams& p, int D, bool bf16,
-                                   int splits, cudaStream_t stream) {
-  return bf16 ? dfp4::dispatch<__nv_bfloat16>(p, D, splits, stream)
-              : dfp4::dispatch<__half>(p, D, splits, stream);
+                                   int splits, bool pdl,
+                                   cudaStream_t stream) {
+  AttnParams a = p;
+  a.sk_chunks = 0;
+  return bf16 ? dfp4::dispatch<__nv_bfloat16>(a, D, splits, pdl, stream)
+              : dfp4::dispatch<__half>(a, D, splits, pdl, stream);
+}
+
+cudaError_t launch_decode_attn_fp4_shares(const AttnParams& p, int D,
+                                          bool bf16, int ctas, bool pdl,
+                                          void* scratch,
+                                          cudaStream_t stream) {
+  AttnParams a = p;
+  char* ws = static_cast<char*>(scratch);
+  const size_t slots = static_cast<size_t>(2) * ctas;
+  a.chunk = 0;
+  a.sk_chunks = ctas;
+  a.part_o = reinterpret_cast<float*>(ws);
+  ws += dfp4::up256(slots * p.sk_rows * D * 4);
+  a.part_lse = reinterpret_cast<float*>(ws);
+  ws += dfp4::up256(slots * p.sk_rows * 4);
+  a.sk_marks = reinterpret_cast<int2*>(ws);
+  cudaError_t e = bf16 ? dfp4::dispatch<__nv_bfloat16>(a, D, 1, pdl, stream)
+                       : dfp4::dispatch<__half>(a, D, 1, pdl, stream);
+  if (e != cudaSuccess || ctas < 2) return e;
+  note_launch();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas - 1));
+  cfg.blockDim = dim3(dfp4::kFoldThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = pdl ? attr : nullptr;
+  cfg.numAttrs = pdl ? 1 : 0;
+  auto go = [&](auto kern) { return cudaLaunchKernelEx(&cfg, kern, a); };
+  switch (D) {
+    case 64:
+      e = bf16 ? go(dfp4::fold_kernel<__nv_bfloat16, 64>)
+               : go(dfp4::fold_kernel<__half, 64>);
+      break;
+    case 128:
+      e = bf16 ? go(dfp4::fold_kernel<__nv_bfloat16, 128>)
+               : go(dfp4::fold_kernel<__half, 128>);
+      break;
+    default:
+      e = bf16 ? go(dfp4::fold_kernel<__nv_bfloat16, 256>)
+               : go(dfp4::fold_kernel<__half, 256>);
+      break;
+  }
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+size_t decode_fp4_shares_bytes(int D, int ctas, int rows) {
+  const size_t slots = static_cast<size_t>(2) * ctas;
+  return dfp4::up256(slots * rows * D * 4) + dfp4::up256(slots * rows * 4) +
+         dfp4::up256(static_cast<size_t>(ctas) * 8);
 }
 
 cudaError_t launch_fp4_combine(const CombineParams& p, bool bf16, bool pdl,

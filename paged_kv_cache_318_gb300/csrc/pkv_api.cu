@@ -97,6 +97,10 @@ bool stride16(int64_t s, int elem) { return (s * elem) % 16 == 0; }
 // choice.
 constexpr int64_t kLongUnitKeys = 2048;
 
+// Calls whose units span at most this many keys run one CTA per unit on a
+// 4-bit cache.
+constexpr int64_t kFp4UnitKeys = 256;
+
 struct Plan {
   int64_t range = 0;      // widest key range of a decode-class unit
   bool decode = false;    // launch the decode (<= 16 packed rows) kernel
@@ -112,7 +116,9 @@ struct Plan {
 
 size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
-// Pieces of a request's key range for the 4-bit decode kernel.
+// Pieces of a request's key range for the 4-bit decode kernel with one CTA
+// per (request, piece, KV head), which takes the calls that the shares do
+// not (below): about two waves of CTAs, 256 keys each or more.
 int fp4_splits(int batch, int max_q, int G, int Hkv, int D, int64_t range,
                int sms) {
   const int64_t rows = static_cast<int64_t>(max_q) * G;
@@ -121,10 +127,9 @@ int fp4_splits(int batch, int max_q, int G, int Hkv, int D, int64_t range,
       static_cast<int64_t>(sms) *
       decode_fp4_ctas_per_sm(D, rows < kDecodeRows ? static_cast<int>(rows)
                                                    : kDecodeRows);
-  int64_t s = (4 * slots + units - 1) / units;
-  const int64_t most = (range + 255) / 256, least = (range + 2047) / 2048;
+  int64_t s = (2 * slots + units - 1) / units;
+  const int64_t most = (range + 255) / 256;
   if (s > most) s = most;
-  if (s < least) s = least;
   if (s > 512) s = 512;
   return s < 1 ? 1 : static_cast<int>(s);
 }
@@ -269,6 +274,16 @@ size_t sk_scratch_bytes(int D, bool kv8, bool q8, int sms, int rows) {
       decode_sk_ctas(D, false, kv8, q8, sms, &b) != cudaSuccess)
     return 0;
   return decode_sk_workspace_bytes(D, a > b ? a : b, rows);
+}
+
+// The 4-bit decode kernel as equal shares of the call's key tiles: when the
+// split is left to the library and units are long enough to be cut.
+bool fp4_shares(const Plan& pl, int num_splits, int fixed_split) {
+  return pl.decode && num_splits == 0 && fixed_split <= 0 &&
+         pl.range > kFp4UnitKeys;
+}
+int fp4_ctas(int D, int rows, int sms) {
+  return sms * decode_fp4_ctas_per_sm(D, rows);
 }
 
 // Workspace layout: the required part (decode split partials, fp8 page
@@ -602,10 +617,14 @@ size_t workspace_bytes_impl(int batch, int total_q, int max_seqlen_q,
                            num_splits, fixed_split_of(opts)),
       total_q, num_heads, head_size);
   const bool q8 = fp8 && q_fp8_of(opts);
+  const int skr = sk_rows(num_heads / num_kv_heads, max_seqlen_q);
   const size_t skb =
-      !kv4 && sk_candidate(num_splits, fixed_split_of(opts), head_size, fp8)
-          ? sk_scratch_bytes(head_size, fp8, q8, sms,
-                             sk_rows(num_heads / num_kv_heads, max_seqlen_q))
+      kv4 ? fp4_shares(pl, num_splits, fixed_split_of(opts))
+                ? decode_fp4_shares_bytes(head_size,
+                                          fp4_ctas(head_size, skr, sms), skr)
+                : 0
+      : sk_candidate(num_splits, fixed_split_of(opts), head_size, fp8)
+          ? sk_scratch_bytes(head_size, fp8, q8, sms, skr)
           : 0;
   size_t need = pl.workspace;
   if ((fp8 || kv4) && pl.prefill) {
@@ -854,8 +873,11 @@ pkv_status attention_impl(
       (dsel == PKV_DECODE_PERSISTENT ||
        (dsel == PKV_DECODE_AUTO && (kv8 || many_units)));
   const int skr = sk_rows(num_heads / num_kv_heads, max_seqlen_q);
+  const bool shares = kv4 && fp4_shares(pl, num_splits, fixed_split);
   const size_t skb =
-      !kv4 && sk_candidate(num_splits, fixed_split, head_size, kv8)
+      shares ? decode_fp4_shares_bytes(head_size,
+                                       fp4_ctas(head_size, skr, sms), skr)
+      : !kv4 && sk_candidate(num_splits, fixed_split, head_size, kv8)
           ? sk_scratch_bytes(head_size, kv8, q8, sms, skr)
           : 0;
   const Layout lay = make_layout(need, pl.prefill, skb, sb);
@@ -873,6 +895,11 @@ pkv_status attention_impl(
     else
       sk_ctas = 0;
   }
+  void* fp4_scratch =
+      shares && pl.decode && ws_ok &&
+              workspace_bytes >= lay.sk_off + lay.sk_bytes
+          ? static_cast<char*>(workspace) + lay.sk_off
+          : nullptr;
   int* sched = nullptr;
   int pre_splits = 1;
   float* pre_o = nullptr;
@@ -1028,7 +1055,11 @@ pkv_status attention_impl(
     const bool persistent = sk_scratch != nullptr;
     if (kv4) {
       d.sk_rows = skr;
-      e = launch_decode_attn_fp4(d, head_size, bf16, pl.splits, s);
+      e = fp4_scratch ? launch_decode_attn_fp4_shares(
+                            d, head_size, bf16, fp4_ctas(head_size, skr, sms),
+                            pdl_ok, fp4_scratch, s)
+                      : launch_decode_attn_fp4(d, head_size, bf16, pl.splits,
+                                               pdl_ok, s);
     } else if (persistent) {
       d.chunk = 0;
       e = launch_decode_attn_sk(d, head_size, bf16, sk_ctas, skr, sk_scratch,
@@ -1040,7 +1071,7 @@ pkv_status attention_impl(
       e = launch_decode_attn(d, head_size, bf16, pl.splits, 1, s);
     }
     if (e != cudaSuccess) return cuda_fail(e, "decode attention launch");
-    if (pl.chunk > 0 && !persistent) {
+    if (pl.chunk > 0 && !persistent && !fp4_scratch) {
       CombineParams c{};
       c.part_o = d.part_o;
       c.part_lse = d.part_lse;

@@ -384,13 +384,23 @@ cudaError_t launch_fp4_dequant_blocks(const void* codes, const int64_t* cs,
                                       int64_t n, int64_t num_blocks, int Hkv,
                                       int D, int BS, void* out, bool bf16,
                                       unsigned* err, cudaStream_t stream);
-// Decode attention over a 4-bit cache (decode_fp4.cu): grid of (request,
-// split, KV head), `splits` pieces of p.chunk keys (0 = one piece, written
-// straight to the output); then the fold of the pieces.
+// Decode attention over a 4-bit cache (decode_fp4.cu); p.sk_rows: the most
+// packed query rows of a request.  One CTA per (request, split, KV head):
+// `splits` pieces of p.chunk keys (0 = one piece, written straight to the
+// output), which launch_fp4_combine folds; or `ctas` equal shares of the key
+// tiles, with decode_fp4_shares_bytes of scratch (256-byte aligned) for the
+// units that their ends cut.
+// pdl: the kernel (which waits at its start for the one queued before it) is
+// launched as that one's programmatic dependent, and the fold as its own.
 cudaError_t launch_decode_attn_fp4(const AttnParams& p, int D, bool bf16,
-                                   int splits, cudaStream_t stream);
+                                   int splits, bool pdl,
+                                   cudaStream_t stream);
 cudaError_t launch_fp4_combine(const CombineParams& p, bool bf16, bool pdl,
                                cudaStream_t stream);
+cudaError_t launch_decode_attn_fp4_shares(const AttnParams& p, int D,
+                                          bool bf16, int ctas, bool pdl,
+                                          void* scratch, cudaStream_t stream);
+size_t decode_fp4_shares_bytes(int D, int ctas, int rows);
 // Resident CTAs of that kernel per SM for `rows` packed query rows.
 int decode_fp4_ctas_per_sm(int D, int rows);
 
