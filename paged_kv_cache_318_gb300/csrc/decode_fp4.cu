@@ -133,6 +133,13 @@ __device__ __forceinline__ void cp_async_n(uint32_t dst, const void* src,
                  "l"(src), "r"(src_bytes), "n"(N));
 }
 
+// One half of an f16x2 in both.
+__device__ __forceinline__ uint32_t spread(uint32_t v, int high) {
+  const __half2 x = *reinterpret_cast<const __half2*>(&v);
+  const __half2 r = high ? __high2half2(x) : __low2half2(x);
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
 // Two float32 values as one operand of the packed instructions.
 __device__ __forceinline__ uint64_t pair(float a, float b) {
   uint64_t r;
@@ -153,7 +160,16 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return r;
 }
 
-// D(16 x 8) += A(16 x 16) B(16 x 8), f16 in, fp32 accumulate.
+// D(16 x 8) = A(16 x 16) B(16 x 8), f16 in, fp32 accumulate; mma: D += ...
+__device__ __forceinline__ void mma_first(float* d, uint32_t a0, uint32_t a1,
+                                          uint32_t a2, uint32_t a3,
+                                          uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+      "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};\n"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
 __device__ __forceinline__ void mma(float* d, uint32_t a0, uint32_t a1,
                                     uint32_t a2, uint32_t a3, uint32_t b0,
                                     uint32_t b1) {
@@ -189,20 +205,20 @@ __device__ __forceinline__ float soft_cap(float x, float t, float u) {
 template <int D, int NR>
 struct Smem {
   // query fragments (one 16-byte load serves two k steps of every subtile),
-  // the warps' rings, and their states at the end of a unit
-  static constexpr int ROWS = 8 * NR;
+  // the warps' rings, and two warps' states (as their lanes hold them) at
+  // the end of a unit
   static constexpr int QBYTES = (D / 32) * NR * 32 * 16;
-  static constexpr int OSTRIDE = ROWS * D + 4 * (ROWS / 2);   // floats a warp
+  static constexpr int SREGS = D / 16 * NR * 4;              // O of a lane
+  static constexpr int SBYTES = 32 * (SREGS + 4 * NR) * 4;
   static constexpr int OFF_RING = QBYTES;
-  static constexpr int OFF_O =
+  static constexpr int OFF_S =
       OFF_RING + kWarps * Geo<D>::STAGES * Geo<D>::STAGE;
-  static constexpr int OFF_ML = OFF_O + kWarps * OSTRIDE * 4;
-  static constexpr int BYTES = OFF_ML + kWarps * ROWS * 8;
+  static constexpr int BYTES = OFF_S + kWarps / 2 * SBYTES;
 };
 
 template <int D, int NR>
 constexpr int min_ctas() {
-  return NR == 1 ? 3 : (D == 256 ? 2 : 3);
+  return NR == 1 ? (D == 256 ? 3 : 4) : (D == 256 ? 2 : 3);
 }
 
 // What a request's rows see of its keys.
@@ -642,11 +658,6 @@ decode_fp4_kernel(const AttnParams p, int splits) {
       __syncwarp();
       // ---- S^T
       float sc[MT][NR][4];
-#pragma unroll
-      for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int n = 0; n < NR; ++n)
-          sc[i][n][0] = sc[i][n][1] = sc[i][n][2] = sc[i][n][3] = 0.f;
       uint32_t kw[MT][2][KW], kf[MT][2];
 #pragma unroll
       for (int i = 0; i < MT; ++i)
@@ -700,12 +711,11 @@ decode_fp4_kernel(const AttnParams p, int splits) {
           e2m1x8_to_f16(kw[i][1][w], c[0], c[1], c[2], c[3]);
           uint32_t fa, fc;
           if constexpr (D == 64) {
-            fa = __byte_perm(fk[i][0][0], 0, 0x1010);
-            fc = __byte_perm(fk[i][0][0], 0, 0x3232);
+            fa = spread(fk[i][0][0], 0);
+            fc = spread(fk[i][0][0], 1);
           } else {
-            const uint32_t sel = (w & 2) ? 0x3232u : 0x1010u;
-            fa = __byte_perm(fk[i][0][w >> 2], 0, sel);
-            fc = __byte_perm(fk[i][1][w >> 2], 0, sel);
+            fa = spread(fk[i][0][w >> 2], w & 2);
+            fc = spread(fk[i][1][w >> 2], w & 2);
           }
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
@@ -714,7 +724,10 @@ decode_fp4_kernel(const AttnParams p, int splits) {
           }
 #pragma unroll
           for (int n = 0; n < NR; ++n) {
-            mma(sc[i][n], a[0], c[0], a[1], c[1], qb[n].x, qb[n].y);
+            if (w == 0)
+              mma_first(sc[i][n], a[0], c[0], a[1], c[1], qb[n].x, qb[n].y);
+            else
+              mma(sc[i][n], a[0], c[0], a[1], c[1], qb[n].x, qb[n].y);
             mma(sc[i][n], a[2], c[2], a[3], c[3], qb[n].z, qb[n].w);
           }
         }
@@ -864,9 +877,9 @@ decode_fp4_kernel(const AttnParams p, int splits) {
         vf[0][0] = d0;
         vf[MT - 1][VG - 1] = d1;
       }
+      if (!interior) {
 #pragma unroll
-      for (int i = 0; i < MT; ++i) {
-        if (!interior) {
+        for (int i = 0; i < MT; ++i) {
           // keys outside [lo, hi): a scale of 0
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
@@ -922,6 +935,9 @@ decode_fp4_kernel(const AttnParams p, int splits) {
             }
           }
         }
+      }
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
 #pragma unroll
         for (int v = 0; v < VG; ++v) {
           const uint32_t s01 = e4m3x2_to_f16(vf[i][v]);
@@ -981,99 +997,131 @@ decode_fp4_kernel(const AttnParams p, int splits) {
       cp_async_commit();
     }
 
-    // ---- the next piece's first copies, then the end of this one: the
-    // warps' states meet, row r of warp w at r D + 4 (r / 2) floats
-    // (conflict-free float4 stores)
+    // ---- the next piece's pages and copies begin before the end of this one
     const Piece done = cur;
-    const int h = done.h, q0 = done.r.q0, rows = done.r.rows;
     const bool more_pieces = left > 0;
     if (more_pieces) {
       pc = next_piece(done);
       begin_pages(pc);
     }
-    float* ow = reinterpret_cast<float*>(smem + SM::OFF_O);
-    float2* ml = reinterpret_cast<float2*>(smem + SM::OFF_ML);
+    float sum[NR][2];                    // of the whole rows
 #pragma unroll
-    for (int n = 0; n < NR; ++n)
+    for (int n = 0; n < NR; ++n) {
+      unpair(l[n], sum[n][0], sum[n][1]);
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        float t, t1;
-        unpair(l[n], t, t1);
-        if (e) t = t1;
+        float t = sum[n][e];
         t += __shfl_xor_sync(0xffffffffu, t, 4);
         t += __shfl_xor_sync(0xffffffffu, t, 8);
         t += __shfl_xor_sync(0xffffffffu, t, 16);
-        const int r = 8 * n + 2 * c4 + e;
-        if (g8 == 0) ml[warp * SM::ROWS + r] = make_float2(m[n][e], t);
-        if (r >= rows) continue;
-        // o[i]: dimensions 2 (i % 8) and the next one of the lane's run
-        // i / 8 (16 g8 of each 128; D = 64: 8 g8), two m tiles a store
-        float* dst = ow + warp * SM::OSTRIDE + r * D + 4 * (r >> 1) +
-                     (D == 64 ? 8 : 16) * g8;
-#pragma unroll
-        for (int i = 0; i < KS; i += 2)
-          *reinterpret_cast<float4*>(dst + 128 * (i >> 3) + 2 * (i & 7)) =
-              make_float4(o[i][n][e], o[i][n][e + 2], o[i + 1][n][e],
-                          o[i + 1][n][e + 2]);
-      }
-    if (more_pieces) begin_copies();
-    load_queries(pc, more_pieces ? pc.r.rows : 0);
-    __syncthreads();
-    for (int i = threadIdx.x; i < rows * (D / 4); i += NT) {
-      const int r = i / (D / 4), col = (i - r * (D / 4)) * 4;
-      float M = -INFINITY;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, ml[w * SM::ROWS + r].x);
-      const float base = M == -INFINITY ? 0.f : M;
-      float sum = 0.f;
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float2 s = ml[w * SM::ROWS + r];
-        // a warp that saw nothing but NaN keeps its NaN sum
-        const float f = s.x == -INFINITY ? (s.y == 0.f ? 0.f : 1.f)
-                                         : ex2(s.x - base);
-        if (f == 0.f) continue;
-        const float4 v = *reinterpret_cast<const float4*>(
-            ow + w * SM::OSTRIDE + r * D + 4 * (r >> 1) + col);
-        sum += f * s.y;
-        acc.x += f * v.x;
-        acc.y += f * v.y;
-        acc.z += f * v.z;
-        acc.w += f * v.w;
-      }
-      const int tok = q0 + row_tok[r], hq = h * G + r - row_tok[r] * G;
-      float inv, lse;
-      finish(M, sum, done.slot >= 0 ? nullptr : p.sinks, hq, &inv, &lse);
-      inv *= vscale;
-      if (done.slot >= 0) {
-        // partial rows: [slot][row] of the sequence, or of the split
-        const int64_t row =
-            sequence ? static_cast<int64_t>(done.slot) * p.sk_rows + r
-                     : (static_cast<int64_t>(done.slot) * p.part_rows +
-                        part_row(p.part_tpr, done.b, q0, tok)) *
-                               p.Hq +
-                           hq;
-        *reinterpret_cast<float4*>(p.part_o + row * D + col) =
-            make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-        if (col == 0)
-          p.part_lse[sequence ? row
-                              : (static_cast<int64_t>(done.slot) * p.Hq +
-                                 hq) * p.part_rows +
-                                    part_row(p.part_tpr, done.b, q0, tok)] =
-              lse;
-      } else {
-        T* dst = static_cast<T*>(p.out) + static_cast<int64_t>(tok) * p.o_st +
-                 static_cast<int64_t>(hq) * p.o_sh + col;
-        *reinterpret_cast<uint2*>(dst) =
-            make_uint2(pack2<T>(acc.x * inv, acc.y * inv),
-                       pack2<T>(acc.z * inv, acc.w * inv));
-        if (p.lse && col == 0)
-          p.lse[static_cast<int64_t>(hq) * p.total_q + tok] = lse;
+        sum[n][e] = t;
       }
     }
+    // the warps' states meet pairwise: the upper half's go through shared
+    // memory into the lower half's registers
+    float4* state = reinterpret_cast<float4*>(
+        smem + SM::OFF_S + (warp & (kWarps / 2 - 1)) * SM::SBYTES) + lane;
+    auto put = [&](float4* dst) {
+#pragma unroll
+      for (int i = 0; i < KS; ++i)
+#pragma unroll
+        for (int n = 0; n < NR; ++n)
+          dst[(i * NR + n) * 32] =
+              make_float4(o[i][n][0], o[i][n][1], o[i][n][2], o[i][n][3]);
+#pragma unroll
+      for (int n = 0; n < NR; ++n)
+        dst[(KS * NR + n) * 32] =
+            make_float4(m[n][0], m[n][1], sum[n][0], sum[n][1]);
+    };
+    auto join = [&](const float4* src) {
+#pragma unroll
+      for (int n = 0; n < NR; ++n) {
+        const float4 t = src[(KS * NR + n) * 32];
+        const float tm[2] = {t.x, t.y}, tl[2] = {t.z, t.w};
+        float f[2], g[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float M = fmaxf(m[n][e], tm[e]);
+          // (a warp that saw nothing but NaN keeps its NaN sum)
+          f[e] = m[n][e] == -INFINITY ? (sum[n][e] == 0.f ? 0.f : 1.f)
+                                      : ex2(m[n][e] - M);
+          g[e] = tm[e] == -INFINITY ? (tl[e] == 0.f ? 0.f : 1.f)
+                                    : ex2(tm[e] - M);
+          sum[n][e] = f[e] * sum[n][e] + g[e] * tl[e];
+          m[n][e] = M;
+        }
+#pragma unroll
+        for (int i = 0; i < KS; ++i) {
+          const float4 v = src[(i * NR + n) * 32];
+          o[i][n][0] = f[0] * o[i][n][0] + g[0] * v.x;
+          o[i][n][1] = f[1] * o[i][n][1] + g[1] * v.y;
+          o[i][n][2] = f[0] * o[i][n][2] + g[0] * v.z;
+          o[i][n][3] = f[1] * o[i][n][3] + g[1] * v.w;
+        }
+      }
+    };
+    if (warp >= 2) put(state);
+    if (more_pieces) begin_copies();
+    __syncthreads();
+    if (warp < 2) join(state);
+    if (warp == 1) put(state);
+    __syncthreads();
+    if (warp == 0) {
+      join(state + SM::SBYTES / 16);
+      // lane (g8, c4) holds, of rows 2 c4 and 2 c4 + 1, the runs of 16 (D =
+      // 64: 8) dimensions at 16 g8 of each 128 (D = 64: 8 g8)
+      constexpr int RUN = D == 64 ? 8 : 16;
+#pragma unroll
+      for (int n = 0; n < NR; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int r = 8 * n + 2 * c4 + e;
+          if (r >= done.r.rows) continue;
+          const int tok = done.r.q0 + row_tok[r];
+          const int hq = done.h * G + r - row_tok[r] * G;
+          float inv, lse;
+          finish(m[n][e], sum[n][e], done.slot >= 0 ? nullptr : p.sinks, hq,
+                 &inv, &lse);
+          inv *= vscale;
+          if (done.slot >= 0) {
+            // partial rows: [slot][row] of the shares, or of the split
+            int64_t row = static_cast<int64_t>(done.slot) * p.sk_rows + r;
+            int64_t at = row;
+            if (!sequence) {
+              const int64_t pr = part_row(p.part_tpr, done.b, done.r.q0, tok);
+              row = (static_cast<int64_t>(done.slot) * p.part_rows + pr) *
+                        p.Hq + hq;
+              at = (static_cast<int64_t>(done.slot) * p.Hq + hq) *
+                       p.part_rows + pr;
+            }
+            float* dst = p.part_o + row * D + RUN * g8;
+#pragma unroll
+            for (int i = 0; i < KS; i += 2)
+              *reinterpret_cast<float4*>(dst + 128 * (i >> 3) + 2 * (i & 7)) =
+                  make_float4(o[i][n][e] * inv, o[i][n][e + 2] * inv,
+                              o[i + 1][n][e] * inv, o[i + 1][n][e + 2] * inv);
+            if (g8 == 0) p.part_lse[at] = lse;
+          } else {
+            T* dst = static_cast<T*>(p.out) +
+                     static_cast<int64_t>(tok) * p.o_st +
+                     static_cast<int64_t>(hq) * p.o_sh + RUN * g8;
+#pragma unroll
+            for (int i = 0; i < KS; i += 4)
+              *reinterpret_cast<uint4*>(dst + 128 * (i >> 3) + 2 * (i & 7)) =
+                  make_uint4(
+                      pack2<T>(o[i][n][e] * inv, o[i][n][e + 2] * inv),
+                      pack2<T>(o[i + 1][n][e] * inv, o[i + 1][n][e + 2] * inv),
+                      pack2<T>(o[i + 2][n][e] * inv, o[i + 2][n][e + 2] * inv),
+                      pack2<T>(o[i + 3][n][e] * inv,
+                               o[i + 3][n][e + 2] * inv));
+            if (p.lse && g8 == 0)
+              p.lse[static_cast<int64_t>(hq) * p.total_q + tok] = lse;
+          }
+        }
+    }
     if (!more_pieces) break;
-    __syncthreads();       // the states and the queries are read
+    load_queries(pc, pc.r.rows);
+    // (the queries and the piece are read: two barriers ago)
   }
   cp_async_wait<0>();
 }
@@ -1323,7 +1371,7 @@ cudaError_t dispatch(const AttnParams& p, int D, int splits, bool pdl,
 }  // namespace dfp4
 
 int decode_fp4_ctas_per_sm(int D, int rows) {
-  return rows <= 8 ? 3 : (D == 256 ? 2 : 3);
+  return rows <= 8 ? (D == 256 ? 3 : 4) : (D == 256 ? 2 : 3);
 }
 
 cudaError_t launch_decode_attn_fp4(const AttnParams& p, int D, bool bf16,
