@@ -54,6 +54,9 @@ constexpr int kWarps = 4;
 constexpr float kRaise = 6.f;      // log2 slack of the running maximum
 // Tiles of a CTA's share at least, so that each warp has some.
 constexpr int kMinTiles = 2 * kWarps;
+// What a unit costs a CTA beside its tiles, in tiles: its queries, the join of
+// the warps' states and the store.
+constexpr int kUnitCost = 8;
 constexpr int kFoldThreads = 256;
 
 inline size_t up256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
@@ -295,7 +298,7 @@ decode_fp4_kernel(const AttnParams p, int splits) {
 
   // ---- this CTA's first piece
   Piece pc;
-  int left = 0;          // tiles of the CTA's share past this piece
+  int left = 0;          // what of the CTA's share is past this piece's unit
   auto tiles_of = [&](const Req& r) {
     const int k0 = r.lo & ~15;
     return r.rows == 0 ? 0 : max(1, (r.hi - k0 + KT - 1) / KT);
@@ -326,9 +329,10 @@ decode_fp4_kernel(const AttnParams p, int splits) {
     pc.t0 = 0;
     pc.t1 = tiles_of(pc.r);
   } else {
-    // The units (request, KV head) in order form a sequence of N tiles, of
-    // which every CTA takes an equal run.  Thread t counts the tiles of a
-    // run of requests; the one whose run holds the CTA's first tile finds it.
+    // The units (request, KV head) in order, each kUnitCost and its tiles
+    // long, form a sequence of length N, of which every CTA takes an equal
+    // run (the tiles in it).  Thread t adds up a run of requests; the one
+    // whose run holds the start of the CTA's share finds it.
     const int per = (p.batch + NT - 1) / NT;
     const int b_lo = min(p.batch, static_cast<int>(threadIdx.x) * per);
     const int b_hi = min(p.batch, b_lo + per);
@@ -336,7 +340,8 @@ decode_fp4_kernel(const AttnParams p, int splits) {
     Req mine_req{};
     for (int b = b_lo; b < b_hi; ++b) {
       mine_req = request(p, b, p.sk_rows, blockIdx.x == 0);
-      sum += static_cast<long long>(tiles_of(mine_req)) * p.Hkv;
+      if (mine_req.rows > 0)
+        sum += static_cast<long long>(kUnitCost + tiles_of(mine_req)) * p.Hkv;
     }
     long long incl = sum;
 #pragma unroll
@@ -369,7 +374,7 @@ decode_fp4_kernel(const AttnParams p, int splits) {
       long long at = excl;
       for (int b = b_lo; b < b_hi; ++b) {
         const Req r = per == 1 ? mine_req : request(p, b, p.sk_rows, false);
-        const int n = tiles_of(r);
+        const int n = r.rows > 0 ? kUnitCost + tiles_of(r) : 0;
         const long long all = static_cast<long long>(n) * p.Hkv;
         if (T0 < at + all) {
           const unsigned off = static_cast<unsigned>(T0 - at);
@@ -385,21 +390,27 @@ decode_fp4_kernel(const AttnParams p, int splits) {
     __syncthreads();
     pc = cur;
     pc.kt0 = pc.r.lo & ~15;
-    const int n = tiles_of(pc.r), want = static_cast<int>(T1 - T0);
-    pc.t1 = min(n, pc.t0 + want);
-    left = want - (pc.t1 - pc.t0);
+    const int n = tiles_of(pc.r);
+    const long long end = T1 - T0 + pc.t0 - kUnitCost;   // from tile 0
+    pc.t1 = static_cast<int>(min(static_cast<long long>(n), end));
+    pc.t0 = max(0, pc.t0 - kUnitCost);
+    left = static_cast<int>(end - n);
+    if (pc.t1 <= 0) {                    // none of the unit's tiles
+      if (threadIdx.x == 0) p.sk_marks[c] = make_int2(-1, -1);
+      return;
+    }
     __syncthreads();                     // (`cur` is written again)
     // a unit cut by the share's ends leaves its part in slot 2 c (begun
     // before) or 2 c + 1 (ending after)
     pc.slot = pc.t0 > 0 ? 2 * c : pc.t1 < n ? 2 * c + 1 : -1;
     if (threadIdx.x == 0) {
       p.sk_marks[c].x = pc.t0 > 0 ? pc.b * p.Hkv + pc.h : -1;
-      if (left == 0)
+      if (left <= kUnitCost)
         p.sk_marks[c].y =
             pc.t0 == 0 && pc.t1 < n ? pc.b * p.Hkv + pc.h : -1;
     }
   }
-  // the piece after `a` in the CTA's share (left > 0)
+  // the piece after `a` in the CTA's share (left > kUnitCost)
   auto next_piece = [&](const Piece& a) {
     Piece x = a;
     if (++x.h == p.Hkv) {
@@ -412,10 +423,10 @@ decode_fp4_kernel(const AttnParams p, int splits) {
     }
     const int n = tiles_of(x.r);
     x.t0 = 0;
-    x.t1 = min(n, left);
-    left -= x.t1;
+    x.t1 = min(n, left - kUnitCost);
+    left -= kUnitCost + n;
     x.slot = x.t1 < n ? 2 * static_cast<int>(blockIdx.x) + 1 : -1;
-    if (left == 0 && threadIdx.x == 0)
+    if (left <= kUnitCost && threadIdx.x == 0)
       p.sk_marks[blockIdx.x].y = x.t1 < n ? x.b * p.Hkv + x.h : -1;
     return x;
   };
@@ -999,7 +1010,7 @@ decode_fp4_kernel(const AttnParams p, int splits) {
 
     // ---- the next piece's pages and copies begin before the end of this one
     const Piece done = cur;
-    const bool more_pieces = left > 0;
+    const bool more_pieces = left > kUnitCost;
     if (more_pieces) {
       pc = next_piece(done);
       begin_pages(pc);

@@ -97,9 +97,13 @@ bool stride16(int64_t s, int elem) { return (s * elem) % 16 == 0; }
 // choice.
 constexpr int64_t kLongUnitKeys = 2048;
 
-// Calls whose units span at most this many keys run one CTA per unit on a
-// 4-bit cache.
-constexpr int64_t kFp4UnitKeys = 256;
+// 4-bit caches: calls whose units span at most this many keys run one CTA per
+// (unit, split), longer ones as equal shares of the key tiles.  Measured on
+// GB300 (32/8 heads, D 128; one CTA per unit against shares): 64 requests of
+// 300-600 keys 17.2 against 24.0 us, 76 of 2000 keys 39.1 against 41.9, 256
+// of 200-2000 keys 79.8 against 82.7; 64 of 512-4096 keys 57.4 against 49.7,
+// 64 of 512-8192 keys 102.4 against 76.3.
+constexpr int64_t kFp4UnitKeys = 2048;
 
 struct Plan {
   int64_t range = 0;      // widest key range of a decode-class unit
@@ -117,8 +121,9 @@ struct Plan {
 size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 // Pieces of a request's key range for the 4-bit decode kernel with one CTA
-// per (request, piece, KV head), which takes the calls that the shares do
-// not (below): about two waves of CTAs, 256 keys each or more.
+// per (request, piece, KV head): as many as one wave of CTAs holds, of 256
+// keys or more (two waves instead: 64 requests of 300-600 keys 26.0 against
+// 17.6 us).
 int fp4_splits(int batch, int max_q, int G, int Hkv, int D, int64_t range,
                int sms) {
   const int64_t rows = static_cast<int64_t>(max_q) * G;
@@ -127,7 +132,7 @@ int fp4_splits(int batch, int max_q, int G, int Hkv, int D, int64_t range,
       static_cast<int64_t>(sms) *
       decode_fp4_ctas_per_sm(D, rows < kDecodeRows ? static_cast<int>(rows)
                                                    : kDecodeRows);
-  int64_t s = (2 * slots + units - 1) / units;
+  int64_t s = slots / units;
   const int64_t most = (range + 255) / 256;
   if (s > most) s = most;
   if (s > 512) s = 512;
