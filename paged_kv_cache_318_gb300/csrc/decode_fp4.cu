@@ -143,26 +143,6 @@ __device__ __forceinline__ uint32_t spread(uint32_t v, int high) {
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 
-// Two float32 values as one operand of the packed instructions.
-__device__ __forceinline__ uint64_t pair(float a, float b) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ void unpair(uint64_t v, float& a, float& b) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-
 // D(16 x 8) = A(16 x 16) B(16 x 8), f16 in, fp32 accumulate; mma: D += ...
 __device__ __forceinline__ void mma_first(float* d, uint32_t a0, uint32_t a1,
                                           uint32_t a2, uint32_t a3,
@@ -851,15 +831,14 @@ decode_fp4_kernel(const AttnParams p, int splits) {
       uint32_t pb[MT][NR][2];
 #pragma unroll
       for (int n = 0; n < NR; ++n) {
-        const uint64_t base = pair(m[n][0] == -INFINITY ? 0.f : -m[n][0],
-                                   m[n][1] == -INFINITY ? 0.f : -m[n][1]);
+        const float base[2] = {m[n][0] == -INFINITY ? 0.f : m[n][0],
+                               m[n][1] == -INFINITY ? 0.f : m[n][1]};
 #pragma unroll
         for (int i = 0; i < MT; ++i) {
           float* x = sc[i][n];
-          unpair(add2(pair(x[0], x[1]), base), x[0], x[1]);
-          unpair(add2(pair(x[2], x[3]), base), x[2], x[3]);
+          // (a packed sum could be fused with the product above)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) x[e] = ex2(x[e]);
+          for (int e = 0; e < 4; ++e) x[e] = ex2(__fsub_rn(x[e], base[e & 1]));
           l[n] = add2(l[n], add2(pair(x[0], x[1]), pair(x[2], x[3])));
           // P rounds to f16 (half a step of 2^-11 relative) for the MMA; the
           // sums keep the float32 values

@@ -20,20 +20,18 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// 16 consecutive 16-bit values at src (16-byte aligned) -> 8 bytes of codes
-// and the group's scale.
+// 16 consecutive 16-bit values -> 8 bytes of codes and the group's scale.
 template <typename T>
-__device__ __forceinline__ void quantize16(const T* src, float scale,
-                                           uint8_t* codes, uint8_t* sf) {
-  const uint4 r0 = *reinterpret_cast<const uint4*>(src);
-  const uint4 r1 = *reinterpret_cast<const uint4*>(src + 8);
+__device__ __forceinline__ void quantize16(uint4 r0, uint4 r1, float scale,
+                                           float sixth, uint8_t* codes,
+                                           uint8_t* sf) {
   float x[16];
   widen8<T>(r0, x);
   widen8<T>(r1, x + 8);
   float top = 0.f;
 #pragma unroll
   for (int i = 0; i < 16; ++i) top = max_nan(top, fabsf(x[i]));
-  const Fp4Scale s = fp4_scale(top, scale);
+  const Fp4Scale s = fp4_scale(top, scale, sixth);
   *reinterpret_cast<uint2*>(codes) =
       make_uint2(fp4_codes8(x, s.inv), fp4_codes8(x + 8, s.inv));
   *sf = static_cast<uint8_t>(s.code);
@@ -90,24 +88,30 @@ cache_write_fp4_kernel(const T* __restrict__ key, const T* __restrict__ value,
   if (tl >= tokens_per_block) return;
   const int r0 = threadIdx.x - tl * per_token;
   const float ks = *k_scale, vs = *v_scale;
+  const float ks6 = fp4_sixth(ks), vs6 = fp4_sixth(vs);
+  const int64_t step = static_cast<int64_t>(gridDim.x) * tokens_per_block;
   for (int64_t t = static_cast<int64_t>(blockIdx.x) * tokens_per_block + tl;
-       t < num_tokens; t += static_cast<int64_t>(gridDim.x) *
-                            tokens_per_block) {
+       t < num_tokens; t += step) {
     const int64_t s = __ldg(slots + t);
-    if (s < 0) continue;                          // padding slot
-    if (s >= num_slots) {                         // outside the cache: skip
-      if (r0 == 0) atomicOr(err, kErrBadSlot);
-      continue;
-    }
-    const int64_t blk = s / BS;
-    const int64_t off = s - blk * BS;
+    int64_t blk = 0, off = 0;
     for (int r = r0; r < per_token; r += kThreads) {
       const int h = r / groups, g = r - h * groups;
+      // (the rows do not wait for the slot)
+      const uint4* kp =
+          reinterpret_cast<const uint4*>(key + t * k_st + h * k_sh + g * 16);
+      const uint4* vp =
+          reinterpret_cast<const uint4*>(value + t * v_st + h * v_sh + g * 16);
+      const uint4 k0 = kp[0], k1 = kp[1], v0 = vp[0], v1 = vp[1];
+      if (s < 0) break;                           // padding slot
+      if (s >= num_slots) {                       // outside the cache: skip
+        if (r == 0) atomicOr(err, kErrBadSlot);
+        break;
+      }
+      if (r == r0) split_slot(s, BS, &blk, &off);
       const int64_t c = blk * c_sb + off * c_sr + h * c_sh + g * 8;
       const int64_t f = blk * f_sb + off * f_sr + h * f_sh + g;
-      quantize16<T>(key + t * k_st + h * k_sh + g * 16, ks, kc + c, k_sf + f);
-      quantize16<T>(value + t * v_st + h * v_sh + g * 16, vs, vc + c,
-                    v_sf + f);
+      quantize16<T>(k0, k1, ks, ks6, kc + c, k_sf + f);
+      quantize16<T>(v0, v1, vs, vs6, vc + c, v_sf + f);
     }
   }
 }

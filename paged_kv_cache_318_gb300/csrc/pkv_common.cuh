@@ -592,8 +592,13 @@ struct Fp4Scale {
   uint32_t code;    // the E4M3 code
   float inv;
 };
-__device__ __forceinline__ Fp4Scale fp4_scale(float top, float scale) {
-  const float t = __fmul_rn(top, __frcp_rn(__fmul_rn(scale, 6.f)));
+// fl(1 / fl(6 scale)), the same for every group.
+__device__ __forceinline__ float fp4_sixth(float scale) {
+  return __frcp_rn(__fmul_rn(scale, 6.f));
+}
+__device__ __forceinline__ Fp4Scale fp4_scale(float top, float scale,
+                                              float sixth) {
+  const float t = __fmul_rn(top, sixth);
   uint16_t c;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c) : "f"(0.f), "f"(t));
   const uint32_t h = e4m3x2_to_f16(c);
@@ -628,6 +633,38 @@ __device__ __forceinline__ uint32_t fp4_codes8(const float* x, float inv) {
   return r;
 }
 
+// Cache block and row of a slot.
+__device__ __forceinline__ void split_slot(int64_t slot, int BS, int64_t* blk,
+                                           int64_t* row) {
+  if ((slot >> 31) == 0) {               // (a 32-bit division)
+    const uint32_t s = static_cast<uint32_t>(slot);
+    *blk = s / static_cast<uint32_t>(BS);
+  } else {
+    *blk = slot / BS;
+  }
+  *row = slot - *blk * BS;
+}
+
+// Two float32 values as one operand of the packed instructions.  (add2 of a
+// mul2 may come out as one fused multiply-add.)
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 // Eight 16-bit values of a 16-byte load, widened.
 template <typename T>
 __device__ __forceinline__ void widen8(const uint4& raw, float* x) {

@@ -26,12 +26,14 @@
 // 16-byte boundaries, and rot = D / 2^n >= 32 (neox) or any multiple of 8
 // (adjacent pairs).  rope_any_kernel takes everything else: one warp a row,
 // through shared memory.
+#include <type_traits>
+
 #include "pkv_common.cuh"
 
 namespace pkv {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kMaxD = 512;
 
 // Axis whose position rotates pair i.
@@ -111,15 +113,16 @@ __device__ __forceinline__ void table_run(const RopeLaunch& p, int64_t pos,
   }
 }
 
-__device__ __forceinline__ float sum8_pairwise(const float* x) {
-  float s[8];
+// Sum of squares of four pairs, neighbours first.
+__device__ __forceinline__ float sum8_pairwise(const uint64_t* x) {
+  float s[4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) s[i] = __fmul_rn(x[i], x[i]);
-#pragma unroll
-  for (int n = 1; n < 8; n *= 2)
-#pragma unroll
-    for (int i = 0; i < 8; i += 2 * n) s[i] = __fadd_rn(s[i], s[i + n]);
-  return s[0];
+  for (int i = 0; i < 4; ++i) {
+    float a, b;
+    unpair(mul2(x[i], x[i]), a, b);
+    s[i] = __fadd_rn(a, b);
+  }
+  return __fadd_rn(__fadd_rn(s[0], s[1]), __fadd_rn(s[2], s[3]));
 }
 
 __device__ __forceinline__ float inv_rms(float sum, int D, float eps) {
@@ -136,9 +139,22 @@ __device__ __forceinline__ void rotate(float& a, float& b, float c, float s) {
 }
 
 template <typename T>
-__device__ __forceinline__ uint4 pack8(const float* x) {
-  return make_uint4(pack2<T>(x[0], x[1]), pack2<T>(x[2], x[3]),
-                    pack2<T>(x[4], x[5]), pack2<T>(x[6], x[7]));
+__device__ __forceinline__ uint4 pack8(const uint64_t* x) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float a, b;
+    unpair(x[i], a, b);
+    w[i] = pack2<T>(a, b);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+template <typename T>
+__device__ __forceinline__ void widen8(const uint4& raw, uint64_t* x) {
+  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    x[i] = pair(elem_f32<T>(w[i], 0), elem_f32<T>(w[i], 1));
 }
 
 __device__ __forceinline__ uint32_t e4m3_codes4(const float* x, float scale) {
@@ -151,56 +167,39 @@ __device__ __forceinline__ uint32_t e4m3_codes4(const float* x, float scale) {
   return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
 }
 
-// One row's chunks A and B (chunk numbers ca, cb) to the cache row.  For
-// the 4-bit cache, chunks 2 m and 2 m + 1 share a block scale: they are a
-// lane's and its neighbour's (lane ^ 1) chunks.  `on`: this lane stores (all
-// lanes take part in the exchange).
-template <typename T, int STORE>
-__device__ __forceinline__ void store_cache(const RopeLaunch& p, bool value,
-                                            int64_t blk, int64_t off, int h,
-                                            int ca, int cb, const float* x,
-                                            const uint4* raw, bool on,
-                                            float scale) {
-  const int64_t row = blk * p.c_sb + off * p.c_sr + h * p.c_sh;
-  void* base = value ? p.vc : p.kc;
-  if constexpr (STORE == kRopeCache16) {
-    if (!on) return;
-    T* dst = static_cast<T*>(base) + row;
-    *reinterpret_cast<uint4*>(dst + 8 * ca) = value ? raw[0] : pack8<T>(x);
-    *reinterpret_cast<uint4*>(dst + 8 * cb) = value ? raw[1] : pack8<T>(x + 8);
-  } else if constexpr (STORE == kRopeCacheFp8) {
-    if (!on) return;
-    uint8_t* dst = static_cast<uint8_t*>(base) + row;
-    *reinterpret_cast<uint2*>(dst + 8 * ca) =
-        make_uint2(e4m3_codes4(x, scale), e4m3_codes4(x + 4, scale));
-    *reinterpret_cast<uint2*>(dst + 8 * cb) =
-        make_uint2(e4m3_codes4(x + 8, scale), e4m3_codes4(x + 12, scale));
-  } else {
-    float top[2];
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      float m = 0.f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) m = max_nan(m, fabsf(x[8 * c + i]));
-      top[c] = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    }
-    if (!on) return;
-    uint8_t* dst = static_cast<uint8_t*>(base) + row;
-    uint8_t* sf = (value ? p.v_sf : p.k_sf) + blk * p.f_sb + off * p.f_sr +
-                  h * p.f_sh;
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const int ch = c ? cb : ca;
-      const Fp4Scale s = fp4_scale(top[c], scale);
-      *reinterpret_cast<uint32_t*>(dst + 4 * ch) =
-          fp4_codes8(x + 8 * c, s.inv);
-      if (!(ch & 1)) sf[ch >> 1] = static_cast<uint8_t>(s.code);
-    }
-  }
+// The E4M3 codes of four values, x / scale rounded to float32 first.  With
+// y = fl(1 / scale) and q = fl(x y), q + fl(x - q scale) y is the correctly
+// rounded quotient (Markstein 1990) where nothing over- or underflows: the
+// scale is in [2^-60, 2^60] and x is cut to where every quotient saturates.
+struct Fp8Scale {
+  float scale, inv, limit;     // limit < 0: an ordinary division
+};
+__device__ __forceinline__ Fp8Scale fp8_scale(float scale) {
+  Fp8Scale s;
+  s.scale = scale;
+  s.inv = __frcp_rn(scale);
+  s.limit = scale >= 0x1p-60f && scale <= 0x1p60f ? 480.f * scale : -1.f;
+  return s;
+}
+__device__ __forceinline__ float quotient(float x, const Fp8Scale& s) {
+  asm("min.NaN.f32 %0, %0, %1;" : "+f"(x) : "f"(s.limit));
+  asm("max.NaN.f32 %0, %0, %1;" : "+f"(x) : "f"(-s.limit));
+  const float q = __fmul_rn(x, s.inv);
+  return __fmaf_rn(__fmaf_rn(-q, s.scale, x), s.inv, q);
+}
+__device__ __forceinline__ uint32_t e4m3_codes4(const float* x,
+                                                const Fp8Scale& s) {
+  if (s.limit < 0.f) return e4m3_codes4(x, s.scale);
+  uint16_t lo, hi;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo)
+      : "f"(quotient(x[1], s)), "f"(quotient(x[0], s)));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi)
+      : "f"(quotient(x[3], s)), "f"(quotient(x[2], s)));
+  return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
 }
 
 template <typename T, int D, int STORE, bool NEOX>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 5)
 rope_kernel(const RopeLaunch p, int parts) {
   // an attention kernel queued next as a programmatic dependent may become
   // resident now (it waits for this grid before reading what this writes)
@@ -217,133 +216,242 @@ rope_kernel(const RopeLaunch p, int parts) {
   const int ca = blk0 * (span / 8) + (j - blk0 * nb), cb = ca + nb;
   const bool rot_a = 8 * ca < p.rot, rot_b = 8 * cb < p.rot;
   const int half = p.rot / 2;
-  const int pq = (p.Hq + RPW - 1) / RPW, pk = (p.Hkv + RPW - 1) / RPW;
-  const int passes = pq + (STORE == kRopeRows ? pk : 2 * pk);
-  const float ks = STORE >= kRopeCacheFp8 ? *p.k_scale : 1.f;
-  const float vs = STORE >= kRopeCacheFp8 ? *p.v_scale : 1.f;
+  // the lane's first pair of each four (adjacent pairs) or of the eight
+  const int ia = NEOX ? 8 * ca : 4 * ca, ib = NEOX ? ia + 4 : 4 * cb;
   const int64_t work = p.num_tokens * parts;
   const int64_t step = static_cast<int64_t>(gridDim.x) * (kThreads / 32);
   for (int64_t w = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) +
                    (threadIdx.x >> 5);
        w < work; w += step) {
-    const int64_t t = w / parts;
-    const int part = static_cast<int>(w - t * parts);
+    const int64_t t = parts == 1 ? w : w / parts;
+    const int part = parts == 1 ? 0 : static_cast<int>(w - t * parts);
+    int64_t slot = -1, blk = 0, off = 0;
+    if constexpr (STORE != kRopeRows)
+      slot = read_slot(p, t, part == 0 && lane == 0);
     int64_t pos[4] = {0, 0, 0, 0};
     if (!read_positions(p, t, part == 0 && lane == 0, pos)) continue;
-    int64_t slot = -1, blk = 0, off = 0;
-    if constexpr (STORE != kRopeRows) {
-      slot = read_slot(p, t, part == 0 && lane == 0);
-      if (slot >= 0) {
-        blk = slot / p.BS;
-        off = slot - blk * p.BS;
-      }
-    }
-    // cos and sin of this lane's pairs: pairs 8 ca .. (neox, A with B), or
-    // 4 ca .. and 4 cb .. (adjacent pairs)
-    float c[8], s[8];
-    if (NEOX ? rot_a : (rot_a || rot_b)) {
+    if (STORE != kRopeRows && slot >= 0) split_slot(slot, p.BS, &blk, &off);
+    // cos and sin of the lane's eight pairs, two to an operand
+    uint64_t c[4], s[4];
+    {
+      float cf[8], sf[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) cf[e] = sf[e] = 0.f;
       if (p.axes == 1) {
         if constexpr (NEOX) {
-          table_run<T, 8>(p, pos[0], 8 * ca, c);
-          table_run<T, 8>(p, pos[0], half + 8 * ca, s);
+          if (rot_a) {
+            table_run<T, 8>(p, pos[0], ia, cf);
+            table_run<T, 8>(p, pos[0], half + ia, sf);
+          }
         } else {
           if (rot_a) {
-            table_run<T, 4>(p, pos[0], 4 * ca, c);
-            table_run<T, 4>(p, pos[0], half + 4 * ca, s);
+            table_run<T, 4>(p, pos[0], ia, cf);
+            table_run<T, 4>(p, pos[0], half + ia, sf);
           }
           if (rot_b) {
-            table_run<T, 4>(p, pos[0], 4 * cb, c + 4);
-            table_run<T, 4>(p, pos[0], half + 4 * cb, s + 4);
+            table_run<T, 4>(p, pos[0], ib, cf + 4);
+            table_run<T, 4>(p, pos[0], half + ib, sf + 4);
           }
         }
       } else {
+        int woven = 0;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const int i = NEOX ? 8 * ca + e
-                             : (e < 4 ? 4 * ca + e : 4 * cb + e - 4);
+          const int i = e < 4 ? ia + e : ib + e - 4;
           if (i >= half) continue;
-          const int a = pair_axis(p, i);
+          int a;
+          if (p.woven) {               // i mod axes, counted on
+            woven = e == 0 || e == 4 ? i % p.axes
+                                     : woven + 1 == p.axes ? 0 : woven + 1;
+            a = i < p.axes * p.sections[woven] ? woven : 0;
+          } else {
+            a = pair_axis(p, i);
+          }
           const int64_t at = a == 0 ? pos[0]
                              : a == 1 ? pos[1] : a == 2 ? pos[2] : pos[3];
-          c[e] = table_at<T>(p, at, i);
-          s[e] = table_at<T>(p, at, half + i);
+          cf[e] = table_at<T>(p, at, i);
+          sf[e] = table_at<T>(p, at, half + i);
         }
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        c[e] = pair(cf[2 * e], cf[2 * e + 1]);
+        s[e] = pair(sf[2 * e], sf[2 * e + 1]);
       }
     }
-    for (int i = part; i < passes; i += parts) {
-      const int kind = i < pq ? 0 : i < pq + pk ? 1 : 2;      // q, k or v
-      const int h0 = (kind == 0 ? i : kind == 1 ? i - pq : i - pq - pk) * RPW;
-      const int h = h0 + sub;
-      const bool on = h < (kind == 0 ? p.Hq : p.Hkv);
-      if (STORE != kRopeRows && kind > 0 && slot < 0) continue;
-      const T* src = static_cast<const T*>(kind == 0   ? p.q
-                                           : kind == 1 ? p.k
-                                                       : p.v) +
-                     t * (kind == 0 ? p.q_st : kind == 1 ? p.k_st : p.v_st) +
-                     h * (kind == 0   ? p.q_sh
-                          : kind == 1 ? p.k_sh
-                                      : p.v_sh);
+
+    // The passes of one kind of row (q, k or v), `parts` apart.  The next
+    // pass's rows load while this one's are worked on.
+    int before = 0;                       // passes of the kinds before
+    auto rows = [&](auto kind_tag, const T* src, int64_t sh, int H,
+                    const T* weight, auto&& store) {
+      constexpr int kind = decltype(kind_tag)::value;
+      const int n = (H + RPW - 1) / RPW;
+      int i = 0;
+      if (parts > 1) {
+        i = part - before % parts;
+        if (i < 0) i += parts;
+      }
+      before += n;
+      if (i >= n) return;
+      const T* at = src + static_cast<int64_t>(i * RPW + sub) * sh;
+      const int64_t hop = static_cast<int64_t>(parts) * RPW * sh;
       uint4 raw[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-      if (on) {
-        raw[0] = *reinterpret_cast<const uint4*>(src + 8 * ca);
-        raw[1] = *reinterpret_cast<const uint4*>(src + 8 * cb);
-      }
-      float x[16];
-      widen8<T>(raw[0], x);
-      widen8<T>(raw[1], x + 8);
-      if (kind < 2) {
-        if (p.norm) {
-          float sa = sum8_pairwise(x), sb = sum8_pairwise(x + 8);
-          // neighbours first: lanes of the span, then A with B, then spans
-          for (int o = 1; o < nb; o *= 2) {
-            sa = __fadd_rn(sa, __shfl_xor_sync(0xffffffffu, sa, o));
-            sb = __fadd_rn(sb, __shfl_xor_sync(0xffffffffu, sb, o));
-          }
-          sa = __fadd_rn(sa, sb);
-          for (int o = nb; o < LPR; o *= 2)
-            sa = __fadd_rn(sa, __shfl_xor_sync(0xffffffffu, sa, o));
-          const float r = inv_rms(sa, D, p.eps);
-          const T* wt = static_cast<const T*>(kind == 0 ? p.q_weight
-                                                        : p.k_weight);
-          float wv[16];
-          widen8<T>(__ldg(reinterpret_cast<const uint4*>(wt + 8 * ca)), wv);
-          widen8<T>(__ldg(reinterpret_cast<const uint4*>(wt + 8 * cb)),
-                    wv + 8);
-#pragma unroll
-          for (int e = 0; e < 16; ++e)
-            x[e] = __fmul_rn(__fmul_rn(x[e], r),
-                             __fadd_rn(wv[e], p.weight_offset));
+      auto load = [&](int h) {
+        if (h < H) {
+          raw[0] = *reinterpret_cast<const uint4*>(at + 8 * ca);
+          raw[1] = *reinterpret_cast<const uint4*>(at + 8 * cb);
         }
-        if constexpr (NEOX) {
-          if (rot_a) {
+        at += hop;
+      };
+      load(i * RPW + sub);
+      uint64_t wv[8];
+      if (kind < 2 && p.norm) {
+        widen8<T>(__ldg(reinterpret_cast<const uint4*>(weight + 8 * ca)), wv);
+        widen8<T>(__ldg(reinterpret_cast<const uint4*>(weight + 8 * cb)),
+                  wv + 4);
+        const uint64_t o = pair(p.weight_offset, p.weight_offset);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) rotate(x[e], x[8 + e], c[e], s[e]);
+        for (int e = 0; e < 8; ++e) wv[e] = add2(wv[e], o);
+      }
+      for (; i < n; i += parts) {
+        const int h = i * RPW + sub;
+        const uint4 now[2] = {raw[0], raw[1]};
+        if (i + parts < n) load(h + parts * RPW);
+        uint64_t x[8];
+        widen8<T>(now[0], x);
+        widen8<T>(now[1], x + 4);
+        if (kind < 2) {
+          if (p.norm) {
+            float sa = sum8_pairwise(x), sb = sum8_pairwise(x + 4);
+            // neighbours first: lanes of the span, then A with B, then spans
+            for (int o = 1; o < nb; o *= 2) {
+              sa = __fadd_rn(sa, __shfl_xor_sync(0xffffffffu, sa, o));
+              sb = __fadd_rn(sb, __shfl_xor_sync(0xffffffffu, sb, o));
+            }
+            sa = __fadd_rn(sa, sb);
+            for (int o = nb; o < LPR; o *= 2)
+              sa = __fadd_rn(sa, __shfl_xor_sync(0xffffffffu, sa, o));
+            // (D is a power of two: the product is the quotient)
+            const float r = __frcp_rn(__fsqrt_rn(
+                __fadd_rn(__fmul_rn(sa, 1.f / D), p.eps)));
+            const uint64_t r2 = pair(r, r);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = mul2(mul2(x[e], r2), wv[e]);
           }
+          if constexpr (NEOX) {
+            if (rot_a) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                // (packed products, but single sums: the assembler turns a
+                // packed sum of products into a fused multiply-add)
+                float ac[2], bs[2], bc[2], as[2];
+                unpair(mul2(x[e], c[e]), ac[0], ac[1]);
+                unpair(mul2(x[4 + e], s[e]), bs[0], bs[1]);
+                unpair(mul2(x[4 + e], c[e]), bc[0], bc[1]);
+                unpair(mul2(x[e], s[e]), as[0], as[1]);
+                x[e] = pair(__fsub_rn(ac[0], bs[0]), __fsub_rn(ac[1], bs[1]));
+                x[4 + e] = pair(__fadd_rn(bc[0], as[0]),
+                                __fadd_rn(bc[1], as[1]));
+              }
+            }
+          } else {
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              if (!(q ? rot_b : rot_a)) continue;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                float a, b, cc[2], ss[2];
+                unpair(x[4 * q + e], a, b);
+                unpair(c[2 * q + (e >> 1)], cc[0], cc[1]);
+                unpair(s[2 * q + (e >> 1)], ss[0], ss[1]);
+                rotate(a, b, cc[e & 1], ss[e & 1]);
+                x[4 * q + e] = pair(a, b);
+              }
+            }
+          }
+        }
+        store(h, h < H, x, now);
+      }
+    };
+    auto row_store = [&](T* base, int64_t sh) {
+      return [=](int h, bool on, const uint64_t* x, const uint4*) {
+        if (!on) return;
+        T* dst = base + h * sh;
+        *reinterpret_cast<uint4*>(dst + 8 * ca) = pack8<T>(x);
+        *reinterpret_cast<uint4*>(dst + 8 * cb) = pack8<T>(x + 4);
+      };
+    };
+    // For the 4-bit cache, chunks 2 m and 2 m + 1 share a block scale: they
+    // are a lane's and its neighbour's (lane ^ 1) chunks.
+    auto cache_store = [&](auto value_tag) {
+      constexpr bool value = decltype(value_tag)::value != 0;
+      const int64_t row = blk * p.c_sb + off * p.c_sr;
+      [[maybe_unused]] const int64_t frow = blk * p.f_sb + off * p.f_sr;
+      const float scale =
+          STORE < kRopeCacheFp8 ? 1.f : value ? *p.v_scale : *p.k_scale;
+      [[maybe_unused]] const float sixth =
+          STORE == kRopeCacheFp4 ? fp4_sixth(scale) : 0.f;
+      const Fp8Scale s8 = STORE == kRopeCacheFp8 ? fp8_scale(scale)
+                                                 : Fp8Scale{};
+      return [=, &p](int h, bool on, const uint64_t* x, const uint4* raw) {
+        void* base = value ? p.vc : p.kc;
+        if constexpr (STORE == kRopeCache16) {
+          if (!on) return;
+          T* dst = static_cast<T*>(base) + row + h * p.c_sh;
+          *reinterpret_cast<uint4*>(dst + 8 * ca) =
+              value ? raw[0] : pack8<T>(x);
+          *reinterpret_cast<uint4*>(dst + 8 * cb) =
+              value ? raw[1] : pack8<T>(x + 4);
         } else {
-          if (rot_a) {
+          float f[16];
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              rotate(x[2 * e], x[2 * e + 1], c[e], s[e]);
-          }
-          if (rot_b) {
+          for (int e = 0; e < 8; ++e) unpair(x[e], f[2 * e], f[2 * e + 1]);
+          uint8_t* dst = static_cast<uint8_t*>(base) + row + h * p.c_sh;
+          if constexpr (STORE == kRopeCacheFp8) {
+            if (!on) return;
+            *reinterpret_cast<uint2*>(dst + 8 * ca) =
+                make_uint2(e4m3_codes4(f, s8), e4m3_codes4(f + 4, s8));
+            *reinterpret_cast<uint2*>(dst + 8 * cb) =
+                make_uint2(e4m3_codes4(f + 8, s8), e4m3_codes4(f + 12, s8));
+          } else {
+            float top[2];
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              rotate(x[8 + 2 * e], x[9 + 2 * e], c[4 + e], s[4 + e]);
+            for (int q = 0; q < 2; ++q) {
+              float m = 0.f;
+#pragma unroll
+              for (int e = 0; e < 8; ++e) m = max_nan(m, fabsf(f[8 * q + e]));
+              top[q] = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 1));
+            }
+            if (!on) return;
+            uint8_t* sf = (value ? p.v_sf : p.k_sf) + frow + h * p.f_sh;
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              const int ch = q ? cb : ca;
+              const Fp4Scale sc = fp4_scale(top[q], scale, sixth);
+              *reinterpret_cast<uint32_t*>(dst + 4 * ch) =
+                  fp4_codes8(f + 8 * q, sc.inv);
+              if (!(ch & 1)) sf[ch >> 1] = static_cast<uint8_t>(sc.code);
+            }
           }
         }
-      }
-      if (kind == 0 || STORE == kRopeRows) {
-        if (on) {
-          T* dst = static_cast<T*>(kind == 0 ? p.q_out : p.k_out) +
-                   t * (kind == 0 ? p.qo_st : p.ko_st) +
-                   h * (kind == 0 ? p.qo_sh : p.ko_sh);
-          *reinterpret_cast<uint4*>(dst + 8 * ca) = pack8<T>(x);
-          *reinterpret_cast<uint4*>(dst + 8 * cb) = pack8<T>(x + 8);
-        }
-      } else if constexpr (STORE != kRopeRows) {
-        store_cache<T, STORE>(p, kind == 2, blk, off, h, ca, cb, x, raw, on,
-                              kind == 2 ? vs : ks);
-      }
+      };
+    };
+    using Q = std::integral_constant<int, 0>;
+    using K = std::integral_constant<int, 1>;
+    using V = std::integral_constant<int, 2>;
+    const T* qt = static_cast<const T*>(p.q) + t * p.q_st;
+    const T* kt = static_cast<const T*>(p.k) + t * p.k_st;
+    rows(Q{}, qt, p.q_sh, p.Hq, static_cast<const T*>(p.q_weight),
+         row_store(static_cast<T*>(p.q_out) + t * p.qo_st, p.qo_sh));
+    if constexpr (STORE == kRopeRows) {
+      rows(K{}, kt, p.k_sh, p.Hkv, static_cast<const T*>(p.k_weight),
+           row_store(static_cast<T*>(p.k_out) + t * p.ko_st, p.ko_sh));
+    } else if (slot >= 0) {
+      rows(K{}, kt, p.k_sh, p.Hkv, static_cast<const T*>(p.k_weight),
+           cache_store(Q{}));
+      rows(V{}, static_cast<const T*>(p.v) + t * p.v_st, p.v_sh, p.Hkv,
+           static_cast<const T*>(nullptr), cache_store(K{}));
     }
   }
 }
@@ -377,10 +485,7 @@ rope_any_kernel(const RopeLaunch p) {
     if constexpr (STORE != kRopeRows) {
       slot = read_slot(p, t, r == 0 && lane == 0);
       if (kind > 0 && slot < 0) continue;
-      if (slot >= 0) {
-        blk = slot / p.BS;
-        off = slot - blk * p.BS;
-      }
+      if (slot >= 0) split_slot(slot, p.BS, &blk, &off);
     }
     const T* src = static_cast<const T*>(kind == 0   ? p.q
                                          : kind == 1 ? p.k
@@ -468,7 +573,7 @@ rope_any_kernel(const RopeLaunch p) {
         float top = 0.f;
         for (int e = 0; e < 16; ++e)
           top = max_nan(top, fabsf(ready[16 * g + e]));
-        const Fp4Scale s = fp4_scale(top, scale);
+        const Fp4Scale s = fp4_scale(top, scale, fp4_sixth(scale));
         for (int e = 0; e < 2; ++e) {
           const uint32_t codes = fp4_codes8(ready + 16 * g + 8 * e, s.inv);
           for (int b = 0; b < 4; ++b)
