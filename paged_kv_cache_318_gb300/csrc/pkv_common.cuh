@@ -436,6 +436,7 @@ struct RopeLaunch {
   const void *q_weight, *k_weight;  // [D], used when `norm` is set
   int norm;
   float eps, weight_offset;
+  float one;                        // 1 (set by the launch)
   unsigned* err;
 };
 cudaError_t launch_rope(const RopeLaunch& p, RopeStore store, bool bf16,
@@ -663,6 +664,11 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   uint64_t r;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
 }
 // Eight 16-bit values of a 16-byte load, widened.

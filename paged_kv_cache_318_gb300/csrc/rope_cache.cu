@@ -113,16 +113,23 @@ __device__ __forceinline__ void table_run(const RopeLaunch& p, int64_t pos,
   }
 }
 
-// Sum of squares of four pairs, neighbours first.
-__device__ __forceinline__ float sum8_pairwise(const uint64_t* x) {
-  float s[4];
+// Sums of squares of the four pairs of A and of B, neighbours first.
+__device__ __forceinline__ uint64_t squares(const uint64_t* x) {
+  uint64_t s[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    float a, b;
-    unpair(mul2(x[i], x[i]), a, b);
-    s[i] = __fadd_rn(a, b);
+    float a0, a1, b0, b1;
+    unpair(mul2(x[i], x[i]), a0, a1);
+    unpair(mul2(x[4 + i], x[4 + i]), b0, b1);
+    s[i] = pair(__fadd_rn(a0, a1), __fadd_rn(b0, b1));
   }
-  return __fadd_rn(__fadd_rn(s[0], s[1]), __fadd_rn(s[2], s[3]));
+  return add2(add2(s[0], s[1]), add2(s[2], s[3]));
+}
+__device__ __forceinline__ uint64_t shfl_xor2(uint64_t v, int o) {
+  float a, b;
+  unpair(v, a, b);
+  return pair(__shfl_xor_sync(0xffffffffu, a, o),
+              __shfl_xor_sync(0xffffffffu, b, o));
 }
 
 __device__ __forceinline__ float inv_rms(float sum, int D, float eps) {
@@ -181,41 +188,55 @@ __device__ __forceinline__ Fp8Scale fp8_scale(float scale) {
   s.limit = scale >= 0x1p-60f && scale <= 0x1p60f ? 480.f * scale : -1.f;
   return s;
 }
-__device__ __forceinline__ float quotient(float x, const Fp8Scale& s) {
-  asm("min.NaN.f32 %0, %0, %1;" : "+f"(x) : "f"(s.limit));
-  asm("max.NaN.f32 %0, %0, %1;" : "+f"(x) : "f"(-s.limit));
-  const float q = __fmul_rn(x, s.inv);
-  return __fmaf_rn(__fmaf_rn(-q, s.scale, x), s.inv, q);
+__device__ __forceinline__ uint64_t quotients(float x0, float x1,
+                                              const Fp8Scale& s) {
+  asm("min.NaN.f32 %0, %0, %1;" : "+f"(x0) : "f"(s.limit));
+  asm("max.NaN.f32 %0, %0, %1;" : "+f"(x0) : "f"(-s.limit));
+  asm("min.NaN.f32 %0, %0, %1;" : "+f"(x1) : "f"(s.limit));
+  asm("max.NaN.f32 %0, %0, %1;" : "+f"(x1) : "f"(-s.limit));
+  const uint64_t x = pair(x0, x1), y = pair(s.inv, s.inv);
+  const uint64_t q = mul2(x, y);
+  return fma2(fma2(q, pair(-s.scale, -s.scale), x), y, q);
 }
 __device__ __forceinline__ uint32_t e4m3_codes4(const float* x,
                                                 const Fp8Scale& s) {
   if (s.limit < 0.f) return e4m3_codes4(x, s.scale);
+  float q[4];
+  unpair(quotients(x[0], x[1], s), q[0], q[1]);
+  unpair(quotients(x[2], x[3], s), q[2], q[3]);
   uint16_t lo, hi;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo)
-      : "f"(quotient(x[1], s)), "f"(quotient(x[0], s)));
+      : "f"(q[1]), "f"(q[0]));
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi)
-      : "f"(quotient(x[3], s)), "f"(quotient(x[2], s)));
+      : "f"(q[3]), "f"(q[2]));
   return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
 }
 
-template <typename T, int D, int STORE, bool NEOX>
+// How the pairs lie: (i, i + D / 2) over the whole row, (i, i + rot / 2) over
+// a part of it, or neighbours.
+enum { kWhole = 0, kPart = 1, kNeighbours = 2 };
+
+template <typename T, int D, int STORE, int PAIRS>
 __global__ void __launch_bounds__(kThreads, 5)
 rope_kernel(const RopeLaunch p, int parts) {
   // an attention kernel queued next as a programmatic dependent may become
   // resident now (it waits for this grid before reading what this writes)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  constexpr bool NEOX = PAIRS != kNeighbours;
   constexpr int LPR = D / 16;             // lanes of a row
   constexpr int RPW = 32 / LPR;           // rows of a pass
   const int lane = threadIdx.x & 31;
   const int j = lane % LPR, sub = lane / LPR;
   // chunk numbers: inside each block of `span` values, A is in the first
   // half and B at the same place of the second
-  const int span = NEOX ? p.rot : D;
+  const int span = PAIRS == kPart ? p.rot : D;
   const int nb = span / 16;               // lanes of a span
   const int blk0 = j / nb;
   const int ca = blk0 * (span / 8) + (j - blk0 * nb), cb = ca + nb;
-  const bool rot_a = 8 * ca < p.rot, rot_b = 8 * cb < p.rot;
-  const int half = p.rot / 2;
+  const bool rot_a = PAIRS == kWhole || 8 * ca < p.rot;
+  const bool rot_b = PAIRS == kWhole || 8 * cb < p.rot;
+  const int half = PAIRS == kWhole ? D / 2 : p.rot / 2;
+  const uint64_t one2 = pair(p.one, p.one), minus2 = pair(-p.one, -p.one);
   // the lane's first pair of each four (adjacent pairs) or of the eight
   const int ia = NEOX ? 8 * ca : 4 * ca, ib = NEOX ? ia + 4 : 4 * cb;
   const int64_t work = p.num_tokens * parts;
@@ -225,6 +246,15 @@ rope_kernel(const RopeLaunch p, int parts) {
        w < work; w += step) {
     const int64_t t = parts == 1 ? w : w / parts;
     const int part = parts == 1 ? 0 : static_cast<int>(w - t * parts);
+    const T* qt = static_cast<const T*>(p.q) + t * p.q_st;
+    const T* kt = static_cast<const T*>(p.k) + t * p.k_st;
+    // the first query rows do not wait for the token's position
+    uint4 first[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+    if (part * RPW + sub < p.Hq) {
+      const T* at = qt + static_cast<int64_t>(part * RPW + sub) * p.q_sh;
+      first[0] = *reinterpret_cast<const uint4*>(at + 8 * ca);
+      first[1] = *reinterpret_cast<const uint4*>(at + 8 * cb);
+    }
     int64_t slot = -1, blk = 0, off = 0;
     if constexpr (STORE != kRopeRows)
       slot = read_slot(p, t, part == 0 && lane == 0);
@@ -294,17 +324,23 @@ rope_kernel(const RopeLaunch p, int parts) {
       }
       before += n;
       if (i >= n) return;
-      const T* at = src + static_cast<int64_t>(i * RPW + sub) * sh;
       const int64_t hop = static_cast<int64_t>(parts) * RPW * sh;
-      uint4 raw[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+      const T* at_a = src + static_cast<int64_t>(i * RPW + sub) * sh + 8 * ca;
+      const T* at_b = at_a + 8 * (cb - ca);
+      uint4 raw[2];
       auto load = [&](int h) {
+        raw[0] = raw[1] = make_uint4(0, 0, 0, 0);
         if (h < H) {
-          raw[0] = *reinterpret_cast<const uint4*>(at + 8 * ca);
-          raw[1] = *reinterpret_cast<const uint4*>(at + 8 * cb);
+          raw[0] = *reinterpret_cast<const uint4*>(at_a);
+          raw[1] = *reinterpret_cast<const uint4*>(at_b);
         }
-        at += hop;
       };
-      load(i * RPW + sub);
+      if constexpr (kind == 0) {
+        raw[0] = first[0];
+        raw[1] = first[1];
+      } else {
+        load(i * RPW + sub);
+      }
       uint64_t wv[8];
       if (kind < 2 && p.norm) {
         widen8<T>(__ldg(reinterpret_cast<const uint4*>(weight + 8 * ca)), wv);
@@ -317,21 +353,29 @@ rope_kernel(const RopeLaunch p, int parts) {
       for (; i < n; i += parts) {
         const int h = i * RPW + sub;
         const uint4 now[2] = {raw[0], raw[1]};
+        at_a += hop;
+        at_b += hop;
         if (i + parts < n) load(h + parts * RPW);
         uint64_t x[8];
         widen8<T>(now[0], x);
         widen8<T>(now[1], x + 4);
         if (kind < 2) {
           if (p.norm) {
-            float sa = sum8_pairwise(x), sb = sum8_pairwise(x + 4);
+            uint64_t ab = squares(x);
+            float sa, sb;
             // neighbours first: lanes of the span, then A with B, then spans
-            for (int o = 1; o < nb; o *= 2) {
-              sa = __fadd_rn(sa, __shfl_xor_sync(0xffffffffu, sa, o));
-              sb = __fadd_rn(sb, __shfl_xor_sync(0xffffffffu, sb, o));
+            if (PAIRS != kPart) {
+#pragma unroll
+              for (int o = 1; o < LPR; o *= 2) ab = add2(ab, shfl_xor2(ab, o));
+              unpair(ab, sa, sb);
+              sa = __fadd_rn(sa, sb);
+            } else {
+              for (int o = 1; o < nb; o *= 2) ab = add2(ab, shfl_xor2(ab, o));
+              unpair(ab, sa, sb);
+              sa = __fadd_rn(sa, sb);
+              for (int o = nb; o < LPR; o *= 2)
+                sa = __fadd_rn(sa, __shfl_xor_sync(0xffffffffu, sa, o));
             }
-            sa = __fadd_rn(sa, sb);
-            for (int o = nb; o < LPR; o *= 2)
-              sa = __fadd_rn(sa, __shfl_xor_sync(0xffffffffu, sa, o));
             // (D is a power of two: the product is the quotient)
             const float r = __frcp_rn(__fsqrt_rn(
                 __fadd_rn(__fmul_rn(sa, 1.f / D), p.eps)));
@@ -343,16 +387,12 @@ rope_kernel(const RopeLaunch p, int parts) {
             if (rot_a) {
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
-                // (packed products, but single sums: the assembler turns a
-                // packed sum of products into a fused multiply-add)
-                float ac[2], bs[2], bc[2], as[2];
-                unpair(mul2(x[e], c[e]), ac[0], ac[1]);
-                unpair(mul2(x[4 + e], s[e]), bs[0], bs[1]);
-                unpair(mul2(x[4 + e], c[e]), bc[0], bc[1]);
-                unpair(mul2(x[e], s[e]), as[0], as[1]);
-                x[e] = pair(__fsub_rn(ac[0], bs[0]), __fsub_rn(ac[1], bs[1]));
-                x[4 + e] = pair(__fadd_rn(bc[0], as[0]),
-                                __fadd_rn(bc[1], as[1]));
+                // (the sums as x 1 + y, with a 1 that is not known here: a
+                // packed sum of products would come out as one fused
+                // multiply-add)
+                const uint64_t a = x[e], b = x[4 + e];
+                x[e] = fma2(mul2(b, s[e]), minus2, mul2(a, c[e]));
+                x[4 + e] = fma2(mul2(b, c[e]), one2, mul2(a, s[e]));
               }
             }
           } else {
@@ -440,8 +480,6 @@ rope_kernel(const RopeLaunch p, int parts) {
     using Q = std::integral_constant<int, 0>;
     using K = std::integral_constant<int, 1>;
     using V = std::integral_constant<int, 2>;
-    const T* qt = static_cast<const T*>(p.q) + t * p.q_st;
-    const T* kt = static_cast<const T*>(p.k) + t * p.k_st;
     rows(Q{}, qt, p.q_sh, p.Hq, static_cast<const T*>(p.q_weight),
          row_store(static_cast<T*>(p.q_out) + t * p.qo_st, p.qo_sh));
     if constexpr (STORE == kRopeRows) {
@@ -635,12 +673,15 @@ cudaError_t launch_chunks(const RopeLaunch& p, cudaStream_t stream) {
   const int64_t cap = static_cast<int64_t>(current_sm_count()) * 64;
   const unsigned grid = static_cast<unsigned>(blocks < cap ? blocks : cap);
   note_launch();
-  if (p.neox)
-    rope_kernel<T, D, STORE, true><<<grid, kThreads, 0, stream>>>(
-        p, static_cast<int>(parts));
+  auto go = [&](auto kern) {
+    kern<<<grid, kThreads, 0, stream>>>(p, static_cast<int>(parts));
+  };
+  if (!p.neox)
+    go(rope_kernel<T, D, STORE, kNeighbours>);
+  else if (p.rot == D)
+    go(rope_kernel<T, D, STORE, kWhole>);
   else
-    rope_kernel<T, D, STORE, false><<<grid, kThreads, 0, stream>>>(
-        p, static_cast<int>(parts));
+    go(rope_kernel<T, D, STORE, kPart>);
   return cudaGetLastError();
 }
 
@@ -677,9 +718,11 @@ cudaError_t launch_type(const RopeLaunch& p, RopeStore store,
 
 }  // namespace
 
-cudaError_t launch_rope(const RopeLaunch& p, RopeStore store, bool bf16,
+cudaError_t launch_rope(const RopeLaunch& launch, RopeStore store, bool bf16,
                         cudaStream_t stream) {
-  if (p.num_tokens == 0) return cudaSuccess;
+  if (launch.num_tokens == 0) return cudaSuccess;
+  RopeLaunch p = launch;
+  p.one = 1.f;
   return bf16 ? launch_type<__nv_bfloat16>(p, store, stream)
               : launch_type<__half>(p, store, stream);
 }
