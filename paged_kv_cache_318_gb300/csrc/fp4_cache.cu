@@ -77,8 +77,9 @@ cache_write_fp4_kernel(const T* __restrict__ key, const T* __restrict__ value,
                        uint8_t* __restrict__ k_sf, uint8_t* __restrict__ v_sf,
                        int64_t f_sb, int64_t f_sr, int64_t f_sh,
                        const int64_t* __restrict__ slots, int64_t num_tokens,
-                       int groups, int per_token, int tokens_per_block,
-                       int BS, int64_t num_slots,
+                       int groups, int group_shift, int per_token,
+                       int tokens_per_block, int BS, int bs_shift,
+                       int64_t num_slots,
                        const float* __restrict__ k_scale,
                        const float* __restrict__ v_scale, unsigned* err) {
   // an attention kernel queued next as a programmatic dependent may become
@@ -95,7 +96,8 @@ cache_write_fp4_kernel(const T* __restrict__ key, const T* __restrict__ value,
     const int64_t s = __ldg(slots + t);
     int64_t blk = 0, off = 0;
     for (int r = r0; r < per_token; r += kThreads) {
-      const int h = r / groups, g = r - h * groups;
+      const int h = group_shift >= 0 ? r >> group_shift : r / groups;
+      const int g = r - h * groups;
       // (the rows do not wait for the slot)
       const uint4* kp =
           reinterpret_cast<const uint4*>(key + t * k_st + h * k_sh + g * 16);
@@ -107,7 +109,7 @@ cache_write_fp4_kernel(const T* __restrict__ key, const T* __restrict__ value,
         if (r == 0) atomicOr(err, kErrBadSlot);
         break;
       }
-      if (r == r0) split_slot(s, BS, &blk, &off);
+      if (r == r0) split_slot(s, BS, bs_shift, &blk, &off);
       const int64_t c = blk * c_sb + off * c_sr + h * c_sh + g * 8;
       const int64_t f = blk * f_sb + off * f_sr + h * f_sh + g;
       quantize16<T>(k0, k1, ks, ks6, kc + c, k_sf + f);
@@ -221,8 +223,8 @@ cudaError_t launch_cache_write_fp4(
     kern<<<grid, kThreads, 0, stream>>>(
         k, v, k_st, k_sh, v_st, v_sh, static_cast<uint8_t*>(kc),
         static_cast<uint8_t*>(vc), cs[0], cs[1], cs[2], k_sf, v_sf, fs[0],
-        fs[1], fs[2], slots, num_tokens, groups, per_token, tpb, BS,
-        num_blocks * BS, k_scale, v_scale, err);
+        fs[1], fs[2], slots, num_tokens, groups, shift_of(groups), per_token,
+        tpb, BS, shift_of(BS), num_blocks * BS, k_scale, v_scale, err);
   };
   if (bf16)
     go(cache_write_fp4_kernel<__nv_bfloat16>,

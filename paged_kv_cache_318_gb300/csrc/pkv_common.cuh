@@ -422,7 +422,7 @@ struct RopeLaunch {
   int64_t f_sb, f_sr, f_sh;
   const int64_t* slots;
   int64_t num_slots;
-  int BS;
+  int BS, bs_shift;                 // (bs_shift is set by the launch)
   const float *k_scale, *v_scale;
   int64_t num_tokens;
   int Hq, Hkv, D, rot, neox;
@@ -539,6 +539,14 @@ __device__ __forceinline__ uint32_t lds32(uint32_t a) {
   return v;
 }
 
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a));
+  return v;
+}
+
 template <typename T>
 __device__ __forceinline__ float elem_f32(uint32_t w, int hi);
 template <>
@@ -552,6 +560,31 @@ __device__ __forceinline__ float elem_f32<__half>(uint32_t w, int hi) {
       static_cast<unsigned short>(hi ? (w >> 16) : (w & 0xffffu))));
 }
 
+// Two float32 values as one operand of the packed instructions.  (add2 of a
+// mul2 may come out as one fused multiply-add.)
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
 // ---- 4-bit caches: E2M1 codes and E4M3 block scales
 
 // Eight E2M1 codes (lowest nibble first) -> four f16x2 (exact).
@@ -620,7 +653,8 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 __device__ __forceinline__ uint32_t fp4_codes8(const float* x, float inv) {
   float y[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) y[i] = __fmul_rn(x[i], inv);
+  for (int i = 0; i < 8; i += 2)
+    unpair(mul2(pair(x[i], x[i + 1]), pair(inv, inv)), y[i], y[i + 1]);
   uint32_t r;
   asm("{\n.reg .b8 a, b, c, d;\n"
       "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n"
@@ -634,10 +668,19 @@ __device__ __forceinline__ uint32_t fp4_codes8(const float* x, float inv) {
   return r;
 }
 
-// Cache block and row of a slot.
-__device__ __forceinline__ void split_slot(int64_t slot, int BS, int64_t* blk,
-                                           int64_t* row) {
-  if ((slot >> 31) == 0) {               // (a 32-bit division)
+// log2 of a power of two, else -1.
+inline int shift_of(int n) {
+  int s = 0;
+  while ((1 << s) < n && s < 30) ++s;
+  return (1 << s) == n ? s : -1;
+}
+
+// Cache block and row of a slot (shift: shift_of(BS)).
+__device__ __forceinline__ void split_slot(int64_t slot, int BS, int shift,
+                                           int64_t* blk, int64_t* row) {
+  if (shift >= 0) {
+    *blk = slot >> shift;
+  } else if ((slot >> 31) == 0) {        // (a 32-bit division)
     const uint32_t s = static_cast<uint32_t>(slot);
     *blk = s / static_cast<uint32_t>(BS);
   } else {
@@ -646,31 +689,6 @@ __device__ __forceinline__ void split_slot(int64_t slot, int BS, int64_t* blk,
   *row = slot - *blk * BS;
 }
 
-// Two float32 values as one operand of the packed instructions.  (add2 of a
-// mul2 may come out as one fused multiply-add.)
-__device__ __forceinline__ uint64_t pair(float a, float b) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ void unpair(uint64_t v, float& a, float& b) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
 // Eight 16-bit values of a 16-byte load, widened.
 template <typename T>
 __device__ __forceinline__ void widen8(const uint4& raw, float* x) {

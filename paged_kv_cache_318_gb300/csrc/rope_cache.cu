@@ -35,6 +35,7 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kMaxD = 512;
+constexpr int kDepth = 2;        // passes on their way to a warp
 
 // Axis whose position rotates pair i.
 __device__ __forceinline__ int pair_axis(const RopeLaunch& p, int i) {
@@ -239,28 +240,47 @@ rope_kernel(const RopeLaunch p, int parts) {
   const uint64_t one2 = pair(p.one, p.one), minus2 = pair(-p.one, -p.one);
   // the lane's first pair of each four (adjacent pairs) or of the eight
   const int ia = NEOX ? 8 * ca : 4 * ca, ib = NEOX ? ia + 4 : 4 * cb;
+  const int pq = (p.Hq + RPW - 1) / RPW, pk = (p.Hkv + RPW - 1) / RPW;
+  const int passes = pq + (STORE == kRopeRows ? pk : 2 * pk);
+  __shared__ uint4 places[kDepth * 2 * kThreads];
+  const uint32_t mine = smem_u32(places + threadIdx.x);
   const int64_t work = p.num_tokens * parts;
   const int64_t step = static_cast<int64_t>(gridDim.x) * (kThreads / 32);
   for (int64_t w = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) +
                    (threadIdx.x >> 5);
        w < work; w += step) {
+    cp_async_wait<0>();                   // (of a token that was skipped)
     const int64_t t = parts == 1 ? w : w / parts;
     const int part = parts == 1 ? 0 : static_cast<int>(w - t * parts);
-    const T* qt = static_cast<const T*>(p.q) + t * p.q_st;
-    const T* kt = static_cast<const T*>(p.k) + t * p.k_st;
-    // the first query rows do not wait for the token's position
-    uint4 first[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-    if (part * RPW + sub < p.Hq) {
-      const T* at = qt + static_cast<int64_t>(part * RPW + sub) * p.q_sh;
-      first[0] = *reinterpret_cast<const uint4*>(at + 8 * ca);
-      first[1] = *reinterpret_cast<const uint4*>(at + 8 * cb);
-    }
+    // The token's passes part, part + parts, ... in the order q, k, v; every
+    // thread copies its own chunks of the next kDepth ones to its own places
+    // in shared memory (nothing of them waits for the position or the slot).
+    auto issue = [&](int i) {
+      const int g = part + i * parts;
+      if (g < passes) {
+        const int kind = g < pq ? 0 : g < pq + pk ? 1 : 2;
+        const int h = (kind == 0 ? g : kind == 1 ? g - pq : g - pq - pk) * RPW +
+                      sub;
+        const bool on = h < (kind == 0 ? p.Hq : p.Hkv);
+        const int64_t st = kind == 0 ? p.q_st : kind == 1 ? p.k_st : p.v_st;
+        const int64_t sh = kind == 0 ? p.q_sh : kind == 1 ? p.k_sh : p.v_sh;
+        const T* src =
+            static_cast<const T*>(kind == 0 ? p.q : kind == 1 ? p.k : p.v) +
+            t * st + (on ? h * sh : 0);
+        const uint32_t dst = mine + (i % kDepth) * (kThreads * 32);
+        cp_async_16(dst, src + 8 * ca, on ? 16 : 0);
+        cp_async_16(dst + kThreads * 16, src + 8 * cb, on ? 16 : 0);
+      }
+      cp_async_commit();
+    };
+    for (int i = 0; i < kDepth; ++i) issue(i);
+    int done = 0;                         // passes worked on
     int64_t slot = -1, blk = 0, off = 0;
     if constexpr (STORE != kRopeRows)
       slot = read_slot(p, t, part == 0 && lane == 0);
     int64_t pos[4] = {0, 0, 0, 0};
     if (!read_positions(p, t, part == 0 && lane == 0, pos)) continue;
-    if (STORE != kRopeRows && slot >= 0) split_slot(slot, p.BS, &blk, &off);
+    if (STORE != kRopeRows && slot >= 0) split_slot(slot, p.BS, p.bs_shift, &blk, &off);
     // cos and sin of the lane's eight pairs, two to an operand
     uint64_t c[4], s[4];
     {
@@ -310,37 +330,14 @@ rope_kernel(const RopeLaunch p, int parts) {
       }
     }
 
-    // The passes of one kind of row (q, k or v), `parts` apart.  The next
-    // pass's rows load while this one's are worked on.
+    // The passes of one kind of row (q, k or v).
     int before = 0;                       // passes of the kinds before
-    auto rows = [&](auto kind_tag, const T* src, int64_t sh, int H,
-                    const T* weight, auto&& store) {
+    auto rows = [&](auto kind_tag, int H, const T* weight, auto&& store) {
       constexpr int kind = decltype(kind_tag)::value;
       const int n = (H + RPW - 1) / RPW;
-      int i = 0;
-      if (parts > 1) {
-        i = part - before % parts;
-        if (i < 0) i += parts;
-      }
+      int i = part + done * parts - before;
       before += n;
       if (i >= n) return;
-      const int64_t hop = static_cast<int64_t>(parts) * RPW * sh;
-      const T* at_a = src + static_cast<int64_t>(i * RPW + sub) * sh + 8 * ca;
-      const T* at_b = at_a + 8 * (cb - ca);
-      uint4 raw[2];
-      auto load = [&](int h) {
-        raw[0] = raw[1] = make_uint4(0, 0, 0, 0);
-        if (h < H) {
-          raw[0] = *reinterpret_cast<const uint4*>(at_a);
-          raw[1] = *reinterpret_cast<const uint4*>(at_b);
-        }
-      };
-      if constexpr (kind == 0) {
-        raw[0] = first[0];
-        raw[1] = first[1];
-      } else {
-        load(i * RPW + sub);
-      }
       uint64_t wv[8];
       if (kind < 2 && p.norm) {
         widen8<T>(__ldg(reinterpret_cast<const uint4*>(weight + 8 * ca)), wv);
@@ -352,10 +349,11 @@ rope_kernel(const RopeLaunch p, int parts) {
       }
       for (; i < n; i += parts) {
         const int h = i * RPW + sub;
-        const uint4 now[2] = {raw[0], raw[1]};
-        at_a += hop;
-        at_b += hop;
-        if (i + parts < n) load(h + parts * RPW);
+        cp_async_wait<kDepth - 1>();
+        const uint32_t place = mine + (done % kDepth) * (kThreads * 32);
+        const uint4 now[2] = {lds128(place), lds128(place + kThreads * 16)};
+        issue(done + kDepth);
+        ++done;
         uint64_t x[8];
         widen8<T>(now[0], x);
         widen8<T>(now[1], x + 4);
@@ -480,16 +478,15 @@ rope_kernel(const RopeLaunch p, int parts) {
     using Q = std::integral_constant<int, 0>;
     using K = std::integral_constant<int, 1>;
     using V = std::integral_constant<int, 2>;
-    rows(Q{}, qt, p.q_sh, p.Hq, static_cast<const T*>(p.q_weight),
+    rows(Q{}, p.Hq, static_cast<const T*>(p.q_weight),
          row_store(static_cast<T*>(p.q_out) + t * p.qo_st, p.qo_sh));
     if constexpr (STORE == kRopeRows) {
-      rows(K{}, kt, p.k_sh, p.Hkv, static_cast<const T*>(p.k_weight),
+      rows(K{}, p.Hkv, static_cast<const T*>(p.k_weight),
            row_store(static_cast<T*>(p.k_out) + t * p.ko_st, p.ko_sh));
     } else if (slot >= 0) {
-      rows(K{}, kt, p.k_sh, p.Hkv, static_cast<const T*>(p.k_weight),
+      rows(K{}, p.Hkv, static_cast<const T*>(p.k_weight),
            cache_store(Q{}));
-      rows(V{}, static_cast<const T*>(p.v) + t * p.v_st, p.v_sh, p.Hkv,
-           static_cast<const T*>(nullptr), cache_store(K{}));
+      rows(V{}, p.Hkv, static_cast<const T*>(nullptr), cache_store(K{}));
     }
   }
 }
@@ -523,7 +520,7 @@ rope_any_kernel(const RopeLaunch p) {
     if constexpr (STORE != kRopeRows) {
       slot = read_slot(p, t, r == 0 && lane == 0);
       if (kind > 0 && slot < 0) continue;
-      if (slot >= 0) split_slot(slot, p.BS, &blk, &off);
+      if (slot >= 0) split_slot(slot, p.BS, p.bs_shift, &blk, &off);
     }
     const T* src = static_cast<const T*>(kind == 0   ? p.q
                                          : kind == 1 ? p.k
@@ -723,6 +720,7 @@ cudaError_t launch_rope(const RopeLaunch& launch, RopeStore store, bool bf16,
   if (launch.num_tokens == 0) return cudaSuccess;
   RopeLaunch p = launch;
   p.one = 1.f;
+  p.bs_shift = shift_of(p.BS);
   return bf16 ? launch_type<__nv_bfloat16>(p, store, stream)
               : launch_type<__half>(p, store, stream);
 }
