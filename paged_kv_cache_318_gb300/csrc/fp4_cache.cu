@@ -91,30 +91,51 @@ cache_write_fp4_kernel(const T* __restrict__ key, const T* __restrict__ value,
   const float ks = *k_scale, vs = *v_scale;
   const float ks6 = fp4_sixth(ks), vs6 = fp4_sixth(vs);
   const int64_t step = static_cast<int64_t>(gridDim.x) * tokens_per_block;
-  for (int64_t t = static_cast<int64_t>(blockIdx.x) * tokens_per_block + tl;
-       t < num_tokens; t += step) {
-    const int64_t s = __ldg(slots + t);
-    int64_t blk = 0, off = 0;
-    for (int r = r0; r < per_token; r += kThreads) {
-      const int h = group_shift >= 0 ? r >> group_shift : r / groups;
-      const int g = r - h * groups;
-      // (the rows do not wait for the slot)
-      const uint4* kp =
-          reinterpret_cast<const uint4*>(key + t * k_st + h * k_sh + g * 16);
-      const uint4* vp =
-          reinterpret_cast<const uint4*>(value + t * v_st + h * v_sh + g * 16);
-      const uint4 k0 = kp[0], k1 = kp[1], v0 = vp[0], v1 = vp[1];
-      if (s < 0) break;                           // padding slot
-      if (s >= num_slots) {                       // outside the cache: skip
-        if (r == 0) atomicOr(err, kErrBadSlot);
-        break;
-      }
-      if (r == r0) split_slot(s, BS, bs_shift, &blk, &off);
-      const int64_t c = blk * c_sb + off * c_sr + h * c_sh + g * 8;
-      const int64_t f = blk * f_sb + off * f_sr + h * f_sh + g;
-      quantize16<T>(k0, k1, ks, ks6, kc + c, k_sf + f);
-      quantize16<T>(v0, v1, vs, vs6, vc + c, v_sf + f);
+  int64_t t = static_cast<int64_t>(blockIdx.x) * tokens_per_block + tl;
+  // the next item's rows and slot load while this one's are worked on (and
+  // the rows do not wait for the slot)
+  struct Item {
+    uint4 k0, k1, v0, v1;
+    int64_t slot;
+  };
+  auto load = [&](int64_t tok, int r, Item& x) {
+    const int h = group_shift >= 0 ? r >> group_shift : r / groups;
+    const int g = r - h * groups;
+    const uint4* kp =
+        reinterpret_cast<const uint4*>(key + tok * k_st + h * k_sh + g * 16);
+    const uint4* vp =
+        reinterpret_cast<const uint4*>(value + tok * v_st + h * v_sh + g * 16);
+    x.slot = __ldg(slots + tok);
+    x.k0 = kp[0];
+    x.k1 = kp[1];
+    x.v0 = vp[0];
+    x.v1 = vp[1];
+  };
+  int r = r0;
+  Item x;
+  if (t < num_tokens) load(t, r, x);
+  while (t < num_tokens) {
+    const Item now = x;
+    const int r_now = r;
+    r += kThreads;                                // (a large token's rest)
+    if (r >= per_token) {
+      r = r0;
+      t += step;
     }
+    if (t < num_tokens) load(t, r, x);
+    if (now.slot < 0) continue;                   // padding slot
+    if (now.slot >= num_slots) {                  // outside the cache: skip
+      if (r_now == 0) atomicOr(err, kErrBadSlot);
+      continue;
+    }
+    int64_t blk, off;
+    split_slot(now.slot, BS, bs_shift, &blk, &off);
+    const int h = group_shift >= 0 ? r_now >> group_shift : r_now / groups;
+    const int g = r_now - h * groups;
+    const int64_t c = blk * c_sb + off * c_sr + h * c_sh + g * 8;
+    const int64_t f = blk * f_sb + off * f_sr + h * f_sh + g;
+    quantize16<T>(now.k0, now.k1, ks, ks6, kc + c, k_sf + f);
+    quantize16<T>(now.v0, now.v1, vs, vs6, vc + c, v_sf + f);
   }
 }
 
@@ -217,7 +238,7 @@ cudaError_t launch_cache_write_fp4(
     cudaStream_t stream) {
   const int groups = D / 16, per_token = Hkv * groups;
   const int tpb = per_token >= kThreads ? 1 : kThreads / per_token;
-  const unsigned grid = capped_grid((num_tokens + tpb - 1) / tpb, 32);
+  const unsigned grid = capped_grid((num_tokens + tpb - 1) / tpb, 3);
   note_launch();
   auto go = [&](auto kern, const auto* k, const auto* v) {
     kern<<<grid, kThreads, 0, stream>>>(
