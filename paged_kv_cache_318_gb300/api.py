@@ -19,6 +19,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 from typing import Optional, Tuple
 
@@ -54,30 +55,16 @@ class _Options(ctypes.Structure):
                 ("q_scale", ctypes.c_void_p), ("no_pdl", ctypes.c_int)]
 
 
-class _Fp4Scales(ctypes.Structure):
-    """pkv_fp4_scales (include/pkv.h)."""
-    _fields_ = [("k_block_scale", ctypes.c_void_p),
-                ("v_block_scale", ctypes.c_void_p),
-                ("strides", ctypes.c_int64 * 4),
-                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p)]
-
-
-class _RopeParams(ctypes.Structure):
-    """pkv_rope_params (include/pkv.h)."""
-    _fields_ = [("positions", ctypes.c_void_p),
-                ("position_axis_stride", ctypes.c_int64),
-                ("num_axes", ctypes.c_int),
-                ("interleaved_axes", ctypes.c_int),
-                ("sections", ctypes.c_int * 4), ("cos_sin", ctypes.c_void_p),
-                ("cos_sin_stride", ctypes.c_int64),
-                ("max_position", ctypes.c_int64),
-                ("cos_sin_f32", ctypes.c_int), ("rot_dim", ctypes.c_int),
-                ("is_neox", ctypes.c_int), ("q_weight", ctypes.c_void_p),
-                ("k_weight", ctypes.c_void_p), ("eps", ctypes.c_float),
-                ("weight_offset", ctypes.c_float)]
-
+# pkv_fp4_scales and pkv_rope_params (include/pkv.h) as bytes, and a row of
+# four strides: arguments of one call, not kept.
+_PACK_FP4 = struct.Struct("@PP4qPP").pack
+_PACK_ROPE = struct.Struct("@Pqii4iPqqiiiPPff").pack
+_PACK_4 = struct.Struct("@4q").pack
 
 _FP8_CACHE = (torch.float8_e4m3fn, torch.uint8)
+
+
+_NO_SIZE = ctypes.c_size_t(-1).value     # a workspace size's error value
 
 
 class PkvError(RuntimeError):
@@ -146,24 +133,24 @@ def load_library():
                                              i32, vp]
         lib.pkv_reshape_and_cache_fp4.restype = i32
         lib.pkv_reshape_and_cache_fp4.argtypes = [
-            vp, vp, i64, i64, i64, i64, vp, vp, c_i64p, vp, vp, i64, i32, i32,
+            vp, vp, i64, i64, i64, i64, vp, vp, vp, vp, vp, i64, i32, i32,
             i32, i64, i32, vp]
         lib.pkv_dequantize_fp4_cache.restype = i32
         lib.pkv_dequantize_fp4_cache.argtypes = [
-            vp, c_i64p, vp, c_i64p, vp, vp, i64, i32, i32, i32, i64, vp, i32,
-            vp]
+            vp, vp, vp, vp, vp, vp, i64, i32, i32, i32, i64, vp, i32, vp]
         lib.pkv_paged_attention_workspace_size_fp4.restype = sz
         lib.pkv_paged_attention_workspace_size_fp4.argtypes = \
             lib.pkv_paged_attention_workspace_size_opts.argtypes
         lib.pkv_paged_attention_varlen_fp4.restype = i32
         at = lib.pkv_paged_attention_varlen_opts.argtypes
-        lib.pkv_paged_attention_varlen_fp4.argtypes = at[:6] + [vp] + at[6:]
+        lib.pkv_paged_attention_varlen_fp4.argtypes = \
+            at[:5] + [vp, vp] + at[6:]
         lib.pkv_qk_norm_rope.restype = i32
         lib.pkv_qk_norm_rope.argtypes = [vp, i64, i64] * 4 + [
             i64, i32, i32, i32, vp, i32, vp]
         lib.pkv_rope_reshape_and_cache.restype = i32
         lib.pkv_rope_reshape_and_cache.argtypes = [vp, i64, i64] * 4 + [
-            vp, vp, c_i64p, vp, i64, i32, i32, i32, i32, i64, vp, i32,
+            vp, vp, vp, vp, i64, i32, i32, i32, i32, i64, vp, i32,
             ctypes.c_char_p, vp, vp, vp, vp]
         lib.pkv_set_prefill_kernel.restype = i32
         lib.pkv_set_prefill_kernel.argtypes = [i32]
@@ -198,35 +185,29 @@ def _ptr(t: Optional[torch.Tensor]):
     return ctypes.c_void_p(0 if t is None else t.data_ptr())
 
 
-def _on_device(*tensors) -> torch.device:
-    """The one CUDA device that every given tensor (None aside) is on."""
-    dev = None
+def _on_device(*tensors) -> int:
+    """Index of the one CUDA device that every given tensor (None aside) is
+    on."""
+    dev = tensors[0].get_device()
     for t in tensors:
-        if t is None:
-            continue
-        if dev is None:
-            dev = t.device
-            if dev.type != "cuda":
-                raise ValueError("tensors must be on a CUDA device")
-        elif t.device != dev:
+        if t is not None and t.get_device() != dev:
             raise ValueError("tensors must be on one device (%s and %s)" %
-                             (dev, t.device))
+                             (tensors[0].device, t.device))
+    if dev < 0:
+        raise ValueError("tensors must be on a CUDA device")
     return dev
 
 
 def _call(dev, fn, *args):
-    """fn(*args, stream): on `dev` and its current stream; checks the
+    """fn(*args, stream): on device `dev` and its current stream; checks the
     status."""
-    if dev.index == torch.cuda.current_device():
-        _check(fn(*args, torch.cuda.current_stream(dev).cuda_stream))
+    if dev == torch.cuda.current_device():
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
     else:
         with torch.cuda.device(dev):
-            _check(fn(*args, torch.cuda.current_stream(dev).cuda_stream))
-
-
-def _call4(dev, fn, opts, *args):
-    """_call of a function that takes its options after the stream."""
-    _call(dev, lambda *a: fn(*a, ctypes.byref(opts)), *args)
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+    if status:
+        _check(status)
 
 
 def _addr(t: Optional[torch.Tensor]):
@@ -252,37 +233,45 @@ def _cache_strides(key_cache, value_cache):
 
 
 def _scalar(t, what):
-    if t is None or t.dtype != torch.float32 or t.numel() < 1:
+    if t is None or t.dtype is not torch.float32 or t.numel() < 1:
         raise ValueError("%s must be a float32 tensor" % what)
+    return t.data_ptr()
 
 
-def _fp4_scales(key_cache, value_cache, k_block_scale, v_block_scale,
+def _cache_views(key_cache, value_cache):
+    """(shape, strides as bytes) of the two views, which must agree."""
+    shape, strides = key_cache.shape, key_cache.stride()
+    if len(shape) != 4:
+        raise ValueError("cache views must be 4-D [num_blocks, block_size, "
+                         "num_kv_heads, head_size]")
+    if value_cache.shape != shape or value_cache.stride() != strides:
+        raise ValueError("key_cache and value_cache must share shape and "
+                         "strides")
+    return shape, _PACK_4(*strides)
+
+
+def _fp4_scales(key_cache, value_cache, shape, k_block_scale, v_block_scale,
                 k_scale, v_scale):
-    """Check a 4-bit cache's views; (pkv_fp4_scales, head_size)."""
-    NB, BS, H, half = key_cache.shape
-    if key_cache.dtype != torch.uint8 or value_cache.dtype != torch.uint8:
+    """pkv_fp4_scales (as bytes) of a 4-bit cache of this codes' shape."""
+    if key_cache.dtype is not torch.uint8 or \
+            value_cache.dtype is not torch.uint8:
         raise ValueError("a 4-bit cache holds its codes as uint8 "
                          "[num_blocks, block_size, num_kv_heads, "
                          "head_size / 2]")
     if k_block_scale is None or v_block_scale is None:
         raise ValueError("a 4-bit cache needs both block scales")
+    want = (shape[0], shape[1], shape[2], shape[3] // 8)
     for t in (k_block_scale, v_block_scale):
-        if t.dtype not in _FP8_CACHE or \
-                tuple(t.shape) != (NB, BS, H, half // 8):
+        if t.dtype not in _FP8_CACHE or t.shape != want:
             raise ValueError("block scales must be float8_e4m3fn (or uint8) "
                              "[num_blocks, block_size, num_kv_heads, "
                              "head_size / 16]")
-    if k_block_scale.stride() != v_block_scale.stride():
+    strides = k_block_scale.stride()
+    if v_block_scale.stride() != strides:
         raise ValueError("both block scales must share their strides")
-    _scalar(k_scale, "k_scale")
-    _scalar(v_scale, "v_scale")
-    f = _Fp4Scales()
-    f.k_block_scale = k_block_scale.data_ptr()
-    f.v_block_scale = v_block_scale.data_ptr()
-    f.strides = (ctypes.c_int64 * 4)(*k_block_scale.stride())
-    f.k_scale = k_scale.data_ptr()
-    f.v_scale = v_scale.data_ptr()
-    return f, half * 2
+    return _PACK_FP4(k_block_scale.data_ptr(), v_block_scale.data_ptr(),
+                     *strides, _scalar(k_scale, "k_scale"),
+                     _scalar(v_scale, "v_scale"))
 
 
 PREFILL_TCGEN05 = 0
@@ -374,41 +363,45 @@ def reshape_and_cache_flash(key, value, key_cache, value_cache, slot_mapping,
         _stream(key)))
 
 
-def _check_rows(t, what, heads, head_size, tokens):
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != head_size or \
-            t.shape[0] < tokens:
+def _rows(t, what, heads, head_size, tokens):
+    """(address, token stride, head stride) of rows [>= tokens, heads,
+    head_size]."""
+    shape, strides = t.shape, t.stride()
+    if len(shape) != 3 or shape[1] != heads or shape[2] != head_size or \
+            shape[0] < tokens:
         raise ValueError("%s must be [>= %d, %d, %d], not %s" %
-                         (what, tokens, heads, head_size, tuple(t.shape)))
-    if t.stride(2) != 1:
+                         (what, tokens, heads, head_size, tuple(shape)))
+    if strides[2] != 1:
         raise ValueError("%s head_size dim must be contiguous" % what)
+    return t.data_ptr(), strides[0], strides[1]
 
 
-def _check_slots(slot_mapping):
-    if slot_mapping.dtype != torch.int64 or slot_mapping.dim() != 1 or \
-            (slot_mapping.shape[0] > 1 and slot_mapping.stride(0) != 1):
+def _slots(slot_mapping):
+    """Token count of a slot mapping."""
+    shape = slot_mapping.shape
+    if slot_mapping.dtype is not torch.int64 or len(shape) != 1 or \
+            (shape[0] > 1 and slot_mapping.stride(0) != 1):
         raise ValueError("slot_mapping must be a contiguous int64 vector")
+    return shape[0]
 
 
 def _reshape_and_cache_fp4(lib, key, value, key_cache, value_cache,
                            slot_mapping, k_scale, v_scale, k_block_scale,
                            v_block_scale):
-    _check_slots(slot_mapping)
-    cs = _cache_strides(key_cache, value_cache)
-    f, D = _fp4_scales(key_cache, value_cache, k_block_scale, v_block_scale,
-                       k_scale, v_scale)
-    NB, BS, H, _ = key_cache.shape
-    n = slot_mapping.shape[0]
-    _check_rows(key, "key", H, D, n)
-    _check_rows(value, "value", H, D, n)
-    if value.dtype != key.dtype:
+    n = _slots(slot_mapping)
+    shape, cs = _cache_views(key_cache, value_cache)
+    f = _fp4_scales(key_cache, value_cache, shape, k_block_scale,
+                    v_block_scale, k_scale, v_scale)
+    NB, BS, H, half = shape
+    kp, k0, k1 = _rows(key, "key", H, 2 * half, n)
+    vptr, v0, v1 = _rows(value, "value", H, 2 * half, n)
+    if value.dtype is not key.dtype:
         raise ValueError("key and value must share a dtype")
     dev = _on_device(key, value, key_cache, value_cache, slot_mapping,
                      k_scale, v_scale, k_block_scale, v_block_scale)
-    _call(dev, lib.pkv_reshape_and_cache_fp4, key.data_ptr(),
-          value.data_ptr(), key.stride(0), key.stride(1), value.stride(0),
-          value.stride(1), key_cache.data_ptr(), value_cache.data_ptr(), cs,
-          ctypes.byref(f), slot_mapping.data_ptr(), n, H, D, BS, NB,
-          _dtype(key))
+    _call(dev, lib.pkv_reshape_and_cache_fp4, kp, vptr, k0, k1, v0, v1,
+          key_cache.data_ptr(), value_cache.data_ptr(), cs, f,
+          slot_mapping.data_ptr(), n, H, 2 * half, BS, NB, _dtype(key))
 
 
 def fp4_kv_cache(num_blocks, block_size, num_kv_heads, head_size,
@@ -442,56 +435,70 @@ def dequantize_fp4_cache(codes, block_scale, scale, dtype=None, out=None,
     cache give zeros and are flagged (``check_device_errors``).
     """
     lib = load_library()
-    if codes.dim() != 4:
+    shape = codes.shape
+    if len(shape) != 4:
         raise ValueError("codes must be [num_blocks, block_size, "
                          "num_kv_heads, head_size / 2]")
-    f, D = _fp4_scales(codes, codes, block_scale, block_scale, scale, scale)
-    NB, BS, H, _ = codes.shape
+    _fp4_scales(codes, codes, shape, block_scale, block_scale, scale, scale)
+    NB, BS, H, half = shape
+    n = NB
     if block_ids is not None:
-        if block_ids.dtype != torch.int64 or block_ids.dim() != 1 or \
-                (block_ids.shape[0] > 1 and block_ids.stride(0) != 1):
+        n = block_ids.shape[0] if block_ids.dim() == 1 else -1
+        if block_ids.dtype is not torch.int64 or n < 0 or \
+                (n > 1 and block_ids.stride(0) != 1):
             raise ValueError("block_ids must be a contiguous int64 vector")
-    n = NB if block_ids is None else block_ids.shape[0]
     if out is None:
         if dtype is None:
             raise ValueError("dequantize_fp4_cache needs dtype or out")
-        out = torch.empty((n, BS, H, D), dtype=dtype, device=codes.device)
-    elif tuple(out.shape) != (n, BS, H, D) or not out.is_contiguous() or \
+        out = torch.empty((n, BS, H, 2 * half), dtype=dtype,
+                          device=codes.device)
+    elif out.shape != (n, BS, H, 2 * half) or not out.is_contiguous() or \
             (dtype is not None and out.dtype != dtype):
         raise ValueError("out must be contiguous %s of dtype" %
-                         ((n, BS, H, D),))
+                         ((n, BS, H, 2 * half),))
     dt = _dtype(out)
     dev = _on_device(codes, block_scale, scale, out, block_ids)
-    strides = (ctypes.c_int64 * 4)(*codes.stride())
-    _call(dev, lib.pkv_dequantize_fp4_cache, codes.data_ptr(), strides,
-          block_scale.data_ptr(), f.strides, scale.data_ptr(),
-          _addr(block_ids), n, H, D, BS, NB, out.data_ptr(), dt)
+    _call(dev, lib.pkv_dequantize_fp4_cache, codes.data_ptr(),
+          _PACK_4(*codes.stride()), block_scale.data_ptr(),
+          _PACK_4(*block_scale.stride()), scale.data_ptr(),
+          _addr(block_ids), n, H, 2 * half, BS, NB, out.data_ptr(), dt)
     return out
 
 
 # ------------------------------------------------- head norms and rotation
 
-def _rope_params(q, positions, cos_sin_cache, q_weight, k_weight, eps,
+def _rope_params(dtype, positions, cos_sin_cache, q_weight, k_weight, eps,
                  is_neox, mrope_section, mrope_interleaved, weight_offset,
                  tokens, head_size):
-    if positions.dtype != torch.int64 or positions.dim() not in (1, 2) or \
-            (positions.shape[-1] > 1 and positions.stride(-1) != 1):
+    """pkv_rope_params (as bytes)."""
+    shape, strides = positions.shape, positions.stride()
+    axes = shape[0] if len(shape) == 2 else 1
+    if positions.dtype is not torch.int64 or len(shape) not in (1, 2) or \
+            (shape[-1] > 1 and strides[-1] != 1):
         raise ValueError("positions must be int64 [tokens] or [axes, tokens] "
                          "with contiguous rows")
-    if positions.shape[-1] < tokens:
+    if shape[-1] < tokens:
         raise ValueError("positions has %d tokens, %d are needed" %
-                         (positions.shape[-1], tokens))
-    if cos_sin_cache.dim() != 2 or (cos_sin_cache.shape[1] > 1 and
-                                    cos_sin_cache.stride(1) != 1):
+                         (shape[-1], tokens))
+    table, ts = cos_sin_cache.shape, cos_sin_cache.stride()
+    if len(table) != 2 or (table[1] > 1 and ts[1] != 1):
         raise ValueError("cos_sin_cache must be [max_position, rot_dim] with "
                          "contiguous rows")
-    if cos_sin_cache.dtype not in (torch.float32, q.dtype):
+    f32 = cos_sin_cache.dtype is torch.float32
+    if not f32 and cos_sin_cache.dtype is not dtype:
         raise ValueError("cos_sin_cache must be float32 or of q's dtype")
-    if (q_weight is None) != (k_weight is None):
+    qw = kw = 0
+    if q_weight is not None and k_weight is not None:
+        for w in (q_weight, k_weight):
+            if w.dtype is not dtype or w.shape != (head_size,) or \
+                    w.stride(0) != 1:
+                raise ValueError("norm weights must be contiguous "
+                                 "[head_size] of q's dtype")
+        qw, kw = q_weight.data_ptr(), k_weight.data_ptr()
+    elif q_weight is not None or k_weight is not None:
         raise ValueError("q_weight and k_weight go together (both or "
                          "neither)")
-    r = _RopeParams()
-    axes = positions.shape[0] if positions.dim() == 2 else 1
+    sections = (0, 0, 0, 0)
     if mrope_section is None:
         if axes != 1:
             raise ValueError("positions of several axes need mrope_section")
@@ -499,30 +506,12 @@ def _rope_params(q, positions, cos_sin_cache, q_weight, k_weight, eps,
         if len(mrope_section) != axes or axes > 4:
             raise ValueError("mrope_section must give one count for each of "
                              "1 to 4 axes of positions")
-        for i, n in enumerate(mrope_section):
-            r.sections[i] = n
-    for w in (q_weight, k_weight):
-        if w is not None and (w.dtype != q.dtype or
-                              tuple(w.shape) != (head_size,) or
-                              w.stride(0) != 1):
-            raise ValueError("norm weights must be contiguous [head_size] of "
-                             "q's dtype")
-    r.positions = positions.data_ptr()
-    r.position_axis_stride = positions.stride(0) if axes > 1 else 0
-    r.num_axes = axes
-    r.interleaved_axes = 1 if mrope_interleaved and axes > 1 else 0
-    r.cos_sin = cos_sin_cache.data_ptr()
-    r.max_position = cos_sin_cache.shape[0]
-    r.cos_sin_stride = cos_sin_cache.stride(0) if r.max_position > 1 else \
-        cos_sin_cache.shape[1]
-    r.cos_sin_f32 = 1 if cos_sin_cache.dtype == torch.float32 else 0
-    r.rot_dim = cos_sin_cache.shape[1]
-    r.is_neox = 1 if is_neox else 0
-    r.q_weight = _addr(q_weight)
-    r.k_weight = _addr(k_weight)
-    r.eps = eps
-    r.weight_offset = weight_offset
-    return r
+        sections = (tuple(mrope_section) + sections)[:4]
+    return _PACK_ROPE(
+        positions.data_ptr(), strides[0] if axes > 1 else 0, axes,
+        1 if mrope_interleaved and axes > 1 else 0, *sections,
+        cos_sin_cache.data_ptr(), ts[0] if table[0] > 1 else table[1],
+        table[0], f32, table[1], bool(is_neox), qw, kw, eps, weight_offset)
 
 
 def qk_norm_rope(q, k, positions, cos_sin_cache, q_weight=None,
@@ -550,23 +539,20 @@ def qk_norm_rope(q, k, positions, cos_sin_cache, q_weight=None,
         q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
     if k_out is None:
         k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
-    _check_rows(q, "q", Hq, D, T)
-    _check_rows(k, "k", Hkv, D, T)
-    _check_rows(q_out, "q_out", Hq, D, T)
-    _check_rows(k_out, "k_out", Hkv, D, T)
-    if not (q.dtype == k.dtype == q_out.dtype == k_out.dtype):
+    rows = (_rows(q, "q", Hq, D, T) + _rows(k, "k", Hkv, D, T) +
+            _rows(q_out, "q_out", Hq, D, T) + _rows(k_out, "k_out", Hkv, D,
+                                                    T))
+    dtype = q.dtype
+    if k.dtype is not dtype or q_out.dtype is not dtype or \
+            k_out.dtype is not dtype:
         raise ValueError("q, k, q_out and k_out must share a dtype")
     dt = _dtype(q)
-    r = _rope_params(q, positions, cos_sin_cache, q_weight, k_weight, eps,
+    r = _rope_params(dtype, positions, cos_sin_cache, q_weight, k_weight, eps,
                      is_neox, mrope_section, mrope_interleaved,
                      weight_offset, T, D)
     dev = _on_device(q, k, positions, cos_sin_cache, q_weight, k_weight,
                      q_out, k_out)
-    _call(dev, lib.pkv_qk_norm_rope, q.data_ptr(), q.stride(0), q.stride(1),
-          k.data_ptr(), k.stride(0), k.stride(1), q_out.data_ptr(),
-          q_out.stride(0), q_out.stride(1), k_out.data_ptr(),
-          k_out.stride(0), k_out.stride(1), T, Hq, Hkv, D, ctypes.byref(r),
-          dt)
+    _call(dev, lib.pkv_qk_norm_rope, *rows, T, Hq, Hkv, D, r, dt)
     return q_out, k_out
 
 
@@ -586,53 +572,46 @@ def rope_reshape_and_cache(q, k, v, key_cache, value_cache, slot_mapping,
     and value are then not stored).  kv_cache_dtype: "auto", "fp8" or "fp4".
     """
     lib = load_library()
-    _check_slots(slot_mapping)
-    T = slot_mapping.shape[0]
+    T = _slots(slot_mapping)
     if q.dim() != 3:
         raise ValueError("q must be [tokens, heads, head_size]")
-    Hq, D = q.shape[1], q.shape[2]
-    cs = _cache_strides(key_cache, value_cache)
-    NB, BS, H, Dc = key_cache.shape
-    fp4 = None
-    scales = (None, None)
+    _, Hq, D = q.shape
+    shape, cs = _cache_views(key_cache, value_cache)
+    NB, BS, H, Dc = shape
+    dtype = q.dtype
+    fp4 = ks = vs = None
     if kv_cache_dtype == "fp4":
-        f, Dc = _fp4_scales(key_cache, value_cache, k_block_scale,
-                            v_block_scale, k_scale, v_scale)
-        fp4 = ctypes.byref(f)
+        fp4 = _fp4_scales(key_cache, value_cache, shape, k_block_scale,
+                          v_block_scale, k_scale, v_scale)
+        Dc *= 2
     elif k_block_scale is not None or v_block_scale is not None:
         raise ValueError("block scales need kv_cache_dtype 'fp4'")
     elif kv_cache_dtype.startswith("fp8"):
         if key_cache.dtype not in _FP8_CACHE or \
                 value_cache.dtype not in _FP8_CACHE:
             raise ValueError("an fp8 cache must be float8_e4m3fn or uint8")
-        _scalar(k_scale, "k_scale")
-        _scalar(v_scale, "v_scale")
-        scales = (k_scale.data_ptr(), v_scale.data_ptr())
-    elif key_cache.dtype != q.dtype or value_cache.dtype != q.dtype:
+        ks, vs = _scalar(k_scale, "k_scale"), _scalar(v_scale, "v_scale")
+    elif key_cache.dtype is not dtype or value_cache.dtype is not dtype:
         raise ValueError("cache dtype must match q's for 'auto'")
     if Dc != D:
         raise ValueError("q and cache head_size differ (%d and %d)" % (D, Dc))
     if q_out is None:
         q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
-    _check_rows(q, "q", Hq, D, T)
-    _check_rows(k, "k", H, D, T)
-    _check_rows(v, "v", H, D, T)
-    _check_rows(q_out, "q_out", Hq, D, T)
-    if not (q.dtype == k.dtype == v.dtype == q_out.dtype):
+    rows = (_rows(q, "q", Hq, D, T) + _rows(k, "k", H, D, T) +
+            _rows(v, "v", H, D, T) + _rows(q_out, "q_out", Hq, D, T))
+    if k.dtype is not dtype or v.dtype is not dtype or \
+            q_out.dtype is not dtype:
         raise ValueError("q, k, v and q_out must share a dtype")
     dt = _dtype(q)
-    r = _rope_params(q, positions, cos_sin_cache, q_weight, k_weight, eps,
+    r = _rope_params(dtype, positions, cos_sin_cache, q_weight, k_weight, eps,
                      is_neox, mrope_section, mrope_interleaved,
                      weight_offset, T, D)
     dev = _on_device(q, k, v, key_cache, value_cache, slot_mapping,
                      positions, cos_sin_cache, k_scale, v_scale,
                      k_block_scale, v_block_scale, q_weight, k_weight, q_out)
-    _call(dev, lib.pkv_rope_reshape_and_cache, q.data_ptr(), q.stride(0),
-          q.stride(1), k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(),
-          v.stride(0), v.stride(1), q_out.data_ptr(), q_out.stride(0),
-          q_out.stride(1), key_cache.data_ptr(), value_cache.data_ptr(), cs,
-          slot_mapping.data_ptr(), T, Hq, H, D, BS, NB, ctypes.byref(r), dt,
-          kv_cache_dtype.encode(), scales[0], scales[1], fp4)
+    _call(dev, lib.pkv_rope_reshape_and_cache, *rows, key_cache.data_ptr(),
+          value_cache.data_ptr(), cs, slot_mapping.data_ptr(), T, Hq, H, D,
+          BS, NB, r, dt, kv_cache_dtype.encode(), ks, vs, fp4)
     return q_out
 
 
@@ -708,6 +687,13 @@ def flash_attn_varlen_func(q, k, v, max_seqlen_q, cu_seqlens_q, max_seqlen_k,
     Returns out (and lse [Hq, T] float32 when return_softmax_lse).
     """
     lib = load_library()
+    if k_block_scale is not None or v_block_scale is not None:
+        return _attend_fp4(
+            lib, q, k, v, max_seqlen_q, cu_seqlens_q, max_seqlen_k, seqused_k,
+            softmax_scale, causal, window_size, softcap, alibi_slopes,
+            block_table, return_softmax_lse, out, num_splits, cu_seqlens_k,
+            workspace, s_aux, k_descale, v_descale, fixed_split_size,
+            enable_pdl, k_block_scale, v_block_scale)
     nonpaged = cu_seqlens_k is not None
     if q.stride(-1) != 1:
         raise ValueError("q head_size dim must be contiguous")
@@ -741,20 +727,10 @@ def flash_attn_varlen_func(q, k, v, max_seqlen_q, cu_seqlens_q, max_seqlen_k,
         # (the row stride of a single request's table says nothing)
         bt_stride = block_table.stride(0) if block_table.shape[0] > 1 else \
             max_blocks
-    kv4 = k_block_scale is not None or v_block_scale is not None
-    q8 = q.dtype in _FP8_CACHE
-    if kv4:
-        if nonpaged or q8:
-            raise NotImplementedError("a 4-bit cache is paged, with a 16-bit "
-                                      "query")
-        fp4, Dk = _fp4_scales(k, v, k_block_scale, v_block_scale, k_descale,
-                              v_descale)
-        dev = _on_device(q, k, v, k_block_scale, v_block_scale, k_descale,
-                         v_descale, cu_seqlens_q, seqused_k, block_table,
-                         alibi_slopes, s_aux, out, workspace)
     if Dk != D:
         raise ValueError("q and k head_size differ")
-    kv8 = not kv4 and k.dtype in _FP8_CACHE
+    kv8 = k.dtype in _FP8_CACHE
+    q8 = q.dtype in _FP8_CACHE
     if q8:
         if not kv8:
             raise NotImplementedError("an fp8 query needs an fp8 cache")
@@ -769,7 +745,7 @@ def flash_attn_varlen_func(q, k, v, max_seqlen_q, cu_seqlens_q, max_seqlen_k,
         if v.dtype not in _FP8_CACHE or k_descale is None or \
                 v_descale is None:
             raise ValueError("an fp8 cache needs k_descale and v_descale")
-    elif not kv4 and (k.dtype != q.dtype or v.dtype != q.dtype):
+    elif k.dtype != q.dtype or v.dtype != q.dtype:
         raise NotImplementedError("q and cache dtypes must match")
     if cu_seqlens_q.dtype != torch.int32:
         raise ValueError("cu_seqlens_q must be int32")
@@ -802,9 +778,7 @@ def flash_attn_varlen_func(q, k, v, max_seqlen_q, cu_seqlens_q, max_seqlen_k,
         opts.total_k = k.shape[0]
     opts.fixed_split_size = int(fixed_split_size)
     opts.no_pdl = 0 if enable_pdl else 1
-    size = lib.pkv_paged_attention_workspace_size_fp4 if kv4 else \
-        lib.pkv_paged_attention_workspace_size_opts
-    ws_need = size(
+    ws_need = lib.pkv_paged_attention_workspace_size_opts(
         batch, T, max_seqlen_q, max_seqlen_k, Hq, Hkv, D, BS,
         int(bool(causal)), int(window_size[0]), int(window_size[1]),
         num_splits, max_blocks, ctypes.byref(opts))
@@ -816,20 +790,6 @@ def flash_attn_varlen_func(q, k, v, max_seqlen_q, cu_seqlens_q, max_seqlen_k,
         workspace.element_size()
     if alibi_slopes is not None and alibi_slopes.dtype != torch.float32:
         raise ValueError("alibi_slopes must be float32")
-    if kv4:
-        if out.shape != q.shape or out.stride(-1) != 1:
-            raise ValueError("out must have q's shape, D contiguous")
-        _call4(dev, lib.pkv_paged_attention_varlen_fp4, opts, q.data_ptr(),
-               q.stride(0), q.stride(1), k.data_ptr(), v.data_ptr(), cs,
-               ctypes.byref(fp4), out.data_ptr(), out.stride(0),
-               out.stride(1), cu_seqlens_q.data_ptr(), seqused_k.data_ptr(),
-               batch, T, int(max_seqlen_q), int(max_seqlen_k),
-               block_table.data_ptr(), bt_stride, max_blocks, Hq, Hkv, D, BS,
-               NB, float(softmax_scale), int(bool(causal)),
-               int(window_size[0]), int(window_size[1]),
-               float(softcap or 0.0), _addr(alibi_slopes), int(num_splits),
-               _addr(lse), _addr(workspace), ws_bytes, _dtype(out))
-        return (out, lse) if return_softmax_lse else out
     _check(lib.pkv_paged_attention_varlen_opts(
         _ptr(q), q.stride(0), q.stride(1), _ptr(k), _ptr(v), cs, _ptr(out),
         out.stride(0), out.stride(1), _ptr(cu_seqlens_q), _ptr(seqused_k),
@@ -842,6 +802,94 @@ def flash_attn_varlen_func(q, k, v, max_seqlen_q, cu_seqlens_q, max_seqlen_k,
     if return_softmax_lse:
         return out, lse
     return out
+
+
+def _attend_fp4(lib, q, k, v, max_seqlen_q, cu_seqlens_q, max_seqlen_k,
+                seqused_k, softmax_scale, causal, window_size, softcap,
+                alibi_slopes, block_table, return_softmax_lse, out,
+                num_splits, cu_seqlens_k, workspace, s_aux, k_descale,
+                v_descale, fixed_split_size, enable_pdl, k_block_scale,
+                v_block_scale):
+    """flash_attn_varlen_func over a 4-bit cache."""
+    if cu_seqlens_k is not None or q.dtype in _FP8_CACHE:
+        raise NotImplementedError("a 4-bit cache is paged, with a 16-bit "
+                                  "query")
+    if q.dim() != 3:
+        raise ValueError("q must be [tokens, heads, head_size]")
+    T, Hq, D = q.shape
+    shape, cs = _cache_views(k, v)
+    fp4 = _fp4_scales(k, v, shape, k_block_scale, v_block_scale, k_descale,
+                      v_descale)
+    NB, BS, Hkv, half = shape
+    if 2 * half != D:
+        raise ValueError("q and k head_size differ")
+    if block_table is None or seqused_k is None:
+        raise ValueError("block_table and seqused_k are required")
+    table = block_table.shape
+    if seqused_k.dtype is not torch.int32 or \
+            block_table.dtype is not torch.int32 or \
+            cu_seqlens_q.dtype is not torch.int32:
+        raise ValueError("cu_seqlens_q, seqused_k and block_table must be "
+                         "int32")
+    batch = seqused_k.shape[0]
+    if len(table) != 2 or table[0] < batch or \
+            (table[1] > 1 and block_table.stride(1) != 1) or \
+            cu_seqlens_q.shape[0] != batch + 1 or \
+            (batch > 1 and seqused_k.stride(0) != 1) or \
+            cu_seqlens_q.stride(0) != 1:
+        raise ValueError("block_table must be [batch, max_blocks] with "
+                         "contiguous rows, seqused_k [batch] and cu_seqlens_q "
+                         "[batch + 1] contiguous")
+    bt_stride = block_table.stride(0) if batch > 1 else table[1]
+    if out is None:
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+    elif out.dtype is not q.dtype or out.shape[0] != T:
+        raise ValueError("out must have q's shape and dtype")
+    qp, q0, q1 = _rows(q, "q", Hq, D, T)
+    op, o0, o1 = _rows(out, "out", Hq, D, T)
+    dt = _dtype(q)
+    for t, what in ((alibi_slopes, "alibi_slopes"), (s_aux, "s_aux (sinks)")):
+        if t is not None and (t.dtype is not torch.float32 or
+                              t.shape != (Hq,) or t.stride(0) != 1):
+            raise ValueError("%s must be float32 [num_heads]" % what)
+    dev = _on_device(q, k, v, k_block_scale, v_block_scale, k_descale,
+                     v_descale, cu_seqlens_q, seqused_k, block_table,
+                     alibi_slopes, s_aux, out, workspace)
+    lse = None
+    if return_softmax_lse:
+        lse = torch.empty((Hq, T), dtype=torch.float32, device=q.device)
+    opts = None
+    if s_aux is not None or fixed_split_size or not enable_pdl:
+        o = _Options()
+        o.sinks = _addr(s_aux)
+        o.fixed_split_size = int(fixed_split_size)
+        o.no_pdl = 0 if enable_pdl else 1
+        opts = ctypes.addressof(o)
+    if softmax_scale is None:
+        softmax_scale = D ** -0.5
+    max_q, max_k, causal = int(max_seqlen_q), int(max_seqlen_k), bool(causal)
+    left, right = window_size
+    if workspace is None:
+        n = lib.pkv_paged_attention_workspace_size_fp4(
+            batch, T, max_q, max_k, Hq, Hkv, D, BS, causal, left, right,
+            num_splits, table[1], opts)
+        if n == _NO_SIZE:
+            raise ValueError(lib.pkv_last_error().decode())
+        if n:
+            workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
+    wp, wn = 0, 0
+    if workspace is not None:
+        wp = workspace.data_ptr()
+        wn = workspace.numel() * workspace.element_size()
+    def call(*a):
+        return lib.pkv_paged_attention_varlen_fp4(*a, opts)
+
+    _call(dev, call, qp, q0, q1, k.data_ptr(), v.data_ptr(), cs, fp4, op, o0,
+          o1, cu_seqlens_q.data_ptr(), seqused_k.data_ptr(), batch, T, max_q,
+          max_k, block_table.data_ptr(), bt_stride, table[1], Hq, Hkv, D, BS,
+          NB, softmax_scale, causal, left, right, softcap or 0.0,
+          _addr(alibi_slopes), num_splits, _addr(lse), wp, wn, dt)
+    return (out, lse) if return_softmax_lse else out
 
 
 def make_local_attention_virtual_batches(attn_chunk_size, query_start_loc,

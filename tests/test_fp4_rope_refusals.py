@@ -18,7 +18,12 @@ def lib():
 P = 1 << 20                       # a pointer that is never followed
 
 
-class Scales(api._Fp4Scales):
+class Scales(ctypes.Structure):
+    _fields_ = [("k_block_scale", ctypes.c_void_p),
+                ("v_block_scale", ctypes.c_void_p),
+                ("strides", ctypes.c_int64 * 4),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p)]
+
     def __init__(self, **kw):
         super().__init__(P, P, (ctypes.c_int64 * 4)(512, 8, 128, 1), P, P)
         for k, v in kw.items():
@@ -29,8 +34,23 @@ def strides(*s):
     return (ctypes.c_int64 * 4)(*s)
 
 
+class RopeParams(ctypes.Structure):
+    """pkv_rope_params (include/pkv.h)."""
+    _fields_ = [("positions", ctypes.c_void_p),
+                ("position_axis_stride", ctypes.c_int64),
+                ("num_axes", ctypes.c_int),
+                ("interleaved_axes", ctypes.c_int),
+                ("sections", ctypes.c_int * 4), ("cos_sin", ctypes.c_void_p),
+                ("cos_sin_stride", ctypes.c_int64),
+                ("max_position", ctypes.c_int64),
+                ("cos_sin_f32", ctypes.c_int), ("rot_dim", ctypes.c_int),
+                ("is_neox", ctypes.c_int), ("q_weight", ctypes.c_void_p),
+                ("k_weight", ctypes.c_void_p), ("eps", ctypes.c_float),
+                ("weight_offset", ctypes.c_float)]
+
+
 def rope(**kw):
-    r = api._RopeParams(positions=P, position_axis_stride=8, num_axes=1,
+    r = RopeParams(positions=P, position_axis_stride=8, num_axes=1,
                         cos_sin=P, cos_sin_stride=128, max_position=100,
                         cos_sin_f32=1, rot_dim=128, is_neox=1, q_weight=P,
                         k_weight=P, eps=1e-6, weight_offset=0.0)
@@ -228,6 +248,20 @@ bf, i64, i32 = torch.bfloat16, torch.int64, torch.int32
 
 def cache(nb=4, bs=16, h=2, d=128):
     return api.fp4_kv_cache(nb, bs, h, d, device="cpu")
+
+
+def test_packed_structs_match_their_declarations():
+    """The bytes the binding passes are the structs of the header."""
+    r = rope(num_axes=3, sections=(1, 2, 3), is_neox=0, interleaved_axes=1)
+    s = list(r.sections)
+    assert api._PACK_ROPE(
+        r.positions, r.position_axis_stride, r.num_axes, r.interleaved_axes,
+        *s, r.cos_sin, r.cos_sin_stride, r.max_position, r.cos_sin_f32,
+        r.rot_dim, r.is_neox, r.q_weight, r.k_weight, r.eps,
+        r.weight_offset) == bytes(r)
+    f = Scales()
+    assert api._PACK_FP4(f.k_block_scale, f.v_block_scale, *f.strides,
+                         f.k_scale, f.v_scale) == bytes(f)
 
 
 def test_cache_layout():
