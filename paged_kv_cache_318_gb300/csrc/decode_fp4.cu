@@ -253,7 +253,7 @@ decode_fp4_kernel(const AttnParams p, int splits) {
   constexpr int KW = D / 32;             // words of a lane's K codes per key
   constexpr int NT = kWarps * 32;
   // (a cp.async chunk pair that straddles 32 bytes of shared memory costs two
-  // L2 sectors: 0.226 against 0.205 ms on 8 x 131072 keys)
+  // L2 sectors: 0.226 against 0.216 ms on 8 x 131072 keys)
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ long long scan[kWarps];
   // what the inner loop seldom needs: the piece, and by packed row the token
@@ -350,10 +350,13 @@ decode_fp4_kernel(const AttnParams p, int splits) {
         const int n = r.rows > 0 ? kUnitCost + tiles_of(r) : 0;
         const long long all = static_cast<long long>(n) * p.Hkv;
         if (T0 < at + all) {
-          const unsigned off = static_cast<unsigned>(T0 - at);
+          const long long off = T0 - at;
           cur.b = b;
-          cur.h = off / n;
-          cur.t0 = off % n;
+          cur.h = static_cast<int>(off < (1LL << 32)
+                                       ? static_cast<unsigned>(off) /
+                                             static_cast<unsigned>(n)
+                                       : off / n);
+          cur.t0 = static_cast<int>(off - static_cast<long long>(cur.h) * n);
           cur.r = r;
           break;
         }
@@ -1223,8 +1226,10 @@ fold_kernel(const AttnParams p) {
   const int q0 = p.cu_q[b];
   const int q_len = min(p.cu_q[b + 1] - q0, p.total_q - q0);
   const int rows = min(q_len * p.G, p.sk_rows);
-  auto row_of = [&](int k, int r) {
-    const int slot = k == 0 ? 2 * (first - 1) + 1 : 2 * (first + k - 1);
+  // (one linear expression: `k == 0 ? a : b` gave a wrong slot for parts 32
+  // .. 63 in the unrolled sum of units with more than 128 parts)
+  auto row_of = [&](int k, int r) -> int64_t {
+    const int slot = 2 * (first - 1 + k) + (k == 0 ? 1 : 0);
     return static_cast<int64_t>(slot) * p.sk_rows + r;
   };
   // this block's items

@@ -170,7 +170,7 @@ def test_write_flags_bad_slots(cuda_device):
 
 # --------------------------------------------------------------- attention
 
-def attend(wl, dev, cache, lse=True, **kw):
+def attend(wl, dev, cache, lse=True, max_k=0, **kw):
     codes, sf, ks, vs = cache
     args = dict(softmax_scale=wl.softmax_scale, causal=wl.causal,
                 window_size=wl.window_size, softcap=wl.softcap,
@@ -180,7 +180,8 @@ def attend(wl, dev, cache, lse=True, **kw):
     args.update(kw)
     return api.flash_attn_varlen_func(
         wl.q.to(dev), codes[0], codes[1], wl.max_seqlen_q,
-        torch.from_numpy(wl.cu_seqlens_q).to(dev), wl.max_seqlen_k,
+        torch.from_numpy(wl.cu_seqlens_q).to(dev),
+        max(wl.max_seqlen_k, max_k),
         seqused_k=torch.from_numpy(wl.seq_lens).to(dev),
         block_table=torch.from_numpy(wl.block_table).to(dev),
         return_softmax_lse=lse, k_descale=ks, v_descale=vs,
@@ -205,6 +206,8 @@ def check(wl, out, lse, refs, sinks=None, keep=None):
         window_size=wl.window_size, softcap=wl.softcap,
         alibi_slopes=wl.alibi_slopes, **({} if sinks is None else
                                          {"sinks": sinks}))
+    if np.isnan(kref).all():             # no request has a key
+        kref = vref = np.zeros_like(kref)
     d = logit_error(wl, kref)
     half = torch.finfo(wl.torch_dtype).eps / 2
     G = wl.num_heads // wl.num_kv_heads
@@ -544,6 +547,222 @@ def test_prefill_range_of_values_is_exact(cuda_device):
 
 
 # --------------------------------------------------- graphs, streams, chain
+
+def shares(idx):
+    """Calls whose key range is long enough (by max_seqlen_k) that every CTA
+    takes an equal share of all units' keys."""
+    g = np.random.default_rng(idx)
+    q, more = None, {}
+    if idx == 0:         # more requests than threads, empty ones among them
+        k = g.integers(0, 150, 310)
+        heads = (4, 2, 64, 16)
+    elif idx == 1:       # up to 16 rows, requests without queries or keys
+        q, k = g.integers(0, 5, 140), g.integers(0, 300, 140)
+        heads = (8, 2, 128, 16)
+        more = dict(dtype="f16")
+    elif idx == 2:
+        q, k = g.integers(1, 4, 40), g.integers(0, 900, 40)
+        heads = (20, 4, 256, 48)
+        more = dict(window_size=(2100, -1), softcap=30.0)
+    elif idx == 3:       # one unit over many CTAs
+        k, heads = [9001], (8, 1, 128, 32)
+    elif idx == 4:       # ... over more than the join looks at in one step
+        k, heads = [70000], (2, 2, 64, 64)
+    elif idx == 5:       # beside prefill-class requests
+        q, k = [1, 40, 2, 1, 90], [2500, 400, 1, 3000, 90]
+        heads, more = (16, 4, 128, 16), dict(alibi=True)
+    elif idx == 6:       # nothing to see at all
+        k, heads = [0] * 9, (8, 4, 128, 16)
+    elif idx == 7:       # one key each: the smallest shares
+        k, heads = [1] * 5 + [3000] + [1] * 700, (8, 1, 256, 16)
+    elif idx == 8:
+        q, k = [3, 2] * 30, g.integers(3, 700, 60)
+        heads, more = (4, 4, 64, 16), dict(causal=False,
+                                           window_size=(2048, 40))
+    q = [1] * len(k) if q is None else q
+    return workload("sh_%d" % idx, 40 + idx, q, k, *heads, **more)
+
+
+@pytest.mark.parametrize("kw", [
+    {}, dict(num_splits=1), dict(num_splits=50), dict(num_splits=200),
+    dict(fixed_split_size=512)], ids=["auto", "1", "50", "200", "fixed"])
+@pytest.mark.parametrize("Hq,Hkv,D,q_lens,L", [
+    (1, 1, 64, [1], [33000]), (2, 2, 64, [1], [70001]),
+    (8, 1, 128, [1, 1], [40000, 11]), (16, 1, 256, [1], [20011]),
+    (4, 1, 128, [3, 0, 2], [26000, 9, 5000]),
+    (4, 2, 128, [40], [3000])])
+def test_equal_weights(cuda_device, Hq, Hkv, D, q_lens, L, kw):
+    """Queries of zero weigh every key alike: the output is the mean of the
+    values a row sees and the LSE the logarithm of their number.  Here P is
+    1 and a piece's sums (of multiples of 2^-1 below 2^23) are exact; what is
+    left are the exp2 and log2 of the pieces' joins (2^-20 relative each) and
+    the output's rounding, so a single piece that is lost or counted twice
+    shows."""
+    dev = cuda_device
+    g = np.random.default_rng(L[0])
+    BS, B = 16, len(L)
+    blocks = [-(-n // BS) for n in L]
+    NB = sum(blocks) + 1
+    table = np.zeros((B, max(blocks)), np.int32)
+    perm = g.permutation(NB)
+    at = 0
+    for b, n in enumerate(blocks):
+        table[b, :n] = perm[at:at + n]
+        at += n
+    codes, sf = api.fp4_kv_cache(NB, BS, Hkv, D, dev)
+    codes.copy_(torch.from_numpy(g.integers(0, 256, codes.shape, np.uint8)))
+    sf.view(torch.uint8).fill_(0x38)                # 1.0
+    one = torch.ones(1, device=dev)
+    v = api.dequantize_fp4_cache(codes[1], sf[1], one, dtype=torch.bfloat16)
+    v = f32(v).astype(np.float64)
+    T = sum(q_lens)
+    cu = np.concatenate([[0], np.cumsum(q_lens)]).astype(np.int32)
+    out, lse = api.flash_attn_varlen_func(
+        torch.zeros(T, Hq, D, dtype=torch.bfloat16, device=dev), codes[0],
+        codes[1], max(q_lens), torch.from_numpy(cu).to(dev), max(L),
+        seqused_k=torch.tensor(L, dtype=torch.int32, device=dev),
+        softmax_scale=1.0, causal=True,
+        block_table=torch.from_numpy(table).to(dev), return_softmax_lse=True,
+        k_descale=one, v_descale=one, k_block_scale=sf[0],
+        v_block_scale=sf[1], **kw)
+    o, lse = f32(out).astype(np.float64), lse.cpu().numpy()
+    for b in range(B):
+        rows = v[table[b]].reshape(-1, Hkv, D)[:L[b]].cumsum(0)
+        for i in range(q_lens[b]):
+            n = L[b] - q_lens[b] + i + 1
+            want = np.repeat(rows[n - 1] / n, Hq // Hkv, axis=0)
+            assert np.abs(lse[:, cu[b] + i] - np.log(n)).max() <= 1e-5
+            err = np.abs(o[cu[b] + i] - want)
+            assert (err <= 2.0 ** -8 * np.abs(want) + 6 * 2.0 ** -18).all()
+
+
+@pytest.mark.parametrize("sinks", [False, True])
+@pytest.mark.parametrize("idx", range(9))
+def test_shares(cuda_device, idx, sinks):
+    dev = cuda_device
+    wl = shares(idx)
+    cache = fill(wl, dev)
+    z = np.linspace(-3, 5, wl.num_heads).astype(np.float32) if sinks else None
+    kw = dict(s_aux=torch.from_numpy(z).to(dev)) if sinks else {}
+    out, lse = attend(wl, dev, cache, max_k=4096, **kw)
+    api.check_device_errors(dev)
+    check(wl, out, lse, oracle_cache(wl)[1], sinks=z)
+    again = attend(wl, dev, cache, max_k=4096, enable_pdl=False, **kw)
+    assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+
+
+def test_shares_need_their_workspace(cuda_device):
+    """A workspace without room for the shares' parts: one CTA a unit."""
+    dev = cuda_device
+    wl = shares(0)
+    out, lse = attend(wl, dev, fill(wl, dev), max_k=4096,
+                      workspace=torch.empty(0, dtype=torch.uint8, device=dev))
+    api.check_device_errors(dev)
+    check(wl, out, lse, oracle_cache(wl)[1])
+
+
+@pytest.mark.parametrize("matrix", [0, 1])
+def test_shares_nan_is_seen_only_by_its_rows(cuda_device, matrix):
+    dev = cuda_device
+    wl = workloads.build_workload("ns4", 8, [4, 1, 2], [5000, 300, 70], 4, 2,
+                                  128, 16)
+    cache = fill(wl, dev)
+    codes, sf, ks, vs = cache
+    nan = np.zeros(wl.q.shape, bool)
+    # (request, key, rows that see it)
+    for b, key, rows in ((0, 4998, slice(2, 4)), (0, 7, slice(0, 4)),
+                         (2, 69, slice(6, 7))):
+        blk, off = wl.block_table[b, key // 16], key % 16
+        sf[matrix].view(torch.uint8)[blk, off, 1, 1] = 0x7F
+        nan[rows, 2:4, slice(0, 128) if matrix == 0 else slice(16, 32)] = True
+    out, lse = attend(wl, dev, cache)
+    o = f32(out)
+    assert np.array_equal(np.isnan(o), nan)
+    assert np.array_equal(np.isnan(f32(lse)), nan.any(-1).T
+                          if matrix == 0 else np.zeros(lse.shape, bool))
+    check(wl, out, None, oracle_cache(wl)[1], keep=~nan)
+
+
+def test_shares_in_a_graph_follow_the_lengths(cuda_device):
+    """A captured call of equal shares, replayed with other lengths (none, a
+    long one) and with queries moved from
+    one request to another."""
+    dev = cuda_device
+    wl = workload("gs4", 8, [1] * 6, [5000, 40, 2000, 0, 1, 3000], 16, 4, 128,
+                  16)
+    cache = fill(wl, dev)
+    codes, sf, ks, vs = cache
+    refs = oracle_cache(wl)[1]
+    q, cu = wl.q.to(dev), torch.from_numpy(wl.cu_seqlens_q).to(dev)
+    k = torch.from_numpy(wl.seq_lens).to(dev)
+    bt = torch.from_numpy(wl.block_table).to(dev)
+    out = torch.empty_like(q)
+
+    def call(work=None, out=out, max_q=2, max_k=5000):
+        return api.flash_attn_varlen_func(
+            q, codes[0], codes[1], max_q, cu, max_k, seqused_k=k,
+            softmax_scale=wl.softmax_scale, causal=True, block_table=bt,
+            out=out, workspace=work, k_descale=ks, v_descale=vs,
+            k_block_scale=sf[0], v_block_scale=sf[1])
+    work = torch.empty(64 << 20, dtype=torch.uint8, device=dev)
+    call(work)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(work)
+    full = wl.seq_lens.copy()
+    for lens, cus in ((full, [0, 1, 2, 3, 4, 5, 6]),
+                      ([0, 0, 0, 0, 0, 1], [0, 1, 2, 3, 4, 5, 6]),
+                      ([17, 40, 1999, 0, 1, 2999], [0, 2, 2, 4, 4, 5, 6]),
+                      ([5000, 33, 0, 0, 0, 0], [0, 2, 4, 4, 4, 4, 6])):
+        wl.seq_lens = np.array(lens, np.int32)
+        wl.cu_seqlens_q = np.array(cus, np.int32)
+        wl.q_lens = np.diff(wl.cu_seqlens_q)
+        k.copy_(torch.from_numpy(wl.seq_lens))
+        cu.copy_(torch.from_numpy(wl.cu_seqlens_q))
+        work.fill_(0xFF)
+        out.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        check(wl, out, None, refs)
+    api.check_device_errors(dev)
+
+
+def test_two_streams_at_once(cuda_device):
+    """Calls of equal shares and their appends on two streams, each with a
+    workspace of its own, many times over."""
+    dev = cuda_device
+    jobs = []
+    for seed in (3, 4):
+        wl = workloads.build_workload("ts%d" % seed, seed, [1] * 24,
+                                      [2500 - 97 * i for i in range(24)], 16,
+                                      4, 128, 16)
+        cache = fill(wl, dev)
+        want = attend(wl, dev, cache)
+        jobs.append((wl, cache, want, torch.cuda.Stream(dev),
+                     wl.q.to(dev), torch.from_numpy(wl.cu_seqlens_q).to(dev),
+                     torch.from_numpy(wl.seq_lens).to(dev),
+                     torch.from_numpy(wl.block_table).to(dev),
+                     wl.k_new.to(dev), wl.v_new.to(dev),
+                     torch.from_numpy(wl.slot_mapping_new).to(dev), []))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for wl, (codes, sf, ks, vs), _, st, q, cu, k, bt, kn, vn, sl, \
+                outs in jobs:
+            with torch.cuda.stream(st):
+                api.reshape_and_cache_flash(
+                    kn, vn, codes[0], codes[1], sl, "fp4", ks, vs,
+                    k_block_scale=sf[0], v_block_scale=sf[1])
+                outs.append(api.flash_attn_varlen_func(
+                    q, codes[0], codes[1], 1, cu, wl.max_seqlen_k,
+                    seqused_k=k, softmax_scale=wl.softmax_scale, causal=True,
+                    block_table=bt, k_descale=ks, v_descale=vs,
+                    k_block_scale=sf[0], v_block_scale=sf[1]))
+    torch.cuda.synchronize()
+    for wl, _, want, *_, outs in jobs:
+        for out in outs:
+            assert torch.equal(out, want[0])
+
 
 def test_two_graphs_share_a_workspace(cuda_device):
     """Two captured calls of different shapes over one workspace, replayed
