@@ -37,32 +37,26 @@ __device__ __forceinline__ void quantize16(uint4 r0, uint4 r1, float scale,
   *sf = static_cast<uint8_t>(s.code);
 }
 
-// One group of 16 codes and its scale -> 16 values; with `scaled`, times
-// `scale` before the rounding to T (else the exact product alone).
+// 8 codes and their group's scale -> 8 values; with `scaled`, times `scale`
+// before the rounding to T (else the exact product alone).
 template <typename T>
-__device__ __forceinline__ void dequantize16(uint2 codes, uint8_t sf,
-                                             bool scaled, float scale,
-                                             uint4* out) {
+__device__ __forceinline__ uint4 dequantize8(uint32_t codes, uint32_t sf,
+                                             bool scaled, float scale) {
   const uint32_t s2 = e4m3x2_to_f16(sf * 0x0101u);
-  uint32_t o[8];
+  uint32_t o[4], f[4];
+  e2m1x8_to_f16(codes, f[0], f[1], f[2], f[3]);
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    uint32_t f[4];
-    e2m1x8_to_f16(h ? codes.y : codes.x, f[0], f[1], f[2], f[3]);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t v = hmul2_u32(f[i], s2);
-      const __half2 hv = *reinterpret_cast<const __half2*>(&v);
-      float a = __low2float(hv), b = __high2float(hv);
-      if (scaled) {
-        a = __fmul_rn(a, scale);
-        b = __fmul_rn(b, scale);
-      }
-      o[4 * h + i] = pack2<T>(a, b);
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t v = hmul2_u32(f[i], s2);
+    const __half2 hv = *reinterpret_cast<const __half2*>(&v);
+    float a = __low2float(hv), b = __high2float(hv);
+    if (scaled) {
+      a = __fmul_rn(a, scale);
+      b = __fmul_rn(b, scale);
     }
+    o[i] = pack2<T>(a, b);
   }
-  out[0] = make_uint4(o[0], o[1], o[2], o[3]);
-  out[1] = make_uint4(o[4], o[5], o[6], o[7]);
+  return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
 // The block's threads cover whole tokens: thread i takes group i % per_token
@@ -139,29 +133,48 @@ cache_write_fp4_kernel(const T* __restrict__ key, const T* __restrict__ value,
   }
 }
 
-// One matrix of one block of rows: [BS, Hkv, D] values from its codes.
-template <typename T>
+// One block of rows, [BS, Hkv, D] values from the codes of MATS matrices
+// (whose caches share their strides).  A thread turns 8 codes into 16 bytes,
+// so a warp stores 512 bytes in a row; it keeps its place in the row and
+// walks down the rows, kRows of each matrix loading at once.
+constexpr int kRows = 4;
+template <typename T, int MATS>
 __device__ __forceinline__ void dequantize_block(
-    const uint8_t* codes, const uint8_t* sf, int64_t c_sr, int64_t c_sh,
-    int64_t f_sr, int64_t f_sh, int BS, int Hkv, int groups, bool bad,
-    bool scaled, float scale, T* out) {
-  const int per_row = Hkv * groups;
-  for (int e = threadIdx.x; e < BS * per_row; e += blockDim.x) {
-    const int row = e / per_row;
-    const int rem = e - row * per_row;
-    const int h = rem / groups, g = rem - h * groups;
-    uint4 v[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-    if (!bad)
-      dequantize16<T>(
-          *reinterpret_cast<const uint2*>(
-              codes + static_cast<int64_t>(row) * c_sr +
-              static_cast<int64_t>(h) * c_sh + g * 8),
-          sf[static_cast<int64_t>(row) * f_sr +
-             static_cast<int64_t>(h) * f_sh + g],
-          scaled, scale, v);
-    uint4* dst = reinterpret_cast<uint4*>(out + static_cast<int64_t>(e) * 16);
-    dst[0] = v[0];
-    dst[1] = v[1];
+    const uint8_t* const (&codes)[MATS], const uint8_t* const (&sf)[MATS],
+    int64_t c_sr, int64_t c_sh, int64_t f_sr, int64_t f_sh, int BS, int Hkv,
+    int groups, bool bad, bool scaled, float scale, T* const (&out)[MATS]) {
+  const int eighths = 2 * groups, per_row = Hkv * eighths;
+  // whole rows at a time (a row of more eighths than threads is looped over)
+  const int rows = per_row >= kThreads ? 1 : kThreads / per_row;
+  const int row0 = per_row >= kThreads ? 0 : threadIdx.x / per_row;
+  if (row0 >= rows) return;
+  for (int r = threadIdx.x - row0 * per_row; r < per_row; r += kThreads) {
+    const int h = r / eighths, g = r - h * eighths;
+    const int64_t c = h * c_sh + g * 4, f = h * f_sh + (g >> 1);
+    for (int row = row0; row < BS; row += rows * kRows) {
+      uint32_t code[kRows][MATS], s[kRows][MATS];
+#pragma unroll
+      for (int i = 0; i < kRows; ++i)
+#pragma unroll
+        for (int m = 0; m < MATS; ++m) {
+          const int64_t at = row + i * rows;
+          code[i][m] = s[i][m] = 0;               // (zeros)
+          if (at < BS && !bad) {
+            code[i][m] = __ldg(reinterpret_cast<const uint32_t*>(
+                codes[m] + at * c_sr + c));
+            s[i][m] = __ldg(sf[m] + at * f_sr + f);
+          }
+        }
+#pragma unroll
+      for (int i = 0; i < kRows; ++i)
+#pragma unroll
+        for (int m = 0; m < MATS; ++m) {
+          const int64_t at = row + i * rows;
+          if (at < BS)
+            *reinterpret_cast<uint4*>(out[m] + (at * per_row + r) * 8) =
+                dequantize8<T>(code[i][m], s[i][m], scaled, scale);
+        }
+    }
   }
 }
 
@@ -180,10 +193,11 @@ fp4_dequant_blocks_kernel(const uint8_t* __restrict__ codes, int64_t c_sb,
     const int64_t blk = ids ? __ldg(ids + i) : i;
     const bool bad = blk < 0 || blk >= num_blocks;
     if (bad && threadIdx.x == 0) atomicOr(err, kErrBadBlock);
-    dequantize_block<T>(codes + (bad ? 0 : blk * c_sb),
-                        sf + (bad ? 0 : blk * f_sb), c_sr, c_sh, f_sr, f_sh,
-                        BS, Hkv, groups, bad, true, sc,
-                        out + i * BS * Hkv * groups * 16);
+    const uint8_t* c[1] = {codes + (bad ? 0 : blk * c_sb)};
+    const uint8_t* f[1] = {sf + (bad ? 0 : blk * f_sb)};
+    T* const o[1] = {out + i * BS * Hkv * groups * 16};
+    dequantize_block<T, 1>(c, f, c_sr, c_sh, f_sr, f_sh, BS, Hkv, groups, bad,
+                           true, sc, o);
   }
 }
 
@@ -197,28 +211,34 @@ fp4_dequant_pages_kernel(const AttnParams p, T* __restrict__ mock_k,
                          int groups) {
   const int64_t pages = static_cast<int64_t>(p.batch) * p.max_blocks;
   const int64_t elems = static_cast<int64_t>(p.BS) * p.Hkv * groups * 16;
+  // (the item counter of the prefill kernel that follows)
+  if (p.sched && blockIdx.x == 0 && threadIdx.x == 0) *p.sched = 0;
   for (int64_t m = blockIdx.x; m < pages; m += gridDim.x) {
-    const int b = static_cast<int>(m / p.max_blocks);
+    const int b = static_cast<int>(
+        pages <= 0xffffffffLL ? static_cast<unsigned>(m) /
+                                    static_cast<unsigned>(p.max_blocks)
+                              : m / p.max_blocks);
     const int j = static_cast<int>(m - static_cast<int64_t>(b) *
                                            p.max_blocks);
     if (threadIdx.x == 0) table[m] = static_cast<int32_t>(m);
+    // (four loads in flight at once)
     const int q0 = p.cu_q[b];
+    const int L = p.seqused_k[b];
+    const int blk = p.block_table[static_cast<int64_t>(b) * p.bt_stride + j];
     const int q_len = min(p.cu_q[b + 1] - q0, p.total_q - q0);
     if (q0 < 0 || q_len <= 0 || q_len * p.G < p.min_rows) continue;
-    const int64_t L_tab =
-        min(static_cast<int64_t>(p.seqused_k[b]),
-            static_cast<int64_t>(p.max_blocks) * p.BS);
+    const int64_t L_tab = min(static_cast<int64_t>(L),
+                              static_cast<int64_t>(p.max_blocks) * p.BS);
     if (static_cast<int64_t>(j) * p.BS >= L_tab) continue;
-    const int blk = p.block_table[static_cast<int64_t>(b) * p.bt_stride + j];
     const bool bad = blk < 0 || blk >= p.num_blocks;
     if (bad && threadIdx.x == 0) atomicOr(p.err, kErrBadBlock);
-    const int64_t c = bad ? 0 : blk * p.c_sb, f = bad ? 0 : blk * p.f_sb;
-    dequantize_block<T>(static_cast<const uint8_t*>(p.kc) + c, p.k_sf + f,
-                        p.c_sr, p.c_sh, p.f_sr, p.f_sh, p.BS, p.Hkv, groups,
-                        bad, false, 1.f, mock_k + m * elems);
-    dequantize_block<T>(static_cast<const uint8_t*>(p.vc) + c, p.v_sf + f,
-                        p.c_sr, p.c_sh, p.f_sr, p.f_sh, p.BS, p.Hkv, groups,
-                        bad, false, 1.f, mock_v + m * elems);
+    const int64_t co = bad ? 0 : blk * p.c_sb, fo = bad ? 0 : blk * p.f_sb;
+    const uint8_t* c[2] = {static_cast<const uint8_t*>(p.kc) + co,
+                           static_cast<const uint8_t*>(p.vc) + co};
+    const uint8_t* f[2] = {p.k_sf + fo, p.v_sf + fo};
+    T* const o[2] = {mock_k + m * elems, mock_v + m * elems};
+    dequantize_block<T, 2>(c, f, p.c_sr, p.c_sh, p.f_sr, p.f_sh, p.BS, p.Hkv,
+                           groups, bad, false, 1.f, o);
   }
 }
 

@@ -1032,9 +1032,9 @@ pkv_status attention_impl(
                              pdl_done == nullptr;
   // the prefill kernel's item counter (and the counter above) is zeroed
   // before any decode kernel, so that the prefill launch can follow those
-  // kernels directly
+  // kernels directly (over a 4-bit cache the page copy zeroes it)
   bool sched_zeroed = false;
-  if (pl.prefill && sched) {
+  if (pl.prefill && sched && !kv4) {
     cudaError_t e = cudaMemsetAsync(sched, 0, 2 * sizeof(int), s);
     if (e != cudaSuccess) return cuda_fail(e, "cudaMemsetAsync");
     sched_zeroed = true;
@@ -1136,6 +1136,7 @@ pkv_status attention_impl(
       e = kv4 ? launch_fp4_dequant_pages(f, head_size, bf16, mk, mv, mt, s)
               : launch_fp8_dequant_pages(f, head_size, bf16, mk, mv, mt, s);
       if (e != cudaSuccess) return cuda_fail(e, "page dequant launch");
+      if (kv4) f.sched_zeroed = 1;     // (by the kernel just launched)
       f.kc = mk;
       f.vc = mv;
       f.c_sb = static_cast<int64_t>(block_size) * num_kv_heads * head_size;
