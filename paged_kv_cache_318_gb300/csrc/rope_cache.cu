@@ -241,7 +241,9 @@ rope_kernel(const RopeLaunch p, int parts) {
   // the lane's first pair of each four (adjacent pairs) or of the eight
   const int ia = NEOX ? 8 * ca : 4 * ca, ib = NEOX ? ia + 4 : 4 * cb;
   const int pq = (p.Hq + RPW - 1) / RPW, pk = (p.Hkv + RPW - 1) / RPW;
-  const int passes = pq + (STORE == kRopeRows ? pk : 2 * pk);
+  // is this lane's row there in the last pass of q, of k and v?
+  const bool q_last = (pq - 1) * RPW + sub < p.Hq;
+  const bool k_last = (pk - 1) * RPW + sub < p.Hkv;
   __shared__ uint4 places[kDepth * 2 * kThreads];
   const uint32_t mine = smem_u32(places + threadIdx.x);
   const int64_t work = p.num_tokens * parts;
@@ -255,21 +257,31 @@ rope_kernel(const RopeLaunch p, int parts) {
     // The token's passes part, part + parts, ... in the order q, k, v; every
     // thread copies its own chunks of the next kDepth ones to its own places
     // in shared memory (nothing of them waits for the position or the slot).
+    // `src` walks down the heads of one kind.
+    int kind = 0, left = pq - part;       // of the pass that is next
+    const T* src = static_cast<const T*>(p.q) + t * p.q_st +
+                   (part * RPW + sub) * p.q_sh + 8 * ca;
+    int64_t down = parts * RPW * p.q_sh;
     auto issue = [&](int i) {
-      const int g = part + i * parts;
-      if (g < passes) {
-        const int kind = g < pq ? 0 : g < pq + pk ? 1 : 2;
-        const int h = (kind == 0 ? g : kind == 1 ? g - pq : g - pq - pk) * RPW +
-                      sub;
-        const bool on = h < (kind == 0 ? p.Hq : p.Hkv);
-        const int64_t st = kind == 0 ? p.q_st : kind == 1 ? p.k_st : p.v_st;
-        const int64_t sh = kind == 0 ? p.q_sh : kind == 1 ? p.k_sh : p.v_sh;
-        const T* src =
-            static_cast<const T*>(kind == 0 ? p.q : kind == 1 ? p.k : p.v) +
-            t * st + (on ? h * sh : 0);
+      while (left <= 0 && kind < (STORE == kRopeRows ? 1 : 2)) {
+        const int h = -left * RPW + sub;
+        ++kind;
+        left += pk;
+        const int64_t sh = kind == 1 ? p.k_sh : p.v_sh;
+        src = (kind == 1 ? static_cast<const T*>(p.k) + t * p.k_st
+                         : static_cast<const T*>(p.v) + t * p.v_st) +
+              h * sh + 8 * ca;
+        down = parts * RPW * sh;
+      }
+      if (left > 0) {
+        // (the last pass of a kind may have fewer rows)
+        const int bytes = left > 1 || (kind == 0 ? q_last : k_last) ? 16 : 0;
+        const T* at = bytes ? src : static_cast<const T*>(p.q);
         const uint32_t dst = mine + (i % kDepth) * (kThreads * 32);
-        cp_async_16(dst, src + 8 * ca, on ? 16 : 0);
-        cp_async_16(dst + kThreads * 16, src + 8 * cb, on ? 16 : 0);
+        cp_async_16(dst, at, bytes);
+        cp_async_16(dst + kThreads * 16, at + 8 * (cb - ca), bytes);
+        left -= parts;
+        src += down;
       }
       cp_async_commit();
     };
@@ -453,24 +465,27 @@ rope_kernel(const RopeLaunch p, int parts) {
             *reinterpret_cast<uint2*>(dst + 8 * cb) =
                 make_uint2(e4m3_codes4(f + 8, s8), e4m3_codes4(f + 12, s8));
           } else {
-            float top[2];
+            // (the even lane takes the scale of both lanes' A, the odd lane
+            // of both lanes' B)
+            const bool odd = lane & 1;
+            float m[2] = {0.f, 0.f};
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-              float m = 0.f;
+            for (int q = 0; q < 2; ++q)
 #pragma unroll
-              for (int e = 0; e < 8; ++e) m = max_nan(m, fabsf(f[8 * q + e]));
-              top[q] = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 1));
-            }
+              for (int e = 0; e < 8; ++e)
+                m[q] = max_nan(m[q], fabsf(f[8 * q + e]));
+            const float top = max_nan(
+                odd ? m[1] : m[0],
+                __shfl_xor_sync(0xffffffffu, odd ? m[0] : m[1], 1));
+            const Fp4Scale sc = fp4_scale(top, scale, sixth);
+            const float other = __shfl_xor_sync(0xffffffffu, sc.inv, 1);
             if (!on) return;
             uint8_t* sf = (value ? p.v_sf : p.k_sf) + frow + h * p.f_sh;
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-              const int ch = q ? cb : ca;
-              const Fp4Scale sc = fp4_scale(top[q], scale, sixth);
-              *reinterpret_cast<uint32_t*>(dst + 4 * ch) =
-                  fp4_codes8(f + 8 * q, sc.inv);
-              if (!(ch & 1)) sf[ch >> 1] = static_cast<uint8_t>(sc.code);
-            }
+            *reinterpret_cast<uint32_t*>(dst + 4 * ca) =
+                fp4_codes8(f, odd ? other : sc.inv);
+            *reinterpret_cast<uint32_t*>(dst + 4 * cb) =
+                fp4_codes8(f + 8, odd ? sc.inv : other);
+            sf[(odd ? cb : ca) >> 1] = static_cast<uint8_t>(sc.code);
           }
         }
       };
