@@ -265,9 +265,10 @@ typedef struct {
   const float* q_scale;
   /* no_pdl != 0: launch every kernel of the call in plain stream order.
    * By default some launches are programmatic dependent launches: the
-   * persistent decode kernel (pkv_set_decode_kernel) depends on the kernel
-   * queued before the call and waits for it (griddepcontrol.wait) before
-   * it reads or writes anything; in a call with both decode-class and
+   * persistent decode kernel (pkv_set_decode_kernel) and the decode kernel
+   * of a 4-bit cache (with its join or combine) depend on the kernel
+   * queued before the call and wait for it (griddepcontrol.wait) before
+   * they read or write anything; in a call with both decode-class and
    * prefill-class requests, the second of the two attention kernels (and
    * the split combine after it) may start while the first still runs, and
    * its grid ends only after the first one's.  The first form is correct
@@ -390,7 +391,10 @@ PKV_API pkv_status pkv_dequantize_fp4_cache(
  * pkv_set_decode_kernel does not apply); prefill-class requests read them
  * through an exact 16-bit copy of their pages in the workspace.  An fp8 cache
  * or query or non-paged keys in opts: PKV_ERR_UNSUPPORTED.
- * workspace: pkv_paged_attention_workspace_size_fp4 bytes.
+ * workspace: pkv_paged_attention_workspace_size_fp4 bytes: the split partials
+ * or the page copies, then room for the parts of the decode kernel's equal
+ * shares.  Without that tail a request's KV head is worked through by one
+ * block.  Nothing in it has to be set before a call or kept after one.
  */
 PKV_API size_t pkv_paged_attention_workspace_size_fp4(
     int batch, int total_q, int max_seqlen_q, int max_seqlen_k,

@@ -10,9 +10,20 @@
 // and the output, as they do for E4M3 caches.
 //
 // All three kernels stream: HBM bounds them (the write reads 2 D and writes
-// D / 2 + D / 16 bytes a row, the read-back the reverse).  A thread owns one
-// group of 16 values, so a group's maximum, its scale and its codes never
-// leave the thread.
+// D / 2 + D / 16 bytes a row, the read-back the reverse).
+//
+// The write: a thread owns one group of 16 values, so a group's maximum, its
+// scale and its codes never leave the thread; the next group loads while one
+// is quantized (its row does not wait for its slot), three blocks of 256
+// threads an SM.  Measured on a GB300 whose copy reaches 6.79 TB/s: 11207
+// tokens of 8 heads, D 128, 14.9 us back to back (3.95 TB/s; 18.4 us without
+// the loads ahead), of which a launch is about 3; 124 tokens 4.8 us, all
+// latency.
+//
+// The read-back: a thread turns 8 codes into 16 bytes and has four rows of
+// each matrix loading at once; the page copy of 8 prompts (20 MB of codes
+// into 83 MB) costs 24 us before the prefill kernel, 31 with 16 values a
+// thread and one row at a time.
 #include "pkv_common.cuh"
 
 namespace pkv {

@@ -13,9 +13,19 @@
 // so a row's bits depend neither on the kernel that takes it nor on the rows
 // beside it: a row that is quantized next has the same codes everywhere.
 //
-// HBM bounds it: a row is read once and written once (2 D + 2 D bytes for 16
-// bits), and the table row of a token is read once per warp that works on
-// the token.
+// A row is read once and written once (2 D + 2 D bytes for 16 bits), and the
+// table row of a token once per warp that works on the token: HBM would bound
+// it, and the instructions (about 17 a value) nearly do too.  Measured on a
+// GB300 whose copy reaches 6.79 TB/s, back to back: 11207 tokens of 32/8
+// heads, D 128, with norms into the 4-bit cache 48.5 us (5.1 TB/s, issue
+// slots 65 % busy, 11 % of the SM time in the last wave of blocks), 8103
+// tokens of 16/8 heads, D 256, into E4M3 47.3 us (5.1 TB/s), 8192 of them
+// with 3 axes and no cache 45.3 us (4.6 TB/s); 64 tokens 5.4 us, all latency.
+// What it took from 97, 85 and 60 us: packed float32 pairs, weights and
+// table entries kept in registers over a token's rows, rows copied two
+// passes ahead, quotients by a rounded reciprocal, pointers that walk.
+// Measured and not kept: the token cut in two (3 axes 51 us against 45),
+// three or more passes ahead (the same), six blocks an SM (spills).
 //
 // rope_kernel: a lane owns the 8-value chunks A and B of a row, rot / 2 apart,
 // so that a rotation never leaves the lane and every load and store of a row
