@@ -349,7 +349,8 @@ typedef struct {
  * each rounded to nearest, ties to even, and saturated (448 and 6); a group
  * whose scale rounds to 0 has codes 0.  A NaN in a group makes its block
  * scale NaN: the whole group reads back as NaN.  Slots, padding and
- * num_tokens behave as in pkv_reshape_and_cache.
+ * num_tokens behave as in pkv_reshape_and_cache; slots (but the negative ones)
+ * have to differ: a slot given twice keeps codes and scales of either token.
  * key, value: 16-bit rows on 16-byte boundaries; head_size a multiple of 64
  *   (PKV_ERR_UNSUPPORTED otherwise).
  */
@@ -491,7 +492,8 @@ PKV_API pkv_status pkv_qk_norm_rope(
  * Every token's q rows go to q_out (also those whose slot is negative, a
  * token whose keys are kept elsewhere); key and value rows of the tokens
  * with a slot go to the cache as pkv_reshape_and_cache places them.  A key is
- * rounded once, from float32 to the cache's type.  kv_cache_dtype: "auto",
+ * rounded once, from float32 to the cache's type; slots (but the negative
+ * ones) have to differ.  kv_cache_dtype: "auto",
  * "fp8" / "fp8_e4m3" (k_scale, v_scale) or "fp4" (`fp4`, with cache_strides
  * in bytes; head_size a multiple of 64 there).
  */

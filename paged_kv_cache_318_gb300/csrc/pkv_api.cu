@@ -4,6 +4,7 @@
 // anything; invalid calls return a pkv_status and a per-thread message and
 // launch nothing.  Kernels never trap: out-of-range indices are skipped and
 // recorded in a device error word (pkv_check_device_errors reads it).
+#include <algorithm>
 #include <math.h>
 #include <stdarg.h>
 #include <stdio.h>
@@ -803,7 +804,7 @@ pkv_status attention_impl(
     // (the decode kernel's offsets inside a block are 32-bit)
     auto in_block = [&](const int64_t* s) {
       return s[0] >= 0 && s[0] <= INT32_MAX && s[1] >= 0 &&
-             s[1] * block_size <= INT32_MAX;
+             s[1] <= INT32_MAX / block_size;
     };
     if (!in_block(cache_strides) || !in_block(fp4->strides))
       return fail(PKV_ERR_UNSUPPORTED,
@@ -820,8 +821,9 @@ pkv_status attention_impl(
       !stride16(cache_strides[1], cb) || !stride16(cache_strides[2], cb))
     return fail(PKV_ERR_UNSUPPORTED,
                 "q/out/cache rows must start on 16-byte boundaries");
-  const int wl = window_left < 0 ? -1 : window_left;
-  const int wr = window_right < 0 ? -1 : window_right;
+  // (the kernels add a window to a position: 2^30 reaches as far as any)
+  const int wl = window_left < 0 ? -1 : std::min(window_left, 1 << 30);
+  const int wr = window_right < 0 ? -1 : std::min(window_right, 1 << 30);
 
   unsigned* err = nullptr;
   int sms = 0;
@@ -960,7 +962,6 @@ pkv_status attention_impl(
   p.k_scale = kv8 ? opts->k_scale : nullptr;
   p.v_scale = kv8 ? opts->v_scale : nullptr;
   if (kv4) {
-    p.kv_fp4 = 1;
     p.k_scale = fp4->k_scale;
     p.v_scale = fp4->v_scale;
     p.k_sf = static_cast<const uint8_t*>(fp4->k_block_scale);

@@ -227,7 +227,6 @@ struct AttnParams {
   // 4-bit cache: kc / vc hold two E2M1 codes a byte (c_sb, c_sr, c_sh in
   // bytes), and these the E4M3 scales of each 16 values of a row (strides
   // in bytes); value = code * block scale * (*k_scale)
-  int kv_fp4;
   const uint8_t* k_sf;
   const uint8_t* v_sf;
   int64_t f_sb, f_sr, f_sh;

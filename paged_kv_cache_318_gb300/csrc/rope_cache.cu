@@ -286,7 +286,7 @@ rope_kernel(const RopeLaunch p, int parts) {
       if (left > 0) {
         // (the last pass of a kind may have fewer rows)
         const int bytes = left > 1 || (kind == 0 ? q_last : k_last) ? 16 : 0;
-        const T* at = bytes ? src : static_cast<const T*>(p.q);
+        const T* at = bytes ? src : static_cast<const T*>(p.k);
         const uint32_t dst = mine + (i % kDepth) * (kThreads * 32);
         cp_async_16(dst, at, bytes);
         cp_async_16(dst + kThreads * 16, at + 8 * (cb - ca), bytes);

@@ -51,7 +51,7 @@ class RopeParams(ctypes.Structure):
 
 def rope(**kw):
     r = RopeParams(positions=P, position_axis_stride=8, num_axes=1,
-                        cos_sin=P, cos_sin_stride=128, max_position=100,
+                   cos_sin=P, cos_sin_stride=128, max_position=100,
                         cos_sin_f32=1, rot_dim=128, is_neox=1, q_weight=P,
                         k_weight=P, eps=1e-6, weight_offset=0.0)
     for k, v in kw.items():
@@ -155,6 +155,7 @@ def attend(lib, **kw):
     (dict(NB=0), 1, b"no blocks"),
     (dict(cs=strides(1 << 31, 64, 1024, 1)), 2, b"2 GB"),
     (dict(cs=strides(4096, 1 << 28, 1024, 1)), 2, b"2 GB"),
+    (dict(cs=strides(4096, 1 << 60, 1024, 1)), 2, b"2 GB"),
 ])
 def test_attention_refuses(lib, kw, status, text):
     assert attend(lib, **kw) == status

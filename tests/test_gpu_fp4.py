@@ -439,6 +439,37 @@ def test_understated_query_length(cuda_device):
     assert (out[1:] == 7).all() and not (out[0] == 7).all()
 
 
+@pytest.mark.parametrize("q_lens,num_splits", [([1, 2], 0), ([1, 2], 3),
+                                               ([40, 1], 0)])
+def test_the_widest_windows(cuda_device, q_lens, num_splits):
+    """Windows up to the largest int hide nothing."""
+    dev = cuda_device
+    wl = workloads.build_workload("w4", 5, q_lens, [700, 2500], 8, 2, 128, 16,
+                                  causal=False, num_splits=num_splits)
+    cache = fill(wl, dev)
+    want = attend(wl, dev, cache)
+    check(wl, want[0], want[1], oracle_cache(wl)[1])
+    for window in ((2 ** 31 - 1, 2 ** 31 - 1), (-1, 2 ** 31 - 1),
+                   (2 ** 31 - 1, -1)):
+        out, lse = attend(wl, dev, cache, window_size=window)
+        check(wl, out, lse, oracle_cache(wl)[1])
+
+
+@pytest.mark.parametrize("which", ["PREFILL_TCGEN05", "PREFILL_MMA_SYNC"])
+def test_both_prefill_kernels(cuda_device, which):
+    dev = cuda_device
+    wl = workloads.build_workload("p4", 6, [70, 1, 200], [600, 900, 200], 8, 2,
+                                  128, 16, window_size=(300, -1))
+    cache = fill(wl, dev)
+    api.set_prefill_kernel(getattr(api, which))
+    try:
+        out, lse = attend(wl, dev, cache)
+        api.check_device_errors(dev)
+    finally:
+        api.set_prefill_kernel(api.PREFILL_TCGEN05)
+    check(wl, out, lse, oracle_cache(wl)[1])
+
+
 def test_padded_rows_stay(cuda_device):
     """Rows of q and out behind the last sequence are left as they were."""
     dev = cuda_device

@@ -121,6 +121,12 @@ CASES = [
     # many tokens: several passes a warp, a partly filled last block
     dict(T=1031, Hq=4, Hkv=2, D=64, max_pos=2000),
     dict(T=5003, Hq=3, Hkv=1, D=128, max_pos=2000),
+    # keys alone, the last pass of each kind partly filled
+    dict(T=5, Hq=0, Hkv=3), dict(T=5, Hq=0, Hkv=5, D=256, rot=64),
+    dict(T=5003, Hq=5, Hkv=3, D=256, max_pos=2000),
+    # more tokens than the grid takes at once
+    dict(T=40003, Hq=1, Hkv=1, D=64, max_pos=2000),
+    dict(T=6001, Hq=7, Hkv=1, D=8, max_pos=2000),
 ]
 
 
