@@ -69,9 +69,9 @@ namespace dfp4 {
 
 constexpr int kWarps = 4;
 constexpr float kRaise = 6.f;      // log2 slack of the running maximum
-// Tiles of a CTA's share at least, so that each warp has some.
+// Tiles of a group's share at least, so that each warp has some.
 constexpr int kMinTiles = 2 * kWarps;
-// What a unit costs a CTA beside its tiles, in tiles: its queries, the join of
+// What a unit costs a group beside its tiles, in tiles: its queries, the join of
 // the warps' states and the store.  (64 requests of 512-4096 keys, 32/8 heads:
 // 0 tiles 55.9 us, 4 51.3, 8 49.8, 12 50.4, 16 51.3.)
 constexpr int kUnitCost = 8;
@@ -198,6 +198,19 @@ __device__ __forceinline__ float soft_cap(float x, float t, float u) {
 
 template <int D, int NR>
 struct Smem {
+  // Groups of kWarps warps on an SM: as many as their registers allow without
+  // spills in the loop.  (9 to 16 rows of D = 128: 2 read 2 requests of 131072
+  // keys, 128/8 heads, in 0.083 ms, 3 with spills in 0.093; of D = 64: 2 take
+  // 0.070 ms on 64 x 4096 keys, 3 take 0.064.)
+  static constexpr int RESIDENT = NR == 1 ? (D == 256 ? 3 : 4)
+                                          : (D == 64 ? 3 : 2);
+  // ... and of a CTA, where each takes a share.  CTAs of one SM run at speeds
+  // of their own, the oldest fastest (of four equal shares of 8 x 131072 keys
+  // the first ended at 153 us and the last at 209); groups of one CTA end
+  // together (at 198).  Where the SM's work bounds the call they also wait
+  // together: 9 to 16 rows 0.088 against 0.083 ms, D = 256 0.211 against
+  // 0.209 on 124 windows of 4096 keys.
+  static constexpr int GROUPS = NR == 1 && D <= 128 ? RESIDENT : 1;
   // query fragments (one 16-byte load serves two k steps of every subtile),
   // the warps' rings, and two warps' states (as their lanes hold them) at
   // the end of a unit
@@ -208,16 +221,8 @@ struct Smem {
   static constexpr int OFF_S =
       OFF_RING + kWarps * Geo<D>::STAGES * Geo<D>::STAGE;
   static constexpr int BYTES = OFF_S + kWarps / 2 * SBYTES;
+  static_assert(BYTES % 128 == 0, "a group's stages are 128-byte aligned");
 };
-
-// Blocks on an SM: as many as their registers allow without spills in the
-// loop.  (9 to 16 rows of D = 128: 2 blocks read 2 requests of 131072 keys,
-// 128/8 heads, in 0.083 ms, 3 with spills in 0.093; of D = 64: 2 blocks 0.070
-// ms on 64 x 4096 keys, 3 blocks 0.064.)
-template <int D, int NR>
-constexpr int min_ctas() {
-  return NR == 1 ? (D == 256 ? 3 : 4) : (D == 64 ? 3 : 2);
-}
 
 // What a request's rows see of its keys.
 struct Req {
@@ -249,7 +254,7 @@ __device__ __forceinline__ Req request(const AttnParams& p, int b,
   return r;
 }
 
-// A run of tiles of one (request, KV head), as a CTA works through it.
+// A run of tiles of one (request, KV head), as a group works through it.
 struct Piece {
   int b, h;
   Req r;
@@ -259,7 +264,9 @@ struct Piece {
 };
 
 template <typename T, int D, int NR>
-__global__ void __launch_bounds__(kWarps * 32, min_ctas<D, NR>())
+__global__ void __launch_bounds__(kWarps * 32 * Smem<D, NR>::GROUPS,
+                                  Smem<D, NR>::RESIDENT /
+                                      Smem<D, NR>::GROUPS)
 decode_fp4_kernel(const AttnParams p, int splits) {
   // the fold of the pieces may become resident once every CTA has started
   // (it waits for this grid before reading them)
@@ -276,24 +283,38 @@ decode_fp4_kernel(const AttnParams p, int splits) {
   constexpr int NT = kWarps * 32;
   // (a cp.async chunk pair that straddles 32 bytes of shared memory costs two
   // L2 sectors: 0.226 against 0.216 ms on 8 x 131072 keys)
-  extern __shared__ __align__(128) unsigned char smem[];
-  __shared__ long long scan[kWarps];
+  extern __shared__ __align__(128) unsigned char all_smem[];
+  constexpr int GR = SM::GROUPS;
+  __shared__ long long scans[GR][kWarps];
   // what the inner loop seldom needs: the piece, and by packed row the token
   // of its request and its ALiBi slope (base 2)
-  __shared__ Piece cur;
-  __shared__ int row_tok[16];
-  __shared__ float row_slope[16];
+  __shared__ Piece pieces[GR];
+  __shared__ int row_toks[GR][16];
+  __shared__ float row_slopes[GR][16];
 
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  // The CTA's groups share nothing: each is what a CTA of its own would be
+  // (one where the call is not a sequence).
+  const int grp = threadIdx.x / NT, tid = threadIdx.x % NT;
+  const int lane = tid & 31, warp = tid >> 5;
   const int g8 = lane >> 2, c4 = lane & 3;
+  unsigned char* const smem = all_smem + grp * SM::BYTES;
+  long long* const scan = scans[grp];
+  Piece& cur = pieces[grp];
+  int* const row_tok = row_toks[grp];
+  float* const row_slope = row_slopes[grp];
+  auto group_sync = [&]() {
+    asm volatile("bar.sync %0, %1;" ::"r"(grp + 1), "n"(NT) : "memory");
+  };
   const int G = p.G;
   const bool sequence = p.sk_chunks > 0;
+  // a share that begins inside a unit: the unit, its first token and rows
+  int4* const marks = reinterpret_cast<int4*>(p.sk_marks);
   const float base_scale = p.scale * *p.k_scale * kLog2e;
   const float vscale = *p.v_scale;
 
-  // ---- this CTA's first piece
+  // ---- the group's first piece
   Piece pc;
-  int left = 0;          // what of the CTA's share is past this piece's unit
+  int left = 0;          // what of its share is past this piece's unit
   auto tiles_of = [&](const Req& r) {
     const int k0 = r.lo & ~15;
     return r.rows == 0 ? 0 : max(1, (r.hi - k0 + KT - 1) / KT);
@@ -304,7 +325,7 @@ decode_fp4_kernel(const AttnParams p, int splits) {
     const unsigned rest = blockIdx.x / p.Hkv;
     const int sp = rest % splits;
     pc.b = rest / splits;
-    pc.r = request(p, pc.b, 8 * NR, sp == 0 && pc.h == 0 && threadIdx.x == 0);
+    pc.r = request(p, pc.b, 8 * NR, sp == 0 && pc.h == 0 && tid == 0);
     if (pc.r.rows == 0) return;
     pc.slot = -1;
     if (p.chunk > 0) {
@@ -325,16 +346,16 @@ decode_fp4_kernel(const AttnParams p, int splits) {
     pc.t1 = tiles_of(pc.r);
   } else {
     // The units (request, KV head) in order, each kUnitCost and its tiles
-    // long, form a sequence of length N, of which every CTA takes an equal
+    // long, form a sequence of length N, of which every group takes an equal
     // run (the tiles in it).  Thread t adds up a run of requests; the one
-    // whose run holds the start of the CTA's share finds it.
+    // whose run holds the start of the group's share finds it.
     const int per = (p.batch + NT - 1) / NT;
-    const int b_lo = min(p.batch, static_cast<int>(threadIdx.x) * per);
+    const int b_lo = min(p.batch, tid * per);
     const int b_hi = min(p.batch, b_lo + per);
     long long sum = 0;
     Req mine_req{};
     for (int b = b_lo; b < b_hi; ++b) {
-      mine_req = request(p, b, p.sk_rows, blockIdx.x == 0);
+      mine_req = request(p, b, p.sk_rows, blockIdx.x == 0 && grp == 0);
       if (mine_req.rows > 0)
         sum += static_cast<long long>(kUnitCost + tiles_of(mine_req)) * p.Hkv;
     }
@@ -345,18 +366,18 @@ decode_fp4_kernel(const AttnParams p, int splits) {
       if (lane >= o) incl += v;
     }
     if (lane == 31) scan[warp] = incl;
-    __syncthreads();
+    group_sync();
     long long N = 0, excl = incl - sum;
     for (int w = 0; w < kWarps; ++w) {
       if (w < warp) excl += scan[w];
       N += scan[w];
     }
-    // at least kMinTiles tiles a CTA
+    // at least kMinTiles tiles a group
     const long long Cs =
         max(1LL, min(static_cast<long long>(p.sk_chunks), N / kMinTiles));
-    const int c = blockIdx.x;
+    const int c = blockIdx.x * GR + grp;
     if (c >= Cs || N == 0) {
-      if (threadIdx.x == 0) p.sk_marks[c] = make_int2(-1, -1);
+      if (tid == 0) marks[c] = make_int4(-1, 0, 0, 0);
       return;
     }
     auto bound = [&](long long k) -> long long {     // (32-bit where it can)
@@ -385,7 +406,7 @@ decode_fp4_kernel(const AttnParams p, int splits) {
         at += all;
       }
     }
-    __syncthreads();
+    group_sync();
     pc = cur;
     pc.kt0 = pc.r.lo & ~15;
     const int n = tiles_of(pc.r);
@@ -394,21 +415,18 @@ decode_fp4_kernel(const AttnParams p, int splits) {
     pc.t0 = max(0, pc.t0 - kUnitCost);
     left = static_cast<int>(end - n);
     if (pc.t1 <= 0) {                    // none of the unit's tiles
-      if (threadIdx.x == 0) p.sk_marks[c] = make_int2(-1, -1);
+      if (tid == 0) marks[c] = make_int4(-1, 0, 0, 0);
       return;
     }
-    __syncthreads();                     // (`cur` is written again)
+    group_sync();                     // (`cur` is written again)
     // a unit cut by the share's ends leaves its part in slot 2 c (begun
     // before) or 2 c + 1 (ending after)
     pc.slot = pc.t0 > 0 ? 2 * c : pc.t1 < n ? 2 * c + 1 : -1;
-    if (threadIdx.x == 0) {
-      p.sk_marks[c].x = pc.t0 > 0 ? pc.b * p.Hkv + pc.h : -1;
-      if (left <= kUnitCost)
-        p.sk_marks[c].y =
-            pc.t0 == 0 && pc.t1 < n ? pc.b * p.Hkv + pc.h : -1;
-    }
+    if (tid == 0)
+      marks[c] = make_int4(pc.t0 > 0 ? pc.b * p.Hkv + pc.h : -1, pc.r.q0,
+                           pc.r.rows, 0);
   }
-  // the piece after `a` in the CTA's share (left > kUnitCost)
+  // the piece after `a` in the group's share (left > kUnitCost)
   auto next_piece = [&](const Piece& a) {
     Piece x = a;
     if (++x.h == p.Hkv) {
@@ -423,9 +441,7 @@ decode_fp4_kernel(const AttnParams p, int splits) {
     x.t0 = 0;
     x.t1 = min(n, left - kUnitCost);
     left -= kUnitCost + n;
-    x.slot = x.t1 < n ? 2 * static_cast<int>(blockIdx.x) + 1 : -1;
-    if (left <= kUnitCost && threadIdx.x == 0)
-      p.sk_marks[blockIdx.x].y = x.t1 < n ? x.b * p.Hkv + x.h : -1;
+    x.slot = x.t1 < n ? 2 * static_cast<int>(blockIdx.x * GR + grp) + 1 : -1;
     return x;
   };
 
@@ -546,7 +562,7 @@ decode_fp4_kernel(const AttnParams p, int splits) {
     return v_rd + stage + (static_cast<int>((e ^ c4) - c4) * GE::RB);
   };
 
-  if (threadIdx.x < 16) row_tok[threadIdx.x] = threadIdx.x / G;
+  if (tid < 16) row_tok[tid] = tid / G;
   const bool plain = p.softcap <= 0.f && p.alibi == nullptr;
   const float cap_t = p.softcap * kLog2e;
   const float cap_u = p.softcap > 0.f ? 2.f / p.softcap : 0.f;
@@ -582,12 +598,10 @@ decode_fp4_kernel(const AttnParams p, int splits) {
   load_queries(pc, pc.r.rows);
   begin_copies();
   for (;;) {
-    if (threadIdx.x == 0) cur = pc;
-    if (p.alibi && threadIdx.x < 16)
-      row_slope[threadIdx.x] =
-          threadIdx.x < pc.r.rows
-              ? p.alibi[pc.h * G + threadIdx.x % G] * kLog2e
-              : 0.f;
+    if (tid == 0) cur = pc;
+    if (p.alibi && tid < 16)
+      row_slope[tid] =
+          tid < pc.r.rows ? p.alibi[pc.h * G + tid % G] * kLog2e : 0.f;
     uint64_t row_scale[NR];   // logit scales (base 2), rows 2 c4, 2 c4 + 1
 #pragma unroll
     for (int n = 0; n < NR; ++n) {
@@ -631,7 +645,7 @@ decode_fp4_kernel(const AttnParams p, int splits) {
               make_uint4(f[0], f[1], f[2], f[3]);
       }
     }
-    __syncthreads();
+    group_sync();
 
     // my tiles i0 <= it < i1 are seen whole by every row
     int i0, i1;
@@ -1070,10 +1084,10 @@ decode_fp4_kernel(const AttnParams p, int splits) {
     };
     if (warp >= 2) put(state);
     if (more_pieces) begin_copies();
-    __syncthreads();
+    group_sync();
     if (warp < 2) join(state);
     if (warp == 1) put(state);
-    __syncthreads();
+    group_sync();
     if (warp == 0) {
       join(state + SM::SBYTES / 16);
       // lane (g8, c4) holds, of rows 2 c4 and 2 c4 + 1, the runs of 16 (D =
@@ -1218,22 +1232,28 @@ fold_kernel(const AttnParams p) {
   __shared__ int reach[2];
   __shared__ float row_base[16], row_inv[16], row_lse[16];
   __shared__ float4 part[kFoldThreads];
+  const int4* const marks = reinterpret_cast<const int4*>(p.sk_marks);
   const int c = blockIdx.x + 1;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int u = p.sk_marks[c].x;
+  // the run of shares around c that mark its unit: the lower half of the
+  // threads looks back, the upper half on (the first step's marks load beside
+  // c's own)
+  const int dir = tid < HALF ? -1 : 1, i_th = tid < HALF ? tid : tid - HALF;
+  auto unit_at = [&](int at) {
+    return at < 0 || at >= p.sk_chunks ? -1 : marks[at].x;
+  };
+  const int4 mark = marks[c];
+  int near = unit_at(c + dir * (1 + i_th));
+  const int u = mark.x;
   if (u < 0) return;
-  // the run of shares around c that mark u: the lower half of the threads
-  // looks back, the upper half on
   int first = c, last = c;
   {
-    const int dir = tid < HALF ? -1 : 1, i = tid < HALF ? tid : tid - HALF;
     bool open[2] = {true, true};
     for (int step = 1; open[0] || open[1]; step += HALF) {
       if (tid < 2) reach[tid] = HALF;
       __syncthreads();
-      const int at = c + dir * (step + i);
-      if (at < 0 || at >= p.sk_chunks || p.sk_marks[at].x != u)
-        atomicMin(&reach[tid < HALF ? 0 : 1], i);
+      if (step > 1) near = unit_at(c + dir * (step + i_th));
+      if (near != u) atomicMin(&reach[tid < HALF ? 0 : 1], i_th);
       __syncthreads();
       const int back = reach[0], on = reach[1];
       if (open[0]) first -= back;
@@ -1244,10 +1264,7 @@ fold_kernel(const AttnParams p) {
     }
   }
   const int np = last - first + 2;       // parts, shares first - 1 .. last
-  const int b = u / p.Hkv, h = u - b * p.Hkv;
-  const int q0 = p.cu_q[b];
-  const int q_len = min(p.cu_q[b + 1] - q0, p.total_q - q0);
-  const int rows = min(q_len * p.G, p.sk_rows);
+  const int h = u % p.Hkv, q0 = mark.y, rows = mark.z;
   // (one linear expression: `k == 0 ? a : b` gave a wrong slot for parts 32
   // .. 63 in the unrolled sum of units with more than 128 parts)
   auto row_of = [&](int k, int r) -> int64_t {
@@ -1259,16 +1276,28 @@ fold_kernel(const AttnParams p) {
   const int per = (all + np - 2) / (np - 1);
   const int i0 = (c - first) * per, i1 = min(all, i0 + per);
   if (i0 >= i1) return;
+  const int width = min(i1 - i0, kFoldThreads);
+  const int kg = kFoldThreads / width;
+  const int grp = tid / width, in = tid - grp * width;
+  // the thread's first values are on their way while the rows' sums are taken
+  float4 ahead = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (grp < kg && grp < np) {
+    const int i = i0 + in, r = i / (D / 4);
+    ahead = *reinterpret_cast<const float4*>(
+        p.part_o + row_of(grp, r) * D + (i - r * (D / 4)) * 4);
+  }
   const int r0 = i0 / (D / 4), r1 = (i1 - 1) / (D / 4);
   for (int r = r0 + warp; r <= r1; r += kFoldThreads / 32) {
-    float M = -INFINITY;
-    for (int k = lane; k < np; k += 32) M = fmaxf(M, p.part_lse[row_of(k, r)]);
+    const float mine = lane < np ? p.part_lse[row_of(lane, r)] : -INFINITY;
+    float M = mine;
+    for (int k = lane + 32; k < np; k += 32)
+      M = fmaxf(M, p.part_lse[row_of(k, r)]);
 #pragma unroll
     for (int o = 16; o; o >>= 1)
       M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
     const float base = M == -INFINITY ? 0.f : M * kLog2e;
-    float sum = 0.f;
-    for (int k = lane; k < np; k += 32)
+    float sum = ex2(mine * kLog2e - base);
+    for (int k = lane + 32; k < np; k += 32)
       sum += ex2(p.part_lse[row_of(k, r)] * kLog2e - base);
 #pragma unroll
     for (int o = 16; o; o >>= 1)
@@ -1283,9 +1312,6 @@ fold_kernel(const AttnParams p) {
     }
   }
   __syncthreads();
-  const int width = min(i1 - i0, kFoldThreads);
-  const int kg = kFoldThreads / width;
-  const int grp = tid / width, in = tid - grp * width;
   for (int ib = i0; ib < i1; ib += width) {
     const int i = ib + in;
     const bool on = i < i1 && grp < kg;
@@ -1297,7 +1323,9 @@ fold_kernel(const AttnParams p) {
       for (int k = grp; k < np; k += kg) {
         const int64_t at = row_of(k, r);
         const float4 v =
-            *reinterpret_cast<const float4*>(p.part_o + at * D + col);
+            ib == i0 && k == grp
+                ? ahead
+                : *reinterpret_cast<const float4*>(p.part_o + at * D + col);
         const float w = ex2(p.part_lse[at] * kLog2e - base);  // -inf -> 0
         if (w == 0.f) continue;
         acc.x += w * v.x;
@@ -1338,17 +1366,20 @@ cudaError_t launch(const AttnParams& p, int splits, bool pdl,
                    cudaStream_t stream) {
   using SM = Smem<D, NR>;
   auto kern = decode_fp4_kernel<T, D, NR>;
-  cudaError_t e = smem_opt_in(reinterpret_cast<const void*>(kern), SM::BYTES);
+  cudaError_t e = smem_opt_in(reinterpret_cast<const void*>(kern),
+                              SM::GROUPS * SM::BYTES);
   if (e != cudaSuccess) return e;
+  // a share a group; else one group a unit
+  const int groups = p.sk_chunks > 0 ? SM::GROUPS : 1;
   const int64_t ctas =
-      p.sk_chunks > 0 ? p.sk_chunks
+      p.sk_chunks > 0 ? p.sk_chunks / groups
                       : static_cast<int64_t>(p.batch) * splits * p.Hkv;
   if (ctas > 0x7fffffff) return cudaErrorInvalidConfiguration;
   note_launch();
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(ctas));
-  cfg.blockDim = dim3(kWarps * 32);
-  cfg.dynamicSmemBytes = SM::BYTES;
+  cfg.blockDim = dim3(kWarps * 32 * groups);
+  cfg.dynamicSmemBytes = SM::BYTES * groups;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1380,8 +1411,16 @@ cudaError_t dispatch(const AttnParams& p, int D, int splits, bool pdl,
 
 }  // namespace dfp4
 
-int decode_fp4_ctas_per_sm(int D, int rows) {
-  return rows <= 8 ? (D == 256 ? 3 : 4) : (D == 64 ? 3 : 2);
+int decode_fp4_resident(int D, int rows) {
+  const bool one = rows <= 8;
+  switch (D) {
+    case 64:
+      return one ? dfp4::Smem<64, 1>::RESIDENT : dfp4::Smem<64, 2>::RESIDENT;
+    case 128:
+      return one ? dfp4::Smem<128, 1>::RESIDENT : dfp4::Smem<128, 2>::RESIDENT;
+    default:
+      return one ? dfp4::Smem<256, 1>::RESIDENT : dfp4::Smem<256, 2>::RESIDENT;
+  }
 }
 
 cudaError_t launch_decode_attn_fp4(const AttnParams& p, int D, bool bf16,
@@ -1441,7 +1480,7 @@ cudaError_t launch_decode_attn_fp4_shares(const AttnParams& p, int D,
 size_t decode_fp4_shares_bytes(int D, int ctas, int rows) {
   const size_t slots = static_cast<size_t>(2) * ctas;
   return dfp4::up256(slots * rows * D * 4) + dfp4::up256(slots * rows * 4) +
-         dfp4::up256(static_cast<size_t>(ctas) * 8);
+         dfp4::up256(static_cast<size_t>(ctas) * 16);
 }
 
 cudaError_t launch_fp4_combine(const CombineParams& p, bool bf16, bool pdl,

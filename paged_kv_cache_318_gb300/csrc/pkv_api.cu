@@ -131,7 +131,7 @@ int fp4_splits(int batch, int max_q, int G, int Hkv, int D, int64_t range,
   const int64_t units = static_cast<int64_t>(batch) * Hkv;
   const int64_t slots =
       static_cast<int64_t>(sms) *
-      decode_fp4_ctas_per_sm(D, rows < kDecodeRows ? static_cast<int>(rows)
+      decode_fp4_resident(D, rows < kDecodeRows ? static_cast<int>(rows)
                                                    : kDecodeRows);
   int64_t s = slots / units;
   const int64_t most = (range + 255) / 256;
@@ -289,7 +289,7 @@ bool fp4_shares(const Plan& pl, int num_splits, int fixed_split) {
          pl.range > kFp4UnitKeys;
 }
 int fp4_ctas(int D, int rows, int sms) {
-  return sms * decode_fp4_ctas_per_sm(D, rows);
+  return sms * decode_fp4_resident(D, rows);
 }
 
 // Workspace layout: the required part (decode split partials, fp8 page

@@ -400,8 +400,8 @@ cudaError_t launch_decode_attn_fp4_shares(const AttnParams& p, int D,
                                           bool bf16, int ctas, bool pdl,
                                           void* scratch, cudaStream_t stream);
 size_t decode_fp4_shares_bytes(int D, int ctas, int rows);
-// Resident CTAs of that kernel per SM for `rows` packed query rows.
-int decode_fp4_ctas_per_sm(int D, int rows);
+// Groups of 4 warps that an SM holds for `rows` packed query rows.
+int decode_fp4_resident(int D, int rows);
 
 // Head norms, rotation and cache append (rope_cache.cu).
 enum RopeStore : int {
