@@ -147,6 +147,17 @@ __device__ __forceinline__ void cp_async_n(uint32_t dst, const void* src,
                  "l"(src), "r"(src_bytes), "n"(N));
 }
 
+// 16 bytes that this call reads once: first to leave L2, so that what other
+// kernels read stays there (and this one's tables: 64 requests of 512-4096
+// keys 47.5 us against 50.0 with plain copies, 8 x 131072 the same).
+__device__ __forceinline__ void cp_async_once(uint32_t dst, const void* src,
+                                              int src_bytes, uint64_t policy) {
+  asm volatile(
+      "cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;\n" ::"r"(
+          dst),
+      "l"(src), "r"(src_bytes), "l"(policy));
+}
+
 // One half of an f16x2 in both.
 __device__ __forceinline__ uint32_t spread(uint32_t v, int high) {
   const __half2 x = *reinterpret_cast<const __half2*>(&v);
@@ -490,6 +501,8 @@ decode_fp4_kernel(const AttnParams p, int splits) {
       id = -1;
     }
   };
+  uint64_t policy;
+  asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
   auto issue = [&](int s0, uint32_t stage) {
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
@@ -502,8 +515,8 @@ decode_fp4_kernel(const AttnParams p, int splits) {
 #pragma unroll
       for (int j = 0; j < NC; ++j) {
         const uint8_t* ks = src + j * RI * c_sr;
-        cp_async_16(stage + k_dst[j] + i * GE::SUB, ks, n);
-        cp_async_16(stage + v_dst[j] + i * GE::SUB, ks + k_to_v, n);
+        cp_async_once(stage + k_dst[j] + i * GE::SUB, ks, n, policy);
+        cp_async_once(stage + v_dst[j] + i * GE::SUB, ks + k_to_v, n, policy);
       }
       cp_async_n<D / 16>(stage + f_dst + i * (D / 16),
                          SF + static_cast<uint64_t>(page) * f_sb + row * f_sr,
