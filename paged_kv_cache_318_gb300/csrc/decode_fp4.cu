@@ -40,19 +40,21 @@
 // What bounds it: 2 Hkv (D / 2 + D / 16) bytes a key from HBM, then the SM's
 // own work, about 590 instructions for a warp's 32 keys (128 conversions, 128
 // scalings, 32 MMAs at 8 rows).  Measured on a GB300 whose copy reaches 6.79
-// TB/s, back to back: 8 requests of 131072 keys, 64/8 heads, D 128, 0.211 ms
-// (5.7 TB/s, 84 %); 124 windows of 4096 keys, two tokens each, 16/8 heads, D
-// 256, soft-cap, 0.209 ms (5.3 TB/s, 79 %); 64 requests of 512-4096 keys,
-// 32/8 heads, 0.050 ms (3.7 TB/s: about 20 us of it are the launch, the first
-// pages, the changes of unit and the join); 2 requests of 131072 keys, 128/8
-// heads (16 rows), 0.083 ms (3.6 TB/s: 655 instructions a tile from two warps
-// a scheduler that wait on their own chains).  The steps, on the first of
-// these: codes loaded straight into registers 0.390 ms, each warp's ring
+// TB/s, back to back: 8 requests of 131072 keys, 64/8 heads, D 128, 0.203 ms
+// (6.0 TB/s, 88 %); 124 windows of 4096 keys, two tokens each, 16/8 heads, D
+// 256, soft-cap, 0.209 ms (5.4 TB/s, 79 %); 64 requests of 512-4096 keys,
+// 32/8 heads, 0.0475 ms (3.9 TB/s: 3 us go to the launch, 3 to finding the
+// share, 3 to the first pages and 6 to the join); 2 requests of 131072 keys,
+// 128/8 heads (16 rows), 0.080 ms (3.8 TB/s: 655 instructions a tile from two
+// warps a scheduler that wait on their own chains).  The steps, on the first
+// of these: codes loaded straight into registers 0.390 ms, each warp's ring
 // 0.269, equal shares and 128-byte aligned stages 0.216, warps' states joined
-// pairwise so that 4 blocks fit an SM 0.211.  Measured and not kept: equal
-// shares for warps instead of blocks (0.222), 3 blocks an SM (the same), more
-// stages for 9 to 16 rows (the same), subtiles of 16 keys one after the other
-// there (0.098 against 0.083).
+// pairwise so that 4 groups fit an SM 0.211, these as one CTA 0.203.  Measured
+// and not kept: equal shares for warps (0.222), 3 groups an SM (the same),
+// shares cut so that an SM's groups take pieces as they finish (0.253), larger
+// shares for an SM's older CTAs (0.217 to 0.229), more stages for 9 to 16 rows
+// (the same), subtiles of 16 keys one after the other there (0.098 against
+// 0.083).
 //
 // Keys outside [lo, hi) of the request are never seen: their logits are
 // -inf and their V scales 0 (a code is always finite, only a scale can be
@@ -71,9 +73,10 @@ constexpr int kWarps = 4;
 constexpr float kRaise = 6.f;      // log2 slack of the running maximum
 // Tiles of a group's share at least, so that each warp has some.
 constexpr int kMinTiles = 2 * kWarps;
-// What a unit costs a group beside its tiles, in tiles: its queries, the join of
-// the warps' states and the store.  (64 requests of 512-4096 keys, 32/8 heads:
-// 0 tiles 55.9 us, 4 51.3, 8 49.8, 12 50.4, 16 51.3.)
+// What a unit costs a group beside its tiles, in tiles: its queries, the join
+// of the warps' states and the store.  (64 requests of 512-4096 keys, 32/8 heads:
+// 0 tiles 55.9 us, 4 51.3, 8 49.8, 12 50.4, 16 51.3; later 4 49.3, 8 47.5, 12
+// 47.5.)
 constexpr int kUnitCost = 8;
 constexpr int kFoldThreads = 256;
 
@@ -153,9 +156,8 @@ __device__ __forceinline__ void cp_async_n(uint32_t dst, const void* src,
 __device__ __forceinline__ void cp_async_once(uint32_t dst, const void* src,
                                               int src_bytes, uint64_t policy) {
   asm volatile(
-      "cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;\n" ::"r"(
-          dst),
-      "l"(src), "r"(src_bytes), "l"(policy));
+      "cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;\n"
+      ::"r"(dst), "l"(src), "r"(src_bytes), "l"(policy));
 }
 
 // One half of an f16x2 in both.
@@ -739,7 +741,8 @@ decode_fp4_kernel(const AttnParams p, int splits) {
         uint4 qb[NR];
 #pragma unroll
         for (int n = 0; n < NR; ++n)
-          qb[n] = reinterpret_cast<const uint4*>(smem)[(w * NR + n) * 32 + lane];
+          qb[n] =
+              reinterpret_cast<const uint4*>(smem)[(w * NR + n) * 32 + lane];
 #pragma unroll
         for (int i = 0; i < MT; ++i) {
           uint32_t a[4], c[4];
@@ -849,7 +852,8 @@ decode_fp4_kernel(const AttnParams p, int splits) {
 #pragma unroll
       for (int n = 0; n < NR; ++n)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) raise = raise || mx[n][e] > m[n][e] + kRaise;
+        for (int e = 0; e < 2; ++e)
+          raise = raise || mx[n][e] > m[n][e] + kRaise;
       if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
         for (int n = 0; n < NR; ++n) {
@@ -1446,14 +1450,14 @@ cudaError_t launch_decode_attn_fp4(const AttnParams& p, int D, bool bf16,
 }
 
 cudaError_t launch_decode_attn_fp4_shares(const AttnParams& p, int D,
-                                          bool bf16, int ctas, bool pdl,
+                                          bool bf16, int shares, bool pdl,
                                           void* scratch,
                                           cudaStream_t stream) {
   AttnParams a = p;
   char* ws = static_cast<char*>(scratch);
-  const size_t slots = static_cast<size_t>(2) * ctas;
+  const size_t slots = static_cast<size_t>(2) * shares;
   a.chunk = 0;
-  a.sk_chunks = ctas;
+  a.sk_chunks = shares;
   a.part_o = reinterpret_cast<float*>(ws);
   ws += dfp4::up256(slots * p.sk_rows * D * 4);
   a.part_lse = reinterpret_cast<float*>(ws);
@@ -1461,10 +1465,10 @@ cudaError_t launch_decode_attn_fp4_shares(const AttnParams& p, int D,
   a.sk_marks = reinterpret_cast<int2*>(ws);
   cudaError_t e = bf16 ? dfp4::dispatch<__nv_bfloat16>(a, D, 1, pdl, stream)
                        : dfp4::dispatch<__half>(a, D, 1, pdl, stream);
-  if (e != cudaSuccess || ctas < 2) return e;
+  if (e != cudaSuccess || shares < 2) return e;
   note_launch();
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(ctas - 1));
+  cfg.gridDim = dim3(static_cast<unsigned>(shares - 1));
   cfg.blockDim = dim3(dfp4::kFoldThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -1490,10 +1494,10 @@ cudaError_t launch_decode_attn_fp4_shares(const AttnParams& p, int D,
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-size_t decode_fp4_shares_bytes(int D, int ctas, int rows) {
-  const size_t slots = static_cast<size_t>(2) * ctas;
+size_t decode_fp4_shares_bytes(int D, int shares, int rows) {
+  const size_t slots = static_cast<size_t>(2) * shares;
   return dfp4::up256(slots * rows * D * 4) + dfp4::up256(slots * rows * 4) +
-         dfp4::up256(static_cast<size_t>(ctas) * 16);
+         dfp4::up256(static_cast<size_t>(shares) * 16);
 }
 
 cudaError_t launch_fp4_combine(const CombineParams& p, bool bf16, bool pdl,

@@ -101,9 +101,8 @@ constexpr int64_t kLongUnitKeys = 2048;
 // 4-bit caches: calls whose units span at most this many keys run one CTA per
 // (unit, split), longer ones as equal shares of the key tiles.  Measured on
 // GB300 (32/8 heads, D 128; one CTA per unit against shares): 64 requests of
-// 300-600 keys 17.2 against 24.0 us, 76 of 2000 keys 39.1 against 41.9, 256
-// of 200-2000 keys 79.8 against 82.7; 64 of 512-4096 keys 57.4 against 49.7,
-// 64 of 512-8192 keys 102.4 against 76.3.
+// 300-600 keys 16.5 against 24.7 us, 76 of 2000 keys 39.0 against 40.5, 256
+// of 200-2000 keys 78.8 against 82.2; 64 of 512-4096 keys 57.4 against 47.2.
 constexpr int64_t kFp4UnitKeys = 2048;
 
 struct Plan {
@@ -288,7 +287,7 @@ bool fp4_shares(const Plan& pl, int num_splits, int fixed_split) {
   return pl.decode && num_splits == 0 && fixed_split <= 0 &&
          pl.range > kFp4UnitKeys;
 }
-int fp4_ctas(int D, int rows, int sms) {
+int fp4_share_num(int D, int rows, int sms) {
   return sms * decode_fp4_resident(D, rows);
 }
 
@@ -626,8 +625,8 @@ size_t workspace_bytes_impl(int batch, int total_q, int max_seqlen_q,
   const int skr = sk_rows(num_heads / num_kv_heads, max_seqlen_q);
   const size_t skb =
       kv4 ? fp4_shares(pl, num_splits, fixed_split_of(opts))
-                ? decode_fp4_shares_bytes(head_size,
-                                          fp4_ctas(head_size, skr, sms), skr)
+                ? decode_fp4_shares_bytes(
+                      head_size, fp4_share_num(head_size, skr, sms), skr)
                 : 0
       : sk_candidate(num_splits, fixed_split_of(opts), head_size, fp8)
           ? sk_scratch_bytes(head_size, fp8, q8, sms, skr)
@@ -882,8 +881,8 @@ pkv_status attention_impl(
   const int skr = sk_rows(num_heads / num_kv_heads, max_seqlen_q);
   const bool shares = kv4 && fp4_shares(pl, num_splits, fixed_split);
   const size_t skb =
-      shares ? decode_fp4_shares_bytes(head_size,
-                                       fp4_ctas(head_size, skr, sms), skr)
+      shares ? decode_fp4_shares_bytes(
+                   head_size, fp4_share_num(head_size, skr, sms), skr)
       : !kv4 && sk_candidate(num_splits, fixed_split, head_size, kv8)
           ? sk_scratch_bytes(head_size, kv8, q8, sms, skr)
           : 0;
@@ -1062,8 +1061,9 @@ pkv_status attention_impl(
     if (kv4) {
       d.sk_rows = skr;
       e = fp4_scratch ? launch_decode_attn_fp4_shares(
-                            d, head_size, bf16, fp4_ctas(head_size, skr, sms),
-                            pdl_ok, fp4_scratch, s)
+                            d, head_size, bf16,
+                            fp4_share_num(head_size, skr, sms), pdl_ok,
+                            fp4_scratch, s)
                       : launch_decode_attn_fp4(d, head_size, bf16, pl.splits,
                                                pdl_ok, s);
     } else if (persistent) {

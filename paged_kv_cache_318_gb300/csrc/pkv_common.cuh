@@ -384,10 +384,10 @@ cudaError_t launch_fp4_dequant_blocks(const void* codes, const int64_t* cs,
                                       int D, int BS, void* out, bool bf16,
                                       unsigned* err, cudaStream_t stream);
 // Decode attention over a 4-bit cache (decode_fp4.cu); p.sk_rows: the most
-// packed query rows of a request.  One CTA per (request, split, KV head):
-// `splits` pieces of p.chunk keys (0 = one piece, written straight to the
-// output), which launch_fp4_combine folds; or `ctas` equal shares of the key
-// tiles, with decode_fp4_shares_bytes of scratch (256-byte aligned) for the
+// packed query rows of a request.  One group of warps per (request, split, KV
+// head): `splits` pieces of p.chunk keys (0 = one piece, written straight to
+// the output), which launch_fp4_combine folds; or `shares` equal shares of the
+// key tiles, with decode_fp4_shares_bytes of scratch (256-byte aligned) for the
 // units that their ends cut.
 // pdl: the kernel (which waits at its start for the one queued before it) is
 // launched as that one's programmatic dependent, and the fold as its own.
@@ -397,9 +397,9 @@ cudaError_t launch_decode_attn_fp4(const AttnParams& p, int D, bool bf16,
 cudaError_t launch_fp4_combine(const CombineParams& p, bool bf16, bool pdl,
                                cudaStream_t stream);
 cudaError_t launch_decode_attn_fp4_shares(const AttnParams& p, int D,
-                                          bool bf16, int ctas, bool pdl,
+                                          bool bf16, int shares, bool pdl,
                                           void* scratch, cudaStream_t stream);
-size_t decode_fp4_shares_bytes(int D, int ctas, int rows);
+size_t decode_fp4_shares_bytes(int D, int shares, int rows);
 // Groups of 4 warps that an SM holds for `rows` packed query rows.
 int decode_fp4_resident(int D, int rows);
 

@@ -302,7 +302,8 @@ rope_kernel(const RopeLaunch p, int parts) {
       slot = read_slot(p, t, part == 0 && lane == 0);
     int64_t pos[4] = {0, 0, 0, 0};
     if (!read_positions(p, t, part == 0 && lane == 0, pos)) continue;
-    if (STORE != kRopeRows && slot >= 0) split_slot(slot, p.BS, p.bs_shift, &blk, &off);
+    if (STORE != kRopeRows && slot >= 0)
+      split_slot(slot, p.BS, p.bs_shift, &blk, &off);
     // cos and sin of the lane's eight pairs, two to an operand
     uint64_t c[4], s[4];
     {
