@@ -1246,7 +1246,7 @@ fold_kernel(const AttnParams p) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   constexpr int HALF = kFoldThreads / 2;
-  __shared__ int reach[2];
+  __shared__ unsigned others[kFoldThreads / 32];
   __shared__ float row_base[16], row_inv[16], row_lse[16];
   __shared__ float4 part[kFoldThreads];
   const int4* const marks = reinterpret_cast<const int4*>(p.sk_marks);
@@ -1266,17 +1266,24 @@ fold_kernel(const AttnParams p) {
   int first = c, last = c;
   {
     bool open[2] = {true, true};
-    for (int step = 1; open[0] || open[1]; step += HALF) {
-      if (tid < 2) reach[tid] = HALF;
-      __syncthreads();
+    for (int step = 1;; step += HALF) {
       if (step > 1) near = unit_at(c + dir * (step + i_th));
-      if (near != u) atomicMin(&reach[tid < HALF ? 0 : 1], i_th);
+      const unsigned o = __ballot_sync(0xffffffffu, near != u);
+      if (lane == 0) others[warp] = o;
       __syncthreads();
-      const int back = reach[0], on = reach[1];
-      if (open[0]) first -= back;
-      if (open[1]) last += on;
-      open[0] = open[0] && back == HALF;
-      open[1] = open[1] && on == HALF;
+      int reach[2] = {HALF, HALF};
+#pragma unroll
+      for (int w = HALF / 32 - 1; w >= 0; --w)
+#pragma unroll
+        for (int d = 0; d < 2; ++d) {
+          const unsigned m = others[d * (HALF / 32) + w];
+          if (m) reach[d] = 32 * w + __ffs(m) - 1;
+        }
+      if (open[0]) first -= reach[0];
+      if (open[1]) last += reach[1];
+      open[0] = open[0] && reach[0] == HALF;
+      open[1] = open[1] && reach[1] == HALF;
+      if (!open[0] && !open[1]) break;
       __syncthreads();
     }
   }
