@@ -198,14 +198,14 @@ def _on_device(*tensors) -> int:
     return dev
 
 
-def _call(dev, fn, *args):
-    """fn(*args, stream): on device `dev` and its current stream; checks the
-    status."""
-    if dev == torch.cuda.current_device():
-        status = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+def _call(dev, fn, args, *more):
+    """fn(*args, stream, *more): on device `dev` (a tensor's, so CUDA is
+    initialised) and its current stream; checks the status."""
+    if dev == torch._C._cuda_getDevice():
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(dev), *more)
     else:
         with torch.cuda.device(dev):
-            status = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(dev), *more)
     if status:
         _check(status)
 
@@ -399,9 +399,10 @@ def _reshape_and_cache_fp4(lib, key, value, key_cache, value_cache,
         raise ValueError("key and value must share a dtype")
     dev = _on_device(key, value, key_cache, value_cache, slot_mapping,
                      k_scale, v_scale, k_block_scale, v_block_scale)
-    _call(dev, lib.pkv_reshape_and_cache_fp4, kp, vptr, k0, k1, v0, v1,
-          key_cache.data_ptr(), value_cache.data_ptr(), cs, f,
-          slot_mapping.data_ptr(), n, H, 2 * half, BS, NB, _dtype(key))
+    _call(dev, lib.pkv_reshape_and_cache_fp4, (
+        kp, vptr, k0, k1, v0, v1, key_cache.data_ptr(),
+        value_cache.data_ptr(), cs, f, slot_mapping.data_ptr(), n, H,
+        2 * half, BS, NB, _dtype(key)))
 
 
 def fp4_kv_cache(num_blocks, block_size, num_kv_heads, head_size,
@@ -458,10 +459,10 @@ def dequantize_fp4_cache(codes, block_scale, scale, dtype=None, out=None,
                          ((n, BS, H, 2 * half),))
     dt = _dtype(out)
     dev = _on_device(codes, block_scale, scale, out, block_ids)
-    _call(dev, lib.pkv_dequantize_fp4_cache, codes.data_ptr(),
-          _PACK_4(*codes.stride()), block_scale.data_ptr(),
-          _PACK_4(*block_scale.stride()), scale.data_ptr(),
-          _addr(block_ids), n, H, 2 * half, BS, NB, out.data_ptr(), dt)
+    _call(dev, lib.pkv_dequantize_fp4_cache, (
+        codes.data_ptr(), _PACK_4(*codes.stride()), block_scale.data_ptr(),
+        _PACK_4(*block_scale.stride()), scale.data_ptr(), _addr(block_ids),
+        n, H, 2 * half, BS, NB, out.data_ptr(), dt))
     return out
 
 
@@ -552,7 +553,7 @@ def qk_norm_rope(q, k, positions, cos_sin_cache, q_weight=None,
                      weight_offset, T, D)
     dev = _on_device(q, k, positions, cos_sin_cache, q_weight, k_weight,
                      q_out, k_out)
-    _call(dev, lib.pkv_qk_norm_rope, *rows, T, Hq, Hkv, D, r, dt)
+    _call(dev, lib.pkv_qk_norm_rope, rows + (T, Hq, Hkv, D, r, dt))
     return q_out, k_out
 
 
@@ -609,9 +610,10 @@ def rope_reshape_and_cache(q, k, v, key_cache, value_cache, slot_mapping,
     dev = _on_device(q, k, v, key_cache, value_cache, slot_mapping,
                      positions, cos_sin_cache, k_scale, v_scale,
                      k_block_scale, v_block_scale, q_weight, k_weight, q_out)
-    _call(dev, lib.pkv_rope_reshape_and_cache, *rows, key_cache.data_ptr(),
-          value_cache.data_ptr(), cs, slot_mapping.data_ptr(), T, Hq, H, D,
-          BS, NB, r, dt, kv_cache_dtype.encode(), ks, vs, fp4)
+    _call(dev, lib.pkv_rope_reshape_and_cache, rows + (
+        key_cache.data_ptr(), value_cache.data_ptr(), cs,
+        slot_mapping.data_ptr(), T, Hq, H, D, BS, NB, r, dt,
+        kv_cache_dtype.encode(), ks, vs, fp4))
     return q_out
 
 
@@ -881,14 +883,12 @@ def _attend_fp4(lib, q, k, v, max_seqlen_q, cu_seqlens_q, max_seqlen_k,
     if workspace is not None:
         wp = workspace.data_ptr()
         wn = workspace.numel() * workspace.element_size()
-    def call(*a):
-        return lib.pkv_paged_attention_varlen_fp4(*a, opts)
-
-    _call(dev, call, qp, q0, q1, k.data_ptr(), v.data_ptr(), cs, fp4, op, o0,
-          o1, cu_seqlens_q.data_ptr(), seqused_k.data_ptr(), batch, T, max_q,
-          max_k, block_table.data_ptr(), bt_stride, table[1], Hq, Hkv, D, BS,
-          NB, softmax_scale, causal, left, right, softcap or 0.0,
-          _addr(alibi_slopes), num_splits, _addr(lse), wp, wn, dt)
+    _call(dev, lib.pkv_paged_attention_varlen_fp4, (
+        qp, q0, q1, k.data_ptr(), v.data_ptr(), cs, fp4, op, o0, o1,
+        cu_seqlens_q.data_ptr(), seqused_k.data_ptr(), batch, T, max_q, max_k,
+        block_table.data_ptr(), bt_stride, table[1], Hq, Hkv, D, BS, NB,
+        softmax_scale, causal, left, right, softcap or 0.0,
+        _addr(alibi_slopes), num_splits, _addr(lse), wp, wn, dt), opts)
     return (out, lse) if return_softmax_lse else out
 
 
