@@ -31,7 +31,7 @@
 // is padding beyond 8, half of what 16-row query tiles would issue; 9 to 16
 // rows take two n tiles over the same converted operands.
 //
-// Each warp walks its own key tiles of a CTA's range, one tile ahead of its
+// Each warp walks its own key tiles of its group's range, one tile ahead of its
 // reads; the warps meet once, at the end.  The running maximum is raised (and
 // O rescaled) only when a logit passes it by 2^6: P stays below 64, which f16
 // holds with the same relative error, and the common tile needs no reduction
@@ -330,7 +330,7 @@ decode_fp4_kernel(const AttnParams p, int splits) {
   int left = 0;          // what of its share is past this piece's unit
   auto tiles_of = [&](const Req& r) {
     const int k0 = r.lo & ~15;
-    return r.rows == 0 ? 0 : max(1, (r.hi - k0 + KT - 1) / KT);
+    return r.rows == 0 ? 0 : (r.hi - k0 - 1) / KT + 1;   // (1: no keys)
   };
   if (!sequence) {
     // one (request, piece, KV head) each; neighbours read the same pages
@@ -1234,7 +1234,7 @@ __global__ void __launch_bounds__(128) combine_kernel(const CombineParams p) {
   }
 }
 
-// Join the parts of the units that the ends of the CTAs' shares cut.  A unit
+// Join the parts of the units that the ends of the shares cut.  A unit
 // in np parts has its first in slot 2 (s - 1) + 1 of share s - 1 (where it
 // begins) and the others in slots 2 s, 2 (s + 1), ... of the shares that mark
 // it as begun before.  Block c stands at the start of share c: the np - 1

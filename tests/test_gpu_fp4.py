@@ -714,7 +714,8 @@ def test_shares_nan_is_seen_only_by_its_rows(cuda_device, matrix):
     check(wl, out, None, oracle_cache(wl)[1], keep=~nan)
 
 
-def test_shares_in_a_graph_follow_the_lengths(cuda_device):
+@pytest.mark.parametrize("own_workspace", [True, False])
+def test_shares_in_a_graph_follow_the_lengths(cuda_device, own_workspace):
     """A captured call of equal shares, replayed with other lengths (none, a
     long one) and with queries moved from
     one request to another."""
@@ -740,7 +741,7 @@ def test_shares_in_a_graph_follow_the_lengths(cuda_device):
     torch.cuda.synchronize()
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
-        call(work)
+        call(work if own_workspace else None)
     full = wl.seq_lens.copy()
     for lens, cus in ((full, [0, 1, 2, 3, 4, 5, 6]),
                       ([0, 0, 0, 0, 0, 1], [0, 1, 2, 3, 4, 5, 6]),
