@@ -241,6 +241,11 @@ struct Smem {
 struct Req {
   int q0, q_len, rows, L, lo, hi;      // rows 0: not of this launch
 };
+// A range without keys is [0, 0): a window that starts past the table's end
+// must not lead to a column behind it.
+__device__ __forceinline__ void no_keys(Req& r) {
+  if (r.hi <= r.lo) r.lo = r.hi = 0;
+}
 __device__ __forceinline__ Req request(const AttnParams& p, int b,
                                        int max_rows, bool flag) {
   Req r{};
@@ -263,7 +268,8 @@ __device__ __forceinline__ Req request(const AttnParams& p, int b,
   int kmin, kmax;
   key_range(r.L, r.q_len, 0, r.q_len - 1, p.causal, p.wl, p.wr, kmin, kmax);
   r.lo = kmin;
-  r.hi = max(kmin, min(kmax, L_tab));
+  r.hi = min(kmax, L_tab);
+  no_keys(r);
   return r;
 }
 
@@ -351,7 +357,8 @@ decode_fp4_kernel(const AttnParams p, int splits) {
       int lo, hi;
       split_bounds(kmin, kmax, p.chunk, ns, sp, lo, hi);
       pc.r.lo = lo;
-      pc.r.hi = max(lo, min(hi, pc.r.hi));
+      pc.r.hi = min(hi, pc.r.hi);
+      no_keys(pc.r);
       pc.slot = sp;
     }
     pc.kt0 = pc.r.lo & ~15;

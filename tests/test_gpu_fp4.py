@@ -918,3 +918,54 @@ def test_the_whole_chain(cuda_device, D, neox):
         wl = workloads.build_workload("c4", 1, [n], [done], Hq, H, D, BS)
         wl.q, wl.block_table = qf, bt
         check(wl, out, lse, (kref, vref))
+
+
+# ------------------------------------------------------------------ limits
+
+@pytest.mark.parametrize("L,window,max_k,kw", [
+    (300, 100, 0, {}), (300, 100, 0, dict(num_splits=1)),
+    (300, 100, 0, dict(num_splits=3)), (300, 270, 0, dict(num_splits=3)),
+    (300, 100, 0, dict(fixed_split_size=64)), (5000, 2500, 8000, {}),
+    (5000, 4950, 8000, {})],
+    ids=["auto", "1", "3", "3-partly", "fixed", "shares", "shares-partly"])
+def test_a_window_past_a_short_table(cuda_device, L, window, max_k, kw):
+    """A table row of 5 columns, whose request's window starts past them (or
+    in them, at a key that is no multiple of 16): no column behind the row is
+    looked at.  The row is a view of a wider table, whose other columns hold
+    ids outside the cache: they would be reported."""
+    dev = cuda_device
+    wl = workload("k4", 8, [1, 3, 1], [70, L, L], 8, 2, 128, 16,
+                  window_size=(window, -1))
+    codes, sf, ks, vs = fill(wl, dev)
+    table = torch.from_numpy(wl.block_table).to(dev)
+    table[:, 5:] = 1 << 30
+    out, lse = api.flash_attn_varlen_func(
+        wl.q.to(dev), codes[0], codes[1], 3,
+        torch.from_numpy(wl.cu_seqlens_q).to(dev), max(L, max_k),
+        seqused_k=torch.from_numpy(wl.seq_lens).to(dev),
+        softmax_scale=wl.softmax_scale, causal=True,
+        window_size=wl.window_size, block_table=table[:, :5],
+        return_softmax_lse=True, k_descale=ks, v_descale=vs,
+        k_block_scale=sf[0], v_block_scale=sf[1], **kw)
+    with pytest.raises(api.PkvError, match="beyond the table") as e:
+        api.check_device_errors(dev)
+    assert "block id outside" not in str(e.value)
+    # the keys that the columns hold are seen, as if they were all
+    o, kref, vref = f32(out).astype(np.float64), *oracle_cache(wl)[1]
+    tol = 2.0 ** -11 + 2 * 1.05 * logit_error(wl, kref) + 2.0 ** -20
+    for b in range(3):
+        page = wl.block_table[b, :5]
+        k, v = (x[page].reshape(80, 2, 128) for x in (kref, vref))
+        n = int(wl.q_lens[b])
+        for i in range(n):
+            t, at = wl.cu_seqlens_q[b] + i, int(wl.seq_lens[b]) - n + i
+            lo, hi = max(0, at - window), min(80, at + 1)
+            if lo >= hi:
+                assert not o[t].any() and torch.isneginf(lse[:, t]).all()
+                continue
+            for h in range(8):
+                x = k[lo:hi, h // 4] @ f32(wl.q)[t, h] * wl.softmax_scale
+                p = np.exp(x - x.max())
+                want = p @ v[lo:hi, h // 4] / p.sum()
+                assert (np.abs(o[t, h] - want) <= 2.0 ** -8 * np.abs(want) +
+                        tol * np.abs(v[lo:hi]).max()).all()
