@@ -1424,7 +1424,7 @@ cudaError_t launch(const AttnParams& p, int splits, bool pdl,
 template <typename T, int D>
 cudaError_t dispatch_rows(const AttnParams& p, int splits, bool pdl,
                           cudaStream_t stream) {
-  const bool one = p.sk_rows <= 8;       // packed query rows of a request
+  const bool one = decode_fp4_rows(p.sk_rows) == 8;
   return one ? launch<T, D, 1>(p, splits, pdl, stream)
              : launch<T, D, 2>(p, splits, pdl, stream);
 }
@@ -1442,8 +1442,10 @@ cudaError_t dispatch(const AttnParams& p, int D, int splits, bool pdl,
 
 }  // namespace dfp4
 
+int decode_fp4_rows(int rows) { return rows <= 8 ? 8 : 16; }
+
 int decode_fp4_resident(int D, int rows) {
-  const bool one = rows <= 8;
+  const bool one = decode_fp4_rows(rows) == 8;
   switch (D) {
     case 64:
       return one ? dfp4::Smem<64, 1>::RESIDENT : dfp4::Smem<64, 2>::RESIDENT;

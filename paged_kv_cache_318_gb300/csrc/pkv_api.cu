@@ -1102,7 +1102,7 @@ pkv_status attention_impl(
       c.splits = pl.splits;
       c.sinks = p.sinks;
       c.min_rows = 1;
-      c.max_rows = kDecodeRows;
+      c.max_rows = kv4 ? decode_fp4_rows(skr) : kDecodeRows;
       // a dependent of the decode grid when that is one itself
       e = kv4 ? launch_fp4_combine(c, bf16, pdl_ok, s)
               : launch_split_combine(c, bf16, s, done != nullptr);

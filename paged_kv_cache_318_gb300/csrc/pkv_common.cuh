@@ -400,6 +400,10 @@ cudaError_t launch_decode_attn_fp4_shares(const AttnParams& p, int D,
                                           bool bf16, int shares, bool pdl,
                                           void* scratch, cudaStream_t stream);
 size_t decode_fp4_shares_bytes(int D, int shares, int rows);
+// Most packed query rows that the kernel computes of a request where a call's
+// requests have `rows` at most; it leaves a request with more alone, and so
+// does the combine (its max_rows).
+int decode_fp4_rows(int rows);
 // Groups of 4 warps that an SM holds for `rows` packed query rows.
 int decode_fp4_resident(int D, int rows);
 

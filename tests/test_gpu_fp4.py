@@ -969,3 +969,30 @@ def test_a_window_past_a_short_table(cuda_device, L, window, max_k, kw):
                 want = p @ v[lo:hi, h // 4] / p.sum()
                 assert (np.abs(o[t, h] - want) <= 2.0 ** -8 * np.abs(want) +
                         tol * np.abs(v[lo:hi]).max()).all()
+
+
+@pytest.mark.parametrize("kw", [dict(num_splits=3), dict(fixed_split_size=64),
+                                dict(num_splits=1)],
+                         ids=["3", "fixed", "1"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_refused_rows_stay_under_splits(cuda_device, D, kw):
+    """max_seqlen_q says 1 while a request has 3 queries of 4 heads: its rows
+    are not computed, and the join of the splits leaves them alone too."""
+    dev = cuda_device
+    wl = workloads.build_workload("v4", 8, [1, 3, 1], [400, 900, 300], 4, 1,
+                                  D, 16)
+    codes, sf, ks, vs = fill(wl, dev)
+    out = torch.full(wl.q.shape, 7.0, dtype=wl.torch_dtype, device=dev)
+    api.flash_attn_varlen_func(
+        wl.q.to(dev), codes[0], codes[1], 1,
+        torch.from_numpy(wl.cu_seqlens_q).to(dev), wl.max_seqlen_k,
+        seqused_k=torch.from_numpy(wl.seq_lens).to(dev), causal=True,
+        block_table=torch.from_numpy(wl.block_table).to(dev), out=out,
+        workspace=torch.zeros(8 << 20, dtype=torch.uint8, device=dev),
+        k_descale=ks, v_descale=vs, k_block_scale=sf[0],
+        v_block_scale=sf[1], **kw)
+    with pytest.raises(api.PkvError, match="more queries than"):
+        api.check_device_errors(dev)
+    assert (out[1:4] == 7).all()
+    check(wl, out, None, oracle_cache(wl)[1],
+          keep=np.array([True, False, False, False, True]))
