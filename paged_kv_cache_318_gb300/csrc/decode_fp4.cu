@@ -35,7 +35,8 @@
 // reads; the warps meet once, at the end.  The running maximum is raised (and
 // O rescaled) only when a logit passes it by 2^6: P stays below 64, which f16
 // holds with the same relative error, and the common tile needs no reduction
-// across lanes.
+// across lanes.  Each row is raised by its own logits, whatever the others of
+// its tile do: with a fixed split its bits are the same in every call.
 //
 // What bounds it: 2 Hkv (D / 2 + D / 16) bytes a key from HBM, then the SM's
 // own work, about 590 instructions for a warp's 32 keys (128 conversions, 128
@@ -207,6 +208,11 @@ __device__ __forceinline__ void finish(float m, float l, const float* sinks,
 // logit).
 __device__ __forceinline__ float soft_cap(float x, float t, float u) {
   return t - __fdividef(2.f * t, 1.f + ex2(x * u));
+}
+
+// f a + g b, rounded the same way in every instance of the kernel.
+__device__ __forceinline__ float fold2(float f, float a, float g, float b) {
+  return __fmaf_rn(f, a, __fmul_rn(g, b));
 }
 
 template <int D, int NR>
@@ -871,7 +877,9 @@ decode_fp4_kernel(const AttnParams p, int splits) {
             t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 4));
             t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
             t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16));
-            t = fmaxf(t, m[n][e]);
+            // (by the row's own logits alone: its bits must not depend on
+            // the rows beside it, which may be padding)
+            t = t > m[n][e] + kRaise ? t : m[n][e];
             al[e] = t == m[n][e] ? 1.f : ex2(m[n][e] - t);
             m[n][e] = t;
 #pragma unroll
@@ -1093,16 +1101,16 @@ decode_fp4_kernel(const AttnParams p, int splits) {
                                       : ex2(m[n][e] - M);
           g[e] = tm[e] == -INFINITY ? (tl[e] == 0.f ? 0.f : 1.f)
                                     : ex2(tm[e] - M);
-          sum[n][e] = f[e] * sum[n][e] + g[e] * tl[e];
+          sum[n][e] = fold2(f[e], sum[n][e], g[e], tl[e]);
           m[n][e] = M;
         }
 #pragma unroll
         for (int i = 0; i < KS; ++i) {
           const float4 v = src[(i * NR + n) * 32];
-          o[i][n][0] = f[0] * o[i][n][0] + g[0] * v.x;
-          o[i][n][1] = f[1] * o[i][n][1] + g[1] * v.y;
-          o[i][n][2] = f[0] * o[i][n][2] + g[0] * v.z;
-          o[i][n][3] = f[1] * o[i][n][3] + g[1] * v.w;
+          o[i][n][0] = fold2(f[0], o[i][n][0], g[0], v.x);
+          o[i][n][1] = fold2(f[1], o[i][n][1], g[1], v.y);
+          o[i][n][2] = fold2(f[0], o[i][n][2], g[0], v.z);
+          o[i][n][3] = fold2(f[1], o[i][n][3], g[1], v.w);
         }
       }
     };

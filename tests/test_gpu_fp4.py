@@ -996,3 +996,38 @@ def test_refused_rows_stay_under_splits(cuda_device, D, kw):
     assert (out[1:4] == 7).all()
     check(wl, out, None, oracle_cache(wl)[1],
           keep=np.array([True, False, False, False, True]))
+
+
+@pytest.mark.parametrize("kw", [dict(fixed_split_size=256),
+                                dict(num_splits=1)], ids=["fixed", "1"])
+@pytest.mark.parametrize("more", [{}, dict(softcap=30.0), dict(alibi=True)],
+                         ids=["plain", "cap", "slopes"])
+@pytest.mark.parametrize("D,q_lens", [(64, [1, 2]), (128, [1, 2]),
+                                      (256, [1, 2]), (128, [1, 40])])
+def test_bits_do_not_depend_on_the_batch(cuda_device, D, q_lens, more, kw):
+    """A request whose rows fill one tile of 8 (8 heads a KV head), alone and
+    beside one that makes the call use two: its window starts inside a key
+    tile, so that a masked tile comes before unmasked ones."""
+    dev = cuda_device
+    q_lens, L, window = q_lens + [1] * 3, [900, 700, 815, 301, 77], 187
+    wl = workload("b8", 11, q_lens, L, 16, 2, D, 16,
+                  window_size=(window, -1), **more)
+    codes, sf, ks, vs = cache = fill(wl, dev)
+    whole = attend(wl, dev, cache, **kw)
+    check(wl, whole[0], whole[1], oracle_cache(wl)[1])
+    slopes = None if wl.alibi_slopes is None else \
+        torch.from_numpy(wl.alibi_slopes).to(dev)
+    for b, n in enumerate(q_lens):
+        at = slice(wl.cu_seqlens_q[b], wl.cu_seqlens_q[b + 1])
+        out, lse = api.flash_attn_varlen_func(
+            wl.q[at].to(dev), codes[0], codes[1], n,
+            torch.tensor([0, n], dtype=torch.int32, device=dev), L[b],
+            seqused_k=torch.from_numpy(wl.seq_lens[b:b + 1]).to(dev),
+            softmax_scale=wl.softmax_scale, causal=True,
+            window_size=wl.window_size, softcap=wl.softcap,
+            alibi_slopes=slopes,
+            block_table=torch.from_numpy(wl.block_table[b:b + 1]).to(dev),
+            return_softmax_lse=True, k_descale=ks, v_descale=vs,
+            k_block_scale=sf[0], v_block_scale=sf[1], **kw)
+        assert torch.equal(out, whole[0][at])
+        assert torch.equal(lse, whole[1][:, at])
