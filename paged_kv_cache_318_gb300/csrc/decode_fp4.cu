@@ -32,11 +32,14 @@
 // rows take two n tiles over the same converted operands.
 //
 // Each warp walks its own key tiles of its group's range, one tile ahead of its
-// reads; the warps meet once, at the end.  The running maximum is raised (and
-// O rescaled) only when a logit passes it by 2^6: P stays below 64, which f16
-// holds with the same relative error, and the common tile needs no reduction
-// across lanes.  Each row is raised by its own logits, whatever the others of
-// its tile do: with a fixed split its bits are the same in every call.
+// reads; the warps meet once, at the end.  P = 2^(logit - reference), with the
+// reference 9 below the running maximum and raised (O rescaled) only when a
+// logit passes it by 15: the common tile needs no reduction across lanes.  P
+// rounds to f16: by at most 2^-11 of itself down to 2^-14, that is 2^-23 of the
+// largest weight, and by at most 2^-25 below, so n keys lose at most n 2^-34 of
+// the largest weight; the sums keep the float32 values.  Each row is raised by
+// its own logits, whatever the others of its tile do: with a fixed split its
+// bits are the same in every call.
 //
 // What bounds it: 2 Hkv (D / 2 + D / 16) bytes a key from HBM, then the SM's
 // own work, about 590 instructions for a warp's 32 keys (128 conversions, 128
@@ -71,7 +74,13 @@ namespace pkv {
 namespace dfp4 {
 
 constexpr int kWarps = 4;
-constexpr float kRaise = 6.f;      // log2 slack of the running maximum
+// P is 2^(logit - reference) and the reference 2^kRoom below a row's running
+// maximum, raised when a logit passes it by 2^kTop: P stays at or below 2^15,
+// where f16 ends, and the smallest P that f16 holds (2^-24, half of it rounds
+// away) is 2^-33 of the maximum.
+constexpr float kRoom = 9.f;
+constexpr float kTop = 15.f;
+constexpr float kUnroom = 1.f / 512.f;            // 2^-kRoom
 // Tiles of a group's share at least, so that each warp has some.
 constexpr int kMinTiles = 2 * kWarps;
 // What a unit costs a group beside its tiles, in tiles: its queries, the join
@@ -695,7 +704,7 @@ decode_fp4_kernel(const AttnParams p, int splits) {
 #pragma unroll
       for (int n = 0; n < NR; ++n)
         o[i][n][0] = o[i][n][1] = o[i][n][2] = o[i][n][3] = 0.f;
-    float m[NR][2];
+    float m[NR][2];                    // the references
     uint64_t l[NR];
 #pragma unroll
     for (int n = 0; n < NR; ++n) {
@@ -866,7 +875,7 @@ decode_fp4_kernel(const AttnParams p, int splits) {
       for (int n = 0; n < NR; ++n)
 #pragma unroll
         for (int e = 0; e < 2; ++e)
-          raise = raise || mx[n][e] > m[n][e] + kRaise;
+          raise = raise || mx[n][e] - m[n][e] > kTop;
       if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
         for (int n = 0; n < NR; ++n) {
@@ -878,8 +887,14 @@ decode_fp4_kernel(const AttnParams p, int splits) {
             t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
             t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16));
             // (by the row's own logits alone: its bits must not depend on
-            // the rows beside it, which may be padding)
-            t = t > m[n][e] + kRaise ? t : m[n][e];
+            // the rows beside it, which may be padding; at logits of 2^27
+            // t - kRoom may round to t - 16, out of f16's range)
+            if (t - m[n][e] > kTop) {
+              const float low = t - kRoom;
+              t = t - low > kTop ? t : low;
+            } else {
+              t = m[n][e];
+            }
             al[e] = t == m[n][e] ? 1.f : ex2(m[n][e] - t);
             m[n][e] = t;
 #pragma unroll
@@ -904,8 +919,8 @@ decode_fp4_kernel(const AttnParams p, int splits) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) x[e] = ex2(__fsub_rn(x[e], base[e & 1]));
           l[n] = add2(l[n], add2(pair(x[0], x[1]), pair(x[2], x[3])));
-          // P rounds to f16 (half a step of 2^-11 relative) for the MMA; the
-          // sums keep the float32 values
+          // P rounds to f16 for the MMA, the sums keep the float32 values
+          // (see the head of this file)
           pb[i][n][0] = movmatrix(pack2<__half>(x[0], x[1]));
           pb[i][n][1] = movmatrix(pack2<__half>(x[2], x[3]));
         }
@@ -1134,9 +1149,10 @@ decode_fp4_kernel(const AttnParams p, int splits) {
           const int tok = done.r.q0 + row_tok[r];
           const int hq = done.h * G + r - row_tok[r] * G;
           float inv, lse;
-          finish(m[n][e], sum[n][e], done.slot >= 0 ? nullptr : p.sinks, hq,
-                 &inv, &lse);
-          inv *= vscale;
+          // (O and the sum are relative to the reference, kRoom below)
+          finish(m[n][e] + kRoom, sum[n][e] * kUnroom,
+                 done.slot >= 0 ? nullptr : p.sinks, hq, &inv, &lse);
+          inv *= kUnroom * vscale;
           if (done.slot >= 0) {
             // partial rows: [slot][row] of the shares, or of the split
             int64_t row = static_cast<int64_t>(done.slot) * p.sk_rows + r;

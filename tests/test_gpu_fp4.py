@@ -1031,3 +1031,109 @@ def test_bits_do_not_depend_on_the_batch(cuda_device, D, q_lens, more, kw):
             k_block_scale=sf[0], v_block_scale=sf[1], **kw)
         assert torch.equal(out, whole[0][at])
         assert torch.equal(lse, whole[1][:, at])
+
+
+def one_hot_call(dev, logit_of, v_codes, D, dtype, k_scale, **kw):
+    """One request of one head whose query is (1, 0, ...): key j's logit is
+    k_scale * logit_of[j] (in -6 .. 6, E2M1 values) and its value row the
+    codes v_codes[j], all block and value scales 1.  Returns out [D] and the
+    LSE as float64, and the values [L, D]."""
+    L, BS = len(logit_of), 16
+    NB = -(-L // BS)
+    mags = np.array([0, 0.5, 1, 1.5, 2, 3, 4, 6])
+    k = np.zeros((NB * BS, D // 2), np.uint8)
+    v = np.zeros((NB * BS, D // 2), np.uint8)
+    k[:L, 0] = np.searchsorted(mags, np.abs(logit_of)) + 8 * (logit_of < 0)
+    v[:L] = v_codes
+    codes, sf = api.fp4_kv_cache(NB, BS, 1, D, dev)
+    codes[0, :, :, 0] = torch.from_numpy(k).view(NB, BS, -1).to(dev)
+    codes[1, :, :, 0] = torch.from_numpy(v).view(NB, BS, -1).to(dev)
+    sf.view(torch.uint8).fill_(0x38)                # 1.0
+    q = torch.zeros(1, 1, D, dtype=DT[dtype], device=dev)
+    q[0, 0, 0] = 1
+    ks, one = scales(dev, k_scale, 1.0)
+    out, lse = api.flash_attn_varlen_func(
+        q, codes[0], codes[1], 1,
+        torch.tensor([0, 1], dtype=torch.int32, device=dev), L,
+        seqused_k=torch.tensor([L], dtype=torch.int32, device=dev),
+        softmax_scale=1.0, causal=True,
+        block_table=torch.arange(NB, dtype=torch.int32, device=dev)[None],
+        return_softmax_lse=True, k_descale=ks, v_descale=one,
+        k_block_scale=sf[0], v_block_scale=sf[1], **kw)
+    nib = np.stack([v & 15, v >> 4], -1).reshape(NB * BS, D)[:L]
+    vals = mags[nib & 7] * np.where(nib & 8, -1, 1)
+    return f32(out)[0, 0].astype(np.float64), float(lse[0, 0]), vals
+
+
+@pytest.mark.parametrize("kw", [dict(num_splits=1), {},
+                                dict(fixed_split_size=8192)],
+                         ids=["1", "auto", "fixed"])
+@pytest.mark.parametrize("at", [0, 40000])
+@pytest.mark.parametrize("D,dtype,gap", [
+    (64, "bf16", 17.5), (128, "f16", 17.5), (256, "bf16", 17.5),
+    (128, "bf16", 8.0), (64, "f16", 15.25), (128, "f16", 20.0)])
+def test_small_weights_are_kept(cuda_device, D, dtype, gap, at, kw):
+    """One key `gap` nats above 70000 others, with a value of 0: the output is
+    the others' share.  A weight is held in f16 relative to 2^-9 of the
+    largest: off by half a step, 2^-11 of itself or 2^-25.  The output is off
+    by that share of the values' magnitudes (they are positive), the float32
+    logit (2^-22 of it), exp2 and joins (2^-18 in all), the sum of the
+    weights, and its rounding.  The sum is float32: a lane of one of the 4
+    warps adds the keys of each of its subtiles of 16 to its sum, so at most
+    L / 64 roundings by half a step, 2^-24 of a sum that is at most the whole.
+    (A weight below 2^-25 of the lane's sum is lost to it: 2188 keys of
+    2.5e-8 in the lane that has the large one, 5.5e-5, of 6.5e-5 allowed.)"""
+    dev = cuda_device
+    L = 70001
+    g = np.random.default_rng(D)
+    logits = np.zeros(L)
+    logits[at] = 1
+    v = g.integers(0, 8, (L, D)).astype(np.uint8)       # positive
+    v = v[:, ::2] | v[:, 1::2] << 4
+    v[at] = 0
+    out, lse, vals = one_hot_call(dev, logits, v, D, dtype, gap, **kw)
+    w = np.exp(logits * gap - gap)
+    want = w @ vals / w.sum()
+    held = 2.0 ** (9 - gap * np.log2(np.e))
+    adds = -(-L // 64) * 2.0 ** -24
+    rel = max(2.0 ** -11, 2.0 ** -25 / held) + gap * 2.0 ** -22 + \
+        2.0 ** -18 + adds
+    half = torch.finfo(DT[dtype]).eps / 2
+    assert (np.abs(out - want) <= want * (rel + half * (1 + rel))).all()
+    assert abs(lse - gap - np.log(w.sum())) <= 2.0 ** -20 * gap + \
+        2.0 ** -18 + adds
+
+
+@pytest.mark.parametrize("size", [3e4, 2e7, 4e7, 7e7, 1e8, 1.2e8, 3e8, 1e12])
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("kw", [dict(num_splits=1), {}], ids=["1", "auto"])
+def test_logits_far_from_zero(cuda_device, sign, size, kw):
+    """Equal logits whose float32 step is above 1: the mean of the values."""
+    L = 50
+    g = np.random.default_rng(5)
+    v = g.integers(0, 256, (L, 64)).astype(np.uint8)
+    out, lse, vals = one_hot_call(cuda_device, np.full(L, float(sign)), v,
+                                  128, "bf16", size, **kw)
+    want = vals.mean(0)
+    assert (np.abs(out - want) <= 2.0 ** -8 * np.abs(want) +
+            6 * 2.0 ** -18).all()
+    # (the logit in base 2 and back, each product rounded, and the sum)
+    assert abs(lse - sign * size) <= size * 2.0 ** -21 + 2 * np.log(L)
+
+
+def test_logits_far_apart(cuda_device):
+    """Rising logits, each key far above the ones before it: the last key's
+    value, whatever the steps of the references were."""
+    dev = cuda_device
+    steps = np.array([-6, -4, -3, -2, -1.5, -1, -.5, 0, .5, 1, 1.5, 2, 3, 4,
+                      6.])
+    g = np.random.default_rng(6)
+    for scale in (20.0, 11.0, 3e7):
+        logits = np.repeat(steps, 40)
+        v = g.integers(0, 256, (600, 64)).astype(np.uint8)
+        out, lse, vals = one_hot_call(dev, logits, v, 128, "f16", scale,
+                                      num_splits=1)
+        w = np.exp((logits - 6) * scale)
+        want = w @ vals / w.sum()
+        assert (np.abs(out - want) <= 2.0 ** -11 * np.abs(want) +
+                6 * (2.0 ** -11 + 2.0 ** -18)).all()
