@@ -1320,12 +1320,10 @@ fold_kernel(const AttnParams p) {
   }
   const int np = last - first + 2;       // parts, shares first - 1 .. last
   const int h = u % p.Hkv, q0 = mark.y, rows = mark.z;
-  // (one linear expression: `k == 0 ? a : b` gave a wrong slot for parts 32
-  // .. 63 in the unrolled sum of units with more than 128 parts)
-  auto row_of = [&](int k, int r) -> int64_t {
-    const int slot = 2 * (first - 1 + k) + (k == 0 ? 1 : 0);
-    return static_cast<int64_t>(slot) * p.sk_rows + r;
-  };
+  // The first part is worked on by itself, so that the slots of the others are
+  // evenly spaced.
+  const int64_t begun = 2LL * (first - 1) + 1;
+  auto later = [&](int k) -> int64_t { return 2LL * (first - 1 + k); };
   // this block's items
   const int all = rows * (D / 4);
   const int per = (all + np - 2) / (np - 1);
@@ -1335,35 +1333,37 @@ fold_kernel(const AttnParams p) {
   const int kg = kFoldThreads / width;
   const int grp = tid / width, in = tid - grp * width;
   // the thread's first values are on their way while the rows' sums are taken
+  const int64_t mine_at = grp == 0 ? begun : later(grp);
   float4 ahead = make_float4(0.f, 0.f, 0.f, 0.f);
   if (grp < kg && grp < np) {
     const int i = i0 + in, r = i / (D / 4);
     ahead = *reinterpret_cast<const float4*>(
-        p.part_o + row_of(grp, r) * D + (i - r * (D / 4)) * 4);
+        p.part_o + (mine_at * p.sk_rows + r) * D + (i - r * (D / 4)) * 4);
   }
   const int r0 = i0 / (D / 4), r1 = (i1 - 1) / (D / 4);
   for (int r = r0 + warp; r <= r1; r += kFoldThreads / 32) {
-    const float mine = lane < np ? p.part_lse[row_of(lane, r)] : -INFINITY;
-    float M = mine;
-    for (int k = lane + 32; k < np; k += 32)
-      M = fmaxf(M, p.part_lse[row_of(k, r)]);
+    const float* lse = p.part_lse + r;
+    const float lse0 = lse[begun * p.sk_rows];
+    const float mine =
+        lane + 1 < np ? lse[later(lane + 1) * p.sk_rows] : -INFINITY;
+    float M = fmaxf(lse0, mine);
+    for (int k = lane + 33; k < np; k += 32)
+      M = fmaxf(M, lse[later(k) * p.sk_rows]);
 #pragma unroll
     for (int o = 16; o; o >>= 1)
       M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
     const float base = M == -INFINITY ? 0.f : M * kLog2e;
     float sum = ex2(mine * kLog2e - base);
-    for (int k = lane + 32; k < np; k += 32)
-      sum += ex2(p.part_lse[row_of(k, r)] * kLog2e - base);
+    for (int k = lane + 33; k < np; k += 32)
+      sum += ex2(lse[later(k) * p.sk_rows] * kLog2e - base);
+    if (lane == 0) sum += ex2(lse0 * kLog2e - base);
 #pragma unroll
     for (int o = 16; o; o >>= 1)
       sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if (lane == 0) {
-      float inv, lse;
-      finish(M == -INFINITY ? M : base, sum, p.sinks, h * p.G + r % p.G, &inv,
-             &lse);
       row_base[r] = base;
-      row_inv[r] = inv;
-      row_lse[r] = lse;
+      finish(M == -INFINITY ? M : base, sum, p.sinks, h * p.G + r % p.G,
+             &row_inv[r], &row_lse[r]);
     }
   }
   __syncthreads();
@@ -1374,20 +1374,22 @@ fold_kernel(const AttnParams p) {
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     if (on) {
       const float base = row_base[r];
-#pragma unroll 4
-      for (int k = grp; k < np; k += kg) {
-        const int64_t at = row_of(k, r);
-        const float4 v =
-            ib == i0 && k == grp
-                ? ahead
-                : *reinterpret_cast<const float4*>(p.part_o + at * D + col);
-        const float w = ex2(p.part_lse[at] * kLog2e - base);  // -inf -> 0
-        if (w == 0.f) continue;
+      auto add = [&](int64_t slot, const float4& v) {
+        const float w =
+            ex2(p.part_lse[slot * p.sk_rows + r] * kLog2e - base);
+        if (w == 0.f) return;                               // (-inf)
         acc.x += w * v.x;
         acc.y += w * v.y;
         acc.z += w * v.z;
         acc.w += w * v.w;
-      }
+      };
+      auto value = [&](int64_t slot) {
+        return *reinterpret_cast<const float4*>(
+            p.part_o + (slot * p.sk_rows + r) * D + col);
+      };
+      if (grp < np) add(mine_at, ib == i0 ? ahead : value(mine_at));
+#pragma unroll 4
+      for (int k = grp + kg; k < np; k += kg) add(later(k), value(later(k)));
     }
     if (kg > 1) {
       __syncthreads();

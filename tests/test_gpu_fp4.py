@@ -1137,3 +1137,28 @@ def test_logits_far_apart(cuda_device):
         want = w @ vals / w.sum()
         assert (np.abs(out - want) <= 2.0 ** -11 * np.abs(want) +
                 6 * (2.0 ** -11 + 2.0 ** -18)).all()
+
+
+@pytest.mark.parametrize("D,dtype", [(64, "bf16"), (128, "f16"),
+                                     (256, "bf16")])
+@pytest.mark.parametrize("L", [40001, 65536])
+def test_join_of_many_parts(cuda_device, D, dtype, L):
+    """One request in more than 128 parts whose weights differ by up to e^9
+    from one run of 500 keys to the next (a part that is read from another's
+    place shows): P rounds by 2^-11, exp2, the sums (a part's own below 256
+    keys) and the join take 2^-17, the output half a step."""
+    g = np.random.default_rng(L + D)
+    steps = g.choice([-6, -3, -1, 0, 1, 2, 3], -(-L // 500))
+    logits = np.repeat(steps.astype(float), 500)[:L]
+    v = g.integers(0, 256, (L, D // 2)).astype(np.uint8)
+    # (values of one sign in a run, so that sums do not cancel)
+    sign = np.repeat(g.integers(0, 2, len(steps)), 500)[:L, None]
+    v = ((v & 0x77) | np.where(sign, 0x88, 0)).astype(np.uint8)
+    out, lse, vals = one_hot_call(cuda_device, logits, v, D, dtype, 1.0)
+    w = np.exp(logits)
+    want = w @ vals / w.sum()
+    size = w @ np.abs(vals) / w.sum()
+    half = torch.finfo(DT[dtype]).eps / 2
+    assert (np.abs(out - want) <= half * np.abs(want) +
+            size * (2.0 ** -11 + 2.0 ** -17)).all()
+    assert abs(lse - np.log(w.sum())) <= 2.0 ** -17
