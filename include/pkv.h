@@ -136,6 +136,7 @@ PKV_API pkv_status pkv_reshape_and_cache(
  *   if alibi_slopes:  s_j -= alibi_slopes[h] * |p - j|
  *   admissible iff (!causal || j <= p) && (window_left < 0 || j >= p -
  *   window_left) && (window_right < 0 || j <= p + window_right)
+ *   (any window up to 2^31 - 1; L_b + total_q stays below 2^31 - 2^16)
  *   out[t,h]  = sum_adm softmax(s)_j * v_j      (rounded to dtype)
  *   lse[h, t] = ln sum_adm exp(s_j)             (float)
  * A row with no admissible key gets out = 0 and lse = -inf.

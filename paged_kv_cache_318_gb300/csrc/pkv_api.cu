@@ -820,17 +820,23 @@ pkv_status attention_impl(
       !stride16(cache_strides[1], cb) || !stride16(cache_strides[2], cb))
     return fail(PKV_ERR_UNSUPPORTED,
                 "q/out/cache rows must start on 16-byte boundaries");
-  // (the kernels add a window to a position: 2^30 reaches as far as any)
-  const int wl = window_left < 0 ? -1 : std::min(window_left, 1 << 30);
-  const int wr = window_right < 0 ? -1 : std::min(window_right, 1 << 30);
+  // The kernels add a window to a position (from -total_q to the last key) in
+  // 32 bits.  Positions are less than total_q before the last key, so a right
+  // window of total_q hides nothing; nor does a left one of 2^31 - 1 - total_q
+  // while L + total_q < 2^31.
+  const int wl =
+      window_left < 0 ? -1 : std::min(window_left, 0x7fffffff - total_q);
+  const int wr = window_right < 0 ? -1 : std::min(window_right, total_q);
 
   unsigned* err = nullptr;
   int sms = 0;
   st = device_info(&err, &sms);
   if (st != PKV_OK) return st;
   const Plan pl = make_plan(batch, total_q, max_seqlen_q, max_seqlen_k,
-                            num_heads, num_kv_heads, head_size, causal, wl, wr,
-                            num_splits, sms, fixed_split, kv4);
+                            num_heads, num_kv_heads, head_size, causal,
+                            window_left < 0 ? -1 : window_left,
+                            window_right < 0 ? -1 : window_right, num_splits,
+                            sms, fixed_split, kv4);
   size_t need = pl.workspace;
   size_t mock_off = 0, q16_off = 0;
   if ((kv8 || kv4) && pl.prefill) {

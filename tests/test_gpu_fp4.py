@@ -1162,3 +1162,60 @@ def test_join_of_many_parts(cuda_device, D, dtype, L):
     assert (np.abs(out - want) <= half * np.abs(want) +
             size * (2.0 ** -11 + 2.0 ** -17)).all()
     assert abs(lse - np.log(w.sum())) <= 2.0 ** -17
+
+
+@pytest.mark.parametrize("window,seen", [
+    ((2 ** 30 + 2 ** 27, -1), 2 ** 30 + 2 ** 27 + 1),
+    ((-1, 2 ** 31 - 1), None), ((2 ** 31 - 1, 2 ** 30), None),
+    ((2 ** 28, 2 ** 31 - 1), 2 ** 28 + 1)])
+def test_windows_over_more_than_2_30_keys(cuda_device, window, seen):
+    """A table whose columns all name one of two blocks, so that a request may
+    have 1.3e9 keys: with a query of zero the LSE is the
+    logarithm of the number of keys seen and the output their mean."""
+    dev = cuda_device
+    BS, D, L = 1 << 16, 64, 2 ** 30 + 2 ** 28 + 5
+    codes, sf = api.fp4_kv_cache(2, BS, 1, D, dev)
+    codes.fill_(0x22)                               # 1.0
+    sf.view(torch.uint8).fill_(0x38)
+    one = torch.ones(1, device=dev)
+    cols = -(-L // BS)
+    table = torch.arange(cols, device=dev, dtype=torch.int32)[None] % 2
+    out, lse = api.flash_attn_varlen_func(
+        torch.zeros(1, 1, D, dtype=torch.bfloat16, device=dev), codes[0],
+        codes[1], 1, torch.tensor([0, 1], dtype=torch.int32, device=dev), L,
+        seqused_k=torch.tensor([L], dtype=torch.int32, device=dev),
+        softmax_scale=1.0, causal=False, window_size=window,
+        block_table=table, return_softmax_lse=True, k_descale=one,
+        v_descale=one, k_block_scale=sf[0], v_block_scale=sf[1])
+    api.check_device_errors(dev)
+    # (the parts' and the whole LSE round to float32 near 16: 2^-20 each, and
+    # the join's exp2 and log2 2^-20)
+    assert abs(float(lse[0, 0]) - np.log(seen or L)) <= 2.0 ** -17
+    assert (out == 1).all()
+
+
+def test_decode_windows_past_2_30_over_16_bits(cuda_device):
+    """Over a 16-bit cache too, windows that reach past every key hide nothing
+    and leave the bits as they are."""
+    dev = cuda_device
+    wl = workloads.build_workload("w16", 5, [1, 2, 40], [700, 2500, 90], 8, 2,
+                                  128, 16, causal=False)
+    NB, BS, H, D = wl.cache_shape()[1:]
+    cache = torch.zeros(2, NB, BS, H, D, dtype=wl.torch_dtype, device=dev)
+    for k, v, slots in ((wl.k_ctx, wl.v_ctx, wl.slot_mapping_ctx),
+                        (wl.k_new, wl.v_new, wl.slot_mapping_new)):
+        api.reshape_and_cache_flash(k.to(dev), v.to(dev), cache[0], cache[1],
+                                    torch.from_numpy(slots).to(dev))
+
+    def call(window):
+        return api.flash_attn_varlen_func(
+            wl.q.to(dev), cache[0], cache[1], wl.max_seqlen_q,
+            torch.from_numpy(wl.cu_seqlens_q).to(dev), wl.max_seqlen_k,
+            seqused_k=torch.from_numpy(wl.seq_lens).to(dev),
+            softmax_scale=wl.softmax_scale, causal=False, window_size=window,
+            block_table=torch.from_numpy(wl.block_table).to(dev),
+            num_splits=1)
+    want = call((-1, -1))
+    for window in ((2 ** 31 - 1, 2 ** 31 - 1), (-1, 2 ** 31 - 1), (-1, 43),
+                   (2 ** 31 - 1, -1), (2 ** 31 - 44, 2 ** 30)):
+        assert torch.equal(call(window), want)
