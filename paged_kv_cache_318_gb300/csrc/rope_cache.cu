@@ -261,7 +261,6 @@ rope_kernel(const RopeLaunch p, int parts) {
   for (int64_t w = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) +
                    (threadIdx.x >> 5);
        w < work; w += step) {
-    cp_async_wait<0>();                   // (of a token that was skipped)
     const int64_t t = parts == 1 ? w : w / parts;
     const int part = parts == 1 ? 0 : static_cast<int>(w - t * parts);
     // The token's passes part, part + parts, ... in the order q, k, v; every
@@ -301,7 +300,10 @@ rope_kernel(const RopeLaunch p, int parts) {
     if constexpr (STORE != kRopeRows)
       slot = read_slot(p, t, part == 0 && lane == 0);
     int64_t pos[4] = {0, 0, 0, 0};
-    if (!read_positions(p, t, part == 0 && lane == 0, pos)) continue;
+    if (!read_positions(p, t, part == 0 && lane == 0, pos)) {
+      cp_async_wait<0>();                 // (nothing reads these rows)
+      continue;
+    }
     if (STORE != kRopeRows && slot >= 0)
       split_slot(slot, p.BS, p.bs_shift, &blk, &off);
     // cos and sin of the lane's eight pairs, two to an operand
@@ -513,6 +515,8 @@ rope_kernel(const RopeLaunch p, int parts) {
       rows(K{}, p.Hkv, static_cast<const T*>(p.k_weight),
            cache_store(Q{}));
       rows(V{}, p.Hkv, static_cast<const T*>(nullptr), cache_store(K{}));
+    } else {
+      cp_async_wait<0>();                 // (nothing reads rows of k and v)
     }
   }
 }
