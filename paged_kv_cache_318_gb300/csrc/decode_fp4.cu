@@ -606,8 +606,9 @@ decode_fp4_kernel(const AttnParams p, int splits) {
 
   // ---- queries: lane (g8, c4) takes row g8 (and g8 + 8), the dimensions of
   // its K run.  A bf16 row is scaled by the power of two that puts its
-  // largest magnitude in [2^14, 2^15): exact in f16; the factor joins the
-  // row's logit scale.
+  // largest magnitude in [2^14, 2^15): exact in f16 for the elements above
+  // 2^-31 of the largest, and off by at most 2^-39 of it for smaller ones; the
+  // factor joins the row's logit scale.
   uint4 raw[NR][KW];
   auto load_queries = [&](const Piece& x, int rows) {
 #pragma unroll
@@ -1322,8 +1323,11 @@ fold_kernel(const AttnParams p) {
   const int h = u % p.Hkv, q0 = mark.y, rows = mark.z;
   // The first part is worked on by itself, so that the slots of the others are
   // evenly spaced.
-  const int64_t begun = 2LL * (first - 1) + 1;
-  auto later = [&](int k) -> int64_t { return 2LL * (first - 1 + k); };
+  const int begun = 2 * (first - 1) + 1;
+  auto later = [&](int k) { return 2 * (first - 1 + k); };
+  auto row_of = [&](int slot, int r) -> int64_t {
+    return static_cast<int64_t>(slot) * p.sk_rows + r;
+  };
   // this block's items
   const int all = rows * (D / 4);
   const int per = (all + np - 2) / (np - 1);
@@ -1333,29 +1337,31 @@ fold_kernel(const AttnParams p) {
   const int kg = kFoldThreads / width;
   const int grp = tid / width, in = tid - grp * width;
   // the thread's first values are on their way while the rows' sums are taken
-  const int64_t mine_at = grp == 0 ? begun : later(grp);
+  const int mine_at = grp == 0 ? begun : later(grp);
   float4 ahead = make_float4(0.f, 0.f, 0.f, 0.f);
+  float ahead_lse = -INFINITY;
   if (grp < kg && grp < np) {
     const int i = i0 + in, r = i / (D / 4);
-    ahead = *reinterpret_cast<const float4*>(
-        p.part_o + (mine_at * p.sk_rows + r) * D + (i - r * (D / 4)) * 4);
+    const int64_t at = row_of(mine_at, r);
+    ahead = *reinterpret_cast<const float4*>(p.part_o + at * D +
+                                             (i - r * (D / 4)) * 4);
+    ahead_lse = p.part_lse[at];
   }
   const int r0 = i0 / (D / 4), r1 = (i1 - 1) / (D / 4);
   for (int r = r0 + warp; r <= r1; r += kFoldThreads / 32) {
-    const float* lse = p.part_lse + r;
-    const float lse0 = lse[begun * p.sk_rows];
+    const float lse0 = p.part_lse[row_of(begun, r)];
     const float mine =
-        lane + 1 < np ? lse[later(lane + 1) * p.sk_rows] : -INFINITY;
+        lane + 1 < np ? p.part_lse[row_of(later(lane + 1), r)] : -INFINITY;
     float M = fmaxf(lse0, mine);
     for (int k = lane + 33; k < np; k += 32)
-      M = fmaxf(M, lse[later(k) * p.sk_rows]);
+      M = fmaxf(M, p.part_lse[row_of(later(k), r)]);
 #pragma unroll
     for (int o = 16; o; o >>= 1)
       M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
     const float base = M == -INFINITY ? 0.f : M * kLog2e;
     float sum = ex2(mine * kLog2e - base);
     for (int k = lane + 33; k < np; k += 32)
-      sum += ex2(lse[later(k) * p.sk_rows] * kLog2e - base);
+      sum += ex2(p.part_lse[row_of(later(k), r)] * kLog2e - base);
     if (lane == 0) sum += ex2(lse0 * kLog2e - base);
 #pragma unroll
     for (int o = 16; o; o >>= 1)
@@ -1374,22 +1380,26 @@ fold_kernel(const AttnParams p) {
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     if (on) {
       const float base = row_base[r];
-      auto add = [&](int64_t slot, const float4& v) {
-        const float w =
-            ex2(p.part_lse[slot * p.sk_rows + r] * kLog2e - base);
+      auto add = [&](float lse, const float4& v) {
+        const float w = ex2(lse * kLog2e - base);
         if (w == 0.f) return;                               // (-inf)
         acc.x += w * v.x;
         acc.y += w * v.y;
         acc.z += w * v.z;
         acc.w += w * v.w;
       };
-      auto value = [&](int64_t slot) {
-        return *reinterpret_cast<const float4*>(
-            p.part_o + (slot * p.sk_rows + r) * D + col);
+      auto load = [&](int slot) {
+        const int64_t at = row_of(slot, r);
+        const float4 v =
+            *reinterpret_cast<const float4*>(p.part_o + at * D + col);
+        add(p.part_lse[at], v);
       };
-      if (grp < np) add(mine_at, ib == i0 ? ahead : value(mine_at));
+      if (ib == i0)
+        add(ahead_lse, ahead);
+      else if (grp < np)
+        load(mine_at);
 #pragma unroll 4
-      for (int k = grp + kg; k < np; k += kg) add(later(k), value(later(k)));
+      for (int k = grp + kg; k < np; k += kg) load(later(k));
     }
     if (kg > 1) {
       __syncthreads();
