@@ -103,6 +103,9 @@ constexpr int64_t kLongUnitKeys = 2048;
 // GB300 (32/8 heads, D 128; one CTA per unit against shares): 64 requests of
 // 300-600 keys 16.5 against 24.7 us, 76 of 2000 keys 39.0 against 40.5, 256
 // of 200-2000 keys 78.8 against 82.2; 64 of 512-4096 keys 57.4 against 47.2.
+// Head sizes 64 and 256 take the same limit, unmeasured.  (The range is the
+// call's max_seqlen_k: a captured step that passes the model's longest takes
+// the shares also while its sequences are short.)
 constexpr int64_t kFp4UnitKeys = 2048;
 
 struct Plan {
