@@ -44,16 +44,17 @@
 // What bounds it: 2 Hkv (D / 2 + D / 16) bytes a key from HBM, then the SM's
 // own work, about 590 instructions for a warp's 32 keys (128 conversions, 128
 // scalings, 32 MMAs at 8 rows).  Measured on a GB300 whose copy reaches 6.79
-// TB/s, back to back: 8 requests of 131072 keys, 64/8 heads, D 128, 0.203 ms
-// (6.0 TB/s, 88 %); 124 windows of 4096 keys, two tokens each, 16/8 heads, D
-// 256, soft-cap, 0.209 ms (5.4 TB/s, 79 %); 64 requests of 512-4096 keys,
-// 32/8 heads, 0.0475 ms (3.9 TB/s: 3 us go to the launch, 3 to finding the
+// TB/s, back to back: 8 requests of 131072 keys, 64/8 heads, D 128, 0.204 ms
+// (5.9 TB/s, 87 %); 124 windows of 4096 keys, two tokens each, 16/8 heads, D
+// 256, soft-cap, 0.210 ms (5.3 TB/s, 78 %); 64 requests of 512-4096 keys,
+// 32/8 heads, 0.048 ms (3.8 TB/s: 3 us go to the launch, 3 to finding the
 // share, 3 to the first pages and 6 to the join); 2 requests of 131072 keys,
-// 128/8 heads (16 rows), 0.080 ms (3.8 TB/s: 655 instructions a tile from two
+// 128/8 heads (16 rows), 0.081 ms (3.7 TB/s: 655 instructions a tile from two
 // warps a scheduler that wait on their own chains).  The steps, on the first
 // of these: codes loaded straight into registers 0.390 ms, each warp's ring
 // 0.269, equal shares and 128-byte aligned stages 0.216, warps' states joined
-// pairwise so that 4 groups fit an SM 0.211, these as one CTA 0.203.  Measured
+// pairwise so that 4 groups fit an SM 0.211, these as one CTA 0.203; the reference
+// below the maximum costs 0.3 to 0.5 % of each of these.  Measured
 // and not kept: equal shares for warps (0.222), 3 groups an SM (the same),
 // shares cut so that an SM's groups take pieces as they finish (0.253), larger
 // shares for an SM's older CTAs (0.217 to 0.229), more stages for 9 to 16 rows
