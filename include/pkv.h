@@ -423,6 +423,71 @@ PKV_API pkv_status pkv_paged_attention_varlen_fp4(
     const pkv_attention_options* opts);
 
 /*
+ * pkv_paged_attention_varlen_tree -- attention of a tree of drafted tokens.
+ * (No counterpart on the source pages, whose drafts are chains.)
+ *
+ * Request b's rows are cu_seqlens_q[b] .. cu_seqlens_q[b+1] - 1: row 0 is the
+ * last certain token, each row after it a drafted token.  tree_parents[row] is
+ * the parent's number within the request, smaller than the row's own; -1 for
+ * a row that follows the context directly (row 0).  The keys of the n rows are
+ * the request's last n keys, in the rows' order, as in the other calls; the
+ * ctx = seqused_k[b] - n keys before them are its context.  Row i, depth(i)
+ * steps below a row without parent, sits at position p = ctx + depth(i) and
+ * sees
+ *   key j < ctx        iff  window_left < 0 || j >= p - window_left
+ *   its own key and those of its ancestors, up to window_left steps away.
+ * Logits, soft-cap, sinks, out and softmax_lse are those of
+ * pkv_paged_attention_varlen.  With tree_parents[i] = i - 1 the call is the
+ * causal one.
+ *
+ * tree_parents : int32 [total_q] device.  A parent that is not an earlier row
+ *   (or -1) counts as -1 and is flagged (PKV_ERR_BAD_INDEX through
+ *   pkv_check_device_errors).
+ * max_seqlen_q : at most PKV_TREE_MAX_ROWS (PKV_ERR_UNSUPPORTED above); a
+ *   request with more rows than it is not computed and flagged.
+ * causal       : must be set; window_right hides nothing then.
+ * scales       : of a 4-bit cache (cache_strides in bytes), else NULL.  An
+ *   E4M3 cache is named in opts.  Both are read through exact 16-bit copies of
+ *   the requests' pages in the workspace.
+ * num_splits   : 0, or 1: each (request, KV head) is worked through by one
+ *   block and its bits do not depend on the rest of the batch.
+ * PKV_ERR_UNSUPPORTED: ALiBi, an fp8 query, non-paged keys, a fixed split
+ *   size, num_splits > 1.
+ * A value row that holds NaN or infinity reaches every row of its request
+ *   that shares a tile of keys with it, also where the tree hides it; key rows
+ *   and the rows behind seqused_k do not.
+ * workspace    : pkv_paged_attention_workspace_size_tree bytes, 256-byte
+ *   aligned: the page copies (needed), then the pieces of units that the
+ *   blocks' shares cut (a workspace without this part works as num_splits 1).
+ *   Nothing in it has to be set before a call or kept after one.
+ */
+#define PKV_TREE_MAX_ROWS 256
+
+PKV_API size_t pkv_paged_attention_workspace_size_tree(
+    int batch, int total_q, int max_seqlen_q, int max_seqlen_k,
+    int num_heads, int num_kv_heads, int head_size, int block_size,
+    int num_splits, int max_blocks_per_seq, int kv_cache_4bit,
+    const pkv_attention_options* opts);
+
+PKV_API pkv_status pkv_paged_attention_varlen_tree(
+    const void* q, int64_t q_stride_tok, int64_t q_stride_head,
+    const void* key_cache, const void* value_cache,
+    const int64_t cache_strides[4], const pkv_fp4_scales* scales,
+    void* out, int64_t o_stride_tok, int64_t o_stride_head,
+    const int32_t* cu_seqlens_q, const int32_t* seqused_k,
+    const int32_t* tree_parents, int batch,
+    int total_q, int max_seqlen_q, int max_seqlen_k,
+    const int32_t* block_table, int64_t block_table_stride,
+    int max_blocks_per_seq,
+    int num_heads, int num_kv_heads, int head_size, int block_size,
+    int64_t num_blocks,
+    float softmax_scale, int causal, int window_left, int window_right,
+    float softcap, int num_splits, float* softmax_lse,
+    void* workspace, size_t workspace_bytes,
+    pkv_dtype dtype, pkv_stream_t stream,
+    const pkv_attention_options* opts);
+
+/*
  * Head norms and rotary positions.  (No counterpart on the source pages,
  * whose backends take q and k after these steps.)
  *

@@ -145,6 +145,14 @@ def load_library():
         at = lib.pkv_paged_attention_varlen_opts.argtypes
         lib.pkv_paged_attention_varlen_fp4.argtypes = \
             at[:5] + [vp, vp] + at[6:]
+        lib.pkv_paged_attention_workspace_size_tree.restype = sz
+        lib.pkv_paged_attention_workspace_size_tree.argtypes = [i32] * 11 + [
+            vp]
+        lib.pkv_paged_attention_varlen_tree.restype = i32
+        lib.pkv_paged_attention_varlen_tree.argtypes = [
+            vp, i64, i64, vp, vp, vp, vp, vp, i64, i64, vp, vp, vp, i32, i32,
+            i32, i32, vp, i64, i32, i32, i32, i32, i32, i64, f32, i32, i32,
+            i32, f32, i32, vp, vp, sz, i32, vp, vp]
         lib.pkv_qk_norm_rope.restype = i32
         lib.pkv_qk_norm_rope.argtypes = [vp, i64, i64] * 4 + [
             i64, i32, i32, i32, vp, i32, vp]
@@ -672,7 +680,7 @@ def flash_attn_varlen_func(q, k, v, max_seqlen_q, cu_seqlens_q, max_seqlen_k,
                            k_descale=None, v_descale=None,
                            fixed_split_size=0, q_descale=None,
                            enable_pdl=True, k_block_scale=None,
-                           v_block_scale=None):
+                           v_block_scale=None, tree_parents=None):
     """Varlen attention over a paged KV cache, or over plain K/V rows.
 
     q [T, Hq, D].  Paged: k, v are cache views [num_blocks, block_size, Hkv,
@@ -686,9 +694,22 @@ def flash_attn_varlen_func(q, k, v, max_seqlen_q, cu_seqlens_q, max_seqlen_k,
     (``no_pdl`` in pkv_attention_options).
     With k_block_scale and v_block_scale, k and v are the codes of a 4-bit
     cache (see ``fp4_kv_cache``) and k_descale / v_descale its tensor scales.
+    With tree_parents (int32 [T]), each request's rows are a tree of drafted
+    tokens: the parent's number within the request, smaller than the row's
+    own, or -1 (row 0).  A row sees the keys before the draft, its own and its
+    ancestors' (the request's last keys are those of its rows), and
+    sits as many positions behind the context as it has ancestors.  ``causal``
+    has to be set; max_seqlen_q is at most 256.
     Returns out (and lse [Hq, T] float32 when return_softmax_lse).
     """
     lib = load_library()
+    if tree_parents is not None:
+        return _attend_tree(
+            lib, q, k, v, max_seqlen_q, cu_seqlens_q, max_seqlen_k, seqused_k,
+            softmax_scale, causal, window_size, softcap, alibi_slopes,
+            block_table, return_softmax_lse, out, num_splits, cu_seqlens_k,
+            workspace, s_aux, k_descale, v_descale, fixed_split_size,
+            enable_pdl, k_block_scale, v_block_scale, tree_parents)
     if k_block_scale is not None or v_block_scale is not None:
         return _attend_fp4(
             lib, q, k, v, max_seqlen_q, cu_seqlens_q, max_seqlen_k, seqused_k,
@@ -889,6 +910,116 @@ def _attend_fp4(lib, q, k, v, max_seqlen_q, cu_seqlens_q, max_seqlen_k,
         block_table.data_ptr(), bt_stride, table[1], Hq, Hkv, D, BS, NB,
         softmax_scale, causal, left, right, softcap or 0.0,
         _addr(alibi_slopes), num_splits, _addr(lse), wp, wn, dt), opts)
+    return (out, lse) if return_softmax_lse else out
+
+
+def _vector(t, what, length):
+    """Address of a contiguous int32 vector of at least this length."""
+    shape = t.shape
+    if t.dtype is not torch.int32 or len(shape) != 1 or shape[0] < length or \
+            (length > 1 and t.stride(0) != 1):
+        raise ValueError("%s must be a contiguous int32 vector of %d" %
+                         (what, length))
+    return t.data_ptr()
+
+
+def _table(block_table, batch):
+    """(address, row stride, columns) of a block table of `batch` rows."""
+    shape = block_table.shape
+    if block_table.dtype is not torch.int32 or len(shape) != 2 or \
+            shape[0] < batch or (shape[1] > 1 and block_table.stride(1) != 1):
+        raise ValueError("block_table must be int32 [batch, max_blocks] with "
+                         "contiguous rows")
+    return (block_table.data_ptr(),
+            block_table.stride(0) if batch > 1 else shape[1], shape[1])
+
+
+def _attend_tree(lib, q, k, v, max_seqlen_q, cu_seqlens_q, max_seqlen_k,
+                 seqused_k, softmax_scale, causal, window_size, softcap,
+                 alibi_slopes, block_table, return_softmax_lse, out,
+                 num_splits, cu_seqlens_k, workspace, s_aux, k_descale,
+                 v_descale, fixed_split_size, enable_pdl, k_block_scale,
+                 v_block_scale, tree_parents):
+    """flash_attn_varlen_func over drafted trees."""
+    if cu_seqlens_k is not None or q.dtype in _FP8_CACHE:
+        raise NotImplementedError("a drafted tree needs a paged cache and a "
+                                  "16-bit query")
+    if alibi_slopes is not None:
+        raise NotImplementedError("a drafted tree takes no ALiBi slopes")
+    if q.dim() != 3:
+        raise ValueError("q must be [tokens, heads, head_size]")
+    T, Hq, D = q.shape
+    shape, cs = _cache_views(k, v)
+    NB, BS, Hkv, Dk = shape
+    fp4, opts = None, None
+    if k_block_scale is not None or v_block_scale is not None:
+        fp4 = _fp4_scales(k, v, shape, k_block_scale, v_block_scale,
+                          k_descale, v_descale)
+        Dk *= 2
+    kv8 = fp4 is None and k.dtype in _FP8_CACHE
+    if fp4 is None and (v.dtype is not k.dtype or
+                        (not kv8 and k.dtype is not q.dtype)):
+        raise NotImplementedError("q and cache dtypes must match")
+    if Dk != D:
+        raise ValueError("q and k head_size differ")
+    if block_table is None or seqused_k is None:
+        raise ValueError("block_table and seqused_k are required")
+    batch = seqused_k.shape[0]
+    if cu_seqlens_q.shape[0] != batch + 1:
+        raise ValueError("cu_seqlens_q must have one entry more than "
+                         "seqused_k")
+    meta = (_vector(cu_seqlens_q, "cu_seqlens_q", batch + 1),
+            _vector(seqused_k, "seqused_k", batch),
+            _vector(tree_parents, "tree_parents", T))
+    bt, bt_stride, max_blocks = _table(block_table, batch)
+    if out is None:
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+    elif out.dtype is not q.dtype or out.shape[0] != T:
+        raise ValueError("out must have q's shape and dtype")
+    qp, q0, q1 = _rows(q, "q", Hq, D, T)
+    op, o0, o1 = _rows(out, "out", Hq, D, T)
+    dt = _dtype(q)
+    if s_aux is not None and (s_aux.dtype is not torch.float32 or
+                              s_aux.shape != (Hq,) or s_aux.stride(0) != 1):
+        raise ValueError("s_aux (sinks) must be float32 [num_heads]")
+    dev = _on_device(q, k, v, k_block_scale, v_block_scale, k_descale,
+                     v_descale, cu_seqlens_q, seqused_k, tree_parents,
+                     block_table, s_aux, out, workspace)
+    lse = None
+    if return_softmax_lse:
+        lse = torch.empty((Hq, T), dtype=torch.float32, device=q.device)
+    if kv8 or s_aux is not None or fixed_split_size or not enable_pdl:
+        o = _Options()
+        o.sinks = _addr(s_aux)
+        o.fixed_split_size = int(fixed_split_size)
+        o.no_pdl = 0 if enable_pdl else 1
+        if kv8:
+            o.kv_cache_fp8 = 1
+            o.k_scale = _scalar(k_descale, "k_descale")
+            o.v_scale = _scalar(v_descale, "v_descale")
+        opts = ctypes.addressof(o)
+    if softmax_scale is None:
+        softmax_scale = D ** -0.5
+    max_q, max_k = int(max_seqlen_q), int(max_seqlen_k)
+    left, right = window_size
+    if workspace is None:
+        n = lib.pkv_paged_attention_workspace_size_tree(
+            batch, T, max_q, max_k, Hq, Hkv, D, BS, num_splits, max_blocks,
+            fp4 is not None, opts)
+        if n == _NO_SIZE:
+            # (the call itself says what is wrong)
+            n = 0
+        if n:
+            workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
+    wp, wn = 0, 0
+    if workspace is not None:
+        wp = workspace.data_ptr()
+        wn = workspace.numel() * workspace.element_size()
+    _call(dev, lib.pkv_paged_attention_varlen_tree, (
+        qp, q0, q1, k.data_ptr(), v.data_ptr(), cs, fp4, op, o0, o1, *meta,
+        batch, T, max_q, max_k, bt, bt_stride, max_blocks, Hq, Hkv, D, BS, NB,
+        softmax_scale, bool(causal), left, right, softcap or 0.0, num_splits,
+        _addr(lse), wp, wn, dt), opts)
     return (out, lse) if return_softmax_lse else out
 
 

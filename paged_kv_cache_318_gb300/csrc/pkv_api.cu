@@ -365,6 +365,22 @@ pkv_status check_attn_shape(int batch, int total_q, int max_q, int max_k,
   return PKV_OK;
 }
 
+// What a call on drafted trees does not take.
+pkv_status check_tree(int max_q, int num_splits,
+                      const pkv_attention_options* o) {
+  if (max_q > PKV_TREE_MAX_ROWS)
+    return fail(PKV_ERR_UNSUPPORTED,
+                "a drafted tree has at most %d rows (max_seqlen_q %d)",
+                PKV_TREE_MAX_ROWS, max_q);
+  if (num_splits > 1 || fixed_split_of(o) > 0)
+    return fail(PKV_ERR_UNSUPPORTED,
+                "a drafted tree takes num_splits 0 or 1 and no fixed split");
+  if (non_paged(o) || q_fp8_of(o))
+    return fail(PKV_ERR_UNSUPPORTED,
+                "a drafted tree needs a paged cache and a 16-bit query");
+  return PKV_OK;
+}
+
 // The 4-bit cache's scales (see pkv_fp4_scales).
 pkv_status check_fp4(const pkv_fp4_scales* f, int head_size) {
   if (!f) return fail(PKV_ERR_INVALID_ARG, "a 4-bit cache needs its scales");
@@ -507,16 +523,20 @@ pkv_status pkv_check_device_errors(pkv_stream_t stream) {
                                : "",
       (host & kErrSmemAlign) ? " shared memory not 1024-byte aligned (the "
                                "kernel did nothing);"
-                             : ""};
+                             : "",
+      (host & kErrBadTree) ? " a draft's parent that is not an earlier row, "
+                             "token outside the vocabulary or row out of "
+                             "order (left out);"
+                           : ""};
   const pkv_status code =
       (host & kErrTimeout)
           ? PKV_ERR_TIMEOUT
           : (host & (kErrBadBlock | kErrBadSlot | kErrBadTable |
-                     kErrQueryLen | kErrBadPosition))
+                     kErrQueryLen | kErrBadPosition | kErrBadTree))
                 ? PKV_ERR_BAD_INDEX
                 : PKV_ERR_CUDA;
-  return fail(code, "device error word 0x%x:%s%s%s%s%s%s%s", host, what[0],
-              what[1], what[2], what[3], what[4], what[5], what[6]);
+  return fail(code, "device error word 0x%x:%s%s%s%s%s%s%s%s", host, what[0],
+              what[1], what[2], what[3], what[4], what[5], what[6], what[7]);
 }
 
 pkv_status pkv_reshape_and_cache(
@@ -747,7 +767,7 @@ pkv_status attention_impl(
     const float* alibi_slopes, int num_splits, float* softmax_lse,
     void* workspace, size_t workspace_bytes, pkv_dtype dtype,
     pkv_stream_t stream, const pkv_attention_options* opts, Internal* in,
-    const pkv_fp4_scales* fp4 = nullptr) {
+    const pkv_fp4_scales* fp4 = nullptr, const int32_t* tree = nullptr) {
   int* pdl_done = in ? in->pdl_done : nullptr;
   const bool nonpaged = non_paged(opts);
   pkv_status st = check_attn_shape(batch, total_q, max_seqlen_q, max_seqlen_k,
@@ -835,14 +855,17 @@ pkv_status attention_impl(
   int sms = 0;
   st = device_info(&err, &sms);
   if (st != PKV_OK) return st;
-  const Plan pl = make_plan(batch, total_q, max_seqlen_q, max_seqlen_k,
-                            num_heads, num_kv_heads, head_size, causal,
-                            window_left < 0 ? -1 : window_left,
-                            window_right < 0 ? -1 : window_right, num_splits,
-                            sms, fixed_split, kv4);
+  // (drafted trees have one kernel of their own, and no plan)
+  const Plan pl =
+      tree ? Plan{}
+           : make_plan(batch, total_q, max_seqlen_q, max_seqlen_k, num_heads,
+                       num_kv_heads, head_size, causal,
+                       window_left < 0 ? -1 : window_left,
+                       window_right < 0 ? -1 : window_right, num_splits, sms,
+                       fixed_split, kv4);
   size_t need = pl.workspace;
   size_t mock_off = 0, q16_off = 0;
-  if ((kv8 || kv4) && pl.prefill) {
+  if ((kv8 || kv4) && (pl.prefill || tree)) {
     mock_off = align256(pl.workspace);
     need = mock_off + fp8_mock_bytes(batch, max_blocks_per_seq, block_size,
                                      num_kv_heads, head_size);
@@ -1001,6 +1024,48 @@ pkv_status attention_impl(
   const bool bf16 = dtype == PKV_BF16;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
 
+  // exact 16-bit copies of the pages that the requests with f.min_rows or
+  // more packed rows read; f then names the copies
+  auto copy_pages = [&](AttnParams& f) -> cudaError_t {
+    const size_t pages = static_cast<size_t>(batch) * max_blocks_per_seq;
+    const size_t page_bytes =
+        static_cast<size_t>(block_size) * num_kv_heads * head_size * 2;
+    char* base_ptr = static_cast<char*>(workspace) + mock_off;
+    void* mk = base_ptr;
+    void* mv = base_ptr + align256(pages * page_bytes);
+    int32_t* mt = reinterpret_cast<int32_t*>(
+        base_ptr + 2 * align256(pages * page_bytes));
+    const cudaError_t e =
+        kv4 ? launch_fp4_dequant_pages(f, head_size, bf16, mk, mv, mt, s)
+            : launch_fp8_dequant_pages(f, head_size, bf16, mk, mv, mt, s);
+    f.kc = mk;
+    f.vc = mv;
+    f.c_sb = static_cast<int64_t>(block_size) * num_kv_heads * head_size;
+    f.c_sr = static_cast<int64_t>(num_kv_heads) * head_size;
+    f.c_sh = head_size;
+    f.block_table = mt;
+    f.bt_stride = max_blocks_per_seq;
+    f.num_blocks = static_cast<int64_t>(pages);
+    f.kv_fp8 = 0;            // 16-bit copies; k_scale / v_scale still apply
+    return e;
+  };
+
+  if (tree) {
+    const size_t at = align256(need);
+    const size_t more = tree_scratch_bytes(head_size, p.G, max_seqlen_q, sms);
+    void* scratch = num_splits == 0 && ws_ok && workspace_bytes >= at + more
+                        ? static_cast<char*>(workspace) + at
+                        : nullptr;
+    p.min_rows = 1;
+    cudaError_t e = cudaSuccess;
+    if (kv8 || kv4) e = copy_pages(p);
+    if (e != cudaSuccess) return cuda_fail(e, "page dequant launch");
+    e = launch_tree_attn(p, tree, max_seqlen_q, max_seqlen_k, head_size, bf16,
+                         sms, scratch, !(opts && opts->no_pdl), s);
+    if (e != cudaSuccess) return cuda_fail(e, "tree attention launch");
+    return PKV_OK;
+  }
+
   // fp8 query: the persistent decode kernel reads the codes; every other
   // kernel reads their exact 16-bit copy, with k_scale * q_scale as k_scale
   AttnParams p16 = p;
@@ -1134,28 +1199,9 @@ pkv_status attention_impl(
     const int64_t prow = static_cast<int64_t>(max_seqlen_q) * p.G;
     cudaError_t e;
     if (kv8 || kv4) {
-      // 16-bit copies of the pages prefill-class requests read
-      const size_t pages = static_cast<size_t>(batch) * max_blocks_per_seq;
-      const size_t page_bytes =
-          static_cast<size_t>(block_size) * num_kv_heads * head_size * 2;
-      char* base_ptr = static_cast<char*>(workspace) + mock_off;
-      void* mk = base_ptr;
-      void* mv = base_ptr + align256(pages * page_bytes);
-      int32_t* mt = reinterpret_cast<int32_t*>(
-          base_ptr + 2 * align256(pages * page_bytes));
-      e = kv4 ? launch_fp4_dequant_pages(f, head_size, bf16, mk, mv, mt, s)
-              : launch_fp8_dequant_pages(f, head_size, bf16, mk, mv, mt, s);
+      e = copy_pages(f);
       if (e != cudaSuccess) return cuda_fail(e, "page dequant launch");
       if (kv4) f.sched_zeroed = 1;     // (by the kernel just launched)
-      f.kc = mk;
-      f.vc = mv;
-      f.c_sb = static_cast<int64_t>(block_size) * num_kv_heads * head_size;
-      f.c_sr = static_cast<int64_t>(num_kv_heads) * head_size;
-      f.c_sh = head_size;
-      f.block_table = mt;
-      f.bt_stride = max_blocks_per_seq;
-      f.num_blocks = static_cast<int64_t>(pages);
-      f.kv_fp8 = 0;          // 16-bit copies; k_scale / v_scale still apply
     }
     int used = 1;
     if (tc_prefill)
@@ -1711,6 +1757,66 @@ pkv_status pkv_paged_attention_varlen_fp4(
       num_blocks, softmax_scale, causal, window_left, window_right, softcap,
       alibi_slopes, num_splits, softmax_lse, workspace, workspace_bytes,
       dtype, stream, opts, nullptr, scales);
+}
+
+size_t pkv_paged_attention_workspace_size_tree(
+    int batch, int total_q, int max_seqlen_q, int max_seqlen_k, int num_heads,
+    int num_kv_heads, int head_size, int block_size, int num_splits,
+    int max_blocks_per_seq, int kv_cache_4bit,
+    const pkv_attention_options* opts) {
+  if (check_attn_shape(batch, total_q, max_seqlen_q, max_seqlen_k, num_heads,
+                       num_kv_heads, head_size, block_size,
+                       num_splits) != PKV_OK ||
+      check_tree(max_seqlen_q, num_splits, opts) != PKV_OK)
+    return static_cast<size_t>(-1);
+  size_t need = 0;
+  if (kv_cache_4bit || (opts && opts->kv_cache_fp8)) {
+    if (max_blocks_per_seq <= 0) {
+      fail(PKV_ERR_INVALID_ARG, "max_blocks_per_seq must be >= 1");
+      return static_cast<size_t>(-1);
+    }
+    need = fp8_mock_bytes(batch, max_blocks_per_seq, block_size, num_kv_heads,
+                          head_size);
+  }
+  if (num_splits != 0 || max_seqlen_q == 0) return need;
+  int sms = 0;
+  if (device_info(nullptr, &sms) != PKV_OK) return static_cast<size_t>(-1);
+  return align256(need) + tree_scratch_bytes(head_size,
+                                             num_heads / num_kv_heads,
+                                             max_seqlen_q, sms);
+}
+
+pkv_status pkv_paged_attention_varlen_tree(
+    const void* q, int64_t q_stride_tok, int64_t q_stride_head,
+    const void* key_cache, const void* value_cache,
+    const int64_t cache_strides[4], const pkv_fp4_scales* scales, void* out,
+    int64_t o_stride_tok, int64_t o_stride_head, const int32_t* cu_seqlens_q,
+    const int32_t* seqused_k, const int32_t* tree_parents, int batch,
+    int total_q, int max_seqlen_q, int max_seqlen_k,
+    const int32_t* block_table, int64_t block_table_stride,
+    int max_blocks_per_seq, int num_heads, int num_kv_heads, int head_size,
+    int block_size, int64_t num_blocks, float softmax_scale, int causal,
+    int window_left, int window_right, float softcap, int num_splits,
+    float* softmax_lse, void* workspace, size_t workspace_bytes,
+    pkv_dtype dtype, pkv_stream_t stream, const pkv_attention_options* opts) {
+  if (!causal)
+    return fail(PKV_ERR_INVALID_ARG, "a drafted tree needs causal attention");
+  pkv_status st = check_tree(max_seqlen_q, num_splits, opts);
+  if (st != PKV_OK) return st;
+  if (total_q > 0 && batch > 0 && max_seqlen_q > 0) {
+    if (!tree_parents)
+      return fail(PKV_ERR_INVALID_ARG, "NULL tree_parents");
+    if (num_blocks < 1)
+      return fail(PKV_ERR_INVALID_ARG, "the cache has no blocks");
+  }
+  return attention_impl(
+      q, q_stride_tok, q_stride_head, key_cache, value_cache, cache_strides,
+      out, o_stride_tok, o_stride_head, cu_seqlens_q, seqused_k, batch,
+      total_q, max_seqlen_q, max_seqlen_k, block_table, block_table_stride,
+      max_blocks_per_seq, num_heads, num_kv_heads, head_size, block_size,
+      num_blocks, softmax_scale, causal, window_left, window_right, softcap,
+      nullptr, num_splits, softmax_lse, workspace, workspace_bytes, dtype,
+      stream, opts, nullptr, scales, tree_parents);
 }
 
 pkv_status pkv_qk_norm_rope(

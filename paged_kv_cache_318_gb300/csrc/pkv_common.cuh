@@ -19,6 +19,9 @@ constexpr unsigned kErrSmemAlign = 16u; // shared memory not 1024-byte aligned
 constexpr unsigned kErrQueryLen = 32u;  // a request's query count is above
                                         // the max_seqlen_q the call gave
 constexpr unsigned kErrBadPosition = 64u;   // position past the rotation table
+constexpr unsigned kErrBadTree = 128u;      // a draft's parent that is not an
+                                            // earlier row, a token outside the
+                                            // vocabulary, rows that do not grow
 
 // ---------------------------------------------------------------- PTX helpers
 
@@ -468,6 +471,15 @@ cudaError_t launch_prefill_attn_tc(const AttnParams& p, int D, bool bf16,
                                    int grid_y, bool p_in_tmem,
                                    int* splits_used, cudaStream_t stream,
                                    bool pdl = false);
+// Attention of drafted trees (tree_attn.cu) over 16-bit pages.  parents: int32
+// [total_q]; max_n, max_k: bounds of a request's rows and keys.  scratch (null,
+// or tree_scratch_bytes, 256-byte aligned): lets the shares of the CTAs cut
+// units; without it a unit is worked through by one CTA.
+size_t tree_scratch_bytes(int D, int G, int max_n, int sms);
+cudaError_t launch_tree_attn(const AttnParams& p, const int32_t* parents,
+                             int max_n, int64_t max_k, int D, bool bf16,
+                             int sms, void* scratch, bool pdl,
+                             cudaStream_t stream);
 // Fold the prefill kernel's split-KV partials (p.splits of them, every one
 // written for each row) of the requests with rows >= p.min_rows.
 cudaError_t launch_prefill_split_combine(const CombineParams& p,

@@ -2636,9 +2636,8 @@ bool make_kv_map(CUtensorMap* map, const void* ptr, bool bf16, int D, int BS,
 // swizzled.  One box holds 64 columns of the 128 packed rows (token, head of
 // one KV group) of a Q tile, in the order and layout the S MMA reads.
 // False when G does not divide 128 or the driver rejects the map.
-static bool make_rows_map(CUtensorMap* map, const void* ptr, bool bf16, int D,
-                          int Hq, int T, int64_t s_tok, int64_t s_head,
-                          int G) {
+bool make_rows_map(CUtensorMap* map, const void* ptr, bool bf16, int D, int Hq,
+                   int T, int64_t s_tok, int64_t s_head, int G) {
   auto fn = encode_fn();
   if (!fn || G <= 0 || 128 % G != 0 || T <= 0) return false;
   cuuint64_t dims[3] = {static_cast<cuuint64_t>(D),

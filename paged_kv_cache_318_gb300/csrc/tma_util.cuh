@@ -234,4 +234,10 @@ bool make_kv_map_ex(CUtensorMap* map, const void* ptr, int elem, int D,
                     int BS, int Hkv, int64_t NB, int64_t s_blk, int64_t s_row,
                     int64_t s_head, int RB, bool hnd);
 
+// 3-D map over query or output rows [T, Hq, D]: a box is 64 columns of the 128
+// packed rows (token, head of one KV group) of a tile, as the MMAs read them.
+// False when G does not divide 128 or the driver rejects the map.
+bool make_rows_map(CUtensorMap* map, const void* ptr, bool bf16, int D, int Hq,
+                   int T, int64_t s_tok, int64_t s_head, int G);
+
 }  // namespace pkv

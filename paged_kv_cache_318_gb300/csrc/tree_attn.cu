@@ -1,0 +1,1391 @@
+// Attention of a tree of drafted tokens over a paged cache (tcgen05 + TMEM +
+// TMA).
+//
+// Request b has n rows (row 0: the last certain token; the others drafted,
+// each with an earlier row as its parent) and L keys, the rows' own keys last:
+// row a's key is ctx + a, ctx = L - n.  Row i, depth(i) steps below row 0, sits
+// at position ctx + depth(i) and sees key j < ctx unless the window hides it
+// (j < position - window), its own key and those of its ancestors at most
+// `window` steps away.  Everything else is the attention of the other kernels:
+// s = scale q k, soft-cap, softmax with an optional sink, natural LSE.
+//
+// A unit is one (request, KV head, block of packed rows): packed row R is row
+// R / G, query head g G + R % G, so the G heads of a KV head share every K/V
+// tile; a block holds 256 packed rows (128 at head size 256).  Almost all keys
+// lie before the draft and need no mask, and what bounds the usual tree (up to
+// 128 packed rows) is reading them once.  So the units' key tiles form one
+// sequence and every CTA (one per SM) takes an equal share of it, whatever the
+// lengths; a unit that a share's end cuts leaves one fp32 partial per piece,
+// and fold_kernel joins the pieces by their LSEs.
+//
+// Inside a CTA two streams x = 0, 1 (softmax warps 4 x .. 4 x + 3, a score
+// buffer S_x and an accumulator O_x in tensor memory) keep the tensor core
+// busy: while one stream's softmax works, the other's products run.
+//   up to 128 rows   both streams hold the same rows; stream x takes every
+//                    other key tile, and the two states meet at the piece's
+//                    end (each thread reads both accumulators)
+//   more             stream x holds rows 128 x .. and both take every tile
+// The probabilities overwrite the scores as packed 16-bit pairs and feed P V
+// from tensor memory.  Head size 256 has room for one accumulator: one stream
+// of 64-key tiles with two score buffers, S of the next tile running under the
+// softmax.
+//
+// K and V tiles share one ring, filled by one warp in the order in which the
+// MMA warp consumes them (walk() below gives both the same order, across the
+// pieces' borders too), so that the stages not in use are all prefetch.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <math.h>
+#include <string.h>
+
+#include <type_traits>
+
+#include "pkv_common.cuh"
+#include "tcgen05_util.cuh"
+#include "tma_util.cuh"
+
+namespace pkv {
+namespace tree {
+
+using namespace tc;
+
+constexpr int kNoParent = 255;         // in the byte list of parents
+static_assert(PKV_TREE_MAX_ROWS <= 256, "parents are bytes");
+
+// Probabilities are held relative to 2^-OFF of the row's reference maximum,
+// and the reference moves when the maximum grows by more than THR (log2
+// units), so a probability stays below 2^(THR + OFF).  bf16 has float32's
+// range.  f16 ends at 2^16 above and 2^-24 below: with OFF = 11 weights keep
+// all their bits down to 2^-25 of the largest and vanish below 2^-35 (with
+// OFF = 0, keys 16.6 nats below an attention sink would vanish).
+template <typename T>
+struct Range {
+  static constexpr float THR = 8.f, OFF = 0.f;
+};
+template <>
+struct Range<__half> {
+  static constexpr float THR = 4.f, OFF = 11.f;
+};
+
+template <int D>
+struct Cfg {
+  static constexpr int NX = D == 256 ? 1 : 2;          // streams
+  static constexpr int BN = D == 256 ? 64 : 128;       // keys of a tile
+  static constexpr int NCB = D / 64;                   // 64-column blocks
+  static constexpr int ROWS = NX * BM;                 // rows of a block
+  static constexpr int STAGE = BN * D * 2;             // one K or V tile
+  static constexpr int STAGES = D == 64 ? 8 : 5;
+  static constexpr int Q_TILE = BM * D * 2;
+  // tensor memory: (S_x, O_x) per stream, or (S_0, S_1, O)
+  static constexpr int S_STEP = NX == 2 ? BN + D : BN;
+  static constexpr int O_COL = NX == 2 ? BN : 2 * BN;  // of stream 0
+  static_assert(NX * (BN + D) + (NX == 1 ? BN : 0) <= 512, "TMEM columns");
+  static constexpr int SM_WARPS = 4 * NX;
+  static constexpr int MMA_WARP = SM_WARPS, LOAD_WARP = SM_WARPS + 1,
+                       DEAL_WARP = SM_WARPS + 2;
+  static constexpr int THREADS = (SM_WARPS + 4) * 32;
+  static constexpr int SLOTS = 2;                      // pieces in flight
+  static constexpr int OFF_Q = 0;
+  static constexpr int OFF_RING = OFF_Q + NX * Q_TILE;
+  static constexpr int OFF_BAR = OFF_RING + STAGES * STAGE;
+  static constexpr int BAR_BYTES = 8 * (2 * STAGES + 22);
+  static constexpr int OFF_PIECE = OFF_BAR + BAR_BYTES;
+  static constexpr int PIECE_BYTES = 80;
+  static constexpr int OFF_PAR = OFF_PIECE + SLOTS * PIECE_BYTES;
+  static constexpr int OFF_XCH = OFF_PAR + SLOTS * PKV_TREE_MAX_ROWS;
+  static constexpr int SMEM_USED = OFF_XCH + (NX == 2 ? 2 * BM * 8 : 0);
+  // one CTA per SM (it takes all of tensor memory)
+  static constexpr int SMEM = SMEM_USED < 120 * 1024 ? 120 * 1024 : SMEM_USED;
+  static_assert(SMEM <= 232448, "shared memory of a CTA");
+};
+// Register split of the two-stream kernels: the launch gives 168 a thread
+// (384 x 168 = 64512); the softmax warps take 200, the others keep 96.
+constexpr int kLaunchRegs = 168, kSoftmaxRegs = 200, kOtherRegs = 96;
+static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= 384 * kLaunchRegs,
+              "register split");
+
+struct Params {
+  const void* q;
+  int64_t q_st, q_sh;
+  void* out;
+  int64_t o_st, o_sh;
+  float* lse;
+  int total_q, batch, max_n;
+  const int32_t* cu_q;
+  const int32_t* seqused_k;
+  const int32_t* parents;
+  const int32_t* block_table;
+  int64_t bt_stride;
+  int max_blocks;
+  int64_t num_blocks;
+  int Hq, Hkv, G, BS, RB;
+  float scale, softcap;
+  const float* sinks;
+  const float* k_scale;     // caches converted from codes: value = code * scale
+  const float* v_scale;
+  int wl;
+  int kv_order_hnd, kv_rg, q_tma, out_v8, once;
+  // shares may cut units: partials [slot][rows_cap] (O rows, LSEs) of CTA c in
+  // slots 2 c (of the unit it starts inside, or all of its share) and 2 c + 1
+  // (of the unit it starts and does not end); marks[c]: the latter's geometry
+  int split, rows_cap;
+  float* part_o;
+  float* part_lse;
+  int4* marks;              // two per CTA: (pieces, q0, rows, row0), (g, ...)
+  unsigned* err;
+};
+
+// A run of consecutive key tiles of one unit.
+struct Piece {
+  int live;                 // 0: no more pieces
+  int b, g, q0, n, rows, row0, ctx;
+  int kt0, nt;              // first key of the first tile, tiles
+  int klo, khi;             // keys any row sees; khi also bounds the reads
+  int pair;                 // more than 128 rows
+  int xs;                   // stream of the first tile (not pair)
+  int whole, slot;          // the whole unit; else its partial's slot
+  int pad[4];
+};
+static_assert(sizeof(Piece) == 80, "copied as 5 x 16 bytes");
+
+// A key tile on its way through the CTA.
+struct Tile {
+  int kt, klo, khi, g;
+  int n;                    // piece
+  int first, last;          // of its stream in the piece
+  int head, tail;           // first / last tile of the piece
+  int id;                   // loader: this lane's page
+};
+
+// What a request asks for; rows <= 0: nothing.
+struct Req {
+  int q0, n, ctx, klo, khi, kstart, tiles, units;
+};
+
+__device__ __forceinline__ Req request(const Params& p, int b, int BN,
+                                       int ROWS, unsigned* flag) {
+  Req r{};
+  if (b >= p.batch) return r;
+  r.q0 = p.cu_q[b];
+  const int end = p.cu_q[b + 1];
+  int L = p.seqused_k[b];
+  r.n = min(end, p.total_q) - r.q0;
+  if (r.q0 < 0 || r.n <= 0) return r;
+  if (r.n > p.max_n) {
+    *flag |= kErrQueryLen;
+    return r;
+  }
+  if (L < 0) L = 0;
+  r.ctx = L - r.n;
+  // keys past the table row are not read
+  const int64_t tab = static_cast<int64_t>(p.max_blocks) * p.BS;
+  r.khi = L > tab ? static_cast<int>(tab) : L;
+  if (r.khi < L) *flag |= kErrBadTable;
+  // (the shallowest row may be row 0, at position ctx)
+  r.klo = p.wl >= 0 ? min(max(r.ctx - p.wl, 0), r.khi) : 0;
+  r.kstart = r.klo / p.RB * p.RB;
+  // a request without keys still has one (empty) tile: its rows are written
+  r.tiles = max((r.khi - r.kstart + BN - 1) / BN, 1);
+  r.units = (r.n * p.G + ROWS - 1) / ROWS * p.Hkv;
+  return r;
+}
+
+// Runs f over the tiles of the CTA's pieces, in the order in which they are
+// worked through: f(x, pv, s) handles the P V product of tile *pv and the
+// score product of tile *s of stream x (2: both streams), either may be null.
+// A tile's P V follows when its stream's next tile comes (or the end).
+// idle(x, n): stream x has no tile in piece n, and its earlier ones are done.
+// take(n, piece): 1 = piece n, 0 = no more, -1 = abort.  make(piece, n, j):
+// the piece's j-th tile.
+template <int NX, class Take, class Make, class Step, class Idle>
+__device__ __forceinline__ bool walk(Take take, Make make, Step f,
+                                     Idle idle) {
+  Tile p0{}, p1{};
+  bool h0 = false, h1 = false;
+  int newer = 0, pair = 0;
+  auto flush = [&]() -> bool {
+    bool ok = true;
+    if (NX == 2 && !pair) {
+      // the older tile first
+      if (newer == 0) {
+        if (h1) ok = f(1, &p1, nullptr);
+        if (ok && h0) ok = f(0, &p0, nullptr);
+      } else {
+        if (h0) ok = f(0, &p0, nullptr);
+        if (ok && h1) ok = f(1, &p1, nullptr);
+      }
+    } else if (h0) {
+      ok = f(NX == 2 ? 2 : 0, &p0, nullptr);
+    }
+    h0 = h1 = false;
+    return ok;
+  };
+  for (int n = 0;; ++n) {
+    Piece pc;
+    const int got = take(n, pc);
+    if (got < 0) return false;
+    if (got == 0) break;
+    if (pc.pair != pair && !flush()) return false;
+    pair = pc.pair;
+    for (int j = 0; j < pc.nt; ++j) {
+      Tile t = make(pc, n, j);
+      t.head = j == 0;
+      t.tail = j == pc.nt - 1;
+      const bool alt = NX == 2 && !pair;
+      t.first = j < (alt ? 2 : 1);
+      t.last = j + (alt ? 2 : 1) >= pc.nt;
+      const int x = alt ? ((pc.xs + j) & 1) : 0;
+      if (x == 0) {
+        if (!f(NX == 2 && pair ? 2 : 0, h0 ? &p0 : nullptr, &t)) return false;
+        p0 = t;
+        h0 = true;
+      } else {
+        if (!f(1, h1 ? &p1 : nullptr, &t)) return false;
+        p1 = t;
+        h1 = true;
+      }
+      newer = x;
+      // a piece of one tile leaves the other stream idle: finish there what
+      // an earlier piece waits for
+      if (alt && pc.nt == 1) {
+        if (x == 0 && h1) {
+          if (!f(1, &p1, nullptr)) return false;
+          h1 = false;
+        } else if (x == 1 && h0) {
+          if (!f(0, &p0, nullptr)) return false;
+          h0 = false;
+        }
+        if (!idle(x ^ 1, n)) return false;
+      }
+    }
+  }
+  return flush();
+}
+
+// 1 / denominator and the natural LSE of a row whose sum is l relative to m
+// (base 2).  NaN sums stay NaN.
+__device__ __forceinline__ void finish(float m, float l, const float* sinks,
+                                       int h, float* inv, float* lse) {
+  const float z = sinks ? sinks[h] * kLog2e : -INFINITY;
+  const float M = fmaxf(m, z);
+  if (M == -INFINITY) {                 // nothing seen (or all NaN)
+    *inv = l != l ? l : 0.f;
+    *lse = l != l ? l : -INFINITY;
+    return;
+  }
+  const float em = m == -INFINITY ? (l != l ? 1.f : 0.f) : ex2(m - M);
+  const float den = l * em + (sinks ? ex2(z - M) : 0.f);
+  *inv = em / den;
+  *lse = (M + lg2(den)) * kLn2;
+}
+
+// Bits [lo, hi) of 32-bit word w of a tile's mask.
+__device__ __forceinline__ uint32_t range_bits(int lo, int hi, int w) {
+  const int a = max(lo - 32 * w, 0), b = min(hi - 32 * w, 32);
+  if (b <= a) return 0u;
+  return (b == 32 ? 0xffffffffu : (1u << b) - 1u) & (0xffffffffu << a);
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
+tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
+                 const __grid_constant__ CUtensorMap tm_v,
+                 const __grid_constant__ CUtensorMap tm_q) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  using C = Cfg<D>;
+  constexpr int BN = C::BN, NX = C::NX, ST = C::STAGES;
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  unsigned char* base = smem_raw;
+  const uint32_t base_u = smem_u32(smem_raw);
+  if (base_u & 1023u) {            // 128-byte swizzle atoms need 1 KB
+    if (threadIdx.x == 0) {
+      atomicOr(p.err, kErrSmemAlign);
+      if (p.split) p.marks[2 * blockIdx.x] = make_int4(0, 0, 0, 0);
+    }
+    return;
+  }
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int G = p.G, RB = p.RB;
+  const uint32_t sQ = base_u + C::OFF_Q;
+  const uint32_t sR = base_u + C::OFF_RING;
+  const uint32_t bar0 = base_u + C::OFF_BAR;
+  auto full = [&](int s) { return bar0 + 8 * s; };
+  auto empty = [&](int s) { return bar0 + 8 * (ST + s); };
+  constexpr int B0 = 2 * ST;
+  auto s_full = [&](int x) { return bar0 + 8 * (B0 + x); };
+  auto p_full = [&](int x) { return bar0 + 8 * (B0 + 2 + x); };
+  auto o_ready = [&](int x) { return bar0 + 8 * (B0 + 4 + x); };
+  auto o_free = [&](int x) { return bar0 + 8 * (B0 + 6 + x); };
+  auto q_full = [&](int s) { return bar0 + 8 * (B0 + 8 + s); };
+  auto q_empty = [&](int s) { return bar0 + 8 * (B0 + 10 + s); };
+  auto it_full = [&](int s) { return bar0 + 8 * (B0 + 12 + s); };
+  auto it_empty = [&](int s) { return bar0 + 8 * (B0 + 14 + s); };
+  const uint32_t xbar = bar0 + 8 * (B0 + 16);       // the streams' states
+  const uint32_t pv_done = bar0 + 8 * (B0 + 17);    // (one stream)
+  const uint32_t drain_bar = bar0 + 8 * (B0 + 18);
+  auto par_full = [&](int s) { return bar0 + 8 * (B0 + 19 + s); };
+  constexpr int OFF_WORDS = C::OFF_BAR + 8 * (B0 + 21);
+  static_assert(OFF_WORDS + 8 <= C::OFF_PIECE, "barrier area");
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + OFF_WORDS);
+  volatile int* abort_flag =
+      reinterpret_cast<volatile int*>(base + OFF_WORDS + 4);
+
+  if (tid == 0) {
+    for (int s = 0; s < ST; ++s) {
+      mbar_init(full(s), 1);
+      mbar_init(empty(s), 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(s_full(s), 1);
+      mbar_init(p_full(s), 128);
+      mbar_init(o_ready(s), 1);
+      mbar_init(o_free(s), NX * 128);
+      mbar_init(q_full(s), p.q_tma ? 1 : 32);
+      mbar_init(q_empty(s), 1);
+      mbar_init(it_full(s), 1);
+      mbar_init(it_empty(s), C::SM_WARPS + 2);
+      mbar_init(par_full(s), 1);
+    }
+    mbar_init(xbar, 256);
+    mbar_init(pv_done, 1);
+    mbar_init(drain_bar, 1);
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == C::MMA_WARP) {
+    asm volatile(
+        "tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::
+            "r"(smem_u32(tmem_slot))
+        : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;"
+                 ::: "memory");
+  }
+  // everything that this kernel reads or writes comes after the kernel
+  // queued before it (a no-op unless launched as its programmatic dependent)
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+
+  // ---- this CTA's share [beg, end) of the sequence of all units' tiles (of
+  // units, when they are not to be cut): a scan over the requests, in the
+  // shared memory of the query tiles
+  int64_t beg = 0, end = 0, n_all = 0, ctas = 0;
+  int b_first = 0;
+  int64_t off_first = 0;             // tiles of request b_first before beg
+  {
+    int64_t* wsum = reinterpret_cast<int64_t*>(base);
+    int64_t* res = wsum + 16;
+    unsigned flag = 0;
+    auto weight = [&](int b) -> int64_t {
+      const Req r = request(p, b, BN, C::ROWS, &flag);
+      return p.split ? static_cast<int64_t>(r.tiles) * r.units : r.units;
+    };
+    // inclusive prefix of v over the block; *sum: the total
+    auto scan = [&](int64_t v, int64_t* sum) -> int64_t {
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += y;
+      }
+      if (lane == 31) wsum[warp] = v;
+      __syncthreads();
+      int64_t pre = 0, all = 0;
+      for (int w = 0; w < C::THREADS / 32; ++w) {
+        const int64_t y = wsum[w];
+        if (w < warp) pre += y;
+        all += y;
+      }
+      *sum = all;
+      __syncthreads();
+      return v + pre;
+    };
+    int64_t w0 = weight(tid), part = 0;
+    int64_t incl = scan(w0, &n_all);
+    for (int c = C::THREADS; c < p.batch; c += C::THREADS) {
+      scan(weight(c + tid), &part);
+      n_all += part;
+    }
+    if (flag && blockIdx.x == 0) atomicOr(p.err, flag);
+    // (as many CTAs as tiles at most: no share between two others is empty)
+    ctas = min(static_cast<int64_t>(gridDim.x), n_all);
+    if (blockIdx.x < ctas) {
+      beg = n_all * blockIdx.x / ctas;
+      end = n_all * (blockIdx.x + 1) / ctas;
+    }
+    int64_t run = 0;
+    if (tid == 0) res[0] = -1;
+    __syncthreads();
+    for (int c = 0; c < p.batch; c += C::THREADS) {
+      if (c > 0) {
+        w0 = weight(c + tid);
+        incl = scan(w0, &part) + run;
+      } else {
+        part = 0;
+      }
+      if (beg < end && beg >= incl - w0 && beg < incl) {
+        res[0] = c + tid;
+        res[1] = beg - (incl - w0);
+      }
+      if (c == 0 && p.batch > C::THREADS) scan(w0, &part);
+      run += part;
+    }
+    __syncthreads();
+    b_first = static_cast<int>(res[0]);
+    off_first = res[1];
+    // (the query tiles are written by TMA)
+    fence_proxy_async();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  // The CTA's n-th piece (all lanes of a reader warp call it in order).  The
+  // slot is given back by release(n).
+  auto take = [&](int n, Piece& pc) -> int {
+    const int s = n & 1;
+    if (!mbar_wait(it_full(s), (n >> 1) & 1, abort_flag, p.err)) return -1;
+    const int4* src = reinterpret_cast<const int4*>(
+        base + C::OFF_PIECE + s * C::PIECE_BYTES);
+    int4 w[5];
+#pragma unroll
+    for (int k = 0; k < 5; ++k) w[k] = src[k];
+    memcpy(&pc, w, sizeof(Piece));
+    return pc.live ? 1 : 0;
+  };
+  auto release = [&](int n) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(it_empty(n & 1));
+  };
+  // K / V tile layout: a 128-byte swizzle atom is 8 keys x 64 columns; cbs is
+  // the stride between column blocks, gs between 8-key groups (the 5-D boxes
+  // land as [8-key group][column block], the 4-D ones as [column block][key])
+  const uint32_t cbs = p.kv_rg ? 1024u : static_cast<uint32_t>(BN * 128);
+  const uint32_t gs = p.kv_rg ? static_cast<uint32_t>(C::NCB * 1024) : 1024u;
+
+  if (warp >= C::SM_WARPS) {
+    if constexpr (NX == 2)
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (warp == C::LOAD_WARP) {
+      // ------------------------------------------------- K / V loader
+      // lane i issues the box of page i of a tile; its page id is fetched a
+      // tile ahead
+      int gi = 0;                      // stages filled so far
+      int nxt = 0;
+      const uint64_t pol = l2_evict_first_policy();
+      auto load = [&](const void* tm, const Tile& t) -> bool {
+        const int s = gi % ST;
+        const int nbox =
+            max(min((t.khi - t.kt + RB - 1) / RB, BN / RB), 0);
+        int stop = 0;
+        if (lane == 0) {
+          if (gi >= ST && !mbar_wait(empty(s), (gi / ST - 1) & 1, abort_flag,
+                                     p.err))
+            stop = 1;
+          else
+            mbar_expect_tx(full(s), nbox * C::NCB * RB * 128);
+        }
+        stop = __shfl_sync(0xffffffffu, stop, 0);
+        if (stop) return false;
+        if (lane < nbox) {
+          const int row = (t.kt + lane * RB) % p.BS;
+          const uint32_t dst0 = sR + s * C::STAGE;
+          if (p.kv_rg) {
+            const uint32_t dst = dst0 + lane * (RB / 8) * gs;
+            const int c3 = p.kv_order_hnd ? row >> 3
+                                          : t.id * (p.BS >> 3) + (row >> 3);
+            const int c4 = p.kv_order_hnd ? t.id * p.Hkv + t.g : t.g;
+            if (p.once)
+              tma_load_5d_hint(dst, tm, 0, 0, 0, c3, c4, full(s), pol);
+            else
+              tma_load_5d(dst, tm, 0, 0, 0, c3, c4, full(s));
+          } else {
+#pragma unroll
+            for (int cb = 0; cb < C::NCB; ++cb) {
+              const uint32_t dst = dst0 + cb * cbs + lane * RB * 128;
+              const int c1 = p.kv_order_hnd ? row : t.g;
+              const int c2 = p.kv_order_hnd ? t.g : row;
+              if (p.once)
+                tma_load_4d_hint(dst, tm, cb * 64, c1, c2, t.id, full(s),
+                                 pol);
+              else
+                tma_load_4d(dst, tm, cb * 64, c1, c2, t.id, full(s));
+            }
+          }
+        }
+        ++gi;
+        return true;
+      };
+      auto fetch = [&](const Piece& pc, int j) -> int {
+        const int k0 = pc.kt0 + j * BN + lane * RB;
+        if (j >= pc.nt || lane >= BN / RB || k0 >= pc.khi) return 0;
+        const int blk = __ldg(p.block_table +
+                              static_cast<int64_t>(pc.b) * p.bt_stride +
+                              k0 / p.BS);
+        if (blk < 0 || blk >= p.num_blocks) {
+          atomicOr(p.err, kErrBadBlock);
+          return 0;
+        }
+        return blk;
+      };
+      walk<NX>(
+          [&](int n, Piece& pc) {
+            const int got = take(n, pc);
+            if (got > 0) {
+              release(n);
+              nxt = fetch(pc, 0);
+            }
+            return got;
+          },
+          [&](const Piece& pc, int n, int j) {
+            Tile t{};
+            t.kt = pc.kt0 + j * BN;
+            t.khi = pc.khi;
+            t.g = pc.g;
+            t.id = nxt;
+            nxt = fetch(pc, j + 1);
+            return t;
+          },
+          [&](int, const Tile* pv, const Tile* s) {
+            // (one stream: the next scores go before P V, except where a
+            // piece starts)
+            if (NX == 1 && s && !s->head) {
+              if (!load(&tm_k, *s)) return false;
+              s = nullptr;
+            }
+            if (pv && !load(&tm_v, *pv)) return false;
+            if (s && !load(&tm_k, *s)) return false;
+            return true;
+          },
+          [](int, int) { return true; });
+      // no copy may be in flight when the CTA exits
+      if (lane == 0)
+        for (int t = max(0, gi - ST); t < gi; ++t)
+          mbar_drain(full(t % ST), (t / ST) & 1);
+    } else if (warp == C::MMA_WARP) {
+      // ------------------------------------------------------ MMA issuer
+      constexpr bool kBF16 = std::is_same<T, __nv_bfloat16>::value;
+      constexpr uint32_t ID_S = idesc(128, BN, kBF16, false);
+      constexpr uint32_t ID_PV = idesc(128, D, kBF16, true);
+      int gi = 0;                      // stages consumed so far
+      int pcnt[2] = {0, 0};            // P of each S buffer
+      int scnt = 0;                    // score products (one stream)
+      auto wait = [&](uint32_t bar, int parity) -> bool {
+        const bool r = mbar_wait(bar, parity & 1, abort_flag, p.err);
+        tc_fence_after();
+        return r;
+      };
+      // V resident, rows that no row of the block sees set to zero (they may
+      // hold another request's NaN)
+      auto v_here = [&](int g_, const Tile& t) -> bool {
+        const int s = g_ % ST;
+        if (!wait(full(s), g_ / ST)) return false;
+        const int lo = max(t.klo - t.kt, 0);
+        const int hi = max(min(t.khi - t.kt, BN), lo);
+        const int dead = lo + BN - hi;
+        if (dead > 0) {
+          const uint32_t v0 = sR + s * C::STAGE;
+          for (int i = lane; i < dead * 8 * C::NCB; i += 32) {
+            const int cb = i / (dead * 8);
+            const int rem = i - cb * (dead * 8);
+            int r = rem / 8;
+            if (r >= lo) r += hi - lo;
+            asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(
+                             v0 + (r >> 3) * gs + cb * cbs + (r & 7) * 128 +
+                             ((rem % 8) << 4)),
+                         "r"(0)
+                         : "memory");
+          }
+          fence_proxy_async();
+          __syncwarp();
+        }
+        return true;
+      };
+      // S of the K tile in stage g_ and the queries in row tile qt
+      auto issue_s = [&](int buf, int g_, int qt) {
+        const uint32_t q0 = sQ + qt * C::Q_TILE;
+        const uint64_t a0 = sdesc(q0, 16, 1024);
+        const uint64_t b0 = sdesc(sR + (g_ % ST) * C::STAGE, 16, gs);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k)
+          mma_f16_warp(tmem + buf * C::S_STEP,
+                       a0 + (((k >> 2) * (BM * 128) + (k & 3) * 32) >> 4),
+                       b0 + (((k >> 2) * cbs + (k & 3) * 32) >> 4), ID_S,
+                       k > 0 ? 1 : 0);
+        mma_commit_warp(s_full(buf));
+      };
+      // P V of the tile whose probabilities lie in S buffer `buf`, into the
+      // accumulator of stream x; false on abort
+      auto issue_pv = [&](int x, int buf, int g_, const Tile& t) -> bool {
+        // the epilogue of the piece before has read the accumulator
+        if (t.first && t.n > 0 && !wait(o_free(x), t.n - 1)) return false;
+        if (!wait(p_full(buf), pcnt[buf])) return false;
+        ++pcnt[buf];
+        const uint64_t b0 = sdesc(sR + (g_ % ST) * C::STAGE, cbs, gs);
+        const uint32_t acc = tmem + x * C::S_STEP + C::O_COL;
+#pragma unroll
+        for (int k = 0; k < BN / 16; ++k)
+          mma_f16_tmem_a_warp(acc, tmem + buf * C::S_STEP + 8 * k,
+                              b0 + ((k * 2 * gs) >> 4), ID_PV,
+                              (!t.first || k > 0) ? 1 : 0);
+        if constexpr (NX == 1) mma_commit_warp(pv_done);
+        return true;
+      };
+      walk<NX>(
+          [&](int n, Piece& pc) {
+            const int got = take(n, pc);
+            if (got > 0) release(n);
+            return got;
+          },
+          [&](const Piece& pc, int n, int j) {
+            Tile t{};
+            t.kt = pc.kt0 + j * BN;
+            t.klo = pc.klo;
+            t.khi = pc.khi;
+            t.n = n;
+            // (slot of the queries: two pieces of one row tile each can be
+            // in shared memory at once)
+            t.g = NX == 2 && !pc.pair ? n & 1 : 0;
+            return t;
+          },
+          [&](int x, const Tile* pv, const Tile* s) -> bool {
+            const int x0 = x == 2 ? 0 : x, x1 = x == 2 ? 1 : x;
+            const bool s_first = NX == 1 && s && !s->head;
+            const int gk = s_first ? gi : gi + (pv ? 1 : 0);
+            const int gv = s_first ? gi + 1 : gi;
+            gi += (pv ? 1 : 0) + (s ? 1 : 0);
+            bool k_here = false;
+            auto do_s = [&](int xx) -> bool {
+              if (!k_here) {
+                if (s->head && !wait(q_full(s->n & 1), s->n >> 1))
+                  return false;
+                if (!wait(full(gk % ST), gk / ST)) return false;
+                k_here = true;
+              }
+              if constexpr (NX == 1) {
+                issue_s(scnt & 1, gk, 0);
+                ++scnt;
+              } else {
+                issue_s(xx, gk, x == 2 ? xx : s->g);
+              }
+              if (xx == x1) {
+                mma_commit_warp(empty(gk % ST));
+                if (s->tail) mma_commit_warp(q_empty(s->n & 1));
+              }
+              return true;
+            };
+            if (s_first && !do_s(0)) return false;
+            bool v_done = false;
+#pragma unroll 1
+            for (int xx = x0; xx <= x1; ++xx) {
+              if (pv) {
+                if (!v_done && !v_here(gv, *pv)) return false;
+                v_done = true;
+                // (one stream: the buffer that the newest S does not hold)
+                const int buf = NX == 1 ? (scnt + (s_first ? 0 : 1)) & 1 : xx;
+                if (!issue_pv(xx, buf, gv, *pv)) return false;
+                if (xx == x1) mma_commit_warp(empty(gv % ST));
+                if (pv->last) mma_commit_warp(o_ready(xx));
+              }
+              if (s && !s_first && !do_s(xx)) return false;
+            }
+            return true;
+          },
+          [&](int x, int n) -> bool {
+            // (no phase of o_free or o_ready is left out)
+            if (n > 0 && !wait(o_free(x), n - 1)) return false;
+            mma_commit_warp(o_ready(x));
+            return true;
+          });
+      // every MMA of this CTA is complete before TMEM is freed
+      mma_commit_warp(drain_bar);
+      mbar_drain(drain_bar, 0);
+    } else if (warp == C::DEAL_WARP) {
+      // -------------------------- the pieces, their queries and parents
+      int b = b_first;
+      int64_t off = off_first, rem = end - beg;
+      int wb = -1;                     // request of lane 0 below
+      Req mine{};                      // request wb + lane
+      int xs = 0, prev_pair = 1;
+      bool marked = false;
+      int q_issued = 0;                // query loads as TMA boxes
+      for (int n = 0;; ++n) {
+        Piece pc{};
+        if (rem > 0) {
+          // the request that the next tile belongs to
+          for (;;) {
+            if (wb < 0 || b >= wb + 32) {
+              unsigned f = 0;
+              wb = b;
+              mine = request(p, wb + lane, BN, C::ROWS, &f);
+            }
+            const unsigned m = __ballot_sync(
+                0xffffffffu, mine.units > 0 && wb + lane >= b);
+            if (m) {
+              const int at = wb + __ffs(m) - 1;
+              if (at != b) off = 0;
+              b = at;
+              break;
+            }
+            b = wb + 32;
+            off = 0;
+            if (b >= p.batch) break;
+          }
+          if (b >= p.batch) rem = 0;   // (the lengths changed under the call)
+        }
+        if (rem > 0) {
+          const int src = b - wb;
+          auto get = [&](int v) { return __shfl_sync(0xffffffffu, v, src); };
+          const int tiles = get(mine.tiles), units = get(mine.units);
+          const int wt = p.split ? tiles : 1;
+          const int u = static_cast<int>(off / wt);
+          const int t = p.split ? static_cast<int>(off - int64_t{u} * wt) : 0;
+          const int nblk = units / p.Hkv;
+          const int g = u / nblk, rb = u - g * nblk;
+          const int nt = !p.split ? tiles
+                         : rem < tiles - t ? static_cast<int>(rem) : tiles - t;
+          pc.live = 1;
+          pc.b = b;
+          pc.g = g;
+          pc.q0 = get(mine.q0);
+          pc.n = get(mine.n);
+          pc.row0 = rb * C::ROWS;
+          pc.rows = min(pc.n * G - pc.row0, C::ROWS);
+          pc.ctx = get(mine.ctx);
+          pc.kt0 = get(mine.kstart) + t * BN;
+          pc.nt = nt;
+          pc.klo = get(mine.klo);
+          pc.khi = get(mine.khi);
+          pc.pair = NX == 2 && pc.rows > BM;
+          pc.xs = prev_pair ? 0 : xs;
+          xs = (pc.xs + nt) & 1;
+          pc.whole = t == 0 && nt == tiles;
+          pc.slot = 2 * blockIdx.x + (t == 0 ? 1 : 0);
+          if (!pc.whole && t == 0) {
+            // this unit's tiles run on to those of CTA `last`
+            const int64_t e = end - rem + tiles;
+            const int last = static_cast<int>((e * ctas - 1) / n_all);
+            if (lane == 0) {
+              p.marks[2 * blockIdx.x] =
+                  make_int4(last - static_cast<int>(blockIdx.x) + 1, pc.q0,
+                            pc.rows, pc.row0);
+              p.marks[2 * blockIdx.x + 1] = make_int4(g, 0, 0, 0);
+            }
+            marked = true;
+          }
+          off += p.split ? nt : 1;
+          rem -= p.split ? nt : 1;
+          if (off == static_cast<int64_t>(units) * wt) {
+            ++b;
+            off = 0;
+          }
+        }
+        const int s = n & 1;
+        if (n >= 2 && !mbar_wait(it_empty(s), (n / 2 - 1) & 1, abort_flag,
+                                 p.err))
+          break;
+        if (lane == 0) {
+          int4 w[5];
+          memcpy(w, &pc, sizeof(Piece));
+          int4* dst = reinterpret_cast<int4*>(base + C::OFF_PIECE +
+                                              s * C::PIECE_BYTES);
+#pragma unroll
+          for (int k = 0; k < 5; ++k) dst[k] = w[k];
+          mbar_arrive(it_full(s));
+        }
+        if (!pc.live) break;
+        // parents: loads first, bytes in shared memory after the queries
+        constexpr int PER = PKV_TREE_MAX_ROWS / 32;
+        int par[PER];
+#pragma unroll
+        for (int k = 0; k < PER; ++k) {
+          const int i = k * 32 + lane;
+          par[k] = i < pc.n ? __ldg(p.parents + pc.q0 + i) : -1;
+        }
+        // the row tile(s) that this piece's queries go to are free: two pieces
+        // of one row tile take them in turn
+        const bool alt = NX == 2 && !pc.pair;
+        const int before = alt && !prev_pair ? n - 2 : n - 1;
+        if (before >= 0 && !mbar_wait(q_empty(before & 1), (before >> 1) & 1,
+                                      abort_flag, p.err))
+          break;
+        prev_pair = pc.pair || NX == 1;
+        const uint32_t dq = sQ + (alt ? (n & 1) * C::Q_TILE : 0);
+        const int qt = pc.rows > BM ? 2 : 1;
+        if (p.q_tma) {
+          // one box per (row tile, 64 columns): 128 / G rows x the G heads.
+          // Rows past the request are the next tokens' (or zeros): they only
+          // feed scores that no output is taken from.
+          if (lane == 0) {
+            mbar_expect_tx(q_full(s), qt * C::Q_TILE);
+            for (int t = 0; t < qt; ++t)
+#pragma unroll
+              for (int cb = 0; cb < C::NCB; ++cb)
+                tma_load_3d(dq + t * C::Q_TILE + cb * (BM * 128), &tm_q,
+                            cb * 64, pc.g * G,
+                            pc.q0 + (pc.row0 + t * BM) / G, q_full(s));
+          }
+          ++q_issued;
+        } else {
+          const T* Q = static_cast<const T*>(p.q);
+          for (int rr = lane; rr < qt * BM; rr += 32) {
+            const int R = pc.row0 + rr;
+            const bool okq = rr < pc.rows;
+            const T* src = Q;
+            if (okq)
+              src = Q + static_cast<int64_t>(pc.q0 + R / G) * p.q_st +
+                    static_cast<int64_t>(pc.g * G + R % G) * p.q_sh;
+            const uint32_t dst = dq + (rr / BM) * C::Q_TILE;
+            const int rq = rr % BM;
+#pragma unroll
+            for (int ch = 0; ch < D / 8; ++ch)
+              cp_async_16(dst + (ch >> 3) * (BM * 128) + sw128(rq, ch & 7),
+                          okq ? src + ch * 8 : src, okq ? 16 : 0);
+          }
+          cp_async_commit();
+          cp_async_wait<0>();
+          fence_proxy_async();
+          mbar_arrive(q_full(s));
+        }
+        unsigned char* pb = base + C::OFF_PAR + s * PKV_TREE_MAX_ROWS;
+        bool bad = false;
+#pragma unroll
+        for (int k = 0; k < PER; ++k) {
+          const int i = k * 32 + lane;
+          const bool no = par[k] < -1 || par[k] >= i;
+          if (i < pc.n) {
+            bad |= no;
+            pb[i] = static_cast<unsigned char>(
+                no || par[k] < 0 ? kNoParent : par[k]);
+          }
+        }
+        if (bad) atomicOr(p.err, kErrBadTree);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(par_full(s));
+      }
+      if (p.split && lane == 0 && !marked)
+        p.marks[2 * blockIdx.x] = make_int4(0, 0, 0, 0);
+      // no query box may be in flight when the CTA exits
+      if (lane == 0)
+        for (int n = max(0, q_issued - 2); n < q_issued; ++n)
+          mbar_drain(q_full(n & 1), (n >> 1) & 1);
+    }
+  } else {
+    // ------------------------------------------------- softmax warps
+    if constexpr (NX == 2)
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    constexpr float THR = Range<T>::THR, OFF = Range<T>::OFF;
+    const int x = NX == 2 ? warp >> 2 : 0;
+    const int r = tid & 127;                   // row of its tile == TMEM lane
+    const float scale_log2 =
+        p.scale * (p.k_scale ? *p.k_scale : 1.f) * kLog2e;
+    const float vscale = p.v_scale ? *p.v_scale : 1.f;
+    const bool capped = p.softcap > 0.f;
+    const float cap_t = p.softcap * kLog2e;
+    const float cap_u = capped ? 2.f / p.softcap : 0.f;
+    // raw: the scale joins the exponent (max(scale s) = scale max(s))
+    const bool raw = !capped && scale_log2 > 0.f;
+    const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    float2* xch = reinterpret_cast<float2*>(base + C::OFF_XCH);
+    int cnt = 0;                               // tiles seen by this stream
+    int n_x = 0;                               // states exchanged
+    for (int n = 0;; ++n) {
+      Piece pc;
+      if (take(n, pc) <= 0) break;
+      const bool alt = NX == 2 && !pc.pair;
+      const int row = (pc.pair ? x * BM : 0) + r;       // of the block
+      const bool valid = row < pc.rows;
+      const bool live = (row & ~31) < pc.rows;          // any row of the warp
+      const int node = (pc.row0 + (valid ? row : 0)) / G;
+      const int h = pc.g * G + (pc.row0 + (valid ? row : 0)) % G;
+      const int tok = pc.q0 + node;
+      const unsigned char* par =
+          base + C::OFF_PAR + (n & 1) * PKV_TREE_MAX_ROWS;
+      bool ok = true;
+      // first key before the draft that this row sees
+      int k_first = 0;
+      if (p.wl >= 0 && live) {
+        ok = mbar_wait(par_full(n & 1), (n >> 1) & 1, abort_flag, p.err);
+        int depth = 0;
+        for (int a = par[node]; ok && a != kNoParent; a = par[a]) ++depth;
+        k_first = max(pc.ctx + depth - p.wl, 0);
+      }
+      // tiles inside [full_lo, full_hi) need no mask
+      const int full_lo =
+          p.wl >= 0 ? max(pc.ctx + pc.n - 1 - p.wl, 0) : 0;
+      const int full_hi = min(pc.ctx, pc.khi);
+      float m_ref = -INFINITY, l = 0.f;
+      const int j0 = alt ? (pc.xs ^ x) : 0, jd = alt ? 2 : 1;
+      for (int j = j0; ok && j < pc.nt; j += jd, ++cnt) {
+        const int buf = NX == 2 ? x : cnt & 1;
+        const int turn = NX == 2 ? cnt : cnt >> 1;
+        if (!mbar_wait(s_full(buf), turn & 1, abort_flag, p.err)) {
+          ok = false;
+          break;
+        }
+        if (!live) {
+          mbar_arrive(p_full(buf));
+          continue;
+        }
+        tc_fence_after();
+        const int kt = pc.kt0 + j * BN;
+        const bool masked = kt < full_lo || kt + BN > full_hi;
+        const uint32_t s_addr = tmem + lane_base + buf * C::S_STEP;
+        float v[BN];
+#pragma unroll
+        for (int c = 0; c < BN / 32; ++c)
+          tmem_ld32(s_addr + c * 32, v + c * 32);
+        tmem_wait_ld();
+        if (!raw) {
+          // logits in log2 units; soft-cap t (1 - 2 / (1 + 2^(u x))), within
+          // about an ulp of the cap (the hardware tanh loses 2^-11 of it)
+#pragma unroll
+          for (int e = 0; e < BN; ++e) {
+            v[e] *= scale_log2;
+            if (capped)
+              v[e] = cap_t - __fdividef(2.f * cap_t, 1.f + ex2(v[e] * cap_u));
+          }
+        }
+        if (masked) {
+          // one bit a key: those before the draft in the window, and the
+          // chain of rows from this one upwards
+          uint32_t w[BN / 32];
+#pragma unroll
+          for (int i = 0; i < BN / 32; ++i)
+            w[i] = range_bits(k_first - kt, full_hi - kt, i);
+          const int rel0 = pc.ctx - kt;        // row 0's key in the tile
+          if (rel0 < BN) {
+            if (!mbar_wait(par_full(n & 1), (n >> 1) & 1, abort_flag,
+                           p.err)) {
+              ok = false;
+              break;
+            }
+            const int in_tile = min(BN, pc.khi - kt);
+            int a = node;
+            for (int far = 0;; ++far) {
+              if (p.wl >= 0 && far > p.wl) break;
+              const int rel = rel0 + a;
+              if (rel >= 0 && rel < in_tile) {
+#pragma unroll
+                for (int i = 0; i < BN / 32; ++i)
+                  w[i] |= (rel >> 5) == i ? 1u << (rel & 31) : 0u;
+              }
+              a = par[a];
+              if (a == kNoParent) break;
+            }
+          }
+          // (a select: whatever stands in a hidden place is dropped)
+#pragma unroll
+          for (int e = 0; e < BN; ++e)
+            v[e] = (w[e >> 5] >> (e & 31)) & 1u ? v[e] : -INFINITY;
+        }
+        float mx8[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) mx8[e] = -INFINITY;
+#pragma unroll
+        for (int e = 0; e < BN; e += 2)
+          mx8[(e >> 1) & 7] = max3f(mx8[(e >> 1) & 7], v[e], v[e + 1]);
+        float mx =
+            max3f(max3f(mx8[0], mx8[1], mx8[2]), max3f(mx8[3], mx8[4], mx8[5]),
+                  fmaxf(mx8[6], mx8[7]));
+        if (raw) mx *= scale_log2;
+        const bool grow = mx > m_ref + THR;
+        float alpha = 1.f;
+        if (grow) {
+          alpha = ex2(m_ref - mx);
+          m_ref = mx;
+          l *= alpha;
+        }
+        const float base_m = (m_ref == -INFINITY ? 0.f : m_ref) - OFF;
+        if (j >= jd && __any_sync(0xffffffffu, grow)) {
+          // the products so far are complete: with two streams the commit
+          // behind s_full covered them
+          if constexpr (NX == 1) {
+            if (!mbar_wait(pv_done, (cnt - 1) & 1, abort_flag, p.err)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+          }
+          const uint32_t o_addr =
+              tmem + lane_base + x * C::S_STEP + C::O_COL;
+#pragma unroll 1
+          for (int c = 0; c < D / 32; ++c) {
+            float ov[32];
+            tmem_ld32(o_addr + c * 32, ov);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) ov[e] *= alpha;
+            tmem_st32(o_addr + c * 32, ov);
+          }
+        }
+        float sum8[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum8[e] = 0.f;
+        const float sc = raw ? scale_log2 : 1.f;
+#pragma unroll
+        for (int e = 0; e < BN; e += 2) {
+          float x0 = v[e], x1 = v[e + 1];
+          fma2(x0, x1, sc, -base_m);
+          x0 = ex2(x0);
+          x1 = ex2(x1);
+          v[e] = x0;
+          v[e + 1] = x1;
+          add2(sum8[2 * ((e >> 1) & 3)], sum8[2 * ((e >> 1) & 3) + 1], x0,
+               x1);
+        }
+        // P over the first BN / 2 columns of S: column c holds the keys 2c
+        // (low half) and 2c + 1 (high half)
+#pragma unroll
+        for (int c = 0; c < BN / 64; ++c) {
+          float pk[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            pk[e] = __uint_as_float(
+                pack2<T>(v[c * 64 + 2 * e], v[c * 64 + 2 * e + 1]));
+          tmem_st32(s_addr + c * 32, pk);
+        }
+        l += ((sum8[0] + sum8[1]) + (sum8[2] + sum8[3])) +
+             ((sum8[4] + sum8[5]) + (sum8[6] + sum8[7]));
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(p_full(buf));
+      }
+      if (!ok) break;
+      release(n);
+
+      // ---- epilogue: O of each stream relative to m (log2 units)
+      float m = m_ref == -INFINITY ? m_ref : m_ref - OFF;
+      float f0 = 1.f, f1 = 0.f;                // weights of O_0 and O_1
+      if (alt) {
+        // (the other stream has read the state of the piece before)
+        if (n > 0 && !mbar_wait(o_free(0), (n - 1) & 1, abort_flag, p.err))
+          break;
+        xch[x * BM + r] = make_float2(m, l);
+        mbar_arrive(xbar);
+        if (!mbar_wait(xbar, n_x & 1, abort_flag, p.err)) break;
+        ++n_x;
+        const float2 o = xch[(x ^ 1) * BM + r];
+        const float M = fmaxf(m, o.x);
+        const float a = m == -INFINITY ? (l != l ? 1.f : 0.f) : ex2(m - M);
+        const float c = o.x == -INFINITY ? (o.y != o.y ? 1.f : 0.f)
+                                         : ex2(o.x - M);
+        // (the same order of the sum in both streams)
+        f0 = x == 0 ? a : c;
+        f1 = x == 0 ? c : a;
+        const float l0 = x == 0 ? l : o.y, l1 = x == 0 ? o.y : l;
+        l = l0 * f0 + l1 * f1;
+        m = M;
+      }
+      if (!mbar_wait(o_ready(x), n & 1, abort_flag, p.err)) break;
+      if (alt && !mbar_wait(o_ready(x ^ 1), n & 1, abort_flag, p.err)) break;
+      tc_fence_after();
+      float inv, lse_v;
+      finish(m, l, pc.whole ? p.sinks : nullptr, h, &inv, &lse_v);
+      inv *= vscale;
+      f0 *= inv;
+      f1 *= inv;
+      const bool has0 = !alt || pc.nt > 1 || pc.xs == 0;
+      const bool has1 = alt && (pc.nt > 1 || pc.xs == 1);
+      if (live) {
+        T* dst = static_cast<T*>(p.out) + static_cast<int64_t>(tok) * p.o_st +
+                 static_cast<int64_t>(h) * p.o_sh;
+        float* part = p.part_o +
+                      (static_cast<int64_t>(pc.slot) * p.rows_cap + row) * D;
+        // alternating streams share the columns of a row
+        const int c0 = alt ? x * (D / 64) : 0;
+        const int c1 = alt ? c0 + D / 64 : D / 32;
+#pragma unroll 1
+        for (int c = c0; c < c1; ++c) {
+          float ov[32], o1[32];
+          const uint32_t at = tmem + lane_base + C::O_COL + c * 32;
+          tmem_ld32(at + (alt ? 0 : x * C::S_STEP), ov);
+          if (NX == 2 && has1) tmem_ld32(at + C::S_STEP, o1);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            float y = has0 ? ov[e] * f0 : 0.f;
+            if (NX == 2 && has1) y += o1[e] * f1;
+            ov[e] = y;
+          }
+          if (!valid) continue;
+          if (!pc.whole) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 8) {
+              uint32_t w[8];
+#pragma unroll
+              for (int k = 0; k < 8; ++k) w[k] = __float_as_uint(ov[e + k]);
+              st_global_v8(part + c * 32 + e, w);
+            }
+          } else if (p.out_v8) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 16) {
+              uint32_t w[8];
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                w[k] = pack2<T>(ov[e + 2 * k], ov[e + 2 * k + 1]);
+              st_global_v8(dst + c * 32 + e, w);
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; e += 8) {
+              uint4 pk;
+              pk.x = pack2<T>(ov[e], ov[e + 1]);
+              pk.y = pack2<T>(ov[e + 2], ov[e + 3]);
+              pk.z = pack2<T>(ov[e + 4], ov[e + 5]);
+              pk.w = pack2<T>(ov[e + 6], ov[e + 7]);
+              *reinterpret_cast<uint4*>(dst + c * 32 + e) = pk;
+            }
+          }
+        }
+        if (valid && !(alt && x == 1)) {
+          if (!pc.whole)
+            p.part_lse[static_cast<int64_t>(pc.slot) * p.rows_cap + row] =
+                lse_v;
+          else if (p.lse)
+            p.lse[static_cast<int64_t>(h) * p.total_q + tok] = lse_v;
+        }
+      }
+      tc_fence_before();
+      if (alt) {
+        mbar_arrive(o_free(0));
+        mbar_arrive(o_free(1));
+      } else {
+        // (counted for both streams' threads)
+        for (int k = 0; k < NX; ++k) mbar_arrive(o_free(x));
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == C::MMA_WARP) {
+    tc_fence_after();
+    asm volatile(
+        "tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem)
+        : "memory");
+  }
+}
+
+// Joins the pieces of the units that the shares' ends cut.  Block (c, y): rows
+// y of the unit that CTA c starts and does not end, a warp per row: M = the
+// largest partial LSE (and the sink), w_k = e^(lse_k - M), out = sum w_k o_k /
+// sum w_k, lse = M + ln sum w_k.
+constexpr int kFoldThreads = 256;
+template <typename T, int D>
+__global__ void __launch_bounds__(kFoldThreads)
+fold_kernel(const Params p) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int c = blockIdx.x;
+  const int4 m0 = p.marks[2 * c];
+  const int np = min(m0.x, static_cast<int>(gridDim.x) - c);
+  if (np <= 0) return;
+  const int g = p.marks[2 * c + 1].x;
+  const int lane = threadIdx.x & 31;
+  constexpr int W = kFoldThreads / 32, V = D / 32;
+  const int rows = min(m0.z, p.rows_cap);
+  for (int row = blockIdx.y * W + (threadIdx.x >> 5); row < rows;
+       row += gridDim.y * W) {
+    const int R = m0.w + row;
+    const int tok = m0.y + R / p.G, h = g * p.G + R % p.G;
+    auto at = [&](int k) -> int64_t {
+      const int slot = k == 0 ? 2 * c + 1 : 2 * (c + k);
+      return static_cast<int64_t>(slot) * p.rows_cap + row;
+    };
+    float M = p.sinks ? p.sinks[h] : -INFINITY;
+    const float z = M;
+    for (int k0 = 0; k0 < np; k0 += 32) {
+      float s = k0 + lane < np ? p.part_lse[at(k0 + lane)] : -INFINITY;
+#pragma unroll
+      for (int o = 16; o; o >>= 1)
+        s = fmaxf(s, __shfl_xor_sync(0xffffffffu, s, o));
+      M = fmaxf(M, s);
+    }
+    const float ref = M == -INFINITY ? 0.f : M;
+    float sum = p.sinks ? ex2((z - ref) * kLog2e) : 0.f;
+    float acc[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) acc[e] = 0.f;
+    for (int k0 = 0; k0 < np; k0 += 4) {
+      float s[4], o[4][V];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int k = min(k0 + i, np - 1);
+        s[i] = p.part_lse[at(k)];
+        const float* src = p.part_o + at(k) * D + lane * V;
+#pragma unroll
+        for (int e = 0; e < V; e += 2) {
+          const float2 t = *reinterpret_cast<const float2*>(src + e);
+          o[i][e] = t.x;
+          o[i][e + 1] = t.y;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        // (a NaN sum stays NaN)
+        const float w = k0 + i < np ? ex2((s[i] - ref) * kLog2e) : 0.f;
+        sum += w;
+#pragma unroll
+        for (int e = 0; e < V; ++e) acc[e] = fmaf(w, o[i][e], acc[e]);
+      }
+    }
+    const float inv = sum > 0.f ? 1.f / sum : sum != sum ? sum : 0.f;
+    T* dst = static_cast<T*>(p.out) + static_cast<int64_t>(tok) * p.o_st +
+             static_cast<int64_t>(h) * p.o_sh + lane * V;
+#pragma unroll
+    for (int e = 0; e < V; e += 2)
+      *reinterpret_cast<uint32_t*>(dst + e) =
+          pack2<T>(acc[e] * inv, acc[e + 1] * inv);
+    if (p.lse && lane == 0)
+      p.lse[static_cast<int64_t>(h) * p.total_q + tok] =
+          sum > 0.f ? ref + lg2(sum) * kLn2 : sum != sum ? sum : -INFINITY;
+  }
+}
+
+int block_rows(int D) { return D == 256 ? Cfg<256>::ROWS : Cfg<128>::ROWS; }
+// Rows of a partial: the most packed rows of a block.
+int rows_cap(int D, int G, int max_n) {
+  const int64_t r = static_cast<int64_t>(max_n) * G;
+  return static_cast<int>(r < block_rows(D) ? r : block_rows(D));
+}
+size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
+
+}  // namespace tree
+
+size_t tree_scratch_bytes(int D, int G, int max_n, int sms) {
+  const size_t rows = static_cast<size_t>(tree::rows_cap(D, G, max_n));
+  return tree::align256(2 * sizeof(int4) * sms) +
+         tree::align256(2 * rows * sms * sizeof(float)) +
+         2 * rows * sms * D * sizeof(float);
+}
+
+cudaError_t launch_tree_attn(const AttnParams& a, const int32_t* parents,
+                             int max_n, int64_t max_k, int D, bool bf16,
+                             int sms, void* scratch, bool pdl,
+                             cudaStream_t stream) {
+  using namespace tree;
+  Params p{};
+  p.q = a.q;
+  p.q_st = a.q_st;
+  p.q_sh = a.q_sh;
+  p.out = a.out;
+  p.o_st = a.o_st;
+  p.o_sh = a.o_sh;
+  p.lse = a.lse;
+  p.total_q = a.total_q;
+  p.batch = a.batch;
+  p.max_n = max_n;
+  p.cu_q = a.cu_q;
+  p.seqused_k = a.seqused_k;
+  p.parents = parents;
+  p.block_table = a.block_table;
+  p.bt_stride = a.bt_stride;
+  p.max_blocks = a.max_blocks;
+  p.num_blocks = a.num_blocks;
+  p.Hq = a.Hq;
+  p.Hkv = a.Hkv;
+  p.G = a.G;
+  p.BS = a.BS;
+  p.scale = a.scale;
+  p.softcap = a.softcap;
+  p.sinks = a.sinks;
+  p.k_scale = a.k_scale;
+  p.v_scale = a.v_scale;
+  p.wl = a.wl;
+  p.err = a.err;
+  int RB = 16;
+  while (RB * 2 <= 64 && a.BS % (RB * 2) == 0) RB *= 2;
+  p.RB = RB;
+  p.kv_order_hnd = a.c_sh > a.c_sr ? 1 : 0;
+  p.out_v8 = (reinterpret_cast<uintptr_t>(a.out) % 32 == 0 &&
+              (a.o_st * 2) % 32 == 0 && (a.o_sh * 2) % 32 == 0)
+                 ? 1
+                 : 0;
+  const int64_t packed = static_cast<int64_t>(max_n) * a.G;
+  const int64_t blocks = (packed + block_rows(D) - 1) / block_rows(D);
+  p.once = blocks <= 1;        // every tile is read by one CTA only
+  // an upper bound of the tiles (a window adds up to a tile at either end)
+  const int bn = D == 256 ? 64 : 128;
+  int64_t keys = max_k;
+  if (a.wl >= 0 && static_cast<int64_t>(a.wl) + max_n + RB < keys)
+    keys = static_cast<int64_t>(a.wl) + max_n + RB;
+  const int64_t units = static_cast<int64_t>(a.batch) * a.Hkv * blocks;
+  const int64_t tiles = units * ((keys + bn - 1) / bn + 1);
+  p.split = scratch != nullptr;
+  p.rows_cap = rows_cap(D, a.G, max_n);
+  const int64_t most = p.split ? tiles : units;
+  const int grid = static_cast<int>(most < sms ? most : sms);
+  if (p.split) {
+    char* s = static_cast<char*>(scratch);
+    p.marks = reinterpret_cast<int4*>(s);
+    s += align256(2 * sizeof(int4) * sms);
+    p.part_lse = reinterpret_cast<float*>(s);
+    s += align256(2 * static_cast<size_t>(p.rows_cap) * sms * sizeof(float));
+    p.part_o = reinterpret_cast<float*>(s);
+  }
+  CUtensorMap mk, mv, mq;
+  memset(&mq, 0, sizeof(mq));
+  // one box per page and matrix where the view allows it
+  p.kv_rg = make_kv_rg_map(&mk, a.kc, bf16, D, a.BS, a.Hkv, a.num_blocks,
+                           a.c_sb, a.c_sr, a.c_sh, RB, p.kv_order_hnd) &&
+            make_kv_rg_map(&mv, a.vc, bf16, D, a.BS, a.Hkv, a.num_blocks,
+                           a.c_sb, a.c_sr, a.c_sh, RB, p.kv_order_hnd);
+  if (!p.kv_rg &&
+      (!make_kv_map(&mk, a.kc, bf16, D, a.BS, a.Hkv, a.num_blocks, a.c_sb,
+                    a.c_sr, a.c_sh, RB, p.kv_order_hnd) ||
+       !make_kv_map(&mv, a.vc, bf16, D, a.BS, a.Hkv, a.num_blocks, a.c_sb,
+                    a.c_sr, a.c_sh, RB, p.kv_order_hnd)))
+    return cudaErrorInvalidValue;
+  p.q_tma = make_rows_map(&mq, a.q, bf16, D, a.Hq, a.total_q, a.q_st, a.q_sh,
+                          a.G);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  auto config = [&](dim3 g, int threads, int smem) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = g;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = pdl ? attr : nullptr;
+    cfg.numAttrs = pdl ? 1 : 0;
+    return cfg;
+  };
+  auto go = [&](auto kern, auto fold, int threads, int smem,
+                bool regs) -> cudaError_t {
+    cudaError_t e;
+    if (regs) {
+      // the register split inside the kernel adds up to the launch's
+      cudaFuncAttributes fa;
+      e = cudaFuncGetAttributes(&fa, kern);
+      if (e != cudaSuccess) return e;
+      if (fa.numRegs != kLaunchRegs) return cudaErrorInvalidConfiguration;
+    }
+    e = smem_opt_in(reinterpret_cast<const void*>(kern), smem);
+    if (e != cudaSuccess) return e;
+    note_launch();
+    const cudaLaunchConfig_t c1 = config(dim3(grid), threads, smem);
+    e = cudaLaunchKernelEx(&c1, kern, p, mk, mv, mq);
+    if (e != cudaSuccess || !p.split) return e;
+    note_launch();
+    int y = (p.rows_cap + 15) / 16;
+    const cudaLaunchConfig_t c2 = config(dim3(grid, y), kFoldThreads, 0);
+    return cudaLaunchKernelEx(&c2, fold, p);
+  };
+#define PKV_TREE_GO(T, DD)                                                 \
+  go(tree_attn_kernel<T, DD>, fold_kernel<T, DD>, Cfg<DD>::THREADS,        \
+     Cfg<DD>::SMEM, Cfg<DD>::NX == 2)
+  switch (D) {
+    case 64:
+      return bf16 ? PKV_TREE_GO(__nv_bfloat16, 64) : PKV_TREE_GO(__half, 64);
+    case 128:
+      return bf16 ? PKV_TREE_GO(__nv_bfloat16, 128)
+                  : PKV_TREE_GO(__half, 128);
+    case 256:
+      return bf16 ? PKV_TREE_GO(__nv_bfloat16, 256)
+                  : PKV_TREE_GO(__half, 256);
+  }
+#undef PKV_TREE_GO
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace pkv
