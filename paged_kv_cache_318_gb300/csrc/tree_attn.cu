@@ -30,9 +30,11 @@
 // of 64-key tiles with two score buffers, S of the next tile running under the
 // softmax.
 //
-// K and V tiles share one ring, filled by one warp in the order in which the
-// MMA warp consumes them (walk() below gives both the same order, across the
-// pieces' borders too), so that the stages not in use are all prefetch.
+// K and V tiles share one ring in the order in which the products take them
+// (place_k, place_v), so that the stages not in use are all prefetch.  Each
+// stream has an MMA warp of its own: one warp for both, which also kept the
+// order across the pieces' borders, ran 3000 clocks of its own instructions a
+// tile, more than the tile's share of HBM (64 KB: 2800).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <math.h>
@@ -81,14 +83,16 @@ struct Cfg {
   static constexpr int O_COL = NX == 2 ? BN : 2 * BN;  // of stream 0
   static_assert(NX * (BN + D) + (NX == 1 ? BN : 0) <= 512, "TMEM columns");
   static constexpr int SM_WARPS = 4 * NX;
-  static constexpr int MMA_WARP = SM_WARPS, LOAD_WARP = SM_WARPS + 1,
-                       DEAL_WARP = SM_WARPS + 2;
+  // the MMA warps (one per stream) on the schedulers that have the least to do
+  // for a small tree, whose rows are those of softmax warps 0, 1, 4 and 5
+  static constexpr int DEAL_WARP = SM_WARPS, LOAD_WARP = SM_WARPS + 1,
+                       MMA_WARP = SM_WARPS + 2;
   static constexpr int THREADS = (SM_WARPS + 4) * 32;
   static constexpr int SLOTS = 2;                      // pieces in flight
   static constexpr int OFF_Q = 0;
   static constexpr int OFF_RING = OFF_Q + NX * Q_TILE;
   static constexpr int OFF_BAR = OFF_RING + STAGES * STAGE;
-  static constexpr int BAR_BYTES = 8 * (2 * STAGES + 22);
+  static constexpr int BAR_BYTES = 8 * ((NX == 2 ? 4 : 2) * STAGES + 22);
   static constexpr int OFF_PIECE = OFF_BAR + BAR_BYTES;
   static constexpr int PIECE_BYTES = 80;
   static constexpr int OFF_PAR = OFF_PIECE + SLOTS * PIECE_BYTES;
@@ -142,20 +146,10 @@ struct Piece {
   int kt0, nt;              // first key of the first tile, tiles
   int klo, khi;             // keys any row sees; khi also bounds the reads
   int pair;                 // more than 128 rows
-  int xs;                   // stream of the first tile (not pair)
   int whole, slot;          // the whole unit; else its partial's slot
-  int pad[4];
+  int pad[5];
 };
 static_assert(sizeof(Piece) == 80, "copied as 5 x 16 bytes");
-
-// A key tile on its way through the CTA.
-struct Tile {
-  int kt, klo, khi, g;
-  int n;                    // piece
-  int first, last;          // of its stream in the piece
-  int head, tail;           // first / last tile of the piece
-  int id;                   // loader: this lane's page
-};
 
 // What a request asks for; rows <= 0: nothing.
 struct Req {
@@ -190,76 +184,16 @@ __device__ __forceinline__ Req request(const Params& p, int b, int BN,
   return r;
 }
 
-// Runs f over the tiles of the CTA's pieces, in the order in which they are
-// worked through: f(x, pv, s) handles the P V product of tile *pv and the
-// score product of tile *s of stream x (2: both streams), either may be null.
-// A tile's P V follows when its stream's next tile comes (or the end).
-// idle(x, n): stream x has no tile in piece n, and its earlier ones are done.
-// take(n, piece): 1 = piece n, 0 = no more, -1 = abort.  make(piece, n, j):
-// the piece's j-th tile.
-template <int NX, class Take, class Make, class Step, class Idle>
-__device__ __forceinline__ bool walk(Take take, Make make, Step f,
-                                     Idle idle) {
-  Tile p0{}, p1{};
-  bool h0 = false, h1 = false;
-  int newer = 0, pair = 0;
-  auto flush = [&]() -> bool {
-    bool ok = true;
-    if (NX == 2 && !pair) {
-      // the older tile first
-      if (newer == 0) {
-        if (h1) ok = f(1, &p1, nullptr);
-        if (ok && h0) ok = f(0, &p0, nullptr);
-      } else {
-        if (h0) ok = f(0, &p0, nullptr);
-        if (ok && h1) ok = f(1, &p1, nullptr);
-      }
-    } else if (h0) {
-      ok = f(NX == 2 ? 2 : 0, &p0, nullptr);
-    }
-    h0 = h1 = false;
-    return ok;
-  };
-  for (int n = 0;; ++n) {
-    Piece pc;
-    const int got = take(n, pc);
-    if (got < 0) return false;
-    if (got == 0) break;
-    if (pc.pair != pair && !flush()) return false;
-    pair = pc.pair;
-    for (int j = 0; j < pc.nt; ++j) {
-      Tile t = make(pc, n, j);
-      t.head = j == 0;
-      t.tail = j == pc.nt - 1;
-      const bool alt = NX == 2 && !pair;
-      t.first = j < (alt ? 2 : 1);
-      t.last = j + (alt ? 2 : 1) >= pc.nt;
-      const int x = alt ? ((pc.xs + j) & 1) : 0;
-      if (x == 0) {
-        if (!f(NX == 2 && pair ? 2 : 0, h0 ? &p0 : nullptr, &t)) return false;
-        p0 = t;
-        h0 = true;
-      } else {
-        if (!f(1, h1 ? &p1 : nullptr, &t)) return false;
-        p1 = t;
-        h1 = true;
-      }
-      newer = x;
-      // a piece of one tile leaves the other stream idle: finish there what
-      // an earlier piece waits for
-      if (alt && pc.nt == 1) {
-        if (x == 0 && h1) {
-          if (!f(1, &p1, nullptr)) return false;
-          h1 = false;
-        } else if (x == 1 && h0) {
-          if (!f(0, &p0, nullptr)) return false;
-          h0 = false;
-        }
-        if (!idle(x ^ 1, n)) return false;
-      }
-    }
-  }
-  return flush();
+// Places in the ring of a piece's K and V tiles, counted from its first: the
+// order in which the products take them.
+//   pair            S(0) | P V(0) S(1) | P V(1) S(2) | ...   of both streams
+//   else, two lines of tiles (or of score buffers):
+//                   S(0) | S(1) | P V(0) S(2) | P V(1) S(3) | ...
+__device__ __forceinline__ int place_k(int j, bool pair) {
+  return pair ? 2 * j : j < 2 ? j : 2 * j - 1;
+}
+__device__ __forceinline__ int place_v(int j, int nt, bool pair) {
+  return pair ? 2 * j + 1 : min(2 * j + 2, 2 * nt - 1);
 }
 
 // 1 / denominator and the natural LSE of a row whose sum is l relative to m
@@ -309,9 +243,14 @@ tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
   const uint32_t sQ = base_u + C::OFF_Q;
   const uint32_t sR = base_u + C::OFF_RING;
   const uint32_t bar0 = base_u + C::OFF_BAR;
-  auto full = [&](int s) { return bar0 + 8 * s; };
-  auto empty = [&](int s) { return bar0 + 8 * (ST + s); };
-  constexpr int B0 = 2 * ST;
+  // A stage's loads of stream 0, of stream 1 and of both complete on barriers
+  // of their own: a waiter sees one parity, so it has to wait for every load of
+  // a barrier, and the streams run ahead of one another.
+  constexpr int SETS = NX == 2 ? 3 : 1;
+  auto full = [&](int set, int s) { return bar0 + 8 * (set * ST + s); };
+  auto empty = [&](int s) { return bar0 + 8 * (SETS * ST + s); };
+  constexpr int B0 = (SETS + 1) * ST;
+  static_assert(SETS * ST <= 32, "parities in a word");
   auto s_full = [&](int x) { return bar0 + 8 * (B0 + x); };
   auto p_full = [&](int x) { return bar0 + 8 * (B0 + 2 + x); };
   auto o_ready = [&](int x) { return bar0 + 8 * (B0 + 4 + x); };
@@ -332,8 +271,8 @@ tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
 
   if (tid == 0) {
     for (int s = 0; s < ST; ++s) {
-      mbar_init(full(s), 1);
-      mbar_init(empty(s), 1);
+      for (int k = 0; k < SETS; ++k) mbar_init(full(k, s), 1);
+      mbar_init(empty(s), NX);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(s_full(s), 1);
@@ -341,14 +280,14 @@ tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
       mbar_init(o_ready(s), 1);
       mbar_init(o_free(s), NX * 128);
       mbar_init(q_full(s), p.q_tma ? 1 : 32);
-      mbar_init(q_empty(s), 1);
+      mbar_init(q_empty(s), NX);
       mbar_init(it_full(s), 1);
-      mbar_init(it_empty(s), C::SM_WARPS + 2);
+      mbar_init(it_empty(s), C::SM_WARPS + NX + 1);
       mbar_init(par_full(s), 1);
     }
     mbar_init(xbar, 256);
     mbar_init(pv_done, 1);
-    mbar_init(drain_bar, 1);
+    mbar_init(drain_bar, NX);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -466,235 +405,231 @@ tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
       asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp == C::LOAD_WARP) {
       // ------------------------------------------------- K / V loader
-      // lane i issues the box of page i of a tile; its page id is fetched a
-      // tile ahead
-      int gi = 0;                      // stages filled so far
-      int nxt = 0;
+      // Step i of a piece loads K tile i (lanes 0 .. 15, a page's box each) and
+      // V tile i - lag (lanes 16 .. 31), which are next to one another in the
+      // ring.  A lane's page id is fetched a step ahead.
+      const int half = lane >> 4, box = lane & 15;
+      const void* tm = half ? static_cast<const void*>(&tm_v)
+                            : static_cast<const void*>(&tm_k);
       const uint64_t pol = l2_evict_first_policy();
-      auto load = [&](const void* tm, const Tile& t) -> bool {
-        const int s = gi % ST;
-        const int nbox =
-            max(min((t.khi - t.kt + RB - 1) / RB, BN / RB), 0);
-        int stop = 0;
-        if (lane == 0) {
-          if (gi >= ST && !mbar_wait(empty(s), (gi / ST - 1) & 1, abort_flag,
-                                     p.err))
-            stop = 1;
-          else
-            mbar_expect_tx(full(s), nbox * C::NCB * RB * 128);
-        }
-        stop = __shfl_sync(0xffffffffu, stop, 0);
-        if (stop) return false;
-        if (lane < nbox) {
-          const int row = (t.kt + lane * RB) % p.BS;
-          const uint32_t dst0 = sR + s * C::STAGE;
-          if (p.kv_rg) {
-            const uint32_t dst = dst0 + lane * (RB / 8) * gs;
-            const int c3 = p.kv_order_hnd ? row >> 3
-                                          : t.id * (p.BS >> 3) + (row >> 3);
-            const int c4 = p.kv_order_hnd ? t.id * p.Hkv + t.g : t.g;
-            if (p.once)
-              tma_load_5d_hint(dst, tm, 0, 0, 0, c3, c4, full(s), pol);
+      const int boxes = BN / RB;
+      const int per_page = p.BS / RB;  // boxes of a page
+      int at = 0;                      // loads of the pieces before
+      uint32_t sent = 0, ever = 0;     // lane 0: loads of each barrier, mod 2
+      bool ok = true;
+      for (int n = 0; ok; ++n) {
+        Piece pc;
+        if (take(n, pc) <= 0) break;
+        release(n);
+        const int lag = NX == 2 && !pc.pair ? 2 : 1;
+        const bool pair = pc.pair;
+        const int32_t* bt =
+            p.block_table + static_cast<int64_t>(pc.b) * p.bt_stride;
+        // this lane's entry of its next tile
+        int k0 = pc.kt0 + box * RB;
+        int col = k0 / p.BS, sub = (k0 - col * p.BS) / RB;
+        int nxt = box < boxes && k0 < pc.khi ? __ldg(bt + col) : 0;
+#pragma unroll 1
+        for (int i = 0; i < pc.nt + lag; ++i) {
+          const int j = half ? i - lag : i;
+          const bool mine = j >= 0 && j < pc.nt;
+          const int kt = pc.kt0 + j * BN;
+          const int nbox =
+              mine ? max(min((pc.khi - kt + RB - 1) / RB, boxes), 0) : 0;
+          int id = nxt;
+          const int row = sub * RB;
+          if (mine) {
+            k0 += BN;
+            sub += boxes;
+            while (sub >= per_page) {
+              sub -= per_page;
+              ++col;
+            }
+            if (box < boxes && k0 < pc.khi) nxt = __ldg(bt + col);
+          }
+          const int pos = at + (half ? place_v(j, pc.nt, pair)
+                                     : place_k(j, pair));
+          const int st = pos % ST;
+          const int set = NX == 1 ? 0 : pair ? 2 : j & 1;
+          int stop = 0;
+          if (box == 0 && mine) {
+            if (pos >= ST && !mbar_wait(empty(st), (pos / ST - 1) & 1,
+                                        abort_flag, p.err))
+              stop = 1;
             else
-              tma_load_5d(dst, tm, 0, 0, 0, c3, c4, full(s));
-          } else {
-#pragma unroll
-            for (int cb = 0; cb < C::NCB; ++cb) {
-              const uint32_t dst = dst0 + cb * cbs + lane * RB * 128;
-              const int c1 = p.kv_order_hnd ? row : t.g;
-              const int c2 = p.kv_order_hnd ? t.g : row;
+              mbar_expect_tx(full(set, st), nbox * C::NCB * RB * 128);
+          }
+          if (__any_sync(0xffffffffu, stop)) {
+            ok = false;
+            break;
+          }
+          if (box < nbox) {
+            if (id < 0 || id >= p.num_blocks) {
+              atomicOr(p.err, kErrBadBlock);
+              id = 0;
+            }
+            const uint32_t dst = sR + st * C::STAGE;
+            if (p.kv_rg) {
+              const uint32_t to = dst + box * (RB / 8) * gs;
+              const int c3 = p.kv_order_hnd
+                                 ? row >> 3
+                                 : id * (p.BS >> 3) + (row >> 3);
+              const int c4 = p.kv_order_hnd ? id * p.Hkv + pc.g : pc.g;
               if (p.once)
-                tma_load_4d_hint(dst, tm, cb * 64, c1, c2, t.id, full(s),
-                                 pol);
+                tma_load_5d_hint(to, tm, 0, 0, 0, c3, c4, full(set, st), pol);
               else
-                tma_load_4d(dst, tm, cb * 64, c1, c2, t.id, full(s));
+                tma_load_5d(to, tm, 0, 0, 0, c3, c4, full(set, st));
+            } else {
+              const int c1 = p.kv_order_hnd ? row : pc.g;
+              const int c2 = p.kv_order_hnd ? pc.g : row;
+#pragma unroll 1
+              for (int cb = 0; cb < C::NCB; ++cb)
+                tma_load_4d(dst + cb * cbs + box * RB * 128, tm, cb * 64, c1,
+                            c2, id, full(set, st));
             }
           }
+          // (for the end: which barrier each load went to)
+          const uint32_t bit = box == 0 && mine ? 1u << (set * ST + st) : 0u;
+          const uint32_t bits =
+              bit | __shfl_xor_sync(0xffffffffu, bit, 16);
+          if (lane == 0) sent ^= bits;
+          if (lane == 0) ever |= bits;
         }
-        ++gi;
-        return true;
-      };
-      auto fetch = [&](const Piece& pc, int j) -> int {
-        const int k0 = pc.kt0 + j * BN + lane * RB;
-        if (j >= pc.nt || lane >= BN / RB || k0 >= pc.khi) return 0;
-        const int blk = __ldg(p.block_table +
-                              static_cast<int64_t>(pc.b) * p.bt_stride +
-                              k0 / p.BS);
-        if (blk < 0 || blk >= p.num_blocks) {
-          atomicOr(p.err, kErrBadBlock);
-          return 0;
-        }
-        return blk;
-      };
-      walk<NX>(
-          [&](int n, Piece& pc) {
-            const int got = take(n, pc);
-            if (got > 0) {
-              release(n);
-              nxt = fetch(pc, 0);
-            }
-            return got;
-          },
-          [&](const Piece& pc, int n, int j) {
-            Tile t{};
-            t.kt = pc.kt0 + j * BN;
-            t.khi = pc.khi;
-            t.g = pc.g;
-            t.id = nxt;
-            nxt = fetch(pc, j + 1);
-            return t;
-          },
-          [&](int, const Tile* pv, const Tile* s) {
-            // (one stream: the next scores go before P V, except where a
-            // piece starts)
-            if (NX == 1 && s && !s->head) {
-              if (!load(&tm_k, *s)) return false;
-              s = nullptr;
-            }
-            if (pv && !load(&tm_v, *pv)) return false;
-            if (s && !load(&tm_k, *s)) return false;
-            return true;
-          },
-          [](int, int) { return true; });
+        at += 2 * pc.nt;
+      }
       // no copy may be in flight when the CTA exits
       if (lane == 0)
-        for (int t = max(0, gi - ST); t < gi; ++t)
-          mbar_drain(full(t % ST), (t / ST) & 1);
-    } else if (warp == C::MMA_WARP) {
-      // ------------------------------------------------------ MMA issuer
+        for (int k = 0; k < SETS * ST; ++k)
+          if (ever >> k & 1) mbar_drain(full(0, k), (sent >> k & 1) ^ 1);
+    } else if (warp >= C::MMA_WARP && warp < C::MMA_WARP + NX) {
+      // -------------------------------------- MMA issuer of stream x
+      const int x = NX == 2 ? warp - C::MMA_WARP : 0;
       constexpr bool kBF16 = std::is_same<T, __nv_bfloat16>::value;
       constexpr uint32_t ID_S = idesc(128, BN, kBF16, false);
       constexpr uint32_t ID_PV = idesc(128, D, kBF16, true);
-      int gi = 0;                      // stages consumed so far
-      int pcnt[2] = {0, 0};            // P of each S buffer
-      int scnt = 0;                    // score products (one stream)
-      auto wait = [&](uint32_t bar, int parity) -> bool {
+      const uint32_t acc = tmem + x * C::S_STEP + C::O_COL;
+      uint32_t s_cnt = 0, pv_cnt = 0;  // products issued
+      int at = 0;                      // loads of the pieces before
+      bool ok = true;
+      auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
         const bool r = mbar_wait(bar, parity & 1, abort_flag, p.err);
         tc_fence_after();
         return r;
       };
-      // V resident, rows that no row of the block sees set to zero (they may
-      // hold another request's NaN)
-      auto v_here = [&](int g_, const Tile& t) -> bool {
-        const int s = g_ % ST;
-        if (!wait(full(s), g_ / ST)) return false;
-        const int lo = max(t.klo - t.kt, 0);
-        const int hi = max(min(t.khi - t.kt, BN), lo);
-        const int dead = lo + BN - hi;
-        if (dead > 0) {
-          const uint32_t v0 = sR + s * C::STAGE;
-          for (int i = lane; i < dead * 8 * C::NCB; i += 32) {
-            const int cb = i / (dead * 8);
-            const int rem = i - cb * (dead * 8);
-            int r = rem / 8;
-            if (r >= lo) r += hi - lo;
-            asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(
-                             v0 + (r >> 3) * gs + cb * cbs + (r & 7) * 128 +
-                             ((rem % 8) << 4)),
-                         "r"(0)
-                         : "memory");
-          }
-          fence_proxy_async();
-          __syncwarp();
+      // The load in stage st has landed.
+      uint32_t f_turn = 0;             // parities of full: ST bits a set
+      auto loaded = [&](int st, int set) -> bool {
+        const int bit = set * ST + st;
+        const bool r = wait(full(set, st), f_turn >> bit);
+        f_turn ^= 1u << bit;
+        return r;
+      };
+      for (int n = 0; ok; ++n) {
+        Piece pc;
+        if (take(n, pc) <= 0) break;
+        release(n);
+        const bool pair = pc.pair;
+        const bool alt = NX == 2 && !pair;
+        // tiles of this stream: j0, j0 + step, ...
+        const int j0 = alt ? x : 0, step = alt ? 2 : 1;
+        const int tiles = (pc.nt - j0 + step - 1) / step;
+        const int set = NX == 1 ? 0 : pair ? 2 : x;
+        const int qt = NX == 1 ? 0 : pair ? x : n & 1;
+        const uint64_t qd = sdesc(sQ + qt * C::Q_TILE, 16, 1024);
+        if (tiles == 0) {
+          // (no phase of q_empty, o_free or o_ready is left out)
+          mma_commit_warp(q_empty(n & 1));
+          if (n > 0 && !wait(o_free(x), n - 1)) break;
         }
-        return true;
-      };
-      // S of the K tile in stage g_ and the queries in row tile qt
-      auto issue_s = [&](int buf, int g_, int qt) {
-        const uint32_t q0 = sQ + qt * C::Q_TILE;
-        const uint64_t a0 = sdesc(q0, 16, 1024);
-        const uint64_t b0 = sdesc(sR + (g_ % ST) * C::STAGE, 16, gs);
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-          mma_f16_warp(tmem + buf * C::S_STEP,
-                       a0 + (((k >> 2) * (BM * 128) + (k & 3) * 32) >> 4),
-                       b0 + (((k >> 2) * cbs + (k & 3) * 32) >> 4), ID_S,
-                       k > 0 ? 1 : 0);
-        mma_commit_warp(s_full(buf));
-      };
-      // P V of the tile whose probabilities lie in S buffer `buf`, into the
-      // accumulator of stream x; false on abort
-      auto issue_pv = [&](int x, int buf, int g_, const Tile& t) -> bool {
-        // the epilogue of the piece before has read the accumulator
-        if (t.first && t.n > 0 && !wait(o_free(x), t.n - 1)) return false;
-        if (!wait(p_full(buf), pcnt[buf])) return false;
-        ++pcnt[buf];
-        const uint64_t b0 = sdesc(sR + (g_ % ST) * C::STAGE, cbs, gs);
-        const uint32_t acc = tmem + x * C::S_STEP + C::O_COL;
-#pragma unroll
-        for (int k = 0; k < BN / 16; ++k)
-          mma_f16_tmem_a_warp(acc, tmem + buf * C::S_STEP + 8 * k,
-                              b0 + ((k * 2 * gs) >> 4), ID_PV,
-                              (!t.first || k > 0) ? 1 : 0);
-        if constexpr (NX == 1) mma_commit_warp(pv_done);
-        return true;
-      };
-      walk<NX>(
-          [&](int n, Piece& pc) {
-            const int got = take(n, pc);
-            if (got > 0) release(n);
-            return got;
-          },
-          [&](const Piece& pc, int n, int j) {
-            Tile t{};
-            t.kt = pc.kt0 + j * BN;
-            t.klo = pc.klo;
-            t.khi = pc.khi;
-            t.n = n;
-            // (slot of the queries: two pieces of one row tile each can be
-            // in shared memory at once)
-            t.g = NX == 2 && !pc.pair ? n & 1 : 0;
-            return t;
-          },
-          [&](int x, const Tile* pv, const Tile* s) -> bool {
-            const int x0 = x == 2 ? 0 : x, x1 = x == 2 ? 1 : x;
-            const bool s_first = NX == 1 && s && !s->head;
-            const int gk = s_first ? gi : gi + (pv ? 1 : 0);
-            const int gv = s_first ? gi + 1 : gi;
-            gi += (pv ? 1 : 0) + (s ? 1 : 0);
-            bool k_here = false;
-            auto do_s = [&](int xx) -> bool {
-              if (!k_here) {
-                if (s->head && !wait(q_full(s->n & 1), s->n >> 1))
-                  return false;
-                if (!wait(full(gk % ST), gk / ST)) return false;
-                k_here = true;
-              }
-              if constexpr (NX == 1) {
-                issue_s(scnt & 1, gk, 0);
-                ++scnt;
-              } else {
-                issue_s(xx, gk, x == 2 ? xx : s->g);
-              }
-              if (xx == x1) {
-                mma_commit_warp(empty(gk % ST));
-                if (s->tail) mma_commit_warp(q_empty(s->n & 1));
-              }
-              return true;
-            };
-            if (s_first && !do_s(0)) return false;
-            bool v_done = false;
 #pragma unroll 1
-            for (int xx = x0; xx <= x1; ++xx) {
-              if (pv) {
-                if (!v_done && !v_here(gv, *pv)) return false;
-                v_done = true;
-                // (one stream: the buffer that the newest S does not hold)
-                const int buf = NX == 1 ? (scnt + (s_first ? 0 : 1)) & 1 : xx;
-                if (!issue_pv(xx, buf, gv, *pv)) return false;
-                if (xx == x1) mma_commit_warp(empty(gv % ST));
-                if (pv->last) mma_commit_warp(o_ready(xx));
-              }
-              if (s && !s_first && !do_s(xx)) return false;
+        for (int i = 0; i < (tiles ? 2 * tiles + 2 : 0); ++i) {
+          // two streams: P V(k - 1), S(k); one: S(k), P V(k - 1)
+          const int k = i >> 1;
+          const bool is_s = ((i & 1) == 0) == (NX == 1);
+          if (is_s) {
+            if (k == tiles) continue;
+            const int j = j0 + k * step;
+            const int pos = at + place_k(j, pair);
+            const int st = pos % ST;
+            if (k == 0 && !wait(q_full(n & 1), n >> 1)) {
+              ok = false;
+              break;
             }
-            return true;
-          },
-          [&](int x, int n) -> bool {
-            // (no phase of o_free or o_ready is left out)
-            if (n > 0 && !wait(o_free(x), n - 1)) return false;
-            mma_commit_warp(o_ready(x));
-            return true;
-          });
+            if (!loaded(st, set)) {
+              ok = false;
+              break;
+            }
+            const int buf = NX == 1 ? s_cnt & 1 : x;
+            const uint64_t kd = sdesc(sR + st * C::STAGE, 16, gs);
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c)
+              mma_f16_warp(tmem + buf * C::S_STEP,
+                           qd + (((c >> 2) * (BM * 128) + (c & 3) * 32) >> 4),
+                           kd + (((c >> 2) * cbs + (c & 3) * 32) >> 4), ID_S,
+                           c > 0 ? 1 : 0);
+            mma_commit_warp(s_full(buf));
+            mma_commit_warp(empty(st));
+            if (alt) mma_commit_warp(empty(st));   // (for the other stream)
+            ++s_cnt;
+            if (k == tiles - 1) mma_commit_warp(q_empty(n & 1));
+          } else {
+            if (k == 0) continue;
+            const int j = j0 + (k - 1) * step;
+            const int pos = at + place_v(j, pc.nt, pair);
+            const int st = pos % ST;
+            if (!loaded(st, set)) {
+              ok = false;
+              break;
+            }
+            // rows of V that no row of the block sees become zero (they may
+            // hold another request's NaN)
+            const int kt = pc.kt0 + j * BN;
+            if (kt < pc.klo || kt + BN > pc.khi) {
+              const int lo = min(max(pc.klo - kt, 0), BN);
+              const int hi = max(min(pc.khi - kt, BN), lo);
+              const uint32_t v0 = sR + st * C::STAGE;
+              for (int e = lane; e < (lo + BN - hi) * 8; e += 32) {
+                int r = e >> 3;
+                if (r >= lo) r += hi - lo;
+                const uint32_t to =
+                    v0 + (r >> 3) * gs + (r & 7) * 128 + ((e & 7) << 4);
+#pragma unroll
+                for (int cb = 0; cb < C::NCB; ++cb)
+                  asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::
+                                   "r"(to + cb * cbs),
+                               "r"(0)
+                               : "memory");
+              }
+              fence_proxy_async();
+              __syncwarp();
+            }
+            // the epilogue of the piece before has read the accumulator
+            if (k == 1 && n > 0 && !wait(o_free(x), n - 1)) {
+              ok = false;
+              break;
+            }
+            const int buf = NX == 1 ? pv_cnt & 1 : x;
+            if (!wait(p_full(buf), NX == 1 ? pv_cnt >> 1 : pv_cnt)) {
+              ok = false;
+              break;
+            }
+            const uint64_t vd = sdesc(sR + st * C::STAGE, cbs, gs);
+            const uint32_t keep = k > 1 ? 1u : 0u;
+#pragma unroll
+            for (int c = 0; c < BN / 16; ++c)
+              mma_f16_tmem_a_warp(acc, tmem + buf * C::S_STEP + 8 * c,
+                                  vd + ((c * 2 * gs) >> 4), ID_PV,
+                                  c > 0 ? 1u : keep);
+            if constexpr (NX == 1) mma_commit_warp(pv_done);
+            mma_commit_warp(empty(st));
+            if (alt) mma_commit_warp(empty(st));
+            ++pv_cnt;
+          }
+        }
+        if (!ok) break;
+        mma_commit_warp(o_ready(x));
+        at += 2 * pc.nt;
+      }
       // every MMA of this CTA is complete before TMEM is freed
       mma_commit_warp(drain_bar);
       mbar_drain(drain_bar, 0);
@@ -704,7 +639,7 @@ tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
       int64_t off = off_first, rem = end - beg;
       int wb = -1;                     // request of lane 0 below
       Req mine{};                      // request wb + lane
-      int xs = 0, prev_pair = 1;
+      int prev_pair = 1;
       bool marked = false;
       int q_issued = 0;                // query loads as TMA boxes
       for (int n = 0;; ++n) {
@@ -755,8 +690,6 @@ tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
           pc.klo = get(mine.klo);
           pc.khi = get(mine.khi);
           pc.pair = NX == 2 && pc.rows > BM;
-          pc.xs = prev_pair ? 0 : xs;
-          xs = (pc.xs + nt) & 1;
           pc.whole = t == 0 && nt == tiles;
           pc.slot = 2 * blockIdx.x + (t == 0 ? 1 : 0);
           if (!pc.whole && t == 0) {
@@ -913,7 +846,7 @@ tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
           p.wl >= 0 ? max(pc.ctx + pc.n - 1 - p.wl, 0) : 0;
       const int full_hi = min(pc.ctx, pc.khi);
       float m_ref = -INFINITY, l = 0.f;
-      const int j0 = alt ? (pc.xs ^ x) : 0, jd = alt ? 2 : 1;
+      const int j0 = alt ? x : 0, jd = alt ? 2 : 1;
       for (int j = j0; ok && j < pc.nt; j += jd, ++cnt) {
         const int buf = NX == 2 ? x : cnt & 1;
         const int turn = NX == 2 ? cnt : cnt >> 1;
@@ -1083,8 +1016,7 @@ tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
       inv *= vscale;
       f0 *= inv;
       f1 *= inv;
-      const bool has0 = !alt || pc.nt > 1 || pc.xs == 0;
-      const bool has1 = alt && (pc.nt > 1 || pc.xs == 1);
+      const bool has1 = alt && pc.nt > 1;
       if (live) {
         T* dst = static_cast<T*>(p.out) + static_cast<int64_t>(tok) * p.o_st +
                  static_cast<int64_t>(h) * p.o_sh;
@@ -1102,7 +1034,7 @@ tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
           tmem_wait_ld();
 #pragma unroll
           for (int e = 0; e < 32; ++e) {
-            float y = has0 ? ov[e] * f0 : 0.f;
+            float y = ov[e] * f0;
             if (NX == 2 && has1) y += o1[e] * f1;
             ov[e] = y;
           }
