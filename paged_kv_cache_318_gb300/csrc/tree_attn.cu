@@ -102,12 +102,6 @@ struct Cfg {
   static constexpr int SMEM = SMEM_USED < 120 * 1024 ? 120 * 1024 : SMEM_USED;
   static_assert(SMEM <= 232448, "shared memory of a CTA");
 };
-// Register split of the two-stream kernels: the launch gives 168 a thread
-// (384 x 168 = 64512); the softmax warps take 200, the others keep 96.
-constexpr int kLaunchRegs = 168, kSoftmaxRegs = 200, kOtherRegs = 96;
-static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= 384 * kLaunchRegs,
-              "register split");
-
 struct Params {
   const void* q;
   int64_t q_st, q_sh;
@@ -123,6 +117,7 @@ struct Params {
   int max_blocks;
   int64_t num_blocks;
   int Hq, Hkv, G, BS, RB;
+  float inv_g;              // 1 / G
   float scale, softcap;
   const float* sinks;
   const float* k_scale;     // caches converted from codes: value = code * scale
@@ -182,6 +177,12 @@ __device__ __forceinline__ Req request(const Params& p, int b, int BN,
   r.tiles = max((r.khi - r.kstart + BN - 1) / BN, 1);
   r.units = (r.n * p.G + ROWS - 1) / ROWS * p.Hkv;
   return r;
+}
+
+// R / G for a packed row (R < 2^20; exact: the product is off by far less than
+// the half).
+__device__ __forceinline__ int row_of(int R, float inv_g) {
+  return static_cast<int>((static_cast<float>(R) + 0.5f) * inv_g);
 }
 
 // Places in the ring of a piece's K and V tiles, counted from its first: the
@@ -299,83 +300,18 @@ tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;"
                  ::: "memory");
   }
-  // everything that this kernel reads or writes comes after the kernel
-  // queued before it (a no-op unless launched as its programmatic dependent)
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-
-  // ---- this CTA's share [beg, end) of the sequence of all units' tiles (of
-  // units, when they are not to be cut): a scan over the requests, in the
-  // shared memory of the query tiles
-  int64_t beg = 0, end = 0, n_all = 0, ctas = 0;
-  int b_first = 0;
-  int64_t off_first = 0;             // tiles of request b_first before beg
-  {
-    int64_t* wsum = reinterpret_cast<int64_t*>(base);
-    int64_t* res = wsum + 16;
-    unsigned flag = 0;
-    auto weight = [&](int b) -> int64_t {
-      const Req r = request(p, b, BN, C::ROWS, &flag);
-      return p.split ? static_cast<int64_t>(r.tiles) * r.units : r.units;
-    };
-    // inclusive prefix of v over the block; *sum: the total
-    auto scan = [&](int64_t v, int64_t* sum) -> int64_t {
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, v, o);
-        if (lane >= o) v += y;
-      }
-      if (lane == 31) wsum[warp] = v;
-      __syncthreads();
-      int64_t pre = 0, all = 0;
-      for (int w = 0; w < C::THREADS / 32; ++w) {
-        const int64_t y = wsum[w];
-        if (w < warp) pre += y;
-        all += y;
-      }
-      *sum = all;
-      __syncthreads();
-      return v + pre;
-    };
-    int64_t w0 = weight(tid), part = 0;
-    int64_t incl = scan(w0, &n_all);
-    for (int c = C::THREADS; c < p.batch; c += C::THREADS) {
-      scan(weight(c + tid), &part);
-      n_all += part;
-    }
-    if (flag && blockIdx.x == 0) atomicOr(p.err, flag);
-    // (as many CTAs as tiles at most: no share between two others is empty)
-    ctas = min(static_cast<int64_t>(gridDim.x), n_all);
-    if (blockIdx.x < ctas) {
-      beg = n_all * blockIdx.x / ctas;
-      end = n_all * (blockIdx.x + 1) / ctas;
-    }
-    int64_t run = 0;
-    if (tid == 0) res[0] = -1;
-    __syncthreads();
-    for (int c = 0; c < p.batch; c += C::THREADS) {
-      if (c > 0) {
-        w0 = weight(c + tid);
-        incl = scan(w0, &part) + run;
-      } else {
-        part = 0;
-      }
-      if (beg < end && beg >= incl - w0 && beg < incl) {
-        res[0] = c + tid;
-        res[1] = beg - (incl - w0);
-      }
-      if (c == 0 && p.batch > C::THREADS) scan(w0, &part);
-      run += part;
-    }
-    __syncthreads();
-    b_first = static_cast<int>(res[0]);
-    off_first = res[1];
-    // (the query tiles are written by TMA)
-    fence_proxy_async();
+  if (tid == 0) {
+    prefetch_map(&tm_k);
+    prefetch_map(&tm_v);
+    if (p.q_tma) prefetch_map(&tm_q);
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  // everything that this kernel reads or writes comes after the kernel
+  // queued before it (a no-op unless launched as its programmatic dependent)
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 
   // The CTA's n-th piece (all lanes of a reader warp call it in order).  The
   // slot is given back by release(n).
@@ -401,13 +337,12 @@ tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
   const uint32_t gs = p.kv_rg ? static_cast<uint32_t>(C::NCB * 1024) : 1024u;
 
   if (warp >= C::SM_WARPS) {
-    if constexpr (NX == 2)
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp == C::LOAD_WARP) {
       // ------------------------------------------------- K / V loader
       // Step i of a piece loads K tile i (lanes 0 .. 15, a page's box each) and
       // V tile i - lag (lanes 16 .. 31), which are next to one another in the
-      // ring.  A lane's page id is fetched a step ahead.
+      // ring.  A lane's page id is fetched a step ahead.  Boxes behind the last
+      // key start outside the tensor: they arrive as zeros.
       const int half = lane >> 4, box = lane & 15;
       const void* tm = half ? static_cast<const void*>(&tm_v)
                             : static_cast<const void*>(&tm_k);
@@ -433,11 +368,9 @@ tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
         for (int i = 0; i < pc.nt + lag; ++i) {
           const int j = half ? i - lag : i;
           const bool mine = j >= 0 && j < pc.nt;
-          const int kt = pc.kt0 + j * BN;
-          const int nbox =
-              mine ? max(min((pc.khi - kt + RB - 1) / RB, boxes), 0) : 0;
           int id = nxt;
           const int row = sub * RB;
+          const bool dead = k0 >= pc.khi;        // (no key in this lane's box)
           if (mine) {
             k0 += BN;
             sub += boxes;
@@ -445,7 +378,7 @@ tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
               sub -= per_page;
               ++col;
             }
-            if (box < boxes && k0 < pc.khi) nxt = __ldg(bt + col);
+            nxt = box < boxes && k0 < pc.khi ? __ldg(bt + col) : 0;
           }
           const int pos = at + (half ? place_v(j, pc.nt, pair)
                                      : place_k(j, pair));
@@ -457,24 +390,27 @@ tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
                                         abort_flag, p.err))
               stop = 1;
             else
-              mbar_expect_tx(full(set, st), nbox * C::NCB * RB * 128);
+              mbar_expect_tx(full(set, st), C::STAGE);
           }
           if (__any_sync(0xffffffffu, stop)) {
             ok = false;
             break;
           }
-          if (box < nbox) {
-            if (id < 0 || id >= p.num_blocks) {
+          if (box < boxes && mine) {
+            if (!dead && (id < 0 || id >= p.num_blocks)) {
               atomicOr(p.err, kErrBadBlock);
               id = 0;
             }
             const uint32_t dst = sR + st * C::STAGE;
             if (p.kv_rg) {
               const uint32_t to = dst + box * (RB / 8) * gs;
-              const int c3 = p.kv_order_hnd
-                                 ? row >> 3
-                                 : id * (p.BS >> 3) + (row >> 3);
-              const int c4 = p.kv_order_hnd ? id * p.Hkv + pc.g : pc.g;
+              // (a box has RB / 8 groups)
+              const int c3 = p.kv_order_hnd ? row >> 3
+                             : dead         ? -(RB >> 3)
+                                    : id * (p.BS >> 3) + (row >> 3);
+              const int c4 = !p.kv_order_hnd ? pc.g
+                             : dead          ? -1
+                                             : id * p.Hkv + pc.g;
               if (p.once)
                 tma_load_5d_hint(to, tm, 0, 0, 0, c3, c4, full(set, st), pol);
               else
@@ -485,7 +421,7 @@ tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
 #pragma unroll 1
               for (int cb = 0; cb < C::NCB; ++cb)
                 tma_load_4d(dst + cb * cbs + box * RB * 128, tm, cb * 64, c1,
-                            c2, id, full(set, st));
+                            c2, dead ? -1 : id, full(set, st));
             }
           }
           // (for the end: which barrier each load went to)
@@ -541,54 +477,55 @@ tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
           mma_commit_warp(q_empty(n & 1));
           if (n > 0 && !wait(o_free(x), n - 1)) break;
         }
-#pragma unroll 1
-        for (int i = 0; i < (tiles ? 2 * tiles + 2 : 0); ++i) {
-          // two streams: P V(k - 1), S(k); one: S(k), P V(k - 1)
-          const int k = i >> 1;
-          const bool is_s = ((i & 1) == 0) == (NX == 1);
-          if (is_s) {
-            if (k == tiles) continue;
-            const int j = j0 + k * step;
-            const int pos = at + place_k(j, pair);
-            const int st = pos % ST;
-            if (k == 0 && !wait(q_full(n & 1), n >> 1)) {
-              ok = false;
-              break;
-            }
-            if (!loaded(st, set)) {
-              ok = false;
-              break;
-            }
-            const int buf = NX == 1 ? s_cnt & 1 : x;
-            const uint64_t kd = sdesc(sR + st * C::STAGE, 16, gs);
+        // Step k: P V of this stream's tile k - 1, S of its tile k (one stream:
+        // the other way round, S has a buffer of its own).  Whatever can be
+        // waited for and worked out before the probabilities come, is.
+        auto score = [&](int st) {
+          const int buf = NX == 1 ? s_cnt & 1 : x;
+          const uint64_t kd = sdesc(sR + st * C::STAGE, 16, gs);
 #pragma unroll
-            for (int c = 0; c < D / 16; ++c)
-              mma_f16_warp(tmem + buf * C::S_STEP,
-                           qd + (((c >> 2) * (BM * 128) + (c & 3) * 32) >> 4),
-                           kd + (((c >> 2) * cbs + (c & 3) * 32) >> 4), ID_S,
-                           c > 0 ? 1 : 0);
-            mma_commit_warp(s_full(buf));
-            mma_commit_warp(empty(st));
-            if (alt) mma_commit_warp(empty(st));   // (for the other stream)
-            ++s_cnt;
-            if (k == tiles - 1) mma_commit_warp(q_empty(n & 1));
-          } else {
-            if (k == 0) continue;
-            const int j = j0 + (k - 1) * step;
-            const int pos = at + place_v(j, pc.nt, pair);
-            const int st = pos % ST;
-            if (!loaded(st, set)) {
+          for (int c = 0; c < D / 16; ++c)
+            mma_f16_warp(tmem + buf * C::S_STEP,
+                         qd + (((c >> 2) * (BM * 128) + (c & 3) * 32) >> 4),
+                         kd + (((c >> 2) * cbs + (c & 3) * 32) >> 4), ID_S,
+                         c > 0 ? 1 : 0);
+          mma_commit_warp(s_full(buf));
+          ++s_cnt;
+        };
+        auto consumed = [&](int st) {
+          mma_commit_warp(empty(st));
+          if (alt) mma_commit_warp(empty(st));       // (for the other stream)
+        };
+        if (tiles > 0 && !wait(q_full(n & 1), n >> 1)) break;
+#pragma unroll 1
+        for (int k = 0; k <= tiles && tiles > 0; ++k) {
+          const int jk = j0 + k * step, jv = jk - step;
+          const int sk = (at + place_k(jk, pair)) % ST;
+          const int sv = (at + place_v(jv, pc.nt, pair)) % ST;
+          if (k < tiles && NX == 1) {
+            if (!loaded(sk, set)) {
+              ok = false;
+              break;
+            }
+            score(sk);
+            consumed(sk);
+          }
+          if (k > 0) {
+            if (!loaded(sv, set)) {
               ok = false;
               break;
             }
             // rows of V that no row of the block sees become zero (they may
-            // hold another request's NaN)
-            const int kt = pc.kt0 + j * BN;
+            // hold another request's NaN): those before the window in the
+            // first box, those behind the last key in the last one
+            const int kt = pc.kt0 + jv * BN;
             if (kt < pc.klo || kt + BN > pc.khi) {
               const int lo = min(max(pc.klo - kt, 0), BN);
               const int hi = max(min(pc.khi - kt, BN), lo);
-              const uint32_t v0 = sR + st * C::STAGE;
-              for (int e = lane; e < (lo + BN - hi) * 8; e += 32) {
+              const int top = min((hi + RB - 1) / RB * RB, BN);
+              const uint32_t v0 = sR + sv * C::STAGE;
+#pragma unroll 1
+              for (int e = lane; e < (lo + top - hi) * 8; e += 32) {
                 int r = e >> 3;
                 if (r >= lo) r += hi - lo;
                 const uint32_t to =
@@ -608,23 +545,36 @@ tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
               ok = false;
               break;
             }
+          }
+          if (k < tiles && NX == 2 && !loaded(sk, set)) {
+            ok = false;
+            break;
+          }
+          if (k > 0) {
             const int buf = NX == 1 ? pv_cnt & 1 : x;
+            const uint64_t vd = sdesc(sR + sv * C::STAGE, cbs, gs);
+            const uint32_t keep = k > 1 ? 1u : 0u;
             if (!wait(p_full(buf), NX == 1 ? pv_cnt >> 1 : pv_cnt)) {
               ok = false;
               break;
             }
-            const uint64_t vd = sdesc(sR + st * C::STAGE, cbs, gs);
-            const uint32_t keep = k > 1 ? 1u : 0u;
 #pragma unroll
             for (int c = 0; c < BN / 16; ++c)
               mma_f16_tmem_a_warp(acc, tmem + buf * C::S_STEP + 8 * c,
                                   vd + ((c * 2 * gs) >> 4), ID_PV,
                                   c > 0 ? 1u : keep);
-            if constexpr (NX == 1) mma_commit_warp(pv_done);
-            mma_commit_warp(empty(st));
-            if (alt) mma_commit_warp(empty(st));
             ++pv_cnt;
+            if constexpr (NX == 1) {
+              mma_commit_warp(pv_done);
+              consumed(sv);
+            }
           }
+          if (NX == 2) {
+            if (k < tiles) score(sk);
+            if (k > 0) consumed(sv);
+            if (k < tiles) consumed(sk);
+          }
+          if (k == tiles - 1) mma_commit_warp(q_empty(n & 1));
         }
         if (!ok) break;
         mma_commit_warp(o_ready(x));
@@ -635,15 +585,73 @@ tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
       mbar_drain(drain_bar, 0);
     } else if (warp == C::DEAL_WARP) {
       // -------------------------- the pieces, their queries and parents
-      int b = b_first;
-      int64_t off = off_first, rem = end - beg;
+      // This CTA's share [beg, end) of the sequence of all units' tiles (of
+      // units, when they are not to be cut).  A lane sums the weights of a run
+      // of requests; one warp does it, as the other warps have nothing to wait
+      // for but the first piece (a scan by the whole block took 2900 clocks).
+      unsigned flag = 0;
+      auto weight = [&](const Req& r) -> unsigned {
+        return static_cast<unsigned>(p.split ? r.tiles * r.units : r.units);
+      };
+      auto scan = [&](unsigned v) -> unsigned {     // inclusive, over the warp
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const unsigned y = __shfl_up_sync(0xffffffffu, v, o);
+          if (lane >= o) v += y;
+        }
+        return v;
+      };
+      const int run = (p.batch + 31) / 32;
+      unsigned sum = 0;
+#pragma unroll 4
+      for (int i = 0; i < run; ++i)
+        sum += weight(request(p, lane * run + i, BN, C::ROWS, &flag));
+      const unsigned incl = scan(sum);
+      const unsigned n_all = __shfl_sync(0xffffffffu, incl, 31);
+      // (as many CTAs as tiles at most: no share between two others is empty)
+      const unsigned ctas = min(gridDim.x, n_all);
+      unsigned beg = 0, end = 0;
+      if (blockIdx.x < ctas) {
+        const unsigned each = n_all / ctas, more = n_all - each * ctas;
+        beg = blockIdx.x * each + blockIdx.x * more / ctas;
+        end = (blockIdx.x + 1) * each + (blockIdx.x + 1) * more / ctas;
+      }
+      int b = 0;
+      unsigned off = 0, rem = end - beg;
       int wb = -1;                     // request of lane 0 below
       Req mine{};                      // request wb + lane
+      if (rem > 0) {
+        const unsigned hit =
+            __ballot_sync(0xffffffffu, beg >= incl - sum && beg < incl);
+        const int src = __ffs(hit) - 1;
+        off = beg - __shfl_sync(0xffffffffu, incl - sum, src);
+        // ... and within the run
+        for (wb = src * run;; wb += 32) {
+          unsigned f = 0;
+          mine = request(p, wb + lane, BN, C::ROWS, &f);
+          const unsigned w = weight(mine), in = scan(w);
+          const unsigned m =
+              __ballot_sync(0xffffffffu, off >= in - w && off < in);
+          if (m) {
+            const int at = __ffs(m) - 1;
+            off -= __shfl_sync(0xffffffffu, in - w, at);
+            b = wb + at;
+            break;
+          }
+          off -= __shfl_sync(0xffffffffu, in, 31);
+          if (wb + 32 >= p.batch) {    // (the lengths changed under the call)
+            rem = 0;
+            break;
+          }
+        }
+      }
+      if (flag && blockIdx.x == 0) atomicOr(p.err, flag);
       int prev_pair = 1;
       bool marked = false;
       int q_issued = 0;                // query loads as TMA boxes
       for (int n = 0;; ++n) {
         Piece pc{};
+        unsigned unit_end = 0;         // of a unit that goes on after the share
         if (rem > 0) {
           // the request that the next tile belongs to
           for (;;) {
@@ -671,12 +679,12 @@ tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
           auto get = [&](int v) { return __shfl_sync(0xffffffffu, v, src); };
           const int tiles = get(mine.tiles), units = get(mine.units);
           const int wt = p.split ? tiles : 1;
-          const int u = static_cast<int>(off / wt);
-          const int t = p.split ? static_cast<int>(off - int64_t{u} * wt) : 0;
+          const int u = static_cast<int>(off / static_cast<unsigned>(wt));
+          const int t = p.split ? static_cast<int>(off) - u * wt : 0;
           const int nblk = units / p.Hkv;
           const int g = u / nblk, rb = u - g * nblk;
-          const int nt = !p.split ? tiles
-                         : rem < tiles - t ? static_cast<int>(rem) : tiles - t;
+          const int nt =
+              p.split ? min(static_cast<int>(rem), tiles - t) : tiles;
           pc.live = 1;
           pc.b = b;
           pc.g = g;
@@ -692,21 +700,10 @@ tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
           pc.pair = NX == 2 && pc.rows > BM;
           pc.whole = t == 0 && nt == tiles;
           pc.slot = 2 * blockIdx.x + (t == 0 ? 1 : 0);
-          if (!pc.whole && t == 0) {
-            // this unit's tiles run on to those of CTA `last`
-            const int64_t e = end - rem + tiles;
-            const int last = static_cast<int>((e * ctas - 1) / n_all);
-            if (lane == 0) {
-              p.marks[2 * blockIdx.x] =
-                  make_int4(last - static_cast<int>(blockIdx.x) + 1, pc.q0,
-                            pc.rows, pc.row0);
-              p.marks[2 * blockIdx.x + 1] = make_int4(g, 0, 0, 0);
-            }
-            marked = true;
-          }
+          unit_end = !pc.whole && t == 0 ? end - rem + tiles : 0;
           off += p.split ? nt : 1;
           rem -= p.split ? nt : 1;
-          if (off == static_cast<int64_t>(units) * wt) {
+          if (off == static_cast<unsigned>(units * wt)) {
             ++b;
             off = 0;
           }
@@ -725,6 +722,18 @@ tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
           mbar_arrive(it_full(s));
         }
         if (!pc.live) break;
+        if (unit_end) {
+          // its tiles run on to those of CTA `last`
+          const int last = static_cast<int>(
+              (static_cast<uint64_t>(unit_end) * ctas - 1) / n_all);
+          if (lane == 0) {
+            p.marks[2 * blockIdx.x] =
+                make_int4(last - static_cast<int>(blockIdx.x) + 1, pc.q0,
+                          pc.rows, pc.row0);
+            p.marks[2 * blockIdx.x + 1] = make_int4(pc.g, 0, 0, 0);
+          }
+          marked = true;
+        }
         // parents: loads first, bytes in shared memory after the queries
         constexpr int PER = PKV_TREE_MAX_ROWS / 32;
         int par[PER];
@@ -803,8 +812,6 @@ tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
     }
   } else {
     // ------------------------------------------------- softmax warps
-    if constexpr (NX == 2)
-      asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     constexpr float THR = Range<T>::THR, OFF = Range<T>::OFF;
     const int x = NX == 2 ? warp >> 2 : 0;
     const int r = tid & 127;                   // row of its tile == TMEM lane
@@ -827,8 +834,9 @@ tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
       const int row = (pc.pair ? x * BM : 0) + r;       // of the block
       const bool valid = row < pc.rows;
       const bool live = (row & ~31) < pc.rows;          // any row of the warp
-      const int node = (pc.row0 + (valid ? row : 0)) / G;
-      const int h = pc.g * G + (pc.row0 + (valid ? row : 0)) % G;
+      const int R = pc.row0 + (valid ? row : 0);
+      const int node = row_of(R, p.inv_g);
+      const int h = pc.g * G + R - node * G;
       const int tok = pc.q0 + node;
       const unsigned char* par =
           base + C::OFF_PAR + (n & 1) * PKV_TREE_MAX_ROWS;
@@ -862,25 +870,10 @@ tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
         const int kt = pc.kt0 + j * BN;
         const bool masked = kt < full_lo || kt + BN > full_hi;
         const uint32_t s_addr = tmem + lane_base + buf * C::S_STEP;
-        float v[BN];
-#pragma unroll
-        for (int c = 0; c < BN / 32; ++c)
-          tmem_ld32(s_addr + c * 32, v + c * 32);
-        tmem_wait_ld();
-        if (!raw) {
-          // logits in log2 units; soft-cap t (1 - 2 / (1 + 2^(u x))), within
-          // about an ulp of the cap (the hardware tanh loses 2^-11 of it)
-#pragma unroll
-          for (int e = 0; e < BN; ++e) {
-            v[e] *= scale_log2;
-            if (capped)
-              v[e] = cap_t - __fdividef(2.f * cap_t, 1.f + ex2(v[e] * cap_u));
-          }
-        }
+        uint32_t w[BN / 32];
         if (masked) {
           // one bit a key: those before the draft in the window, and the
           // chain of rows from this one upwards
-          uint32_t w[BN / 32];
 #pragma unroll
           for (int i = 0; i < BN / 32; ++i)
             w[i] = range_bits(k_first - kt, full_hi - kt, i);
@@ -893,6 +886,7 @@ tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
             }
             const int in_tile = min(BN, pc.khi - kt);
             int a = node;
+#pragma unroll 1
             for (int far = 0;; ++far) {
               if (p.wl >= 0 && far > p.wl) break;
               const int rel = rel0 + a;
@@ -905,17 +899,57 @@ tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
               if (a == kNoParent) break;
             }
           }
-          // (a select: whatever stands in a hidden place is dropped)
-#pragma unroll
-          for (int e = 0; e < BN; ++e)
-            v[e] = (w[e >> 5] >> (e & 31)) & 1u ? v[e] : -INFINITY;
         }
+        if (!raw || masked) {
+          // the final logits, 32 keys at a time, back to where they came from
+          // (a short loop: in line with the code below, for every key of the
+          // tile, it pushed that out of the instruction cache)
+#pragma unroll 1
+          for (int c = 0; c < BN; c += 32) {
+            float v[32];
+            tmem_ld32(s_addr + c, v);
+            tmem_wait_ld();
+            if (!raw) {
+              // log2 units; soft-cap t (1 - 2 / (1 + 2^(u x))), within about
+              // an ulp of the cap (the hardware tanh loses 2^-11 of it)
+#pragma unroll
+              for (int e = 0; e < 32; ++e) {
+                v[e] *= scale_log2;
+                if (capped)
+                  v[e] = cap_t -
+                         __fdividef(2.f * cap_t, 1.f + ex2(v[e] * cap_u));
+              }
+            }
+            if (masked) {
+              // (a select: whatever stands in a hidden place is dropped)
+              uint32_t bits = w[0];
+#pragma unroll
+              for (int i = 1; i < BN / 32; ++i)
+                if (c == 32 * i) bits = w[i];
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                v[e] = (bits >> e) & 1u ? v[e] : -INFINITY;
+            }
+            tmem_st32(s_addr + c, v);
+          }
+          tmem_wait_st();
+        }
+        // The tile 64 keys at a time, read from tensor memory twice (for the
+        // maximum, then for the exponentials): half the registers of a row, and
+        // code that stays in the instruction cache.
         float mx8[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) mx8[e] = -INFINITY;
+#pragma unroll 1
+        for (int c = 0; c < BN; c += 64) {
+          float v[64];
+          tmem_ld32(s_addr + c, v);
+          tmem_ld32(s_addr + c + 32, v + 32);
+          tmem_wait_ld();
 #pragma unroll
-        for (int e = 0; e < BN; e += 2)
-          mx8[(e >> 1) & 7] = max3f(mx8[(e >> 1) & 7], v[e], v[e + 1]);
+          for (int e = 0; e < 64; e += 2)
+            mx8[(e >> 1) & 7] = max3f(mx8[(e >> 1) & 7], v[e], v[e + 1]);
+        }
         float mx =
             max3f(max3f(mx8[0], mx8[1], mx8[2]), max3f(mx8[3], mx8[4], mx8[5]),
                   fmaxf(mx8[6], mx8[7]));
@@ -941,40 +975,38 @@ tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
           const uint32_t o_addr =
               tmem + lane_base + x * C::S_STEP + C::O_COL;
 #pragma unroll 1
-          for (int c = 0; c < D / 32; ++c) {
+          for (int c = 0; c < D; c += 32) {
             float ov[32];
-            tmem_ld32(o_addr + c * 32, ov);
+            tmem_ld32(o_addr + c, ov);
             tmem_wait_ld();
 #pragma unroll
             for (int e = 0; e < 32; ++e) ov[e] *= alpha;
-            tmem_st32(o_addr + c * 32, ov);
+            tmem_st32(o_addr + c, ov);
           }
         }
         float sum8[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) sum8[e] = 0.f;
         const float sc = raw ? scale_log2 : 1.f;
+        // P over the first BN / 2 columns of S (read by then): column c holds
+        // the keys 2c (low half) and 2c + 1 (high half)
+#pragma unroll 1
+        for (int c = 0; c < BN; c += 64) {
+          float v[64];
+          tmem_ld32(s_addr + c, v);
+          tmem_ld32(s_addr + c + 32, v + 32);
+          tmem_wait_ld();
 #pragma unroll
-        for (int e = 0; e < BN; e += 2) {
-          float x0 = v[e], x1 = v[e + 1];
-          fma2(x0, x1, sc, -base_m);
-          x0 = ex2(x0);
-          x1 = ex2(x1);
-          v[e] = x0;
-          v[e + 1] = x1;
-          add2(sum8[2 * ((e >> 1) & 3)], sum8[2 * ((e >> 1) & 3) + 1], x0,
-               x1);
-        }
-        // P over the first BN / 2 columns of S: column c holds the keys 2c
-        // (low half) and 2c + 1 (high half)
-#pragma unroll
-        for (int c = 0; c < BN / 64; ++c) {
-          float pk[32];
-#pragma unroll
-          for (int e = 0; e < 32; ++e)
-            pk[e] = __uint_as_float(
-                pack2<T>(v[c * 64 + 2 * e], v[c * 64 + 2 * e + 1]));
-          tmem_st32(s_addr + c * 32, pk);
+          for (int e = 0; e < 64; e += 2) {
+            float x0 = v[e], x1 = v[e + 1];
+            fma2(x0, x1, sc, -base_m);
+            x0 = ex2(x0);
+            x1 = ex2(x1);
+            add2(sum8[2 * ((e >> 1) & 3)], sum8[2 * ((e >> 1) & 3) + 1], x0,
+                 x1);
+            v[e >> 1] = __uint_as_float(pack2<T>(x0, x1));
+          }
+          tmem_st32(s_addr + (c >> 1), v);
         }
         l += ((sum8[0] + sum8[1]) + (sum8[2] + sum8[3])) +
              ((sum8[4] + sum8[5]) + (sum8[6] + sum8[7]));
@@ -1022,50 +1054,42 @@ tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
                  static_cast<int64_t>(h) * p.o_sh;
         float* part = p.part_o +
                       (static_cast<int64_t>(pc.slot) * p.rows_cap + row) * D;
-        // alternating streams share the columns of a row
-        const int c0 = alt ? x * (D / 64) : 0;
-        const int c1 = alt ? c0 + D / 64 : D / 32;
+        // alternating streams share the columns of a row (16 at a time: a
+        // loop that stays in the instruction cache; unrolled over 32 columns
+        // of both accumulators an epilogue took 4500 clocks)
+        const int c1 = alt ? (x + 1) * (D / 2) : D;
 #pragma unroll 1
-        for (int c = c0; c < c1; ++c) {
-          float ov[32], o1[32];
-          const uint32_t at = tmem + lane_base + C::O_COL + c * 32;
-          tmem_ld32(at + (alt ? 0 : x * C::S_STEP), ov);
-          if (NX == 2 && has1) tmem_ld32(at + C::S_STEP, o1);
+        for (int c = alt ? x * (D / 2) : 0; c < c1; c += 16) {
+          float ov[16], o1[16];
+          const uint32_t at = tmem + lane_base + C::O_COL + c;
+          tmem_ld16(at + (alt ? 0 : x * C::S_STEP), ov);
+          if (NX == 2 && has1) tmem_ld16(at + C::S_STEP, o1);
           tmem_wait_ld();
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            float y = ov[e] * f0;
-            if (NX == 2 && has1) y += o1[e] * f1;
-            ov[e] = y;
+          for (int e = 0; e < 16; ++e) {
+            ov[e] *= f0;
+            if (NX == 2 && has1) ov[e] += o1[e] * f1;
           }
           if (!valid) continue;
+          uint32_t w[8];
           if (!pc.whole) {
 #pragma unroll
-            for (int e = 0; e < 32; e += 8) {
-              uint32_t w[8];
+            for (int k = 0; k < 8; ++k) w[k] = __float_as_uint(ov[k]);
+            st_global_v8(part + c, w);
 #pragma unroll
-              for (int k = 0; k < 8; ++k) w[k] = __float_as_uint(ov[e + k]);
-              st_global_v8(part + c * 32 + e, w);
-            }
-          } else if (p.out_v8) {
+            for (int k = 0; k < 8; ++k) w[k] = __float_as_uint(ov[8 + k]);
+            st_global_v8(part + c + 8, w);
+            continue;
+          }
 #pragma unroll
-            for (int e = 0; e < 32; e += 16) {
-              uint32_t w[8];
-#pragma unroll
-              for (int k = 0; k < 8; ++k)
-                w[k] = pack2<T>(ov[e + 2 * k], ov[e + 2 * k + 1]);
-              st_global_v8(dst + c * 32 + e, w);
-            }
+          for (int k = 0; k < 8; ++k) w[k] = pack2<T>(ov[2 * k], ov[2 * k + 1]);
+          if (p.out_v8) {
+            st_global_v8(dst + c, w);
           } else {
-#pragma unroll
-            for (int e = 0; e < 32; e += 8) {
-              uint4 pk;
-              pk.x = pack2<T>(ov[e], ov[e + 1]);
-              pk.y = pack2<T>(ov[e + 2], ov[e + 3]);
-              pk.z = pack2<T>(ov[e + 4], ov[e + 5]);
-              pk.w = pack2<T>(ov[e + 6], ov[e + 7]);
-              *reinterpret_cast<uint4*>(dst + c * 32 + e) = pk;
-            }
+            *reinterpret_cast<uint4*>(dst + c) =
+                make_uint4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<uint4*>(dst + c + 8) =
+                make_uint4(w[4], w[5], w[6], w[7]);
           }
         }
         if (valid && !(alt && x == 1)) {
@@ -1216,6 +1240,7 @@ cudaError_t launch_tree_attn(const AttnParams& a, const int32_t* parents,
   p.Hq = a.Hq;
   p.Hkv = a.Hkv;
   p.G = a.G;
+  p.inv_g = 1.f / static_cast<float>(a.G);
   p.BS = a.BS;
   p.scale = a.scale;
   p.softcap = a.softcap;
@@ -1282,17 +1307,8 @@ cudaError_t launch_tree_attn(const AttnParams& a, const int32_t* parents,
     cfg.numAttrs = pdl ? 1 : 0;
     return cfg;
   };
-  auto go = [&](auto kern, auto fold, int threads, int smem,
-                bool regs) -> cudaError_t {
-    cudaError_t e;
-    if (regs) {
-      // the register split inside the kernel adds up to the launch's
-      cudaFuncAttributes fa;
-      e = cudaFuncGetAttributes(&fa, kern);
-      if (e != cudaSuccess) return e;
-      if (fa.numRegs != kLaunchRegs) return cudaErrorInvalidConfiguration;
-    }
-    e = smem_opt_in(reinterpret_cast<const void*>(kern), smem);
+  auto go = [&](auto kern, auto fold, int threads, int smem) -> cudaError_t {
+    cudaError_t e = smem_opt_in(reinterpret_cast<const void*>(kern), smem);
     if (e != cudaSuccess) return e;
     note_launch();
     const cudaLaunchConfig_t c1 = config(dim3(grid), threads, smem);
@@ -1305,7 +1321,7 @@ cudaError_t launch_tree_attn(const AttnParams& a, const int32_t* parents,
   };
 #define PKV_TREE_GO(T, DD)                                                 \
   go(tree_attn_kernel<T, DD>, fold_kernel<T, DD>, Cfg<DD>::THREADS,        \
-     Cfg<DD>::SMEM, Cfg<DD>::NX == 2)
+     Cfg<DD>::SMEM)
   switch (D) {
     case 64:
       return bf16 ? PKV_TREE_GO(__nv_bfloat16, 64) : PKV_TREE_GO(__half, 64);
