@@ -488,6 +488,79 @@ PKV_API pkv_status pkv_paged_attention_varlen_tree(
     const pkv_attention_options* opts);
 
 /*
+ * pkv_verify_draft_tokens -- which drafted tokens stand, and the token that
+ * follows them.  (No counterpart on the source pages.)
+ *
+ * Rows and parents as in pkv_paged_attention_varlen_tree; row 0 of a request is
+ * its last certain token.  Row i's drafted token is draft_token_ids[i] (row 0's
+ * is not read); target_probs[i] is the target model's distribution of the token
+ * behind row i, and draft_probs[i], where given, the one that row i's children
+ * were drawn from, each by itself.  Per request, with node = 0, R =
+ * target_probs[node], Z = 1, for the rows c = 1, 2, .. whose parent is node:
+ *   x = draft_token_ids[c], Q = draft_probs[node][x] (1 without)
+ *   uniform[c] Q Z < R[x]:  c stands; node = c, R = target_probs[c], Z = 1
+ *   else, with draft_probs: R = max(R - Z draft_probs[node], 0), Z = sum R
+ *   else, without:          Z = Z - R[x], R[x] = 0
+ * and at the end the first token whose running sum of R exceeds uniform[row 0]
+ * sum R.  If nothing is left of R, R = target_probs[node] there; if no running
+ * sum exceeds (a number of 1 or more), the last token with R > 0; if there is
+ * none, -1.  Sums and comparisons are exact to about 1e-13 of the sum (entries
+ * of R after the first subtraction carry float32 roundings); negative
+ * probabilities count as 0.
+ *
+ * target_probs, draft_probs : [total_q, vocab_size], dtype (PKV_F16, PKV_BF16
+ *   or PKV_F32, the same for both), row strides in elements, any alignment.
+ * draft_token_ids : int32 [total_q]; uniform: float [total_q], in [0, 1).
+ * tree_parents : int32 [total_q], or NULL: every row's parent is the one
+ *   before it.
+ * token_ids, rows : int32 [batch, max_seqlen_q]: the tokens that stand, then
+ *   the one that follows; row 0 and the rows that stand; -1 behind them.
+ * counts : int32 [batch]: how many of either (0 for a request without rows).
+ * max_seqlen_q <= PKV_TREE_MAX_ROWS, vocab_size <= PKV_VERIFY_MAX_VOCAB
+ *   (PKV_ERR_UNSUPPORTED above).  Flagged (pkv_check_device_errors): requests
+ *   with more rows than max_seqlen_q (count 0), parents that are no earlier
+ *   row and tokens outside the vocabulary (such rows never stand).
+ */
+#define PKV_VERIFY_MAX_VOCAB (1 << 20)
+
+PKV_API pkv_status pkv_verify_draft_tokens(
+    const void* target_probs, int64_t target_stride, const void* draft_probs,
+    int64_t draft_stride, const int32_t* draft_token_ids,
+    const float* uniform, const int32_t* cu_seqlens_q,
+    const int32_t* tree_parents, int batch, int total_q, int max_seqlen_q,
+    int vocab_size, int32_t* token_ids, int32_t* rows, int32_t* counts,
+    pkv_dtype dtype, pkv_stream_t stream);
+
+/*
+ * pkv_compact_draft_cache -- moves the cache rows of the tokens that stand
+ * together behind the context, in place.  (No counterpart on the source pages.)
+ *
+ * For request b with n rows, ctx = seqused_k[b] - n and i < counts[b]:
+ *   cache[slot(ctx + i)] = cache[slot(ctx + rows[b][i])]
+ * for every cache and head, as bytes; slots by the block table.  ctx +
+ * counts[b] is then the request's length.  Other rows stay as they are.
+ *
+ * caches : host array of num_caches device pointers (any number), views
+ *   [num_blocks, block_size, num_heads, row] that share cache_strides[0..2]
+ *   (BYTES) and rows of row_bytes contiguous bytes; no two may overlap.  Keys
+ *   and values of every layer of a 16-bit or E4M3 cache, or the codes of a
+ *   4-bit cache and, in a second call, its block scales.
+ * rows : int32 [batch, max_rows], row stride rows_stride, as
+ *   pkv_verify_draft_tokens gives them: growing, rows[b][i] >= i.  An entry
+ *   that does not grow or lies outside the request, and one whose block is out
+ *   of range, is left out and flagged (PKV_ERR_BAD_INDEX through
+ *   pkv_check_device_errors).  max_rows <= PKV_TREE_MAX_ROWS.
+ */
+PKV_API pkv_status pkv_compact_draft_cache(
+    void* const* caches, int num_caches, const int64_t cache_strides[3],
+    int num_heads, int row_bytes, int block_size, int64_t num_blocks,
+    const int32_t* block_table, int64_t block_table_stride,
+    int max_blocks_per_seq, const int32_t* cu_seqlens_q,
+    const int32_t* seqused_k, const int32_t* rows, int64_t rows_stride,
+    int max_rows, const int32_t* counts, int batch, int total_q,
+    pkv_stream_t stream);
+
+/*
  * Head norms and rotary positions.  (No counterpart on the source pages,
  * whose backends take q and k after these steps.)
  *

@@ -153,6 +153,14 @@ def load_library():
             vp, i64, i64, vp, vp, vp, vp, vp, i64, i64, vp, vp, vp, i32, i32,
             i32, i32, vp, i64, i32, i32, i32, i32, i32, i64, f32, i32, i32,
             i32, f32, i32, vp, vp, sz, i32, vp, vp]
+        lib.pkv_verify_draft_tokens.restype = i32
+        lib.pkv_verify_draft_tokens.argtypes = [
+            vp, i64, vp, i64, vp, vp, vp, vp, i32, i32, i32, i32, vp, vp, vp,
+            i32, vp]
+        lib.pkv_compact_draft_cache.restype = i32
+        lib.pkv_compact_draft_cache.argtypes = [
+            vp, i32, vp, i32, i32, i32, i64, vp, i64, i32, vp, vp, vp, i64,
+            i32, vp, i32, i32, vp]
         lib.pkv_qk_norm_rope.restype = i32
         lib.pkv_qk_norm_rope.argtypes = [vp, i64, i64] * 4 + [
             i64, i32, i32, i32, vp, i32, vp]
@@ -1021,6 +1029,120 @@ def _attend_tree(lib, q, k, v, max_seqlen_q, cu_seqlens_q, max_seqlen_k,
         softmax_scale, bool(causal), left, right, softcap or 0.0, num_splits,
         _addr(lse), wp, wn, dt), opts)
     return (out, lse) if return_softmax_lse else out
+
+
+# --------------------------------------------------------- drafted tokens
+
+def verify_draft_tokens(target_probs, draft_token_ids, cu_seqlens_q,
+                        max_seqlen_q, uniform, tree_parents=None,
+                        draft_probs=None, out=None):
+    """Which drafted tokens stand, and the token that follows them; returns
+    (token_ids, rows, counts), or writes them to ``out``, such a triple.
+
+    Row 0 of a request is its last certain token, the rows after it drafted
+    ones, with their parents in tree_parents (int32 [T], see
+    ``flash_attn_varlen_func``; None: chains).  target_probs [T, V] is the
+    target model's distribution of the token behind each row, draft_probs, if
+    given, the one that a row's children were drawn from (without it a drafted
+    token stands with its target probability).  draft_token_ids int32 [T];
+    uniform float32 [T], numbers in [0, 1), row 0's for the token that follows.
+    token_ids and rows are int32 [B, max_seqlen_q] (the tokens that stand and
+    the one that follows; row 0 and the rows that stand), -1 behind the first
+    counts[b] entries.
+    """
+    lib = load_library()
+    if target_probs.dim() != 2:
+        raise ValueError("target_probs must be [tokens, vocab]")
+    T, V = target_probs.shape
+    dt = _dtype(target_probs)
+    strides = []
+    for t, what in ((target_probs, "target_probs"),
+                    (draft_probs, "draft_probs")):
+        if t is None:
+            strides.append(0)
+            continue
+        if t.shape != (T, V) or t.dtype is not target_probs.dtype or \
+                (V > 1 and t.stride(1) != 1):
+            raise ValueError("%s must be [tokens, vocab] of one dtype with "
+                             "contiguous rows" % what)
+        strides.append(t.stride(0))
+    if uniform.dtype is not torch.float32 or uniform.dim() != 1 or \
+            uniform.shape[0] < T or (T > 1 and uniform.stride(0) != 1):
+        raise ValueError("uniform must be a contiguous float32 vector of %d" %
+                         T)
+    if cu_seqlens_q.dim() != 1 or cu_seqlens_q.shape[0] < 1:
+        raise ValueError("cu_seqlens_q must be int32 [batch + 1]")
+    batch, n = cu_seqlens_q.shape[0] - 1, int(max_seqlen_q)
+    cu = _vector(cu_seqlens_q, "cu_seqlens_q", batch + 1)
+    ids = _vector(draft_token_ids, "draft_token_ids", T)
+    par = None if tree_parents is None else _vector(tree_parents,
+                                                    "tree_parents", T)
+    if out is None:
+        dev = target_probs.device
+        out = (torch.empty((batch, n), dtype=torch.int32, device=dev),
+               torch.empty((batch, n), dtype=torch.int32, device=dev),
+               torch.empty(batch, dtype=torch.int32, device=dev))
+    else:
+        for t, shape in zip(out, ((batch, n), (batch, n), (batch,))):
+            if t.dtype is not torch.int32 or t.shape != shape or \
+                    not t.is_contiguous():
+                raise ValueError("out must be contiguous int32 [batch, "
+                                 "max_seqlen_q] twice and [batch]")
+    dev = _on_device(target_probs, draft_probs, draft_token_ids, uniform,
+                     cu_seqlens_q, tree_parents, *out)
+    _call(dev, lib.pkv_verify_draft_tokens, (
+        target_probs.data_ptr(), strides[0], _addr(draft_probs), strides[1],
+        ids, uniform.data_ptr(), cu, par, batch, T, n, V, out[0].data_ptr(),
+        out[1].data_ptr(), out[2].data_ptr(), dt))
+    return tuple(out)
+
+
+def compact_draft_cache(caches, block_table, cu_seqlens_q, seqused_k, rows,
+                        counts):
+    """Moves the cache rows of the tokens that stand together behind each
+    request's context, in place, in every cache of the list: row rows[b][i] of
+    the request's draft becomes row i, for i < counts[b].
+
+    caches: views [num_blocks, block_size, heads, X] that share shape, strides
+    and dtype (keys and values of every layer; for a 4-bit cache the codes, and
+    the block scales in a call of their own).  The other arguments are those of
+    the attention call over the draft and the rows and counts that
+    ``verify_draft_tokens`` gave.
+    """
+    lib = load_library()
+    if isinstance(caches, torch.Tensor):
+        caches = [caches]
+    if not caches:
+        return
+    first = caches[0]
+    shape, strides, dtype = first.shape, first.stride(), first.dtype
+    if len(shape) != 4 or strides[3] != 1:
+        raise ValueError("caches must be [num_blocks, block_size, heads, X] "
+                         "views with contiguous rows")
+    for c in caches:
+        if c.shape != shape or c.stride() != strides or c.dtype is not dtype:
+            raise ValueError("caches must share shape, strides and dtype")
+    NB, BS, H, X = shape
+    es = first.element_size()
+    if rows.dtype is not torch.int32 or rows.dim() != 2 or \
+            (rows.shape[1] > 1 and rows.stride(1) != 1):
+        raise ValueError("rows must be int32 [batch, max_rows] with "
+                         "contiguous rows")
+    batch, n = rows.shape
+    if cu_seqlens_q.shape[0] != batch + 1 or seqused_k.shape[0] != batch:
+        raise ValueError("cu_seqlens_q and seqused_k must be of rows' batch")
+    cu = _vector(cu_seqlens_q, "cu_seqlens_q", batch + 1)
+    used = _vector(seqused_k, "seqused_k", batch)
+    cnt = _vector(counts, "counts", batch)
+    bt, bt_stride, max_blocks = _table(block_table, batch)
+    dev = _on_device(*caches, block_table, cu_seqlens_q, seqused_k, rows,
+                     counts)
+    _call(dev, lib.pkv_compact_draft_cache, (
+        struct.pack("@%dP" % len(caches), *(c.data_ptr() for c in caches)),
+        len(caches), struct.pack("@3q", strides[0] * es, strides[1] * es,
+                                 strides[2] * es), H, X * es, BS, NB, bt,
+        bt_stride, max_blocks, cu, used, rows.data_ptr(),
+        rows.stride(0) if batch > 1 else n, n, cnt, batch, 0x7fffffff))
 
 
 def make_local_attention_virtual_batches(attn_chunk_size, query_start_loc,

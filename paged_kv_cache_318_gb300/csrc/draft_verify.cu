@@ -1,0 +1,519 @@
+// Verification of drafted tokens against the target model's probabilities.
+//
+// A request's rows form a tree (see tree_attn.cu): row i holds token x_i,
+// drafted from the distribution q of its parent's row (or, without draft
+// probabilities, proposed outright), and the target's distribution p behind
+// it.  With given numbers u in [0, 1) the walk from row 0 keeps, at each row,
+// what is left of its distribution, R = p, and its mass Z = 1, and tries the
+// row's children c in order:
+//   u_c q(x_c) Z < R(x_c)   c stands: the walk goes on there
+//   else, with draft        R <- max(R - Z q, 0), Z <- sum R
+//   without (q = 1)         Z <- Z - R(x_c), R(x_c) <- 0
+// Where no child stands, the token that follows is the first whose running sum
+// of R exceeds u_0 sum R.  So the tokens said are distributed as if the target
+// had drawn each of them.
+//
+// What has to be read is a few single elements and, per request, the last
+// row's p (and q) once: HBM bounds a batch, the chain of dependent reads a
+// single request.  The elements p(x_i), q(x_i) of all rows are fetched side by
+// side at the start, so the walk itself runs in shared memory.  A cluster of 1
+// to 8 CTAs shares the vocabulary of a request; every CTA walks the same way,
+// and only the sums cross between them.
+//
+// The answers are whole numbers that turn on sums over the vocabulary: with
+// 100000 near-equal probabilities, a sum that is off by 1e-8 of itself moves
+// the sampled token once in a thousand draws.  Sums of 32 values are therefore
+// carried as two floats (a value and its rounding error, about 2^-48), sums
+// across lanes and chunks and all comparisons in float64.
+#include <math.h>
+
+#include <type_traits>
+
+#include "pkv_common.cuh"
+
+namespace pkv {
+namespace verify {
+
+constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kMaxRows = PKV_TREE_MAX_ROWS;
+constexpr int kChunk = 1024;            // vocabulary entries of a partial sum
+constexpr int kMaxChunks = PKV_VERIFY_MAX_VOCAB / kChunk + 1;
+
+struct Params {
+  const void* target;
+  int64_t t_st;
+  const void* draft;
+  int64_t d_st;
+  const int32_t* tokens;
+  const float* uniform;
+  const int32_t* cu_q;
+  const int32_t* parents;               // null: each row's parent is the one before
+  int total_q, max_n, vocab;
+  int32_t* out_tokens;                  // [batch, max_n]
+  int32_t* out_rows;
+  int32_t* out_count;
+  unsigned* err;
+};
+
+struct Shared {
+  int par[kMaxRows], tok[kMaxRows];
+  float u[kMaxRows], pt[kMaxRows], qt[kMaxRows];
+  int said[kMaxRows], rows[kMaxRows];
+  // of the row the walk is at: with draft, the masses that q was taken off
+  // with (as a double and as two floats); without, the tokens taken out
+  double z[kMaxRows];
+  float zh[kMaxRows], zl[kMaxRows];
+  int gone[kMaxRows];
+  float gone_p[kMaxRows];
+  double chunk[kMaxChunks];
+  double total[2];                      // this CTA's sum, of even and odd passes
+  double mass;
+  int node, next, m, count, known, ask; // known: the mass is; ask: a sum is
+                                        // wanted (else: the end)
+};
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile(
+      "barrier.cluster.arrive.release;\n"
+      "barrier.cluster.wait.acquire;" ::: "memory");
+}
+// *p of the CTA with this rank in the cluster.
+__device__ __forceinline__ double remote(const double* p, int rank) {
+  uint32_t a;
+  double v;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;"
+      : "=r"(a)
+      : "r"(smem_u32(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(v) : "r"(a) : "memory");
+  return v;
+}
+
+// A sum and the rounding errors made on the way (Knuth's two-sum).
+struct Sum2 {
+  float hi, lo;
+  __device__ __forceinline__ void add(float x) {
+    const float s = __fadd_rn(hi, x);
+    const float b = __fsub_rn(s, hi);
+    lo = __fadd_rn(lo, __fadd_rn(__fsub_rn(hi, __fsub_rn(s, b)),
+                                 __fsub_rn(x, b)));
+    hi = s;
+  }
+};
+
+// One row of a distribution: entry x lies `pad` entries behind a 16-byte
+// boundary's; places y = x + pad divide into aligned vectors.
+template <typename T>
+struct Row {
+  static constexpr int VEC = 16 / static_cast<int>(sizeof(T));
+  const T* p;
+  int pad;
+  __device__ __forceinline__ void set(const void* base, int64_t at) {
+    p = static_cast<const T*>(base) + at;
+    pad = static_cast<int>((reinterpret_cast<uintptr_t>(p) & 15) / sizeof(T));
+  }
+  // Entries at places y .. y + VEC - 1 of a row shifted by `shift` (this row's
+  // pad or another's).  WHOLE: all are entries of the row, and one vector.
+  template <bool WHOLE>
+  __device__ __forceinline__ void load(int y, int shift, int vocab,
+                                       float* v) const {
+    const int x = y - shift;
+    if constexpr (WHOLE) {
+      const uint4 raw = __ldg(reinterpret_cast<const uint4*>(p + x));
+      if constexpr (std::is_same<T, float>::value) {
+        v[0] = __uint_as_float(raw.x);
+        v[1] = __uint_as_float(raw.y);
+        v[2] = __uint_as_float(raw.z);
+        v[3] = __uint_as_float(raw.w);
+      } else {
+        widen8<T>(raw, v);
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e)
+        v[e] = x + e >= 0 && x + e < vocab ? to_f32(p[x + e]) : 0.f;
+    }
+  }
+};
+
+// What is left of p after q has been taken off m times.
+__device__ __forceinline__ float rest(const Shared& s, float p, float q,
+                                      int m) {
+  float r = fmaxf(p, 0.f);
+  if (m > 0) r = fmaxf(__fsub_rn(r, q), 0.f);       // (the first mass is 1)
+  for (int k = 1; k < m; ++k)
+    r = fmaxf(__fmaf_rn(-s.zl[k], q, __fmaf_rn(-s.zh[k], q, r)), 0.f);
+  return r;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads)
+verify_kernel(const Params p) {
+  __shared__ Shared s;
+  uint32_t rank, ranks;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(ranks));
+  const int b = blockIdx.x / ranks;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int start = p.cu_q[b];
+  int n = min(p.cu_q[b + 1], p.total_q) - start;
+  if (start < 0 || n < 0) n = 0;
+  if (n > p.max_n) {
+    if (tid == 0 && rank == 0) atomicOr(p.err, kErrQueryLen);
+    n = 0;
+  }
+  int32_t* out_t = p.out_tokens + static_cast<int64_t>(b) * p.max_n;
+  int32_t* out_r = p.out_rows + static_cast<int64_t>(b) * p.max_n;
+  if (n == 0) {                          // (the same in the whole cluster)
+    if (rank == 0) {
+      for (int i = tid; i < p.max_n; i += kThreads) out_t[i] = out_r[i] = -1;
+      if (tid == 0) p.out_count[b] = 0;
+    }
+    return;
+  }
+  const bool draft = p.draft != nullptr;
+
+  // ---- every row's numbers, and what its parent's row gives its token
+  for (int i = tid; i < n; i += kThreads) {
+    const int row = start + i;
+    int par = p.parents ? p.parents[row] : i - 1;
+    const int tok = i > 0 ? p.tokens[row] : 0;
+    s.u[i] = p.uniform[row];
+    float pt = 0.f, qt = 0.f;
+    const bool bad = par < -1 || par >= i || tok < 0 || tok >= p.vocab;
+    if (bad) {
+      if (rank == 0) atomicOr(p.err, kErrBadTree);
+      par = -1;                          // (never reached)
+    } else if (i > 0 && par >= 0) {
+      pt = to_f32(static_cast<const T*>(p.target)[(start + par) * p.t_st +
+                                                  tok]);
+      if (draft)
+        qt = to_f32(static_cast<const T*>(p.draft)[(start + par) * p.d_st +
+                                                   tok]);
+    }
+    s.par[i] = i > 0 ? par : -1;
+    s.tok[i] = tok;
+    s.pt[i] = fmaxf(pt, 0.f);
+    s.qt[i] = qt;
+  }
+  if (tid == 0) {
+    s.node = 0;
+    s.next = 1;
+    s.m = 0;
+    s.count = 1;
+    s.rows[0] = 0;
+    s.mass = 1.0;
+    s.known = 1;
+    s.ask = 0;
+  }
+  __syncthreads();
+
+  const int chunks = (p.vocab + 15 + kChunk - 1) / kChunk;
+  const int c_lo = static_cast<int>(int64_t{chunks} * rank / ranks);
+  const int c_hi = static_cast<int>(int64_t{chunks} * (rank + 1) / ranks);
+  using R = Row<T>;
+  constexpr int VEC = R::VEC, PER = kChunk / (32 * VEC);
+  R tr, dr;
+  int pass = 0;
+  // Sum of what is left of the node's row after m times, over the whole
+  // vocabulary; the chunks' sums stay in s.chunk.
+  auto sum = [&](int node, int m) -> double {
+    tr.set(p.target, (start + node) * p.t_st);
+    const bool use_q = draft && m > 0;
+    if (use_q) dr.set(p.draft, (start + node) * p.d_st);
+    for (int c = c_lo + warp; c < c_hi; c += kWarps) {
+      float v[PER][VEC], q[PER][VEC];
+      const int y0 = c * kChunk + lane * VEC;
+      // (all loads of a chunk side by side)
+      auto read = [&](auto whole) {
+        constexpr bool W = decltype(whole)::value;
+#pragma unroll
+        for (int k = 0; k < PER; ++k)
+          tr.template load<W>(y0 + k * 32 * VEC, tr.pad, p.vocab, v[k]);
+        if (use_q) {
+#pragma unroll
+          for (int k = 0; k < PER; ++k)
+            dr.template load<W>(y0 + k * 32 * VEC, tr.pad, p.vocab, q[k]);
+        }
+      };
+      if (c * kChunk >= tr.pad && (c + 1) * kChunk <= p.vocab + tr.pad &&
+          (!use_q || dr.pad == tr.pad))
+        read(std::true_type{});
+      else
+        read(std::false_type{});
+      Sum2 a{0.f, 0.f};
+#pragma unroll
+      for (int k = 0; k < PER; ++k)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+          a.add(use_q ? rest(s, v[k][e], q[k][e], m) : fmaxf(v[k][e], 0.f));
+#pragma unroll
+      for (int o = 16; o; o >>= 1) {
+        const float h = __shfl_xor_sync(0xffffffffu, a.hi, o);
+        const float l = __shfl_xor_sync(0xffffffffu, a.lo, o);
+        a.add(h);
+        a.lo = __fadd_rn(a.lo, l);
+      }
+      if (lane == 0)
+        s.chunk[c - c_lo] = static_cast<double>(a.hi) + a.lo;
+    }
+    __syncthreads();
+    if (warp == 0) {
+      // tokens that were tried in vain are out of it
+      if (!draft && m > 0) {
+        if (lane == 0)
+          for (int k = 0; k < m; ++k) {
+            const int c = (s.gone[k] + tr.pad) / kChunk - c_lo;
+            if (c >= 0 && c < c_hi - c_lo)
+              s.chunk[c] = fmax(s.chunk[c] - s.gone_p[k], 0.0);
+          }
+        __syncwarp();
+      }
+      double t = 0.0;
+      for (int c = lane; c < c_hi - c_lo; c += 32) t += s.chunk[c];
+#pragma unroll
+      for (int o = 16; o; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+      if (lane == 0) s.total[pass & 1] = t;
+    }
+    cluster_sync();
+    double all = 0.0;
+    for (uint32_t r = 0; r < ranks; ++r) all += remote(&s.total[pass & 1], r);
+    ++pass;
+    return all;
+  };
+
+  // ---- the walk: warp 0 goes on until it needs a sum, or to the end
+  for (;;) {
+    if (warp == 0) {
+      int node = s.node, i = s.next, m = s.m, count = s.count, ask = 0;
+      // (after a rejection with draft probabilities the mass is not known yet)
+      double mass = s.mass;
+      bool known = s.known;
+      while (i < n) {
+        const int r = i + lane;
+        const unsigned kids =
+            __ballot_sync(0xffffffffu, r < n && s.par[r] == node);
+        if (!kids) {
+          i += 32;
+          continue;
+        }
+        i += __ffs(kids) - 1;
+        if (!known) {
+          ask = 1;
+          break;
+        }
+        const int x = s.tok[i];
+        double have = s.pt[i];
+        double likely = 1.0;
+        if (draft) {
+          likely = s.qt[i];
+          for (int k = 0; k < m; ++k) have = fmax(have - s.z[k] * likely, 0.0);
+        } else {
+          for (int k = lane; k - lane < m; k += 32)
+            if (__any_sync(0xffffffffu, k < m && s.gone[k] == x)) have = 0.0;
+        }
+        if (static_cast<double>(s.u[i]) * likely * mass < have) {
+          if (lane == 0) {
+            s.said[count - 1] = x;
+            s.rows[count] = i;
+          }
+          ++count;
+          node = i;
+          m = 0;
+          mass = 1.0;
+        } else if (draft) {
+          if (lane == 0) {
+            s.z[m] = mass;
+            s.zh[m] = static_cast<float>(mass);
+            s.zl[m] = static_cast<float>(mass - static_cast<float>(mass));
+          }
+          ++m;
+          known = false;
+        } else if (have > 0.0) {
+          if (lane == 0) {
+            s.gone[m] = x;
+            s.gone_p[m] = s.pt[i];
+          }
+          ++m;
+          mass -= have;
+        }
+        __syncwarp();
+        ++i;
+      }
+      if (lane == 0) {
+        s.node = node;
+        s.next = i;
+        s.m = m;
+        s.count = count;
+        s.mass = mass;
+        s.known = known;
+        s.ask = ask;
+      }
+    }
+    __syncthreads();
+    if (!s.ask) break;
+    const double z = sum(s.node, s.m);
+    if (tid == 0) {
+      s.mass = z;
+      s.known = 1;
+    }
+    __syncthreads();
+  }
+
+  // ---- the token that follows
+  const int node = s.node, count = s.count;
+  int m = s.m;
+  double all = sum(node, m);
+  if (!(all > 0.0) && m > 0) {           // nothing is left: the row as it is
+    m = 0;
+    all = sum(node, 0);
+  }
+  if (rank == 0) {
+    for (int i = tid; i < p.max_n; i += kThreads) {
+      if (i != count - 1) out_t[i] = i < count - 1 ? s.said[i] : -1;
+      out_r[i] = i < count ? s.rows[i] : -1;
+    }
+    if (tid == 0) {
+      p.out_count[b] = count;
+      if (!(all > 0.0)) out_t[count - 1] = -1;
+    }
+  }
+  if (warp == 0 && all > 0.0) {
+    const double want = static_cast<double>(s.u[0]) * all;
+    // the first CTA whose running sum exceeds it; none (u_0 >= 1): the last
+    // with any mass
+    double before = 0.0, run = 0.0, mine_before = 0.0;
+    int owner = -1, last = -1;
+    const int par = (pass - 1) & 1;
+    for (uint32_t r = 0; r < ranks; ++r) {
+      const double t = remote(&s.total[par], r);
+      if (r == rank) mine_before = run;
+      if (t > 0.0) last = r;
+      run += t;
+      if (owner < 0 && run > want) owner = r;
+    }
+    const bool past = owner < 0;
+    if (past) owner = last;
+    before = mine_before;
+    if (owner == static_cast<int>(rank)) {
+      // ... then its chunk (32 at a time) ...
+      int found = -1, some = -1;
+      double at = before;
+      for (int c0 = 0; c0 < c_hi - c_lo && found < 0; c0 += 32) {
+        const double own = c0 + lane < c_hi - c_lo ? s.chunk[c0 + lane] : 0.0;
+        double in = own;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const double y = __shfl_up_sync(0xffffffffu, in, o);
+          if (lane >= o) in += y;
+        }
+        const unsigned hit =
+            __ballot_sync(0xffffffffu, !past && at + in > want);
+        const unsigned any = __ballot_sync(0xffffffffu, own > 0.0);
+        if (any) some = c0 + 31 - __clz(any);
+        if (hit) {
+          const int src = __ffs(hit) - 1;
+          found = c0 + src;
+          at += __shfl_sync(0xffffffffu, in - own, src);
+        } else {
+          at += __shfl_sync(0xffffffffu, in, 31);
+        }
+      }
+      // (rounding may leave a sum's last bit short: the last chunk with mass)
+      const bool end = found < 0;
+      if (end) found = some;
+      // ... then the entry
+      const bool use_q = draft && m > 0;
+      const int y0 = (c_lo + found) * kChunk + lane * VEC;
+      int token = -1, top = -1;          // top: last entry with mass so far
+      for (int k = 0; k < PER && token < 0; ++k) {
+        float v[VEC], q[VEC];
+        tr.template load<false>(y0 + k * 32 * VEC, tr.pad, p.vocab, v);
+        if (use_q)
+          dr.template load<false>(y0 + k * 32 * VEC, tr.pad, p.vocab, q);
+        const int x0 = y0 + k * 32 * VEC - tr.pad;
+        double own = 0.0, part[VEC];
+        int mine = -1;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          float r = use_q ? rest(s, v[e], q[e], m) : fmaxf(v[e], 0.f);
+          if (!draft)
+            for (int j = 0; j < m; ++j)
+              if (s.gone[j] == x0 + e) r = 0.f;
+          if (r > 0.f) mine = x0 + e;
+          own += r;
+          part[e] = own;
+        }
+        double in = own;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const double y = __shfl_up_sync(0xffffffffu, in, o);
+          if (lane >= o) in += y;
+        }
+        const unsigned any = __ballot_sync(0xffffffffu, mine >= 0);
+        if (any) top = __shfl_sync(0xffffffffu, mine, 31 - __clz(any));
+        const unsigned hit =
+            __ballot_sync(0xffffffffu, !end && at + in > want);
+        if (hit) {
+          int x = mine;
+#pragma unroll
+          for (int e = VEC - 1; e >= 0; --e)
+            if (at + (in - own) + part[e] > want) x = x0 + e;
+          token = __shfl_sync(0xffffffffu, x, __ffs(hit) - 1);
+        }
+        at += __shfl_sync(0xffffffffu, in, 31);
+      }
+      if (token < 0) token = top;
+      if (lane == 0) out_t[count - 1] = token;
+    }
+  }
+  cluster_sync();                        // (the others read this CTA's sums)
+}
+
+}  // namespace verify
+
+cudaError_t launch_verify(const VerifyLaunch& a, int elem, cudaStream_t stream) {
+  using namespace verify;
+  Params p{};
+  p.target = a.target;
+  p.t_st = a.t_st;
+  p.draft = a.draft;
+  p.d_st = a.d_st;
+  p.tokens = a.tokens;
+  p.uniform = a.uniform;
+  p.cu_q = a.cu_q;
+  p.parents = a.parents;
+  p.total_q = a.total_q;
+  p.max_n = a.max_n;
+  p.vocab = a.vocab;
+  p.out_tokens = a.out_tokens;
+  p.out_rows = a.out_rows;
+  p.out_count = a.out_count;
+  p.err = a.err;
+  // CTAs of a request: as many as one wave holds, with 4 chunks each at least
+  const int sms = current_sm_count();
+  const int chunks = (a.vocab + 15 + kChunk - 1) / kChunk;
+  int c = 1;
+  while (c < 8 && a.batch * c * 2 <= sms && chunks >= c * 8) c *= 2;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = c;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(a.batch) * c);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  note_launch();
+  switch (elem) {
+    case PKV_F32:
+      return cudaLaunchKernelEx(&cfg, verify_kernel<float>, p);
+    case PKV_BF16:
+      return cudaLaunchKernelEx(&cfg, verify_kernel<__nv_bfloat16>, p);
+    default:
+      return cudaLaunchKernelEx(&cfg, verify_kernel<__half>, p);
+  }
+}
+
+}  // namespace pkv

@@ -1819,6 +1819,130 @@ pkv_status pkv_paged_attention_varlen_tree(
       stream, opts, nullptr, scales, tree_parents);
 }
 
+pkv_status pkv_verify_draft_tokens(
+    const void* target_probs, int64_t target_stride, const void* draft_probs,
+    int64_t draft_stride, const int32_t* draft_token_ids,
+    const float* uniform, const int32_t* cu_seqlens_q,
+    const int32_t* tree_parents, int batch, int total_q, int max_seqlen_q,
+    int vocab_size, int32_t* token_ids, int32_t* rows, int32_t* counts,
+    pkv_dtype dtype, pkv_stream_t stream) {
+  if (dtype != PKV_F16 && dtype != PKV_BF16 && dtype != PKV_F32)
+    return fail(PKV_ERR_UNSUPPORTED,
+                "probabilities must be fp16, bf16 or float32");
+  if (batch < 0 || total_q < 0 || max_seqlen_q < 0)
+    return fail(PKV_ERR_INVALID_ARG, "negative size argument");
+  if (vocab_size <= 0)
+    return fail(PKV_ERR_INVALID_ARG, "vocab_size must be > 0");
+  if (vocab_size > PKV_VERIFY_MAX_VOCAB)
+    return fail(PKV_ERR_UNSUPPORTED, "vocab_size is at most %d",
+                PKV_VERIFY_MAX_VOCAB);
+  if (max_seqlen_q > PKV_TREE_MAX_ROWS)
+    return fail(PKV_ERR_UNSUPPORTED,
+                "a draft has at most %d rows (max_seqlen_q %d)",
+                PKV_TREE_MAX_ROWS, max_seqlen_q);
+  if (batch > 65536)
+    return fail(PKV_ERR_UNSUPPORTED, "at most 65536 requests");
+  if (batch == 0) return PKV_OK;
+  if (max_seqlen_q == 0)
+    return fail(PKV_ERR_INVALID_ARG, "max_seqlen_q must be > 0");
+  if (!target_probs || !draft_token_ids || !uniform || !cu_seqlens_q ||
+      !token_ids || !rows || !counts)
+    return fail(PKV_ERR_INVALID_ARG, "NULL tensor pointer");
+  const int es = dtype == PKV_F32 ? 4 : 2;
+  if (reinterpret_cast<uintptr_t>(target_probs) % es ||
+      reinterpret_cast<uintptr_t>(draft_probs) % es)
+    return fail(PKV_ERR_INVALID_ARG, "misaligned probabilities");
+  VerifyLaunch a{};
+  pkv_status st = device_info(&a.err, nullptr);
+  if (st != PKV_OK) return st;
+  a.target = target_probs;
+  a.draft = draft_probs;
+  a.t_st = target_stride;
+  a.d_st = draft_stride;
+  a.tokens = draft_token_ids;
+  a.uniform = uniform;
+  a.cu_q = cu_seqlens_q;
+  a.parents = tree_parents;
+  a.batch = batch;
+  a.total_q = total_q;
+  a.max_n = max_seqlen_q;
+  a.vocab = vocab_size;
+  a.out_tokens = token_ids;
+  a.out_rows = rows;
+  a.out_count = counts;
+  const cudaError_t e =
+      launch_verify(a, dtype, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "verify_draft_tokens launch");
+  return PKV_OK;
+}
+
+pkv_status pkv_compact_draft_cache(
+    void* const* caches, int num_caches, const int64_t cache_strides[3],
+    int num_heads, int row_bytes, int block_size, int64_t num_blocks,
+    const int32_t* block_table, int64_t block_table_stride,
+    int max_blocks_per_seq, const int32_t* cu_seqlens_q,
+    const int32_t* seqused_k, const int32_t* rows, int64_t rows_stride,
+    int max_rows, const int32_t* counts, int batch, int total_q,
+    pkv_stream_t stream) {
+  if (num_caches < 0 || batch < 0 || total_q < 0 || max_rows < 0 ||
+      num_blocks < 0)
+    return fail(PKV_ERR_INVALID_ARG, "negative size argument");
+  if (num_heads <= 0 || row_bytes <= 0)
+    return fail(PKV_ERR_INVALID_ARG, "num_heads / row_bytes must be > 0");
+  if (block_size <= 0 || block_size % 16 != 0)
+    return fail(PKV_ERR_INVALID_ARG, "block_size must be a multiple of 16");
+  if (max_rows > PKV_TREE_MAX_ROWS)
+    return fail(PKV_ERR_UNSUPPORTED, "a draft has at most %d rows (max_rows "
+                "%d)", PKV_TREE_MAX_ROWS, max_rows);
+  if (!cache_strides)
+    return fail(PKV_ERR_INVALID_ARG, "cache_strides is NULL");
+  if (num_caches == 0 || batch == 0 || total_q == 0 || max_rows == 0)
+    return PKV_OK;
+  if (!caches || !block_table || !cu_seqlens_q || !seqused_k || !rows ||
+      !counts)
+    return fail(PKV_ERR_INVALID_ARG, "NULL tensor pointer");
+  if (max_blocks_per_seq <= 0 || block_table_stride < max_blocks_per_seq)
+    return fail(PKV_ERR_INVALID_ARG,
+                "block_table: need max_blocks_per_seq >= 1 and stride >= it");
+  if (rows_stride < max_rows)
+    return fail(PKV_ERR_INVALID_ARG, "rows_stride must be >= max_rows");
+  for (int i = 0; i < num_caches; ++i) {
+    if (!caches[i]) return fail(PKV_ERR_INVALID_ARG, "NULL cache pointer");
+    for (int j = 0; j < i; ++j)
+      if (caches[i] == caches[j])
+        return fail(PKV_ERR_INVALID_ARG, "cache %d is cache %d", i, j);
+  }
+  CompactLaunch a{};
+  pkv_status st = device_info(&a.err, nullptr);
+  if (st != PKV_OK) return st;
+  a.c_sb = cache_strides[0];
+  a.c_sr = cache_strides[1];
+  a.c_sh = cache_strides[2];
+  a.heads = num_heads;
+  a.row_bytes = row_bytes;
+  a.bs = block_size;
+  a.table = block_table;
+  a.bt_stride = block_table_stride;
+  a.max_blocks = max_blocks_per_seq;
+  a.num_blocks = num_blocks;
+  a.cu_q = cu_seqlens_q;
+  a.seqused_k = seqused_k;
+  a.rows = rows;
+  a.rows_st = rows_stride;
+  a.max_rows = max_rows;
+  a.count = counts;
+  a.batch = batch;
+  a.total_q = total_q;
+  for (int i = 0; i < num_caches; i += kCompactCaches) {
+    a.caches.n = std::min(num_caches - i, kCompactCaches);
+    for (int j = 0; j < a.caches.n; ++j) a.caches.ptr[j] = caches[i + j];
+    const cudaError_t e =
+        launch_compact(a, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "compact_draft_cache launch");
+  }
+  return PKV_OK;
+}
+
 pkv_status pkv_qk_norm_rope(
     const void* q, int64_t q_stride_tok, int64_t q_stride_head, const void* k,
     int64_t k_stride_tok, int64_t k_stride_head, void* q_out,

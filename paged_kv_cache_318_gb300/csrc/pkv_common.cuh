@@ -480,6 +480,42 @@ cudaError_t launch_tree_attn(const AttnParams& p, const int32_t* parents,
                              int max_n, int64_t max_k, int D, bool bf16,
                              int sms, void* scratch, bool pdl,
                              cudaStream_t stream);
+// Verification of drafted tokens (draft_verify.cu); elem: pkv_dtype of both
+// distributions.
+struct VerifyLaunch {
+  const void *target, *draft;       // [total_q, vocab]; draft or null
+  int64_t t_st, d_st;
+  const int32_t* tokens;
+  const float* uniform;
+  const int32_t *cu_q, *parents;    // parents or null (chains)
+  int batch, total_q, max_n, vocab;
+  int32_t *out_tokens, *out_rows, *out_count;
+  unsigned* err;
+};
+cudaError_t launch_verify(const VerifyLaunch& a, int elem,
+                          cudaStream_t stream);
+// Compaction of caches that share one layout (draft_compact.cu).
+constexpr int kCompactCaches = 256; // caches of a launch (2 KB of parameters)
+struct CompactCaches {
+  int n;
+  void* ptr[kCompactCaches];
+};
+struct CompactLaunch {
+  CompactCaches caches;
+  int64_t c_sb, c_sr, c_sh;         // bytes
+  int heads, row_bytes, bs;
+  const int32_t* table;
+  int64_t bt_stride;
+  int max_blocks;
+  int64_t num_blocks;
+  const int32_t *cu_q, *seqused_k, *rows;
+  int64_t rows_st;
+  int max_rows;
+  const int32_t* count;
+  int batch, total_q;
+  unsigned* err;
+};
+cudaError_t launch_compact(const CompactLaunch& a, cudaStream_t stream);
 // Fold the prefill kernel's split-KV partials (p.splits of them, every one
 // written for each row) of the requests with rows >= p.min_rows.
 cudaError_t launch_prefill_split_combine(const CombineParams& p,
