@@ -447,8 +447,7 @@ PKV_API pkv_status pkv_paged_attention_varlen_fp4(
  *   request with more rows than it is not computed and flagged.
  * causal       : must be set; window_right hides nothing then.
  * scales       : of a 4-bit cache (cache_strides in bytes), else NULL.  An
- *   E4M3 cache is named in opts.  Both are read through exact 16-bit copies of
- *   the requests' pages in the workspace.
+ *   E4M3 cache is named in opts.
  * num_splits   : 0, or 1: each (request, KV head) is worked through by one
  *   block and its bits do not depend on the rest of the batch.
  * PKV_ERR_UNSUPPORTED: ALiBi, an fp8 query, non-paged keys, a fixed split
@@ -457,17 +456,16 @@ PKV_API pkv_status pkv_paged_attention_varlen_fp4(
  *   that shares a tile of keys with it, also where the tree hides it; key rows
  *   and the rows behind seqused_k do not.
  * workspace    : pkv_paged_attention_workspace_size_tree bytes, 256-byte
- *   aligned: the page copies (needed), then the pieces of units that the
- *   blocks' shares cut (a workspace without this part works as num_splits 1).
- *   Nothing in it has to be set before a call or kept after one.
+ *   aligned, for the pieces of units that the blocks' shares cut (NULL or less
+ *   works as num_splits 1).  Nothing in it has to be set before a call or kept
+ *   after one.
  */
 #define PKV_TREE_MAX_ROWS 256
 
 PKV_API size_t pkv_paged_attention_workspace_size_tree(
     int batch, int total_q, int max_seqlen_q, int max_seqlen_k,
     int num_heads, int num_kv_heads, int head_size, int block_size,
-    int num_splits, int max_blocks_per_seq, int kv_cache_4bit,
-    const pkv_attention_options* opts);
+    int num_splits, const pkv_attention_options* opts);
 
 PKV_API pkv_status pkv_paged_attention_varlen_tree(
     const void* q, int64_t q_stride_tok, int64_t q_stride_head,

@@ -146,8 +146,7 @@ def load_library():
         lib.pkv_paged_attention_varlen_fp4.argtypes = \
             at[:5] + [vp, vp] + at[6:]
         lib.pkv_paged_attention_workspace_size_tree.restype = sz
-        lib.pkv_paged_attention_workspace_size_tree.argtypes = [i32] * 11 + [
-            vp]
+        lib.pkv_paged_attention_workspace_size_tree.argtypes = [i32] * 9 + [vp]
         lib.pkv_paged_attention_varlen_tree.restype = i32
         lib.pkv_paged_attention_varlen_tree.argtypes = [
             vp, i64, i64, vp, vp, vp, vp, vp, i64, i64, vp, vp, vp, i32, i32,
@@ -1012,12 +1011,8 @@ def _attend_tree(lib, q, k, v, max_seqlen_q, cu_seqlens_q, max_seqlen_k,
     left, right = window_size
     if workspace is None:
         n = lib.pkv_paged_attention_workspace_size_tree(
-            batch, T, max_q, max_k, Hq, Hkv, D, BS, num_splits, max_blocks,
-            fp4 is not None, opts)
-        if n == _NO_SIZE:
-            # (the call itself says what is wrong)
-            n = 0
-        if n:
+            batch, T, max_q, max_k, Hq, Hkv, D, BS, num_splits, opts)
+        if n and n != _NO_SIZE:        # (the call itself says what is wrong)
             workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
     wp, wn = 0, 0
     if workspace is not None:

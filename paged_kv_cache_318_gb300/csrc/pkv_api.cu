@@ -865,7 +865,7 @@ pkv_status attention_impl(
                        fixed_split, kv4);
   size_t need = pl.workspace;
   size_t mock_off = 0, q16_off = 0;
-  if ((kv8 || kv4) && (pl.prefill || tree)) {
+  if ((kv8 || kv4) && pl.prefill) {
     mock_off = align256(pl.workspace);
     need = mock_off + fp8_mock_bytes(batch, max_blocks_per_seq, block_size,
                                      num_kv_heads, head_size);
@@ -1024,43 +1024,14 @@ pkv_status attention_impl(
   const bool bf16 = dtype == PKV_BF16;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
 
-  // exact 16-bit copies of the pages that the requests with f.min_rows or
-  // more packed rows read; f then names the copies
-  auto copy_pages = [&](AttnParams& f) -> cudaError_t {
-    const size_t pages = static_cast<size_t>(batch) * max_blocks_per_seq;
-    const size_t page_bytes =
-        static_cast<size_t>(block_size) * num_kv_heads * head_size * 2;
-    char* base_ptr = static_cast<char*>(workspace) + mock_off;
-    void* mk = base_ptr;
-    void* mv = base_ptr + align256(pages * page_bytes);
-    int32_t* mt = reinterpret_cast<int32_t*>(
-        base_ptr + 2 * align256(pages * page_bytes));
-    const cudaError_t e =
-        kv4 ? launch_fp4_dequant_pages(f, head_size, bf16, mk, mv, mt, s)
-            : launch_fp8_dequant_pages(f, head_size, bf16, mk, mv, mt, s);
-    f.kc = mk;
-    f.vc = mv;
-    f.c_sb = static_cast<int64_t>(block_size) * num_kv_heads * head_size;
-    f.c_sr = static_cast<int64_t>(num_kv_heads) * head_size;
-    f.c_sh = head_size;
-    f.block_table = mt;
-    f.bt_stride = max_blocks_per_seq;
-    f.num_blocks = static_cast<int64_t>(pages);
-    f.kv_fp8 = 0;            // 16-bit copies; k_scale / v_scale still apply
-    return e;
-  };
-
   if (tree) {
     const size_t at = align256(need);
     const size_t more = tree_scratch_bytes(head_size, p.G, max_seqlen_q, sms);
     void* scratch = num_splits == 0 && ws_ok && workspace_bytes >= at + more
                         ? static_cast<char*>(workspace) + at
                         : nullptr;
-    p.min_rows = 1;
-    cudaError_t e = cudaSuccess;
-    if (kv8 || kv4) e = copy_pages(p);
-    if (e != cudaSuccess) return cuda_fail(e, "page dequant launch");
-    e = launch_tree_attn(p, tree, max_seqlen_q, max_seqlen_k, head_size, bf16,
+    const cudaError_t e =
+        launch_tree_attn(p, tree, max_seqlen_q, max_seqlen_k, head_size, bf16,
                          sms, scratch, !(opts && opts->no_pdl), s);
     if (e != cudaSuccess) return cuda_fail(e, "tree attention launch");
     return PKV_OK;
@@ -1199,9 +1170,28 @@ pkv_status attention_impl(
     const int64_t prow = static_cast<int64_t>(max_seqlen_q) * p.G;
     cudaError_t e;
     if (kv8 || kv4) {
-      e = copy_pages(f);
+      // 16-bit copies of the pages prefill-class requests read
+      const size_t pages = static_cast<size_t>(batch) * max_blocks_per_seq;
+      const size_t page_bytes =
+          static_cast<size_t>(block_size) * num_kv_heads * head_size * 2;
+      char* base_ptr = static_cast<char*>(workspace) + mock_off;
+      void* mk = base_ptr;
+      void* mv = base_ptr + align256(pages * page_bytes);
+      int32_t* mt = reinterpret_cast<int32_t*>(
+          base_ptr + 2 * align256(pages * page_bytes));
+      e = kv4 ? launch_fp4_dequant_pages(f, head_size, bf16, mk, mv, mt, s)
+              : launch_fp8_dequant_pages(f, head_size, bf16, mk, mv, mt, s);
       if (e != cudaSuccess) return cuda_fail(e, "page dequant launch");
       if (kv4) f.sched_zeroed = 1;     // (by the kernel just launched)
+      f.kc = mk;
+      f.vc = mv;
+      f.c_sb = static_cast<int64_t>(block_size) * num_kv_heads * head_size;
+      f.c_sr = static_cast<int64_t>(num_kv_heads) * head_size;
+      f.c_sh = head_size;
+      f.block_table = mt;
+      f.bt_stride = max_blocks_per_seq;
+      f.num_blocks = static_cast<int64_t>(pages);
+      f.kv_fp8 = 0;          // 16-bit copies; k_scale / v_scale still apply
     }
     int used = 1;
     if (tc_prefill)
@@ -1762,28 +1752,17 @@ pkv_status pkv_paged_attention_varlen_fp4(
 size_t pkv_paged_attention_workspace_size_tree(
     int batch, int total_q, int max_seqlen_q, int max_seqlen_k, int num_heads,
     int num_kv_heads, int head_size, int block_size, int num_splits,
-    int max_blocks_per_seq, int kv_cache_4bit,
     const pkv_attention_options* opts) {
   if (check_attn_shape(batch, total_q, max_seqlen_q, max_seqlen_k, num_heads,
                        num_kv_heads, head_size, block_size,
                        num_splits) != PKV_OK ||
       check_tree(max_seqlen_q, num_splits, opts) != PKV_OK)
     return static_cast<size_t>(-1);
-  size_t need = 0;
-  if (kv_cache_4bit || (opts && opts->kv_cache_fp8)) {
-    if (max_blocks_per_seq <= 0) {
-      fail(PKV_ERR_INVALID_ARG, "max_blocks_per_seq must be >= 1");
-      return static_cast<size_t>(-1);
-    }
-    need = fp8_mock_bytes(batch, max_blocks_per_seq, block_size, num_kv_heads,
-                          head_size);
-  }
-  if (num_splits != 0 || max_seqlen_q == 0) return need;
+  if (num_splits != 0 || max_seqlen_q == 0) return 0;
   int sms = 0;
   if (device_info(nullptr, &sms) != PKV_OK) return static_cast<size_t>(-1);
-  return align256(need) + tree_scratch_bytes(head_size,
-                                             num_heads / num_kv_heads,
-                                             max_seqlen_q, sms);
+  return tree_scratch_bytes(head_size, num_heads / num_kv_heads, max_seqlen_q,
+                            sms);
 }
 
 pkv_status pkv_paged_attention_varlen_tree(

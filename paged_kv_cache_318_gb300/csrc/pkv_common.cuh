@@ -35,6 +35,12 @@ __device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src,
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst),
                "l"(src), "r"(src_bytes));
 }
+// 4-byte global->shared async copy; src_bytes == 0 writes zeros.
+__device__ __forceinline__ void cp_async_4(uint32_t dst, const void* src,
+                                           int src_bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;\n" ::"r"(dst),
+               "l"(src), "r"(src_bytes));
+}
 __device__ __forceinline__ void cp_async_commit() {
   asm volatile("cp.async.commit_group;\n" ::);
 }
@@ -471,7 +477,8 @@ cudaError_t launch_prefill_attn_tc(const AttnParams& p, int D, bool bf16,
                                    int grid_y, bool p_in_tmem,
                                    int* splits_used, cudaStream_t stream,
                                    bool pdl = false);
-// Attention of drafted trees (tree_attn.cu) over 16-bit pages.  parents: int32
+// Attention of drafted trees (tree_attn.cu), 16-bit, E4M3 (p.kv_fp8) and 4-bit
+// (p.k_sf) caches.  parents: int32
 // [total_q]; max_n, max_k: bounds of a request's rows and keys.  scratch (null,
 // or tree_scratch_bytes, 256-byte aligned): lets the shares of the CTAs cut
 // units; without it a unit is worked through by one CTA.
