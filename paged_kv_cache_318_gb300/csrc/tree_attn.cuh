@@ -507,7 +507,17 @@ tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
         constexpr int VALS = KV == kE4m3 ? 16 : 32;      // values of a copy
         constexpr int ROW = D / VALS;                    // copies of a row
         constexpr int PER = BN * ROW / 128;              // ... of a thread
-        const int t = tid - C::CODE_WARP * 32;
+        // Warp w copies rows w RW .. of a tile, RI at a time: copy i of a lane
+        // is part `cp` of row w RW + i RI + ln, so the addresses of its copies
+        // and stores differ by constants.
+        constexpr int RW = BN / 4, RI = 32 / ROW;
+        const int cw = warp - C::CODE_WARP, ln = lane / ROW, cp = lane % ROW;
+        auto row_in_8 = [&](int i) {
+          return RI >= 8 ? ln & 7 : i % (8 / (RI < 8 ? RI : 8)) * RI + ln;
+        };
+        auto eights = [&](int i) {     // eights of rows before its own
+          return RI >= 8 ? i * (RI / 8) + (ln >> 3) : i / (8 / (RI < 8 ? RI : 8));
+        };
         unsigned char* codes = base + C::OFF_CODES;
         const uint32_t codes_u = sR + C::STAGES * C::STAGE;
         // a tile: its first key, the keys that count, V or K, its barrier
@@ -582,24 +592,34 @@ tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
             }
             const uint8_t* from = j.v ? p.vc : p.kc;
             const uint8_t* sfrom = j.v ? p.v_sf : p.k_sf;
-            const uint32_t to = codes_u + slot_in * C::CODE_TILE;
+            const uint32_t to = codes_u + slot_in * C::CODE_TILE +
+                                cw * (RW * ROW * 16) + lane * 16;
+            const uint32_t sto = codes_u + slot_in * C::CODE_TILE +
+                                 C::CODE_BYTES + cw * (RW * D / 16) +
+                                 ln * (D / 16) + cp * 2;
+            const int key0 = j.kt + cw * RW + ln;
+            const bool whole = j.kt >= j.klo && j.kt + BN <= j.khi;
 #pragma unroll
-            for (int i = 0; i < PER; ++i) {
-              const int idx = i * 128 + t;
-              const int r = idx / ROW, c = idx % ROW;
-              const int64_t o = __shfl_sync(0xffffffffu, off, r >> 4);
-              const int key = j.kt + r;
-              const bool in = o >= 0 && key >= j.klo && key < j.khi;
-              cp_async_16(to + idx * 16,
-                          in ? from + o + (r & 15) * p.c_sr + c * 16 : from,
-                          in ? 16 : 0);
-              if (KV == kE2m1) {
+            for (int g = 0; g < RW / 16; ++g) {
+              // (16 rows, one page)
+              const int64_t o =
+                  __shfl_sync(0xffffffffu, off, cw * (RW / 16) + g);
+              int64_t so = 0;
+              if (KV == kE2m1)
+                so = __shfl_sync(0xffffffffu, soff, cw * (RW / 16) + g);
+#pragma unroll
+              for (int i = g * 16 / RI; i < (g + 1) * 16 / RI; ++i) {
+                const int r16 = i * RI - g * 16 + ln;    // row in the page's 16
+                const int key = key0 + i * RI;
+                const bool in =
+                    o >= 0 && (whole || (key >= j.klo && key < j.khi));
+                cp_async_16(to + i * 512,
+                            in ? from + o + r16 * p.c_sr + cp * 16 : from,
+                            in ? 16 : 0);
                 // (four scales, of two copies)
-                const int64_t so = __shfl_sync(0xffffffffu, soff, r >> 4);
-                if ((c & 1) == 0)
-                  cp_async_4(to + C::CODE_BYTES + r * (D / 16) + c * 2,
-                             in ? sfrom + so + (r & 15) * p.f_sr + c * 2
-                                : sfrom,
+                if (KV == kE2m1 && (cp & 1) == 0)
+                  cp_async_4(sto + i * (RI * D / 16),
+                             in ? sfrom + so + r16 * p.f_sr + cp * 2 : sfrom,
                              in ? 4 : 0);
               }
             }
@@ -607,8 +627,10 @@ tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
           }
           cp_async_commit();
         };
-        Job job[AHEAD], nj;            // copies under way, oldest first; the
-        bool live[AHEAD];              // tile whose entries are loading
+        // A tile passes through: its entries load (nj), its copies are under
+        // way (set: its barrier, oldest first; -1 for none), it is widened.
+        Job nj{};
+        int set[AHEAD];
         bool have = false, more = true, ok = true;
         auto fetch = [&](bool block) {
           if (have || !more) return;
@@ -617,59 +639,74 @@ tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
           more = got == 1 || got == 2;
           ok = got >= 0;
         };
-        auto push = [&](int a) {
-          job[a] = nj;
-          live[a] = have;
+        auto advance = [&]() {
+#pragma unroll
+          for (int a = 0; a + 1 < AHEAD; ++a) set[a] = set[a + 1];
+          set[AHEAD - 1] = have ? nj.set : -1;
           copy(nj, have);
           have = false;
-        };
-        fetch(true);
-#pragma unroll
-        for (int a = 0; a < AHEAD; ++a) {
-          push(a);
           fetch(false);
-        }
+        };
+#pragma unroll
+        for (int a = 0; a < AHEAD; ++a) set[a] = -1;
+        fetch(true);
+#pragma unroll 1
+        for (int a = 0; a < AHEAD; ++a) advance();
         int st = 0, slot = 0;
         uint32_t turn = 1;             // parity of the stage's last release
         bool again = false;            // (the first round fills empty stages)
         while (ok) {
           bool any = have;
 #pragma unroll
-          for (int a = 0; a < AHEAD; ++a) any |= live[a];
+          for (int a = 0; a < AHEAD; ++a) any |= set[a] >= 0;
           if (!any) {
             if (!more) break;
             fetch(true);
           }
           cp_async_wait<AHEAD - 1>();
-          if (live[0]) {
+          if (set[0] >= 0) {
             // (scales are copied by the neighbour)
             if (KV == kE2m1) __syncwarp();
             if (again && !mbar_wait(empty(st), turn, abort_flag, p.err)) {
               ok = false;
               break;
             }
-            const uint32_t to = sR + st * C::STAGE;
-            const unsigned char* src = codes + slot * C::CODE_TILE;
+            const uint32_t to =
+                sR + st * C::STAGE + cw * (RW / 8) * gs;
+            const unsigned char* src = codes + slot * C::CODE_TILE +
+                                       cw * (RW * ROW * 16) + lane * 16;
+            const unsigned char* ssrc = codes + slot * C::CODE_TILE +
+                                        C::CODE_BYTES + cw * (RW * D / 16) +
+                                        ln * (D / 16) + cp * 2;
 #pragma unroll
             for (int i = 0; i < PER; ++i) {
-              const int idx = i * 128 + t;
-              const int r = idx / ROW, c = idx % ROW;
-              const uint4 w = *reinterpret_cast<const uint4*>(src + idx * 16);
-              const uint32_t line = to + (r >> 3) * gs + (r & 7) * 128;
+              const uint4 w = *reinterpret_cast<const uint4*>(src + i * 512);
+              const int r8 = row_in_8(i);
+              const uint32_t line = to + eights(i) * gs + r8 * 128;
               if constexpr (KV == kE4m3) {
-                const uint32_t at = line + (c >> 2) * 1024;
+                const uint32_t at = line + (cp >> 2) * 1024;
                 uint32_t h[8];
                 e4m3x4_to_f16(w.x, h[0], h[1]);
                 e4m3x4_to_f16(w.y, h[2], h[3]);
                 e4m3x4_to_f16(w.z, h[4], h[5]);
                 e4m3x4_to_f16(w.w, h[6], h[7]);
-                store_wide<T>(at + ((((c & 3) * 2) ^ (r & 7)) << 4), h);
-                store_wide<T>(at + ((((c & 3) * 2 + 1) ^ (r & 7)) << 4), h + 4);
+                // (the two halves in an order that keeps the lanes of a row
+                // in different banks)
+                const uint32_t c0 = (cp & 3) * 2 + ((cp >> 2) & 1);
+                const bool odd = (cp >> 2) & 1;
+                uint32_t x[4], y[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  x[e] = odd ? h[4 + e] : h[e];
+                  y[e] = odd ? h[e] : h[4 + e];
+                }
+                store_wide<T>(at + ((c0 ^ r8) << 4), x);
+                store_wide<T>(at + ((c0 ^ 1 ^ r8) << 4), y);
               } else {
-                const uint32_t at = line + (c >> 1) * 1024;
+                const uint32_t at = line + (cp >> 1) * 1024;
                 const uint32_t f = e4m3x2_to_f16(
-                    *reinterpret_cast<const uint16_t*>(
-                        src + C::CODE_BYTES + r * (D / 16) + c * 2));
+                    *reinterpret_cast<const uint16_t*>(ssrc +
+                                                       i * (RI * D / 16)));
                 const uint32_t f0 = __byte_perm(f, f, 0x1010),
                                f1 = __byte_perm(f, f, 0x3232);
                 const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
@@ -680,13 +717,13 @@ tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
 #pragma unroll
                   for (int e = 0; e < 4; ++e)
                     h[e] = hmul2_u32(h[e], k < 2 ? f0 : f1);
-                  store_wide<T>(at + ((((c & 1) * 4 + k) ^ (r & 7)) << 4), h);
+                  store_wide<T>(at + ((((cp & 1) * 4 + k) ^ r8) << 4), h);
                 }
               }
             }
             fence_proxy_async();
             __syncwarp();
-            if (lane == 0) mbar_arrive(full(job[0].set, st));
+            if (lane == 0) mbar_arrive(full(set[0], st));
             if (++st == ST) {
               st = 0;
               turn ^= 1;
@@ -694,13 +731,7 @@ tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
             }
             if (++slot == AHEAD) slot = 0;
           }
-#pragma unroll
-          for (int a = 0; a + 1 < AHEAD; ++a) {
-            job[a] = job[a + 1];
-            live[a] = live[a + 1];
-          }
-          push(AHEAD - 1);
-          fetch(false);
+          advance();
         }
         cp_async_wait<0>();
       }
