@@ -518,20 +518,27 @@ tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
         auto eights = [&](int i) {     // eights of rows before its own
           return RI >= 8 ? i * (RI / 8) + (ln >> 3) : i / (8 / (RI < 8 ? RI : 8));
         };
+        // bytes from a 16-row page part to this lane's first copy, and on
+        const int64_t row0 = ln * p.c_sr + cp * 16, step = RI * p.c_sr;
+        const int64_t srow0 = ln * p.f_sr + cp * 2, sstep = RI * p.f_sr;
         unsigned char* codes = base + C::OFF_CODES;
         const uint32_t codes_u = sR + C::STAGES * C::STAGE;
-        // a tile: its first key, the keys that count, V or K, its barrier
+        // a tile: its first key, its barrier, and where its rows lie: K's table
+        // entry is on its way, V takes what K's gave (1: the newest, 2: the one
+        // before)
         struct Job {
-          int kt, klo, khi, set, v;
-          int64_t row;                 // this lane's 16 keys: their page's row
-          int64_t srow;                // ... of block scales
+          int kt, set, v;
         };
         Piece pc{};
         int n = -1, pos = 0;
-        // The next tile of the ring; its page entries start loading.  2: its
-        // piece has not been dealt yet, and without `block` nothing waits for
-        // it (the dealer may be waiting for tiles still to be widened here).
-        int blk = 0;
+        // lane l: keys 16 l .. of the next K tile, their column and page row
+        int col = 0, prow = 0, blk = 0, blk_row = 0;
+        const int32_t* bt = nullptr;
+        int c_klo = 0, c_khi = 0;      // of the piece whose tiles are copied
+        int64_t head = 0, shead = 0;   // ... and its head's rows
+        // The next tile of the ring.  2: its piece has not been dealt yet, and
+        // without `block` nothing waits for it (the dealer may be waiting for
+        // tiles still to be widened here).
         auto next = [&](Job& j, bool block) -> int {
           if (pos == 2 * pc.nt) {
             const int m = n + 1;
@@ -543,84 +550,101 @@ tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
             n = m;
             release(n);
             pos = 0;
+            bt = p.block_table + static_cast<int64_t>(pc.b) * p.bt_stride;
+            const int k0 = pc.kt0 + lane * 16;
+            col = k0 / p.BS;
+            prow = k0 - col * p.BS;
           }
-          int i;
-          if (pc.pair) {
-            j.v = pos & 1;
-            i = pos >> 1;
-          } else if (pos < 2) {
-            j.v = pos == 2 * pc.nt - 1;
-            i = j.v ? 0 : pos;
-          } else if (pos == 2 * pc.nt - 1) {
-            j.v = 1;
-            i = pc.nt - 1;
-          } else {
-            j.v = !(pos & 1);
-            i = j.v ? (pos - 2) >> 1 : (pos + 1) >> 1;
-          }
+          const bool last = pos == 2 * pc.nt - 1;
+          const bool v = pc.pair ? pos & 1 : last || (pos > 1 && !(pos & 1));
+          const int i = pc.pair ? pos >> 1
+                        : last  ? pc.nt - 1
+                        : v     ? (pos - 2) >> 1
+                                : (pos + 1) >> 1;
           ++pos;
           j.kt = pc.kt0 + i * BN;
-          j.klo = pc.klo;
-          j.khi = pc.khi;
           j.set = NX == 1 ? 0 : pc.pair ? 2 : i & 1;
-          // (16 keys on from a multiple of 16 lie in one page)
-          const int k0 = j.kt + lane * 16;
-          j.row = -1;
-          if (lane < BN / 16 && k0 < pc.khi) {
-            const int col = k0 / p.BS;
-            blk = __ldg(p.block_table +
-                        static_cast<int64_t>(pc.b) * p.bt_stride + col);
-            j.row = (k0 - col * p.BS) * p.c_sr + pc.g * p.c_sh;
-            if (KV == kE2m1)
-              j.srow = (k0 - col * p.BS) * p.f_sr + pc.g * p.f_sh;
+          j.v = !v ? 0 : pc.pair || last ? 1 : 2;
+          if (!v) {
+            // (16 keys on from a multiple of 16 lie in one page)
+            blk_row = lane < BN / 16 && j.kt + lane * 16 < pc.khi ? prow : -1;
+            if (blk_row >= 0) blk = __ldg(bt + col);
+            prow += BN;
+            while (prow >= p.BS) {
+              prow -= p.BS;
+              ++col;
+            }
           }
           return 1;
         };
-        // its copies, once the entries are there
+        // its copies
         int slot_in = 0;
+        int64_t off1 = -1, off2 = -1, soff1 = 0, soff2 = 0;
         auto copy = [&](const Job& j, bool any) {
           if (any) {
-            int64_t off = j.row, soff = j.srow;
-            if (off >= 0) {
-              if (blk < 0 || blk >= p.num_blocks) {
+            if (j.v == 0) {
+              off2 = off1;
+              if (blk_row >= 0 && (blk < 0 || blk >= p.num_blocks)) {
                 atomicOr(p.err, kErrBadBlock);
-                off = -1;
-              } else {
-                off += blk * p.c_sb;
-                if (KV == kE2m1) soff += blk * p.f_sb;
+                blk_row = -1;
+              }
+              off1 = blk_row < 0 ? -1 : blk * p.c_sb + blk_row * p.c_sr;
+              if (KV == kE2m1) {
+                soff2 = soff1;
+                soff1 = blk * p.f_sb + blk_row * p.f_sr;
               }
             }
-            const uint8_t* from = j.v ? p.vc : p.kc;
-            const uint8_t* sfrom = j.v ? p.v_sf : p.k_sf;
+            const int64_t off = j.v == 2 ? off2 : off1;
+            const int64_t soff = j.v == 2 ? soff2 : soff1;
+            const uint8_t* from = (j.v ? p.vc : p.kc) + head;
+            const uint8_t* sfrom = (j.v ? p.v_sf : p.k_sf) + shead;
             const uint32_t to = codes_u + slot_in * C::CODE_TILE +
                                 cw * (RW * ROW * 16) + lane * 16;
             const uint32_t sto = codes_u + slot_in * C::CODE_TILE +
                                  C::CODE_BYTES + cw * (RW * D / 16) +
                                  ln * (D / 16) + cp * 2;
             const int key0 = j.kt + cw * RW + ln;
-            const bool whole = j.kt >= j.klo && j.kt + BN <= j.khi;
+            // (all rows: no test of each)
+            const bool whole = j.kt >= c_klo && j.kt + BN <= c_khi &&
+                               __all_sync(0xffffffffu,
+                                          off >= 0 || lane >= BN / 16);
 #pragma unroll
             for (int g = 0; g < RW / 16; ++g) {
               // (16 rows, one page)
               const int64_t o =
                   __shfl_sync(0xffffffffu, off, cw * (RW / 16) + g);
-              int64_t so = 0;
+              const uint8_t* at = from + o + row0;
+              const uint8_t* sat = nullptr;
               if (KV == kE2m1)
-                so = __shfl_sync(0xffffffffu, soff, cw * (RW / 16) + g);
+                sat = sfrom + __shfl_sync(0xffffffffu, soff,
+                                          cw * (RW / 16) + g) + srow0;
+              if (whole) {
 #pragma unroll
-              for (int i = g * 16 / RI; i < (g + 1) * 16 / RI; ++i) {
-                const int r16 = i * RI - g * 16 + ln;    // row in the page's 16
-                const int key = key0 + i * RI;
-                const bool in =
-                    o >= 0 && (whole || (key >= j.klo && key < j.khi));
-                cp_async_16(to + i * 512,
-                            in ? from + o + r16 * p.c_sr + cp * 16 : from,
-                            in ? 16 : 0);
-                // (four scales, of two copies)
-                if (KV == kE2m1 && (cp & 1) == 0)
-                  cp_async_4(sto + i * (RI * D / 16),
-                             in ? sfrom + so + r16 * p.f_sr + cp * 2 : sfrom,
-                             in ? 4 : 0);
+                for (int i = 0; i < 16 / RI; ++i) {
+                  const int e = g * 16 / RI + i;
+                  cp_async_16(to + e * 512, at, 16);
+                  at += step;
+                  if (KV == kE2m1) {
+                    if ((cp & 1) == 0)
+                      cp_async_4(sto + e * (RI * D / 16), sat, 4);
+                    sat += sstep;
+                  }
+                }
+              } else {
+#pragma unroll 1
+                for (int i = 0; i < 16 / RI; ++i) {
+                  const int e = g * 16 / RI + i;
+                  const int key = key0 + e * RI;
+                  const bool in = o >= 0 && key >= c_klo && key < c_khi;
+                  cp_async_16(to + e * 512, in ? at : from, in ? 16 : 0);
+                  at += step;
+                  if (KV == kE2m1) {
+                    if ((cp & 1) == 0)
+                      cp_async_4(sto + e * (RI * D / 16), in ? sat : sfrom,
+                                 in ? 4 : 0);
+                    sat += sstep;
+                  }
+                }
               }
             }
             if (++slot_in == AHEAD) slot_in = 0;
@@ -643,6 +667,13 @@ tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
 #pragma unroll
           for (int a = 0; a + 1 < AHEAD; ++a) set[a] = set[a + 1];
           set[AHEAD - 1] = have ? nj.set : -1;
+          if (have) {
+            // (copies lag `next` by a tile: the piece of the one at hand)
+            c_klo = pc.klo;
+            c_khi = pc.khi;
+            head = pc.g * p.c_sh;
+            if (KV == kE2m1) shead = pc.g * p.f_sh;
+          }
           copy(nj, have);
           have = false;
           fetch(false);
