@@ -95,7 +95,8 @@ struct Cfg {
   static constexpr int DEAL_WARP = SM_WARPS, LOAD_WARP = SM_WARPS + 1,
                        MMA_WARP = SM_WARPS + 2;
   // codes: the warps that copy and widen them, in place of the loader
-  static constexpr int CODE_WARP = SM_WARPS + 4, CODE_WARPS = KV ? 4 : 0;
+  static constexpr int CODE_WARP = SM_WARPS + 4,
+                       CODE_WARPS = KV == 0 ? 0 : NX == 2 ? 8 : 4;
   static constexpr int THREADS = (SM_WARPS + 4 + CODE_WARPS) * 32;
   // warps that take every piece and are done with it at once: the MMA warps,
   // and the loader or the code warps
@@ -119,12 +120,12 @@ struct Cfg {
   // one CTA per SM (it takes all of tensor memory)
   static constexpr int SMEM = SMEM_USED < 120 * 1024 ? 120 * 1024 : SMEM_USED;
   static_assert(SMEM <= 232448, "shared memory of a CTA");
-  // Codes with two streams: 512 threads, launched with 128 registers each; the
-  // softmax warps take 168, the others keep 88.
+  // Codes with two streams: 640 threads, launched with 96 registers each; the
+  // softmax warps take 144, the others keep 64.
   static constexpr bool SPLIT_REGS = KV != 0 && NX == 2;
-  static constexpr int LAUNCH_REGS = 128, SOFTMAX_REGS = 168, OTHER_REGS = 88;
+  static constexpr int LAUNCH_REGS = 96, SOFTMAX_REGS = 144, OTHER_REGS = 64;
   static_assert(!SPLIT_REGS ||
-                    256 * SOFTMAX_REGS + 256 * OTHER_REGS <=
+                    256 * SOFTMAX_REGS + (THREADS - 256) * OTHER_REGS <=
                         THREADS * LAUNCH_REGS,
                 "register split");
 };
@@ -506,11 +507,11 @@ tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
         constexpr int AHEAD = C::AHEAD;
         constexpr int VALS = KV == kE4m3 ? 16 : 32;      // values of a copy
         constexpr int ROW = D / VALS;                    // copies of a row
-        constexpr int PER = BN * ROW / 128;              // ... of a thread
+        constexpr int PER = BN * ROW / (32 * C::CODE_WARPS);  // of a thread
         // Warp w copies rows w RW .. of a tile, RI at a time: copy i of a lane
         // is part `cp` of row w RW + i RI + ln, so the addresses of its copies
         // and stores differ by constants.
-        constexpr int RW = BN / 4, RI = 32 / ROW;
+        constexpr int RW = BN / C::CODE_WARPS, RI = 32 / ROW;
         const int cw = warp - C::CODE_WARP, ln = lane / ROW, cp = lane % ROW;
         auto row_in_8 = [&](int i) {
           return RI >= 8 ? ln & 7 : i % (8 / (RI < 8 ? RI : 8)) * RI + ln;
