@@ -2623,6 +2623,30 @@ bool make_kv_rg_map(CUtensorMap* map, const void* ptr, bool bf16, int D,
   return r == CUDA_SUCCESS;
 }
 
+bool make_code_map(CUtensorMap* map, const void* ptr, int row_bytes, int BS,
+                   int Hkv, int64_t NB, int64_t s_blk, int64_t s_row,
+                   int64_t s_head, int RB, bool hnd) {
+  auto fn = encode_fn();
+  if (!fn || row_bytes % 16 != 0 || row_bytes > 256 || RB > 256) return false;
+  cuuint64_t dims[4], strides[3];
+  cuuint32_t box[4], estr[4] = {1, 1, 1, 1};
+  dims[0] = row_bytes;
+  dims[1] = hnd ? BS : Hkv;
+  dims[2] = hnd ? Hkv : BS;
+  dims[3] = static_cast<cuuint64_t>(NB);
+  strides[0] = static_cast<cuuint64_t>(hnd ? s_row : s_head);
+  strides[1] = static_cast<cuuint64_t>(hnd ? s_head : s_row);
+  strides[2] = static_cast<cuuint64_t>(s_blk);
+  box[0] = row_bytes;
+  box[1] = hnd ? RB : 1;
+  box[2] = hnd ? 1 : RB;
+  box[3] = 1;
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(ptr),
+            dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool make_kv_map(CUtensorMap* map, const void* ptr, bool bf16, int D, int BS,
                  int Hkv, int64_t NB, int64_t s_blk, int64_t s_row,
                  int64_t s_head, int RB, bool hnd) {

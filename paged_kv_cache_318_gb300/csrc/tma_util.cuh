@@ -241,6 +241,11 @@ bool make_kv_map_ex(CUtensorMap* map, const void* ptr, int elem, int D,
                     int BS, int Hkv, int64_t NB, int64_t s_blk, int64_t s_row,
                     int64_t s_head, int RB, bool hnd);
 
+// 4-D map over a cache of codes, [NB, BS, Hkv, row_bytes] (strides in bytes): a box is RB whole rows of
+// row_bytes, one behind the other.
+bool make_code_map(CUtensorMap* map, const void* ptr, int row_bytes, int BS,
+                   int Hkv, int64_t NB, int64_t s_blk, int64_t s_row,
+                   int64_t s_head, int RB, bool hnd);
 // 3-D map over query or output rows [T, Hq, D]: a box is 64 columns of the 128
 // packed rows (token, head of one KV group) of a tile, as the MMAs read them.
 // False when G does not divide 128 or the driver rejects the map.

@@ -169,16 +169,17 @@ cudaError_t launch_tree_attn(const AttnParams& a, const int32_t* parents,
   memset(&mq, 0, sizeof(mq));
   const int kv = a.k_sf ? kE2m1 : a.kv_fp8 ? kE4m3 : kValues;
   if (kv != kValues) {
-    p.kc = static_cast<const uint8_t*>(a.kc);
-    p.vc = static_cast<const uint8_t*>(a.vc);
     p.k_sf = a.k_sf;
     p.v_sf = a.v_sf;
-    p.c_sb = a.c_sb;
-    p.c_sr = a.c_sr;
-    p.c_sh = a.c_sh;
     p.f_sb = a.f_sb;
     p.f_sr = a.f_sr;
     p.f_sh = a.f_sh;
+    const int row = kv == kE4m3 ? D : D / 2;
+    if (!make_code_map(&mk, a.kc, row, a.BS, a.Hkv, a.num_blocks, a.c_sb,
+                       a.c_sr, a.c_sh, RB, p.kv_order_hnd) ||
+        !make_code_map(&mv, a.vc, row, a.BS, a.Hkv, a.num_blocks, a.c_sb,
+                       a.c_sr, a.c_sh, RB, p.kv_order_hnd))
+      return cudaErrorInvalidValue;
   } else {
     // one box per page and matrix where the view allows it
     p.kv_rg = make_kv_rg_map(&mk, a.kc, bf16, D, a.BS, a.Hkv, a.num_blocks,
@@ -199,7 +200,8 @@ cudaError_t launch_tree_attn(const AttnParams& a, const int32_t* parents,
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   const cudaLaunchAttribute* at = pdl ? attr : nullptr;
   cudaError_t e =
-      kv != kValues ? launch_codes(p, D, bf16, kv, mq, grid, at, stream)
+      kv != kValues ? launch_codes(p, D, bf16, kv, mk, mv, mq, grid, at,
+                                   stream)
       : bf16 ? launch_d<__nv_bfloat16, kValues>(p, D, mk, mv, mq, grid, at,
                                                 stream)
              : launch_d<__half, kValues>(p, D, mk, mv, mq, grid, at, stream);

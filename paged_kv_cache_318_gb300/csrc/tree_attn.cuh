@@ -83,7 +83,7 @@ struct Cfg {
   static constexpr int NCB = D / 64;                   // 64-column blocks
   static constexpr int ROWS = NX * BM;                 // rows of a block
   static constexpr int STAGE = BN * D * 2;             // one K or V tile
-  static constexpr int STAGES = KV ? (D == 64 ? 6 : 4) : D == 64 ? 8 : 5;
+  static constexpr int STAGES = KV ? (D == 64 ? 6 : 3) : D == 64 ? 8 : 5;
   static constexpr int Q_TILE = BM * D * 2;
   // tensor memory: (S_x, O_x) per stream, or (S_0, S_1, O)
   static constexpr int S_STEP = NX == 2 ? BN + D : BN;
@@ -98,20 +98,19 @@ struct Cfg {
   static constexpr int CODE_WARP = SM_WARPS + 4,
                        CODE_WARPS = KV == 0 ? 0 : NX == 2 ? 8 : 4;
   static constexpr int THREADS = (SM_WARPS + 4 + CODE_WARPS) * 32;
-  // warps that take every piece and are done with it at once: the MMA warps,
-  // and the loader or the code warps
-  static constexpr int TAKERS = NX + (KV ? CODE_WARPS : 1);
-  // codes on their way, in tiles: the bytes of a tile, its scales behind them
-  static constexpr int CODE_BYTES = KV == kE4m3 ? BN * D : BN * D / 2;
-  static constexpr int CODE_TILE =
-      KV == kE2m1 ? CODE_BYTES + BN * D / 16 : CODE_BYTES;
-  static constexpr int AHEAD = KV == 0 ? 0 : KV == kE2m1 ? 3 : D == 64 ? 4 : 2;
+  // warps that take every piece and are done with it at once
+  static constexpr int TAKERS = 1 + NX + CODE_WARPS;
+  // tiles of codes on their way
+  static constexpr int CODE_ROW = KV == kE4m3 ? D : D / 2;   // bytes
+  static constexpr int CODE_TILE = BN * CODE_ROW;
+  static constexpr int AHEAD = KV == 0 ? 0 : KV == kE2m1 ? 6 : 4;
   static constexpr int SLOTS = 2;                      // pieces in flight
   static constexpr int OFF_Q = 0;
   static constexpr int OFF_RING = OFF_Q + NX * Q_TILE;
   static constexpr int OFF_CODES = OFF_RING + STAGES * STAGE;
   static constexpr int OFF_BAR = OFF_CODES + AHEAD * CODE_TILE;
-  static constexpr int BAR_BYTES = 8 * ((NX == 2 ? 4 : 2) * STAGES + 22);
+  static constexpr int BAR_BYTES =
+      8 * ((NX == 2 ? 4 : 2) * STAGES + 22 + 2 * AHEAD);
   static constexpr int OFF_PIECE = OFF_BAR + BAR_BYTES;
   static constexpr int PIECE_BYTES = 80;
   static constexpr int OFF_PAR = OFF_PIECE + SLOTS * PIECE_BYTES;
@@ -148,10 +147,9 @@ struct Params {
   float inv_g;              // 1 / G
   float scale, softcap;
   const float* sinks;
-  // caches of codes: value = code (* block scale) * scale, rows read by plain
-  // copies (strides in bytes)
-  const uint8_t *kc, *vc, *k_sf, *v_sf;
-  int64_t c_sb, c_sr, c_sh, f_sb, f_sr, f_sh;
+  // caches of codes: value = code (* block scale, strides in bytes) * scale
+  const uint8_t *k_sf, *v_sf;
+  int64_t f_sb, f_sr, f_sh;
   const float* k_scale;
   const float* v_scale;
   int wl;
@@ -314,7 +312,10 @@ tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
   const uint32_t pv_done = bar0 + 8 * (B0 + 17);    // (one stream)
   const uint32_t drain_bar = bar0 + 8 * (B0 + 18);
   auto par_full = [&](int s) { return bar0 + 8 * (B0 + 19 + s); };
-  constexpr int OFF_WORDS = C::OFF_BAR + 8 * (B0 + 21);
+  // codes of a tile have arrived / are widened
+  auto raw_full = [&](int s) { return bar0 + 8 * (B0 + 21 + s); };
+  auto raw_empty = [&](int s) { return bar0 + 8 * (B0 + 21 + C::AHEAD + s); };
+  constexpr int OFF_WORDS = C::OFF_BAR + 8 * (B0 + 21 + 2 * C::AHEAD);
   static_assert(OFF_WORDS + 8 <= C::OFF_PIECE, "barrier area");
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + OFF_WORDS);
   volatile int* abort_flag =
@@ -337,6 +338,10 @@ tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
       mbar_init(it_empty(s), C::SM_WARPS + C::TAKERS);
       mbar_init(par_full(s), 1);
     }
+    for (int s = 0; s < C::AHEAD; ++s) {
+      mbar_init(raw_full(s), 1);
+      mbar_init(raw_empty(s), C::CODE_WARPS);
+    }
     mbar_init(xbar, 256);
     mbar_init(pv_done, 1);
     mbar_init(drain_bar, NX);
@@ -352,10 +357,8 @@ tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
                  ::: "memory");
   }
   if (tid == 0) {
-    if (KV == 0) {
-      prefetch_map(&tm_k);
-      prefetch_map(&tm_v);
-    }
+    prefetch_map(&tm_k);
+    prefetch_map(&tm_v);
     if (p.q_tma) prefetch_map(&tm_q);
   }
   tc_fence_before();
@@ -395,12 +398,14 @@ tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
   if (warp >= C::SM_WARPS) {
     if constexpr (C::SPLIT_REGS)
       asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::OTHER_REGS));
-    if (KV == 0 && warp == C::LOAD_WARP) {
+    if (warp == C::LOAD_WARP) {
       // ------------------------------------------------- K / V loader
       // Step i of a piece loads K tile i (lanes 0 .. 15, a page's box each) and
       // V tile i - lag (lanes 16 .. 31), which are next to one another in the
       // ring.  A lane's page id is fetched a step ahead.  Boxes behind the last
-      // key start outside the tensor: they arrive as zeros.
+      // key, and those of a page outside the cache, start outside the tensor:
+      // they arrive as zeros.  Codes go to the places that the code warps read.
+      constexpr int RING = KV ? C::AHEAD : ST;
       const int half = lane >> 4, box = lane & 15;
       const void* tm = half ? static_cast<const void*>(&tm_v)
                             : static_cast<const void*>(&tm_k);
@@ -428,7 +433,7 @@ tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
           const bool mine = j >= 0 && j < pc.nt;
           int id = nxt;
           const int row = sub * RB;
-          const bool dead = k0 >= pc.khi;        // (no key in this lane's box)
+          bool dead = k0 >= pc.khi;              // (no key in this lane's box)
           if (mine) {
             k0 += BN;
             sub += boxes;
@@ -440,15 +445,17 @@ tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
           }
           const int pos = at + (half ? place_v(j, pc.nt, pair)
                                      : place_k(j, pair));
-          const int st = pos % ST;
-          const int set = NX == 1 ? 0 : pair ? 2 : j & 1;
+          const int st = pos % RING;
+          const int set = NX == 1 || KV ? 0 : pair ? 2 : j & 1;
+          const uint32_t bar = KV ? raw_full(st) : full(set, st);
           int stop = 0;
           if (box == 0 && mine) {
-            if (pos >= ST && !mbar_wait(empty(st), (pos / ST - 1) & 1,
-                                        abort_flag, p.err))
+            if (pos >= RING && !mbar_wait(KV ? raw_empty(st) : empty(st),
+                                          (pos / RING - 1) & 1, abort_flag,
+                                          p.err))
               stop = 1;
             else
-              mbar_expect_tx(full(set, st), C::STAGE);
+              mbar_expect_tx(bar, KV ? C::CODE_TILE : C::STAGE);
           }
           if (__any_sync(0xffffffffu, stop)) {
             ok = false;
@@ -457,11 +464,17 @@ tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
           if (box < boxes && mine) {
             if (!dead && (id < 0 || id >= p.num_blocks)) {
               atomicOr(p.err, kErrBadBlock);
-              id = 0;
+              dead = true;
             }
-            const uint32_t dst = sR + st * C::STAGE;
-            if (p.kv_rg) {
-              const uint32_t to = dst + box * (RB / 8) * gs;
+            if (KV) {
+              const int c1 = p.kv_order_hnd ? row : pc.g;
+              const int c2 = p.kv_order_hnd ? pc.g : row;
+              const uint32_t to = base_u + C::OFF_CODES + st * C::CODE_TILE +
+                                  box * RB * C::CODE_ROW;
+              tma_load_4d_hint(to, tm, 0, c1, c2, dead ? -1 : id, bar, pol);
+            } else if (p.kv_rg) {
+              const uint32_t to =
+                  sR + st * C::STAGE + box * (RB / 8) * gs;
               // (a box has RB / 8 groups)
               const int c3 = p.kv_order_hnd ? row >> 3
                              : dead         ? -(RB >> 3)
@@ -470,20 +483,21 @@ tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
                              : dead          ? -1
                                              : id * p.Hkv + pc.g;
               if (p.once)
-                tma_load_5d_hint(to, tm, 0, 0, 0, c3, c4, full(set, st), pol);
+                tma_load_5d_hint(to, tm, 0, 0, 0, c3, c4, bar, pol);
               else
-                tma_load_5d(to, tm, 0, 0, 0, c3, c4, full(set, st));
+                tma_load_5d(to, tm, 0, 0, 0, c3, c4, bar);
             } else {
+              const uint32_t to = sR + st * C::STAGE + box * RB * 128;
               const int c1 = p.kv_order_hnd ? row : pc.g;
               const int c2 = p.kv_order_hnd ? pc.g : row;
 #pragma unroll 1
               for (int cb = 0; cb < C::NCB; ++cb)
-                tma_load_4d(dst + cb * cbs + box * RB * 128, tm, cb * 64, c1,
-                            c2, dead ? -1 : id, full(set, st));
+                tma_load_4d(to + cb * cbs, tm, cb * 64, c1, c2,
+                            dead ? -1 : id, bar);
             }
           }
           // (for the end: which barrier each load went to)
-          const uint32_t bit = box == 0 && mine ? 1u << (set * ST + st) : 0u;
+          const uint32_t bit = box == 0 && mine ? 1u << (set * RING + st) : 0u;
           const uint32_t bits =
               bit | __shfl_xor_sync(0xffffffffu, bit, 16);
           if (lane == 0) sent ^= bits;
@@ -493,230 +507,117 @@ tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
       }
       // no copy may be in flight when the CTA exits
       if (lane == 0)
-        for (int k = 0; k < SETS * ST; ++k)
-          if (ever >> k & 1) mbar_drain(full(0, k), (sent >> k & 1) ^ 1);
+        for (int k = 0; k < (KV ? RING : SETS * ST); ++k)
+          if (ever >> k & 1)
+            mbar_drain(KV ? raw_full(k) : full(0, k), (sent >> k & 1) ^ 1);
     } else if (KV != 0 && warp >= C::CODE_WARP) {
-      // --------------------------------- codes: copied, widened, handed on
-      // Tile after tile of the ring's order, the 128 threads copy the codes of
-      // the tile AHEAD places on (cp.async, 16 bytes each) and widen those of
-      // this one to the 16-bit layout that the products read: exactly, the
-      // tensor scales joining the logits and the output.  A thread widens what
-      // it copied itself, so the copies need no barrier.  Rows without a key
-      // (and pages outside the cache) arrive as zeros.
+      // ------------------------------------------------- codes widened
+      // Tile after tile of the ring's order, from the loader's rows of codes to
+      // the 16-bit layout that the products read: exactly, the tensor scales
+      // joining the logits and the output.  A warp widens 16 rows (they lie in
+      // one page, so it has one page's block scales to fetch).
       if constexpr (KV != 0) {
-        constexpr int AHEAD = C::AHEAD;
-        constexpr int VALS = KV == kE4m3 ? 16 : 32;      // values of a copy
-        constexpr int ROW = D / VALS;                    // copies of a row
-        constexpr int PER = BN * ROW / (32 * C::CODE_WARPS);  // of a thread
-        // Warp w copies rows w RW .. of a tile, RI at a time: copy i of a lane
-        // is part `cp` of row w RW + i RI + ln, so the addresses of its copies
-        // and stores differ by constants.
-        constexpr int RW = BN / C::CODE_WARPS, RI = 32 / ROW;
+        constexpr int RW = 16;                           // rows of a warp
+        static_assert(BN == RW * C::CODE_WARPS, "all rows of a tile");
+        constexpr int VALS = KV == kE4m3 ? 16 : 32;      // values of 16 bytes
+        constexpr int ROW = D / VALS;                    // 16 bytes of a row
+        constexpr int RI = 32 / ROW;                     // rows at a time
+        constexpr int PER = RW / RI;
         const int cw = warp - C::CODE_WARP, ln = lane / ROW, cp = lane % ROW;
+        // row and eight of step i's row
         auto row_in_8 = [&](int i) {
           return RI >= 8 ? ln & 7 : i % (8 / (RI < 8 ? RI : 8)) * RI + ln;
         };
-        auto eights = [&](int i) {     // eights of rows before its own
+        auto eights = [&](int i) {
           return RI >= 8 ? i * (RI / 8) + (ln >> 3) : i / (8 / (RI < 8 ? RI : 8));
         };
-        // bytes from a 16-row page part to this lane's first copy, and on
-        const int64_t row0 = ln * p.c_sr + cp * 16, step = RI * p.c_sr;
-        const int64_t srow0 = ln * p.f_sr + cp * 2, sstep = RI * p.f_sr;
-        unsigned char* codes = base + C::OFF_CODES;
-        const uint32_t codes_u = sR + C::STAGES * C::STAGE;
-        // a tile: its first key, its barrier, and where its rows lie: K's table
-        // entry is on its way, V takes what K's gave (1: the newest, 2: the one
-        // before)
-        struct Job {
-          int kt, set, v;
-        };
-        Piece pc{};
-        int n = -1, pos = 0;
-        // lane l: keys 16 l .. of the next K tile, their column and page row
-        int col = 0, prow = 0, blk = 0, blk_row = 0;
-        const int32_t* bt = nullptr;
-        int c_klo = 0, c_khi = 0;      // of the piece whose tiles are copied
-        int64_t head = 0, shead = 0;   // ... and its head's rows
-        // The next tile of the ring.  2: its piece has not been dealt yet, and
-        // without `block` nothing waits for it (the dealer may be waiting for
-        // tiles still to be widened here).
-        auto next = [&](Job& j, bool block) -> int {
-          if (pos == 2 * pc.nt) {
-            const int m = n + 1;
-            if (!block && !__any_sync(0xffffffffu, mbar_try(it_full(m & 1),
-                                                            (m >> 1) & 1)))
-              return 2;
-            const int got = take(m, pc);
-            if (got <= 0) return got;
-            n = m;
-            release(n);
-            pos = 0;
-            bt = p.block_table + static_cast<int64_t>(pc.b) * p.bt_stride;
-            const int k0 = pc.kt0 + lane * 16;
-            col = k0 / p.BS;
-            prow = k0 - col * p.BS;
-          }
-          const bool last = pos == 2 * pc.nt - 1;
-          const bool v = pc.pair ? pos & 1 : last || (pos > 1 && !(pos & 1));
-          const int i = pc.pair ? pos >> 1
-                        : last  ? pc.nt - 1
-                        : v     ? (pos - 2) >> 1
-                                : (pos + 1) >> 1;
-          ++pos;
-          j.kt = pc.kt0 + i * BN;
-          j.set = NX == 1 ? 0 : pc.pair ? 2 : i & 1;
-          j.v = !v ? 0 : pc.pair || last ? 1 : 2;
-          if (!v) {
-            // (16 keys on from a multiple of 16 lie in one page)
-            blk_row = lane < BN / 16 && j.kt + lane * 16 < pc.khi ? prow : -1;
-            if (blk_row >= 0) blk = __ldg(bt + col);
-            prow += BN;
-            while (prow >= p.BS) {
-              prow -= p.BS;
-              ++col;
+        int at = 0;                    // tiles of the pieces before
+        bool ok = true;
+        for (int n = 0; ok; ++n) {
+          Piece pc;
+          if (take(n, pc) <= 0) break;
+          release(n);
+          const int total = 2 * pc.nt;
+          // place q of the piece: its tile, and K (0) or V
+          auto tile = [&](int q, int& v) -> int {
+            if (pc.pair) {
+              v = q & 1;
+              return q >> 1;
             }
-          }
-          return 1;
-        };
-        // its copies
-        int slot_in = 0;
-        int64_t off1 = -1, off2 = -1, soff1 = 0, soff2 = 0;
-        auto copy = [&](const Job& j, bool any) {
-          if (any) {
-            if (j.v == 0) {
-              off2 = off1;
-              if (blk_row >= 0 && (blk < 0 || blk >= p.num_blocks)) {
-                atomicOr(p.err, kErrBadBlock);
-                blk_row = -1;
-              }
-              off1 = blk_row < 0 ? -1 : blk * p.c_sb + blk_row * p.c_sr;
-              if (KV == kE2m1) {
-                soff2 = soff1;
-                soff1 = blk * p.f_sb + blk_row * p.f_sr;
-              }
+            v = q == total - 1 || (q > 1 && !(q & 1));
+            return q == total - 1 ? pc.nt - 1 : v ? (q - 2) >> 1 : (q + 1) >> 1;
+          };
+          // block scales: the table's entry two tiles ahead, the scales of
+          // this lane's bytes one ahead
+          const int32_t* bt =
+              p.block_table + static_cast<int64_t>(pc.b) * p.bt_stride;
+          int blk = 0;
+          uint16_t sf[PER] = {}, sf_next[PER] = {};
+          auto entry = [&](int q) {
+            int v;
+            const int key = pc.kt0 + tile(q, v) * BN + cw * RW;
+            if (KV == kE2m1 && q < total && key < pc.khi)
+              blk = __ldg(bt + key / p.BS);
+          };
+          auto scales = [&](int q) {
+            int v;
+            const int key = pc.kt0 + tile(q, v) * BN + cw * RW;
+            if (KV == kE2m1 && q < total && key < pc.khi && blk >= 0 &&
+                blk < p.num_blocks) {
+              const uint8_t* from = (v ? p.v_sf : p.k_sf) + blk * p.f_sb +
+                                    (key % p.BS + ln) * p.f_sr +
+                                    pc.g * p.f_sh + cp * 2;
+#pragma unroll
+              for (int i = 0; i < PER; ++i)
+                sf_next[i] = __ldg(reinterpret_cast<const uint16_t*>(
+                    from + i * RI * p.f_sr));
+            } else {
+#pragma unroll
+              for (int i = 0; i < PER; ++i) sf_next[i] = 0;
             }
-            const int64_t off = j.v == 2 ? off2 : off1;
-            const int64_t soff = j.v == 2 ? soff2 : soff1;
-            const uint8_t* from = (j.v ? p.vc : p.kc) + head;
-            const uint8_t* sfrom = (j.v ? p.v_sf : p.k_sf) + shead;
-            const uint32_t to = codes_u + slot_in * C::CODE_TILE +
-                                cw * (RW * ROW * 16) + lane * 16;
-            const uint32_t sto = codes_u + slot_in * C::CODE_TILE +
-                                 C::CODE_BYTES + cw * (RW * D / 16) +
-                                 ln * (D / 16) + cp * 2;
-            const int key0 = j.kt + cw * RW + ln;
-            // (all rows: no test of each)
-            const bool whole = j.kt >= c_klo && j.kt + BN <= c_khi &&
-                               __all_sync(0xffffffffu,
-                                          off >= 0 || lane >= BN / 16);
-#pragma unroll
-            for (int g = 0; g < RW / 16; ++g) {
-              // (16 rows, one page)
-              const int64_t o =
-                  __shfl_sync(0xffffffffu, off, cw * (RW / 16) + g);
-              const uint8_t* at = from + o + row0;
-              const uint8_t* sat = nullptr;
-              if (KV == kE2m1)
-                sat = sfrom + __shfl_sync(0xffffffffu, soff,
-                                          cw * (RW / 16) + g) + srow0;
-              if (whole) {
-#pragma unroll
-                for (int i = 0; i < 16 / RI; ++i) {
-                  const int e = g * 16 / RI + i;
-                  cp_async_16(to + e * 512, at, 16);
-                  at += step;
-                  if (KV == kE2m1) {
-                    if ((cp & 1) == 0)
-                      cp_async_4(sto + e * (RI * D / 16), sat, 4);
-                    sat += sstep;
-                  }
-                }
-              } else {
+          };
+          entry(0);
+          scales(0);
+          entry(1);
 #pragma unroll 1
-                for (int i = 0; i < 16 / RI; ++i) {
-                  const int e = g * 16 / RI + i;
-                  const int key = key0 + e * RI;
-                  const bool in = o >= 0 && key >= c_klo && key < c_khi;
-                  cp_async_16(to + e * 512, in ? at : from, in ? 16 : 0);
-                  at += step;
-                  if (KV == kE2m1) {
-                    if ((cp & 1) == 0)
-                      cp_async_4(sto + e * (RI * D / 16), in ? sat : sfrom,
-                                 in ? 4 : 0);
-                    sat += sstep;
-                  }
-                }
-              }
+          for (int q = 0; q < total; ++q) {
+            const int pos = at + q, st = pos % ST, slot = pos % C::AHEAD;
+            int v;
+            const int i_tile = tile(q, v);
+            const int set = NX == 1 ? 0 : pc.pair ? 2 : i_tile & 1;
+            if (KV == kE2m1) {
+#pragma unroll
+              for (int i = 0; i < PER; ++i) sf[i] = sf_next[i];
+              scales(q + 1);
+              entry(q + 2);
             }
-            if (++slot_in == AHEAD) slot_in = 0;
-          }
-          cp_async_commit();
-        };
-        // A tile passes through: its entries load (nj), its copies are under
-        // way (set: its barrier, oldest first; -1 for none), it is widened.
-        Job nj{};
-        int set[AHEAD];
-        bool have = false, more = true, ok = true;
-        auto fetch = [&](bool block) {
-          if (have || !more) return;
-          const int got = next(nj, block);
-          have = got == 1;
-          more = got == 1 || got == 2;
-          ok = got >= 0;
-        };
-        auto advance = [&]() {
-#pragma unroll
-          for (int a = 0; a + 1 < AHEAD; ++a) set[a] = set[a + 1];
-          set[AHEAD - 1] = have ? nj.set : -1;
-          if (have) {
-            // (copies lag `next` by a tile: the piece of the one at hand)
-            c_klo = pc.klo;
-            c_khi = pc.khi;
-            head = pc.g * p.c_sh;
-            if (KV == kE2m1) shead = pc.g * p.f_sh;
-          }
-          copy(nj, have);
-          have = false;
-          fetch(false);
-        };
-#pragma unroll
-        for (int a = 0; a < AHEAD; ++a) set[a] = -1;
-        fetch(true);
-#pragma unroll 1
-        for (int a = 0; a < AHEAD; ++a) advance();
-        int st = 0, slot = 0;
-        uint32_t turn = 1;             // parity of the stage's last release
-        bool again = false;            // (the first round fills empty stages)
-        while (ok) {
-          bool any = have;
-#pragma unroll
-          for (int a = 0; a < AHEAD; ++a) any |= set[a] >= 0;
-          if (!any) {
-            if (!more) break;
-            fetch(true);
-          }
-          cp_async_wait<AHEAD - 1>();
-          if (set[0] >= 0) {
-            // (scales are copied by the neighbour)
-            if (KV == kE2m1) __syncwarp();
-            if (again && !mbar_wait(empty(st), turn, abort_flag, p.err)) {
+            if (!mbar_wait(raw_full(slot), (pos / C::AHEAD) & 1, abort_flag,
+                           p.err) ||
+                (pos >= ST && !mbar_wait(empty(st), (pos / ST - 1) & 1,
+                                         abort_flag, p.err))) {
               ok = false;
               break;
             }
-            const uint32_t to =
-                sR + st * C::STAGE + cw * (RW / 8) * gs;
-            const unsigned char* src = codes + slot * C::CODE_TILE +
-                                       cw * (RW * ROW * 16) + lane * 16;
-            const unsigned char* ssrc = codes + slot * C::CODE_TILE +
-                                        C::CODE_BYTES + cw * (RW * D / 16) +
-                                        ln * (D / 16) + cp * 2;
+            const uint32_t to = sR + st * C::STAGE + cw * (RW / 8) * gs;
+            const unsigned char* src = base + C::OFF_CODES +
+                                       slot * C::CODE_TILE +
+                                       cw * (RW * C::CODE_ROW) + lane * 16;
+            // (V rows that no row of the block sees are zeros: they may hold
+            // another request's NaN)
+            const int key0 = pc.kt0 + i_tile * BN + cw * RW + ln;
+            const bool edge = v && (key0 - ln < pc.klo ||
+                                    key0 - ln + RW > pc.khi);
 #pragma unroll
             for (int i = 0; i < PER; ++i) {
-              const uint4 w = *reinterpret_cast<const uint4*>(src + i * 512);
+              uint4 w = *reinterpret_cast<const uint4*>(src + i * 512);
+              if (edge && (key0 + i * RI < pc.klo || key0 + i * RI >= pc.khi)) {
+                w = make_uint4(0, 0, 0, 0);
+                sf[i] = 0;
+              }
               const int r8 = row_in_8(i);
               const uint32_t line = to + eights(i) * gs + r8 * 128;
               if constexpr (KV == kE4m3) {
-                const uint32_t at = line + (cp >> 2) * 1024;
+                const uint32_t dst = line + (cp >> 2) * 1024;
                 uint32_t h[8];
                 e4m3x4_to_f16(w.x, h[0], h[1]);
                 e4m3x4_to_f16(w.y, h[2], h[3]);
@@ -724,21 +625,19 @@ tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
                 e4m3x4_to_f16(w.w, h[6], h[7]);
                 // (the two halves in an order that keeps the lanes of a row
                 // in different banks)
-                const uint32_t c0 = (cp & 3) * 2 + ((cp >> 2) & 1);
                 const bool odd = (cp >> 2) & 1;
+                const uint32_t c0 = (cp & 3) * 2 + (odd ? 1 : 0);
                 uint32_t x[4], y[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                   x[e] = odd ? h[4 + e] : h[e];
                   y[e] = odd ? h[e] : h[4 + e];
                 }
-                store_wide<T>(at + ((c0 ^ r8) << 4), x);
-                store_wide<T>(at + ((c0 ^ 1 ^ r8) << 4), y);
+                store_wide<T>(dst + ((c0 ^ r8) << 4), x);
+                store_wide<T>(dst + ((c0 ^ 1 ^ r8) << 4), y);
               } else {
-                const uint32_t at = line + (cp >> 1) * 1024;
-                const uint32_t f = e4m3x2_to_f16(
-                    *reinterpret_cast<const uint16_t*>(ssrc +
-                                                       i * (RI * D / 16)));
+                const uint32_t dst = line + (cp >> 1) * 1024;
+                const uint32_t f = e4m3x2_to_f16(sf[i]);
                 const uint32_t f0 = __byte_perm(f, f, 0x1010),
                                f1 = __byte_perm(f, f, 0x3232);
                 const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
@@ -749,23 +648,19 @@ tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
 #pragma unroll
                   for (int e = 0; e < 4; ++e)
                     h[e] = hmul2_u32(h[e], k < 2 ? f0 : f1);
-                  store_wide<T>(at + ((((cp & 1) * 4 + k) ^ r8) << 4), h);
+                  store_wide<T>(dst + ((((cp & 1) * 4 + k) ^ r8) << 4), h);
                 }
               }
             }
             fence_proxy_async();
             __syncwarp();
-            if (lane == 0) mbar_arrive(full(set[0], st));
-            if (++st == ST) {
-              st = 0;
-              turn ^= 1;
-              again = true;
+            if (lane == 0) {
+              mbar_arrive(full(set, st));
+              mbar_arrive(raw_empty(slot));
             }
-            if (++slot == AHEAD) slot = 0;
           }
-          advance();
+          at += total;
         }
-        cp_async_wait<0>();
       }
     } else if (warp >= C::MMA_WARP && warp < C::MMA_WARP + NX) {
       // -------------------------------------- MMA issuer of stream x
@@ -1494,6 +1389,7 @@ cudaError_t launch_d(const Params& p, int D, const CUtensorMap& mk,
 }
 // Caches of codes (tree_codes.cu).
 cudaError_t launch_codes(const Params& p, int D, bool bf16, int kv,
+                         const CUtensorMap& mk, const CUtensorMap& mv,
                          const CUtensorMap& mq, int grid,
                          const cudaLaunchAttribute* attr, cudaStream_t stream);
 

@@ -6,20 +6,18 @@ namespace pkv {
 namespace tree {
 
 cudaError_t launch_codes(const Params& p, int D, bool bf16, int kv,
+                         const CUtensorMap& mk, const CUtensorMap& mv,
                          const CUtensorMap& mq, int grid,
                          const cudaLaunchAttribute* attr,
                          cudaStream_t stream) {
-  CUtensorMap none;
-  memset(&none, 0, sizeof(none));
   if (kv == kE4m3)
-    return bf16 ? launch_d<__nv_bfloat16, kE4m3>(p, D, none, none, mq, grid,
-                                                 attr, stream)
-                : launch_d<__half, kE4m3>(p, D, none, none, mq, grid, attr,
+    return bf16 ? launch_d<__nv_bfloat16, kE4m3>(p, D, mk, mv, mq, grid, attr,
+                                                 stream)
+                : launch_d<__half, kE4m3>(p, D, mk, mv, mq, grid, attr,
                                           stream);
-  return bf16 ? launch_d<__nv_bfloat16, kE2m1>(p, D, none, none, mq, grid,
-                                               attr, stream)
-              : launch_d<__half, kE2m1>(p, D, none, none, mq, grid, attr,
-                                        stream);
+  return bf16 ? launch_d<__nv_bfloat16, kE2m1>(p, D, mk, mv, mq, grid, attr,
+                                               stream)
+              : launch_d<__half, kE2m1>(p, D, mk, mv, mq, grid, attr, stream);
 }
 
 }  // namespace tree
