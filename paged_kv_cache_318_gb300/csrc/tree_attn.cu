@@ -128,6 +128,7 @@ cudaError_t launch_tree_attn(const AttnParams& a, const int32_t* parents,
   p.G = a.G;
   p.inv_g = 1.f / static_cast<float>(a.G);
   p.BS = a.BS;
+  p.bs_shift = a.bs_shift;
   p.scale = a.scale;
   p.softcap = a.softcap;
   p.sinks = a.sinks;

@@ -144,6 +144,7 @@ struct Params {
   int max_blocks;
   int64_t num_blocks;
   int Hq, Hkv, G, BS, RB;
+  int bs_shift;             // log2(BS) of a power of two, else -1
   float inv_g;              // 1 / G
   float scale, softcap;
   const float* sinks;
@@ -531,13 +532,16 @@ tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
         auto eights = [&](int i) {
           return RI >= 8 ? i * (RI / 8) + (ln >> 3) : i / (8 / (RI < 8 ? RI : 8));
         };
-        int at = 0;                    // tiles of the pieces before
-        bool ok = true;
+        int st = 0, slot = 0;          // stage, place of its codes
+        uint32_t s_turn = 1, r_turn = 0;     // their parities
+        bool ok = true, again = false; // (the first round fills empty stages)
         for (int n = 0; ok; ++n) {
           Piece pc;
           if (take(n, pc) <= 0) break;
           release(n);
           const int total = 2 * pc.nt;
+          const bool low = pc.kt0 < pc.klo;
+          const bool high = pc.kt0 + pc.nt * BN > pc.khi;
           // place q of the piece: its tile, and K (0) or V
           auto tile = [&](int q, int& v) -> int {
             if (pc.pair) {
@@ -557,16 +561,18 @@ tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
             int v;
             const int key = pc.kt0 + tile(q, v) * BN + cw * RW;
             if (KV == kE2m1 && q < total && key < pc.khi)
-              blk = __ldg(bt + key / p.BS);
+              blk = __ldg(bt + (p.bs_shift >= 0 ? key >> p.bs_shift
+                                                : key / p.BS));
           };
           auto scales = [&](int q) {
             int v;
             const int key = pc.kt0 + tile(q, v) * BN + cw * RW;
             if (KV == kE2m1 && q < total && key < pc.khi && blk >= 0 &&
                 blk < p.num_blocks) {
+              const int row = p.bs_shift >= 0 ? key & (p.BS - 1) : key % p.BS;
               const uint8_t* from = (v ? p.v_sf : p.k_sf) + blk * p.f_sb +
-                                    (key % p.BS + ln) * p.f_sr +
-                                    pc.g * p.f_sh + cp * 2;
+                                    (row + ln) * p.f_sr + pc.g * p.f_sh +
+                                    cp * 2;
 #pragma unroll
               for (int i = 0; i < PER; ++i)
                 sf_next[i] = __ldg(reinterpret_cast<const uint16_t*>(
@@ -581,20 +587,16 @@ tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
           entry(1);
 #pragma unroll 1
           for (int q = 0; q < total; ++q) {
-            const int pos = at + q, st = pos % ST, slot = pos % C::AHEAD;
             int v;
             const int i_tile = tile(q, v);
-            const int set = NX == 1 ? 0 : pc.pair ? 2 : i_tile & 1;
             if (KV == kE2m1) {
 #pragma unroll
               for (int i = 0; i < PER; ++i) sf[i] = sf_next[i];
               scales(q + 1);
               entry(q + 2);
             }
-            if (!mbar_wait(raw_full(slot), (pos / C::AHEAD) & 1, abort_flag,
-                           p.err) ||
-                (pos >= ST && !mbar_wait(empty(st), (pos / ST - 1) & 1,
-                                         abort_flag, p.err))) {
+            if (!mbar_wait(raw_full(slot), r_turn, abort_flag, p.err) ||
+                (again && !mbar_wait(empty(st), s_turn, abort_flag, p.err))) {
               ok = false;
               break;
             }
@@ -605,8 +607,8 @@ tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
             // (V rows that no row of the block sees are zeros: they may hold
             // another request's NaN)
             const int key0 = pc.kt0 + i_tile * BN + cw * RW + ln;
-            const bool edge = v && (key0 - ln < pc.klo ||
-                                    key0 - ln + RW > pc.khi);
+            const bool edge = v && ((low && i_tile == 0) ||
+                                    (high && i_tile == pc.nt - 1));
 #pragma unroll
             for (int i = 0; i < PER; ++i) {
               uint4 w = *reinterpret_cast<const uint4*>(src + i * 512);
@@ -655,11 +657,20 @@ tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
             fence_proxy_async();
             __syncwarp();
             if (lane == 0) {
+              const int set = NX == 1 ? 0 : pc.pair ? 2 : i_tile & 1;
               mbar_arrive(full(set, st));
               mbar_arrive(raw_empty(slot));
             }
+            if (++st == ST) {
+              st = 0;
+              s_turn ^= 1;
+              again = true;
+            }
+            if (++slot == C::AHEAD) {
+              slot = 0;
+              r_turn ^= 1;
+            }
           }
-          at += total;
         }
       }
     } else if (warp >= C::MMA_WARP && warp < C::MMA_WARP + NX) {
