@@ -96,7 +96,7 @@ struct Cfg {
                        MMA_WARP = SM_WARPS + 2;
   // codes: the warps that copy and widen them, in place of the loader
   static constexpr int CODE_WARP = SM_WARPS + 4,
-                       CODE_WARPS = KV == 0 ? 0 : NX == 2 ? 8 : 4;
+                       CODE_WARPS = KV ? 8 : 0;
   static constexpr int THREADS = (SM_WARPS + 4 + CODE_WARPS) * 32;
   // warps that take every piece and are done with it at once
   static constexpr int TAKERS = 1 + NX + CODE_WARPS;
@@ -119,12 +119,15 @@ struct Cfg {
   // one CTA per SM (it takes all of tensor memory)
   static constexpr int SMEM = SMEM_USED < 120 * 1024 ? 120 * 1024 : SMEM_USED;
   static_assert(SMEM <= 232448, "shared memory of a CTA");
-  // Codes with two streams: 640 threads, launched with 96 registers each; the
-  // softmax warps take 144, the others keep 64.
-  static constexpr bool SPLIT_REGS = KV != 0 && NX == 2;
-  static constexpr int LAUNCH_REGS = 96, SOFTMAX_REGS = 144, OTHER_REGS = 64;
+  // Codes: 640 or 512 threads, launched with 96 or 128 registers each; the
+  // softmax warps take 144 or 200, the others keep 64 or 104.
+  static constexpr bool SPLIT_REGS = KV != 0;
+  static constexpr int LAUNCH_REGS = NX == 2 ? 96 : 128,
+                       SOFTMAX_REGS = NX == 2 ? 144 : 200,
+                       OTHER_REGS = NX == 2 ? 64 : 104;
   static_assert(!SPLIT_REGS ||
-                    256 * SOFTMAX_REGS + (THREADS - 256) * OTHER_REGS <=
+                    NX * 128 * SOFTMAX_REGS +
+                            (THREADS - NX * 128) * OTHER_REGS <=
                         THREADS * LAUNCH_REGS,
                 "register split");
 };
@@ -515,11 +518,12 @@ tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
       // ------------------------------------------------- codes widened
       // Tile after tile of the ring's order, from the loader's rows of codes to
       // the 16-bit layout that the products read: exactly, the tensor scales
-      // joining the logits and the output.  A warp widens 16 rows (they lie in
-      // one page, so it has one page's block scales to fetch).
+      // joining the logits and the output.  A warp widens 16 rows (8 at
+      // head size 256): they lie in one page, so it has one page's block scales
+      // to fetch.
       if constexpr (KV != 0) {
-        constexpr int RW = 16;                           // rows of a warp
-        static_assert(BN == RW * C::CODE_WARPS, "all rows of a tile");
+        constexpr int RW = BN / C::CODE_WARPS;           // rows of a warp
+        static_assert(RW == 16 || RW == 8, "whole eights of rows of one page");
         constexpr int VALS = KV == kE4m3 ? 16 : 32;      // values of 16 bytes
         constexpr int ROW = D / VALS;                    // 16 bytes of a row
         constexpr int RI = 32 / ROW;                     // rows at a time
