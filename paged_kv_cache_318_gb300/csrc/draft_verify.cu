@@ -37,6 +37,7 @@ namespace verify {
 constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kMaxRows = PKV_TREE_MAX_ROWS;
 constexpr int kChunk = 1024;            // vocabulary entries of a partial sum
+constexpr int kMaxRanks = 8;            // CTAs of a request
 constexpr int kMaxChunks = PKV_VERIFY_MAX_VOCAB / kChunk + 1;
 
 struct Params {
@@ -66,26 +67,27 @@ struct Shared {
   int gone[kMaxRows];
   float gone_p[kMaxRows];
   double chunk[kMaxChunks];
-  double total[2];                      // this CTA's sum, of even and odd passes
+  double total[2][kMaxRanks];           // the CTAs' sums, of even and odd passes
+  double all;                           // ... and theirs
+  float left[33 * 32];                  // a chunk, 32 entries and a gap
   double mass;
   int node, next, m, count, known, ask; // known: the mass is; ask: a sum is
                                         // wanted (else: the end)
 };
 
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile(
-      "barrier.cluster.arrive.release;\n"
-      "barrier.cluster.wait.acquire;" ::: "memory");
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
 }
-// *p of the CTA with this rank in the cluster.
-__device__ __forceinline__ double remote(const double* p, int rank) {
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+}
+// v to *p of the CTA with this rank in the cluster.
+__device__ __forceinline__ void put(double* p, int rank, double v) {
   uint32_t a;
-  double v;
   asm("mapa.shared::cluster.u32 %0, %1, %2;"
       : "=r"(a)
       : "r"(smem_u32(p)), "r"(rank));
-  asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(v) : "r"(a) : "memory");
-  return v;
+  asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(a), "d"(v) : "memory");
 }
 
 // A sum and the rounding errors made on the way (Knuth's two-sum).
@@ -171,6 +173,7 @@ verify_kernel(const Params p) {
     return;
   }
   const bool draft = p.draft != nullptr;
+  cluster_arrive();                      // (this CTA runs: others may write to it)
 
   // ---- every row's numbers, and what its parent's row gives its token
   for (int i = tid; i < n; i += kThreads) {
@@ -206,6 +209,7 @@ verify_kernel(const Params p) {
     s.ask = 0;
   }
   __syncthreads();
+  cluster_wait();
 
   const int chunks = (p.vocab + 15 + kChunk - 1) / kChunk;
   const int c_lo = static_cast<int>(int64_t{chunks} * rank / ranks);
@@ -214,32 +218,38 @@ verify_kernel(const Params p) {
   constexpr int VEC = R::VEC, PER = kChunk / (32 * VEC);
   R tr, dr;
   int pass = 0;
+  // Chunk c of the two rows: vector k of a lane is (32 k + lane) of the chunk's
+  // (all loads side by side).
+  auto read = [&](int c, bool use_q, float (&v)[PER][VEC],
+                  float (&q)[PER][VEC]) {
+    const int y0 = c * kChunk + lane * VEC;
+    auto go = [&](auto whole) {
+      constexpr bool W = decltype(whole)::value;
+#pragma unroll
+      for (int k = 0; k < PER; ++k)
+        tr.template load<W>(y0 + k * 32 * VEC, tr.pad, p.vocab, v[k]);
+      if (use_q) {
+#pragma unroll
+        for (int k = 0; k < PER; ++k)
+          dr.template load<W>(y0 + k * 32 * VEC, tr.pad, p.vocab, q[k]);
+      }
+    };
+    if (c * kChunk >= tr.pad && (c + 1) * kChunk <= p.vocab + tr.pad &&
+        (!use_q || dr.pad == tr.pad))
+      go(std::true_type{});
+    else
+      go(std::false_type{});
+  };
   // Sum of what is left of the node's row after m times, over the whole
-  // vocabulary; the chunks' sums stay in s.chunk.
+  // vocabulary; the chunks' sums stay in s.chunk.  (float64 is done by one warp
+  // only: an SM adds two values a clock.)
   auto sum = [&](int node, int m) -> double {
     tr.set(p.target, (start + node) * p.t_st);
     const bool use_q = draft && m > 0;
     if (use_q) dr.set(p.draft, (start + node) * p.d_st);
     for (int c = c_lo + warp; c < c_hi; c += kWarps) {
       float v[PER][VEC], q[PER][VEC];
-      const int y0 = c * kChunk + lane * VEC;
-      // (all loads of a chunk side by side)
-      auto read = [&](auto whole) {
-        constexpr bool W = decltype(whole)::value;
-#pragma unroll
-        for (int k = 0; k < PER; ++k)
-          tr.template load<W>(y0 + k * 32 * VEC, tr.pad, p.vocab, v[k]);
-        if (use_q) {
-#pragma unroll
-          for (int k = 0; k < PER; ++k)
-            dr.template load<W>(y0 + k * 32 * VEC, tr.pad, p.vocab, q[k]);
-        }
-      };
-      if (c * kChunk >= tr.pad && (c + 1) * kChunk <= p.vocab + tr.pad &&
-          (!use_q || dr.pad == tr.pad))
-        read(std::true_type{});
-      else
-        read(std::false_type{});
+      read(c, use_q, v, q);
       Sum2 a{0.f, 0.f};
 #pragma unroll
       for (int k = 0; k < PER; ++k)
@@ -272,13 +282,18 @@ verify_kernel(const Params p) {
       for (int c = lane; c < c_hi - c_lo; c += 32) t += s.chunk[c];
 #pragma unroll
       for (int o = 16; o; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-      if (lane == 0) s.total[pass & 1] = t;
+      if (lane < ranks) put(&s.total[pass & 1][rank], lane, t);
     }
-    cluster_sync();
-    double all = 0.0;
-    for (uint32_t r = 0; r < ranks; ++r) all += remote(&s.total[pass & 1], r);
+    cluster_arrive();
+    cluster_wait();
+    if (tid == 0) {
+      double all = 0.0;
+      for (uint32_t r = 0; r < ranks; ++r) all += s.total[pass & 1][r];
+      s.all = all;
+    }
+    __syncthreads();
     ++pass;
-    return all;
+    return s.all;
   };
 
   // ---- the walk: warp 0 goes on until it needs a sum, or to the end
@@ -385,7 +400,7 @@ verify_kernel(const Params p) {
     int owner = -1, last = -1;
     const int par = (pass - 1) & 1;
     for (uint32_t r = 0; r < ranks; ++r) {
-      const double t = remote(&s.total[par], r);
+      const double t = s.total[par][r];
       if (r == rank) mine_before = run;
       if (t > 0.0) last = r;
       run += t;
@@ -421,52 +436,52 @@ verify_kernel(const Params p) {
       // (rounding may leave a sum's last bit short: the last chunk with mass)
       const bool end = found < 0;
       if (end) found = some;
-      // ... then the entry
+      // ... then the 32 entries (a lane's) that hold it ...
       const bool use_q = draft && m > 0;
-      const int y0 = (c_lo + found) * kChunk + lane * VEC;
-      int token = -1, top = -1;          // top: last entry with mass so far
-      for (int k = 0; k < PER && token < 0; ++k) {
-        float v[VEC], q[VEC];
-        tr.template load<false>(y0 + k * 32 * VEC, tr.pad, p.vocab, v);
-        if (use_q)
-          dr.template load<false>(y0 + k * 32 * VEC, tr.pad, p.vocab, q);
-        const int x0 = y0 + k * 32 * VEC - tr.pad;
-        double own = 0.0, part[VEC];
-        int mine = -1;
+      float v[PER][VEC], q[PER][VEC];
+      read(c_lo + found, use_q, v, q);
+      const int x0 = (c_lo + found) * kChunk - tr.pad;
+#pragma unroll
+      for (int k = 0; k < PER; ++k)
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
-          float r = use_q ? rest(s, v[e], q[e], m) : fmaxf(v[e], 0.f);
+          const int i = (k * 32 + lane) * VEC + e;
+          float r = use_q ? rest(s, v[k][e], q[k][e], m) : fmaxf(v[k][e], 0.f);
           if (!draft)
             for (int j = 0; j < m; ++j)
-              if (s.gone[j] == x0 + e) r = 0.f;
-          if (r > 0.f) mine = x0 + e;
-          own += r;
-          part[e] = own;
+              if (s.gone[j] == x0 + i) r = 0.f;
+          s.left[i + (i >> 5)] = r;
         }
-        double in = own;
+      __syncwarp();
+      Sum2 a{0.f, 0.f};
+#pragma unroll 8
+      for (int e = 0; e < 32; ++e) a.add(s.left[lane * 33 + e]);
+      const double own = static_cast<double>(a.hi) + a.lo;
+      auto scan = [&](double x) -> double {
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-          const double y = __shfl_up_sync(0xffffffffu, in, o);
-          if (lane >= o) in += y;
+          const double y = __shfl_up_sync(0xffffffffu, x, o);
+          if (lane >= o) x += y;
         }
-        const unsigned any = __ballot_sync(0xffffffffu, mine >= 0);
-        if (any) top = __shfl_sync(0xffffffffu, mine, 31 - __clz(any));
-        const unsigned hit =
-            __ballot_sync(0xffffffffu, !end && at + in > want);
-        if (hit) {
-          int x = mine;
-#pragma unroll
-          for (int e = VEC - 1; e >= 0; --e)
-            if (at + (in - own) + part[e] > want) x = x0 + e;
-          token = __shfl_sync(0xffffffffu, x, __ffs(hit) - 1);
-        }
-        at += __shfl_sync(0xffffffffu, in, 31);
-      }
-      if (token < 0) token = top;
+        return x;
+      };
+      const double in = scan(own);
+      const unsigned hit = __ballot_sync(0xffffffffu, !end && at + in > want);
+      const unsigned any = __ballot_sync(0xffffffffu, own > 0.0);
+      // (none: the last one with mass)
+      const int src = hit ? __ffs(hit) - 1 : any ? 31 - __clz(any) : 0;
+      at += __shfl_sync(0xffffffffu, in - own, src);
+      // ... then the entry
+      const float r = s.left[src * 33 + lane];
+      const double inr = scan(static_cast<double>(r));
+      const unsigned hit1 =
+          __ballot_sync(0xffffffffu, hit != 0 && at + inr > want);
+      const unsigned any1 = __ballot_sync(0xffffffffu, r > 0.f);
+      const int e1 = hit1 ? __ffs(hit1) - 1 : any1 ? 31 - __clz(any1) : 0;
+      const int token = x0 + src * 32 + e1;
       if (lane == 0) out_t[count - 1] = token;
     }
   }
-  cluster_sync();                        // (the others read this CTA's sums)
 }
 
 }  // namespace verify
