@@ -102,49 +102,123 @@ struct Sum2 {
   }
 };
 
-// One row of a distribution: entry x lies `pad` entries behind a 16-byte
-// boundary's; places y = x + pad divide into aligned vectors.
-template <typename T>
-struct Row {
-  static constexpr int VEC = 16 / static_cast<int>(sizeof(T));
-  const T* p;
-  int pad;
-  __device__ __forceinline__ void set(const void* base, int64_t at) {
-    p = static_cast<const T*>(base) + at;
-    pad = static_cast<int>((reinterpret_cast<uintptr_t>(p) & 15) / sizeof(T));
-  }
-  // Entries at places y .. y + VEC - 1 of a row shifted by `shift` (this row's
-  // pad or another's).  WHOLE: all are entries of the row, and one vector.
-  template <bool WHOLE>
-  __device__ __forceinline__ void load(int y, int shift, int vocab,
-                                       float* v) const {
-    const int x = y - shift;
-    if constexpr (WHOLE) {
-      const uint4 raw = __ldg(reinterpret_cast<const uint4*>(p + x));
-      if constexpr (std::is_same<T, float>::value) {
-        v[0] = __uint_as_float(raw.x);
-        v[1] = __uint_as_float(raw.y);
-        v[2] = __uint_as_float(raw.z);
-        v[3] = __uint_as_float(raw.w);
-      } else {
-        widen8<T>(raw, v);
-      }
-    } else {
-#pragma unroll
-      for (int e = 0; e < VEC; ++e)
-        v[e] = x + e >= 0 && x + e < vocab ? to_f32(p[x + e]) : 0.f;
-    }
+// Two such sums side by side.
+struct Sum4 {
+  uint64_t hi, lo;
+  __device__ __forceinline__ void add(uint64_t x) {
+    const uint64_t neg = pair(-1.f, -1.f);
+    const uint64_t s = add2(hi, x);
+    const uint64_t b = fma2(hi, neg, s);             // s - hi
+    const uint64_t t = fma2(b, neg, s);              // s - b
+    lo = add2(lo, add2(fma2(t, neg, hi), fma2(b, neg, x)));
+    hi = s;
   }
 };
 
-// What is left of p after q has been taken off m times.
-__device__ __forceinline__ float rest(const Shared& s, float p, float q,
-                                      int m) {
-  float r = fmaxf(p, 0.f);
-  if (m > 0) r = fmaxf(__fsub_rn(r, q), 0.f);       // (the first mass is 1)
-  for (int k = 1; k < m; ++k)
-    r = fmaxf(__fmaf_rn(-s.zl[k], q, __fmaf_rn(-s.zh[k], q, r)), 0.f);
-  return r;
+// Entries x .. x + VEC - 1 of a row, as 16 bytes; zero outside [0, vocab).
+template <typename T>
+__device__ __noinline__ uint4 edge(const T* row, int x, int vocab) {
+  constexpr int VEC = 16 / static_cast<int>(sizeof(T));
+  union {
+    uint4 v;
+    T e[VEC];
+  } r;
+#pragma unroll
+  for (int e = 0; e < VEC; ++e)
+    r.e[e] = x + e >= 0 && x + e < vocab ? row[x + e] : from_f32<T>(0.f);
+  return r.v;
+}
+
+// Places of a row: entry x lies at place x + pad, and places divide into
+// 16-byte vectors of memory.
+template <typename T>
+__device__ __forceinline__ int pad_of(const T* row) {
+  return static_cast<int>((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(T));
+}
+
+// What is left, R, of the entries at places c kChunk .. of a row of `target`
+// after q (the same entries of `draft`) has been taken off m times: this lane's
+// share of their sum, and with `keep` the values to s.left.  (One piece of code
+// for both: a launch runs it a few times only, so what it costs is to be
+// fetched.  Unrolled twice over, the kernel spent most of its time on that.)
+template <typename T>
+__device__ __noinline__ Sum2 chunk_rest(Shared& s, const T* target,
+                                        const T* draft, int c, int m,
+                                        int vocab, bool keep) {
+  constexpr int VEC = 16 / static_cast<int>(sizeof(T));
+  constexpr int PER = kChunk / (32 * VEC), W = VEC / 2;
+  const int lane = threadIdx.x & 31;
+  // vector k of a lane is number 32 k + lane of the chunk; all loads are under
+  // way together
+  const int x0 = c * kChunk - pad_of(target) + lane * VEC;
+  uint4 a[PER], b[PER];
+  const int first = c * kChunk - pad_of(target);
+  if (first >= 0 && first + kChunk <= vocab &&
+      (m == 0 || pad_of(draft) == pad_of(target))) {
+    const uint4* from = reinterpret_cast<const uint4*>(target + x0);
+#pragma unroll
+    for (int k = 0; k < PER; ++k) a[k] = __ldg(from + k * 32);
+    if (m > 0) {
+      from = reinterpret_cast<const uint4*>(draft + x0);
+#pragma unroll
+      for (int k = 0; k < PER; ++k) b[k] = __ldg(from + k * 32);
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+      a[k] = edge(target, x0 + k * 32 * VEC, vocab);
+      if (m > 0) b[k] = edge(draft, x0 + k * 32 * VEC, vocab);
+    }
+  }
+  auto two = [](const uint4& v, int w) -> uint64_t {
+    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+    if constexpr (std::is_same<T, float>::value)
+      return pair(__uint_as_float(u[2 * w]), __uint_as_float(u[2 * w + 1]));
+    else
+      return pair(elem_f32<T>(u[w], 0), elem_f32<T>(u[w], 1));
+  };
+  auto positive = [](uint64_t v) -> uint64_t {
+    float x, y;
+    unpair(v, x, y);
+    return pair(fmaxf(x, 0.f), fmaxf(y, 0.f));
+  };
+  uint64_t r[PER * W];
+#pragma unroll
+  for (int k = 0; k < PER; ++k)
+#pragma unroll
+    for (int w = 0; w < W; ++w) r[k * W + w] = positive(two(a[k], w));
+#pragma unroll 1
+  for (int i = 0; i < m; ++i) {
+    // (the mass as two floats; the first is 1)
+    const uint64_t zh = pair(-s.zh[i], -s.zh[i]),
+                   zl = pair(-s.zl[i], -s.zl[i]);
+#pragma unroll
+    for (int k = 0; k < PER; ++k)
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        const uint64_t q = two(b[k], w);
+        uint64_t& v = r[k * W + w];
+        v = positive(fma2(zl, q, fma2(zh, q, v)));
+      }
+  }
+  Sum4 t{0, 0};
+#pragma unroll
+  for (int k = 0; k < PER * W; ++k) t.add(r[k]);
+  if (keep) {
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+      const int i = (k * 32 + lane) * VEC;
+      float* to = s.left + i + (i >> 5);
+#pragma unroll
+      for (int w = 0; w < W; ++w) unpair(r[k * W + w], to[2 * w], to[2 * w + 1]);
+    }
+  }
+  float h0, h1, l0, l1;
+  unpair(t.hi, h0, h1);
+  unpair(t.lo, l0, l1);
+  Sum2 sum{h0, __fadd_rn(l0, l1)};
+  sum.add(h1);
+  return sum;
 }
 
 template <typename T>
@@ -214,49 +288,19 @@ verify_kernel(const Params p) {
   const int chunks = (p.vocab + 15 + kChunk - 1) / kChunk;
   const int c_lo = static_cast<int>(int64_t{chunks} * rank / ranks);
   const int c_hi = static_cast<int>(int64_t{chunks} * (rank + 1) / ranks);
-  using R = Row<T>;
-  constexpr int VEC = R::VEC, PER = kChunk / (32 * VEC);
-  R tr, dr;
-  int pass = 0;
-  // Chunk c of the two rows: vector k of a lane is (32 k + lane) of the chunk's
-  // (all loads side by side).
-  auto read = [&](int c, bool use_q, float (&v)[PER][VEC],
-                  float (&q)[PER][VEC]) {
-    const int y0 = c * kChunk + lane * VEC;
-    auto go = [&](auto whole) {
-      constexpr bool W = decltype(whole)::value;
-#pragma unroll
-      for (int k = 0; k < PER; ++k)
-        tr.template load<W>(y0 + k * 32 * VEC, tr.pad, p.vocab, v[k]);
-      if (use_q) {
-#pragma unroll
-        for (int k = 0; k < PER; ++k)
-          dr.template load<W>(y0 + k * 32 * VEC, tr.pad, p.vocab, q[k]);
-      }
-    };
-    if (c * kChunk >= tr.pad && (c + 1) * kChunk <= p.vocab + tr.pad &&
-        (!use_q || dr.pad == tr.pad))
-      go(std::true_type{});
-    else
-      go(std::false_type{});
-  };
+  const T* tr = nullptr;                 // the rows at hand, and their pad
+  const T* dr = nullptr;
+  int pad = 0, pass = 0;
   // Sum of what is left of the node's row after m times, over the whole
   // vocabulary; the chunks' sums stay in s.chunk.  (float64 is done by one warp
   // only: an SM adds two values a clock.)
   auto sum = [&](int node, int m) -> double {
-    tr.set(p.target, (start + node) * p.t_st);
-    const bool use_q = draft && m > 0;
-    if (use_q) dr.set(p.draft, (start + node) * p.d_st);
+    tr = static_cast<const T*>(p.target) + (start + node) * p.t_st;
+    dr = static_cast<const T*>(p.draft) + (start + node) * p.d_st;
+    pad = pad_of(tr);
     for (int c = c_lo + warp; c < c_hi; c += kWarps) {
-      float v[PER][VEC], q[PER][VEC];
-      read(c, use_q, v, q);
-      Sum2 a{0.f, 0.f};
-#pragma unroll
-      for (int k = 0; k < PER; ++k)
-#pragma unroll
-        for (int e = 0; e < VEC; ++e)
-          a.add(use_q ? rest(s, v[k][e], q[k][e], m) : fmaxf(v[k][e], 0.f));
-#pragma unroll
+      Sum2 a = chunk_rest(s, tr, dr, c, draft ? m : 0, p.vocab, false);
+#pragma unroll 1
       for (int o = 16; o; o >>= 1) {
         const float h = __shfl_xor_sync(0xffffffffu, a.hi, o);
         const float l = __shfl_xor_sync(0xffffffffu, a.lo, o);
@@ -272,7 +316,7 @@ verify_kernel(const Params p) {
       if (!draft && m > 0) {
         if (lane == 0)
           for (int k = 0; k < m; ++k) {
-            const int c = (s.gone[k] + tr.pad) / kChunk - c_lo;
+            const int c = (s.gone[k] + pad) / kChunk - c_lo;
             if (c >= 0 && c < c_hi - c_lo)
               s.chunk[c] = fmax(s.chunk[c] - s.gone_p[k], 0.0);
           }
@@ -437,24 +481,17 @@ verify_kernel(const Params p) {
       const bool end = found < 0;
       if (end) found = some;
       // ... then the 32 entries (a lane's) that hold it ...
-      const bool use_q = draft && m > 0;
-      float v[PER][VEC], q[PER][VEC];
-      read(c_lo + found, use_q, v, q);
-      const int x0 = (c_lo + found) * kChunk - tr.pad;
-#pragma unroll
-      for (int k = 0; k < PER; ++k)
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          const int i = (k * 32 + lane) * VEC + e;
-          float r = use_q ? rest(s, v[k][e], q[k][e], m) : fmaxf(v[k][e], 0.f);
-          if (!draft)
-            for (int j = 0; j < m; ++j)
-              if (s.gone[j] == x0 + i) r = 0.f;
-          s.left[i + (i >> 5)] = r;
+      const int x0 = (c_lo + found) * kChunk - pad;
+      chunk_rest(s, tr, dr, c_lo + found, draft ? m : 0, p.vocab, true);
+      __syncwarp();
+      if (!draft)
+        for (int j = lane; j < m; j += 32) {
+          const int i = s.gone[j] - x0;
+          if (i >= 0 && i < kChunk) s.left[i + (i >> 5)] = 0.f;
         }
       __syncwarp();
       Sum2 a{0.f, 0.f};
-#pragma unroll 8
+#pragma unroll 4
       for (int e = 0; e < 32; ++e) a.add(s.left[lane * 33 + e]);
       const double own = static_cast<double>(a.hi) + a.lo;
       auto scan = [&](double x) -> double {
