@@ -27,6 +27,7 @@
 // across lanes and chunks and all comparisons in float64.
 #include <math.h>
 
+#include <mutex>
 #include <type_traits>
 
 #include "pkv_common.cuh"
@@ -541,31 +542,46 @@ cudaError_t launch_verify(const VerifyLaunch& a, int elem, cudaStream_t stream) 
   p.out_rows = a.out_rows;
   p.out_count = a.out_count;
   p.err = a.err;
-  // CTAs of a request: as many as one wave holds, with 4 chunks each at least
-  const int sms = current_sm_count();
-  const int chunks = (a.vocab + 15 + kChunk - 1) / kChunk;
-  int c = 1;
-  while (c < 8 && a.batch * c * 2 <= sms && chunks >= c * 8) c *= 2;
+  auto kern = elem == PKV_F32    ? verify_kernel<float>
+              : elem == PKV_BF16 ? verify_kernel<__nv_bfloat16>
+                                 : verify_kernel<__half>;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = c;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(a.batch) * c);
   cfg.blockDim = dim3(kThreads);
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  note_launch();
-  switch (elem) {
-    case PKV_F32:
-      return cudaLaunchKernelEx(&cfg, verify_kernel<float>, p);
-    case PKV_BF16:
-      return cudaLaunchKernelEx(&cfg, verify_kernel<__nv_bfloat16>, p);
-    default:
-      return cudaLaunchKernelEx(&cfg, verify_kernel<__half>, p);
+  // CTAs of a request: as many as one wave holds, with 4 chunks each at least.
+  // (Clusters do not cross the GPU's SM groups, so the driver says how many
+  // fit: 76 of 2 CTAs, but 46 of 3 and 15 of 8 on 152 SMs.)
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  static std::mutex mu;
+  static int fits[64][kMaxRanks + 1] = {};     // clusters, per device and size
+  const int chunks = (a.vocab + 15 + kChunk - 1) / kChunk;
+  int c = chunks / 4 < kMaxRanks ? chunks / 4 : kMaxRanks;
+  for (; c > 1; --c) {
+    if (static_cast<int64_t>(a.batch) * c > current_sm_count()) continue;
+    std::lock_guard<std::mutex> lk(mu);
+    int& n = fits[dev & 63][c];
+    if (n == 0) {
+      attr[0].val.clusterDim.x = c;
+      cfg.gridDim = dim3(c);
+      e = cudaOccupancyMaxActiveClusters(&n, verify_kernel<float>, &cfg);
+      if (e != cudaSuccess) return e;
+      if (n == 0) n = -1;
+    }
+    if (a.batch <= n) break;
   }
+  if (c < 1) c = 1;
+  attr[0].val.clusterDim.x = c;
+  cfg.gridDim = dim3(static_cast<unsigned>(a.batch) * c);
+  note_launch();
+  return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
 }  // namespace pkv

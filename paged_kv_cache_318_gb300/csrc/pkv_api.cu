@@ -1758,7 +1758,10 @@ size_t pkv_paged_attention_workspace_size_tree(
                        num_splits) != PKV_OK ||
       check_tree(max_seqlen_q, num_splits, opts) != PKV_OK)
     return static_cast<size_t>(-1);
-  if (num_splits != 0 || max_seqlen_q == 0) return 0;
+  // (a unit of one tile of keys is not cut)
+  if (num_splits != 0 || max_seqlen_q == 0 ||
+      max_seqlen_k <= tree_tile_keys(head_size))
+    return 0;
   int sms = 0;
   if (device_info(nullptr, &sms) != PKV_OK) return static_cast<size_t>(-1);
   return tree_scratch_bytes(head_size, num_heads / num_kv_heads, max_seqlen_q,

@@ -477,6 +477,7 @@ cudaError_t launch_prefill_attn_tc(const AttnParams& p, int D, bool bf16,
 // or tree_scratch_bytes, 256-byte aligned): lets the shares of the CTAs cut
 // units; without it a unit is worked through by one CTA.
 size_t tree_scratch_bytes(int D, int G, int max_n, int sms);
+inline int tree_tile_keys(int D) { return D == 256 ? 64 : 128; }
 cudaError_t launch_tree_attn(const AttnParams& p, const int32_t* parents,
                              int max_n, int64_t max_k, int D, bool bf16,
                              int sms, void* scratch, bool pdl,

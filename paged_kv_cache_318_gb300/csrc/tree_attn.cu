@@ -5,79 +5,92 @@
 namespace pkv {
 namespace tree {
 
-// Joins the pieces of the units that the shares' ends cut.  Block (c, y): rows
-// y of the unit that CTA c starts and does not end, a warp per row: M = the
-// largest partial LSE (and the sink), w_k = e^(lse_k - M), out = sum w_k o_k /
-// sum w_k, lse = M + ln sum w_k.
+// Joins the pieces of the units that the shares' ends cut.  Blocks (x, .) look
+// through the marks of CTAs x, x + gridDim.x, ..; a unit's rows go round the
+// warps of the blocks (., y): M = the largest partial LSE (and the sink), w_k =
+// e^(lse_k - M), out = sum w_k o_k / sum w_k, lse = M + ln sum w_k.
 constexpr int kFoldThreads = 256;
 template <typename T, int D>
-__global__ void __launch_bounds__(kFoldThreads)
-fold_kernel(const Params p) {
+__global__ void __launch_bounds__(kFoldThreads, 2)
+fold_kernel(const Params p, int ctas) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int c = blockIdx.x;
-  const int4 m0 = p.marks[2 * c];
-  const int np = min(m0.x, static_cast<int>(gridDim.x) - c);
-  if (np <= 0) return;
-  const int g = p.marks[2 * c + 1].x;
+  constexpr int WARPS = kFoldThreads / 32, V = D / 32, N = V > 4 ? 4 : 8;
   const int lane = threadIdx.x & 31;
-  constexpr int W = kFoldThreads / 32, V = D / 32;
-  const int rows = min(m0.z, p.rows_cap);
-  for (int row = blockIdx.y * W + (threadIdx.x >> 5); row < rows;
-       row += gridDim.y * W) {
-    const int R = m0.w + row;
-    const int tok = m0.y + R / p.G, h = g * p.G + R % p.G;
-    auto at = [&](int k) -> int64_t {
-      const int slot = k == 0 ? 2 * c + 1 : 2 * (c + k);
-      return static_cast<int64_t>(slot) * p.rows_cap + row;
-    };
-    float M = p.sinks ? p.sinks[h] : -INFINITY;
-    const float z = M;
-    for (int k0 = 0; k0 < np; k0 += 32) {
-      float s = k0 + lane < np ? p.part_lse[at(k0 + lane)] : -INFINITY;
-#pragma unroll
-      for (int o = 16; o; o >>= 1)
-        s = fmaxf(s, __shfl_xor_sync(0xffffffffu, s, o));
-      M = fmaxf(M, s);
-    }
-    const float ref = M == -INFINITY ? 0.f : M;
-    float sum = p.sinks ? ex2((z - ref) * kLog2e) : 0.f;
-    float acc[V];
-#pragma unroll
-    for (int e = 0; e < V; ++e) acc[e] = 0.f;
-    for (int k0 = 0; k0 < np; k0 += 4) {
-      float s[4], o[4][V];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int k = min(k0 + i, np - 1);
-        s[i] = p.part_lse[at(k)];
-        const float* src = p.part_o + at(k) * D + lane * V;
-#pragma unroll
-        for (int e = 0; e < V; e += 2) {
-          const float2 t = *reinterpret_cast<const float2*>(src + e);
-          o[i][e] = t.x;
-          o[i][e + 1] = t.y;
+  for (int c0 = blockIdx.x; c0 < ctas; c0 += 32 * gridDim.x) {
+    const int mine = c0 + lane * gridDim.x;
+    const unsigned cut = __ballot_sync(
+        0xffffffffu, mine < ctas && p.marks[2 * mine].x > 0);
+    for (unsigned left = cut; left; left &= left - 1) {
+      const int c = c0 + (__ffs(left) - 1) * gridDim.x;
+      const int4 m0 = p.marks[2 * c];
+      const int g = p.marks[2 * c + 1].x;
+      const int np = min(m0.x, ctas - c);
+      const int rows = min(m0.z, p.rows_cap);
+      for (int row = blockIdx.y * WARPS + (threadIdx.x >> 5); row < rows;
+           row += gridDim.y * WARPS) {
+        const int R = m0.w + row;
+        const int node = row_of(R, p.inv_g);
+        const int tok = m0.y + node, h = g * p.G + R - node * p.G;
+        // piece k: the tail of CTA c's share, then the heads of the next ones'
+        auto at = [&](int k) -> int64_t {
+          const int slot = k == 0 ? 2 * c + 1 : 2 * (c + k);
+          return static_cast<int64_t>(slot) * p.rows_cap + row;
+        };
+        const float z = p.sinks ? p.sinks[h] : -INFINITY;
+        float M = z;
+        for (int k0 = 0; k0 < np; k0 += 32) {
+          const float s =
+              k0 + lane < np ? p.part_lse[at(k0 + lane)] : -INFINITY;
+          M = fmaxf(M, s);
         }
-      }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        // (a NaN sum stays NaN)
-        const float w = k0 + i < np ? ex2((s[i] - ref) * kLog2e) : 0.f;
-        sum += w;
+        for (int o = 16; o; o >>= 1)
+          M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+        const float ref = M == -INFINITY ? 0.f : M;
+        float sum = p.sinks ? ex2((z - ref) * kLog2e) : 0.f;
+        float acc[V];
 #pragma unroll
-        for (int e = 0; e < V; ++e) acc[e] = fmaf(w, o[i][e], acc[e]);
+        for (int e = 0; e < V; ++e) acc[e] = 0.f;
+        // (N pieces' rows are under way at once)
+#pragma unroll 1
+        for (int k0 = 0; k0 < np; k0 += N) {
+          float s[N], o[N][V];
+#pragma unroll
+          for (int i = 0; i < N; ++i) {
+            const int k = min(k0 + i, np - 1);
+            s[i] = p.part_lse[at(k)];
+            const float* src = p.part_o + at(k) * D + lane * V;
+#pragma unroll
+            for (int e = 0; e < V; e += 2) {
+              const float2 t = *reinterpret_cast<const float2*>(src + e);
+              o[i][e] = t.x;
+              o[i][e + 1] = t.y;
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < N; ++i) {
+            // (a NaN sum stays NaN)
+            const float w = k0 + i < np ? ex2((s[i] - ref) * kLog2e) : 0.f;
+            sum += w;
+#pragma unroll
+            for (int e = 0; e < V; ++e) acc[e] = fmaf(w, o[i][e], acc[e]);
+          }
+        }
+        const float inv = sum > 0.f ? 1.f / sum : sum != sum ? sum : 0.f;
+        T* dst = static_cast<T*>(p.out) +
+                 static_cast<int64_t>(tok) * p.o_st +
+                 static_cast<int64_t>(h) * p.o_sh + lane * V;
+#pragma unroll
+        for (int e = 0; e < V; e += 2)
+          *reinterpret_cast<uint32_t*>(dst + e) =
+              pack2<T>(acc[e] * inv, acc[e + 1] * inv);
+        if (p.lse && lane == 0)
+          p.lse[static_cast<int64_t>(h) * p.total_q + tok] =
+              sum > 0.f ? ref + lg2(sum) * kLn2
+                        : sum != sum ? sum : -INFINITY;
       }
     }
-    const float inv = sum > 0.f ? 1.f / sum : sum != sum ? sum : 0.f;
-    T* dst = static_cast<T*>(p.out) + static_cast<int64_t>(tok) * p.o_st +
-             static_cast<int64_t>(h) * p.o_sh + lane * V;
-#pragma unroll
-    for (int e = 0; e < V; e += 2)
-      *reinterpret_cast<uint32_t*>(dst + e) =
-          pack2<T>(acc[e] * inv, acc[e + 1] * inv);
-    if (p.lse && lane == 0)
-      p.lse[static_cast<int64_t>(h) * p.total_q + tok] =
-          sum > 0.f ? ref + lg2(sum) * kLn2 : sum != sum ? sum : -INFINITY;
   }
 }
 
@@ -148,13 +161,14 @@ cudaError_t launch_tree_attn(const AttnParams& a, const int32_t* parents,
   const int64_t blocks = (packed + block_rows(D) - 1) / block_rows(D);
   p.once = blocks <= 1;        // every tile is read by one CTA only
   // an upper bound of the tiles (a window adds up to a tile at either end)
-  const int bn = D == 256 ? 64 : 128;
+  const int bn = tree_tile_keys(D);
   int64_t keys = max_k;
   if (a.wl >= 0 && static_cast<int64_t>(a.wl) + max_n + RB < keys)
     keys = static_cast<int64_t>(a.wl) + max_n + RB;
   const int64_t units = static_cast<int64_t>(a.batch) * a.Hkv * blocks;
   const int64_t tiles = units * ((keys + bn - 1) / bn + 1);
-  p.split = scratch != nullptr;
+  // (units of one tile are not cut, and need no join behind the kernel)
+  p.split = scratch != nullptr && keys > bn;
   p.rows_cap = rows_cap(D, a.G, max_n);
   const int64_t most = p.split ? tiles : units;
   const int grid = static_cast<int>(most < sms ? most : sms);
@@ -208,14 +222,16 @@ cudaError_t launch_tree_attn(const AttnParams& a, const int32_t* parents,
              : launch_d<__half, kValues>(p, D, mk, mv, mq, grid, at, stream);
   if (e != cudaSuccess || !p.split) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid, (p.rows_cap + 15) / 16);
+  // (a block per share, or two per unit where there are few units)
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * units < grid ? 2 * units : grid),
+                     (p.rows_cap + 7) / 8);
   cfg.blockDim = dim3(kFoldThreads);
   cfg.stream = stream;
   cfg.attrs = const_cast<cudaLaunchAttribute*>(at);
   cfg.numAttrs = at ? 1 : 0;
   auto join = [&](auto fold) {
     note_launch();
-    return cudaLaunchKernelEx(&cfg, fold, p);
+    return cudaLaunchKernelEx(&cfg, fold, p, grid);
   };
   switch (D) {
     case 64:
