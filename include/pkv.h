@@ -498,7 +498,7 @@ PKV_API pkv_status pkv_paged_attention_varlen_tree(
  *   x = draft_token_ids[c], Q = draft_probs[node][x] (1 without)
  *   uniform[c] Q Z < R[x]:  c stands; node = c, R = target_probs[c], Z = 1
  *   else, with draft_probs: R = max(R - Z draft_probs[node], 0), Z = sum R
- *   else, without:          Z = Z - R[x], R[x] = 0
+ *   else, without:          Z = max(Z - R[x], 0), R[x] = 0
  * and at the end the first token whose running sum of R exceeds uniform[row 0]
  * sum R.  If nothing is left of R, R = target_probs[node] there; if no running
  * sum exceeds (a number of 1 or more), the last token with R > 0; if there is

@@ -76,7 +76,7 @@ def verify(target, tokens, uniform, parents, draft=None):
             rows.append(i)
             rest, mass = np.maximum(target[i], 0.0), 1.0
         elif draft is None:
-            mass -= rest[x]
+            mass = max(mass - rest[x], 0.0)
             rest[x] = 0.0
         else:
             rest = np.maximum(rest - mass * draft[node], 0.0)

@@ -967,6 +967,8 @@ def _attend_tree(lib, q, k, v, max_seqlen_q, cu_seqlens_q, max_seqlen_k,
     if fp4 is None and (v.dtype is not k.dtype or
                         (not kv8 and k.dtype is not q.dtype)):
         raise NotImplementedError("q and cache dtypes must match")
+    if kv8 and (k_descale is None or v_descale is None):
+        raise ValueError("an fp8 cache needs k_descale and v_descale")
     if Dk != D:
         raise ValueError("q and k head_size differ")
     if block_table is None or seqused_k is None:
@@ -1117,6 +1119,8 @@ def compact_draft_cache(caches, block_table, cu_seqlens_q, seqused_k, rows,
     for c in caches:
         if c.shape != shape or c.stride() != strides or c.dtype is not dtype:
             raise ValueError("caches must share shape, strides and dtype")
+    if 0 in strides:
+        raise ValueError("rows of a cache must not overlap")
     NB, BS, H, X = shape
     es = first.element_size()
     if rows.dtype is not torch.int32 or rows.dim() != 2 or \

@@ -44,8 +44,7 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const Params p) {
   const int start = p.cu_q[b];
   const int n = min(p.cu_q[b + 1], p.total_q) - start;
   if (k <= 0 || start < 0 || n <= 0) return;
-  const int L = p.seqused_k[b];
-  const int ctx = L - n;
+  const int ctx = p.seqused_k[b] - n;
   // ---- byte offsets of the rows that move (-1: stays, or left out)
   const int32_t* rows = p.rows + b * p.rows_st;
   unsigned bad = 0;
@@ -83,23 +82,26 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const Params p) {
   if (bad && blockIdx.y == 0) atomicOr(p.err, bad);
   if (!__syncthreads_or(moves)) return;
   // ---- this thread's vector of every row of one cache
-  const int64_t id = static_cast<int64_t>(blockIdx.y) * kThreads + threadIdx.x;
-  const int c = static_cast<int>(id / p.per_token);
-  if (c >= p.caches.n) return;
-  const int v = static_cast<int>(id - static_cast<int64_t>(c) * p.per_token);
-  const int h = v / p.per_head;
-  char* base = static_cast<char*>(p.caches.ptr[c]) + h * p.c_sh +
-               static_cast<int64_t>(v - h * p.per_head) * sizeof(V);
-  for (int i0 = 0; i0 < k; i0 += kAhead) {
-    V t[kAhead];
+  // (a cache's rows may have more vectors than the grid has threads)
+  for (int64_t id = static_cast<int64_t>(blockIdx.y) * kThreads + threadIdx.x;
+       id < static_cast<int64_t>(p.per_token) * p.caches.n;
+       id += static_cast<int64_t>(gridDim.y) * kThreads) {
+    const int c = static_cast<int>(id / p.per_token);
+    const int v = static_cast<int>(id - static_cast<int64_t>(c) * p.per_token);
+    const int h = v / p.per_head;
+    char* base = static_cast<char*>(p.caches.ptr[c]) + h * p.c_sh +
+                 static_cast<int64_t>(v - h * p.per_head) * sizeof(V);
+    for (int i0 = 0; i0 < k; i0 += kAhead) {
+      V t[kAhead];
 #pragma unroll
-    for (int e = 0; e < kAhead; ++e)
-      if (i0 + e < k && src[i0 + e] >= 0)
-        t[e] = *reinterpret_cast<const V*>(base + src[i0 + e]);
+      for (int e = 0; e < kAhead; ++e)
+        if (i0 + e < k && src[i0 + e] >= 0)
+          t[e] = *reinterpret_cast<const V*>(base + src[i0 + e]);
 #pragma unroll
-    for (int e = 0; e < kAhead; ++e)
-      if (i0 + e < k && src[i0 + e] >= 0)
-        *reinterpret_cast<V*>(base + dst[i0 + e]) = t[e];
+      for (int e = 0; e < kAhead; ++e)
+        if (i0 + e < k && src[i0 + e] >= 0)
+          *reinterpret_cast<V*>(base + dst[i0 + e]) = t[e];
+    }
   }
 }
 
@@ -138,8 +140,7 @@ cudaError_t launch_compact(const CompactLaunch& a, cudaStream_t stream) {
   const int64_t y =
       (static_cast<int64_t>(p.per_token) * a.caches.n + kThreads - 1) /
       kThreads;
-  if (y > 65535) return cudaErrorInvalidValue;
-  const dim3 grid(a.batch, static_cast<unsigned>(y));
+  const dim3 grid(a.batch, static_cast<unsigned>(y < 65535 ? y : 65535));
   note_launch();
   switch (w) {
     case 16: compact_kernel<uint4><<<grid, kThreads, 0, stream>>>(p); break;

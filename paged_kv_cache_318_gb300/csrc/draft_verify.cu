@@ -8,7 +8,7 @@
 // row's children c in order:
 //   u_c q(x_c) Z < R(x_c)   c stands: the walk goes on there
 //   else, with draft        R <- max(R - Z q, 0), Z <- sum R
-//   without (q = 1)         Z <- Z - R(x_c), R(x_c) <- 0
+//   without (q = 1)         Z <- max(Z - R(x_c), 0), R(x_c) <- 0
 // Where no child stands, the token that follows is the first whose running sum
 // of R exceeds u_0 sum R.  So the tokens said are distributed as if the target
 // had drawn each of them.
@@ -66,7 +66,6 @@ struct Shared {
   double z[kMaxRows];
   float zh[kMaxRows], zl[kMaxRows];
   int gone[kMaxRows];
-  float gone_p[kMaxRows];
   double chunk[kMaxChunks];
   double total[2][kMaxRanks];           // the CTAs' sums, of even and odd passes
   double all;                           // ... and theirs
@@ -138,8 +137,9 @@ __device__ __forceinline__ int pad_of(const T* row) {
 }
 
 // What is left, R, of the entries at places c kChunk .. of a row of `target`
-// after q (the same entries of `draft`) has been taken off m times: this lane's
-// share of their sum, and with `keep` the values to s.left.  (One piece of code
+// after q (the same entries of `draft`) has been taken off m times, or m tokens
+// have been taken out (no `draft`): this lane's share of their sum, and with
+// `keep` the values to s.left.  (One piece of code
 // for both: a launch runs it a few times only, so what it costs is to be
 // fetched.  Unrolled twice over, the kernel spent most of its time on that.)
 template <typename T>
@@ -155,11 +155,11 @@ __device__ __noinline__ Sum2 chunk_rest(Shared& s, const T* target,
   uint4 a[PER], b[PER];
   const int first = c * kChunk - pad_of(target);
   if (first >= 0 && first + kChunk <= vocab &&
-      (m == 0 || pad_of(draft) == pad_of(target))) {
+      (m == 0 || !draft || pad_of(draft) == pad_of(target))) {
     const uint4* from = reinterpret_cast<const uint4*>(target + x0);
 #pragma unroll
     for (int k = 0; k < PER; ++k) a[k] = __ldg(from + k * 32);
-    if (m > 0) {
+    if (m > 0 && draft) {
       from = reinterpret_cast<const uint4*>(draft + x0);
 #pragma unroll
       for (int k = 0; k < PER; ++k) b[k] = __ldg(from + k * 32);
@@ -168,7 +168,7 @@ __device__ __noinline__ Sum2 chunk_rest(Shared& s, const T* target,
 #pragma unroll
     for (int k = 0; k < PER; ++k) {
       a[k] = edge(target, x0 + k * 32 * VEC, vocab);
-      if (m > 0) b[k] = edge(draft, x0 + k * 32 * VEC, vocab);
+      if (m > 0 && draft) b[k] = edge(draft, x0 + k * 32 * VEC, vocab);
     }
   }
   auto two = [](const uint4& v, int w) -> uint64_t {
@@ -190,6 +190,21 @@ __device__ __noinline__ Sum2 chunk_rest(Shared& s, const T* target,
     for (int w = 0; w < W; ++w) r[k * W + w] = positive(two(a[k], w));
 #pragma unroll 1
   for (int i = 0; i < m; ++i) {
+    if (!draft) {
+      // (zero itself, not a difference of sums: nothing may be left of a row
+      // whose every token was taken out)
+      const int at = s.gone[i] - first;
+      if (at >= 0 && at < kChunk && (at / VEC & 31) == lane) {
+#pragma unroll
+        for (int k = 0; k < PER * W; ++k) {
+          const bool hit = k == at / (32 * VEC) * W + at % VEC / 2;
+          float x, y;
+          unpair(r[k], x, y);
+          r[k] = pair(hit && !(at & 1) ? 0.f : x, hit && (at & 1) ? 0.f : y);
+        }
+      }
+      continue;
+    }
     // (the mass as two floats; the first is 1)
     const uint64_t zh = pair(-s.zh[i], -s.zh[i]),
                    zl = pair(-s.zl[i], -s.zl[i]);
@@ -297,10 +312,11 @@ verify_kernel(const Params p) {
   // only: an SM adds two values a clock.)
   auto sum = [&](int node, int m) -> double {
     tr = static_cast<const T*>(p.target) + (start + node) * p.t_st;
-    dr = static_cast<const T*>(p.draft) + (start + node) * p.d_st;
+    dr = draft ? static_cast<const T*>(p.draft) + (start + node) * p.d_st
+               : nullptr;
     pad = pad_of(tr);
     for (int c = c_lo + warp; c < c_hi; c += kWarps) {
-      Sum2 a = chunk_rest(s, tr, dr, c, draft ? m : 0, p.vocab, false);
+      Sum2 a = chunk_rest(s, tr, dr, c, m, p.vocab, false);
 #pragma unroll 1
       for (int o = 16; o; o >>= 1) {
         const float h = __shfl_xor_sync(0xffffffffu, a.hi, o);
@@ -313,16 +329,6 @@ verify_kernel(const Params p) {
     }
     __syncthreads();
     if (warp == 0) {
-      // tokens that were tried in vain are out of it
-      if (!draft && m > 0) {
-        if (lane == 0)
-          for (int k = 0; k < m; ++k) {
-            const int c = (s.gone[k] + pad) / kChunk - c_lo;
-            if (c >= 0 && c < c_hi - c_lo)
-              s.chunk[c] = fmax(s.chunk[c] - s.gone_p[k], 0.0);
-          }
-        __syncwarp();
-      }
       double t = 0.0;
       for (int c = lane; c < c_hi - c_lo; c += 32) t += s.chunk[c];
 #pragma unroll
@@ -389,12 +395,9 @@ verify_kernel(const Params p) {
           ++m;
           known = false;
         } else if (have > 0.0) {
-          if (lane == 0) {
-            s.gone[m] = x;
-            s.gone_p[m] = s.pt[i];
-          }
+          if (lane == 0) s.gone[m] = x;
           ++m;
-          mass -= have;
+          mass = fmax(mass - have, 0.0);
         }
         __syncwarp();
         ++i;
@@ -438,7 +441,7 @@ verify_kernel(const Params p) {
     }
   }
   if (warp == 0 && all > 0.0) {
-    const double want = static_cast<double>(s.u[0]) * all;
+    const double want = fmax(static_cast<double>(s.u[0]), 0.0) * all;
     // the first CTA whose running sum exceeds it; none (u_0 >= 1): the last
     // with any mass
     double before = 0.0, run = 0.0, mine_before = 0.0;
@@ -449,13 +452,14 @@ verify_kernel(const Params p) {
       if (r == rank) mine_before = run;
       if (t > 0.0) last = r;
       run += t;
-      if (owner < 0 && run > want) owner = r;
+      if (owner < 0 && t > 0.0 && run > want) owner = r;
     }
     const bool past = owner < 0;
     if (past) owner = last;
     before = mine_before;
     if (owner == static_cast<int>(rank)) {
-      // ... then its chunk (32 at a time) ...
+      // ... then its chunk (32 at a time; rounding must not pick one without
+      // mass) ...
       int found = -1, some = -1;
       double at = before;
       for (int c0 = 0; c0 < c_hi - c_lo && found < 0; c0 += 32) {
@@ -467,7 +471,7 @@ verify_kernel(const Params p) {
           if (lane >= o) in += y;
         }
         const unsigned hit =
-            __ballot_sync(0xffffffffu, !past && at + in > want);
+            __ballot_sync(0xffffffffu, !past && own > 0.0 && at + in > want);
         const unsigned any = __ballot_sync(0xffffffffu, own > 0.0);
         if (any) some = c0 + 31 - __clz(any);
         if (hit) {
@@ -483,13 +487,7 @@ verify_kernel(const Params p) {
       if (end) found = some;
       // ... then the 32 entries (a lane's) that hold it ...
       const int x0 = (c_lo + found) * kChunk - pad;
-      chunk_rest(s, tr, dr, c_lo + found, draft ? m : 0, p.vocab, true);
-      __syncwarp();
-      if (!draft)
-        for (int j = lane; j < m; j += 32) {
-          const int i = s.gone[j] - x0;
-          if (i >= 0 && i < kChunk) s.left[i + (i >> 5)] = 0.f;
-        }
+      chunk_rest(s, tr, dr, c_lo + found, m, p.vocab, true);
       __syncwarp();
       Sum2 a{0.f, 0.f};
 #pragma unroll 4
@@ -504,7 +502,8 @@ verify_kernel(const Params p) {
         return x;
       };
       const double in = scan(own);
-      const unsigned hit = __ballot_sync(0xffffffffu, !end && at + in > want);
+      const unsigned hit =
+          __ballot_sync(0xffffffffu, !end && own > 0.0 && at + in > want);
       const unsigned any = __ballot_sync(0xffffffffu, own > 0.0);
       // (none: the last one with mass)
       const int src = hit ? __ffs(hit) - 1 : any ? 31 - __clz(any) : 0;
@@ -513,7 +512,7 @@ verify_kernel(const Params p) {
       const float r = s.left[src * 33 + lane];
       const double inr = scan(static_cast<double>(r));
       const unsigned hit1 =
-          __ballot_sync(0xffffffffu, hit != 0 && at + inr > want);
+          __ballot_sync(0xffffffffu, hit != 0 && r > 0.f && at + inr > want);
       const unsigned any1 = __ballot_sync(0xffffffffu, r > 0.f);
       const int e1 = hit1 ? __ffs(hit1) - 1 : any1 ? 31 - __clz(any1) : 0;
       const int token = x0 + src * 32 + e1;

@@ -5,6 +5,7 @@
 // launch nothing.  Kernels never trap: out-of-range indices are skipped and
 // recorded in a device error word (pkv_check_device_errors reads it).
 #include <algorithm>
+#include <limits.h>
 #include <math.h>
 #include <stdarg.h>
 #include <stdio.h>
@@ -1788,6 +1789,18 @@ pkv_status pkv_paged_attention_varlen_tree(
   if (total_q > 0 && batch > 0 && max_seqlen_q > 0) {
     if (!tree_parents)
       return fail(PKV_ERR_INVALID_ARG, "NULL tree_parents");
+    // (counted in 32 bits by the kernel)
+    if (num_kv_heads > 0 &&
+        (static_cast<int64_t>(max_seqlen_q) * (num_heads / num_kv_heads) >=
+             (1 << 20) ||
+         static_cast<int64_t>(batch) * num_heads * max_seqlen_q / 128 +
+                 static_cast<int64_t>(batch) * num_kv_heads >
+             INT_MAX))
+      return fail(PKV_ERR_UNSUPPORTED, "too many rows of a drafted tree");
+    if (static_cast<int64_t>(max_blocks_per_seq) * block_size >
+        INT_MAX - 1024)
+      return fail(PKV_ERR_UNSUPPORTED,
+                  "block_table: at most 2^31 - 1025 keys of a drafted tree");
     if (num_blocks < 1)
       return fail(PKV_ERR_INVALID_ARG, "the cache has no blocks");
   }
@@ -1871,6 +1884,8 @@ pkv_status pkv_compact_draft_cache(
     return fail(PKV_ERR_INVALID_ARG, "negative size argument");
   if (num_heads <= 0 || row_bytes <= 0)
     return fail(PKV_ERR_INVALID_ARG, "num_heads / row_bytes must be > 0");
+  if (static_cast<int64_t>(num_heads) * row_bytes > (1 << 30))
+    return fail(PKV_ERR_UNSUPPORTED, "a token's row is at most 1 GB");
   if (block_size <= 0 || block_size % 16 != 0)
     return fail(PKV_ERR_INVALID_ARG, "block_size must be a multiple of 16");
   if (max_rows > PKV_TREE_MAX_ROWS)

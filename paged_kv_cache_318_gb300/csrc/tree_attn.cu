@@ -1,5 +1,7 @@
 // Attention of a tree of drafted tokens: the join of the pieces, and the launch
 // (the kernel and its design: tree_attn.cuh).
+#include <limits.h>
+
 #include "tree_attn.cuh"
 
 namespace pkv {
@@ -167,8 +169,10 @@ cudaError_t launch_tree_attn(const AttnParams& a, const int32_t* parents,
     keys = static_cast<int64_t>(a.wl) + max_n + RB;
   const int64_t units = static_cast<int64_t>(a.batch) * a.Hkv * blocks;
   const int64_t tiles = units * ((keys + bn - 1) / bn + 1);
-  // (units of one tile are not cut, and need no join behind the kernel)
-  p.split = scratch != nullptr && keys > bn;
+  // (units of one tile are not cut, and need no join behind the kernel; where
+  // the tables could name more tiles than 32 bits count, whole units go round)
+  const int64_t cols = static_cast<int64_t>(a.max_blocks) * a.BS / bn + 2;
+  p.split = scratch != nullptr && keys > bn && cols <= INT_MAX / units;
   p.rows_cap = rows_cap(D, a.G, max_n);
   const int64_t most = p.split ? tiles : units;
   const int grid = static_cast<int>(most < sms ? most : sms);
