@@ -12,7 +12,10 @@
  * Beside them stand the steps between a model's QKV projection and the cache
  * (pkv_qk_norm_rope, pkv_rope_reshape_and_cache) and a 4-bit cache
  * (pkv_reshape_and_cache_fp4, pkv_paged_attention_varlen_fp4,
- * pkv_dequantize_fp4_cache); the pages have no counterpart of these.
+ * pkv_dequantize_fp4_cache), and one step of speculative decoding over the
+ * paged cache: attention of drafted trees (pkv_paged_attention_varlen_tree),
+ * verification (pkv_verify_draft_tokens) and the move of what stands
+ * (pkv_compact_draft_cache); the pages have no counterpart of these.
  *
  * Conventions shared by every entry point:
  *   - Every tensor pointer is a DEVICE pointer owned by the caller.  The
@@ -55,9 +58,9 @@ typedef enum {
   PKV_ERR_UNSUPPORTED = 2,          /* valid but not built (dtype, D, fp8 ...) */
   PKV_ERR_WORKSPACE_TOO_SMALL = 3,  /* workspace_bytes below the needed size  */
   PKV_ERR_CUDA = 4,                 /* a CUDA runtime call failed              */
-  PKV_ERR_BAD_INDEX = 5,            /* a kernel met an out-of-range block id or
-                                       slot and skipped it (see
-                                       pkv_check_device_errors)               */
+  PKV_ERR_BAD_INDEX = 5,            /* a kernel met an out-of-range block id,
+                                       slot, parent, token or row and skipped
+                                       it (see pkv_check_device_errors)       */
   PKV_ERR_TIMEOUT = 6               /* a kernel's bounded wait for data ran
                                        out; its CTA drained its copies and
                                        stopped without writing (see

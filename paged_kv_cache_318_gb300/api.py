@@ -13,7 +13,8 @@ Names and argument orders follow those pages: ``reshape_and_cache_flash``,
 ("vllm/v1/attention/backends/flash_attn.py").  ``qk_norm_rope``,
 ``rope_reshape_and_cache`` and the 4-bit cache (``fp4_kv_cache``,
 ``dequantize_fp4_cache``, the ``*_block_scale`` arguments) have no counterpart
-there.
+there, nor has the speculative decoding step: drafted trees (``tree_parents``),
+``verify_draft_tokens`` and ``compact_draft_cache``.
 """
 from __future__ import annotations
 
