@@ -599,8 +599,7 @@ tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
               scales(q + 1);
               entry(q + 2);
             }
-            if (!mbar_wait(raw_full(slot), r_turn, abort_flag, p.err) ||
-                (again && !mbar_wait(empty(st), s_turn, abort_flag, p.err))) {
+            if (!mbar_wait(raw_full(slot), r_turn, abort_flag, p.err)) {
               ok = false;
               break;
             }
@@ -608,6 +607,15 @@ tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
             const unsigned char* src = base + C::OFF_CODES +
                                        slot * C::CODE_TILE +
                                        cw * (RW * C::CODE_ROW) + lane * 16;
+            // (all codes at once: the stores below let no load past them)
+            uint4 ws[PER];
+#pragma unroll
+            for (int i = 0; i < PER; ++i)
+              ws[i] = *reinterpret_cast<const uint4*>(src + i * 512);
+            if (again && !mbar_wait(empty(st), s_turn, abort_flag, p.err)) {
+              ok = false;
+              break;
+            }
             // (V rows that no row of the block sees are zeros: they may hold
             // another request's NaN)
             const int key0 = pc.kt0 + i_tile * BN + cw * RW + ln;
@@ -615,7 +623,7 @@ tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
                                     (high && i_tile == pc.nt - 1));
 #pragma unroll
             for (int i = 0; i < PER; ++i) {
-              uint4 w = *reinterpret_cast<const uint4*>(src + i * 512);
+              uint4 w = ws[i];
               if (edge && (key0 + i * RI < pc.klo || key0 + i * RI >= pc.khi)) {
                 w = make_uint4(0, 0, 0, 0);
                 sf[i] = 0;
@@ -646,11 +654,11 @@ tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
                 const uint32_t f = e4m3x2_to_f16(sf[i]);
                 const uint32_t f0 = __byte_perm(f, f, 0x1010),
                                f1 = __byte_perm(f, f, 0x3232);
-                const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+                const uint32_t part[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                   uint32_t h[4];
-                  e2m1x8_to_f16(ws[k], h[0], h[1], h[2], h[3]);
+                  e2m1x8_to_f16(part[k], h[0], h[1], h[2], h[3]);
 #pragma unroll
                   for (int e = 0; e < 4; ++e)
                     h[e] = hmul2_u32(h[e], k < 2 ? f0 : f1);
