@@ -110,7 +110,7 @@ struct Cfg {
   static constexpr int OFF_CODES = OFF_RING + STAGES * STAGE;
   static constexpr int OFF_BAR = OFF_CODES + AHEAD * CODE_TILE;
   static constexpr int BAR_BYTES =
-      8 * ((NX == 2 ? 4 : 2) * STAGES + 22 + 2 * AHEAD);
+      8 * ((NX == 2 ? 4 : 2) * STAGES + 24 + 2 * AHEAD);
   static constexpr int OFF_PIECE = OFF_BAR + BAR_BYTES;
   static constexpr int PIECE_BYTES = 80;
   static constexpr int OFF_PAR = OFF_PIECE + SLOTS * PIECE_BYTES;
@@ -319,7 +319,9 @@ tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
   // codes of a tile have arrived / are widened
   auto raw_full = [&](int s) { return bar0 + 8 * (B0 + 21 + s); };
   auto raw_empty = [&](int s) { return bar0 + 8 * (B0 + 21 + C::AHEAD + s); };
-  constexpr int OFF_WORDS = C::OFF_BAR + 8 * (B0 + 21 + 2 * C::AHEAD);
+  // the streams' turns at the tensor core
+  auto turn = [&](int x) { return bar0 + 8 * (B0 + 21 + 2 * C::AHEAD + x); };
+  constexpr int OFF_WORDS = C::OFF_BAR + 8 * (B0 + 23 + 2 * C::AHEAD);
   static_assert(OFF_WORDS + 8 <= C::OFF_PIECE, "barrier area");
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + OFF_WORDS);
   volatile int* abort_flag =
@@ -341,6 +343,7 @@ tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
       mbar_init(it_full(s), 1);
       mbar_init(it_empty(s), C::SM_WARPS + C::TAKERS);
       mbar_init(par_full(s), 1);
+      mbar_init(turn(s), 1);
     }
     for (int s = 0; s < C::AHEAD; ++s) {
       mbar_init(raw_full(s), 1);
@@ -693,6 +696,7 @@ tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
       constexpr uint32_t ID_PV = idesc(128, D, kBF16, true);
       const uint32_t acc = tmem + x * C::S_STEP + C::O_COL;
       uint32_t s_cnt = 0, pv_cnt = 0;  // products issued
+      uint32_t turns = 0;
       int at = 0;                      // loads of the pieces before
       bool ok = true;
       auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
@@ -802,7 +806,8 @@ tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
             const int buf = NX == 1 ? pv_cnt & 1 : x;
             const uint64_t vd = sdesc(sR + sv * C::STAGE, cbs, gs);
             const uint32_t keep = k > 1 ? 1u : 0u;
-            if (!wait(p_full(buf), NX == 1 ? pv_cnt >> 1 : pv_cnt)) {
+            if (!wait(p_full(buf), NX == 1 ? pv_cnt >> 1 : pv_cnt) ||
+                (NX == 2 && pair && !wait(turn(x), turns + 1 - x))) {
               ok = false;
               break;
             }
@@ -821,6 +826,14 @@ tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
             if (k < tiles) score(sk);
             if (k > 0) consumed(sv);
             if (k < tiles) consumed(sk);
+            // Of two streams that take every tile, one's P V and next S run as
+            // a whole while the other is at its softmax.  (Left to themselves
+            // the two interleave, end together, and then the tensor core waits
+            // for two softmaxes at once: 2000 clocks of 4500 a tile.)
+            if (pair && k > 0) {
+              ++turns;
+              if (lane == 0) mbar_arrive(turn(1 - x));
+            }
           }
           if (k == tiles - 1) mma_commit_warp(q_empty(n & 1));
         }
