@@ -83,7 +83,8 @@ struct Cfg {
   static constexpr int NCB = D / 64;                   // 64-column blocks
   static constexpr int ROWS = NX * BM;                 // rows of a block
   static constexpr int STAGE = BN * D * 2;             // one K or V tile
-  static constexpr int STAGES = KV ? (D == 64 ? 6 : 3) : D == 64 ? 8 : 5;
+  static constexpr int STAGES =
+      KV == kE2m1 ? (D == 64 ? 6 : 4) : KV ? (D == 64 ? 6 : 3) : D == 64 ? 8 : 5;
   static constexpr int Q_TILE = BM * D * 2;
   // tensor memory: (S_x, O_x) per stream, or (S_0, S_1, O)
   static constexpr int S_STEP = NX == 2 ? BN + D : BN;
@@ -96,23 +97,32 @@ struct Cfg {
                        MMA_WARP = SM_WARPS + 2;
   // codes: the warps that copy and widen them, in place of the loader
   static constexpr int CODE_WARP = SM_WARPS + 4,
-                       CODE_WARPS = KV ? 8 : 0;
+                       CODE_WARPS = KV ? 8 : 0,
+                       GROUP = CODE_WARPS / 2;   // warps that share a tile
   static constexpr int THREADS = (SM_WARPS + 4 + CODE_WARPS) * 32;
   // warps that take every piece and are done with it at once
   static constexpr int TAKERS = 1 + NX + CODE_WARPS;
   // tiles of codes on their way
   static constexpr int CODE_ROW = KV == kE4m3 ? D : D / 2;   // bytes
   static constexpr int CODE_TILE = BN * CODE_ROW;
-  static constexpr int AHEAD = KV == 0 ? 0 : KV == kE2m1 ? 6 : 4;
+  static constexpr int AHEAD = KV == 0 ? 0 : 4;
+  // The two groups that widen codes take the ring's places in turn.  A waiter
+  // sees one parity, so each phase of a barrier has to be waited for by one
+  // group: with an odd number of stages there are two `empty` barriers a stage,
+  // each for one group's turns.
+  static constexpr int EMPTIES = KV && STAGES % 2 ? 2 : 1;
+  static_assert(AHEAD % 2 == 0, "a group keeps to its places of codes");
   static constexpr int SLOTS = 2;                      // pieces in flight
   static constexpr int OFF_Q = 0;
   static constexpr int OFF_RING = OFF_Q + NX * Q_TILE;
   static constexpr int OFF_CODES = OFF_RING + STAGES * STAGE;
   static constexpr int OFF_BAR = OFF_CODES + AHEAD * CODE_TILE;
   static constexpr int BAR_BYTES =
-      8 * ((NX == 2 ? 4 : 2) * STAGES + 24 + 2 * AHEAD);
+      (8 * (((NX == 2 ? 3 : 1) + EMPTIES) * STAGES + 24 + 2 * AHEAD) + 15) /
+      16 * 16;
   static constexpr int OFF_PIECE = OFF_BAR + BAR_BYTES;
-  static constexpr int PIECE_BYTES = 80;
+  static constexpr int PIECE_BYTES = 64;
+  static_assert(OFF_PIECE % 16 == 0, "pieces are copied as vectors");
   static constexpr int OFF_PAR = OFF_PIECE + SLOTS * PIECE_BYTES;
   static constexpr int OFF_XCH = OFF_PAR + SLOTS * PKV_TREE_MAX_ROWS;
   static constexpr int SMEM_USED = OFF_XCH + (NX == 2 ? 2 * BM * 8 : 0);
@@ -176,9 +186,9 @@ struct Piece {
   int klo, khi;             // keys any row sees; khi also bounds the reads
   int pair;                 // more than 128 rows
   int whole, slot;          // the whole unit; else its partial's slot
-  int pad[5];
+  int pad;
 };
-static_assert(sizeof(Piece) == 80, "copied as 5 x 16 bytes");
+static_assert(sizeof(Piece) == 64, "copied as 4 x 16 bytes");
 
 // What a request asks for; rows <= 0: nothing.
 struct Req {
@@ -301,8 +311,10 @@ tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
   // a barrier, and the streams run ahead of one another.
   constexpr int SETS = NX == 2 ? 3 : 1;
   auto full = [&](int set, int s) { return bar0 + 8 * (set * ST + s); };
-  auto empty = [&](int s) { return bar0 + 8 * (SETS * ST + s); };
-  constexpr int B0 = (SETS + 1) * ST;
+  auto empty = [&](int s, int group = 0) {
+    return bar0 + 8 * ((SETS + (C::EMPTIES == 2 ? group : 0)) * ST + s);
+  };
+  constexpr int B0 = (SETS + C::EMPTIES) * ST;
   static_assert(SETS * ST <= 32, "parities in a word");
   auto s_full = [&](int x) { return bar0 + 8 * (B0 + x); };
   auto p_full = [&](int x) { return bar0 + 8 * (B0 + 2 + x); };
@@ -330,8 +342,8 @@ tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
   if (tid == 0) {
     for (int s = 0; s < ST; ++s) {
       for (int k = 0; k < SETS; ++k)
-        mbar_init(full(k, s), KV ? C::CODE_WARPS : 1);
-      mbar_init(empty(s), NX);
+        mbar_init(full(k, s), KV ? C::GROUP : 1);
+      for (int g = 0; g < C::EMPTIES; ++g) mbar_init(empty(s, g), NX);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(s_full(s), 1);
@@ -347,7 +359,7 @@ tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
     }
     for (int s = 0; s < C::AHEAD; ++s) {
       mbar_init(raw_full(s), 1);
-      mbar_init(raw_empty(s), C::CODE_WARPS);
+      mbar_init(raw_empty(s), C::GROUP);
     }
     mbar_init(xbar, 256);
     mbar_init(pv_done, 1);
@@ -383,9 +395,9 @@ tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
     if (!mbar_wait(it_full(s), (n >> 1) & 1, abort_flag, p.err)) return -1;
     const int4* src = reinterpret_cast<const int4*>(
         base + C::OFF_PIECE + s * C::PIECE_BYTES);
-    int4 w[5];
+    int4 w[4];
 #pragma unroll
-    for (int k = 0; k < 5; ++k) w[k] = src[k];
+    for (int k = 0; k < 4; ++k) w[k] = src[k];
     memcpy(&pc, w, sizeof(Piece));
     return pc.live ? 1 : 0;
   };
@@ -519,19 +531,24 @@ tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
             mbar_drain(KV ? raw_full(k) : full(0, k), (sent >> k & 1) ^ 1);
     } else if (KV != 0 && warp >= C::CODE_WARP) {
       // ------------------------------------------------- codes widened
-      // Tile after tile of the ring's order, from the loader's rows of codes to
-      // the 16-bit layout that the products read: exactly, the tensor scales
-      // joining the logits and the output.  A warp widens 16 rows (8 at
-      // head size 256): they lie in one page, so it has one page's block scales
-      // to fetch.
+      // From the loader's rows of codes to the 16-bit layout that the products
+      // read: exactly, the tensor scales joining the logits and the output.
+      // Two groups of warps take the places of the ring in turn, so that one
+      // converts while the other waits, fences and signs off (head size 256,
+      // 48 requests of 4364 keys: 375 us with one group of 8, 320 with two of
+      // 4 for 4 bits, 258 and 226 for E4M3; 199 and 187 at 128 for 4 bits).  A
+      // warp widens 16 rows at a time: they lie in one page, whose block scales
+      // it fetches.
       if constexpr (KV != 0) {
-        constexpr int RW = BN / C::CODE_WARPS;           // rows of a warp
-        static_assert(RW == 16 || RW == 8, "whole eights of rows of one page");
+        constexpr int RW = BN / C::GROUP;                // rows of a warp
+        constexpr int H = RW / 16;
+        static_assert(H * 16 == RW, "whole sixteens");
         constexpr int VALS = KV == kE4m3 ? 16 : 32;      // values of 16 bytes
         constexpr int ROW = D / VALS;                    // 16 bytes of a row
         constexpr int RI = 32 / ROW;                     // rows at a time
-        constexpr int PER = RW / RI;
+        constexpr int PER = 16 / RI;
         const int cw = warp - C::CODE_WARP, ln = lane / ROW, cp = lane % ROW;
+        const int group = cw / C::GROUP, sub = cw % C::GROUP;
         // row and eight of step i's row
         auto row_in_8 = [&](int i) {
           return RI >= 8 ? ln & 7 : i % (8 / (RI < 8 ? RI : 8)) * RI + ln;
@@ -539,18 +556,19 @@ tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
         auto eights = [&](int i) {
           return RI >= 8 ? i * (RI / 8) + (ln >> 3) : i / (8 / (RI < 8 ? RI : 8));
         };
-        int st = 0, slot = 0;          // stage, place of its codes
-        uint32_t s_turn = 1, r_turn = 0;     // their parities
-        bool ok = true, again = false; // (the first round fills empty stages)
+        int pos = group;               // place in the ring
+        bool ok = true;
         for (int n = 0; ok; ++n) {
           Piece pc;
           if (take(n, pc) <= 0) break;
           release(n);
-          const int total = 2 * pc.nt;
+          const int total = 2 * pc.nt, steps = pc.nt * H;
           const bool low = pc.kt0 < pc.klo;
           const bool high = pc.kt0 + pc.nt * BN > pc.khi;
-          // place q of the piece: its tile, and K (0) or V
-          auto tile = [&](int q, int& v) -> int {
+          // step s: rows 16 (s % H) .. of place 2 (s / H) + group of the piece:
+          // its tile, and K (0) or V
+          auto tile = [&](int s, int& v) -> int {
+            const int q = s / H * 2 + group;
             if (pc.pair) {
               v = q & 1;
               return q >> 1;
@@ -558,23 +576,26 @@ tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
             v = q == total - 1 || (q > 1 && !(q & 1));
             return q == total - 1 ? pc.nt - 1 : v ? (q - 2) >> 1 : (q + 1) >> 1;
           };
-          // block scales: the table's entry two tiles ahead, the scales of
+          // block scales: the table's entry two steps ahead, the scales of
           // this lane's bytes one ahead
           const int32_t* bt =
               p.block_table + static_cast<int64_t>(pc.b) * p.bt_stride;
           int blk = 0;
           uint16_t sf[PER] = {}, sf_next[PER] = {};
-          auto entry = [&](int q) {
+          auto first_key = [&](int s, int& v) -> int {
+            return pc.kt0 + tile(s, v) * BN + sub * RW + s % H * 16;
+          };
+          auto entry = [&](int s) {
             int v;
-            const int key = pc.kt0 + tile(q, v) * BN + cw * RW;
-            if (KV == kE2m1 && q < total && key < pc.khi)
+            const int key = first_key(s, v);
+            if (KV == kE2m1 && s < steps && key < pc.khi)
               blk = __ldg(bt + (p.bs_shift >= 0 ? key >> p.bs_shift
                                                 : key / p.BS));
           };
-          auto scales = [&](int q) {
+          auto scales = [&](int s) {
             int v;
-            const int key = pc.kt0 + tile(q, v) * BN + cw * RW;
-            if (KV == kE2m1 && q < total && key < pc.khi && blk >= 0 &&
+            const int key = first_key(s, v);
+            if (KV == kE2m1 && s < steps && key < pc.khi && blk >= 0 &&
                 blk < p.num_blocks) {
               const int row = p.bs_shift >= 0 ? key & (p.BS - 1) : key % p.BS;
               const uint8_t* from = (v ? p.v_sf : p.k_sf) + blk * p.f_sb +
@@ -593,35 +614,42 @@ tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
           scales(0);
           entry(1);
 #pragma unroll 1
-          for (int q = 0; q < total; ++q) {
+          for (int s = 0; s < steps; ++s) {
             int v;
-            const int i_tile = tile(q, v);
+            const int i_tile = tile(s, v), part = s % H;
             if (KV == kE2m1) {
 #pragma unroll
               for (int i = 0; i < PER; ++i) sf[i] = sf_next[i];
-              scales(q + 1);
-              entry(q + 2);
+              scales(s + 1);
+              entry(s + 2);
             }
-            if (!mbar_wait(raw_full(slot), r_turn, abort_flag, p.err)) {
+            const int st = pos % ST, slot = pos % C::AHEAD;
+            if (part == 0 &&
+                !mbar_wait(raw_full(slot), (pos / C::AHEAD) & 1, abort_flag,
+                           p.err)) {
               ok = false;
               break;
             }
-            const uint32_t to = sR + st * C::STAGE + cw * (RW / 8) * gs;
+            const int row0 = sub * RW + part * 16;
+            const uint32_t to = sR + st * C::STAGE + row0 / 8 * gs;
             const unsigned char* src = base + C::OFF_CODES +
                                        slot * C::CODE_TILE +
-                                       cw * (RW * C::CODE_ROW) + lane * 16;
+                                       row0 * C::CODE_ROW + lane * 16;
             // (all codes at once: the stores below let no load past them)
             uint4 ws[PER];
 #pragma unroll
             for (int i = 0; i < PER; ++i)
               ws[i] = *reinterpret_cast<const uint4*>(src + i * 512);
-            if (again && !mbar_wait(empty(st), s_turn, abort_flag, p.err)) {
+            if (part == 0 && pos >= ST &&
+                !mbar_wait(empty(st, group),
+                           (pos - ST) / (ST * C::EMPTIES) & 1, abort_flag,
+                           p.err)) {
               ok = false;
               break;
             }
             // (V rows that no row of the block sees are zeros: they may hold
             // another request's NaN)
-            const int key0 = pc.kt0 + i_tile * BN + cw * RW + ln;
+            const int key0 = pc.kt0 + i_tile * BN + row0 + ln;
             const bool edge = v && ((low && i_tile == 0) ||
                                     (high && i_tile == pc.nt - 1));
 #pragma unroll
@@ -669,6 +697,7 @@ tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
                 }
               }
             }
+            if (part != H - 1) continue;
             fence_proxy_async();
             __syncwarp();
             if (lane == 0) {
@@ -676,15 +705,7 @@ tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
               mbar_arrive(full(set, st));
               mbar_arrive(raw_empty(slot));
             }
-            if (++st == ST) {
-              st = 0;
-              s_turn ^= 1;
-              again = true;
-            }
-            if (++slot == C::AHEAD) {
-              slot = 0;
-              r_turn ^= 1;
-            }
+            pos += 2;
           }
         }
       }
@@ -744,23 +765,26 @@ tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
           mma_commit_warp(s_full(buf));
           ++s_cnt;
         };
-        auto consumed = [&](int st) {
-          mma_commit_warp(empty(st));
-          if (alt) mma_commit_warp(empty(st));       // (for the other stream)
+        // (place pos; its stage's next turn is the other group's, if any)
+        auto consumed = [&](int pos) {
+          const uint32_t bar = empty(pos % ST, (pos + ST) & 1);
+          mma_commit_warp(bar);
+          if (alt) mma_commit_warp(bar);             // (for the other stream)
         };
         if (tiles > 0 && !wait(q_full(n & 1), n >> 1)) break;
 #pragma unroll 1
         for (int k = 0; k <= tiles && tiles > 0; ++k) {
           const int jk = j0 + k * step, jv = jk - step;
-          const int sk = (at + place_k(jk, pair)) % ST;
-          const int sv = (at + place_v(jv, pc.nt, pair)) % ST;
+          const int pk = at + place_k(jk, pair);
+          const int pv = at + place_v(jv, pc.nt, pair);
+          const int sk = pk % ST, sv = pv % ST;
           if (k < tiles && NX == 1) {
             if (!loaded(sk, set)) {
               ok = false;
               break;
             }
             score(sk);
-            consumed(sk);
+            consumed(pk);
           }
           if (k > 0) {
             if (!loaded(sv, set)) {
@@ -798,7 +822,7 @@ tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
               break;
             }
           }
-          if (k < tiles && NX == 2 && !loaded(sk, set)) {
+          if (k < tiles && NX == 2 && KV == 0 && !loaded(sk, set)) {
             ok = false;
             break;
           }
@@ -817,15 +841,20 @@ tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
                                   vd + ((c * 2 * gs) >> 4), ID_PV,
                                   c > 0 ? 1u : keep);
             ++pv_cnt;
-            if constexpr (NX == 1) {
-              mma_commit_warp(pv_done);
-              consumed(sv);
-            }
+            if constexpr (NX == 1) mma_commit_warp(pv_done);
+            if (NX == 1 || KV != 0) consumed(pv);
           }
           if (NX == 2) {
+            // (codes: the widening of the next K waits for V's stage, so V is
+            // given back before K is waited for: 173 -> 165 us on 48 requests
+            // of 4364 E4M3 keys)
+            if (k < tiles && KV != 0 && !loaded(sk, set)) {
+              ok = false;
+              break;
+            }
             if (k < tiles) score(sk);
-            if (k > 0) consumed(sv);
-            if (k < tiles) consumed(sk);
+            if (k > 0 && KV == 0) consumed(pv);
+            if (k < tiles) consumed(pk);
             // Of two streams that take every tile, one's P V and next S run as
             // a whole while the other is at its softmax.  (Left to themselves
             // the two interleave, end together, and then the tensor core waits
@@ -974,12 +1003,12 @@ tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
                                  p.err))
           break;
         if (lane == 0) {
-          int4 w[5];
+          int4 w[4];
           memcpy(w, &pc, sizeof(Piece));
           int4* dst = reinterpret_cast<int4*>(base + C::OFF_PIECE +
                                               s * C::PIECE_BYTES);
 #pragma unroll
-          for (int k = 0; k < 5; ++k) dst[k] = w[k];
+          for (int k = 0; k < 4; ++k) dst[k] = w[k];
           mbar_arrive(it_full(s));
         }
         if (!pc.live) break;
