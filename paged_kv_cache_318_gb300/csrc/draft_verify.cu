@@ -20,6 +20,11 @@
 // to 8 CTAs shares the vocabulary of a request; every CTA walks the same way,
 // and only the sums cross between them.
 //
+// Measured on the device, launches in a graph: one chain of 5 over 32001 tokens
+// 11 us; 64 chains of 5 over 131072, both distributions, 22 us (3.1 TB/s); 48
+// trees of 16 without the draft's 19 us; 24 trees of 9 to 24 over 100003 in bf16
+// 34 us, about 3 us for each rejection on a request's way.
+//
 // The answers are whole numbers that turn on sums over the vocabulary: with
 // 100000 near-equal probabilities, a sum that is off by 1e-8 of itself moves
 // the sampled token once in a thousand draws.  Sums of 32 values are therefore

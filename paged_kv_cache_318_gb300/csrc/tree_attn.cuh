@@ -36,6 +36,13 @@
 // stream has an MMA warp of its own: one warp for both, which also kept the
 // order across the pieces' borders, ran 3000 clocks of its own instructions a
 // tile, more than the tile's share of HBM (64 KB: 2800).
+//
+// Measured (32/8 heads of 128 unless said; time on the device, launches in a
+// graph): 64 requests of 16 rows over 512 to 4096 keys 123 us, 5.5 TB/s while
+// the kernel runs; one of 61 rows over 16384 keys 30 us; 4 of 64 rows over 65536
+// keys, 64/8 heads, 430 us, 1280 TFLOP/s; 124 of 2 to 8 rows, windows of 4095
+// keys, 16/8 heads of 256, 565 us, 6.7 TB/s; 48 of 12 rows over 4364 keys: 16
+// bits 157 us, E4M3 165, 4 bits 187.
 #pragma once
 
 #include <cuda.h>
@@ -118,7 +125,8 @@ struct Cfg {
   static constexpr int OFF_CODES = OFF_RING + STAGES * STAGE;
   static constexpr int OFF_BAR = OFF_CODES + AHEAD * CODE_TILE;
   static constexpr int BAR_BYTES =
-      (8 * (((NX == 2 ? 3 : 1) + EMPTIES) * STAGES + 24 + 2 * AHEAD) + 15) /
+      (8 * (((NX == 2 ? 3 : 1) + EMPTIES) * STAGES + (KV ? 24 : 26) +
+            2 * AHEAD) + 15) /
       16 * 16;
   static constexpr int OFF_PIECE = OFF_BAR + BAR_BYTES;
   static constexpr int PIECE_BYTES = 64;
@@ -333,7 +341,11 @@ tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
   auto raw_empty = [&](int s) { return bar0 + 8 * (B0 + 21 + C::AHEAD + s); };
   // the streams' turns at the tensor core
   auto turn = [&](int x) { return bar0 + 8 * (B0 + 21 + 2 * C::AHEAD + x); };
-  constexpr int OFF_WORDS = C::OFF_BAR + 8 * (B0 + 23 + 2 * C::AHEAD);
+  // the probabilities of a tile's first half (16-bit caches, two streams)
+  constexpr bool HALVES = NX == 2 && KV == 0;
+  auto p_half = [&](int x) { return bar0 + 8 * (B0 + 23 + 2 * C::AHEAD + x); };
+  constexpr int OFF_WORDS =
+      C::OFF_BAR + 8 * (B0 + (KV ? 23 : 25) + 2 * C::AHEAD);
   static_assert(OFF_WORDS + 8 <= C::OFF_PIECE, "barrier area");
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + OFF_WORDS);
   volatile int* abort_flag =
@@ -356,6 +368,7 @@ tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
       mbar_init(it_empty(s), C::SM_WARPS + C::TAKERS);
       mbar_init(par_full(s), 1);
       mbar_init(turn(s), 1);
+      if (KV == 0) mbar_init(p_half(s), 128);
     }
     for (int s = 0; s < C::AHEAD; ++s) {
       mbar_init(raw_full(s), 1);
@@ -830,16 +843,30 @@ tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
             const int buf = NX == 1 ? pv_cnt & 1 : x;
             const uint64_t vd = sdesc(sR + sv * C::STAGE, cbs, gs);
             const uint32_t keep = k > 1 ? 1u : 0u;
-            if (!wait(p_full(buf), NX == 1 ? pv_cnt >> 1 : pv_cnt) ||
+            if (!wait(HALVES ? p_half(x) : p_full(buf),
+                      NX == 1 ? pv_cnt >> 1 : pv_cnt) ||
                 (NX == 2 && pair && !wait(turn(x), turns + 1 - x))) {
               ok = false;
               break;
             }
-#pragma unroll
-            for (int c = 0; c < BN / 16; ++c)
+            auto products = [&](int c) {
               mma_f16_tmem_a_warp(acc, tmem + buf * C::S_STEP + 8 * c,
                                   vd + ((c * 2 * gs) >> 4), ID_PV,
                                   c > 0 ? 1u : keep);
+            };
+            constexpr int FIRST = HALVES ? BN / 32 : BN / 16;
+#pragma unroll
+            for (int c = 0; c < FIRST; ++c) products(c);
+            if constexpr (HALVES) {
+              // (the first half runs under the second half of the softmax:
+              // 190 -> 185 us on 64 requests of 64 rows over 2368 keys)
+              if (!wait(p_full(x), pv_cnt)) {
+                ok = false;
+                break;
+              }
+#pragma unroll
+              for (int c = FIRST; c < BN / 16; ++c) products(c);
+            }
             ++pv_cnt;
             if constexpr (NX == 1) mma_commit_warp(pv_done);
             if (NX == 1 || KV != 0) consumed(pv);
@@ -858,7 +885,8 @@ tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
             // Of two streams that take every tile, one's P V and next S run as
             // a whole while the other is at its softmax.  (Left to themselves
             // the two interleave, end together, and then the tensor core waits
-            // for two softmaxes at once: 2000 clocks of 4500 a tile.)
+            // for two softmaxes at once, 2000 clocks of 4500 a tile: 483 us
+            // against 430 on 4 requests of 64 rows, 64 heads, 65600 keys.)
             if (pair && k > 0) {
               ++turns;
               if (lane == 0) mbar_arrive(turn(1 - x));
@@ -1156,6 +1184,7 @@ tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
           break;
         }
         if (!live) {
+          if (HALVES) mbar_arrive(p_half(x));
           mbar_arrive(p_full(buf));
           continue;
         }
@@ -1300,12 +1329,19 @@ tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
             v[e >> 1] = __uint_as_float(pack2<T>(x0, x1));
           }
           tmem_st32(s_addr + (c >> 1), v);
+          if constexpr (HALVES) {
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(c == 0 ? p_half(x) : p_full(x));
+          }
         }
         l += ((sum8[0] + sum8[1]) + (sum8[2] + sum8[3])) +
              ((sum8[4] + sum8[5]) + (sum8[6] + sum8[7]));
-        tmem_wait_st();
-        tc_fence_before();
-        mbar_arrive(p_full(buf));
+        if constexpr (!HALVES) {
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive(p_full(buf));
+        }
       }
       if (!ok) break;
       release(n);
