@@ -1838,10 +1838,12 @@ pkv_status pkv_verify_draft_tokens(
   if (batch > 65536)
     return fail(PKV_ERR_UNSUPPORTED, "at most 65536 requests");
   if (batch == 0) return PKV_OK;
-  if (max_seqlen_q == 0)
+  if (max_seqlen_q == 0 && total_q > 0)
     return fail(PKV_ERR_INVALID_ARG, "max_seqlen_q must be > 0");
-  if (!target_probs || !draft_token_ids || !uniform || !cu_seqlens_q ||
-      !token_ids || !rows || !counts)
+  // (a batch without rows has counts of 0, and nothing to read)
+  if (!cu_seqlens_q || !counts ||
+      (total_q > 0 && (!target_probs || !draft_token_ids || !uniform)) ||
+      (max_seqlen_q > 0 && (!token_ids || !rows)))
     return fail(PKV_ERR_INVALID_ARG, "NULL tensor pointer");
   const int es = dtype == PKV_F32 ? 4 : 2;
   if (reinterpret_cast<uintptr_t>(target_probs) % es ||

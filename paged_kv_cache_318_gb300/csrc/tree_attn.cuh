@@ -676,21 +676,15 @@ tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
               const uint32_t line = to + eights(i) * gs + r8 * 128;
               if constexpr (KV == kE4m3) {
                 const uint32_t dst = line + (cp >> 2) * 1024;
-                uint32_t h[8];
-                e4m3x4_to_f16(w.x, h[0], h[1]);
-                e4m3x4_to_f16(w.y, h[2], h[3]);
-                e4m3x4_to_f16(w.z, h[4], h[5]);
-                e4m3x4_to_f16(w.w, h[6], h[7]);
                 // (the two halves in an order that keeps the lanes of a row
                 // in different banks)
                 const bool odd = (cp >> 2) & 1;
                 const uint32_t c0 = (cp & 3) * 2 + (odd ? 1 : 0);
                 uint32_t x[4], y[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  x[e] = odd ? h[4 + e] : h[e];
-                  y[e] = odd ? h[e] : h[4 + e];
-                }
+                e4m3x4_to_f16(odd ? w.z : w.x, x[0], x[1]);
+                e4m3x4_to_f16(odd ? w.w : w.y, x[2], x[3]);
+                e4m3x4_to_f16(odd ? w.x : w.z, y[0], y[1]);
+                e4m3x4_to_f16(odd ? w.y : w.w, y[2], y[3]);
                 store_wide<T>(dst + ((c0 ^ r8) << 4), x);
                 store_wide<T>(dst + ((c0 ^ 1 ^ r8) << 4), y);
               } else {

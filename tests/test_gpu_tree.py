@@ -664,6 +664,22 @@ def test_verification_of_the_largest_vocabulary(cuda_device):
     c.check(*api.verify_draft_tokens(*c.args()))
 
 
+@pytest.mark.parametrize("max_n", [0, 3])
+def test_verification_of_requests_without_rows(cuda_device, max_n):
+    d = cuda_device
+    tok, rows, cnt = api.verify_draft_tokens(
+        torch.empty((0, 100), device=d), ints([], d), ints([0, 0, 0], d),
+        max_n, torch.empty(0, device=d), ints([], d))
+    assert tok.shape == rows.shape == (2, max_n)
+    assert (tok == -1).all() and (rows == -1).all() and cnt.tolist() == [0, 0]
+
+
+def test_attention_of_requests_without_rows(cuda_device):
+    t = Draft(cuda_device, [0, 0], [9, 30], 4, 2, 64, 16)
+    out, lse = t.run()
+    assert out.shape == (0, 4, 64) and lse.shape == (4, 0)
+
+
 def one(dev, p, tok, u, par, q=None):
     p = torch.tensor(p, dtype=torch.float32, device=dev)
     n = p.shape[0]
