@@ -38,11 +38,11 @@
 // tile, more than the tile's share of HBM (64 KB: 2800).
 //
 // Measured (32/8 heads of 128 unless said; time on the device, launches in a
-// graph): 64 requests of 16 rows over 512 to 4096 keys 123 us, 5.5 TB/s while
+// graph): 64 requests of 16 rows over 512 to 4096 keys 122 us, 5.5 TB/s while
 // the kernel runs; one of 61 rows over 16384 keys 30 us; 4 of 64 rows over 65536
-// keys, 64/8 heads, 430 us, 1280 TFLOP/s; 124 of 2 to 8 rows, windows of 4095
-// keys, 16/8 heads of 256, 565 us, 6.7 TB/s; 48 of 12 rows over 4364 keys: 16
-// bits 157 us, E4M3 165, 4 bits 187.
+// keys, 64/8 heads, 410 to 430 us, 1300 TFLOP/s; 124 of 2 to 8 rows, windows of
+// 4095 keys, 16/8 heads of 256, 565 us, 6.7 TB/s; 48 of 12 rows over 4364 keys:
+// 16 bits 158 us, E4M3 158, 4 bits 187.
 #pragma once
 
 #include <cuda.h>
@@ -437,10 +437,10 @@ tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
       // ring.  A lane's page id is fetched a step ahead.  Boxes behind the last
       // key, and those of a page outside the cache, start outside the tensor:
       // they arrive as zeros.  Codes go to the places that the code warps read.
-      // (With pages of 16 keys the loader sets the pace of small tiles: 16 boxes
-      // of a step leave one after the other, about 90 clocks each.  One elected
-      // lane in a loop, fed by shuffles, was slower still: 228 us against 158 on
-      // 48 requests of 12 rows over 4364 16-bit keys.)
+      // (With pages of 16 keys the copies set the pace of small tiles: a row of
+      // 128 bytes takes about 7 clocks.  A second loader warp changed nothing;
+      // one elected lane in a loop, fed by shuffles, was slower: 228 us against
+      // 158 on 48 requests of 12 rows over 4364 16-bit keys.)
       constexpr int RING = KV ? C::AHEAD : ST;
       const int half = lane >> 4, box = lane & 15;
       const void* tm = half ? static_cast<const void*>(&tm_v)
