@@ -506,8 +506,8 @@ PKV_API pkv_status pkv_paged_attention_varlen_tree(
  * sum R.  If nothing is left of R, R = target_probs[node] there; if no running
  * sum exceeds (a number of 1 or more), the last token with R > 0; if there is
  * none, -1.  Sums and comparisons are exact to about 1e-13 of the sum (entries
- * of R after the first subtraction carry float32 roundings); negative
- * probabilities count as 0.
+ * of R after the first subtraction carry float32 roundings); probabilities
+ * below 0 and NaN count as 0, the target's and the draft's.
  *
  * target_probs, draft_probs : [total_q, vocab_size], dtype (PKV_F16, PKV_BF16
  *   or PKV_F32, the same for both), row strides in elements, any alignment.

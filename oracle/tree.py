@@ -59,7 +59,9 @@ def tree_attention(q, k, v, parents, scale, softcap=0.0, window_left=-1,
 def verify(target, tokens, uniform, parents, draft=None):
     """One request's rows: (tokens said, rows that stand)."""
     target = np.asarray(target, np.float64)
-    draft = None if draft is None else np.asarray(draft, np.float64)
+    # (probabilities below 0 or NaN count as 0)
+    draft = None if draft is None else \
+        np.fmax(np.asarray(draft, np.float64), 0.0)
     n, vocab = target.shape
     node, said, rows = 0, [], [0]
     rest, mass = np.maximum(target[0], 0.0), 1.0

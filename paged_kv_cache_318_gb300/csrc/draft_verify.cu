@@ -217,7 +217,8 @@ __device__ __noinline__ Sum2 chunk_rest(Shared& s, const T* target,
     for (int k = 0; k < PER; ++k)
 #pragma unroll
       for (int w = 0; w < W; ++w) {
-        const uint64_t q = two(b[k], w);
+        // (below 0 or NaN: none, as in the target)
+        const uint64_t q = positive(two(b[k], w));
         uint64_t& v = r[k * W + w];
         v = positive(fma2(zl, q, fma2(zh, q, v)));
       }
@@ -291,7 +292,7 @@ verify_kernel(const Params p) {
     s.par[i] = i > 0 ? par : -1;
     s.tok[i] = tok;
     s.pt[i] = fmaxf(pt, 0.f);
-    s.qt[i] = qt;
+    s.qt[i] = fmaxf(qt, 0.f);
   }
   if (tid == 0) {
     s.node = 0;

@@ -715,6 +715,31 @@ def test_verification_at_the_edges(cuda_device):
     api.check_device_errors(d)
 
 
+@pytest.mark.parametrize("bad", [-.2, -1e30, float("-inf"), float("nan")])
+@pytest.mark.parametrize("vocab", [4, 2000])
+def test_negative_draft_probabilities_count_as_none(cuda_device, vocab, bad):
+    """In 2000 entries: of the vectors that a row reads whole."""
+    d = cuda_device
+
+    def row(*x):
+        return list(x) + [0.0] * (vocab - len(x))
+    P = [row(.5, .5), row(0, 0, 1)]
+    # a token of the draft below 0 that the target does not have either
+    assert one(d, P, [0, 2], [.7, .5], [-1, 0], [row(.6, .6, bad, 0)] * 2) \
+        == ([1], [0])
+    # ... that the target has: it stands with whatever number
+    assert one(d, P, [0, 1], [0., .99], [-1, 0], [row(1, bad)] * 2) == \
+        ([1, 2], [0, 1])
+    # entries below 0 beside a refused token add nothing to what is left:
+    # [0, .25, .25] twice over, with u_0 at .4 and .6 of it
+    P = [row(.5, .25, .25), row(1), row(1)]
+    Q = [row(.75, bad, 0, bad)] * 3
+    assert one(d, P[:2], [0, 0], [.4, .9], [-1, 0], Q[:2]) == ([1], [0])
+    assert one(d, P, [0, 0, 0], [.6, .9, .9], [-1, 0, 0], Q) == ([2], [0])
+    assert one(d, P, [0, 0, 3], [.6, .9, 0.], [-1, 0, 0], Q) == ([2], [0])
+    api.check_device_errors(d)
+
+
 @pytest.mark.parametrize("tok,par", [
     (1000, 0), (-1, 0), (1 << 30, 0), (3, 1), (3, 2), (3, -2), (3, 1 << 30)])
 def test_verification_flags(cuda_device, tok, par):

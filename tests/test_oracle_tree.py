@@ -104,6 +104,21 @@ def test_verify_with_draft_probabilities():
     assert verify(P, [9, 0, 0], [.99, .7, .9], [-1, 0, 1], q) == ([2], [0])
 
 
+@pytest.mark.parametrize("bad", [-.2, float("-inf"), float("nan")])
+def test_verify_counts_a_negative_draft_probability_as_none(bad):
+    p = np.array([[.5, .25, .25, 0], [1, 0, 0, 0], [1, 0, 0, 0]])
+    q = np.array([[.75, bad, 0, bad]] * 3)
+    # token 3, which neither has, does not stand
+    assert verify(p[:2], [9, 3], [.6, .5], [-1, 0], q[:2]) == ([2], [0])
+    # token 1, which the draft does not have, does
+    assert verify(p[:2], [9, 1], [.6, .99], [-1, 0], q[:2]) == ([1, 0],
+                                                               [0, 1])
+    # what is left after token 0 is refused: (0, .25, .25, 0)
+    tree = [-1, 0, 0]
+    assert verify(p, [9, 0, 3], [.4, .9, 0.], tree, q) == ([1], [0])
+    assert verify(p, [9, 0, 0], [.6, .9, .9], tree, q) == ([2], [0])
+
+
 def test_verify_with_nothing_left():
     # the draft covers the target: R becomes nothing, the target stays
     q = np.ones((3, 4))
