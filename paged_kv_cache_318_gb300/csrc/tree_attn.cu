@@ -10,7 +10,8 @@ namespace tree {
 // Joins the pieces of the units that the shares' ends cut.  Blocks (x, .) look
 // through the marks of CTAs x, x + gridDim.x, ..; a unit's rows go round the
 // warps of the blocks (., y): M = the largest partial LSE (and the sink), w_k =
-// e^(lse_k - M), out = sum w_k o_k / sum w_k, lse = M + ln sum w_k.
+// e^(lse_k - M), out = sum w_k o_k / sum w_k, lse = M + ln sum w_k.  Where a
+// wait ran out in one of a unit's CTAs, its rows stay as they are.
 constexpr int kFoldThreads = 256;
 template <typename T, int D>
 __global__ void __launch_bounds__(kFoldThreads, 2)
@@ -41,11 +42,14 @@ fold_kernel(const Params p, int ctas) {
         };
         const float z = p.sinks ? p.sinks[h] : -INFINITY;
         float M = z;
+        int gone = 0;
         for (int k0 = 0; k0 < np; k0 += 32) {
-          const float s =
-              k0 + lane < np ? p.part_lse[at(k0 + lane)] : -INFINITY;
+          const bool in = k0 + lane < np;
+          const float s = in ? p.part_lse[at(k0 + lane)] : -INFINITY;
+          gone |= in ? p.marks[2 * (c + k0 + lane) + 1].y : 0;
           M = fmaxf(M, s);
         }
+        if (__any_sync(0xffffffffu, gone)) break;
 #pragma unroll
         for (int o = 16; o; o >>= 1)
           M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
@@ -151,6 +155,7 @@ cudaError_t launch_tree_attn(const AttnParams& a, const int32_t* parents,
   p.v_scale = a.v_scale;
   p.wl = a.wl;
   p.err = a.err;
+  p.wait_ns = a.wait_ns;
   int RB = 16;
   while (RB * 2 <= 64 && a.BS % (RB * 2) == 0) RB *= 2;
   p.RB = RB;

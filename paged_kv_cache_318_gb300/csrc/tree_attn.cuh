@@ -182,8 +182,10 @@ struct Params {
   int split, rows_cap;
   float* part_o;
   float* part_lse;
-  int4* marks;              // two per CTA: (pieces, q0, rows, row0), (g, ...)
+  int4* marks;              // two per CTA: (pieces, q0, rows, row0), (g, gave
+                            // up, ...)
   unsigned* err;
+  uint64_t wait_ns;         // limit of the bounded waits
 };
 
 // A run of consecutive key tiles of one unit.
@@ -303,9 +305,13 @@ tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
   unsigned char* base = smem_raw;
   const uint32_t base_u = smem_u32(smem_raw);
   if (base_u & 1023u) {            // 128-byte swizzle atoms need 1 KB
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     if (threadIdx.x == 0) {
       atomicOr(p.err, kErrSmemAlign);
-      if (p.split) p.marks[2 * blockIdx.x] = make_int4(0, 0, 0, 0);
+      if (p.split) {
+        p.marks[2 * blockIdx.x] = make_int4(0, 0, 0, 0);
+        p.marks[2 * blockIdx.x + 1] = make_int4(0, 1, 0, 0);
+      }
     }
     return;
   }
@@ -401,11 +407,17 @@ tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
   // queued before it (a no-op unless launched as its programmatic dependent)
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
+  // (A poll is one instruction of a converged warp on one address, so its lanes
+  // get one answer and what is collective behind it stays whole.  Votes on it
+  // measured 1 to 3 % slower, in the slow path alone too.)
+  auto wait_for = [&](uint32_t bar, uint32_t parity) -> bool {
+    return mbar_wait_lim(bar, parity, abort_flag, p.err, p.wait_ns);
+  };
   // The CTA's n-th piece (all lanes of a reader warp call it in order).  The
   // slot is given back by release(n).
   auto take = [&](int n, Piece& pc) -> int {
     const int s = n & 1;
-    if (!mbar_wait(it_full(s), (n >> 1) & 1, abort_flag, p.err)) return -1;
+    if (!wait_for(it_full(s), (n >> 1) & 1)) return -1;
     const int4* src = reinterpret_cast<const int4*>(
         base + C::OFF_PIECE + s * C::PIECE_BYTES);
     int4 w[4];
@@ -490,9 +502,10 @@ tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
           const uint32_t bar = KV ? raw_full(st) : full(set, st);
           int stop = 0;
           if (box == 0 && mine) {
-            if (pos >= RING && !mbar_wait(KV ? raw_empty(st) : empty(st),
-                                          (pos / RING - 1) & 1, abort_flag,
-                                          p.err))
+            if (pos >= RING &&
+                !mbar_wait_lim(KV ? raw_empty(st) : empty(st),
+                               (pos / RING - 1) & 1, abort_flag, p.err,
+                               p.wait_ns))
               stop = 1;
             else
               mbar_expect_tx(bar, KV ? C::CODE_TILE : C::STAGE);
@@ -646,8 +659,7 @@ tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
             }
             const int st = pos % ST, slot = pos % C::AHEAD;
             if (part == 0 &&
-                !mbar_wait(raw_full(slot), (pos / C::AHEAD) & 1, abort_flag,
-                           p.err)) {
+                !wait_for(raw_full(slot), (pos / C::AHEAD) & 1)) {
               ok = false;
               break;
             }
@@ -662,9 +674,8 @@ tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
             for (int i = 0; i < PER; ++i)
               ws[i] = *reinterpret_cast<const uint4*>(src + i * 512);
             if (part == 0 && pos >= ST &&
-                !mbar_wait(empty(st, group),
-                           (pos - ST) / (ST * C::EMPTIES) & 1, abort_flag,
-                           p.err)) {
+                !wait_for(empty(st, group),
+                           (pos - ST) / (ST * C::EMPTIES) & 1)) {
               ok = false;
               break;
             }
@@ -736,7 +747,7 @@ tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
       int at = 0;                      // loads of the pieces before
       bool ok = true;
       auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
-        const bool r = mbar_wait(bar, parity & 1, abort_flag, p.err);
+        const bool r = wait_for(bar, parity & 1);
         tc_fence_after();
         return r;
       };
@@ -1029,8 +1040,7 @@ tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
           }
         }
         const int s = n & 1;
-        if (n >= 2 && !mbar_wait(it_empty(s), (n / 2 - 1) & 1, abort_flag,
-                                 p.err))
+        if (n >= 2 && !wait_for(it_empty(s), (n / 2 - 1) & 1))
           break;
         if (lane == 0) {
           int4 w[4];
@@ -1066,8 +1076,7 @@ tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
         // of one row tile take them in turn
         const bool alt = NX == 2 && !pc.pair;
         const int before = alt && !prev_pair ? n - 2 : n - 1;
-        if (before >= 0 && !mbar_wait(q_empty(before & 1), (before >> 1) & 1,
-                                      abort_flag, p.err))
+        if (before >= 0 && !wait_for(q_empty(before & 1), (before >> 1) & 1))
           break;
         prev_pair = pc.pair || NX == 1;
         const uint32_t dq = sQ + (alt ? (n & 1) * C::Q_TILE : 0);
@@ -1167,7 +1176,7 @@ tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
       // first key before the draft that this row sees
       int k_first = 0;
       if (p.wl >= 0 && live) {
-        ok = mbar_wait(par_full(n & 1), (n >> 1) & 1, abort_flag, p.err);
+        ok = wait_for(par_full(n & 1), (n >> 1) & 1);
         int depth = 0;
         for (int a = par[node]; ok && a != kNoParent; a = par[a]) ++depth;
         k_first = max(pc.ctx + depth - p.wl, 0);
@@ -1181,7 +1190,7 @@ tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
       for (int j = j0; ok && j < pc.nt; j += jd, ++cnt) {
         const int buf = NX == 2 ? x : cnt & 1;
         const int turn = NX == 2 ? cnt : cnt >> 1;
-        if (!mbar_wait(s_full(buf), turn & 1, abort_flag, p.err)) {
+        if (!wait_for(s_full(buf), turn & 1)) {
           ok = false;
           break;
         }
@@ -1203,8 +1212,7 @@ tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
             w[i] = range_bits(k_first - kt, full_hi - kt, i);
           const int rel0 = pc.ctx - kt;        // row 0's key in the tile
           if (rel0 < BN) {
-            if (!mbar_wait(par_full(n & 1), (n >> 1) & 1, abort_flag,
-                           p.err)) {
+            if (!wait_for(par_full(n & 1), (n >> 1) & 1)) {
               ok = false;
               break;
             }
@@ -1290,7 +1298,7 @@ tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
           // the products so far are complete: with two streams the commit
           // behind s_full covered them
           if constexpr (NX == 1) {
-            if (!mbar_wait(pv_done, (cnt - 1) & 1, abort_flag, p.err)) {
+            if (!wait_for(pv_done, (cnt - 1) & 1)) {
               ok = false;
               break;
             }
@@ -1353,11 +1361,11 @@ tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
       float f0 = 1.f, f1 = 0.f;                // weights of O_0 and O_1
       if (alt) {
         // (the other stream has read the state of the piece before)
-        if (n > 0 && !mbar_wait(o_free(0), (n - 1) & 1, abort_flag, p.err))
+        if (n > 0 && !wait_for(o_free(0), (n - 1) & 1))
           break;
         xch[x * BM + r] = make_float2(m, l);
         mbar_arrive(xbar);
-        if (!mbar_wait(xbar, n_x & 1, abort_flag, p.err)) break;
+        if (!wait_for(xbar, n_x & 1)) break;
         ++n_x;
         const float2 o = xch[(x ^ 1) * BM + r];
         const float M = fmaxf(m, o.x);
@@ -1371,8 +1379,8 @@ tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
         l = l0 * f0 + l1 * f1;
         m = M;
       }
-      if (!mbar_wait(o_ready(x), n & 1, abort_flag, p.err)) break;
-      if (alt && !mbar_wait(o_ready(x ^ 1), n & 1, abort_flag, p.err)) break;
+      if (!wait_for(o_ready(x), n & 1)) break;
+      if (alt && !wait_for(o_ready(x ^ 1), n & 1)) break;
       tc_fence_after();
       float inv, lse_v;
       finish(m, l, pc.whole ? p.sinks : nullptr, h, &inv, &lse_v);
@@ -1444,6 +1452,8 @@ tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
 
   tc_fence_before();
   __syncthreads();
+  // (the join leaves a unit alone that has a piece in a CTA that gave up)
+  if (p.split && tid == 0) p.marks[2 * blockIdx.x + 1].y = *abort_flag;
   if (warp == C::MMA_WARP) {
     tc_fence_after();
     asm volatile(

@@ -474,6 +474,52 @@ def test_two_calls_at_once(cuda_device):
         assert all(torch.equal(x, y) for x, y in zip(gb, wb))
 
 
+@pytest.mark.parametrize("kind", ["auto", "fp8", "fp4"])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("splits", [0, 1])
+@pytest.mark.parametrize("empty", [0, 1000, 6000])
+def test_a_wait_that_runs_out(cuda_device, empty, splits, d, kind):
+    """With a limit of 0 a wait gives up at its second poll, some 8 us on:
+    without empty requests on the way a few blocks at head size 256 do, half
+    way; with 1000 some of those that have to search for their share; with
+    6000 all, before their first piece.  The call ends and is flagged; no row
+    is joined from pieces that were not written (the workspace holds NaN), so
+    what is written is right, and so is the next call."""
+    dev = cuda_device
+    ns = [9, 30] + [0] * empty + [70, 12]
+    t = Draft(dev, ns, [3000, 1500] + [0] * empty + [2100, 4000], 8, 2, d, 16,
+              kind=kind)
+    ws = torch.empty(api.load_library().
+                     pkv_paged_attention_workspace_size_tree(
+                         len(ns), 121, 70, 4000, 8, 2, d, 16, 0, None),
+                     dtype=torch.uint8, device=dev)
+    a = t.args(num_splits=splits, workspace=ws)
+    out, lse = api.flash_attn_varlen_func(**a)
+    t.check(out, lse)
+    a["out"] = torch.empty_like(out)
+    status = []
+    try:
+        api.set_wait_limit_ns(0)
+        for _ in range(5):
+            ws.fill_(255)
+            a["out"].fill_(42.0)
+            api.flash_attn_varlen_func(**a)
+            try:
+                api.check_device_errors(dev)
+            except api.PkvError as e:
+                status.append(e.status)
+            assert ((a["out"] == 42.0) | (a["out"] == out)).all()
+            if empty == 6000:
+                assert (a["out"] == 42.0).all()
+    finally:
+        api.set_wait_limit_ns(api.WAIT_LIMIT_DEFAULT_NS)
+    assert set(status) <= {api.PKV_ERR_TIMEOUT}
+    assert status or empty < 6000
+    got, lse2 = api.flash_attn_varlen_func(**a)
+    api.check_device_errors(dev)
+    assert torch.equal(got, out) and torch.equal(lse2, lse)
+
+
 def test_captured_and_replayed(cuda_device):
     """A graph over largest sizes, replayed with other lengths."""
     ns, Ls = [9, 30, 4], [700, 1500, 30]
