@@ -10,6 +10,7 @@ from __future__ import annotations
 import concurrent.futures as cf
 import glob
 import os
+import re
 import shutil
 import subprocess
 
@@ -55,14 +56,40 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(f) <= t for f in _inputs())
 
 
+# Kernels whose warps trade registers (setmaxnreg) and have no stand-in: the
+# registers a thread that their split adds up to (LAUNCH_REGS in tree_attn.cuh).
+# With fewer the warps that ask for more would wait for ever.
+LAUNCH_REGS = ((re.compile(r"tree_attn_kernelI\w+?Li(64|128)ELi[12]E"), 96),
+               (re.compile(r"tree_attn_kernelI\w+?Li256ELi[12]E"), 128))
+
+
+def check_registers(log):
+    """Raises if ptxas (-v) gave one of those kernels another count."""
+    want, name = None, ""
+    for line in log.splitlines():
+        if "Compiling entry function" in line:
+            name = line.split("'")[1]
+            want = next((n for pat, n in LAUNCH_REGS if pat.search(name)),
+                        None)
+        used = re.search(r"Used (\d+) registers", line)
+        if used and want is not None and int(used.group(1)) != want:
+            raise RuntimeError(
+                "%s: compiled for %s registers, its register split needs %d" %
+                (name, used.group(1), want))
+
+
 def _compile(nvcc, src, extra):
     obj = os.path.join(BUILD_DIR,
                        os.path.basename(src).replace(".cu", ".o"))
-    cmd = [nvcc] + NVCC_FLAGS + extra + ["-c", src, "-o", obj]
+    split = os.path.basename(src) == "tree_codes.cu"
+    cmd = [nvcc] + NVCC_FLAGS + extra + (["-Xptxas", "-v"] if split else []) \
+        + ["-c", src, "-o", obj]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError("nvcc failed for %s:\n%s\n%s" %
                            (src, " ".join(cmd), res.stderr))
+    if split:
+        check_registers(res.stderr)
     return obj, res.stderr
 
 

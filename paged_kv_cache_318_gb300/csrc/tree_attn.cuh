@@ -50,6 +50,7 @@
 #include <math.h>
 #include <string.h>
 
+#include <atomic>
 #include <type_traits>
 
 #include "pkv_common.cuh"
@@ -138,7 +139,9 @@ struct Cfg {
   static constexpr int SMEM = SMEM_USED < 120 * 1024 ? 120 * 1024 : SMEM_USED;
   static_assert(SMEM <= 232448, "shared memory of a CTA");
   // Codes: 640 or 512 threads, launched with 96 or 128 registers each; the
-  // softmax warps take 144 or 200, the others keep 64 or 104.
+  // softmax warps take 144 or 200, the others keep 64 or 104.  (A kernel that
+  // uses setmaxnreg is compiled for as many registers as its launch bounds
+  // leave; _build.py refuses any other count.)
   static constexpr bool SPLIT_REGS = KV != 0;
   static constexpr int LAUNCH_REGS = NX == 2 ? 96 : 128,
                        SOFTMAX_REGS = NX == 2 ? 144 : 200,
@@ -1471,11 +1474,18 @@ cudaError_t launch(const Params& p, const CUtensorMap& mk,
   auto kern = tree_attn_kernel<T, D, KV>;
   cudaError_t e;
   if (C::SPLIT_REGS) {
-    // the split inside the kernel adds up to the launch's registers
-    cudaFuncAttributes fa;
-    e = cudaFuncGetAttributes(&fa, kern);
-    if (e != cudaSuccess) return e;
-    if (fa.numRegs != C::LAUNCH_REGS) return cudaErrorInvalidConfiguration;
+    // the split inside the kernel adds up to the launch's registers (with fewer
+    // it would wait for ever).  The build has made sure of the count, which is
+    // the same on every device; it is asked for once.
+    static std::atomic<int> regs{0};
+    if (regs.load(std::memory_order_relaxed) == 0) {
+      cudaFuncAttributes fa;
+      e = cudaFuncGetAttributes(&fa, kern);
+      if (e != cudaSuccess) return e;
+      regs.store(fa.numRegs, std::memory_order_relaxed);
+    }
+    if (regs.load(std::memory_order_relaxed) != C::LAUNCH_REGS)
+      return cudaErrorInvalidConfiguration;
   }
   e = smem_opt_in(reinterpret_cast<const void*>(kern), C::SMEM);
   if (e != cudaSuccess) return e;
