@@ -548,8 +548,12 @@ tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
               const int c2 = p.kv_order_hnd ? pc.g : row;
 #pragma unroll 1
               for (int cb = 0; cb < C::NCB; ++cb)
-                tma_load_4d(to + cb * cbs, tm, cb * 64, c1, c2,
-                            dead ? -1 : id, bar);
+                if (p.once)
+                  tma_load_4d_hint(to + cb * cbs, tm, cb * 64, c1, c2,
+                                   dead ? -1 : id, bar, pol);
+                else
+                  tma_load_4d(to + cb * cbs, tm, cb * 64, c1, c2,
+                              dead ? -1 : id, bar);
             }
           }
           // (for the end: which barrier each load went to)
