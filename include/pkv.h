@@ -453,6 +453,8 @@ PKV_API pkv_status pkv_paged_attention_varlen_fp4(
  *   E4M3 cache is named in opts.
  * num_splits   : 0, or 1: each (request, KV head) is worked through by one
  *   block and its bits do not depend on the rest of the batch.
+ * softcap      : at most PKV_TREE_MAX_SOFTCAP (PKV_ERR_UNSUPPORTED above): a
+ *   capped logit is right to within about 2^-22 of the cap, whatever its size.
  * PKV_ERR_UNSUPPORTED: ALiBi, an fp8 query, non-paged keys, a fixed split
  *   size, num_splits > 1.
  * A value row that holds NaN or infinity reaches every row of its request
@@ -464,6 +466,7 @@ PKV_API pkv_status pkv_paged_attention_varlen_fp4(
  *   after one.
  */
 #define PKV_TREE_MAX_ROWS 256
+#define PKV_TREE_MAX_SOFTCAP 4096.0f
 
 PKV_API size_t pkv_paged_attention_workspace_size_tree(
     int batch, int total_q, int max_seqlen_q, int max_seqlen_k,

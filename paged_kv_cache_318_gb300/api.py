@@ -707,7 +707,7 @@ def flash_attn_varlen_func(q, k, v, max_seqlen_q, cu_seqlens_q, max_seqlen_k,
     own, or -1 (row 0).  A row sees the keys before the draft, its own and its
     ancestors' (the request's last keys are those of its rows), and
     sits as many positions behind the context as it has ancestors.  ``causal``
-    has to be set; max_seqlen_q is at most 256.
+    has to be set; max_seqlen_q is at most 256 and softcap 4096.
     Returns out (and lse [Hq, T] float32 when return_softmax_lse).
     """
     lib = load_library()

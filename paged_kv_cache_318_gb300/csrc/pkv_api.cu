@@ -1784,6 +1784,10 @@ pkv_status pkv_paged_attention_varlen_tree(
     pkv_dtype dtype, pkv_stream_t stream, const pkv_attention_options* opts) {
   if (!causal)
     return fail(PKV_ERR_INVALID_ARG, "a drafted tree needs causal attention");
+  if (softcap > PKV_TREE_MAX_SOFTCAP)
+    return fail(PKV_ERR_UNSUPPORTED,
+                "softcap %g: at most %g over a drafted tree (0 = none)",
+                softcap, PKV_TREE_MAX_SOFTCAP);
   pkv_status st = check_tree(max_seqlen_q, num_splits, opts);
   if (st != PKV_OK) return st;
   if (total_q > 0 && batch > 0 && max_seqlen_q > 0) {

@@ -1250,7 +1250,9 @@ tree_attn_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
             tmem_wait_ld();
             if (!raw) {
               // log2 units; soft-cap t (1 - 2 / (1 + 2^(u x))), within about
-              // an ulp of the cap (the hardware tanh loses 2^-11 of it)
+              // an ulp of the cap (the hardware tanh loses 2^-11 of it), so
+              // that large caps are refused: a series for small logits beside
+              // it measured 1 to 4 % of every call
 #pragma unroll
               for (int e = 0; e < 32; ++e) {
                 v[e] *= scale_log2;

@@ -115,3 +115,14 @@ def test_large_rows_of_a_long_context(cuda_device, d, kind):
     """One request: every block's share is a piece of it."""
     t = Loud(cuda_device, [11], [6011], 4, 1, d, 16, BF, kind)
     t.hold(*t.run())
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("softcap", [0.5, 50.0, 1000.0, 4096.0])
+def test_soft_caps(cuda_device, softcap, d):
+    """Small logits, and some of up to a hundred."""
+    t = Loud(cuda_device, [12, 45], [300, 500], 8, 2, d, 16, HF)
+    t.hold(*t.run(softcap=softcap), softcap=softcap)
+    t = Draft(cuda_device, [12, 45], [300, 500], 8, 2, d, 16, HF, spread=8.0)
+    t.window = -1
+    Loud.hold(t, *t.run(softcap=softcap), softcap=softcap)

@@ -99,6 +99,12 @@ def test_attention_refuses(lib, kw, status, text):
     assert text in lib.pkv_last_error()
 
 
+@pytest.mark.parametrize("cap", [4097.0, 1e6, 1e30, float("inf")])
+def test_attention_refuses_large_soft_caps(lib, cap):
+    assert attend(lib, softcap=cap) == 2
+    assert b"softcap" in lib.pkv_last_error()
+
+
 @pytest.mark.parametrize("kw", [dict(batch=0), dict(total_q=0),
                                 dict(max_q=0, q=None, par=None)])
 def test_nothing_to_attend_is_a_noop(lib, kw):
