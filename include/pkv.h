@@ -553,7 +553,10 @@ PKV_API pkv_status pkv_verify_draft_tokens(
  *   pkv_verify_draft_tokens gives them: growing, rows[b][i] >= i.  An entry
  *   that does not grow or lies outside the request, and one whose block is out
  *   of range, is left out and flagged (PKV_ERR_BAD_INDEX through
- *   pkv_check_device_errors).  max_rows <= PKV_TREE_MAX_ROWS.
+ *   pkv_check_device_errors), and so is what counts[b] has above max_rows.
+ *   max_rows <= PKV_TREE_MAX_ROWS.
+ * The pages that rows move in belong to one request each (those of its context
+ *   before may be shared).
  */
 PKV_API pkv_status pkv_compact_draft_cache(
     void* const* caches, int num_caches, const int64_t cache_strides[3],

@@ -49,7 +49,7 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const Params p) {
   const int ctx = p.seqused_k[b] - n;
   // ---- byte offsets of the rows that move (-1: stays, or left out)
   const int32_t* rows = p.rows + b * p.rows_st;
-  unsigned bad = 0;
+  unsigned bad = p.count[b] > p.max_rows ? kErrBadTree : 0u;
   int moves = 0;
   for (int i = threadIdx.x; i < k; i += kThreads) {
     const int r = rows[i];

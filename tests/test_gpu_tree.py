@@ -961,6 +961,26 @@ def test_compaction_flags(cuda_device):
     np.testing.assert_array_equal(got, base)
 
 
+def test_compaction_of_more_rows_than_are_given(cuda_device):
+    """The rows that are there move; the call is flagged, unless the request
+    has no rows at all."""
+    dev = cuda_device
+    c = torch.arange(5 * 16, device=dev, dtype=torch.int32).view(5, 16, 1, 1)
+    c = c.clone()
+    a = (c, ints([[1, 0], [2, 3]], dev), ints([0, 6, 6], dev),
+         ints([20, 26], dev), ints([[0, 2, 5], [0, 1, 2]], dev))
+    api.compact_draft_cache(*a, ints([3, 4], dev))
+    api.check_device_errors(dev)
+    want = compact(np.arange(80).reshape(5, 16, 1, 1), np.array([1, 0]), 14,
+                   [0, 2, 5]).ravel()
+    np.testing.assert_array_equal(raw(c).view(np.int32).ravel(), want)
+    for cnt in ([4, 0], [1 << 30, 3]):
+        c.copy_(torch.arange(80, dtype=torch.int32).view_as(c))
+        api.compact_draft_cache(*a, ints(cnt, dev))
+        flagged(dev)
+        np.testing.assert_array_equal(raw(c).view(np.int32).ravel(), want)
+
+
 def test_compaction_past_32_bits(cuda_device):
     nb = 1 + (5 << 30) // (16 * 256)
     c = torch.zeros((nb, 16, 1, 256), dtype=torch.uint8, device=cuda_device)
