@@ -944,9 +944,10 @@ PKV_API pkv_status pkv_set_decode_kernel(int which);
  * PKV_WAIT_LIMIT_DEFAULT_NS (2 s).  A wait that runs out records a timeout in
  * the device error word, the CTA drains the copies it issued (those drains
  * always keep the 2 s limit), frees what it holds and returns without writing
- * the outputs it was at (of a drafted tree also those that other CTAs hold
- * pieces of); pkv_check_device_errors then reports PKV_ERR_TIMEOUT and the next
- * call runs normally.  A process-wide diagnostic for testing that path: a small
+ * the outputs it was at.  (Outputs that several CTAs hold pieces of: the join
+ * of drafted trees leaves them alone, that of the persistent decode kernel may
+ * write them from what the workspace held.)  pkv_check_device_errors then
+ * reports PKV_ERR_TIMEOUT and the next call runs normally.  A process-wide diagnostic for testing that path: a small
  * limit makes calls fail.  No counterpart on the source pages.
  */
 #define PKV_WAIT_LIMIT_DEFAULT_NS 2000000000ull
