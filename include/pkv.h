@@ -947,8 +947,9 @@ PKV_API pkv_status pkv_set_decode_kernel(int which);
  * the outputs it was at.  (Outputs that several CTAs hold pieces of: the join
  * of drafted trees leaves them alone, that of the persistent decode kernel may
  * write them from what the workspace held.)  pkv_check_device_errors then
- * reports PKV_ERR_TIMEOUT and the next call runs normally.  A process-wide diagnostic for testing that path: a small
- * limit makes calls fail.  No counterpart on the source pages.
+ * reports PKV_ERR_TIMEOUT and the next call runs normally.  A process-wide
+ * diagnostic for testing that path: a small limit makes calls fail.  No
+ * counterpart on the source pages.
  */
 #define PKV_WAIT_LIMIT_DEFAULT_NS 2000000000ull
 PKV_API pkv_status pkv_set_wait_limit_ns(uint64_t ns);

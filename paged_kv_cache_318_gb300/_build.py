@@ -64,18 +64,22 @@ LAUNCH_REGS = ((re.compile(r"tree_attn_kernelI\w+?Li(64|128)ELi[12]E"), 96),
 
 
 def check_registers(log):
-    """Raises if ptxas (-v) gave one of those kernels another count."""
-    want, name = None, ""
+    """Raises if ptxas (-v) gave one of those kernels another count; returns
+    how many of them it saw."""
+    want, name, seen = None, "", 0
     for line in log.splitlines():
         if "Compiling entry function" in line:
             name = line.split("'")[1]
             want = next((n for pat, n in LAUNCH_REGS if pat.search(name)),
                         None)
         used = re.search(r"Used (\d+) registers", line)
-        if used and want is not None and int(used.group(1)) != want:
-            raise RuntimeError(
-                "%s: compiled for %s registers, its register split needs %d" %
-                (name, used.group(1), want))
+        if used and want is not None:
+            if int(used.group(1)) != want:
+                raise RuntimeError(
+                    "%s: compiled for %s registers, its register split needs "
+                    "%d" % (name, used.group(1), want))
+            seen, want = seen + 1, None
+    return seen
 
 
 def _compile(nvcc, src, extra):
@@ -88,8 +92,8 @@ def _compile(nvcc, src, extra):
     if res.returncode != 0:
         raise RuntimeError("nvcc failed for %s:\n%s\n%s" %
                            (src, " ".join(cmd), res.stderr))
-    if split:
-        check_registers(res.stderr)
+    if split and check_registers(res.stderr) == 0:
+        raise RuntimeError("no register counts from ptxas for %s" % src)
     return obj, res.stderr
 
 

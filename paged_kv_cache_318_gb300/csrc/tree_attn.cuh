@@ -40,9 +40,9 @@
 // Measured (32/8 heads of 128 unless said; time on the device, launches in a
 // graph): 64 requests of 16 rows over 512 to 4096 keys 122 us, 5.5 TB/s while
 // the kernel runs; one of 61 rows over 16384 keys 30 us; 4 of 64 rows over 65536
-// keys, 64/8 heads, 410 to 450 us, 1220 to 1340 TFLOP/s; 124 of 2 to 8 rows, windows of
-// 4095 keys, 16/8 heads of 256, 565 us, 6.7 TB/s; 48 of 12 rows over 4364 keys:
-// 16 bits 158 us, E4M3 158, 4 bits 187.
+// keys, 64/8 heads, 410 to 450 us, 1220 to 1340 TFLOP/s; 124 of 2 to 8 rows,
+// windows of 4095 keys, 16/8 heads of 256, 565 us, 6.7 TB/s; 48 of 12 rows over
+// 4364 keys: 16 bits 158 us, E4M3 158, 4 bits 187.
 #pragma once
 
 #include <cuda.h>
