@@ -22,8 +22,10 @@ def reference(q, k, v, parents, eps, scale, softcap=0.0, window=-1,
     * its own rounding, eps / 2, or 2^-25 below f16's normal numbers."""
     q, k, v = (np.asarray(x, np.float64) for x in (q, k, v))
     out, lse = tree_attention(q, k, v, parents, scale, softcap, window, sinks)
-    if not len(k):
-        return out, lse, np.zeros_like(out), np.zeros_like(lse)
+    alive = np.where(np.isneginf(lse), 0.0, lse)
+    if not len(k):          # (zeros, and the sinks through a logarithm)
+        return out, lse, np.zeros_like(out), \
+            2.0 ** -20 + 2.0 ** -22 * np.abs(alive)
     mean, _ = tree_attention(q, k, np.abs(v), parents, scale, softcap, window,
                              sinks)
     n, hq, depth = q.shape
@@ -35,7 +37,6 @@ def reference(q, k, v, parents, eps, scale, softcap=0.0, window=-1,
         2.0 ** -18
     tiny = len(k) * 2.0 ** -36 * np.abs(v).max() + 2.0 ** -24
     tol = mean * share * (1 + eps) + np.abs(out) * eps / 2 + tiny
-    alive = np.where(np.isneginf(lse), 0.0, lse)
     return out, lse, tol, d.T + 2.0 ** -20 + 2.0 ** -22 * np.abs(alive) + \
         2.0 ** -24 * len(k)
 
